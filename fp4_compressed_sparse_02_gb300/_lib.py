@@ -60,6 +60,46 @@ class SwaQuantArgs(ctypes.Structure):
                 ("row_idx", c_vp), ("swa", c_vp), ("swa_scale", c_vp), ("swa_rows", c_i32)]
 
 
+class Fp4RowsArg(ctypes.Structure):
+    _fields_ = [("codes", c_vp), ("scales", c_vp), ("gscale", c_vp), ("rows", c_i32), ("cols", c_i32)]
+
+
+c_i64 = ctypes.c_int64
+
+
+class RmsNormArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("T", c_i32), ("D", c_i32), ("x", c_vp), ("x_dtype", c_i32),
+                ("res_dtype", c_i32), ("x_stride", c_i64), ("residual", c_vp), ("residual_out", c_vp),
+                ("residual_stride", c_i64), ("residual_out_stride", c_i64), ("weight", c_vp),
+                ("weight_dtype", c_i32), ("eps", ctypes.c_float), ("out_form", c_i32), ("scale_group", c_i32),
+                ("out", c_vp), ("out_stride", c_i64), ("out_scale", c_vp), ("out4", Fp4RowsArg)]
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("T", c_i32), ("H", c_i32), ("D", c_i32), ("d_rope", c_i32),
+                ("rot_first", c_i32), ("interleaved", c_i32), ("inverse", c_i32), ("dtype", c_i32), ("x", c_vp),
+                ("out", c_vp), ("x_stride_t", c_i64), ("x_stride_h", c_i64), ("out_stride_t", c_i64),
+                ("out_stride_h", c_i64), ("pos", c_vp), ("rope_cos", c_vp), ("rope_sin", c_vp),
+                ("rope_max_pos", c_i32)]
+
+
+class RopeTableArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("positions", c_i32), ("d_rope", c_i32), ("scaling", c_i32),
+                ("orig_positions", c_i32), ("theta", ctypes.c_double), ("factor", ctypes.c_double),
+                ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double), ("magnitude", ctypes.c_double),
+                ("rope_cos", c_vp), ("rope_sin", c_vp)]
+
+
+class Fp4QuantArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("x", c_vp), ("x_dtype", c_i32), ("x_stride", c_i64),
+                ("out", Fp4RowsArg)]
+
+
+class Fp4LinearArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("x", Fp4RowsArg), ("w", Fp4RowsArg), ("out", c_vp),
+                ("out_dtype", c_i32)]
+
+
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED_SHAPE", 3: "ERR_WORKSPACE_TOO_SMALL",
           4: "ERR_CUDA", 5: "ERR_DEVICE_CHECK", 6: "ERR_TIMEOUT"}
 
@@ -67,7 +107,8 @@ EXPORTS = ["csa2_compress_quant", "csa2_compress_quant_workspace", "csa2_index_f
            "csa2_index_full_workspace", "csa2_index_reindex", "csa2_index_reindex_workspace",
            "csa2_sparse_attn", "csa2_sparse_attn_workspace", "csa2_last_error_message",
            "csa2_get_device_error", "csa2_version", "csa2_index_full_noalloc", "csa2_selftest_wait_timeout",
-           "csa2_swa_quant", "csa2_compress_append", "csa2_compress_append_workspace"]
+           "csa2_swa_quant", "csa2_compress_append", "csa2_compress_append_workspace",
+           "csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear"]
 
 _lib = None
 
@@ -99,6 +140,11 @@ def lib():
         g.restype = c_i32
     L.csa2_swa_quant.argtypes = [ctypes.POINTER(SwaQuantArgs), c_vp]
     L.csa2_swa_quant.restype = c_i32
+    for name, st in [("csa2_rms_norm", RmsNormArgs), ("csa2_rope", RopeArgs), ("csa2_rope_table", RopeTableArgs),
+                     ("csa2_fp4_quant", Fp4QuantArgs), ("csa2_fp4_linear", Fp4LinearArgs)]:
+        f = getattr(L, name)
+        f.argtypes = [ctypes.POINTER(st), c_vp]
+        f.restype = c_i32
     L.csa2_index_full_noalloc.argtypes = [ctypes.POINTER(IndexFullArgs), c_vp]
     L.csa2_index_full_noalloc.restype = c_i32
     L.csa2_last_error_message.argtypes = []

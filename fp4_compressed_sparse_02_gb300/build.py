@@ -15,7 +15,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libcsa2.so")
-UNITS = ["api.cu", "compress.cu", "proj_tc.cu", "index.cu", "score_tc.cu", "attn.cu"]
+UNITS = ["api.cu", "compress.cu", "proj_tc.cu", "index.cu", "score_tc.cu", "attn.cu", "norm.cu", "rope.cu",
+         "fp4.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

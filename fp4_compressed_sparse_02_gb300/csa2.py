@@ -1,6 +1,7 @@
 """Python face of the CSA2 C ABI: torch tensors in, device pointers to libcsa2.so.
 
-Names follow include/csa2.h: compress_quant, index_full, index_reindex, sparse_attn.
+Names follow include/csa2.h: compress_quant, index_full, index_reindex, sparse_attn, and the
+operators around them: rms_norm, rope, rope_table, fp4_quant, fp4_linear.
 PyTorch provides device memory and the current stream; every computation runs in the
 library's kernels.  Outputs are allocated here when the caller passes none (pass them
 in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
@@ -15,7 +16,7 @@ import torch
 from . import _lib
 
 PAGE = 64
-BF16, F32, FP8E4M3 = 0, 1, 2
+BF16, F32, FP8E4M3, FP4E2M1X2 = 0, 1, 2, 3
 
 
 def _ptr(t: Optional[torch.Tensor]):
@@ -294,6 +295,226 @@ def swa_quant(x, swa, swa_scale, row_idx=None):
     a.x, a.row_idx, a.swa, a.swa_scale = _ptr(x), _ptr(row_idx), _ptr(swa), _ptr(swa_scale)
     a.swa_rows = swa.shape[0]
     _lib.check(_lib.lib().csa2_swa_quant(ctypes.byref(a), _stream()))
+
+
+def _float_type(t, name):
+    if t.dtype is torch.bfloat16:
+        return BF16
+    if t.dtype is torch.float32:
+        return F32
+    raise TypeError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
+
+
+def _rows_of(t, name, ndim=2):
+    """Data pointer of a CUDA tensor whose last dimension is contiguous."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name}: expected {ndim} dimensions, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr()
+
+
+def _launch(fn, args):
+    _lib.check(getattr(_lib.lib(), fn)(ctypes.byref(args), _stream()))
+
+
+@dataclass
+class Fp4Rows:
+    """A matrix [rows, cols] in FP4: codes uint8 [rows, cols/2] (two E2M1 codes a byte, the even
+    column in the low half), scales uint8 [ceil(rows/128), ceil(cols/64), 512] (E4M3 bytes in the
+    tiles of include/csa2.h) and an optional float32 scale of the whole matrix (one element);
+    value = code * scale * gscale."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    gscale: Optional[torch.Tensor] = None
+
+    @property
+    def rows(self):
+        return self.codes.shape[0]
+
+    @property
+    def cols(self):
+        return self.codes.shape[1] * 2
+
+    @staticmethod
+    def allocate(rows, cols, device, gscale=None):
+        if cols <= 0 or cols % 16:
+            raise ValueError(f"cols must be a positive multiple of 16 (got {cols})")
+        return Fp4Rows(torch.empty((rows, cols // 2), dtype=torch.uint8, device=device),
+                       torch.empty(((rows + 127) // 128, (cols + 63) // 64, 512), dtype=torch.uint8, device=device),
+                       gscale)
+
+    def row_scales(self):
+        """The scale bytes row by row: uint8 [rows, cols/16]."""
+        a, b = self.scales.shape[:2]
+        return self.scales.view(a, b, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(a * 128, b * 4)[:self.rows,
+                                                                                             :self.cols // 16]
+
+    def c_struct(self):
+        for t, n in [(self.codes, "codes"), (self.scales, "scales")]:
+            _expect(t, _U8, n)
+        if self.codes.dim() != 2 or self.scales.shape != ((self.rows + 127) // 128, (self.cols + 63) // 64, 512):
+            raise ValueError(f"scales {tuple(self.scales.shape)} do not belong to codes {tuple(self.codes.shape)}")
+        g = self.gscale
+        if g is not None:
+            _expect(g, _F32, "gscale")
+            if g.numel() != 1:
+                raise ValueError("gscale must have one element")
+        return _lib.Fp4RowsArg(_ptr(self.codes), _ptr(self.scales), _ptr(g), self.rows, self.cols)
+
+
+def _norm_args(x, weight, eps, residual, residual_out):
+    T, D = x.shape
+    a = _lib.RmsNormArgs()
+    a.struct_size = ctypes.sizeof(_lib.RmsNormArgs)
+    a.T, a.D, a.eps = T, D, eps
+    a.x, a.x_dtype, a.x_stride = _rows_of(x, "x"), _float_type(x, "x"), x.stride(0)
+    if weight is not None:
+        if weight.shape != (D,):
+            raise ValueError(f"weight must have {D} elements")
+        a.weight, a.weight_dtype = _rows_of(weight, "weight", 1), _float_type(weight, "weight")
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out without a residual")
+        return a, None
+    if residual_out is None:
+        residual_out = torch.empty((T, D), dtype=residual.dtype, device=x.device)
+    if residual.shape != x.shape or residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
+        raise ValueError("residual and residual_out must have x's shape and one type")
+    a.res_dtype = _float_type(residual, "residual")
+    a.residual, a.residual_stride = _rows_of(residual, "residual"), residual.stride(0)
+    a.residual_out, a.residual_out_stride = _rows_of(residual_out, "residual_out"), residual_out.stride(0)
+    return a, residual_out
+
+
+def rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, out_dtype=torch.bfloat16, out=None):
+    """Residual addition and root-mean-square norm: h = x + residual (kept in residual_out),
+    y = h / sqrt(mean(h^2) + eps) * weight.  x, residual [T, D] bf16 or float32 (rows may be
+    strided); residual_out may be residual itself.  Returns (y [T, D] bf16 or float32,
+    residual_out or None)."""
+    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
+    if out.shape != x.shape:
+        raise ValueError("out must have x's shape")
+    a.out_form, a.out, a.out_stride = _float_type(out, "out"), _rows_of(out, "out"), out.stride(0)
+    _launch("csa2_rms_norm", a)
+    return out, residual_out
+
+
+def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, group=0, out=None, out_scale=None):
+    """rms_norm with an E4M3 output and one float32 scale (amax / 448) for each row, or for each
+    128 channels of it (group=128).  Returns (out uint8 [T, D], out_scale float32 [T, 1 or
+    ceil(D/128)], residual_out or None)."""
+    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
+    T, D = x.shape
+    n = (D + group - 1) // group if group else 1
+    if out is None:
+        out = torch.empty((T, D), dtype=torch.uint8, device=x.device)
+    if out_scale is None:
+        out_scale = torch.empty((T, n), dtype=torch.float32, device=x.device)
+    _expect(out, _U8, "out")
+    _expect(out_scale, _F32, "out_scale")
+    if out.shape != x.shape or out_scale.shape != (T, n):
+        raise ValueError(f"out must have x's shape and out_scale must be [{T}, {n}]")
+    a.out_form, a.scale_group = FP8E4M3, group
+    a.out, a.out_stride, a.out_scale = _rows_of(out, "out"), out.stride(0), _ptr(out_scale)
+    _launch("csa2_rms_norm", a)
+    return out, out_scale, residual_out
+
+
+def rms_norm_fp4(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, gscale=None, out=None):
+    """rms_norm with its output as FP4 rows (D % 16 == 0), as fp4_quant of y would give them.
+    Returns (Fp4Rows, residual_out or None)."""
+    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
+    if out is None:
+        out = Fp4Rows.allocate(x.shape[0], x.shape[1], x.device, gscale)
+    elif gscale is not None:
+        raise ValueError("give gscale with out, or out alone")
+    a.out_form, a.out4 = FP4E2M1X2, out.c_struct()
+    _launch("csa2_rms_norm", a)
+    return out, residual_out
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
+
+
+def rope_table(positions, d_rope, *, theta=10000.0, scaling="none", factor=1.0, orig_positions=0, beta_fast=32.0,
+               beta_slow=1.0, magnitude=1.0, device="cuda", out=None):
+    """The rotary tables of positions [0, positions): (cos, sin), each float32 [positions,
+    d_rope/2], read by rope, compress_quant and compress_append.  scaling: "none", "linear"
+    (every frequency divided by factor) or "yarn" (blended by how often a channel turns within
+    orig_positions).  magnitude multiplies both tables."""
+    if scaling not in ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    if out is None:
+        shape = (max(0, positions), max(0, d_rope // 2))
+        out = (torch.empty(shape, dtype=torch.float32, device=device),
+               torch.empty(shape, dtype=torch.float32, device=device))
+    for t in out:
+        _expect(t, _F32, "out")
+        if t.shape != (positions, d_rope // 2):
+            raise ValueError(f"out tables must be [{positions}, {d_rope // 2}]")
+    a = _lib.RopeTableArgs(ctypes.sizeof(_lib.RopeTableArgs), positions, d_rope, ROPE_SCALING[scaling],
+                           orig_positions, theta, factor, beta_fast, beta_slow, magnitude, _ptr(out[0]),
+                           _ptr(out[1]))
+    _launch("csa2_rope_table", a)
+    return out
+
+
+def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=None):
+    """Rotary positions: the d_rope = 2 * cos.shape[1] channels of x [T, H, D] (bf16 or float32,
+    tokens and heads may be strided) from channel `first` on (by default the last d_rope, as in
+    the compressor) turn by the angles of pos int32 [T]; the others are copied.  Pairs (2i, 2i+1),
+    or (i, i + d_rope/2) with interleaved=False.  inverse turns back.  out=x works in place.
+    Returns out."""
+    T, H, D = x.shape
+    _expect(pos, _I32, "pos")
+    _expect(cos, _F32, "cos")
+    _expect(sin, _F32, "sin")
+    if cos.shape != sin.shape or cos.dim() != 2 or pos.shape != (T,):
+        raise ValueError("cos and sin must be [positions, d_rope/2] and pos [T]")
+    if out is None:
+        out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and type")
+    d_rope = 2 * cos.shape[1]
+    a = _lib.RopeArgs(ctypes.sizeof(_lib.RopeArgs), T, H, D, d_rope, D - d_rope if first is None else first,
+                      int(interleaved), int(inverse), _float_type(x, "x"), _rows_of(x, "x", 3),
+                      _rows_of(out, "out", 3), x.stride(0), x.stride(1), out.stride(0), out.stride(1), _ptr(pos),
+                      _ptr(cos), _ptr(sin), cos.shape[0])
+    _launch("csa2_rope", a)
+    return out
+
+
+def fp4_quant(x, gscale=None, out=None):
+    """Rows x [T, K] (bf16 or float32, rows may be strided, K % 16 == 0) to FP4 rows: x / gscale
+    with one E4M3 scale per 16 columns.  Returns Fp4Rows."""
+    p = _rows_of(x, "x")
+    if out is None:
+        out = Fp4Rows.allocate(x.shape[0], x.shape[1], x.device, gscale)
+    elif gscale is not None:
+        raise ValueError("give gscale with out, or out alone")
+    if (out.rows, out.cols) != tuple(x.shape):
+        raise ValueError("out must have x's shape")
+    a = _lib.Fp4QuantArgs(ctypes.sizeof(_lib.Fp4QuantArgs), p, _float_type(x, "x"), x.stride(0), out.c_struct())
+    _launch("csa2_fp4_quant", a)
+    return out
+
+
+def fp4_linear(x: Fp4Rows, w: Fp4Rows, *, out_dtype=torch.bfloat16, out=None):
+    """The product of FP4 rows x [T, K] with FP4 weights w [N, K] (K % 32 == 0) on the
+    block-scaled tensor cores.  Returns out [T, N] bf16 or float32."""
+    if out is None:
+        out = torch.empty((x.rows, w.rows), dtype=out_dtype, device=x.codes.device)
+    if out.shape != (x.rows, w.rows):
+        raise ValueError(f"out must be [{x.rows}, {w.rows}]")
+    a = _lib.Fp4LinearArgs(ctypes.sizeof(_lib.Fp4LinearArgs), x.c_struct(), w.c_struct(), _ptr(out),
+                           _float_type(out, "out"))
+    _launch("csa2_fp4_linear", a)
+    return out
 
 
 def device_error():

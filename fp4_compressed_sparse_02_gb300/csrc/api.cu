@@ -201,6 +201,139 @@ csa2_status check_swa_quant(const csa2_swa_quant_args* a) {
   return CSA2_OK;
 }
 
+bool is_float(csa2_dtype t) { return t == CSA2_BF16 || t == CSA2_F32; }
+bool on(const void* p, csa2_dtype t) { return ((uintptr_t)p & (t == CSA2_F32 ? 3 : 1)) == 0; }
+
+csa2_status check_fp4_rows(const csa2_fp4_rows& m, const char* name, int multiple) {
+  REQUIRE(m.rows >= 0 && m.rows <= (1 << 23), CSA2_ERR_UNSUPPORTED_SHAPE, "%s.rows must be in 0..2^23 (got %d)", name,
+          m.rows);
+  REQUIRE(m.cols > 0 && m.cols % multiple == 0, CSA2_ERR_UNSUPPORTED_SHAPE,
+          "%s.cols must be a positive multiple of %d (got %d)", name, multiple, m.cols);
+  if (m.rows > 0) {
+    REQUIRE(m.codes && m.scales, CSA2_ERR_INVALID_ARG, "%s.codes/scales is NULL", name);
+    REQUIRE(((uintptr_t)m.codes & 15) == 0 && ((uintptr_t)m.scales & 15) == 0, CSA2_ERR_INVALID_ARG,
+            "%s.codes/scales must be 16-byte aligned", name);
+    REQUIRE(((uintptr_t)m.gscale & 3) == 0, CSA2_ERR_INVALID_ARG, "%s.gscale must be 4-byte aligned", name);
+  }
+  return CSA2_OK;
+}
+
+csa2_status check_rms_norm(const csa2_rms_norm_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_rms_norm_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(a->T >= 0, CSA2_ERR_INVALID_ARG, "T < 0");
+  REQUIRE(a->D >= 1 && a->D <= 32768, CSA2_ERR_UNSUPPORTED_SHAPE, "D must be in 1..32768 (got %d)", a->D);
+  REQUIRE(is_float(a->x_dtype), CSA2_ERR_INVALID_ARG, "bad x_dtype");
+  REQUIRE(a->eps >= 0.f, CSA2_ERR_INVALID_ARG, "eps must be >= 0");
+  REQUIRE(!a->weight || is_float(a->weight_dtype), CSA2_ERR_INVALID_ARG, "bad weight_dtype");
+  REQUIRE(!a->weight || on(a->weight, a->weight_dtype), CSA2_ERR_INVALID_ARG, "weight is not aligned to its type");
+  REQUIRE(a->out_form >= CSA2_BF16 && a->out_form <= CSA2_FP4E2M1X2, CSA2_ERR_INVALID_ARG, "bad out_form");
+  if (a->out_form == CSA2_FP8E4M3)
+    REQUIRE(a->scale_group == 0 || a->scale_group == 128, CSA2_ERR_UNSUPPORTED_SHAPE,
+            "scale_group must be 0 or 128 (got %d)", a->scale_group);
+  if (a->out_form == CSA2_FP4E2M1X2) {
+    REQUIRE(a->out4.rows == a->T && a->out4.cols == a->D, CSA2_ERR_INVALID_ARG, "out4 must be [T][D]");
+    csa2_status s = check_fp4_rows(a->out4, "out4", 16);
+    if (s != CSA2_OK) return s;
+  }
+  if (a->T > 0) {
+    REQUIRE(a->x && on(a->x, a->x_dtype), CSA2_ERR_INVALID_ARG, "x is NULL or not aligned to its type");
+    if (a->residual) {
+      REQUIRE(is_float(a->res_dtype), CSA2_ERR_INVALID_ARG, "bad res_dtype");
+      REQUIRE(a->residual_out, CSA2_ERR_INVALID_ARG, "residual_out is NULL with a residual");
+      REQUIRE(on(a->residual, a->res_dtype) && on(a->residual_out, a->res_dtype), CSA2_ERR_INVALID_ARG,
+              "residual or residual_out is not aligned to its type");
+      REQUIRE(a->T == 1 || a->residual_out_stride >= a->D, CSA2_ERR_INVALID_ARG, "residual_out rows overlap");
+    } else {
+      REQUIRE(!a->residual_out, CSA2_ERR_INVALID_ARG, "residual_out without a residual");
+    }
+    if (a->out_form != CSA2_FP4E2M1X2) {
+      REQUIRE(a->out, CSA2_ERR_INVALID_ARG, "out is NULL");
+      REQUIRE(a->out_form == CSA2_FP8E4M3 || on(a->out, a->out_form), CSA2_ERR_INVALID_ARG,
+              "out is not aligned to its type");
+      REQUIRE(a->T == 1 || a->out_stride >= a->D, CSA2_ERR_INVALID_ARG, "out rows overlap");
+    }
+    if (a->out_form == CSA2_FP8E4M3)
+      REQUIRE(a->out_scale && on(a->out_scale, CSA2_F32), CSA2_ERR_INVALID_ARG, "out_scale is NULL or not aligned");
+  }
+  return CSA2_OK;
+}
+
+csa2_status check_rope(const csa2_rope_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_rope_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(a->T >= 0 && a->H >= 0, CSA2_ERR_INVALID_ARG, "T or H < 0");
+  REQUIRE(a->D >= 1 && a->D <= 4096, CSA2_ERR_UNSUPPORTED_SHAPE, "D must be in 1..4096 (got %d)", a->D);
+  REQUIRE(a->d_rope >= 2 && a->d_rope % 2 == 0, CSA2_ERR_UNSUPPORTED_SHAPE, "d_rope must be even and >= 2 (got %d)",
+          a->d_rope);
+  REQUIRE(a->rot_first >= 0 && a->rot_first <= a->D - a->d_rope, CSA2_ERR_INVALID_ARG,
+          "rot_first + d_rope must lie in 0..D");
+  REQUIRE(is_float(a->dtype), CSA2_ERR_INVALID_ARG, "bad dtype");
+  if (a->T > 0 && a->H > 0) {
+    REQUIRE(a->x && a->out && a->pos && a->rope_cos && a->rope_sin, CSA2_ERR_INVALID_ARG, "a required pointer is NULL");
+    REQUIRE(a->rope_max_pos > 0, CSA2_ERR_INVALID_ARG, "rope_max_pos must be positive");
+    REQUIRE(on(a->x, a->dtype) && on(a->out, a->dtype), CSA2_ERR_INVALID_ARG, "x or out is not aligned to its type");
+    REQUIRE(on(a->pos, CSA2_F32) && on(a->rope_cos, CSA2_F32) && on(a->rope_sin, CSA2_F32), CSA2_ERR_INVALID_ARG,
+            "pos or a table is not aligned to its type");
+    REQUIRE(a->out != a->x || (a->out_stride_t == a->x_stride_t && a->out_stride_h == a->x_stride_h),
+            CSA2_ERR_INVALID_ARG, "in place x and out must have the same strides");
+    // the heads of a token, or the tokens of a head, are the inner rows of the output
+    const int64_t st = a->T > 1 ? a->out_stride_t : INT64_MAX, sh = a->H > 1 ? a->out_stride_h : INT64_MAX;
+    const int64_t inner = sh <= st ? sh : st, outer = sh <= st ? st : sh, n = sh <= st ? a->H : a->T;
+    REQUIRE(inner >= a->D && (outer == INT64_MAX || outer >= (n - 1) * inner + a->D), CSA2_ERR_INVALID_ARG,
+            "out rows overlap");
+  }
+  return CSA2_OK;
+}
+
+csa2_status check_rope_table(const csa2_rope_table_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_rope_table_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(a->positions >= 0 && a->positions <= (1 << 24), CSA2_ERR_UNSUPPORTED_SHAPE,
+          "positions must be in 0..2^24 (got %d)", a->positions);
+  REQUIRE(a->d_rope >= 2 && a->d_rope % 2 == 0 && a->d_rope <= 256, CSA2_ERR_UNSUPPORTED_SHAPE,
+          "d_rope must be even and in 2..256 (got %d)", a->d_rope);
+  REQUIRE(a->scaling >= CSA2_ROPE_PLAIN && a->scaling <= CSA2_ROPE_YARN, CSA2_ERR_INVALID_ARG, "bad scaling");
+  REQUIRE(a->theta > 1.0 && a->theta <= 1e30, CSA2_ERR_INVALID_ARG, "theta must be in (1, 1e30]");
+  REQUIRE(a->magnitude > 0.0 && a->magnitude <= 1e30, CSA2_ERR_INVALID_ARG, "magnitude must be in (0, 1e30]");
+  if (a->scaling != CSA2_ROPE_PLAIN)
+    REQUIRE(a->factor >= 1.0 && a->factor <= 1e30, CSA2_ERR_INVALID_ARG, "factor must be in [1, 1e30]");
+  if (a->scaling == CSA2_ROPE_YARN) {
+    REQUIRE(a->orig_positions > 0, CSA2_ERR_INVALID_ARG, "orig_positions must be positive");
+    REQUIRE(a->beta_slow > 0.0 && a->beta_slow < a->beta_fast && a->beta_fast <= 1e30, CSA2_ERR_INVALID_ARG,
+            "need 0 < beta_slow < beta_fast");
+  }
+  if (a->positions > 0)
+    REQUIRE(a->rope_cos && a->rope_sin && on(a->rope_cos, CSA2_F32) && on(a->rope_sin, CSA2_F32), CSA2_ERR_INVALID_ARG,
+            "rope_cos/rope_sin is NULL or not aligned");
+  return CSA2_OK;
+}
+
+csa2_status check_fp4_quant(const csa2_fp4_quant_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_fp4_quant_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(is_float(a->x_dtype), CSA2_ERR_INVALID_ARG, "bad x_dtype");
+  csa2_status s = check_fp4_rows(a->out, "out", 16);
+  if (s != CSA2_OK) return s;
+  if (a->out.rows > 0)
+    REQUIRE(a->x && on(a->x, a->x_dtype), CSA2_ERR_INVALID_ARG, "x is NULL or not aligned to its type");
+  return CSA2_OK;
+}
+
+csa2_status check_fp4_linear(const csa2_fp4_linear_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_fp4_linear_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  csa2_status s = check_fp4_rows(a->x, "x", 32);
+  if (s != CSA2_OK) return s;
+  s = check_fp4_rows(a->w, "w", 32);
+  if (s != CSA2_OK) return s;
+  REQUIRE(a->x.cols == a->w.cols, CSA2_ERR_INVALID_ARG, "x.cols (%d) != w.cols (%d)", a->x.cols, a->w.cols);
+  REQUIRE(is_float(a->out_dtype), CSA2_ERR_INVALID_ARG, "bad out_dtype");
+  if (a->x.rows > 0 && a->w.rows > 0)
+    REQUIRE(a->out && on(a->out, a->out_dtype), CSA2_ERR_INVALID_ARG, "out is NULL or not aligned to its type");
+  return CSA2_OK;
+}
+
 csa2_status check_ws(size_t need, void* ws, size_t have) {
   REQUIRE(have >= need, CSA2_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes, got %zu", need, have);
   REQUIRE(need == 0 || ws, CSA2_ERR_INVALID_ARG, "workspace is NULL");
@@ -318,6 +451,36 @@ csa2_status csa2_swa_quant(const csa2_swa_quant_args* a, void* stream) {
   return cuda_status(csa2::launch_swa_quant(*a, static_cast<cudaStream_t>(stream)), "csa2_swa_quant");
 }
 
+csa2_status csa2_rms_norm(const csa2_rms_norm_args* a, void* stream) {
+  csa2_status s = check_rms_norm(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_rms_norm(*a, static_cast<cudaStream_t>(stream)), "csa2_rms_norm");
+}
+
+csa2_status csa2_rope(const csa2_rope_args* a, void* stream) {
+  csa2_status s = check_rope(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_rope(*a, static_cast<cudaStream_t>(stream)), "csa2_rope");
+}
+
+csa2_status csa2_rope_table(const csa2_rope_table_args* a, void* stream) {
+  csa2_status s = check_rope_table(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_rope_table(*a, static_cast<cudaStream_t>(stream)), "csa2_rope_table");
+}
+
+csa2_status csa2_fp4_quant(const csa2_fp4_quant_args* a, void* stream) {
+  csa2_status s = check_fp4_quant(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_fp4_quant(*a, static_cast<cudaStream_t>(stream)), "csa2_fp4_quant");
+}
+
+csa2_status csa2_fp4_linear(const csa2_fp4_linear_args* a, void* stream) {
+  csa2_status s = check_fp4_linear(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_fp4_linear(*a, static_cast<cudaStream_t>(stream)), "csa2_fp4_linear");
+}
+
 const char* csa2_last_error_message(void) { return g_msg; }
 
 csa2_status csa2_get_device_error(uint32_t* word) {
@@ -325,7 +488,8 @@ csa2_status csa2_get_device_error(uint32_t* word) {
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return cuda_status(e, "csa2_get_device_error");
   *word = csa2::read_clear_error_compress() | csa2::read_clear_error_proj() | csa2::read_clear_error_index() |
-          csa2::read_clear_error_score() | csa2::read_clear_error_attn();
+          csa2::read_clear_error_score() | csa2::read_clear_error_attn() | csa2::read_clear_error_rope() |
+          csa2::read_clear_error_fp4();
   csa2_status s = cuda_status(cudaGetLastError(), "csa2_get_device_error");
   if (s != CSA2_OK) return s;
   if (*word & CSA2_DEVERR_TIMEOUT) return fail(CSA2_ERR_TIMEOUT, "a bounded wait gave up (device word 0x%x)", *word);

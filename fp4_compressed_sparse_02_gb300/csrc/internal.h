@@ -51,4 +51,17 @@ cudaError_t launch_attn(const csa2_attn_args& a, void* ws, cudaStream_t st);
 uint32_t read_clear_error_attn();
 cudaError_t launch_selftest_wait(int polls, cudaStream_t st);
 
+// norm.cu
+cudaError_t launch_rms_norm(const csa2_rms_norm_args& a, cudaStream_t st);
+
+// rope.cu
+cudaError_t launch_rope(const csa2_rope_args& a, cudaStream_t st);
+cudaError_t launch_rope_table(const csa2_rope_table_args& a, cudaStream_t st);
+uint32_t read_clear_error_rope();
+
+// fp4.cu
+cudaError_t launch_fp4_quant(const csa2_fp4_quant_args& a, cudaStream_t st);
+cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st);
+uint32_t read_clear_error_fp4();
+
 }  // namespace csa2

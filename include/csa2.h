@@ -55,8 +55,8 @@ typedef enum csa2_status {
 } csa2_status;
 
 /* Element types.  CSA2_FP8E4M3 selects the compressed indexer-K plane (csa2_cache);
- * CSA2_FP4E2M1X2 names the packed Main KV codes (two E2M1 codes per byte), which no
- * argument takes as a choice. */
+ * CSA2_FP4E2M1X2 names packed E2M1 codes (two per byte): the Main KV codes, and the FP4 form
+ * of csa2_rms_norm's output. */
 typedef enum csa2_dtype { CSA2_BF16 = 0, CSA2_F32 = 1, CSA2_FP8E4M3 = 2, CSA2_FP4E2M1X2 = 3 } csa2_dtype;
 
 /* Device error word bits (csa2_get_device_error). */
@@ -411,6 +411,182 @@ typedef struct csa2_swa_quant_args {
 } csa2_swa_quant_args;
 
 csa2_status csa2_swa_quant(const csa2_swa_quant_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * FP4 rows: a matrix [rows][cols] of E2M1 codes with one E4M3 scale per 16 columns and one
+ * float32 scale of the whole matrix; value = code * scale * gscale.
+ *   codes   [rows][cols/2], two codes per byte, the even column in the low nibble
+ *   scales  tiles of 128 rows x 4 scales (64 columns), 512 bytes each, tile (i, j) =
+ *           (row / 128, column / 64) at index i * ceil(cols/64) + j; inside a tile, scale
+ *           c = column / 16 of row r is byte (r % 32) * 16 + (r % 128 / 32) * 4 + c % 4: the
+ *           order in which the block-scaled tensor-core product reads them.  Scales of
+ *           columns past cols must be 0 (csa2_fp4_quant and csa2_rms_norm write 0 there and
+ *           for the rows past the last).
+ * cols is a multiple of 16 (of 32 for csa2_fp4_linear).  codes and scales 16-byte aligned.
+ * The cache's planes (csa2_cache) hold the same codes and scales row by row instead: there
+ * an entry is read by gathering single rows.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_fp4_rows {
+  uint8_t* codes;              /* device [rows][cols/2] */
+  uint8_t* scales;             /* device [ceil(rows/128)][ceil(cols/64)][512] */
+  const float* gscale;         /* device f32 [1], positive; NULL = 1 */
+  int32_t rows;
+  int32_t cols;
+} csa2_fp4_rows;
+
+/* ------------------------------------------------------------------------------
+ * csa2_rms_norm -- the residual addition and root-mean-square norm between two blocks, with
+ * the quantiser of the product that follows.  For each row t:
+ *   h   = x + residual (float32), rounded to res_dtype and stored to residual_out;
+ *         without a residual h = x
+ *   ms  = mean_i h_i^2, summed in two float32 words (error 2^-46) and rounded once
+ *   y_i = (h_i * (1 / sqrt(ms + eps))) * weight_i, each operation rounded to float32
+ * and, by out_form:
+ *   CSA2_BF16 / CSA2_F32   out[t][i] = y_i, rounded once
+ *   CSA2_FP8E4M3           per group of scale_group channels (the whole row if 0):
+ *                          s = amax|y| / 448, byte = E4M3_RNE_satfinite(y / s) (float32
+ *                          divisions), s == 0 -> zero bytes: the rows csa2_swa_quant writes
+ *   CSA2_FP4E2M1X2         out4, as csa2_fp4_quant writes y
+ * The codes are decided on values that do not depend on how a row is split over threads.
+ * NaN and infinities follow the formulas; a NaN in a group gives it a NaN scale and zero codes.
+ * Strides are in elements between rows (the last dimension is contiguous); any alignment of
+ * the element type is accepted, 16-byte aligned rows are faster.  residual_out may be
+ * residual or x themselves, out may be x itself where the types agree; no other overlap.
+ * Supported: 1 <= D <= 32768; D % 16 == 0 for the FP4 form; scale_group 0 or 128.
+ * Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_rms_norm_args {
+  size_t struct_size;
+  int32_t T;                   /* rows */
+  int32_t D;                   /* channels */
+  const void* x;               /* device [T][D] */
+  csa2_dtype x_dtype;          /* CSA2_BF16 or CSA2_F32 */
+  csa2_dtype res_dtype;        /* type of residual and residual_out */
+  int64_t x_stride;
+  const void* residual;        /* device [T][D], or NULL */
+  void* residual_out;          /* device [T][D]; required with a residual */
+  int64_t residual_stride;
+  int64_t residual_out_stride;
+  const void* weight;          /* device [D], or NULL = 1 */
+  csa2_dtype weight_dtype;
+  float eps;                   /* >= 0 */
+  csa2_dtype out_form;
+  int32_t scale_group;         /* CSA2_FP8E4M3 only */
+  void* out;                   /* device [T][D] bf16, f32 or E4M3; unused in the FP4 form */
+  int64_t out_stride;
+  float* out_scale;            /* device f32 [T][ceil(D/scale_group) or 1] (CSA2_FP8E4M3) */
+  csa2_fp4_rows out4;          /* rows = T, cols = D (CSA2_FP4E2M1X2) */
+} csa2_rms_norm_args;
+
+csa2_status csa2_rms_norm(const csa2_rms_norm_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_rope -- rotary positions of T tokens x H heads x D channels: the d_rope channels from
+ * rot_first on turn by the angles of the token's position,
+ *   y0 = x0 * c - x1 * s,  y1 = x0 * s + x1 * c   (float32, each product rounded; inverse:
+ *   s negated), pair i = channels (2i, 2i+1) of the slice (interleaved, as the compressor
+ *   turns the Main KV entries) or (i, i + d_rope/2) (half),
+ * c, s = rope_cos / rope_sin[pos[t]][i], the compressor's tables.  The other channels are
+ * copied.  The inverse turns the attention output of shared K = V entries back, and is the
+ * gradient of the forward call with respect to x.
+ * out may be x itself (the same strides): then only the rotated channels are touched.  No
+ * other overlap.  A position outside [0, rope_max_pos) sets CSA2_DEVERR_POS and that token
+ * is copied unturned.
+ * Strides in elements; the channels of a head are contiguous.  Supported: 1 <= D <= 4096,
+ * even d_rope in 2..D.  Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_rope_args {
+  size_t struct_size;
+  int32_t T;
+  int32_t H;
+  int32_t D;
+  int32_t d_rope;
+  int32_t rot_first;           /* first rotated channel, rot_first + d_rope <= D */
+  int32_t interleaved;         /* 1: pairs (2i, 2i+1); 0: pairs (i, i + d_rope/2) */
+  int32_t inverse;
+  csa2_dtype dtype;            /* of x and out: CSA2_BF16 or CSA2_F32 */
+  const void* x;               /* device, element (t, h, c) at t*x_stride_t + h*x_stride_h + c */
+  void* out;
+  int64_t x_stride_t;
+  int64_t x_stride_h;
+  int64_t out_stride_t;
+  int64_t out_stride_h;
+  const int32_t* pos;          /* device [T] */
+  const float* rope_cos;       /* device f32 [rope_max_pos][d_rope/2] */
+  const float* rope_sin;
+  int32_t rope_max_pos;
+} csa2_rope_args;
+
+csa2_status csa2_rope(const csa2_rope_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_rope_table -- the tables csa2_rope and the compressor read: for p in [0, positions)
+ *   cos[p][i], sin[p][i] = magnitude * cos, sin(p * f_i)
+ *   CSA2_ROPE_PLAIN   f_i = theta^(-2i/d_rope)
+ *   CSA2_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   CSA2_ROPE_YARN    f_i blended with f_i / factor by how often channel i turns within
+ *                     orig_positions: beta_fast turns or more keep f_i, beta_slow or fewer
+ *                     take f_i / factor, a linear ramp over i joins the two ("YaRN", Peng
+ *                     et al. 2023, equations 17-23, with the ramp over the channel index)
+ * The angle is held as a 64-bit fraction of a turn, so that a far position loses nothing:
+ * |error| <= 2^-24 (1 + 1/2) * magnitude.
+ * Supported: even d_rope in 2..256, positions <= 2^24, theta > 1, factor >= 1,
+ * 0 < beta_slow < beta_fast.  Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef enum csa2_rope_scaling { CSA2_ROPE_PLAIN = 0, CSA2_ROPE_LINEAR = 1, CSA2_ROPE_YARN = 2 } csa2_rope_scaling;
+
+typedef struct csa2_rope_table_args {
+  size_t struct_size;
+  int32_t positions;
+  int32_t d_rope;
+  csa2_rope_scaling scaling;
+  int32_t orig_positions;      /* CSA2_ROPE_YARN: the context the model was trained on */
+  double theta;
+  double factor;
+  double beta_fast;
+  double beta_slow;
+  double magnitude;
+  float* rope_cos;             /* device f32 [positions][d_rope/2] */
+  float* rope_sin;
+} csa2_rope_table_args;
+
+csa2_status csa2_rope_table(const csa2_rope_table_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_fp4_quant -- rows to FP4 rows: u = x / gscale (float32 division), per 16 columns
+ *   s = E4M3_RNE_satfinite(amax|u| / 6), codes = E2M1_RNE_sat(u / s) (float32 divisions; s == 0
+ *   gives zero codes): the compressor's quantiser with a scale of the whole matrix in front.
+ * A NaN in a group gives it a NaN scale (0x7F) and zero codes; infinities saturate.
+ * Supported: x bf16 or f32, out.cols % 16 == 0.  Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_fp4_quant_args {
+  size_t struct_size;
+  const void* x;               /* device [out.rows][out.cols] */
+  csa2_dtype x_dtype;
+  int64_t x_stride;            /* elements between rows */
+  csa2_fp4_rows out;
+} csa2_fp4_quant_args;
+
+csa2_status csa2_fp4_quant(const csa2_fp4_quant_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_fp4_linear -- the product of FP4 rows with FP4 weights on the block-scaled tensor cores:
+ *   out[t][n] = x.gscale * w.gscale * sum_k x[t][k] * w[n][k]
+ * Products and block scales are exact; the sum runs in the tensor core's float32 accumulators
+ * (and, where the sum is split over CTAs, in a fixed order: results repeat bit for bit);
+ * one rounding to out_dtype.  A NaN scale byte (0x7F / 0xFF) makes its row's results NaN.
+ * Supported: x.cols == w.cols, a positive multiple of 32.  x.rows and w.rows >= 0.
+ * Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_fp4_linear_args {
+  size_t struct_size;
+  csa2_fp4_rows x;             /* [T][K] */
+  csa2_fp4_rows w;             /* [N][K] */
+  void* out;                   /* device [T][N] contiguous */
+  csa2_dtype out_dtype;        /* CSA2_BF16 or CSA2_F32 */
+} csa2_fp4_linear_args;
+
+csa2_status csa2_fp4_linear(const csa2_fp4_linear_args* args, void* stream);
 
 /* ------------------------------------------------------------------------------
  * Helpers
