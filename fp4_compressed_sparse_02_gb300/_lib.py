@@ -140,10 +140,9 @@ def lib():
         g.restype = c_i32
     L.csa2_swa_quant.argtypes = [ctypes.POINTER(SwaQuantArgs), c_vp]
     L.csa2_swa_quant.restype = c_i32
-    for name, st in [("csa2_rms_norm", RmsNormArgs), ("csa2_rope", RopeArgs), ("csa2_rope_table", RopeTableArgs),
-                     ("csa2_fp4_quant", Fp4QuantArgs), ("csa2_fp4_linear", Fp4LinearArgs)]:
+    for name in ["csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear"]:
         f = getattr(L, name)
-        f.argtypes = [ctypes.POINTER(st), c_vp]
+        f.argtypes = [c_vp, c_vp]          # a struct by reference, or its packed bytes
         f.restype = c_i32
     L.csa2_index_full_noalloc.argtypes = [ctypes.POINTER(IndexFullArgs), c_vp]
     L.csa2_index_full_noalloc.restype = c_i32

@@ -8,6 +8,7 @@ in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
 """
 import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
@@ -297,27 +298,50 @@ def swa_quant(x, swa, swa_scale, row_idx=None):
     _lib.check(_lib.lib().csa2_swa_quant(ctypes.byref(a), _stream()))
 
 
+_FLOAT = {torch.bfloat16: BF16, torch.float32: F32}
+
+
 def _float_type(t, name):
-    if t.dtype is torch.bfloat16:
-        return BF16
-    if t.dtype is torch.float32:
-        return F32
-    raise TypeError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
+    k = _FLOAT.get(t.dtype)
+    if k is None:
+        raise TypeError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
+    return k
 
 
-def _rows_of(t, name, ndim=2):
+def _rows_of(t, name):
     """Data pointer of a CUDA tensor whose last dimension is contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.dim() != ndim:
-        raise ValueError(f"{name}: expected {ndim} dimensions, got {t.dim()}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr()
 
 
-def _launch(fn, args):
-    _lib.check(getattr(_lib.lib(), fn)(ctypes.byref(args), _stream()))
+def _dense(t, dtype, name):
+    """Data pointer of a contiguous CUDA tensor of one type, None of None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+# The argument structs of the row operators as one packed string each: a call of a single token
+# costs more in ctypes field assignments than on the GPU.  0P pads a struct to its alignment.
+_FP4_ROWS = "PPPii"
+_RMS_NORM = struct.Struct("@NiiPiiqPPqqPifiiPqP" + _FP4_ROWS + "0P")
+_ROPE = struct.Struct("@NiiiiiiiiPPqqqqPPPi0P")
+_FP4_QUANT = struct.Struct("@NPiq" + _FP4_ROWS + "0P")
+_FP4_LINEAR = struct.Struct("@N" + 2 * _FP4_ROWS + "Pi0P")
+
+
+def _launch(fn, packed, t):
+    """Call fn on the current stream of tensor t's device."""
+    _lib.check(getattr(_lib.lib(), fn)(packed, torch._C._cuda_getCurrentRawStream(t.get_device())))
 
 
 @dataclass
@@ -352,41 +376,45 @@ class Fp4Rows:
         return self.scales.view(a, b, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(a * 128, b * 4)[:self.rows,
                                                                                              :self.cols // 16]
 
-    def c_struct(self):
-        for t, n in [(self.codes, "codes"), (self.scales, "scales")]:
-            _expect(t, _U8, n)
-        if self.codes.dim() != 2 or self.scales.shape != ((self.rows + 127) // 128, (self.cols + 63) // 64, 512):
+    def fields(self):
+        """(codes, scales, gscale, rows, cols) of the C struct, after its checks."""
+        rows, half = self.codes.shape
+        if self.scales.shape != ((rows + 127) // 128, (half + 31) // 32, 512):
             raise ValueError(f"scales {tuple(self.scales.shape)} do not belong to codes {tuple(self.codes.shape)}")
         g = self.gscale
-        if g is not None:
-            _expect(g, _F32, "gscale")
-            if g.numel() != 1:
-                raise ValueError("gscale must have one element")
-        return _lib.Fp4RowsArg(_ptr(self.codes), _ptr(self.scales), _ptr(g), self.rows, self.cols)
+        if g is not None and g.numel() != 1:
+            raise ValueError("gscale must have one element")
+        return (_dense(self.codes, torch.uint8, "codes"), _dense(self.scales, torch.uint8, "scales"),
+                _dense(g, torch.float32, "gscale"), rows, 2 * half)
 
 
-def _norm_args(x, weight, eps, residual, residual_out):
+def _norm(x, weight, eps, residual, residual_out, out_form, group, out, out_stride, out_scale, out4):
+    """One csa2_rms_norm call; returns residual_out (allocated here if need be)."""
     T, D = x.shape
-    a = _lib.RmsNormArgs()
-    a.struct_size = ctypes.sizeof(_lib.RmsNormArgs)
-    a.T, a.D, a.eps = T, D, eps
-    a.x, a.x_dtype, a.x_stride = _rows_of(x, "x"), _float_type(x, "x"), x.stride(0)
+    wp = wt = rp = rs = op = os_ = rt = 0
     if weight is not None:
         if weight.shape != (D,):
             raise ValueError(f"weight must have {D} elements")
-        a.weight, a.weight_dtype = _rows_of(weight, "weight", 1), _float_type(weight, "weight")
-    if residual is None:
-        if residual_out is not None:
-            raise ValueError("residual_out without a residual")
-        return a, None
-    if residual_out is None:
-        residual_out = torch.empty((T, D), dtype=residual.dtype, device=x.device)
-    if residual.shape != x.shape or residual_out.shape != x.shape or residual_out.dtype != residual.dtype:
-        raise ValueError("residual and residual_out must have x's shape and one type")
-    a.res_dtype = _float_type(residual, "residual")
-    a.residual, a.residual_stride = _rows_of(residual, "residual"), residual.stride(0)
-    a.residual_out, a.residual_out_stride = _rows_of(residual_out, "residual_out"), residual_out.stride(0)
-    return a, residual_out
+        wp, wt = _rows_of(weight, "weight"), _float_type(weight, "weight")
+    if residual is not None:
+        if residual_out is None:
+            residual_out = torch.empty((T, D), dtype=residual.dtype, device=x.device)
+        elif residual_out.shape != x.shape or residual_out.dtype is not residual.dtype:
+            raise ValueError("residual and residual_out must have x's shape and one type")
+        if residual.shape != x.shape:
+            raise ValueError("residual and residual_out must have x's shape and one type")
+        rt = _float_type(residual, "residual")
+        rp, rs = _rows_of(residual, "residual"), residual.stride(0)
+        op, os_ = _rows_of(residual_out, "residual_out"), residual_out.stride(0)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual")
+    _launch("csa2_rms_norm", _RMS_NORM.pack(
+        _RMS_NORM.size, T, D, _rows_of(x, "x"), _float_type(x, "x"), rt, x.stride(0), rp, op, rs, os_, wp, wt, eps,
+        out_form, group, out, out_stride, out_scale, *out4), x)
+    return residual_out
+
+
+_NO_FP4 = (0, 0, 0, 0, 0)
 
 
 def rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, out_dtype=torch.bfloat16, out=None):
@@ -394,48 +422,41 @@ def rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, out_
     y = h / sqrt(mean(h^2) + eps) * weight.  x, residual [T, D] bf16 or float32 (rows may be
     strided); residual_out may be residual itself.  Returns (y [T, D] bf16 or float32,
     residual_out or None)."""
-    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
     if out is None:
         out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
-    if out.shape != x.shape:
+    elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
-    a.out_form, a.out, a.out_stride = _float_type(out, "out"), _rows_of(out, "out"), out.stride(0)
-    _launch("csa2_rms_norm", a)
-    return out, residual_out
+    return out, _norm(x, weight, eps, residual, residual_out, _float_type(out, "out"), 0, _rows_of(out, "out"),
+                      out.stride(0), 0, _NO_FP4)
 
 
 def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, group=0, out=None, out_scale=None):
     """rms_norm with an E4M3 output and one float32 scale (amax / 448) for each row, or for each
     128 channels of it (group=128).  Returns (out uint8 [T, D], out_scale float32 [T, 1 or
     ceil(D/128)], residual_out or None)."""
-    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
     T, D = x.shape
     n = (D + group - 1) // group if group else 1
     if out is None:
         out = torch.empty((T, D), dtype=torch.uint8, device=x.device)
+    elif out.dtype is not torch.uint8 or out.shape != x.shape:
+        raise ValueError("out must be uint8 with x's shape")
     if out_scale is None:
         out_scale = torch.empty((T, n), dtype=torch.float32, device=x.device)
-    _expect(out, _U8, "out")
-    _expect(out_scale, _F32, "out_scale")
-    if out.shape != x.shape or out_scale.shape != (T, n):
-        raise ValueError(f"out must have x's shape and out_scale must be [{T}, {n}]")
-    a.out_form, a.scale_group = FP8E4M3, group
-    a.out, a.out_stride, a.out_scale = _rows_of(out, "out"), out.stride(0), _ptr(out_scale)
-    _launch("csa2_rms_norm", a)
+    elif out_scale.shape != (T, n):
+        raise ValueError(f"out_scale must be [{T}, {n}]")
+    residual_out = _norm(x, weight, eps, residual, residual_out, FP8E4M3, group, _rows_of(out, "out"), out.stride(0),
+                         _dense(out_scale, torch.float32, "out_scale"), _NO_FP4)
     return out, out_scale, residual_out
 
 
 def rms_norm_fp4(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, gscale=None, out=None):
     """rms_norm with its output as FP4 rows (D % 16 == 0), as fp4_quant of y would give them.
     Returns (Fp4Rows, residual_out or None)."""
-    a, residual_out = _norm_args(x, weight, eps, residual, residual_out)
     if out is None:
         out = Fp4Rows.allocate(x.shape[0], x.shape[1], x.device, gscale)
     elif gscale is not None:
         raise ValueError("give gscale with out, or out alone")
-    a.out_form, a.out4 = FP4E2M1X2, out.c_struct()
-    _launch("csa2_rms_norm", a)
-    return out, residual_out
+    return out, _norm(x, weight, eps, residual, residual_out, FP4E2M1X2, 0, 0, 0, 0, out.fields())
 
 
 ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
@@ -449,18 +470,16 @@ def rope_table(positions, d_rope, *, theta=10000.0, scaling="none", factor=1.0, 
     orig_positions).  magnitude multiplies both tables."""
     if scaling not in ROPE_SCALING:
         raise ValueError(f"scaling must be one of {sorted(ROPE_SCALING)}")
+    shape = (max(0, positions), max(0, d_rope // 2))
     if out is None:
-        shape = (max(0, positions), max(0, d_rope // 2))
         out = (torch.empty(shape, dtype=torch.float32, device=device),
                torch.empty(shape, dtype=torch.float32, device=device))
-    for t in out:
-        _expect(t, _F32, "out")
-        if t.shape != (positions, d_rope // 2):
-            raise ValueError(f"out tables must be [{positions}, {d_rope // 2}]")
+    elif out[0].shape != shape or out[1].shape != shape:
+        raise ValueError(f"out tables must be {list(shape)}")
+    cos, sin = (_dense(t, torch.float32, "table") for t in out)
     a = _lib.RopeTableArgs(ctypes.sizeof(_lib.RopeTableArgs), positions, d_rope, ROPE_SCALING[scaling],
-                           orig_positions, theta, factor, beta_fast, beta_slow, magnitude, _ptr(out[0]),
-                           _ptr(out[1]))
-    _launch("csa2_rope_table", a)
+                           orig_positions, theta, factor, beta_fast, beta_slow, magnitude, cos, sin)
+    _launch("csa2_rope_table", ctypes.byref(a), out[0])
     return out
 
 
@@ -471,49 +490,48 @@ def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=N
     or (i, i + d_rope/2) with interleaved=False.  inverse turns back.  out=x works in place.
     Returns out."""
     T, H, D = x.shape
-    _expect(pos, _I32, "pos")
-    _expect(cos, _F32, "cos")
-    _expect(sin, _F32, "sin")
-    if cos.shape != sin.shape or cos.dim() != 2 or pos.shape != (T,):
+    positions, half = cos.shape
+    if sin.shape != cos.shape or pos.shape != (T,):
         raise ValueError("cos and sin must be [positions, d_rope/2] and pos [T]")
     if out is None:
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype:
+    elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
-    d_rope = 2 * cos.shape[1]
-    a = _lib.RopeArgs(ctypes.sizeof(_lib.RopeArgs), T, H, D, d_rope, D - d_rope if first is None else first,
-                      int(interleaved), int(inverse), _float_type(x, "x"), _rows_of(x, "x", 3),
-                      _rows_of(out, "out", 3), x.stride(0), x.stride(1), out.stride(0), out.stride(1), _ptr(pos),
-                      _ptr(cos), _ptr(sin), cos.shape[0])
-    _launch("csa2_rope", a)
+    xt, xh, _ = x.stride()
+    ot, oh, _ = out.stride()
+    _launch("csa2_rope", _ROPE.pack(
+        _ROPE.size, T, H, D, 2 * half, D - 2 * half if first is None else first, 1 if interleaved else 0,
+        1 if inverse else 0, _float_type(x, "x"), _rows_of(x, "x"), _rows_of(out, "out"), xt, xh, ot, oh,
+        _dense(pos, torch.int32, "pos"), _dense(cos, torch.float32, "cos"), _dense(sin, torch.float32, "sin"),
+        positions), x)
     return out
 
 
 def fp4_quant(x, gscale=None, out=None):
     """Rows x [T, K] (bf16 or float32, rows may be strided, K % 16 == 0) to FP4 rows: x / gscale
     with one E4M3 scale per 16 columns.  Returns Fp4Rows."""
-    p = _rows_of(x, "x")
+    T, K = x.shape
     if out is None:
-        out = Fp4Rows.allocate(x.shape[0], x.shape[1], x.device, gscale)
+        out = Fp4Rows.allocate(T, K, x.device, gscale)
     elif gscale is not None:
         raise ValueError("give gscale with out, or out alone")
-    if (out.rows, out.cols) != tuple(x.shape):
+    elif out.codes.shape != (T, K // 2):
         raise ValueError("out must have x's shape")
-    a = _lib.Fp4QuantArgs(ctypes.sizeof(_lib.Fp4QuantArgs), p, _float_type(x, "x"), x.stride(0), out.c_struct())
-    _launch("csa2_fp4_quant", a)
+    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, _rows_of(x, "x"), _float_type(x, "x"), x.stride(0),
+                                              *out.fields()), x)
     return out
 
 
 def fp4_linear(x: Fp4Rows, w: Fp4Rows, *, out_dtype=torch.bfloat16, out=None):
     """The product of FP4 rows x [T, K] with FP4 weights w [N, K] (K % 32 == 0) on the
     block-scaled tensor cores.  Returns out [T, N] bf16 or float32."""
+    fx, fw = x.fields(), w.fields()
     if out is None:
-        out = torch.empty((x.rows, w.rows), dtype=out_dtype, device=x.codes.device)
-    if out.shape != (x.rows, w.rows):
-        raise ValueError(f"out must be [{x.rows}, {w.rows}]")
-    a = _lib.Fp4LinearArgs(ctypes.sizeof(_lib.Fp4LinearArgs), x.c_struct(), w.c_struct(), _ptr(out),
-                           _float_type(out, "out"))
-    _launch("csa2_fp4_linear", a)
+        out = torch.empty((fx[3], fw[3]), dtype=out_dtype, device=x.codes.device)
+    elif out.shape != (fx[3], fw[3]):
+        raise ValueError(f"out must be [{fx[3]}, {fw[3]}]")
+    _launch("csa2_fp4_linear", _FP4_LINEAR.pack(_FP4_LINEAR.size, *fx, *fw, _dense(out, out.dtype, "out"),
+                                                _float_type(out, "out")), out)
     return out
 
 

@@ -85,18 +85,19 @@ constexpr int BKB = 128;                   // bytes of codes per row and stage: 
 constexpr int THREADS = 192;               // warps 0..3 epilogue, 4 loads, 5 products
 constexpr uint32_t MAX_POLL = 1u << 24;
 
-template <int BN>                          // tokens of a tile: TMEM columns
+template <int BN>                          // tokens, up to 128: TMEM columns
 struct Cfg {
-  static constexpr int XATOMS = (BN + 127) / 128;                  // 128-row scale tiles of x
-  static constexpr int A = BM * BKB, B = BN * BKB, SFA = 4 * 512, SFB = XATOMS * 4 * 512;
-  static constexpr int STAGE = A + B + SFA + SFB;
+  static constexpr int A = BM * BKB, B = BN * BKB, SF = 4 * 512;   // SF: scale tiles of w, and of x
+  static constexpr int STAGE = A + B + 2 * SF;
   static constexpr int STAGES = (212 * 1024) / STAGE < 9 ? (212 * 1024) / STAGE : 9;
+  // stages of a CTA that leaves room for a second one on its SM (TMEM: 256 columns each)
+  static constexpr int STAGES2 = (113 * 1024) / STAGE < 4 ? (113 * 1024) / STAGE : 4;
   static constexpr int SMEM = STAGES * STAGE + 256;
   static constexpr int DCOLS = BN < 32 ? 32 : BN;
-  // two sets of scale columns: 4 per 64-column step for w, 4 per step and atom for x
-  static constexpr int SFCOLS = 16 + 16 * XATOMS;
-  static constexpr int COLS = DCOLS + 2 * SFCOLS <= 128 ? 128 : DCOLS + 2 * SFCOLS <= 256 ? 256 : 512;
+  static constexpr int SFCOLS = 32;        // scale columns of a stage: 4 per 64-column step, for w and for x
   static_assert(B % 1024 == 0 && STAGE % 1024 == 0, "operand tiles start on 1024-byte boundaries");
+  static_assert(STAGES2 * STAGE >= BN * 512, "a partial result fits where the stages were");
+  static_assert(DCOLS + STAGES * SFCOLS <= 512 && DCOLS + STAGES2 * SFCOLS <= 256, "TMEM columns");
 };
 
 struct Params {
@@ -105,8 +106,8 @@ struct Params {
   const float* gx;
   const float* gw;
   void* out;
-  int T, N, nkt;
-  bool out32;
+  int T, N, nkt, stages, tmem_cols;
+  bool out32, vec4;                        // vec4: rows of out are whole, aligned groups of four
 };
 
 // Instruction descriptor of kind::mxf4nvf4: E2M1 operands (1), both K-major, E4M3 scales (0),
@@ -115,24 +116,33 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
   return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// Shared-memory descriptor of one scale tile: 8-row groups of 16-byte rows, 128 bytes apart,
-// no swizzle.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-  return (uint64_t)((saddr >> 4) & 0x3FFF) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+// The descriptors' upper words are constants and their lower words the address / 16 (csrc/tc.cuh),
+// so that the issuing thread adds one 32-bit offset an instruction: at 100 to 200 cycles of
+// tensor work per product, its own instructions are what a product waits for.
+constexpr uint32_t kOperandHi = (1024 >> 4) | (1u << 14) | (2u << 29);   // SBO 1024, version, 128-byte swizzle
+constexpr uint32_t kScaleHi = (128 >> 4) | (1u << 14);                   // SBO 128, version, no swizzle
+
+// One lane of the converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r != 0;
 }
 
 // One 512-byte scale tile into four TMEM columns (column j, lane l: the four scales of row
 // 32 j + l), repeated for the four lane quarters.
-__device__ __forceinline__ void sf_copy(uint32_t tmem, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" :: "r"(tmem), "l"(desc) : "memory");
+__device__ __forceinline__ void sf_copy(uint32_t tmem, uint32_t lo) {
+  asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], t;\n}"
+               :: "r"(tmem), "r"(lo), "r"(kScaleHi) : "memory");
 }
 
-__device__ __forceinline__ void mma_fp4(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t sfa, uint32_t sfb,
+__device__ __forceinline__ void mma_fp4(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t sfa, uint32_t sfb,
                                         uint32_t accumulate) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n}"
-      :: "r"(d), "l"(a), "l"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate) : "memory");
+      "{\n .reg .pred p;\n .reg .b64 ta, tb;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 ta, {%1, %7};\n mov.b64 tb, {%2, %7};\n"
+      " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ta, tb, %3, [%4], [%5], p;\n}"
+      :: "r"(d), "r"(a), "r"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(kOperandHi) : "memory");
 }
 
 __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t a) {
@@ -141,20 +151,44 @@ __device__ __forceinline__ float4 ld_dsmem_f4(uint32_t a) {
   return v;
 }
 
-__device__ __forceinline__ void put(const Params& p, long long at, float v) {
+template <typename P>
+__device__ __forceinline__ void put(const P& p, long long at, float v) {
   if (p.out32)
     static_cast<float*>(p.out)[at] = v;
   else
     static_cast<uint16_t*>(p.out)[at] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
+// Four neighbouring results, of which the first n exist.
+template <typename P>
+__device__ __forceinline__ void put4(const P& p, long long at, int n, float a, float b, float c, float d) {
+  if (p.vec4) {
+    if (p.out32)
+      *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(a, b, c, d);
+    else
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + at) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
+    return;
+  }
+  put(p, at, a);
+  if (n > 1) put(p, at + 1, b);
+  if (n > 2) put(p, at + 2, c);
+  if (n > 3) put(p, at + 3, d);
+}
+
 }  // namespace lin
 
-// Tile = 128 features x BN tokens of out^T = w x^T, so that few tokens fill the N side of the
-// product and the weights stream through the M side.  A cluster of S CTAs splits the sum over
-// K; each leaves its float32 partial in shared memory and the CTAs add them in rank order.
+// Up to 128 tokens: what bounds it is reading the weights once.  Tile = 128 features x BN tokens of
+// out^T = w x^T, so that few tokens fill the N side of the product and the weights stream through
+// the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32 partial in shared
+// memory and the CTAs add them in rank order.
+//   Occupancy: at 1 x 5120 -> 32768 (256 tiles) one CTA an SM with nine stages takes 21.0 us, two
+// with four stages 17.2 us (its loads alone: 17.2 us; the floor of 94 MB is 13.9 us): a second
+// CTA's loads run during the first's start and end.
+//   Split, 1 x 32768 -> 5120 (40 tiles), two CTAs an SM: S = 1 51 us, 3 21.1 us, 6 17.8 us, 7 26.3 us
+// (clusters of seven pack badly: some wait for a second round), so S is the largest whose
+// clusters all run at once.
 template <int BN>
-__global__ void __launch_bounds__(lin::THREADS, 1)
+__global__ void __launch_bounds__(lin::THREADS)
     k_fp4_linear(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, lin::Params p) {
   using namespace lin;
   using C = Cfg<BN>;
@@ -162,19 +196,19 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
   pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * C::STAGE);
   uint64_t* empty = full + C::STAGES;
   uint64_t* accf = empty + C::STAGES;
   uint32_t* tslot = reinterpret_cast<uint32_t*>(accf + 1);
   volatile int* failed = reinterpret_cast<volatile int*>(accf + 2);
   const int S = (int)gridDim.x / ((p.N + BM - 1) / BM);   // CTAs of a cluster
   const int rank = blockIdx.x % S;
-  const int f0 = (blockIdx.x / S) * BM, t0 = blockIdx.y * BN;
+  const int f0 = (blockIdx.x / S) * BM;
   const int nkb = (p.nkt + 3) / 4;
   const int kb0 = (int)((long long)nkb * rank / S), kb1 = (int)((long long)nkb * (rank + 1) / S);
   // the same in every CTA; the barriers of a cluster are reached either way
   const bool aligned = (smem_u32(smem) & 1023) == 0;
-  if (warp == 5) tc::tmem_alloc(tslot, C::COLS);
+  if (warp == 5) tc::tmem_alloc(tslot, p.tmem_cols);
   if (tid == 0) {
     for (int s = 0; s < C::STAGES; ++s) {
       tc::mbar_init(&full[s], 1);
@@ -191,59 +225,62 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tb = *tslot;
-  const int xa0 = t0 >> 7;                                // first scale tile row of the tokens
-  const int xatoms = min(C::XATOMS, ((p.T + 127) >> 7) - xa0);
   int issued = kb0;                                       // loads of [kb0, issued) are on their way
   if (warp == 4) {
     if (lane == 0 && aligned) {
       for (int kb = kb0; kb < kb1; ++kb) {
-        const int it = kb - kb0, s = it % C::STAGES;
-        if (it >= C::STAGES && !tc::mbar_wait(&empty[s], (uint32_t)((it / C::STAGES - 1) & 1), MAX_POLL)) {
+        const int it = kb - kb0, s = it % p.stages;
+        if (it >= p.stages && !tc::mbar_wait(&empty[s], (uint32_t)((it / p.stages - 1) & 1), MAX_POLL)) {
           raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
           *failed = 1;
           break;
         }
         uint8_t* st = smem + s * C::STAGE;
         const int nt = min(4, p.nkt - 4 * kb);            // 64-column steps of this stage
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(C::A + C::B + nt * 512 * (1 + xatoms)));
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(C::A + C::B + nt * 1024));
         tc::tma_load_2d(st, &mw, kb * BKB, f0, &full[s]);
-        tc::tma_load_2d(st + C::A, &mx, kb * BKB, t0, &full[s]);
+        tc::tma_load_2d(st + C::A, &mx, kb * BKB, 0, &full[s]);
         uint8_t* sf = st + C::A + C::B;
         tc::bulk_load(sf, p.wt + ((long long)(f0 >> 7) * p.nkt + 4 * kb) * 512, nt * 512, &full[s]);
-        for (int j = 0; j < xatoms; ++j)
-          tc::bulk_load(sf + C::SFA + j * 2048, p.xt + ((long long)(xa0 + j) * p.nkt + 4 * kb) * 512, nt * 512, &full[s]);
+        tc::bulk_load(sf + C::SF, p.xt + (long long)4 * kb * 512, nt * 512, &full[s]);
         issued = kb + 1;
       }
     }
   } else if (warp == 5) {
-    if (lane == 0 && aligned) {
+    if (aligned) {
       constexpr uint32_t id = idesc(BM, BN);
-      const uint32_t sf0 = tb + C::DCOLS;
-      // tokens that start inside a 128-row scale tile start at a later column of it
-      const uint32_t xcol = (uint32_t)((t0 & 127) >> 5);
+      const uint32_t sf0 = tb + C::DCOLS, base = smem_u32(smem) >> 4;
+      int s = 0;
+      uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        const int it = kb - kb0, s = it % C::STAGES;
-        if (!tc::mbar_wait(&full[s], (uint32_t)((it / C::STAGES) & 1), MAX_POLL)) {
-          raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
-          *failed = 1;
+        if (!tc::mbar_wait_warp(&full[s], phase, MAX_POLL)) {
+          if (lane == 0) {
+            raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+            *failed = 1;
+          }
           break;
         }
         tc::fence_after_sync();
-        const uint32_t a = smem_u32(smem + s * C::STAGE), b = a + C::A, sf = b + C::B;
-        const uint32_t sft = sf0 + (it & 1) * C::SFCOLS;
+        const uint32_t a = base + (uint32_t)s * (C::STAGE >> 4), sft = sf0 + (uint32_t)s * C::SFCOLS;
         const int nt = min(4, p.nkt - 4 * kb);
-        for (int k = 0; k < nt; ++k) {
-          sf_copy(sft + 4 * k, sf_desc(sf + 512 * k));
+        if (elect_one()) {
 #pragma unroll
-          for (int j = 0; j < C::XATOMS; ++j)
-            sf_copy(sft + 16 + 4 * (C::XATOMS * k + j), sf_desc(sf + C::SFA + 2048 * j + 512 * k));
+          for (int k = 0; k < 4; ++k)
+            if (k < nt) {
+              sf_copy(sft + 4 * k, a + ((C::A + C::B + 512 * k) >> 4));
+              sf_copy(sft + 16 + 4 * k, a + ((C::A + C::B + C::SF + 512 * k) >> 4));
+            }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < nt)
+              mma_fp4(tb, a + 2 * k, a + ((C::A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 4 * k, kb > kb0 || k > 0);
+          tc::mma_commit(&empty[s]);
         }
-        for (int k = 0; k < nt; ++k)
-          mma_fp4(tb, tc::smem_desc_sw128(a + 32 * k, 16, 1024), tc::smem_desc_sw128(b + 32 * k, 16, 1024), id,
-                  sft + 4 * k, sft + 16 + 4 * C::XATOMS * k + xcol, (it | k) != 0 ? 1u : 0u);
-        tc::mma_commit(&empty[s]);
+        __syncwarp();
+        if (++s == p.stages) s = 0, phase ^= 1;
       }
-      tc::mma_commit(accf);
+      if (elect_one()) tc::mma_commit(accf);
+      __syncwarp();
     }
   } else if (aligned) {
     if (!tc::mbar_wait_warp(accf, 0, MAX_POLL)) {
@@ -257,28 +294,27 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
   __syncthreads();
   const bool bad = *failed != 0;
   if (warp == 4 && lane == 0 && bad) {                    // copies in flight land before the CTA leaves
-    for (int kb = issued - min(issued - kb0, C::STAGES); kb < issued; ++kb)
-      tc::mbar_wait(&full[(kb - kb0) % C::STAGES], (uint32_t)(((kb - kb0) / C::STAGES) & 1), MAX_POLL);
+    for (int kb = issued - min(issued - kb0, p.stages); kb < issued; ++kb)
+      tc::mbar_wait(&full[(kb - kb0) % p.stages], (uint32_t)(((kb - kb0) / p.stages) & 1), MAX_POLL);
   }
-  const int nt = min(BN, p.T - t0);                       // tokens that exist
   const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
   if (warp < 4 && !bad) {
     const uint32_t tq = tb + ((uint32_t)(32 * warp) << 16);
     const int f = 32 * warp + lane;
     float* part = reinterpret_cast<float*>(smem);
 #pragma unroll 1
-    for (int c = 0; c < nt; c += 32) {
+    for (int c = 0; c < p.T; c += 32) {
       uint32_t v[32];
       tc::tmem_ld32(tq + (uint32_t)c, v);
       tc::tmem_ld_wait();
       if (S > 1) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < nt) part[(c + i) * BM + f] = __uint_as_float(v[i]);
+          if (c + i < p.T) part[(c + i) * BM + f] = __uint_as_float(v[i]);
       } else if (f0 + f < p.N) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-          if (c + i < nt) put(p, (long long)(t0 + c + i) * p.N + f0 + f, __uint_as_float(v[i]) * alpha);
+          if (c + i < p.T) put(p, (long long)(c + i) * p.N + f0 + f, __uint_as_float(v[i]) * alpha);
       }
     }
   }
@@ -287,17 +323,17 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
     tc::cluster_sync();
     if (warp < 4 && !bad) {
       const uint32_t mine = smem_u32(smem);
-      for (int u = rank * 128 + tid; u < nt * (BM / 4); u += S * 128) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int q = 0; q < S; ++q) {
-          const float4 v = ld_dsmem_f4(tc::mapa(mine, q) + 16 * u);
-          s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-        }
-        const int t = u / (BM / 4), f = f0 + 4 * (u % (BM / 4));
-        const float e[4] = {s.x, s.y, s.z, s.w};
+      for (int u = rank * 128 + tid; u < p.T * (BM / 4); u += S * 128) {
+        float4 v[8];                                      // every peer's piece, on its way at once
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (f + i < p.N) put(p, (long long)(t0 + t) * p.N + f + i, e[i] * alpha);
+        for (int q = 0; q < 8; ++q)
+          if (q < S) v[q] = ld_dsmem_f4(tc::mapa(mine, q) + 16 * u);
+        float4 s = v[0];
+#pragma unroll
+        for (int q = 1; q < 8; ++q)
+          if (q < S) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
+        const int t = u / (BM / 4), f = f0 + 4 * (u % (BM / 4));
+        if (f < p.N) put4(p, (long long)t * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
       }
     }
     __syncwarp();
@@ -305,10 +341,393 @@ __global__ void __launch_bounds__(lin::THREADS, 1)
   }
   tc::fence_before_sync();
   __syncthreads();
-  if (warp == 5) tc::tmem_dealloc(tb, C::COLS);
+  if (warp == 5) tc::tmem_dealloc(tb, p.tmem_cols);
+}
+
+// ---------------------------------------------------------------------------------
+// Product of many tokens: CTA pairs
+// ---------------------------------------------------------------------------------
+namespace pairs {
+
+using lin::BKB;
+using lin::BM;
+using lin::MAX_POLL;
+constexpr int BN = 256;                    // features of a tile; each CTA holds half of their rows
+constexpr int EPI = 8;                     // epilogue warps; then a warp of loads, one of products
+constexpr int THREADS = 32 * (EPI + 2);
+constexpr int A = BM * BKB, B = BN / 2 * BKB, SFA = 4 * 512, SFB = 2 * 4 * 512;
+constexpr int STAGE = A + B + SFA + SFB;   // 38 KB
+constexpr int STAGES = 5;
+constexpr int SLICE = 2048;                // 32 rows x 32 bf16 columns on their way out
+constexpr int OUT = STAGES * STAGE;        // two slices for each epilogue warp
+constexpr int BARS = OUT + EPI * 2 * SLICE;
+constexpr int SMEM = BARS + 256;
+constexpr int SFCOLS = 16 + 32;            // scale columns of a stage, beside the accumulator: a stage's scales
+                                           // stay until its products are done
+static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BN + STAGES * SFCOLS <= 512, "alignment, TMEM columns");
+
+struct Params {
+  const float* gx;
+  const float* gw;
+  void* out;
+  int T, N, nkt, nft, ntt, band, split;
+  bool out32, tma_out, vec4;
+};
+
+__device__ __forceinline__ void tmem_alloc2(uint32_t* slot, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+               :: "r"((uint32_t)__cvta_generic_to_shared(slot)), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc2(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" :: "r"(taddr), "r"(ncols) : "memory");
+}
+
+// The scale tile at the same place in both CTAs' shared memory into both CTAs' TMEM.
+__device__ __forceinline__ void sf_copy2(uint32_t tmem, uint32_t lo) {
+  asm volatile("{\n .reg .b64 t;\n mov.b64 t, {%1, %2};\n tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], t;\n}"
+               :: "r"(tmem), "r"(lo), "r"(lin::kScaleHi) : "memory");
+}
+
+__device__ __forceinline__ void mma_fp4_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t sfa, uint32_t sfb,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b64 ta, tb;\n setp.ne.b32 p, %6, 0;\n"
+      " mov.b64 ta, {%1, %7};\n mov.b64 tb, {%2, %7};\n"
+      " tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], ta, tb, %3, [%4], [%5], p;\n}"
+      :: "r"(d), "r"(a), "r"(b), "r"(id), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(lin::kOperandHi) : "memory");
+}
+
+// Arrive on the mbarrier at this place in every CTA of `mask` once the products issued so far
+// are done.
+__device__ __forceinline__ void commit_pair(uint64_t* mbar, uint16_t mask) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               :: "r"((uint32_t)__cvta_generic_to_shared(mbar)), "h"(mask) : "memory");
+}
+
+// TMA load into this CTA's shared memory that completes on an mbarrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_pair(void* dst, const void* map, int x, int y, uint32_t mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+      :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(map), "r"(mbar), "r"(x), "r"(y)
+      : "memory");
+}
+
+__device__ __forceinline__ void arrive_cluster(uint32_t mbar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" :: "r"(mbar) : "memory");
+}
+
+// TMA store of the box at (x, y) from shared memory, in a bulk group of this thread.
+__device__ __forceinline__ void tma_store(const void* map, int x, int y, uint32_t src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n"
+               "cp.async.bulk.commit_group;"
+               :: "l"(map), "r"(src), "r"(x), "r"(y) : "memory");
+}
+template <int PENDING>
+__device__ __forceinline__ void store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(PENDING) : "memory");
+}
+
+// Tile t: bands of `band` token tiles; within a band the token tile runs fastest.
+__device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) {
+  const int per = p.band * p.nft, bnd = t / per, first = bnd * p.band;
+  const int w = min(p.band, p.ntt - first), r = t - bnd * per;
+  ft = r / w;
+  tt = first + r % w;
+}
+
+}  // namespace pairs
+
+// Persistent CTA pairs: a tile is 256 tokens x 256 features, each CTA holds 128 tokens and half of
+// the features' rows, and the products of the pair read both halves.  The accumulator takes
+// half of TMEM and the scales part of the rest, so the next tile starts when this one has been
+// read: eight warps take it into registers in one go and release it before anything is stored.
+//   What bounds it, 8192 x 5120 -> 32768: products alone take 316 us, the loads alone 279 us, the
+// scale copies alone 282 us, together without the results 414 us; all of it 445 us, 6.2 PFLOP/s.
+//   Tile: 256 x 192 with two accumulators (results stored while the next tile runs) took 526 us:
+// per product it loads a sixth more.  Reading the accumulator 32 columns at a time between stores
+// took 496 us.  Half of an earlier 1270 us was the issuing thread's own descriptor arithmetic.
+//   Split, 192 x 32768 -> 5120 (20 tiles): 1 46 us, 2 31 us, 3 26 us, 4 40 us (20 clusters of eight
+// do not all run at once); one-CTA tiles of 128 x 192 split in three took 28 us.
+__global__ void __launch_bounds__(pairs::THREADS, 1)
+    k_fp4_linear_pair(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
+                      const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
+                      const __grid_constant__ CUtensorMap mo, pairs::Params p) {
+  using namespace pairs;
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + BARS);   // the leader's are used
+  uint64_t* empty = full + STAGES;
+  uint64_t* accf = empty + STAGES;                        // accumulator complete
+  uint64_t* acce = accf + 1;                              // read by both CTAs (the leader's)
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(acce + 1);
+  volatile uint32_t* failed = tslot + 1;
+  // cluster: `split` pairs that share a tile's sum over K; split > 1 only with one tile a cluster
+  const int S = p.split, crank = (int)tc::cluster_ctarank(), part = crank >> 1;
+  const uint32_t rank = crank & 1, leader = crank & ~1;   // rank 0 leads its pair
+  const uint16_t both = (uint16_t)(3u << leader);
+  const bool aligned = (smem_u32(smem) & 1023) == 0;      // the same in every CTA
+  if (warp == EPI + 1) tmem_alloc2(tslot, 512);
+  if (tid == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(accf, 1);
+    tc::mbar_init(acce, 2 * EPI);
+    *failed = 0;
+    if (!aligned) raise_error(&g_err_fp4, CSA2_DEVERR_SMEM_ALIGN);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();                                     // barriers and TMEM of both CTAs are there
+  tc::fence_after_sync();
+  const uint32_t tb = *tslot;
+  const int npair = gridDim.x / (2 * S), pr = blockIdx.x / (2 * S);
+  const int ntile = p.nft * p.ntt, nkb = (p.nkt + 3) / 4;
+  const int kb0 = (int)((long long)nkb * part / S), kb1 = (int)((long long)nkb * (part + 1) / S);
+  const bool run = aligned && tb == 0;                    // all 512 columns: they start at 0
+  if (warp == EPI) {
+    if (lane == 0 && run) {
+      int s = 0, fill = 0;                                // fill: how often the stages have been filled
+      bool ok = true;
+      for (int t = pr; t < ntile && ok; t += npair) {
+        int ft, tt;
+        place(p, t, ft, tt);
+        const int t0 = (2 * tt + (int)rank) * BM, f0 = ft * BN;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)((fill - 1) & 1), MAX_POLL)) {
+            raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+            *failed = 1;
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * STAGE;
+          if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * STAGE);
+          const uint32_t mb = tc::mapa(smem_u32(&full[s]), leader);
+          tma_load_pair(st, &mx, kb * BKB, t0, mb);
+          tma_load_pair(st + A, &mw, kb * BKB, f0 + (int)rank * (BN / 2), mb);
+          tma_load_pair(st + A + B, &msx, kb * 256, t0 >> 7, mb);
+          tma_load_pair(st + A + B + SFA, &msw, kb * 256, f0 >> 7, mb);
+          if (++s == STAGES) s = 0, ++fill;
+        }
+      }
+    }
+  } else if (warp == EPI + 1) {
+    if (rank == 0 && run) {
+      constexpr uint32_t id = lin::idesc(2 * BM, BN);
+      const uint32_t base = smem_u32(smem) >> 4;
+      int s = 0;
+      uint32_t phase = 0, drained = 1;                    // the first tile finds the accumulator free
+      bool ok = true;
+      for (int t = pr; t < ntile && ok; t += npair) {
+        if (!tc::mbar_wait_warp(acce, drained, MAX_POLL)) {
+          if (lane == 0) {
+            raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+            *failed = 1;
+          }
+          break;
+        }
+        drained ^= 1;
+        tc::fence_after_sync();
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!tc::mbar_wait_warp(&full[s], phase, MAX_POLL)) {
+            if (lane == 0) {
+              raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+              *failed = 1;
+            }
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          const uint32_t a = base + (uint32_t)s * (STAGE >> 4), sft = BN + (uint32_t)s * SFCOLS;
+          const int nt = min(4, p.nkt - 4 * kb);
+          if (lin::elect_one()) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < nt) {
+                sf_copy2(sft + 4 * k, a + ((A + B + 512 * k) >> 4));
+                sf_copy2(sft + 16 + 8 * k, a + ((A + B + SFA + 512 * k) >> 4));
+                sf_copy2(sft + 20 + 8 * k, a + ((A + B + SFA + 2048 + 512 * k) >> 4));
+              }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (k < nt)
+                mma_fp4_pair(0, a + 2 * k, a + ((A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 8 * k,
+                             kb > kb0 || k > 0);
+            commit_pair(&empty[s], both);
+          }
+          __syncwarp();
+          if (++s == STAGES) s = 0, phase ^= 1;
+        }
+        if (lin::elect_one()) commit_pair(accf, both);
+        __syncwarp();
+      }
+    }
+  } else if (run) {
+    // warp w: rows (tokens) 32 (w % 4) .. of the CTA's 128, columns (features) 128 (w / 4) ..
+    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+    const uint32_t slice = smem_u32(smem + OUT + warp * 2 * SLICE);
+    const uint32_t tq = ((uint32_t)(32 * (warp & 3)) << 16) + 128u * (warp >> 2);
+    uint32_t phase = 0;
+    for (int t = pr; t < ntile; t += npair) {
+      int ft, tt;
+      place(p, t, ft, tt);
+      if (!tc::mbar_wait_warp(accf, phase, MAX_POLL)) {
+        if (lane == 0) {
+          raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+          *failed = 1;
+        }
+        break;
+      }
+      phase ^= 1;
+      tc::fence_after_sync();
+      if (S > 1) {                                        // this pair's part of the sum, 16-byte chunk j at j ^ (row % 8)
+        const uint32_t row = 32 * (warp & 3) + lane, at = smem_u32(smem) + row * 1024;
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(tq + (uint32_t)c, v);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};"
+                         :: "r"(at + ((((warp >> 2) * 32 + c / 4 + j) ^ (row & 7)) << 4)), "r"(v[4 * j]),
+                         "r"(v[4 * j + 1]), "r"(v[4 * j + 2]), "r"(v[4 * j + 3]) : "memory");
+        }
+        break;                                            // the cluster's only tile
+      }
+      const int t0 = (2 * tt + (int)rank) * BM + 32 * (warp & 3), f0 = ft * BN + 128 * (warp >> 2);
+      uint32_t acc[4][32];                                // all of this warp's part, so that it is free at once
+#pragma unroll
+      for (int i = 0; i < 4; ++i) tc::tmem_ld32(tq + 32u * i, acc[i]);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
+#pragma unroll
+      for (int ci = 0; ci < 4; ++ci) {
+        const int c = 32 * ci;
+        const uint32_t(&v)[32] = acc[ci];
+        if (t0 >= p.T || f0 + c >= p.N) continue;
+        // the slice's last store has read it (float32 slices take both halves)
+        if (lane == 0) p.out32 ? store_wait_read<0>() : store_wait_read<1>();
+        __syncwarp();
+        const uint32_t at = slice + (p.out32 ? 0u : (uint32_t)(c & 32) * (SLICE / 32));
+        if (p.out32) {                                    // rows of 128 bytes, 16-byte chunk j at j ^ (row % 8)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                         "f"(__uint_as_float(v[4 * j]) * alpha), "f"(__uint_as_float(v[4 * j + 1]) * alpha),
+                         "f"(__uint_as_float(v[4 * j + 2]) * alpha), "f"(__uint_as_float(v[4 * j + 3]) * alpha) : "memory");
+        } else {                                          // rows of 64 bytes, chunk j at j ^ (row / 2 % 4)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]) * alpha, __uint_as_float(v[8 * j + 2 * i + 1]) * alpha);
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+          }
+        }
+        if (p.tma_out) {
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store(&mo, f0 + c, t0, at);
+        } else {                                          // rows that TMA cannot address: 32 columns at a time
+          __syncwarp();
+          const int rows = min(32, p.T - t0);
+          for (int r = 0; r < rows && f0 + c + lane < p.N; ++r) {
+            const long long o = (long long)(t0 + r) * p.N + f0 + c + lane;
+            if (p.out32) {
+              float e;
+              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e)
+                           : "r"(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
+              static_cast<float*>(p.out)[o] = e;
+            } else {
+              uint16_t e;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e)
+                           : "r"(at + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
+              static_cast<uint16_t*>(p.out)[o] = e;
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (lane == 0) store_wait_read<0>();
+  }
+  if (S > 1) {
+    // the parts of a row, in the order of K, from the CTAs that hold it; each adds its share of rows
+    __syncwarp();
+    tc::cluster_sync();
+    if (warp < EPI && run) {
+      const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+      int ft, tt;
+      place(p, pr, ft, tt);
+      const int t0 = (2 * tt + (int)rank) * BM, rows = min(BM, p.T - t0);
+      for (int u = part * 32 * EPI + tid; u < rows * (BN / 4); u += S * 32 * EPI) {
+        const int row = u / (BN / 4), j = u % (BN / 4), f = ft * BN + 4 * j;
+        if (f >= p.N) continue;
+        const uint32_t at = smem_u32(smem) + row * 1024 + ((j ^ (row & 7)) << 4);
+        float4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (q < S) v[q] = lin::ld_dsmem_f4(tc::mapa(at, 2 * q + rank));
+        float4 e = v[0];
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (q < S) e.x += v[q].x, e.y += v[q].y, e.z += v[q].z, e.w += v[q].w;
+        lin::put4(p, (long long)(t0 + row) * p.N + f, p.N - f, e.x * alpha, e.y * alpha, e.z * alpha, e.w * alpha);
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncwarp();
+  __syncthreads();
+  if (tid == 0 && *failed)                                // given up: the copies in flight land in a few us
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  __syncwarp();
+  tc::cluster_sync();                                     // the peer's loads, products and arrivals are done
+  if (warp == EPI + 1) tmem_dealloc2(tb, 512);
 }
 
 namespace {
+
+bool groups_of_four(const csa2_fp4_linear_args& a) {
+  return a.w.rows % 4 == 0 && ((uintptr_t)a.out & (a.out_dtype == CSA2_F32 ? 15 : 7)) == 0;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+// How many clusters of `cta` CTAs of a kernel the GPU holds at once.
+template <typename K>
+int resident_clusters(K* kernel, int cta, int threads, size_t smem) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cta;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = (unsigned)cta;
+  cfg.blockDim = (unsigned)threads;
+  cfg.dynamicSmemBytes = smem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return n;
+}
 
 // uint8 matrix [rows][bytes], boxes of box_rows x 128 bytes, 128-byte swizzle: packed FP4 codes
 // as the K-major operand of the product.
@@ -324,6 +743,79 @@ bool codes_map(CUtensorMap* map, const void* base, long long rows, long long byt
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The scale tiles of FP4 rows as a matrix [row tiles][512 column tiles' bytes] of 8-byte words, boxes
+// of box_tiles x 4 tiles; tiles past the last read as zero.
+bool scales_map(CUtensorMap* map, const csa2_fp4_rows& m, int box_tiles) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t nkt = (cuuint64_t)((m.cols + 63) / 64);
+  const cuuint64_t gdim[2] = {nkt * 64, (cuuint64_t)((m.rows + 127) / 128)};
+  const cuuint64_t gstride[1] = {nkt * 512};
+  const cuuint32_t box[2] = {256, (cuuint32_t)box_tiles};
+  const cuuint32_t estride[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, m.scales, gdim, gstride, box, estride,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The output [rows][cols] as boxes of 32 rows x 32 columns, rows of 64 (bf16) or 128 (float32)
+// swizzled bytes in shared memory.
+bool out_map(CUtensorMap* map, void* base, long long rows, long long cols, bool f32) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t gstride[1] = {(cuuint64_t)cols * (f32 ? 4 : 2)};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estride[2] = {1, 1};
+  return enc(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, gdim, gstride, box,
+             estride, CU_TENSOR_MAP_INTERLEAVE_NONE, f32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
+  using namespace pairs;
+  CUtensorMap mx, mw, msx, msw, mo{};
+  pairs::Params p{};
+  p.out32 = a.out_dtype == CSA2_F32;
+  p.tma_out = ((uintptr_t)a.out & 15) == 0 && (long long)a.w.rows * (p.out32 ? 4 : 2) % 16 == 0;
+  if (!codes_map(&mx, a.x.codes, a.x.rows, a.x.cols / 2, BM) || !codes_map(&mw, a.w.codes, a.w.rows, a.w.cols / 2, BN / 2) ||
+      !scales_map(&msx, a.x, 1) || !scales_map(&msw, a.w, 2) ||
+      (p.tma_out && !out_map(&mo, a.out, a.x.rows, a.w.rows, p.out32)))
+    return cudaErrorInvalidValue;
+  p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out;
+  p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64;
+  p.nft = (p.N + BN - 1) / BN, p.ntt = (p.T + 2 * BM - 1) / (2 * BM);
+  p.band = 16;
+  const long long ntile = (long long)p.nft * p.ntt;
+  if (ntile > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
+  p.vec4 = groups_of_four(a);
+  static int pairs_at[5] = {0};                           // clusters of s pairs the GPU holds at once
+  if (!pairs_at[1]) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_pair, 2 * s, THREADS, SMEM);
+    if (!pairs_at[1]) return cudaErrorInvalidConfiguration;
+  }
+  // few tiles: split the sum as far as every cluster still runs at once, two stages a CTA or more
+  const int nkb = (p.nkt + 3) / 4;
+  p.split = 1;
+  for (int s = 2; s <= 4; ++s)
+    if (ntile <= pairs_at[s] && 2 * s <= nkb) p.split = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2u * (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  const long long clusters = p.split > 1 || ntile < pairs_at[1] ? ntile : pairs_at[1];
+  cfg.gridDim = dim3(2u * (unsigned)(p.split * clusters));   // persistent: started late
+  cfg.blockDim = pairs::THREADS;
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k_fp4_linear_pair, mx, mw, msx, msw, mo, p);
+}
+
 template <int BN>
 cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   using C = lin::Cfg<BN>;
@@ -334,19 +826,25 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   lin::Params p{};
   p.wt = a.w.scales, p.xt = a.x.scales, p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out;
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64, p.out32 = a.out_dtype == CSA2_F32;
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int ft = (p.N + lin::BM - 1) / lin::BM, tt = (p.T + BN - 1) / BN, nkb = (p.nkt + 3) / 4;
-  // few tiles: split the sum until the tiles fill the GPU, each CTA keeping two stages or more
-  int S = 1;
-  while (S < 8 && 2LL * S * ft * tt <= sms && 4 * S <= nkb) S *= 2;
-  static bool attr_set = false;
-  if (!attr_set) {
+  p.vec4 = groups_of_four(a);
+  const int ft = (p.N + lin::BM - 1) / lin::BM, nkb = (p.nkt + 3) / 4;
+  // two CTAs to an SM where both fit, or one with all stages
+  static int two[9] = {0}, one = 0;                       // clusters of s CTAs, and SMs, of the GPU
+  const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
+  if (!one) {
     cudaError_t e = cudaFuncSetAttribute(k_fp4_linear<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    attr_set = true;
+    for (int s = 1; s <= 8; ++s) two[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
+    if (!two[1]) return cudaErrorInvalidConfiguration;
+    one = sm_count();
   }
+  // few tiles: split the sum as far as every cluster still runs at once, two stages a CTA or more
+  int S = 1;
+  for (int s = 2; s <= 8; ++s)
+    if (ft <= two[s] && 2 * s <= nkb) S = s;
+  p.stages = S == 1 && ft <= one ? C::STAGES : C::STAGES2;
+  p.tmem_cols = 128;
+  while (p.tmem_cols < C::DCOLS + p.stages * C::SFCOLS) p.tmem_cols *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)S;
@@ -354,9 +852,9 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(ft * S), (unsigned)tt);
+  cfg.gridDim = (unsigned)(ft * S);
   cfg.blockDim = lin::THREADS;
-  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.dynamicSmemBytes = (size_t)p.stages * C::STAGE + 256;
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
@@ -372,7 +870,7 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (T <= 32) return launch_linear<32>(a, st);
   if (T <= 64) return launch_linear<64>(a, st);
   if (T <= 128) return launch_linear<128>(a, st);
-  return launch_linear<256>(a, st);
+  return launch_linear_pair(a, st);
 }
 
 uint32_t read_clear_error_fp4() {

@@ -138,9 +138,26 @@ def test_python_refusals():
     q = csa2.Fp4Rows.allocate(130, 80, "cpu")
     assert q.scales.shape == (2, 2, 512) and q.row_scales().shape == (130, 5)
     with pytest.raises(ValueError, match="belong"):
-        csa2.Fp4Rows(q.codes, q.scales[:1]).c_struct()
+        csa2.Fp4Rows(q.codes, q.scales[:1]).fields()
     with pytest.raises(ValueError, match="one element"):
-        csa2.Fp4Rows(q.codes, q.scales, torch.zeros(2)).c_struct()
+        csa2.Fp4Rows(q.codes, q.scales, torch.zeros(2)).fields()
+
+
+def test_packed_structs_have_the_c_layout():
+    for packed, st in [(csa2._RMS_NORM, _lib.RmsNormArgs), (csa2._ROPE, _lib.RopeArgs), (csa2._FP4_QUANT, _lib.Fp4QuantArgs),
+                       (csa2._FP4_LINEAR, _lib.Fp4LinearArgs)]:
+        assert packed.size == ctypes.sizeof(st)
+        n = len(packed.unpack(bytes(packed.size)))
+        a = st.from_buffer_copy(packed.pack(*range(1, n + 1)))
+        got = []
+
+        def walk(v):
+            for name, kind in v._fields_:
+                x = getattr(v, name)
+                walk(x) if issubclass(kind, ctypes.Structure) else got.append(x)
+
+        walk(a)
+        assert got == list(range(1, n + 1))
 
 
 def test_scale_tiles_round_trip():
