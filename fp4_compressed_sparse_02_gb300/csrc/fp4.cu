@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(lin::THREADS)
       int s = 0;
       uint32_t phase = 0;
       for (int kb = kb0; kb < kb1; ++kb) {
-        if (!tc::mbar_wait_warp(&full[s], phase, MAX_POLL)) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase, MAX_POLL))) {
           if (lane == 0) {
             raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
             *failed = 1;
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
         drained ^= 1;
         tc::fence_after_sync();
         for (int kb = kb0; kb < kb1; ++kb) {
-          if (!tc::mbar_wait_warp(&full[s], phase, MAX_POLL)) {
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase, MAX_POLL))) {
             if (lane == 0) {
               raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
               *failed = 1;
