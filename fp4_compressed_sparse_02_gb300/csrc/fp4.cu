@@ -20,7 +20,6 @@ struct QuantRowsParams {
   const float* gscale;
   long long sx;
   int T, K, nkt;
-  bool x32, vx;
 };
 
 constexpr int kQuantTiles = 4;   // column tiles (of 64 columns) of a CTA
@@ -30,6 +29,7 @@ constexpr int kQuantTiles = 4;   // column tiles (of 64 columns) of a CTA
 // CTA = 128 rows x 4 column tiles, 256 threads: half a warp takes 16 groups (256 columns) of a
 // row, so codes leave in 128-byte runs; the scale bytes meet in shared memory and leave as
 // whole 512-byte tiles, zero where there is no row or column.
+template <bool X32, bool VEC>
 __global__ void __launch_bounds__(256) k_fp4_quant(QuantRowsParams p) {
   pdl_wait();
   pdl_trigger();
@@ -42,18 +42,30 @@ __global__ void __launch_bounds__(256) k_fp4_quant(QuantRowsParams p) {
   const int rows = min(128, p.T - r0);
   const int g = tid & 15, c = kt0 * 4 + g;                // the thread's 16-column group
   if (16 * c < p.K) {
-    const float gs = p.gscale ? __ldg(p.gscale) : 1.f;
+    const float gs = p.gscale ? ld_f32(p.gscale) : 1.f;
+    const f32x2 minus = pk(-1.f, -1.f);
 #pragma unroll 2
     for (int r = tid >> 4; r < rows; r += 16) {
       const long long row = r0 + r;
-      float u[16];
-      load16(u, p.x, row * p.sx + 16 * c, p.x32, p.vx, 16);
-      if (p.gscale) {
+      f32x2 n[8];                                         // the channels, negated (rows.cuh)
+      if (VEC) {
+        Raw16<X32> raw;
+        raw.load(p.x, row * p.sx + 16 * c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) u[i] = __fdiv_rn(u[i], gs);
+        for (int i = 0; i < 8; ++i) n[i] = mul2(raw.pair(i), minus);
+      } else {
+        load16_any(n, p.x, row * p.sx + 16 * c, X32, 16);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = mul2(n[i], minus);
+      }
+      if (p.gscale) {
+        f32x2 u[8];
+        quotients16(u, n, gs, amax16(n));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = mul2(u[i], minus);
       }
       uint32_t w0, w1, sb;
-      fp4_encode16(u, w0, w1, sb);
+      fp4_encode16(n, w0, w1, sb);
       *reinterpret_cast<uint2*>(p.codes + row * (p.K / 2) + 8 * c) = make_uint2(w0, w1);
       reinterpret_cast<uint8_t*>(tile)[fp4_scale_offset(r, g, kQuantTiles)] = (uint8_t)sb;
     }
@@ -68,11 +80,13 @@ cudaError_t launch_fp4_quant(const csa2_fp4_quant_args& a, cudaStream_t st) {
   QuantRowsParams p{};
   p.x = a.x, p.codes = a.out.codes, p.tiles = a.out.scales, p.gscale = a.out.gscale;
   p.sx = a.x_stride, p.T = a.out.rows, p.K = a.out.cols, p.nkt = (a.out.cols + 63) / 64;
-  p.x32 = a.x_dtype == CSA2_F32;
-  p.vx = ((uintptr_t)a.x & 15) == 0 && (p.T == 1 || (a.x_stride * (p.x32 ? 4 : 2)) % 16 == 0);
+  const bool x32 = a.x_dtype == CSA2_F32;
+  const bool vec = ((uintptr_t)a.x & 15) == 0 && (p.T == 1 || (a.x_stride * (x32 ? 4 : 2)) % 16 == 0);
   const long long grid = (long long)((p.nkt + kQuantTiles - 1) / kQuantTiles) * ((p.T + 127) / 128);
   if (grid > INT32_MAX) return cudaErrorInvalidConfiguration;
-  return launch_k(k_fp4_quant, (unsigned)grid, 256, 0, st, p);
+  const auto k = x32 ? (vec ? k_fp4_quant<true, true> : k_fp4_quant<true, false>)
+                     : (vec ? k_fp4_quant<false, true> : k_fp4_quant<false, false>);
+  return launch_k(k, (unsigned)grid, 256, 0, st, p);
 }
 
 // ---------------------------------------------------------------------------------
@@ -297,7 +311,7 @@ __global__ void __launch_bounds__(lin::THREADS)
     for (int kb = issued - min(issued - kb0, p.stages); kb < issued; ++kb)
       tc::mbar_wait(&full[(kb - kb0) % p.stages], (uint32_t)(((kb - kb0) / p.stages) & 1), MAX_POLL);
   }
-  const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+  const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
   if (warp < 4 && !bad) {
     const uint32_t tq = tb + ((uint32_t)(32 * warp) << 16);
     const int f = 32 * warp + lane;
@@ -568,7 +582,7 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
     }
   } else if (run) {
     // warp w: rows (tokens) 32 (w % 4) .. of the CTA's 128, columns (features) 128 (w / 4) ..
-    const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+    const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
     const uint32_t slice = smem_u32(smem + OUT + warp * 2 * SLICE);
     const uint32_t tq = ((uint32_t)(32 * (warp & 3)) << 16) + 128u * (warp >> 2);
     uint32_t phase = 0;
@@ -665,7 +679,7 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
     __syncwarp();
     tc::cluster_sync();
     if (warp < EPI && run) {
-      const float alpha = (p.gx ? __ldg(p.gx) : 1.f) * (p.gw ? __ldg(p.gw) : 1.f);
+      const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
       int ft, tt;
       place(p, pr, ft, tt);
       const int t0 = (2 * tt + (int)rank) * BM, rows = min(BM, p.T - t0);

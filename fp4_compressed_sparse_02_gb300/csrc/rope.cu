@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   T* o = static_cast<T*>(p.out) + t * p.ot;
   const int h0 = blockIdx.y * blockDim.y + threadIdx.y, hs = gridDim.y * blockDim.y;
   const int half = p.d_rope / 2;
-  const int ps = __ldg(p.pos + t);
+  const int ps = ld_s32(p.pos + t);
   const bool turns = ps >= 0 && ps < p.max_pos;
   if (!turns && threadIdx.x == 0 && threadIdx.y == 0) raise_error(&g_err_rope, CSA2_DEVERR_POS);
   for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
@@ -72,8 +72,8 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const long long at = (long long)ps * half + u * NP + i;
-      cs[i] = turns ? __ldg(p.cos + at) : 1.f;
-      sn[i] = turns ? __ldg(p.sin + at) : 0.f;
+      cs[i] = turns ? ld_f32(p.cos + at) : 1.f;
+      sn[i] = turns ? ld_f32(p.sin + at) : 0.f;
       if (p.inverse) sn[i] = -sn[i];
     }
     if (INTERLEAVED && V > 1) {

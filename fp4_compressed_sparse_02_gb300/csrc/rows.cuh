@@ -1,116 +1,240 @@
-// Device helpers of the row operators (norm.cu, fp4.cu): 16 consecutive channels at a time,
-// and the FP4 / E4M3 quantisers of such a group.
+// Device helpers of the row operators (norm.cu, fp4.cu): 16 consecutive channels at a time as
+// eight float32 pairs, whose adds, products and fused products take one instruction a pair, and
+// the FP4 / E4M3 quantisers of such a group.
 #pragma once
 
 #include "common.cuh"
 
 namespace csa2 {
 
-// 16 channels of a row as float32; vec: the address is 16-byte aligned and all 16 exist.
-// Channels from n on are 0.
-__device__ __forceinline__ void load16(float* v, const void* base, long long off, bool f32, bool vec, int n) {
-  if (f32) {
-    const float* p = static_cast<const float*>(base) + off;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 q = *reinterpret_cast<const float4*>(p + 4 * i);
-        v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = i < n ? p[i] : 0.f;
-    }
-  } else {
-    const uint16_t* p = static_cast<const uint16_t*>(base) + off;
-    if (vec) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint4 q = *reinterpret_cast<const uint4*>(p + 8 * i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-          v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = i < n ? bf16_bits_to_f32(p[i]) : 0.f;
-    }
-  }
+// Two float32 in one register pair; every operation rounds each half to nearest.
+using f32x2 = uint64_t;
+__device__ __forceinline__ f32x2 pk(float a, float b) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
 }
-
+__device__ __forceinline__ float2 unpk(f32x2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 sub2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// Two bf16 in a word as a float32 pair, and back (rounded to nearest).
+__device__ __forceinline__ f32x2 bf16_pair(uint32_t w) {
+  return pk(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+__device__ __forceinline__ uint32_t pack_bf16(f32x2 v) {
+  const float2 f = unpk(v);
+  return pack_bf16(f.x, f.y);
+}
 
-__device__ __forceinline__ void store16(const float* v, void* base, long long off, bool f32, bool vec, int n) {
-  if (f32) {
-    float* p = static_cast<float*>(base) + off;
-    if (vec) {
+// Loads that stay behind pdl_wait() and in order with this thread's own stores (an output may be
+// the input itself), which ld.global.nc and __ldg do not promise: what the previous kernel on the
+// stream wrote is read after it.
+__device__ __forceinline__ uint4 ld_once_v4(const void* p) {   // 16 bytes that nobody reads again
+  uint4 r;
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ uint4 ld_v4(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+__device__ __forceinline__ float ld_f32(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int ld_s32(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+// 16 channels of a row as they lie in memory: 8 words of bf16 pairs or 16 of float32.
+template <bool F32>
+struct Raw16 {
+  uint4 q[F32 ? 4 : 2];
+  __device__ __forceinline__ void load(const void* base, long long off, bool again = false) {
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + off * (F32 ? 4 : 2));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(p + 4 * i) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = again ? ld_v4(p + i) : ld_once_v4(p + i);
+  }
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = v[i];
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ f32x2 pair(int i) const {    // channels 2 i, 2 i + 1
+    if (F32) {
+      const uint4& v = q[i / 2];
+      return i % 2 ? pk(__uint_as_float(v.z), __uint_as_float(v.w)) : pk(__uint_as_float(v.x), __uint_as_float(v.y));
+    }
+    const uint4& v = q[i / 4];
+    return bf16_pair(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+  }
+};
+
+// 16 channels one at a time, for rows that are not aligned; channels from n on are 0.
+__device__ __forceinline__ void load16_any(f32x2* v, const void* base, long long off, bool f32, int n) {
+  float e[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    e[i] = i >= n ? 0.f : f32 ? static_cast<const float*>(base)[off + i]
+                              : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[off + i]);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = pk(e[2 * i], e[2 * i + 1]);
+}
+
+__device__ __forceinline__ void store16_any(const f32x2* v, void* base, long long off, bool f32, int n) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float2 f = unpk(v[i / 2]);
+    const float e = i % 2 ? f.y : f.x;
+    if (i >= n) continue;
+    if (f32)
+      static_cast<float*>(base)[off + i] = e;
+    else
+      static_cast<uint16_t*>(base)[off + i] = __bfloat16_as_ushort(__float2bfloat16_rn(e));
+  }
+}
+
+template <bool F32>
+__device__ __forceinline__ void store16(const f32x2* v, void* base, long long off) {
+  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+  if (F32) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 a = unpk(v[2 * i]), b = unpk(v[2 * i + 1]);
+      p[i] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
     }
   } else {
-    uint16_t* p = static_cast<uint16_t*>(base) + off;
-    if (vec) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<uint4*>(p + 8 * i) =
-            make_uint4(pack_bf16(v[8 * i], v[8 * i + 1]), pack_bf16(v[8 * i + 2], v[8 * i + 3]),
-                       pack_bf16(v[8 * i + 4], v[8 * i + 5]), pack_bf16(v[8 * i + 6], v[8 * i + 7]));
-    } else {
+    for (int i = 0; i < 2; ++i)
+      p[i] = make_uint4(pack_bf16(v[4 * i]), pack_bf16(v[4 * i + 1]), pack_bf16(v[4 * i + 2]), pack_bf16(v[4 * i + 3]));
+  }
+}
+
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float amax16(const f32x2* v) {
+  float m = 0.f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) p[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpk(v[i]);
+    m = max3_abs(f.x, f.y, m);
+  }
+  return m;
+}
+
+// Quotients by an invariant divisor (Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000", 1990): with y = RN(1 / s), q = RN(u y) is within two steps of u / s, the
+// remainder u - s q is exact in a fused product, and adding remainder * y leaves an error of 2^-47
+// before the rounding; a second such step gives the correctly rounded quotient.  The
+// arguments are negated, n = -u and ny = -y, so that a remainder of +0 keeps the sign of a zero.
+__device__ __forceinline__ f32x2 quotient_step(f32x2 q, f32x2 n, f32x2 s, f32x2 ny) { return fma2(fma2(s, q, n), ny, q); }
+
+// Whether the steps stay inside float32's range for every |u| <= amax (a NaN or a larger one
+// takes the division).  Values so small that a remainder underflows give zero codes either way.
+__device__ __forceinline__ bool quotient_ok(float amax, float s) {
+  return amax <= 0x1p60f && s >= 0x1p-60f && s <= 0x1p60f;
+}
+
+// q[i] = RN(-n[i] / s): both steps, or the division.
+__device__ __forceinline__ void quotients16(f32x2* q, const f32x2* n, float s, float amax) {
+  if (quotient_ok(amax, s)) {
+    const float y = -__frcp_rn(s);
+    const f32x2 ny = pk(y, y), ss = pk(s, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const f32x2 q0 = mul2(n[i], ny);
+      q[i] = quotient_step(quotient_step(q0, n[i], ss, ny), n[i], ss, ny);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 f = unpk(n[i]);
+      q[i] = pk(__fdiv_rn(-f.x, s), __fdiv_rn(-f.y, s));
     }
   }
 }
 
-// Bits of max |v|: magnitudes order like their bit patterns, and a NaN is above all of them.
-__device__ __forceinline__ uint32_t amax_bits16(const float* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-  return m;
+// Eight float32 -> eight E2M1 codes in a word, the first in the low nibble.
+__device__ __forceinline__ uint32_t e2m1x8(const f32x2* q) {
+  const float2 a = unpk(q[0]), b = unpk(q[1]), c = unpk(q[2]), d = unpk(q[3]);
+  uint32_t r;
+  asm("{\n .reg .b8 t0, t1, t2, t3;\n cvt.rn.satfinite.e2m1x2.f32 t0, %2, %1;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 t1, %4, %3;\n cvt.rn.satfinite.e2m1x2.f32 t2, %6, %5;\n"
+      " cvt.rn.satfinite.e2m1x2.f32 t3, %8, %7;\n mov.b32 %0, {t0, t1, t2, t3};\n}"
+      : "=r"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y), "f"(d.x), "f"(d.y));
+  return r;
 }
 
-// FP4 codes and scale of 16 channels u (csa2_fp4_quant): w0 the first eight codes, w1 the
+// FP4 codes and scale of the 16 channels u = -n (csa2_fp4_quant): w0 the first eight codes, w1 the
 // others.  The code is E2M1 of the correctly rounded quotient u / s.  Only the side of the seven
-// borders m s (m = 1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5) matters, and m s is exact: a u off a border
-// is off by 2^-24 of it or more.  One Newton step (Markstein 1990: q = u y with y = RN(1/s),
-// q - (s q - u) y with both steps fused) leaves 2^-47, so it decides as the division does, and
-// u = m s gives m itself, whose tie the conversion resolves.  Written with s q - u, a zero keeps
-// its sign.  Magnitudes that could overflow take the division.
-__device__ __forceinline__ void fp4_encode16(const float* u, uint32_t& w0, uint32_t& w1, uint32_t& sbyte) {
-  const float a = __uint_as_float(amax_bits16(u));
+// borders m s (m = 1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5) matters, and m s is exact: a u off a border is
+// off by 2^-24 of it or more, so one quotient step decides as the division does, and u = m s
+// gives m itself, whose tie the conversion resolves.
+__device__ __forceinline__ void fp4_encode16(const f32x2* n, uint32_t& w0, uint32_t& w1, uint32_t& sbyte) {
+  const float a = amax16(n);
   sbyte = cvt_e4m3(__fdiv_rn(a, 6.0f));
   const float s = e4m3_to_f32(sbyte);
   w0 = w1 = 0;
   if (!(s > 0.f)) return;
-  float q[16];
-  if (a < 1e30f) {
-    const float y = __frcp_rn(s);
+  f32x2 q[8];
+  if (a <= 0x1p60f) {
+    const float y = -__frcp_rn(s);
+    const f32x2 ny = pk(y, y), ss = pk(s, s);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float q0 = __fmul_rn(u[i], y);
-      q[i] = __fmaf_rn(-__fmaf_rn(s, q0, -u[i]), y, q0);
-    }
+    for (int i = 0; i < 8; ++i) q[i] = quotient_step(mul2(n[i], ny), n[i], ss, ny);
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = __fdiv_rn(u[i], s);
+    quotients16(q, n, s, a);
   }
+  w0 = e2m1x8(q);
+  w1 = e2m1x8(q + 4);
+}
+
+// E4M3 bytes of RN(-n / s), four words; zero where s is not positive.
+__device__ __forceinline__ void fp8_encode16(const f32x2* n, float s, float amax, uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = 0;
+  if (!(s > 0.f)) return;
+  f32x2 q[8];
+  quotients16(q, n, s, amax);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w0 |= cvt_e2m1x2(q[2 * i], q[2 * i + 1]) << (8 * i);
-    w1 |= cvt_e2m1x2(q[8 + 2 * i], q[9 + 2 * i]) << (8 * i);
+    const float2 a = unpk(q[2 * i]), b = unpk(q[2 * i + 1]);
+    asm("{\n .reg .b16 t0, t1;\n cvt.rn.satfinite.e4m3x2.f32 t0, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 t1, %4, %3;\n"
+        " mov.b32 %0, {t0, t1};\n}" : "=r"(w[i]) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   }
 }
 
