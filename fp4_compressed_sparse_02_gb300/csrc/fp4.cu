@@ -30,44 +30,55 @@ constexpr int kQuantTiles = 4;   // column tiles (of 64 columns) of a CTA
 // row, so codes leave in 128-byte runs; the scale bytes meet in shared memory and leave as
 // whole 512-byte tiles, zero where there is no row or column.
 template <bool X32, bool VEC>
-__global__ void __launch_bounds__(256) k_fp4_quant(QuantRowsParams p) {
+__global__ void __launch_bounds__(256, 5) k_fp4_quant(QuantRowsParams p) {
   pdl_wait();
   pdl_trigger();
   __shared__ uint4 tile[kQuantTiles * 32];
   const int tid = threadIdx.x;
+  const int nct = (p.nkt + kQuantTiles - 1) / kQuantTiles;
+  const int rt = blockIdx.x / nct, kt0 = (blockIdx.x % nct) * kQuantTiles;
+  const long long r0 = rt * 128LL;
+  const int rows = (int)min(128LL, p.T - r0);
+  const int c = kt0 * 4 + (tid & 15), r1 = tid >> 4;      // the thread's 16-column group and first row of 16
   if (tid < kQuantTiles * 32) tile[tid] = make_uint4(0, 0, 0, 0);
   __syncthreads();
-  const int nct = (p.nkt + kQuantTiles - 1) / kQuantTiles;
-  const int rt = blockIdx.x / nct, r0 = rt * 128, kt0 = (blockIdx.x % nct) * kQuantTiles;
-  const int rows = min(128, p.T - r0);
-  const int g = tid & 15, c = kt0 * 4 + g;                // the thread's 16-column group
   if (16 * c < p.K) {
-    const float gs = p.gscale ? ld_f32(p.gscale) : 1.f;
-    const f32x2 minus = pk(-1.f, -1.f);
+    const float g = p.gscale ? ld_f32(p.gscale) : 1.f;
+    const bool over = p.gscale != nullptr, fast = quotient_ok(g);
+    long long x = (r0 + r1) * p.sx + 16 * c;
+    uint8_t* codes = p.codes + (r0 + r1) * (p.K / 2) + 8 * c;
+    uint8_t* sf = reinterpret_cast<uint8_t*>(tile) + fp4_scale_offset(r1, c & 15, kQuantTiles);
 #pragma unroll 2
-    for (int r = tid >> 4; r < rows; r += 16) {
-      const long long row = r0 + r;
-      f32x2 n[8];                                         // the channels, negated (rows.cuh)
+    for (int r = r1; r < rows; r += 16) {
+      f32x2 n[8];                                         // u, negated (rows.cuh)
       if (VEC) {
         Raw16<X32> raw;
-        raw.load(p.x, row * p.sx + 16 * c);
+        raw.load(p.x, x);
+        if (!over) raw.negate();                          // dividing by g negates
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = mul2(raw.pair(i), minus);
+        for (int i = 0; i < 8; ++i) n[i] = raw.pair(i);
       } else {
-        load16_any(n, p.x, row * p.sx + 16 * c, X32, 16);
+        load16_any(n, p.x, x, X32, 16);
+        if (!over)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = mul2(n[i], minus);
+          for (int i = 0; i < 8; ++i) n[i] = mul2(n[i], pk(-1.f, -1.f));
       }
-      if (p.gscale) {
-        f32x2 u[8];
-        quotients16(u, n, gs, amax16(n));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) n[i] = mul2(u[i], minus);
+      if (over) quotients16(n, g);
+      const float a = amax16(n);
+      uint32_t w[3];
+      if (fast && a <= 0x1p60f) {
+        fp4_encode16(n, a, w);
+      } else {
+        f32x2 t[8];
+        uint32_t b[3];
+        load16_any(t, p.x, x, X32, 16);
+        fp4_encode16_any(t, g, b);
+        w[0] = b[0], w[1] = b[1], w[2] = b[2];
       }
-      uint32_t w0, w1, sb;
-      fp4_encode16(n, w0, w1, sb);
-      *reinterpret_cast<uint2*>(p.codes + row * (p.K / 2) + 8 * c) = make_uint2(w0, w1);
-      reinterpret_cast<uint8_t*>(tile)[fp4_scale_offset(r, g, kQuantTiles)] = (uint8_t)sb;
+      *reinterpret_cast<uint2*>(codes) = make_uint2(w[0], w[1]);
+      sf[(r & 16) * 16 + (r >> 5) * 4] = (uint8_t)w[2];
+      x += 16 * p.sx;
+      codes += 8 * (long long)p.K;
     }
   }
   __syncthreads();

@@ -1,5 +1,7 @@
 // Residual addition and root-mean-square norm (csa2_rms_norm), with the output in bf16,
 // float32, E4M3 with scales, or FP4 rows.
+#include <cfloat>
+
 #include "internal.h"
 #include "rows.cuh"
 
@@ -24,12 +26,7 @@ struct NormParams {
 };
 
 // (hi, lo) += (b, blo) in two float32 words: the rounding error of the sum goes into lo (Knuth's
-// TwoSum), once for a pair of sums.
-__device__ __forceinline__ void sum_pair(f32x2& hi, f32x2& lo, f32x2 b) {
-  const f32x2 s = add2(hi, b), t = sub2(s, hi);
-  lo = add2(lo, add2(sub2(hi, sub2(s, t)), sub2(b, t)));
-  hi = s;
-}
+// TwoSum).
 __device__ __forceinline__ void sum2(float& hi, float& lo, float b, float blo) {
   const float s = __fadd_rn(hi, b), t = __fsub_rn(s, hi);
   lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b, t)) + blo;
@@ -42,27 +39,96 @@ __device__ __forceinline__ void lanes_sum2(float& hi, float& lo, int lanes) {
   }
 }
 
-// The sum of squares of 16 channels (times sc^2) in two words.  A square is h^2 = p + fma(h, h, -p)
-// exactly; that of a bf16 value has no second word.
-template <bool EXACT>
-__device__ __forceinline__ void squares16(const f32x2* h, float sc, float& hi, float& lo) {
-  f32x2 a = 0, b = 0;
+// The sum of squares of 16 channels (scaled: times 2^-128) in two words.  The running sums start at a
+// power of two c of at least 16 times the largest square, so every step's rounding error is
+// h^2 - (s - s_before), a difference that is exact and a fused product that keeps 2^-48 of c; c
+// leaves the sums exactly.  Two steps a pair fewer than TwoSum.
+__device__ __forceinline__ void squares16(const f32x2* h, bool scaled, float& hi, float& lo) {
+  const float m = scaled ? amax16(h) * 0x1p-64f : amax16(h), q = __fmul_rn(m, m);
+  const float c = __uint_as_float((__float_as_uint(fminf(q, 0x1p100f)) & 0x7f800000u) + (5u << 23));
+  f32x2 a = pk(c, c), b = 0;
+  if (!scaled) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const f32x2 v = sc == 1.f ? h[i] : mul2(h[i], pk(sc, sc));
-    const f32x2 q = mul2(v, v);
-    sum_pair(a, b, q);
-    if (!EXACT) b = add2(b, fma2(v, v, mul2(q, pk(-1.f, -1.f))));
+    for (int i = 0; i < 8; ++i) {
+      const f32x2 s = fma2(h[i], h[i], a);
+      b = add2(b, fma2(h[i], h[i], sub2(a, s)));
+      a = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const f32x2 v = mul2(h[i], pk(0x1p-64f, 0x1p-64f)), s = fma2(v, v, a);
+      b = add2(b, fma2(v, v, sub2(a, s)));
+      a = s;
+    }
   }
-  const float2 ah = unpk(a), bl = unpk(b);
+  const float2 ah = unpk(sub2(a, pk(c, c))), bl = unpk(b);
   hi = ah.x, lo = bl.x;
   sum2(hi, lo, ah.y, bl.y);
+  if (!(q < 0x1p100f)) hi = m <= FLT_MAX ? INFINITY : q;  // beyond the range: infinite or NaN, or treated as such
 }
 
-// RN((hi + lo) / D): the remainder of the rounded quotient is exact.
+// RN((hi + lo) / D): a rounded quotient (rows.cuh) whose remainder, exact, takes the rest along.
 __device__ __forceinline__ float mean2(float hi, float lo, int D) {
-  const float d = (float)D, q = __fdiv_rn(hi, d);
-  return q + __fdiv_rn(__fmaf_rn(-q, d, hi) + lo, d);
+  const float d = (float)D, y = __frcp_rn(d), q0 = __fmul_rn(hi, y);
+  const float q = __fmaf_rn(__fmaf_rn(-q0, d, hi), y, q0);
+  return __fmaf_rn(__fmaf_rn(-q, d, hi) + lo, y, q);
+}
+
+// 1 / sqrt(ms + eps) of the two-word sum of a row's squares; scaled: the sum is that of the squares
+// times 2^-128.
+__device__ __forceinline__ float inverse_rms(float hi, float lo, int D, float eps, bool scaled) {
+  float ms = hi;                                          // an infinity or a NaN stays one
+  if (isfinite(hi)) {
+    ms = mean2(hi, lo, D);
+    if (scaled) ms = ms * 0x1p64f * 0x1p64f;
+  }
+  return __fdiv_rn(1.0f, __fsqrt_rn(ms + eps));
+}
+
+// The weights of a chunk, 1 where there are none.
+__device__ __forceinline__ void load_weights(f32x2* w, const NormParams& p, int ch, bool has) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pk(1.f, 1.f);
+  if (!p.w || !has) return;
+  if (p.w32) {
+    Raw16<true> r;
+    r.load(p.w, 16 * ch, true);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
+  } else {
+    Raw16<false> r;
+    r.load(p.w, 16 * ch, true);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
+  }
+}
+
+// h = x + residual, rounded to the residual's type; a bf16 sum is left in rr too.  The sum of two bf16
+// is exact in float32, or one is so small that it moves neither rounding: rounding once gives
+// what rounding to float32 first gives.
+template <bool X32, int RES>
+__device__ __forceinline__ void add_residual(f32x2* h, const Raw16<X32>& xr, Raw16<RES == 2>& rr) {
+  if constexpr (RES == 1) {
+    uint32_t b[8];
+    if constexpr (X32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) b[i] = pack_bf16(add2(xr.pair(i), rr.pair(i)));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        b[4 * j] = add_bf16x2(xr.q[j].x, rr.q[j].x), b[4 * j + 1] = add_bf16x2(xr.q[j].y, rr.q[j].y);
+        b[4 * j + 2] = add_bf16x2(xr.q[j].z, rr.q[j].z), b[4 * j + 3] = add_bf16x2(xr.q[j].w, rr.q[j].w);
+      }
+    }
+    rr.q[0] = make_uint4(b[0], b[1], b[2], b[3]);
+    rr.q[1] = make_uint4(b[4], b[5], b[6], b[7]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = rr.pair(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = RES ? add2(xr.pair(i), rr.pair(i)) : xr.pair(i);
+  }
 }
 
 // The scale byte of a chunk and those of the next three of its row, which neighbouring lanes hold.
@@ -74,6 +140,25 @@ __device__ __forceinline__ uint32_t merge_scales(uint32_t sb, int ch, int nchunk
   return sb;
 }
 
+// FP4 of 16 channels v: y over the matrix's scale g where there is one (dividing negates, rows.cuh), else -y.
+__device__ __forceinline__ void fp4_chunk(f32x2* v, bool over, float g, uint32_t* w) {
+  f32x2 n[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) n[i] = v[i];
+  if (over) quotients16(n, g);
+  const float a = amax16(n);
+  if (quotient_ok(g) && a <= 0x1p60f) {
+    fp4_encode16(n, a, w);
+  } else {
+    f32x2 t[8];
+    uint32_t b[3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = over ? v[i] : mul2(v[i], pk(-1.f, -1.f));
+    fp4_encode16_any(t, g, b);
+    w[0] = b[0], w[1] = b[1], w[2] = b[2];
+  }
+}
+
 // Zero scales for the rows past the last, up to a whole tile of 128.
 __device__ __forceinline__ void zero_tail(const NormParams& p) {
   const int n = ((p.T + 127) & ~127) - p.T;
@@ -83,152 +168,84 @@ __device__ __forceinline__ void zero_tail(const NormParams& p) {
 
 }  // namespace
 
-// Aligned rows of D = 16 c channels, D <= 8192.  A thread holds one 16-channel chunk of a row from the
-// addition to the last store, so the row is read once and written once, and its weights for
-// every row it works on.  SMALL (D <= 512): p.lanes lanes of a warp share a row; otherwise a CTA
-// does, with one barrier for the sum (and one for a row's E4M3 scale).  The next row's loads are
-// issued before this row's arithmetic.
-//
-// The sum of squares is kept in two float32 words.  The mean then differs from the exact one by
-// 2^-46, and the float32 it rounds to, and with it every 4- or 8-bit code, does not depend on the
-// split of the row over threads.
-template <int OUT, bool X32, int RES, bool SMALL>
-__global__ void __launch_bounds__(SMALL ? 256 : 512) k_rms_norm(NormParams p) {
+// The two kernels below keep the sum of squares in two float32 words.  The mean then differs from the
+// exact one by 2^-46, and the float32 it rounds to, and with it every 4- or 8-bit code, does not
+// depend on the split of the row over threads.
+
+// Aligned rows of D = 16 c channels, D <= 512: p.lanes lanes of a warp share a row, each holds one
+// 16-channel chunk from the addition to the last store, and its weights for every row it works on.
+// The next rows' loads are issued before this row's arithmetic.
+template <int OUT, bool X32, int RES>
+__global__ void __launch_bounds__(256) k_rms_norm_small(NormParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float2 part[2][16];
-  __shared__ float apart[2][16];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int nchunk = p.D / 16;
   int grid = gridDim.x;
   if (OUT == CSA2_FP4E2M1X2 && (p.T & 127)) {
     if (blockIdx.x == --grid) return zero_tail(p);
   }
-  const int rpb = SMALL ? (int)blockDim.x / p.lanes : 1;  // rows of a CTA at a time
-  const int ch = SMALL ? lane & (p.lanes - 1) : tid;
+  const int rpb = (int)blockDim.x / p.lanes;              // rows of a CTA at a time
+  const int ch = lane & (p.lanes - 1);
   const bool has = ch < nchunk;
   f32x2 w[8];
-  if (p.w && has) {
-    if (p.w32) {
-      Raw16<true> r;
-      r.load(p.w, 16 * ch, true);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
-    } else {
-      Raw16<false> r;
-      r.load(p.w, 16 * ch, true);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = pk(1.f, 1.f);
-  }
+  load_weights(w, p, ch, has);
   const float g = OUT == CSA2_FP4E2M1X2 && p.gscale ? ld_f32(p.gscale) : 1.f;
   Raw16<X32> xr;
   Raw16<RES == 2> rr;
   const long long step = (long long)grid * rpb;
-  long long row = (long long)blockIdx.x * rpb + (SMALL ? tid / p.lanes : 0);
+  long long row = (long long)blockIdx.x * rpb + tid / p.lanes;
   const auto fetch = [&](long long r) {
     if (has && r < p.T) {
       xr.load(p.x, r * p.sx + 16 * ch);
       if (RES) rr.load(p.res, r * p.sr + 16 * ch);
     } else {
       xr.zero();
-      if (RES) rr.zero();
+      rr.zero();
     }
   };
   fetch(row);
-  // a warp's rows are neighbours: it runs while its first exists (a CTA's row is the same in all)
-  for (int par = 0; row - (SMALL ? lane / p.lanes : 0) < p.T; row += step, par ^= 1) {
+  // a warp's rows are neighbours: it runs while its first exists
+  for (; row - lane / p.lanes < p.T; row += step) {
     const bool mine = has && row < p.T;
     f32x2 h[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = RES ? add2(xr.pair(i), rr.pair(i)) : xr.pair(i);
-    if (RES == 1) {
-      uint32_t b[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        b[i] = pack_bf16(h[i]);
-        h[i] = bf16_pair(b[i]);
-      }
-      if (mine) {
-        uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.res_out) + row * p.so_res + 16 * ch);
-        o[0] = make_uint4(b[0], b[1], b[2], b[3]);
-        o[1] = make_uint4(b[4], b[5], b[6], b[7]);
-      }
-    } else if (RES == 2) {
-      if (mine) store16<true>(h, p.res_out, row * p.so_res + 16 * ch);
-    }
+    add_residual<X32, RES>(h, xr, rr);
+    if (RES == 2 && mine) store16<true>(h, p.res_out, row * p.so_res + 16 * ch);
+    if (RES == 1 && mine) rr.store(p.res_out, row * p.so_res + 16 * ch);   // the sum, in bf16
     fetch(row + step);
-    float ms;
-    {
-      constexpr bool EXACT = RES == 1 || (RES == 0 && !X32);
+    float r = 0.f;
+    bool done = false;
+    for (bool scaled = false;; scaled = true) {           // again where squares leave float32's range
       float hi, lo;
-      squares16<EXACT>(h, 1.f, hi, lo);
-      lanes_sum2(hi, lo, SMALL ? p.lanes : 32);
-      if (!SMALL) {
-        if (lane == 0) part[par][warp] = make_float2(hi, lo);
-        __syncthreads();
-        const float2 z = (lane & 15) < nwarp ? part[par][lane & 15] : make_float2(0.f, 0.f);
-        hi = z.x, lo = z.y;
-        lanes_sum2(hi, lo, 16);
-      }
-      ms = mean2(hi, lo, p.D);
-      // squares beyond float32's range: once more, scaled by 2^-64
-      const bool big = !isfinite(hi);
-      if (SMALL ? __any_sync(0xffffffffu, big) : big) {
-        float hi2, lo2;
-        squares16<EXACT>(h, 0x1p-64f, hi2, lo2);
-        lanes_sum2(hi2, lo2, SMALL ? p.lanes : 32);
-        if (!SMALL) {
-          __syncthreads();                                // every warp has read the first sums
-          if (lane == 0) part[par][warp] = make_float2(hi2, lo2);
-          __syncthreads();
-          const float2 z = (lane & 15) < nwarp ? part[par][lane & 15] : make_float2(0.f, 0.f);
-          hi2 = z.x, lo2 = z.y;
-          lanes_sum2(hi2, lo2, 16);
-        }
-        if (big) ms = isfinite(hi2) ? mean2(hi2, lo2, p.D) * 0x1p64f * 0x1p64f : hi2;
-      }
+      squares16(h, scaled, hi, lo);
+      lanes_sum2(hi, lo, p.lanes);
+      const float v = inverse_rms(hi, lo, p.D, p.eps, scaled);
+      if (!done) r = v;                                   // rows of the warp that were fine keep what they had
+      done = isfinite(hi);
+      if (scaled || !__any_sync(0xffffffffu, !done)) break;
     }
-    // quantised forms take the negated value (rows.cuh)
-    constexpr bool NEG = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2;
-    const float r0 = __fdiv_rn(1.0f, __fsqrt_rn(ms + p.eps)), r = NEG ? -r0 : r0;
+    // quantised forms take the negated value (rows.cuh); dividing by the matrix's scale negates
+    if (OUT == CSA2_FP8E4M3 || (OUT == CSA2_FP4E2M1X2 && !p.gscale)) r = -r;
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = mul2(mul2(h[i], pk(r, r)), w[i]);
     if (OUT == CSA2_BF16 || OUT == CSA2_F32) {
       if (mine) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch);
     } else if (OUT == CSA2_FP4E2M1X2) {
-      if (p.gscale) {                                     // u = RN(y / g), negated again
-        f32x2 u[8];
-        quotients16(u, h, g, amax16(h));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = mul2(u[i], pk(-1.f, -1.f));
-      }
-      uint32_t w0 = 0, w1 = 0, sb = 0;
+      uint32_t e[3] = {0, 0, 0};
       if (mine) {
-        fp4_encode16(h, w0, w1, sb);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (p.D / 2) + 8 * ch) = make_uint2(w0, w1);
+        fp4_chunk(h, p.gscale, g, e);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (p.D / 2) + 8 * ch) = make_uint2(e[0], e[1]);
       }
-      sb = merge_scales(sb, ch, nchunk);
+      const uint32_t sb = merge_scales(e[2], ch, nchunk);
       if (mine && (ch & 3) == 0) *reinterpret_cast<uint32_t*>(p.tiles + fp4_scale_offset((int)row, ch, p.nkt)) = sb;
     } else {
       float m = has ? amax16(h) : 0.f;
-      if (p.group || SMALL) {                             // 128 channels are eight lanes, or a row's lanes
-        const int over = p.group && (!SMALL || p.lanes > 8) ? 8 : p.lanes;
-        for (int o = over >> 1; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-      } else {
-        for (int o = 16; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-        if (lane == 0) apart[par][warp] = m;
-        __syncthreads();
-        m = (lane & 15) < nwarp ? apart[par][lane & 15] : 0.f;
-        for (int o = 8; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
-      }
+      const int over = p.group && p.lanes > 8 ? 8 : p.lanes;   // 128 channels are eight lanes
+      for (int o = over >> 1; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
       const float s = __fdiv_rn(m, 448.0f);
       uint32_t b[4];
       if (mine) {
-        fp8_encode16(h, s, m, b);
+        fp8_encode16(h, s, b);
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * p.so + 16 * ch) = make_uint4(b[0], b[1], b[2], b[3]);
         if (p.group ? (ch & 7) == 0 : ch == 0)
           p.out_scale[p.group ? row * ((p.D + 127) / 128) + ch / 8 : row] = s;
@@ -237,154 +254,247 @@ __global__ void __launch_bounds__(SMALL ? 256 : 512) k_rms_norm(NormParams p) {
   }
 }
 
-// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row; chunks are read and written
-// channel by channel, two to a thread above 16384 channels.
-template <int OUT, int NCH>
+// Aligned rows of D = 16 c channels, D <= 8192: a CTA a row at a time, one chunk a thread from the
+// addition to the last store; one barrier for the sum (and one for a row's E4M3 scale).  The next
+// row's loads are issued before this row's arithmetic.
+template <int OUT, bool X32, int RES>
+__global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
+  pdl_wait();
+  pdl_trigger();
+  __shared__ float2 part[2][16];
+  __shared__ float apart[2][16];
+  const int tid = threadIdx.x, ch = tid, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
+  const int nchunk = p.D / 16;
+  const bool has = ch < nchunk;
+  int grid = gridDim.x;
+  if (OUT == CSA2_FP4E2M1X2 && (p.T & 127)) {
+    if (blockIdx.x == --grid) return zero_tail(p);
+  }
+  f32x2 w[8];
+  load_weights(w, p, ch, has);
+  const float g = OUT == CSA2_FP4E2M1X2 && p.gscale ? ld_f32(p.gscale) : 1.f;
+  Raw16<X32> xr;
+  Raw16<RES == 2> rr;
+  xr.zero();
+  rr.zero();
+  long long row = blockIdx.x;
+  if (has && row < p.T) {
+    xr.load(p.x, row * p.sx + 16 * ch);
+    if (RES) rr.load(p.res, row * p.sr + 16 * ch);
+  }
+  for (int par = 0; row < p.T; row += grid, par ^= 1) {
+    f32x2 h[8];
+    add_residual<X32, RES>(h, xr, rr);
+    if (has) {
+      if (RES == 2) store16<true>(h, p.res_out, row * p.so_res + 16 * ch);
+      if (RES == 1) rr.store(p.res_out, row * p.so_res + 16 * ch);   // the sum, in bf16
+      if (row + grid < p.T) {
+        xr.load(p.x, (row + grid) * p.sx + 16 * ch);
+        if (RES) rr.load(p.res, (row + grid) * p.sr + 16 * ch);
+      }
+    }
+    float r;
+    for (bool scaled = false;; scaled = true) {           // again where squares leave float32's range
+      float hi, lo;
+      squares16(h, scaled, hi, lo);
+      lanes_sum2(hi, lo, 32);
+      if (scaled) __syncthreads();                        // every warp has read the first sums
+      if (lane == 0) part[par][warp] = make_float2(hi, lo);
+      __syncthreads();
+      const float2 z = (lane & 15) < nwarp ? part[par][lane & 15] : make_float2(0.f, 0.f);
+      hi = z.x, lo = z.y;
+      lanes_sum2(hi, lo, 16);
+      r = inverse_rms(hi, lo, p.D, p.eps, scaled);
+      if (scaled || isfinite(hi)) break;
+    }
+    // quantised forms take the negated value (rows.cuh); dividing by the matrix's scale negates
+    if (OUT == CSA2_FP8E4M3 || (OUT == CSA2_FP4E2M1X2 && !p.gscale)) r = -r;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = mul2(mul2(h[i], pk(r, r)), w[i]);
+    if (OUT == CSA2_BF16 || OUT == CSA2_F32) {
+      if (has) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch);
+    } else if (OUT == CSA2_FP4E2M1X2) {
+      uint32_t e[3] = {0, 0, 0};
+      if (has) {
+        fp4_chunk(h, p.gscale, g, e);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (p.D / 2) + 8 * ch) = make_uint2(e[0], e[1]);
+      }
+      const uint32_t sb = merge_scales(e[2], ch, nchunk);
+      if (has && (ch & 3) == 0) *reinterpret_cast<uint32_t*>(p.tiles + fp4_scale_offset((int)row, ch, p.nkt)) = sb;
+    } else {
+      float m = has ? amax16(h) : 0.f;
+      if (p.group) {                                      // 128 channels: eight lanes
+        for (int o = 4; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
+      } else {
+        m = warp_max_abs(m);
+        if (lane == 0) apart[par][warp] = m;
+        __syncthreads();
+        m = warp_max_abs(lane < nwarp ? apart[par][lane] : 0.f);
+      }
+      const float s = __fdiv_rn(m, 448.0f);
+      if (has) {
+        uint32_t b[4];
+        fp8_encode16(h, s, b);
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + row * p.so + 16 * ch) = make_uint4(b[0], b[1], b[2], b[3]);
+        if (p.group ? (ch & 7) == 0 : ch == 0) p.out_scale[p.group ? row * ((p.D + 127) / 128) + ch / 8 : row] = s;
+      }
+    }
+  }
+}
+
+// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row, kept in shared memory: channels are
+// read and written one by one, neighbouring threads neighbouring channels; the quantised forms
+// take 16-channel chunks from there (17 words apart, so that the lanes' banks differ).
+template <int OUT>
 __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
   pdl_wait();
   pdl_trigger();
-  __shared__ float2 part[32];
-  __shared__ float apart[32];
+  extern __shared__ float buf[];
+  __shared__ float2 part[1024];
+  __shared__ float apart[32], rms;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
   const int nchunk = (p.D + 15) / 16;
   if (OUT == CSA2_FP4E2M1X2 && blockIdx.x >= p.T) return zero_tail(p);
   const long long row = blockIdx.x;
-  f32x2 h[NCH][8];
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int ch = tid + c * blockDim.x, n = min(16, p.D - 16 * ch);
-    load16_any(h[c], p.x, row * p.sx + 16 * ch, p.x32, n);
-    if (p.res && n > 0) {
-      f32x2 r[8];
-      load16_any(r, p.res, row * p.sr + 16 * ch, p.r32, n);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        h[c][i] = add2(h[c][i], r[i]);
-        if (!p.r32) h[c][i] = bf16_pair(pack_bf16(h[c][i]));
-      }
-      store16_any(h[c], p.res_out, row * p.so_res + 16 * ch, p.r32, n);
+  const auto at = [&](int i) -> float& { return buf[(i >> 4) * 17 + (i & 15)]; };
+  const auto get = [](const void* base, long long i, bool f32) {
+    return f32 ? static_cast<const float*>(base)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[i]);
+  };
+  const auto put = [](void* base, long long i, bool f32, float v) {
+    if (f32)
+      static_cast<float*>(base)[i] = v;
+    else
+      static_cast<uint16_t*>(base)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+  };
+#pragma unroll 4
+  for (int i = tid; i < p.D; i += blockDim.x) {
+    float h = get(p.x, row * p.sx + i, p.x32);
+    if (p.res) {
+      h += get(p.res, row * p.sr + i, p.r32);
+      if (!p.r32) h = __bfloat162float(__float2bfloat16_rn(h));
+      put(p.res_out, row * p.so_res + i, p.r32, h);
     }
+    at(i) = h;
   }
-  // the second pass, of a row whose squares leave float32's range, scales by 2^-64
-  float ms = 0.f;
-#pragma unroll 1
-  for (float sc = 1.f;; sc = 0x1p-64f) {
+  float r;
+  for (bool scaled = false;; scaled = true) {             // again where squares leave float32's range
     float hi = 0.f, lo = 0.f;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      float a, b;
-      squares16<false>(h[c], sc, a, b);
-      sum2(hi, lo, a, b);
+    for (int i = tid; i < p.D; i += blockDim.x) {
+      const float v = scaled ? at(i) * 0x1p-64f : at(i), q = __fmul_rn(v, v);
+      sum2(hi, lo, q, __fmaf_rn(v, v, -q));
     }
-    lanes_sum2(hi, lo, 32);
-    if (sc != 1.f) __syncthreads();                       // every warp has read the first partials
-    if (lane == 0) part[warp] = make_float2(hi, lo);
+    part[tid] = make_float2(hi, lo);
     __syncthreads();
-    const float2 z = lane < nwarp ? part[lane] : make_float2(0.f, 0.f);
-    hi = z.x, lo = z.y;
-    lanes_sum2(hi, lo, 32);
-    ms = mean2(hi, lo, p.D);
-    if (isfinite(hi)) {
-      if (sc != 1.f) ms = ms * 0x1p64f * 0x1p64f;
-      break;
+    if (warp == 0) {
+      hi = part[lane].x, lo = part[lane].y;
+      for (int i = lane + 32; i < blockDim.x; i += 32) sum2(hi, lo, part[i].x, part[i].y);
+      lanes_sum2(hi, lo, 32);
+      const float v = inverse_rms(hi, lo, p.D, p.eps, scaled);
+      if (lane == 0) rms = !scaled && !isfinite(hi) ? -1.f : v;
     }
-    ms = hi;
-    if (sc != 1.f) break;
+    __syncthreads();
+    r = rms;
+    if (scaled || r != -1.f) break;
   }
-  constexpr bool NEG = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2;
-  const float r0 = __fdiv_rn(1.0f, __fsqrt_rn(ms + p.eps)), r = NEG ? -r0 : r0;
+  if (OUT == CSA2_FP8E4M3 || (OUT == CSA2_FP4E2M1X2 && !p.gscale)) r = -r;   // as in k_rms_norm
+  for (int i = tid; i < p.D; i += blockDim.x) {
+    float y = __fmul_rn(at(i), r);
+    if (p.w) y = __fmul_rn(y, get(p.w, i, p.w32));
+    if (OUT == CSA2_BF16 || OUT == CSA2_F32)
+      put(p.out, row * p.so + i, OUT == CSA2_F32, y);
+    else
+      at(i) = y;
+  }
+  if (OUT == CSA2_BF16 || OUT == CSA2_F32) return;
+  for (int i = p.D + tid; i < 16 * nchunk; i += blockDim.x) at(i) = 0.f;
+  __syncthreads();
+  const auto chunk = [&](f32x2* v, int ch) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = ch < nchunk ? pk(buf[ch * 17 + 2 * i], buf[ch * 17 + 2 * i + 1]) : 0;
+  };
+  const int rounds = (nchunk + blockDim.x - 1) / blockDim.x;
   float rm = 0.f;
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int ch = tid + c * blockDim.x, n = min(16, p.D - 16 * ch);
-    f32x2 w[8];
-    if (p.w && n > 0) {
-      load16_any(w, p.w, 16 * ch, p.w32, n);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = pk(1.f, 1.f);
+  if (OUT == CSA2_FP8E4M3 && p.group == 0) {
+    for (int k = 0; k < rounds; ++k) {
+      f32x2 v[8];
+      chunk(v, k * blockDim.x + tid);
+      rm = max3_abs(rm, amax16(v), 0.f);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) h[c][i] = mul2(mul2(h[c][i], pk(r, r)), w[i]);
-    if (OUT == CSA2_BF16 || OUT == CSA2_F32) {
-      if (n > 0) store16_any(h[c], p.out, row * p.so + 16 * ch, OUT == CSA2_F32, n);
-    } else if (OUT == CSA2_FP4E2M1X2) {
-      if (p.gscale) {
-        f32x2 u[8];
-        quotients16(u, h[c], ld_f32(p.gscale), amax16(h[c]));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[c][i] = mul2(u[i], pk(-1.f, -1.f));
-      }
-      uint32_t w0 = 0, w1 = 0, sb = 0;
+    rm = warp_max_abs(rm);
+    if (lane == 0) apart[warp] = rm;
+    __syncthreads();
+    rm = warp_max_abs(lane < nwarp ? apart[lane] : 0.f);
+    if (tid == 0) p.out_scale[row] = __fdiv_rn(rm, 448.0f);
+  }
+  for (int k = 0; k < rounds; ++k) {
+    const int ch = k * blockDim.x + tid;
+    f32x2 v[8];
+    chunk(v, ch);
+    if (OUT == CSA2_FP4E2M1X2) {
+      uint32_t e[3] = {0, 0, 0};
       if (ch < nchunk) {
-        fp4_encode16(h[c], w0, w1, sb);
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (p.D / 2) + 8 * ch) = make_uint2(w0, w1);
+        fp4_chunk(v, p.gscale, p.gscale ? ld_f32(p.gscale) : 1.f, e);
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.out) + row * (p.D / 2) + 8 * ch) = make_uint2(e[0], e[1]);
       }
-      sb = merge_scales(sb, ch, nchunk);
+      const uint32_t sb = merge_scales(e[2], ch, nchunk);
       if ((ch & 3) == 0 && ch < nchunk)
         *reinterpret_cast<uint32_t*>(p.tiles + fp4_scale_offset((int)row, ch, p.nkt)) = sb;
-    } else if (ch < nchunk) {
-      rm = max3_abs(rm, amax16(h[c]), 0.f);
-    }
-  }
-  if (OUT == CSA2_FP8E4M3) {
-    if (p.group == 0) {                                   // one scale for the row
-      for (int o = 16; o > 0; o >>= 1) rm = max3_abs(rm, __shfl_xor_sync(0xffffffffu, rm, o), 0.f);
-      if (lane == 0) apart[warp] = rm;
-      __syncthreads();
-      rm = lane < nwarp ? apart[lane] : 0.f;
-      for (int o = 16; o > 0; o >>= 1) rm = max3_abs(rm, __shfl_xor_sync(0xffffffffu, rm, o), 0.f);
-      if (tid == 0) p.out_scale[row] = __fdiv_rn(rm, 448.0f);
-    }
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) {
-      const int ch = tid + c * blockDim.x, n = min(16, p.D - 16 * ch);
+    } else {
       float m = rm;
       if (p.group) {                                      // 128 channels: eight lanes
-        m = ch < nchunk ? amax16(h[c]) : 0.f;
+        m = amax16(v);
         for (int o = 4; o > 0; o >>= 1) m = max3_abs(m, __shfl_xor_sync(0xffffffffu, m, o), 0.f);
         if ((ch & 7) == 0 && ch < nchunk) p.out_scale[row * ((p.D + 127) / 128) + ch / 8] = __fdiv_rn(m, 448.0f);
       }
-      if (ch >= nchunk) continue;
       uint32_t b[4];
-      fp8_encode16(h[c], __fdiv_rn(m, 448.0f), m, b);
-      uint8_t* o = static_cast<uint8_t*>(p.out) + row * p.so + 16 * ch;
+      fp8_encode16(v, __fdiv_rn(m, 448.0f), b);
+      if (ch < nchunk)
 #pragma unroll
-      for (int i = 0; i < 16; ++i)
-        if (i < n) o[i] = (uint8_t)(b[i / 4] >> (8 * (i % 4)));
+        for (int i = 0; i < 16; ++i) buf[ch * 17 + i] = __uint_as_float((b[i / 4] >> (8 * (i % 4))) & 0xffu);
     }
+  }
+  if (OUT == CSA2_FP8E4M3) {
+    __syncthreads();
+    for (int i = tid; i < p.D; i += blockDim.x)
+      static_cast<uint8_t*>(p.out)[row * p.so + i] = (uint8_t)__float_as_uint(at(i));
   }
 }
 
 namespace {
 
-template <int OUT, bool X32, int RES, bool SMALL>
-cudaError_t launch_aligned(const NormParams& p, int threads, cudaStream_t st) {
-  static int resident[17] = {0};                          // CTAs the GPU holds, by warps of a CTA
-  int& r = resident[threads / 32];
-  if (!r) {
+// A persistent grid: as many CTAs as the GPU holds at once (looked up once for a kernel and shape).
+template <typename K>
+cudaError_t launch_rows(K* kernel, int& resident, const NormParams& p, int rows, int threads, bool tail, cudaStream_t st) {
+  if (!resident) {
     int dev = 0, sms = 0, per = 0;
     cudaGetDevice(&dev);
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k_rms_norm<OUT, X32, RES, SMALL>, threads, 0);
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
     if (e != cudaSuccess) return e;
-    r = sms * (per > 0 ? per : 1);
+    resident = sms * (per > 0 ? per : 1);
   }
-  const int rpb = SMALL ? threads / p.lanes : 1;
-  const int blocks = (p.T + rpb - 1) / rpb;
-  const unsigned tail = OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u;
-  return launch_k(k_rms_norm<OUT, X32, RES, SMALL>, (unsigned)(blocks < r ? blocks : r) + tail, threads, 0, st, p);
+  const int blocks = (p.T + rows - 1) / rows;
+  return launch_k(kernel, (unsigned)(blocks < resident ? blocks : resident) + (tail ? 1u : 0u), threads, 0, st, p);
+}
+
+template <int OUT, bool X32, int RES>
+cudaError_t launch_aligned(const NormParams& p, cudaStream_t st) {
+  const bool tail = OUT == CSA2_FP4E2M1X2 && p.T % 128;
+  if (p.D <= 512) {
+    static int resident = 0;
+    return launch_rows(k_rms_norm_small<OUT, X32, RES>, resident, p, 256 / p.lanes, 256, tail, st);
+  }
+  static int resident[17] = {0};                          // by warps of a CTA
+  const int threads = (p.D / 16 + 31) & ~31;
+  return launch_rows(k_rms_norm<OUT, X32, RES>, resident[threads / 32], p, 1, threads, tail, st);
 }
 
 template <int OUT>
 cudaError_t launch_form(const NormParams& p, bool aligned, cudaStream_t st) {
   if (aligned && p.D <= 8192) {
     const int res = !p.res ? 0 : p.r32 ? 2 : 1;
-    const bool small = p.D <= 512;
-    const int threads = small ? 256 : (p.D / 16 + 31) & ~31;
 #define CSA2_NORM(X, R) \
-  if (p.x32 == X && res == R) \
-    return small ? launch_aligned<OUT, X, R, true>(p, threads, st) : launch_aligned<OUT, X, R, false>(p, threads, st)
+  if (p.x32 == X && res == R) return launch_aligned<OUT, X, R>(p, st)
     CSA2_NORM(false, 0);
     CSA2_NORM(false, 1);
     CSA2_NORM(false, 2);
@@ -393,11 +503,16 @@ cudaError_t launch_form(const NormParams& p, bool aligned, cudaStream_t st) {
     CSA2_NORM(true, 2);
 #undef CSA2_NORM
   }
-  const int nchunk = (p.D + 15) / 16, nch = nchunk > 1024 ? 2 : 1;
-  const int threads = ((nchunk + nch - 1) / nch + 31) & ~31;
-  const unsigned grid = (unsigned)p.T + (OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u);
-  return nch == 1 ? launch_k(k_rms_norm_any<OUT, 1>, grid, threads, 0, st, p)
-                  : launch_k(k_rms_norm_any<OUT, 2>, grid, threads, 0, st, p);
+  const int nchunk = (p.D + 15) / 16;
+  const int threads = p.D >= 4096 ? 1024 : (p.D / 4 + 31) & ~31 ? (p.D / 4 + 31) & ~31 : 32;
+  const size_t smem = (size_t)nchunk * 17 * 4;
+  static bool attr_set = false;
+  if (!attr_set) {
+    cudaError_t e = cudaFuncSetAttribute(k_rms_norm_any<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  return launch_k(k_rms_norm_any<OUT>, (unsigned)p.T + (OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u), threads, smem, st, p);
 }
 
 bool rows_aligned(const void* p, long long stride, int esize) {

@@ -42,16 +42,35 @@ struct alignas(sizeof(T) * V) Vec {
 
 }  // namespace
 
+// N floats from a 4 N- (16- at most) byte aligned address.
+template <int N>
+__device__ __forceinline__ void load_angles(float* v, const float* p) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 q = ld_v4(p + i);
+      v[i] = __uint_as_float(q.x), v[i + 1] = __uint_as_float(q.y);
+      v[i + 2] = __uint_as_float(q.z), v[i + 3] = __uint_as_float(q.w);
+    }
+  } else if constexpr (N == 2) {
+    asm volatile("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "l"(p));
+  } else {
+    v[0] = ld_f32(p);
+  }
+}
+
 // A unit is V neighbouring channels that are copied, or that turn: V channels of V/2
 // interleaved pairs (V = 1: one pair), or V channels of each half.  A thread keeps its unit and
-// runs over heads, so a token's angles are read once for all of them.  A token with a bad
-// position is copied as it is.
+// runs over heads, HEADS of them at a time, so a token's angles are read once for all of them and
+// several loads are under way.  A token with a bad position is copied as it is.
 template <typename T, int V, bool INTERLEAVED>
 __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   pdl_wait();
   pdl_trigger();
   using Vt = Vec<T, V>;
   constexpr int NP = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;   // pairs of a unit
+  constexpr int PARTS = INTERLEAVED && V > 1 ? 1 : 2;         // vectors of a unit that turns
+  constexpr int HEADS = 4;
   const long long t = blockIdx.x;
   const T* x = static_cast<const T*>(p.x) + t * p.xt;
   T* o = static_cast<T*>(p.out) + t * p.ot;
@@ -61,51 +80,47 @@ __global__ void __launch_bounds__(256) k_rope(RopeParams p) {
   const bool turns = ps >= 0 && ps < p.max_pos;
   if (!turns && threadIdx.x == 0 && threadIdx.y == 0) raise_error(&g_err_rope, CSA2_DEVERR_POS);
   for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
-    if (u >= p.turn_units) {                              // channels that are copied
-      int c = (u - p.turn_units) * V;
-      if (c >= p.first) c += p.d_rope;
-      for (int h = h0; h < p.H; h += hs)
-        *reinterpret_cast<Vt*>(o + h * p.oh + c) = *reinterpret_cast<const Vt*>(x + h * p.xh + c);
-      continue;
-    }
+    const bool turn = u < p.turn_units;
     float cs[NP], sn[NP];
+    int c = (u - p.turn_units) * V, c2 = 0;
+    if (!turn) {                                          // channels that are copied
+      if (c >= p.first) c += p.d_rope;
+    } else {
+      c = p.first + (PARTS == 1 ? u * V : INTERLEAVED ? 2 * u : u * V);
+      c2 = PARTS == 1 ? 0 : INTERLEAVED ? c + 1 : c + half;
+      if (turns) {
+        load_angles<NP>(cs, p.cos + (long long)ps * half + u * NP);
+        load_angles<NP>(sn, p.sin + (long long)ps * half + u * NP);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const long long at = (long long)ps * half + u * NP + i;
-      cs[i] = turns ? ld_f32(p.cos + at) : 1.f;
-      sn[i] = turns ? ld_f32(p.sin + at) : 0.f;
-      if (p.inverse) sn[i] = -sn[i];
+        for (int i = 0; i < NP; ++i) sn[i] = p.inverse ? -sn[i] : sn[i];
+      }
     }
-    if (INTERLEAVED && V > 1) {
-      const int c = p.first + u * V;
-      for (int h = h0; h < p.H; h += hs) {
-        Vt v = *reinterpret_cast<const Vt*>(x + h * p.xh + c);
-        if (turns) {
+    for (int h = h0; h < p.H; h += HEADS * hs) {
+      Vt v[HEADS], w[HEADS];
+#pragma unroll
+      for (int k = 0; k < HEADS; ++k) {
+        const T* at = x + (long long)(h + k * hs) * p.xh;
+        if (h + k * hs >= p.H) continue;
+        v[k] = *reinterpret_cast<const Vt*>(at + c);
+        if (PARTS == 2 && turn) w[k] = *reinterpret_cast<const Vt*>(at + c2);
+      }
+#pragma unroll
+      for (int k = 0; k < HEADS; ++k) {
+        if (h + k * hs >= p.H) continue;
+        if (turn && turns) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            float a = to_f32(v.e[2 * i]), b = to_f32(v.e[2 * i + (V > 1)]);
+            T& e0 = PARTS == 1 ? v[k].e[2 * i] : v[k].e[i];
+            T& e1 = PARTS == 1 ? v[k].e[2 * i + (V > 1)] : w[k].e[i];
+            float a = to_f32(e0), b = to_f32(e1);
             rope_pair(a, b, cs[i], sn[i]);
-            v.e[2 * i] = from_f32<T>(a);
-            v.e[2 * i + (V > 1)] = from_f32<T>(b);
+            e0 = from_f32<T>(a);
+            e1 = from_f32<T>(b);
           }
         }
-        *reinterpret_cast<Vt*>(o + h * p.oh + c) = v;
-      }
-    } else {
-      const int c = p.first + (INTERLEAVED ? 2 * u : u * V), c2 = INTERLEAVED ? c + 1 : c + half;
-      for (int h = h0; h < p.H; h += hs) {
-        Vt v = *reinterpret_cast<const Vt*>(x + h * p.xh + c), w = *reinterpret_cast<const Vt*>(x + h * p.xh + c2);
-        if (turns) {
-#pragma unroll
-          for (int i = 0; i < V; ++i) {
-            float a = to_f32(v.e[i]), b = to_f32(w.e[i]);
-            rope_pair(a, b, cs[i], sn[i]);
-            v.e[i] = from_f32<T>(a);
-            w.e[i] = from_f32<T>(b);
-          }
-        }
-        *reinterpret_cast<Vt*>(o + h * p.oh + c) = v;
-        *reinterpret_cast<Vt*>(o + h * p.oh + c2) = w;
+        T* at = o + (long long)(h + k * hs) * p.oh;
+        *reinterpret_cast<Vt*>(at + c) = v[k];
+        if (PARTS == 2 && turn) *reinterpret_cast<Vt*>(at + c2) = w[k];
       }
     }
   }
@@ -143,7 +158,8 @@ cudaError_t launch_rope(const csa2_rope_args& a, cudaStream_t st) {
   const int v = a.dtype == CSA2_F32 ? 4 : 8;
   const bool vec = ((uintptr_t)a.x & 15) == 0 && ((uintptr_t)a.out & 15) == 0 && a.x_stride_t % v == 0 &&
                    a.x_stride_h % v == 0 && a.out_stride_t % v == 0 && a.out_stride_h % v == 0 && a.D % v == 0 &&
-                   a.rot_first % v == 0 && (a.interleaved ? a.d_rope : a.d_rope / 2) % v == 0;
+                   a.rot_first % v == 0 && (a.interleaved ? a.d_rope : a.d_rope / 2) % v == 0 &&
+                   ((uintptr_t)a.rope_cos & 15) == 0 && ((uintptr_t)a.rope_sin & 15) == 0;
   if (a.dtype == CSA2_F32) return vec ? launch_rope_v<float, 4>(a, p, st) : launch_rope_v<float, 1>(a, p, st);
   return vec ? launch_rope_v<uint16_t, 8>(a, p, st) : launch_rope_v<uint16_t, 1>(a, p, st);
 }
@@ -161,23 +177,83 @@ struct TableParams {
   unsigned long long turn[128];   // turns per position of channel i, times 2^64
 };
 
+// sin and cos of pi/2 x / 2^32 for a pair of |x| <= 2^31 (an eighth of a turn at most): Taylor's series to
+// the powers 9 and 10, whose next terms are below 2e-9, at the rounded angle a, and the first
+// derivative for what the rounding (of x's last 8 bits, of pi and of the product) left out.
+__device__ __forceinline__ void sincos_pair(int x0, int x1, f32x2& s, f32x2& c) {
+  const float q = 1.57079632679489662f * 0x1p-32f;
+  const float ql = (float)((1.57079632679489662 - (double)1.57079632679489662f) * 0x1p-32);
+  const auto k = [](float v) { return pk(v, v); };
+  const f32x2 xh = pk((float)(x0 & ~255), (float)(x1 & ~255));
+  const f32x2 xl = pk((float)(x0 & 255), (float)(x1 & 255));
+  const f32x2 a = mul2(xh, k(q)), z = mul2(a, a);
+  // minus what a leaves out
+  const f32x2 left = fma2(xh, k(-ql), fma2(xl, k(-q), fma2(xh, k(-q), a)));
+  f32x2 t = fma2(z, k(-1.0f / 3628800), k(1.0f / 40320));
+  t = fma2(z, t, k(-1.0f / 720));
+  t = fma2(z, t, k(1.0f / 24));
+  t = fma2(z, t, k(-0.5f));
+  c = add2(k(1.0f), fma2(z, t, mul2(left, a)));
+  t = fma2(z, k(1.0f / 362880), k(-1.0f / 5040));
+  t = fma2(z, t, k(1.0f / 120));
+  t = fma2(z, t, k(-1.0f / 6));
+  s = add2(a, sub2(mul2(mul2(a, z), t), mul2(left, c)));
+}
+
 }  // namespace
 
-// The angle p f_i in turns, modulo 1, is a 64-bit product; its nearest multiple of a quarter
-// turn picks which of +-sin, +-cos of the remainder (at most an eighth of a turn) is which.
-__global__ void __launch_bounds__(256) k_rope_table(TableParams t) {
+// The angle p f_i in turns, modulo 1, is a 64-bit product that a thread carries from one of its
+// positions to the next by an addition.  Its nearest multiple of a quarter turn picks which of
+// +-sin, +-cos of the remainder is which.  V channels a thread (4, or 1 where half % 4 != 0).
+//   1,048,576 positions x 32 pairs (268 MB written, 39.5 us at the copy rate): TABLE_US; with the library's
+// sincospif and a 64-bit division for the place it took 271 us.
+template <int V>
+__global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams t) {
   pdl_wait();
   pdl_trigger();
-  const long long n = (long long)t.positions * t.half;
-  for (long long e = (long long)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (long long)gridDim.x * blockDim.x) {
-    const unsigned long long a = (unsigned long long)(e / t.half) * t.turn[e % t.half];
-    const unsigned long long q = (a + (1ull << 61)) >> 62;          // quarter turns, 0..4
-    const long long r = (long long)(a - (q << 62));                 // remainder, +-2^61
-    float s, c;
-    sincospif((float)r * 0x1p-63f, &s, &c);                         // half turns
-    const float cv = (q & 1) ? s : c, sv = (q & 1) ? c : s;
-    t.cos[e] = t.magnitude * (((q + 1) & 2) ? -cv : cv);
-    t.sin[e] = t.magnitude * ((q & 2) ? -sv : sv);
+  const int groups = t.half / V, slots = blockDim.x / groups, slot = threadIdx.x / groups;
+  if (slot >= slots) return;
+  const int i0 = (threadIdx.x - slot * groups) * V;
+  const int step = gridDim.x * slots;
+  int p = blockIdx.x * slots + slot;
+  unsigned long long a[V], d[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    a[i] = (unsigned long long)p * t.turn[i0 + i];
+    d[i] = (unsigned long long)step * t.turn[i0 + i];
+  }
+  const f32x2 mag = pk(t.magnitude, t.magnitude);
+  for (; p < t.positions; p += step) {
+    float c[V + V % 2], s[V + V % 2];
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const int j = V > 1 ? i + 1 : i;
+      // the fraction of a quarter turn, as a signed number the distance to the nearest one
+      const int x0 = (int)__funnelshift_l((uint32_t)a[i], (uint32_t)(a[i] >> 32), 2);
+      const int x1 = (int)__funnelshift_l((uint32_t)a[j], (uint32_t)(a[j] >> 32), 2);
+      f32x2 sp, cp;
+      sincos_pair(x0, x1, sp, cp);
+      const float2 sv = unpk(mul2(sp, mag)), cv = unpk(mul2(cp, mag));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        // bits 31, 30: the nearest multiple of a quarter turn
+        const uint32_t q = (uint32_t)(a[k ? j : i] >> 32) + 0x20000000u;
+        const float sk = k ? sv.y : sv.x, ck = k ? cv.y : cv.x;
+        const bool odd = q & 0x40000000u;
+        c[i + k] = __uint_as_float(__float_as_uint(odd ? sk : ck) ^ ((q + 0x40000000u) & 0x80000000u));
+        s[i + k] = __uint_as_float(__float_as_uint(odd ? ck : sk) ^ (q & 0x80000000u));
+      }
+    }
+    const long long at = (long long)p * t.half + i0;
+    if constexpr (V == 4) {
+      *reinterpret_cast<float4*>(t.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
+      *reinterpret_cast<float4*>(t.sin + at) = make_float4(s[0], s[1], s[2], s[3]);
+    } else {
+      t.cos[at] = c[0];
+      t.sin[at] = s[0];
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) a[i] += d[i];
   }
 }
 
@@ -206,9 +282,14 @@ cudaError_t launch_rope_table(const csa2_rope_table_args& a, cudaStream_t st) {
     const double turn = f / two_pi;                       // below 1/6: theta > 1
     t.turn[i] = (unsigned long long)std::ldexp(turn, 64);
   }
-  const long long n = (long long)t.positions * t.half;
-  const long long blocks = (n + 255) / 256;
-  return launch_k(k_rope_table, (unsigned)(blocks < (1 << 20) ? blocks : (1 << 20)), 256, 0, st, t);
+  const bool vec = t.half % 4 == 0 && ((uintptr_t)t.cos & 15) == 0 && ((uintptr_t)t.sin & 15) == 0;
+  const int slots = 256 / (vec ? t.half / 4 : t.half);    // half <= 128
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int blocks = (t.positions + slots - 1) / slots, most = 8 * sms;
+  return vec ? launch_k(k_rope_table<4>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t)
+             : launch_k(k_rope_table<1>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t);
 }
 
 uint32_t read_clear_error_rope() {

@@ -77,6 +77,12 @@ __device__ __forceinline__ int ld_s32(const int* p) {
   return v;
 }
 
+__device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // 16 channels of a row as they lie in memory: 8 words of bf16 pairs or 16 of float32.
 template <bool F32>
 struct Raw16 {
@@ -86,9 +92,19 @@ struct Raw16 {
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = again ? ld_v4(p + i) : ld_once_v4(p + i);
   }
+  __device__ __forceinline__ void store(void* base, long long off) const {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) p[i] = q[i];
+  }
   __device__ __forceinline__ void zero() {
 #pragma unroll
     for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void negate() {
+    const uint32_t m = F32 ? 0x80000000u : 0x80008000u;
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i].x ^= m, q[i].y ^= m, q[i].z ^= m, q[i].w ^= m;
   }
   __device__ __forceinline__ f32x2 pair(int i) const {    // channels 2 i, 2 i + 1
     if (F32) {
@@ -156,6 +172,13 @@ __device__ __forceinline__ float amax16(const f32x2* v) {
   return m;
 }
 
+// The same over a warp's lanes.
+__device__ __forceinline__ float warp_max_abs(float v) {
+  float d;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(d) : "f"(v));
+  return d;
+}
+
 // Quotients by an invariant divisor (Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000", 1990): with y = RN(1 / s), q = RN(u y) is within two steps of u / s, the
 // remainder u - s q is exact in a fused product, and adding remainder * y leaves an error of 2^-47
@@ -163,29 +186,15 @@ __device__ __forceinline__ float amax16(const f32x2* v) {
 // arguments are negated, n = -u and ny = -y, so that a remainder of +0 keeps the sign of a zero.
 __device__ __forceinline__ f32x2 quotient_step(f32x2 q, f32x2 n, f32x2 s, f32x2 ny) { return fma2(fma2(s, q, n), ny, q); }
 
-// Whether the steps stay inside float32's range for every |u| <= amax (a NaN or a larger one
-// takes the division).  Values so small that a remainder underflows give zero codes either way.
-__device__ __forceinline__ bool quotient_ok(float amax, float s) {
-  return amax <= 0x1p60f && s >= 0x1p-60f && s <= 0x1p60f;
-}
-
-// q[i] = RN(-n[i] / s): both steps, or the division.
-__device__ __forceinline__ void quotients16(f32x2* q, const f32x2* n, float s, float amax) {
-  if (quotient_ok(amax, s)) {
-    const float y = -__frcp_rn(s);
-    const f32x2 ny = pk(y, y), ss = pk(s, s);
+// v = RN(-v / s), both steps.  s in [2^-60, 2^60] (quotient_ok), and no quotient near the ends of float32's
+// range: one that overflows becomes an infinity or a NaN.  Values so small that a remainder
+// underflows give zero codes either way.
+__device__ __forceinline__ bool quotient_ok(float s) { return s >= 0x1p-60f && s <= 0x1p60f; }
+__device__ __forceinline__ void quotients16(f32x2* v, float s) {
+  const float y = -__frcp_rn(s);
+  const f32x2 ny = pk(y, y), ss = pk(s, s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const f32x2 q0 = mul2(n[i], ny);
-      q[i] = quotient_step(quotient_step(q0, n[i], ss, ny), n[i], ss, ny);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 f = unpk(n[i]);
-      q[i] = pk(__fdiv_rn(-f.x, s), __fdiv_rn(-f.y, s));
-    }
-  }
+  for (int i = 0; i < 8; ++i) v[i] = quotient_step(quotient_step(mul2(v[i], ny), v[i], ss, ny), v[i], ss, ny);
 }
 
 // Eight float32 -> eight E2M1 codes in a word, the first in the low nibble.
@@ -199,42 +208,86 @@ __device__ __forceinline__ uint32_t e2m1x8(const f32x2* q) {
   return r;
 }
 
-// FP4 codes and scale of the 16 channels u = -n (csa2_fp4_quant): w0 the first eight codes, w1 the
-// others.  The code is E2M1 of the correctly rounded quotient u / s.  Only the side of the seven
-// borders m s (m = 1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5) matters, and m s is exact: a u off a border is
-// off by 2^-24 of it or more, so one quotient step decides as the division does, and u = m s
-// gives m itself, whose tie the conversion resolves.
-__device__ __forceinline__ void fp4_encode16(const f32x2* n, uint32_t& w0, uint32_t& w1, uint32_t& sbyte) {
-  const float a = amax16(n);
-  sbyte = cvt_e4m3(__fdiv_rn(a, 6.0f));
-  const float s = e4m3_to_f32(sbyte);
-  w0 = w1 = 0;
+// FP4 codes and scale of the 16 channels u = -n (csa2_fp4_quant) with a = max |u| <= 2^60: w[0] the first
+// eight codes, w[1] the others, w[2] the scale byte.  The code is E2M1 of the correctly rounded
+// quotient u / s.  Only the side of the seven borders m s (m = 1/4, 3/4, 5/4, 7/4, 5/2, 7/2, 5)
+// matters, and m s is exact: a u off a border is off by 2^-24 of it or more, so one quotient step,
+// with a reciprocal good to a step, decides as the division does, and u = m s gives m itself, whose
+// tie the conversion resolves.  The same holds for the scale: the borders between E4M3 values,
+// times 6, are exact.
+__device__ __forceinline__ void fp4_encode16(const f32x2* n, float a, uint32_t* w) {
+  const float a0 = __fmul_rn(a, 1.0f / 6.0f);
+  w[2] = cvt_e4m3(__fmaf_rn(__fmaf_rn(-6.0f, a0, a), 1.0f / 6.0f, a0));
+  const float s = e4m3_to_f32(w[2]);
+  w[0] = w[1] = 0;
   if (!(s > 0.f)) return;
-  f32x2 q[8];
-  if (a <= 0x1p60f) {
-    const float y = -__frcp_rn(s);
-    const f32x2 ny = pk(y, y), ss = pk(s, s);
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-s));
+  const f32x2 ny = pk(y, y), ss = pk(s, s);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = quotient_step(mul2(n[i], ny), n[i], ss, ny);
-  } else {
-    quotients16(q, n, s, a);
+  for (int h = 0; h < 2; ++h) {
+    f32x2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = quotient_step(mul2(n[4 * h + i], ny), n[4 * h + i], ss, ny);
+    w[h] = e2m1x8(q);
   }
-  w0 = e2m1x8(q);
-  w1 = e2m1x8(q + 4);
 }
 
-// E4M3 bytes of RN(-n / s), four words; zero where s is not positive.
-__device__ __forceinline__ void fp8_encode16(const f32x2* n, float s, float amax, uint32_t* w) {
+// The same by the definition, for any x and g: u = x / g.
+static __device__ __noinline__ void fp4_encode16_any(const f32x2* x, float g, uint32_t* w) {
+  f32x2 u[8];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = 0;
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpk(x[i]);
+    u[i] = pk(__fdiv_rn(f.x, g), __fdiv_rn(f.y, g));
+  }
+  w[2] = cvt_e4m3(__fdiv_rn(amax16(u), 6.0f));
+  const float s = e4m3_to_f32(w[2]);
+  w[0] = w[1] = 0;
   if (!(s > 0.f)) return;
-  f32x2 q[8];
-  quotients16(q, n, s, amax);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpk(u[i]);
+    u[i] = pk(__fdiv_rn(f.x, s), __fdiv_rn(f.y, s));
+  }
+  w[0] = e2m1x8(u);
+  w[1] = e2m1x8(u + 4);
+}
+
+__device__ __forceinline__ void e4m3x16(const f32x2* q, uint32_t* w) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 a = unpk(q[2 * i]), b = unpk(q[2 * i + 1]);
     asm("{\n .reg .b16 t0, t1;\n cvt.rn.satfinite.e4m3x2.f32 t0, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 t1, %4, %3;\n"
         " mov.b32 %0, {t0, t1};\n}" : "=r"(w[i]) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  }
+}
+static __device__ __noinline__ void fp8_encode16_any(const f32x2* n, float s, uint32_t* w) {
+  f32x2 q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float2 f = unpk(n[i]);
+    q[i] = pk(__fdiv_rn(-f.x, s), __fdiv_rn(-f.y, s));
+  }
+  e4m3x16(q, w);
+}
+
+// E4M3 bytes of RN(-n / s) with s = RN(max |n| / 448), four words; zero where s is not positive.  n is used up.
+__device__ __forceinline__ void fp8_encode16(f32x2* n, float s, uint32_t* w) {
+  if (quotient_ok(s)) {
+    quotients16(n, s);
+    e4m3x16(n, w);
+  } else if (s > 0.f) {
+    f32x2 t[8];
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = n[i];
+    fp8_encode16_any(t, s, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = b[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = 0;
   }
 }
 

@@ -108,21 +108,22 @@ def test_rms_norm_in_place_and_no_weight():
     assert (np.abs(y.double().cpu().numpy() - ref) <= np.abs(ref) * (4 * U + UB) * 1.001).all()
 
 
-def test_rms_norm_extremes():
-    """Zero rows, squares beyond float32, and non-finite values, row by row."""
-    x = np.zeros((6, 256), np.float32)
+@pytest.mark.parametrize("D,pad", [(256, 0), (1024, 0), (256, 1)])
+def test_rms_norm_extremes(D, pad):
+    """Zero rows, squares beyond float32, and non-finite values, row by row, on each kernel."""
+    x = np.zeros((6, D), np.float32)
     x[1] = 3e18                                     # the sum of squares overflows, the mean does not
     x[2] = 1e38                                     # the mean overflows: r = 0
     x[3, 5], x[4, 7] = np.inf, np.nan
     x[3, 6] = x[4, 8] = 1
-    x[5] = np.linspace(-1, 1, 256)
-    y, _ = csa2.rms_norm(gpu(x), out_dtype=torch.float32)
+    x[5] = np.linspace(-1, 1, D)
+    y, _ = csa2.rms_norm(strided(x, torch.float32, pad), out_dtype=torch.float32)
     y = y.cpu().numpy()
     assert (y[0] == 0).all() and np.allclose(y[1], 1, rtol=8 * U, atol=0) and (y[2] == 0).all()
     assert np.isnan(y[3, 5]) and (np.delete(y[3], 5) == 0).all() and np.isnan(y[4]).all()
     ref = rows.rms_norm(x[5], None, 1e-6)
     assert (np.abs(y[5] - ref) <= np.abs(ref) * 5 * U).all()
-    q, _ = csa2.rms_norm_fp4(gpu(x))
+    q, _ = csa2.rms_norm_fp4(strided(x, torch.float32, pad))
     s = q.row_scales().cpu().numpy()
     assert (s[0] == 0).all() and (s[4] == 0x7F).all() and (q.codes[4] == 0).all()
 
@@ -161,6 +162,36 @@ def test_fp4_quant_borders():
     assert np.array_equal(q.row_scales().cpu().numpy(), rs)
     assert (rs == np.arange(1, 127)[:, None]).all()
     assert np.array_equal(q.codes.cpu().numpy(), rc)
+
+
+@pytest.mark.parametrize("bf16", [True, False])
+def test_fp4_quant_random_gscales(bf16):
+    """Matrix scales over 80 octaves (and beyond, where the kernel divides): the quotients x / gscale
+    decide the codes bit for bit."""
+    r = np.random.default_rng(12)
+    x = values(r, (64, 1024), bf16)
+    for e in [-75, -61, -40, -12, -3, 0, 5, 20, 59, 63]:
+        g = np.float32(np.ldexp(1 + r.random(), e))
+        with np.errstate(over="ignore"):
+            y = (x * np.float32(2.0 ** e)).astype(np.float32)
+        y = formats.bf16_value(formats.bf16_round(y)).astype(np.float32) if bf16 else y
+        q = csa2.fp4_quant(gpu(y, T[bf16]), gpu(np.array([g], np.float32)))
+        rc, rs = rows.fp4_quantize(y, g)
+        assert np.array_equal(q.row_scales().cpu().numpy(), rs), e
+        assert np.array_equal(q.codes.cpu().numpy(), rc), e
+
+
+def test_fp4_quant_scale_borders():
+    """Groups whose amax is at, just below and just above 6 times each border between E4M3 values."""
+    v = formats.e4m3_value(np.arange(0, 127))
+    m = ((v[1:] + v[:-1]) / 2).astype(np.float32) * np.float32(6)
+    x = np.zeros((126, 48), np.float32)
+    for j, u in enumerate((m, np.nextafter(m, np.float32(0)), np.nextafter(m, np.float32(np.inf)))):
+        x[:, 16 * j + 3] = -u
+        x[:, 16 * j + 4] = u / 2
+    q = csa2.fp4_quant(gpu(x))
+    rc, rs = rows.fp4_quantize(x)
+    assert np.array_equal(q.row_scales().cpu().numpy(), rs) and np.array_equal(q.codes.cpu().numpy(), rc)
 
 
 def test_fp4_quant_nonfinite():
