@@ -309,16 +309,17 @@ def _float_type(t, name):
 
 
 def _rows_of(t, name):
-    """Data pointer of a CUDA tensor whose last dimension is contiguous."""
+    """(data pointer, row stride) of a CUDA matrix whose rows are contiguous."""
     if not t.is_cuda:
         raise ValueError(f"{name}: expected a CUDA tensor")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    rows, last = t.stride()
+    if last != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr()
+    return t.data_ptr(), rows
 
 
 def _dense(t, dtype, name):
-    """Data pointer of a contiguous CUDA tensor of one type, None of None."""
+    """Data pointer of a contiguous CUDA tensor of one type, 0 of None."""
     if t is None:
         return 0
     if t.dtype is not dtype:
@@ -341,7 +342,9 @@ _FP4_LINEAR = struct.Struct("@N" + 2 * _FP4_ROWS + "Pi0P")
 
 def _launch(fn, packed, t):
     """Call fn on the current stream of tensor t's device."""
-    _lib.check(getattr(_lib.lib(), fn)(packed, torch._C._cuda_getCurrentRawStream(t.get_device())))
+    status = getattr(_lib.lib(), fn)(packed, torch._C._cuda_getCurrentRawStream(t.get_device()))
+    if status:
+        _lib.check(status)
 
 
 @dataclass
@@ -390,27 +393,29 @@ class Fp4Rows:
 
 def _norm(x, weight, eps, residual, residual_out, out_form, group, out, out_stride, out_scale, out4):
     """One csa2_rms_norm call; returns residual_out (allocated here if need be)."""
-    T, D = x.shape
+    T, D = shape = x.shape
+    xp, xs = _rows_of(x, "x")
     wp = wt = rp = rs = op = os_ = rt = 0
     if weight is not None:
         if weight.shape != (D,):
             raise ValueError(f"weight must have {D} elements")
-        wp, wt = _rows_of(weight, "weight"), _float_type(weight, "weight")
+        wt = _float_type(weight, "weight")
+        wp = _dense(weight, weight.dtype, "weight")
     if residual is not None:
         if residual_out is None:
-            residual_out = torch.empty((T, D), dtype=residual.dtype, device=x.device)
-        elif residual_out.shape != x.shape or residual_out.dtype is not residual.dtype:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        elif residual_out.shape != shape or residual_out.dtype is not residual.dtype:
             raise ValueError("residual and residual_out must have x's shape and one type")
-        if residual.shape != x.shape:
+        if residual.shape != shape:
             raise ValueError("residual and residual_out must have x's shape and one type")
         rt = _float_type(residual, "residual")
-        rp, rs = _rows_of(residual, "residual"), residual.stride(0)
-        op, os_ = _rows_of(residual_out, "residual_out"), residual_out.stride(0)
+        rp, rs = _rows_of(residual, "residual")
+        op, os_ = _rows_of(residual_out, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     _launch("csa2_rms_norm", _RMS_NORM.pack(
-        _RMS_NORM.size, T, D, _rows_of(x, "x"), _float_type(x, "x"), rt, x.stride(0), rp, op, rs, os_, wp, wt, eps,
-        out_form, group, out, out_stride, out_scale, *out4), x)
+        _RMS_NORM.size, T, D, xp, _float_type(x, "x"), rt, xs, rp, op, rs, os_, wp, wt, eps, out_form, group, out,
+        out_stride, out_scale, *out4), x)
     return residual_out
 
 
@@ -426,8 +431,8 @@ def rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, out_
         out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
-    return out, _norm(x, weight, eps, residual, residual_out, _float_type(out, "out"), 0, _rows_of(out, "out"),
-                      out.stride(0), 0, _NO_FP4)
+    return out, _norm(x, weight, eps, residual, residual_out, _float_type(out, "out"), 0, *_rows_of(out, "out"), 0,
+                      _NO_FP4)
 
 
 def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, group=0, out=None, out_scale=None):
@@ -444,7 +449,7 @@ def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, 
         out_scale = torch.empty((T, n), dtype=torch.float32, device=x.device)
     elif out_scale.shape != (T, n):
         raise ValueError(f"out_scale must be [{T}, {n}]")
-    residual_out = _norm(x, weight, eps, residual, residual_out, FP8E4M3, group, _rows_of(out, "out"), out.stride(0),
+    residual_out = _norm(x, weight, eps, residual, residual_out, FP8E4M3, group, *_rows_of(out, "out"),
                          _dense(out_scale, torch.float32, "out_scale"), _NO_FP4)
     return out, out_scale, residual_out
 
@@ -497,11 +502,15 @@ def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=N
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
-    xt, xh, _ = x.stride()
-    ot, oh, _ = out.stride()
+    if not x.is_cuda or not out.is_cuda:
+        raise ValueError("expected CUDA tensors")
+    xt, xh, xc = x.stride()
+    ot, oh, oc = out.stride()
+    if (xc != 1 or oc != 1) and D > 1:
+        raise ValueError("the last dimension must be contiguous")
     _launch("csa2_rope", _ROPE.pack(
         _ROPE.size, T, H, D, 2 * half, D - 2 * half if first is None else first, 1 if interleaved else 0,
-        1 if inverse else 0, _float_type(x, "x"), _rows_of(x, "x"), _rows_of(out, "out"), xt, xh, ot, oh,
+        1 if inverse else 0, _float_type(x, "x"), x.data_ptr(), out.data_ptr(), xt, xh, ot, oh,
         _dense(pos, torch.int32, "pos"), _dense(cos, torch.float32, "cos"), _dense(sin, torch.float32, "sin"),
         positions), x)
     return out
@@ -517,8 +526,8 @@ def fp4_quant(x, gscale=None, out=None):
         raise ValueError("give gscale with out, or out alone")
     elif out.codes.shape != (T, K // 2):
         raise ValueError("out must have x's shape")
-    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, _rows_of(x, "x"), _float_type(x, "x"), x.stride(0),
-                                              *out.fields()), x)
+    xp, xs = _rows_of(x, "x")
+    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, xp, _float_type(x, "x"), xs, *out.fields()), x)
     return out
 
 

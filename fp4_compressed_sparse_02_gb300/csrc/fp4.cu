@@ -396,7 +396,7 @@ struct Params {
   const float* gw;
   void* out;
   int T, N, nkt, nft, ntt, band, split;
-  bool out32, tma_out, vec4;
+  bool out32, vec4;
 };
 
 __device__ __forceinline__ void tmem_alloc2(uint32_t* slot, uint32_t ncols) {
@@ -453,6 +453,28 @@ __device__ __forceinline__ void store_wait_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" :: "n"(PENDING) : "memory");
 }
 
+// 32 columns of 32 rows (a lane's) into shared memory as a TMA store wants them: float32 rows of 128
+// bytes, 16-byte chunk j at j ^ (row % 8), or bf16 rows of 64 bytes, chunk j at j ^ (row / 2 % 4).
+__device__ __forceinline__ void stage32(const uint32_t (&v)[32], uint32_t at, int lane, float alpha, bool out32) {
+  if (out32) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 128 + ((j ^ (lane & 7)) << 4)),
+                   "f"(__uint_as_float(v[4 * j]) * alpha), "f"(__uint_as_float(v[4 * j + 1]) * alpha),
+                   "f"(__uint_as_float(v[4 * j + 2]) * alpha), "f"(__uint_as_float(v[4 * j + 3]) * alpha) : "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]) * alpha, __uint_as_float(v[8 * j + 2 * i + 1]) * alpha);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
+                   "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+}
+
 // Tile t: bands of `band` token tiles; within a band the token tile runs fastest.
 __device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) {
   const int per = p.band * p.nft, bnd = t / per, first = bnd * p.band;
@@ -471,9 +493,11 @@ __device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) 
 // scale copies alone 282 us, together without the results 414 us; all of it 445 us, 6.2 PFLOP/s.
 //   Tile: 256 x 192 with two accumulators (results stored while the next tile runs) took 526 us:
 // per product it loads a sixth more.  Reading the accumulator 32 columns at a time between stores
-// took 496 us.  Half of an earlier 1270 us was the issuing thread's own descriptor arithmetic.
+// took 496 us.  Two thirds of an earlier 1270 us was the issuing thread's own descriptor arithmetic.
 //   Split, 192 x 32768 -> 5120 (20 tiles): 1 46 us, 2 31 us, 3 26 us, 4 40 us (20 clusters of eight
 // do not all run at once); one-CTA tiles of 128 x 192 split in three took 28 us.
+// TMA_OUT: rows of the result that TMA can address; otherwise warps store them 32 columns at a time.
+template <bool TMA_OUT>
 __global__ void __launch_bounds__(pairs::THREADS, 1)
     k_fp4_linear_pair(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mw,
                       const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
@@ -625,58 +649,63 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
         break;                                            // the cluster's only tile
       }
       const int t0 = (2 * tt + (int)rank) * BM + 32 * (warp & 3), f0 = ft * BN + 128 * (warp >> 2);
-      uint32_t acc[4][32];                                // all of this warp's part, so that it is free at once
+      if (TMA_OUT) {
+        uint32_t acc[4][32];                              // all of this warp's part, so that it is free at once
 #pragma unroll
-      for (int i = 0; i < 4; ++i) tc::tmem_ld32(tq + 32u * i, acc[i]);
-      tc::tmem_ld_wait();
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
-#pragma unroll
-      for (int ci = 0; ci < 4; ++ci) {
-        const int c = 32 * ci;
-        const uint32_t(&v)[32] = acc[ci];
-        if (t0 >= p.T || f0 + c >= p.N) continue;
-        // the slice's last store has read it (float32 slices take both halves)
-        if (lane == 0) p.out32 ? store_wait_read<0>() : store_wait_read<1>();
+        for (int i = 0; i < 4; ++i) tc::tmem_ld32(tq + 32u * i, acc[i]);
+        tc::tmem_ld_wait();
+        tc::fence_before_sync();
         __syncwarp();
-        const uint32_t at = slice + (p.out32 ? 0u : (uint32_t)(c & 32) * (SLICE / 32));
-        if (p.out32) {                                    // rows of 128 bytes, 16-byte chunk j at j ^ (row % 8)
+        if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            asm volatile("st.shared.v4.f32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 128 + ((j ^ (lane & 7)) << 4)),
-                         "f"(__uint_as_float(v[4 * j]) * alpha), "f"(__uint_as_float(v[4 * j + 1]) * alpha),
-                         "f"(__uint_as_float(v[4 * j + 2]) * alpha), "f"(__uint_as_float(v[4 * j + 3]) * alpha) : "memory");
-        } else {                                          // rows of 64 bytes, chunk j at j ^ (row / 2 % 4)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]) * alpha, __uint_as_float(v[8 * j + 2 * i + 1]) * alpha);
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-          }
-        }
-        if (p.tma_out) {
+        for (int i = 0; i < 4; ++i) {
+          if (t0 >= p.T || f0 + 32 * i >= p.N) continue;
+          // the slice's last store has read it (float32 slices take both halves)
+          if (lane == 0) p.out32 ? store_wait_read<0>() : store_wait_read<1>();
+          __syncwarp();
+          const uint32_t at = slice + (p.out32 ? 0u : (uint32_t)(i & 1) * SLICE);
+          stage32(acc[i], at, lane, alpha, p.out32);
           tc::fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) tma_store(&mo, f0 + c, t0, at);
-        } else {                                          // rows that TMA cannot address: 32 columns at a time
+          if (lane == 0) tma_store(&mo, f0 + 32 * i, t0, at);
+        }
+      } else {
+        const int rows = min(32, p.T - t0);
+#pragma unroll 1
+        for (int c = 0; c < 128; c += 32) {
+          uint32_t v[32];
+          tc::tmem_ld32(tq + (uint32_t)c, v);
+          tc::tmem_ld_wait();
+          if (c == 96) {                                  // this warp has read its part
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
+          }
+          if (rows <= 0 || f0 + c >= p.N) continue;
+          stage32(v, slice, lane, alpha, p.out32);
           __syncwarp();
-          const int rows = min(32, p.T - t0);
-          for (int r = 0; r < rows && f0 + c + lane < p.N; ++r) {
-            const long long o = (long long)(t0 + r) * p.N + f0 + c + lane;
-            if (p.out32) {
-              float e;
-              asm volatile("ld.shared.f32 %0, [%1];" : "=f"(e)
-                           : "r"(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
-              static_cast<float*>(p.out)[o] = e;
-            } else {
-              uint16_t e;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(e)
-                           : "r"(at + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
-              static_cast<uint16_t*>(p.out)[o] = e;
+          const bool in = f0 + c + lane < p.N;
+          const long long o = (long long)t0 * p.N + f0 + c + lane;
+#pragma unroll
+          for (int r0 = 0; r0 < 32; r0 += 16) {           // sixteen rows' values, then their stores
+            uint32_t e[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int r = r0 + i;
+              if (p.out32)
+                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(e[i])
+                             : "r"(slice + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
+              else
+                asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}" : "=r"(e[i])
+                             : "r"(slice + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (!in || r0 + i >= rows) continue;
+              if (p.out32)
+                static_cast<uint32_t*>(p.out)[o + (long long)(r0 + i) * p.N] = e[i];
+              else
+                static_cast<uint16_t*>(p.out)[o + (long long)(r0 + i) * p.N] = (uint16_t)e[i];
             }
           }
           __syncwarp();
@@ -797,15 +826,15 @@ bool out_map(CUtensorMap* map, void* base, long long rows, long long cols, bool 
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <bool TMA_OUT>
 cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   using namespace pairs;
   CUtensorMap mx, mw, msx, msw, mo{};
   pairs::Params p{};
   p.out32 = a.out_dtype == CSA2_F32;
-  p.tma_out = ((uintptr_t)a.out & 15) == 0 && (long long)a.w.rows * (p.out32 ? 4 : 2) % 16 == 0;
   if (!codes_map(&mx, a.x.codes, a.x.rows, a.x.cols / 2, BM) || !codes_map(&mw, a.w.codes, a.w.rows, a.w.cols / 2, BN / 2) ||
       !scales_map(&msx, a.x, 1) || !scales_map(&msw, a.w, 2) ||
-      (p.tma_out && !out_map(&mo, a.out, a.x.rows, a.w.rows, p.out32)))
+      (TMA_OUT && !out_map(&mo, a.out, a.x.rows, a.w.rows, p.out32)))
     return cudaErrorInvalidValue;
   p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out;
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64;
@@ -816,9 +845,9 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.vec4 = groups_of_four(a);
   static int pairs_at[5] = {0};                           // clusters of s pairs the GPU holds at once
   if (!pairs_at[1]) {
-    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_pair, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_pair<TMA_OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
     if (e != cudaSuccess) return e;
-    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_pair, 2 * s, THREADS, SMEM);
+    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_pair<TMA_OUT>, 2 * s, THREADS, SMEM);
     if (!pairs_at[1]) return cudaErrorInvalidConfiguration;
   }
   // few tiles: split the sum as far as every cluster still runs at once, two stages a CTA or more
@@ -826,19 +855,21 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.split = 1;
   for (int s = 2; s <= 4; ++s)
     if (ntile <= pairs_at[s] && 2 * s <= nkb) p.split = s;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2u * (unsigned)p.split;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   const long long clusters = p.split > 1 || ntile < pairs_at[1] ? ntile : pairs_at[1];
-  cfg.gridDim = dim3(2u * (unsigned)(p.split * clusters));   // persistent: started late
+  cfg.gridDim = dim3(2u * (unsigned)(p.split * clusters));
   cfg.blockDim = pairs::THREADS;
   cfg.dynamicSmemBytes = SMEM;
   cfg.stream = st;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_fp4_linear_pair, mx, mw, msx, msw, mo, p);
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_fp4_linear_pair<TMA_OUT>, mx, mw, msx, msw, mo, p);
 }
 
 template <int BN>
@@ -895,7 +926,8 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (T <= 32) return launch_linear<32>(a, st);
   if (T <= 64) return launch_linear<64>(a, st);
   if (T <= 128) return launch_linear<128>(a, st);
-  return launch_linear_pair(a, st);
+  const bool tma = ((uintptr_t)a.out & 15) == 0 && (long long)a.w.rows * (a.out_dtype == CSA2_F32 ? 4 : 2) % 16 == 0;
+  return tma ? launch_linear_pair<true>(a, st) : launch_linear_pair<false>(a, st);
 }
 
 uint32_t read_clear_error_fp4() {

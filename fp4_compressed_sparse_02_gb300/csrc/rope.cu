@@ -10,6 +10,8 @@ CSA2_DEFINE_ERROR_WORD(g_err_rope);
 
 namespace {
 
+constexpr int kThreads = 128;
+
 struct RopeParams {
   const void* x;
   void* out;
@@ -17,7 +19,7 @@ struct RopeParams {
   const float* cos;
   const float* sin;
   long long xt, xh, ot, oh;
-  int H, D, d_rope, first, max_pos, units, turn_units;
+  int T, H, D, d_rope, first, max_pos, units, turn_units;
   bool inverse;
 };
 
@@ -61,66 +63,61 @@ __device__ __forceinline__ void load_angles(float* v, const float* p) {
 
 // A unit is V neighbouring channels that are copied, or that turn: V channels of V/2
 // interleaved pairs (V = 1: one pair), or V channels of each half.  A thread keeps its unit and
-// runs over heads, HEADS of them at a time, so a token's angles are read once for all of them and
-// several loads are under way.  A token with a bad position is copied as it is.
+// runs over heads, so a token's angles are read once for all of them, and over tokens, whose
+// positions it reads one ahead: a CTA for each token spends its life waiting for the position
+// and then for the angles.  A token with a bad position is copied as it is.
+//   What bounds it: memory.  8192 tokens x 64 heads x 128 channels in bf16 (273 MB, 40.2 us at the copy
+// rate): 46.0 us; a CTA for each token 52.4 us, two heads' loads at once 51 us (fewer CTAs fit),
+// 256 threads 46.4 us.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) k_rope(RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 10) k_rope(RopeParams p) {
   pdl_wait();
   pdl_trigger();
   using Vt = Vec<T, V>;
   constexpr int NP = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;   // pairs of a unit
   constexpr int PARTS = INTERLEAVED && V > 1 ? 1 : 2;         // vectors of a unit that turns
-  constexpr int HEADS = 4;
-  const long long t = blockIdx.x;
-  const T* x = static_cast<const T*>(p.x) + t * p.xt;
-  T* o = static_cast<T*>(p.out) + t * p.ot;
   const int h0 = blockIdx.y * blockDim.y + threadIdx.y, hs = gridDim.y * blockDim.y;
   const int half = p.d_rope / 2;
-  const int ps = ld_s32(p.pos + t);
-  const bool turns = ps >= 0 && ps < p.max_pos;
-  if (!turns && threadIdx.x == 0 && threadIdx.y == 0) raise_error(&g_err_rope, CSA2_DEVERR_POS);
-  for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
-    const bool turn = u < p.turn_units;
-    float cs[NP], sn[NP];
-    int c = (u - p.turn_units) * V, c2 = 0;
-    if (!turn) {                                          // channels that are copied
-      if (c >= p.first) c += p.d_rope;
-    } else {
-      c = p.first + (PARTS == 1 ? u * V : INTERLEAVED ? 2 * u : u * V);
-      c2 = PARTS == 1 ? 0 : INTERLEAVED ? c + 1 : c + half;
+  int next = blockIdx.x < p.T ? ld_s32(p.pos + blockIdx.x) : 0;   // a token's position, one token ahead
+  for (long long t = blockIdx.x; t < p.T; t += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + t * p.xt;
+    T* o = static_cast<T*>(p.out) + t * p.ot;
+    const int ps = next;
+    const bool good = ps >= 0 && ps < p.max_pos;
+    if (t + gridDim.x < p.T) next = ld_s32(p.pos + t + gridDim.x);
+    if (!good && threadIdx.x == 0 && threadIdx.y == 0) raise_error(&g_err_rope, CSA2_DEVERR_POS);
+    for (int u = threadIdx.x; u < p.units; u += blockDim.x) {
+      const bool turn = u < p.turn_units, turns = turn && good;
+      int c = (u - p.turn_units) * V, c2 = 0;             // the unit's channels
+      if (!turn) {
+        if (c >= p.first) c += p.d_rope;
+      } else {
+        c = p.first + (PARTS == 2 && INTERLEAVED ? 2 * u : u * V);
+        c2 = INTERLEAVED ? c + 1 : c + half;
+      }
+      float cs[NP], sn[NP];
       if (turns) {
         load_angles<NP>(cs, p.cos + (long long)ps * half + u * NP);
         load_angles<NP>(sn, p.sin + (long long)ps * half + u * NP);
-#pragma unroll
-        for (int i = 0; i < NP; ++i) sn[i] = p.inverse ? -sn[i] : sn[i];
       }
-    }
-    for (int h = h0; h < p.H; h += HEADS * hs) {
-      Vt v[HEADS], w[HEADS];
-#pragma unroll
-      for (int k = 0; k < HEADS; ++k) {
-        const T* at = x + (long long)(h + k * hs) * p.xh;
-        if (h + k * hs >= p.H) continue;
-        v[k] = *reinterpret_cast<const Vt*>(at + c);
-        if (PARTS == 2 && turn) w[k] = *reinterpret_cast<const Vt*>(at + c2);
-      }
-#pragma unroll
-      for (int k = 0; k < HEADS; ++k) {
-        if (h + k * hs >= p.H) continue;
-        if (turn && turns) {
+      for (int h = h0; h < p.H; h += hs) {
+        const T* from = x + h * p.xh;
+        T* to = o + h * p.oh;
+        Vt v = *reinterpret_cast<const Vt*>(from + c), w = v;
+        if (PARTS == 2 && turn) w = *reinterpret_cast<const Vt*>(from + c2);
+        if (turns) {
 #pragma unroll
           for (int i = 0; i < NP; ++i) {
-            T& e0 = PARTS == 1 ? v[k].e[2 * i] : v[k].e[i];
-            T& e1 = PARTS == 1 ? v[k].e[2 * i + (V > 1)] : w[k].e[i];
+            T& e0 = PARTS == 1 ? v.e[2 * i] : v.e[i];
+            T& e1 = PARTS == 1 ? v.e[2 * i + (V > 1)] : w.e[i];
             float a = to_f32(e0), b = to_f32(e1);
-            rope_pair(a, b, cs[i], sn[i]);
+            rope_pair(a, b, cs[i], p.inverse ? -sn[i] : sn[i]);
             e0 = from_f32<T>(a);
             e1 = from_f32<T>(b);
           }
         }
-        T* at = o + (long long)(h + k * hs) * p.oh;
-        *reinterpret_cast<Vt*>(at + c) = v[k];
-        if (PARTS == 2 && turn) *reinterpret_cast<Vt*>(at + c2) = w[k];
+        *reinterpret_cast<Vt*>(to + c) = v;
+        if (PARTS == 2 && turn) *reinterpret_cast<Vt*>(to + c2) = w;
       }
     }
   }
@@ -133,17 +130,25 @@ cudaError_t launch_rope_v(const csa2_rope_args& a, RopeParams p, cudaStream_t st
   const bool in_place = a.out == a.x;
   p.turn_units = a.interleaved ? (V > 1 ? a.d_rope / V : a.d_rope / 2) : a.d_rope / 2 / V;
   p.units = p.turn_units + (in_place ? 0 : (a.D - a.d_rope) / V);
-  const int tx = p.units < 256 ? p.units : 256;
-  const int ty = 256 / tx < a.H ? 256 / tx : a.H;
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const auto k = a.interleaved ? k_rope<T, V, true> : k_rope<T, V, false>;
+  static int resident[2] = {0};                           // CTAs the GPU holds at once
+  int& r = resident[a.interleaved != 0];
+  if (!r) {
+    int dev = 0, sms = 0, per = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kThreads, 0);
+    if (e != cudaSuccess) return e;
+    r = sms * (per > 0 ? per : 1);
+  }
+  const int tx = p.units < kThreads ? p.units : kThreads;
+  const int ty = kThreads / tx < a.H ? kThreads / tx : a.H;
   const int per = (a.H + ty - 1) / ty;                    // CTAs that give each thread one head
-  long long gy = (8LL * sms + a.T - 1) / a.T;             // fill the GPU, then several heads a thread
+  long long gy = (r + a.T - 1) / a.T;                     // fill the GPU, then several heads a thread
   if (gy > per) gy = per;
-  const dim3 grid((unsigned)a.T, (unsigned)gy), block((unsigned)tx, (unsigned)ty);
-  return a.interleaved ? launch_k(k_rope<T, V, true>, grid, block, 0, st, p)
-                       : launch_k(k_rope<T, V, false>, grid, block, 0, st, p);
+  const long long gx = a.T < r / gy ? a.T : r / gy;
+  const dim3 grid((unsigned)(gx > 0 ? gx : 1), (unsigned)gy), block((unsigned)tx, (unsigned)ty);
+  return launch_k(k, grid, block, 0, st, p);
 }
 
 }  // namespace
@@ -153,7 +158,7 @@ cudaError_t launch_rope(const csa2_rope_args& a, cudaStream_t st) {
   RopeParams p{};
   p.x = a.x, p.out = a.out, p.pos = a.pos, p.cos = a.rope_cos, p.sin = a.rope_sin;
   p.xt = a.x_stride_t, p.xh = a.x_stride_h, p.ot = a.out_stride_t, p.oh = a.out_stride_h;
-  p.H = a.H, p.D = a.D, p.d_rope = a.d_rope, p.first = a.rot_first, p.max_pos = a.rope_max_pos;
+  p.T = a.T, p.H = a.H, p.D = a.D, p.d_rope = a.d_rope, p.first = a.rot_first, p.max_pos = a.rope_max_pos;
   p.inverse = a.inverse != 0;
   const int v = a.dtype == CSA2_F32 ? 4 : 8;
   const bool vec = ((uintptr_t)a.x & 15) == 0 && ((uintptr_t)a.out & 15) == 0 && a.x_stride_t % v == 0 &&
@@ -205,7 +210,7 @@ __device__ __forceinline__ void sincos_pair(int x0, int x1, f32x2& s, f32x2& c) 
 // The angle p f_i in turns, modulo 1, is a 64-bit product that a thread carries from one of its
 // positions to the next by an addition.  Its nearest multiple of a quarter turn picks which of
 // +-sin, +-cos of the remainder is which.  V channels a thread (4, or 1 where half % 4 != 0).
-//   1,048,576 positions x 32 pairs (268 MB written, 39.5 us at the copy rate): TABLE_US; with the library's
+//   1,048,576 positions x 32 pairs (268 MB written, 39.5 us at the copy rate): 38.3 us; with the library's
 // sincospif and a 64-bit division for the place it took 271 us.
 template <int V>
 __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams t) {
