@@ -3,4 +3,4 @@ sparse indexer (Full / Reindex / Reuse) and sparse MQA attention, behind the C A
 include/csa2.h.  Importing this package does not load the CUDA library; the first call
 does, and raises if it has not been built."""
 
-__all__ = ["csa2", "synth", "schedule"]
+__all__ = ["csa2", "layer", "synth", "schedule"]
