@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(256, 5) k_fp4_quant(QuantRowsParams p) {
       f32x2 n[8];                                         // u, negated (rows.cuh)
       if (VEC) {
         Raw16<X32> raw;
-        raw.load(p.x, x);
+        raw.load(p.x, x, false);
         if (!over) raw.negate();                          // dividing by g negates
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i] = raw.pair(i);

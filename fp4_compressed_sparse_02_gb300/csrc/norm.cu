@@ -22,7 +22,7 @@ struct NormParams {
   int T, D, nkt, lanes;
   float eps;
   int group;
-  bool x32, r32, w32;
+  bool x32, r32, w32, wide;                // wide: rows of x, the residual and the output are 32-byte aligned
 };
 
 // (hi, lo) += (b, blo) in two float32 words: the rounding error of the sum goes into lo (Knuth's
@@ -39,24 +39,25 @@ __device__ __forceinline__ void lanes_sum2(float& hi, float& lo, int lanes) {
   }
 }
 
-// The sum of squares of 16 channels (scaled: times 2^-128) in two words.  The running sums start at a
-// power of two c of at least 16 times the largest square, so every step's rounding error is
-// h^2 - (s - s_before), a difference that is exact and a fused product that keeps 2^-48 of c; c
+// The sum of squares of NP <= 16 pairs of channels (scaled: times 2^-128) in two words.  The running sums
+// start at a power of two c of at least 16 times the largest square, so every step's rounding error
+// is h^2 - (s - s_before), a difference that is exact and a fused product that keeps 2^-48 of c; c
 // leaves the sums exactly.  Two steps a pair fewer than TwoSum.
-__device__ __forceinline__ void squares16(const f32x2* h, bool scaled, float& hi, float& lo) {
-  const float m = scaled ? amax16(h) * 0x1p-64f : amax16(h), q = __fmul_rn(m, m);
+template <int NP>
+__device__ __forceinline__ void squares(const f32x2* h, bool scaled, float& hi, float& lo) {
+  const float m = amax_pairs<NP>(h) * (scaled ? 0x1p-64f : 1.f), q = __fmul_rn(m, m);
   const float c = __uint_as_float((__float_as_uint(fminf(q, 0x1p100f)) & 0x7f800000u) + (5u << 23));
   f32x2 a = pk(c, c), b = 0;
   if (!scaled) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NP; ++i) {
       const f32x2 s = fma2(h[i], h[i], a);
       b = add2(b, fma2(h[i], h[i], sub2(a, s)));
       a = s;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < NP; ++i) {
       const f32x2 v = mul2(h[i], pk(0x1p-64f, 0x1p-64f)), s = fma2(v, v, a);
       b = add2(b, fma2(v, v, sub2(a, s)));
       a = s;
@@ -93,12 +94,12 @@ __device__ __forceinline__ void load_weights(f32x2* w, const NormParams& p, int 
   if (!p.w || !has) return;
   if (p.w32) {
     Raw16<true> r;
-    r.load(p.w, 16 * ch, true);
+    r.load_again(p.w, 16 * ch);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
   } else {
     Raw16<false> r;
-    r.load(p.w, 16 * ch, true);
+    r.load_again(p.w, 16 * ch);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = r.pair(i);
   }
@@ -197,8 +198,8 @@ __global__ void __launch_bounds__(256) k_rms_norm_small(NormParams p) {
   long long row = (long long)blockIdx.x * rpb + tid / p.lanes;
   const auto fetch = [&](long long r) {
     if (has && r < p.T) {
-      xr.load(p.x, r * p.sx + 16 * ch);
-      if (RES) rr.load(p.res, r * p.sr + 16 * ch);
+      xr.load(p.x, r * p.sx + 16 * ch, p.wide);
+      if (RES) rr.load(p.res, r * p.sr + 16 * ch, p.wide);
     } else {
       xr.zero();
       rr.zero();
@@ -210,14 +211,14 @@ __global__ void __launch_bounds__(256) k_rms_norm_small(NormParams p) {
     const bool mine = has && row < p.T;
     f32x2 h[8];
     add_residual<X32, RES>(h, xr, rr);
-    if (RES == 2 && mine) store16<true>(h, p.res_out, row * p.so_res + 16 * ch);
-    if (RES == 1 && mine) rr.store(p.res_out, row * p.so_res + 16 * ch);   // the sum, in bf16
+    if (RES == 2 && mine) store16<true>(h, p.res_out, row * p.so_res + 16 * ch, p.wide);
+    if (RES == 1 && mine) rr.store(p.res_out, row * p.so_res + 16 * ch, p.wide);   // the sum, in bf16
     fetch(row + step);
     float r = 0.f;
     bool done = false;
     for (bool scaled = false;; scaled = true) {           // again where squares leave float32's range
       float hi, lo;
-      squares16(h, scaled, hi, lo);
+      squares<8>(h, scaled, hi, lo);
       lanes_sum2(hi, lo, p.lanes);
       const float v = inverse_rms(hi, lo, p.D, p.eps, scaled);
       if (!done) r = v;                                   // rows of the warp that were fine keep what they had
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(256) k_rms_norm_small(NormParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = mul2(mul2(h[i], pk(r, r)), w[i]);
     if (OUT == CSA2_BF16 || OUT == CSA2_F32) {
-      if (mine) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch);
+      if (mine) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch, p.wide);
     } else if (OUT == CSA2_FP4E2M1X2) {
       uint32_t e[3] = {0, 0, 0};
       if (mine) {
@@ -257,6 +258,10 @@ __global__ void __launch_bounds__(256) k_rms_norm_small(NormParams p) {
 // Aligned rows of D = 16 c channels, D <= 8192: a CTA a row at a time, one chunk a thread from the
 // addition to the last store; one barrier for the sum (and one for a row's E4M3 scale).  The next
 // row's loads are issued before this row's arithmetic.
+//   What bounds it: 8192 x 5120 with a residual to FP4 (275 MB, 40.6 us at the copy rate) takes 50.0 us, 5.5 TB/s;
+// 55 us when two 16-byte accesses touch every sector where one of 32 bytes does.  One CTA an SM 73 us, two
+// (76 registers a thread) 55, three (64 registers, spills) 53 us.  Copying the next row to shared memory
+// instead of registers took 69 us; two chunks a thread 70 us.
 template <int OUT, bool X32, int RES>
 __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
   pdl_wait();
@@ -279,24 +284,24 @@ __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
   rr.zero();
   long long row = blockIdx.x;
   if (has && row < p.T) {
-    xr.load(p.x, row * p.sx + 16 * ch);
-    if (RES) rr.load(p.res, row * p.sr + 16 * ch);
+    xr.load(p.x, row * p.sx + 16 * ch, p.wide);
+    if (RES) rr.load(p.res, row * p.sr + 16 * ch, p.wide);
   }
   for (int par = 0; row < p.T; row += grid, par ^= 1) {
     f32x2 h[8];
     add_residual<X32, RES>(h, xr, rr);
     if (has) {
-      if (RES == 2) store16<true>(h, p.res_out, row * p.so_res + 16 * ch);
-      if (RES == 1) rr.store(p.res_out, row * p.so_res + 16 * ch);   // the sum, in bf16
+      if (RES == 2) store16<true>(h, p.res_out, row * p.so_res + 16 * ch, p.wide);
+      if (RES == 1) rr.store(p.res_out, row * p.so_res + 16 * ch, p.wide);   // the sum, in bf16
       if (row + grid < p.T) {
-        xr.load(p.x, (row + grid) * p.sx + 16 * ch);
-        if (RES) rr.load(p.res, (row + grid) * p.sr + 16 * ch);
+        xr.load(p.x, (row + grid) * p.sx + 16 * ch, p.wide);
+        if (RES) rr.load(p.res, (row + grid) * p.sr + 16 * ch, p.wide);
       }
     }
     float r;
     for (bool scaled = false;; scaled = true) {           // again where squares leave float32's range
       float hi, lo;
-      squares16(h, scaled, hi, lo);
+      squares<8>(h, scaled, hi, lo);
       lanes_sum2(hi, lo, 32);
       if (scaled) __syncthreads();                        // every warp has read the first sums
       if (lane == 0) part[par][warp] = make_float2(hi, lo);
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) h[i] = mul2(mul2(h[i], pk(r, r)), w[i]);
     if (OUT == CSA2_BF16 || OUT == CSA2_F32) {
-      if (has) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch);
+      if (has) store16<OUT == CSA2_F32>(h, p.out, row * p.so + 16 * ch, p.wide);
     } else if (OUT == CSA2_FP4E2M1X2) {
       uint32_t e[3] = {0, 0, 0};
       if (has) {
@@ -342,21 +347,21 @@ __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
   }
 }
 
-// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row, kept in shared memory: channels are
-// read and written one by one, neighbouring threads neighbouring channels; the quantised forms
-// take 16-channel chunks from there (17 words apart, so that the lanes' banks differ).
-template <int OUT>
+// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row, N channels a thread, neighbouring threads
+// neighbouring channels, read and written one by one; the quantised forms pass the row through
+// shared memory to 16-channel chunks (17 words apart, so that the lanes' banks differ).
+//   4099 x 1001 from float32 to bf16 (24.6 MB, 3.6 us at the copy rate): 8.7 us; with the row in shared memory
+// and one warp adding the threads' sums it took 12.9 us, a thread reading 16 neighbours 28 us.
+template <int OUT, int N>
 __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ float buf[];
-  __shared__ float2 part[1024];
-  __shared__ float apart[32], rms;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5;
-  const int nchunk = (p.D + 15) / 16;
+  __shared__ float2 part[32];
+  __shared__ float apart[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5, nt = blockDim.x;
   if (OUT == CSA2_FP4E2M1X2 && blockIdx.x >= p.T) return zero_tail(p);
   const long long row = blockIdx.x;
-  const auto at = [&](int i) -> float& { return buf[(i >> 4) * 17 + (i & 15)]; };
   const auto get = [](const void* base, long long i, bool f32) {
     return f32 ? static_cast<const float*>(base)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[i]);
   };
@@ -366,58 +371,63 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
     else
       static_cast<uint16_t*>(base)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
   };
-#pragma unroll 4
-  for (int i = tid; i < p.D; i += blockDim.x) {
-    float h = get(p.x, row * p.sx + i, p.x32);
-    if (p.res) {
-      h += get(p.res, row * p.sr + i, p.r32);
-      if (!p.r32) h = __bfloat162float(__float2bfloat16_rn(h));
-      put(p.res_out, row * p.so_res + i, p.r32, h);
+  float h[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) h[k] = tid + k * nt < p.D ? get(p.x, row * p.sx + tid + k * nt, p.x32) : 0.f;
+  if (p.res) {
+    float r[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) r[k] = tid + k * nt < p.D ? get(p.res, row * p.sr + tid + k * nt, p.r32) : 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      h[k] += r[k];
+      if (!p.r32) h[k] = __bfloat162float(__float2bfloat16_rn(h[k]));
+      if (tid + k * nt < p.D) put(p.res_out, row * p.so_res + tid + k * nt, p.r32, h[k]);
     }
-    at(i) = h;
   }
   float r;
   for (bool scaled = false;; scaled = true) {             // again where squares leave float32's range
-    float hi = 0.f, lo = 0.f;
-    for (int i = tid; i < p.D; i += blockDim.x) {
-      const float v = scaled ? at(i) * 0x1p-64f : at(i), q = __fmul_rn(v, v);
-      sum2(hi, lo, q, __fmaf_rn(v, v, -q));
-    }
-    part[tid] = make_float2(hi, lo);
+    float hi, lo;
+    f32x2 v[N / 2];
+#pragma unroll
+    for (int k = 0; k < N / 2; ++k) v[k] = pk(h[2 * k], h[2 * k + 1]);
+    squares<N / 2>(v, scaled, hi, lo);
+    lanes_sum2(hi, lo, 32);
+    if (scaled) __syncthreads();                          // every warp has read the first sums
+    if (lane == 0) part[warp] = make_float2(hi, lo);
     __syncthreads();
-    if (warp == 0) {
-      hi = part[lane].x, lo = part[lane].y;
-      for (int i = lane + 32; i < blockDim.x; i += 32) sum2(hi, lo, part[i].x, part[i].y);
-      lanes_sum2(hi, lo, 32);
-      const float v = inverse_rms(hi, lo, p.D, p.eps, scaled);
-      if (lane == 0) rms = !scaled && !isfinite(hi) ? -1.f : v;
-    }
-    __syncthreads();
-    r = rms;
-    if (scaled || r != -1.f) break;
+    const float2 z = lane < nwarp ? part[lane] : make_float2(0.f, 0.f);
+    hi = z.x, lo = z.y;
+    lanes_sum2(hi, lo, 32);
+    r = inverse_rms(hi, lo, p.D, p.eps, scaled);
+    if (scaled || isfinite(hi)) break;
   }
   if (OUT == CSA2_FP8E4M3 || (OUT == CSA2_FP4E2M1X2 && !p.gscale)) r = -r;   // as in k_rms_norm
-  for (int i = tid; i < p.D; i += blockDim.x) {
-    float y = __fmul_rn(at(i), r);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = tid + k * nt;
+    if (i >= p.D) continue;
+    float y = __fmul_rn(h[k], r);
     if (p.w) y = __fmul_rn(y, get(p.w, i, p.w32));
     if (OUT == CSA2_BF16 || OUT == CSA2_F32)
       put(p.out, row * p.so + i, OUT == CSA2_F32, y);
     else
-      at(i) = y;
+      buf[(i >> 4) * 17 + (i & 15)] = y;
   }
   if (OUT == CSA2_BF16 || OUT == CSA2_F32) return;
-  for (int i = p.D + tid; i < 16 * nchunk; i += blockDim.x) at(i) = 0.f;
+  const int nchunk = (p.D + 15) / 16;
+  for (int i = p.D + tid; i < 16 * nchunk; i += nt) buf[(i >> 4) * 17 + (i & 15)] = 0.f;
   __syncthreads();
   const auto chunk = [&](f32x2* v, int ch) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ch < nchunk ? pk(buf[ch * 17 + 2 * i], buf[ch * 17 + 2 * i + 1]) : 0;
   };
-  const int rounds = (nchunk + blockDim.x - 1) / blockDim.x;
+  const int rounds = (nchunk + nt - 1) / nt;
   float rm = 0.f;
   if (OUT == CSA2_FP8E4M3 && p.group == 0) {
     for (int k = 0; k < rounds; ++k) {
       f32x2 v[8];
-      chunk(v, k * blockDim.x + tid);
+      chunk(v, k * nt + tid);
       rm = max3_abs(rm, amax16(v), 0.f);
     }
     rm = warp_max_abs(rm);
@@ -427,7 +437,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
     if (tid == 0) p.out_scale[row] = __fdiv_rn(rm, 448.0f);
   }
   for (int k = 0; k < rounds; ++k) {
-    const int ch = k * blockDim.x + tid;
+    const int ch = k * nt + tid;
     f32x2 v[8];
     chunk(v, ch);
     if (OUT == CSA2_FP4E2M1X2) {
@@ -455,8 +465,8 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
   }
   if (OUT == CSA2_FP8E4M3) {
     __syncthreads();
-    for (int i = tid; i < p.D; i += blockDim.x)
-      static_cast<uint8_t*>(p.out)[row * p.so + i] = (uint8_t)__float_as_uint(at(i));
+    for (int i = tid; i < p.D; i += nt)
+      static_cast<uint8_t*>(p.out)[row * p.so + i] = (uint8_t)__float_as_uint(buf[(i >> 4) * 17 + (i & 15)]);
   }
 }
 
@@ -489,6 +499,22 @@ cudaError_t launch_aligned(const NormParams& p, cudaStream_t st) {
   return launch_rows(k_rms_norm<OUT, X32, RES>, resident[threads / 32], p, 1, threads, tail, st);
 }
 
+template <int OUT, int N>
+cudaError_t launch_any(const NormParams& p, cudaStream_t st) {
+  const bool quantised = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2;
+  const int threads = ((p.D + N - 1) / N + 31) & ~31;
+  const size_t smem = quantised ? (size_t)((p.D + 15) / 16) * 17 * 4 : 0;
+  static bool attr_set = false;
+  if (quantised && !attr_set) {
+    cudaError_t e =
+        cudaFuncSetAttribute(k_rms_norm_any<OUT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
+    if (e != cudaSuccess) return e;
+    attr_set = true;
+  }
+  return launch_k(k_rms_norm_any<OUT, N>, (unsigned)p.T + (OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u), threads, smem, st,
+                  p);
+}
+
 template <int OUT>
 cudaError_t launch_form(const NormParams& p, bool aligned, cudaStream_t st) {
   if (aligned && p.D <= 8192) {
@@ -503,20 +529,11 @@ cudaError_t launch_form(const NormParams& p, bool aligned, cudaStream_t st) {
     CSA2_NORM(true, 2);
 #undef CSA2_NORM
   }
-  const int nchunk = (p.D + 15) / 16;
-  const int threads = p.D >= 4096 ? 1024 : (p.D / 4 + 31) & ~31 ? (p.D / 4 + 31) & ~31 : 32;
-  const size_t smem = (size_t)nchunk * 17 * 4;
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_rms_norm_any<OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
-  return launch_k(k_rms_norm_any<OUT>, (unsigned)p.T + (OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u), threads, smem, st, p);
+  return p.D <= 8192 ? launch_any<OUT, 8>(p, st) : p.D <= 16384 ? launch_any<OUT, 16>(p, st) : launch_any<OUT, 32>(p, st);
 }
 
-bool rows_aligned(const void* p, long long stride, int esize) {
-  return ((uintptr_t)p & 15) == 0 && (stride * esize) % 16 == 0;
+bool rows_aligned(const void* p, long long stride, int esize, int to = 16) {
+  return ((uintptr_t)p & (to - 1)) == 0 && (stride * esize) % to == 0;
 }
 
 }  // namespace
@@ -538,11 +555,15 @@ cudaError_t launch_rms_norm(const csa2_rms_norm_args& a, cudaStream_t st) {
   p.lanes = 1;
   while (p.lanes < 32 && p.lanes * 16 < a.D) p.lanes *= 2;
   const int rb = p.r32 ? 4 : 2;
-  const bool aligned =
-      a.D % 16 == 0 && rows_aligned(a.x, many ? a.x_stride : 0, p.x32 ? 4 : 2) &&
-      rows_aligned(a.residual, many ? a.residual_stride : 0, rb) &&
-      rows_aligned(a.residual_out, many ? a.residual_out_stride : 0, rb) && rows_aligned(a.weight, 0, 1) &&
-      (fp4 || rows_aligned(a.out, many ? a.out_stride : 0, a.out_form == CSA2_F32 ? 4 : a.out_form == CSA2_BF16 ? 2 : 1));
+  const int xb = p.x32 ? 4 : 2, ob = a.out_form == CSA2_F32 ? 4 : a.out_form == CSA2_BF16 ? 2 : 1;
+  const auto rows_to = [&](int to) {
+    return rows_aligned(a.x, many ? a.x_stride : 0, xb, to) && rows_aligned(a.residual, many ? a.residual_stride : 0, rb, to) &&
+           rows_aligned(a.residual_out, many ? a.residual_out_stride : 0, rb, to) &&
+           (a.out_form > CSA2_F32 || rows_aligned(a.out, many ? a.out_stride : 0, ob, to));
+  };
+  const bool aligned = a.D % 16 == 0 && rows_to(16) && rows_aligned(a.weight, 0, 1) &&
+                       (a.out_form != CSA2_FP8E4M3 || rows_aligned(a.out, many ? a.out_stride : 0, 1));
+  p.wide = aligned && rows_to(32);
   switch (a.out_form) {
     case CSA2_BF16: return launch_form<CSA2_BF16>(p, aligned, st);
     case CSA2_F32: return launch_form<CSA2_F32>(p, aligned, st);

@@ -83,23 +83,30 @@ __device__ __forceinline__ uint32_t add_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
-// 16 channels of a row as they lie in memory: 8 words of bf16 pairs or 16 of float32.
+// 16 channels of a row as they lie in memory: 8 words of bf16 pairs or 16 of float32.  wide: the
+// address is 32-byte aligned, not only 16; one access then takes the sectors that two half-sector
+// accesses each would touch.
 template <bool F32>
 struct Raw16 {
   uint4 q[F32 ? 4 : 2];
-  __device__ __forceinline__ void load(const void* base, long long off, bool again = false) {
+  __device__ __forceinline__ void load(const void* base, long long off, bool wide) {   // read once
     const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + off * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = again ? ld_v4(p + i) : ld_once_v4(p + i);
+    for (int i = 0; i < (F32 ? 4 : 2); i += 2) {
+      if (wide) {
+        asm volatile("ld.global.L1::no_allocate.L2::256B.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(q[i].x), "=r"(q[i].y), "=r"(q[i].z), "=r"(q[i].w), "=r"(q[i + 1].x), "=r"(q[i + 1].y),
+                       "=r"(q[i + 1].z), "=r"(q[i + 1].w) : "l"(p + i));
+      } else {
+        q[i] = ld_once_v4(p + i);
+        q[i + 1] = ld_once_v4(p + i + 1);
+      }
+    }
   }
-  __device__ __forceinline__ void store(void* base, long long off) const {
-    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+  __device__ __forceinline__ void load_again(const void* base, long long off) {        // what others read too
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const char*>(base) + off * (F32 ? 4 : 2));
 #pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) p[i] = q[i];
-  }
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = ld_v4(p + i);
   }
   __device__ __forceinline__ void negate() {
     const uint32_t m = F32 ? 0x80000000u : 0x80008000u;
@@ -113,6 +120,24 @@ struct Raw16 {
     }
     const uint4& v = q[i / 4];
     return bf16_pair(i % 4 == 0 ? v.x : i % 4 == 1 ? v.y : i % 4 == 2 ? v.z : v.w);
+  }
+  __device__ __forceinline__ void store(void* base, long long off, bool wide) const {
+    uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); i += 2) {
+      if (wide) {
+        asm volatile("st.global.v8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};"
+                     :: "r"(q[i].x), "r"(q[i].y), "r"(q[i].z), "r"(q[i].w), "r"(q[i + 1].x), "r"(q[i + 1].y),
+                        "r"(q[i + 1].z), "r"(q[i + 1].w), "l"(p + i) : "memory");
+      } else {
+        p[i] = q[i];
+        p[i + 1] = q[i + 1];
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (F32 ? 4 : 2); ++i) q[i] = make_uint4(0, 0, 0, 0);
   }
 };
 
@@ -141,19 +166,18 @@ __device__ __forceinline__ void store16_any(const f32x2* v, void* base, long lon
 }
 
 template <bool F32>
-__device__ __forceinline__ void store16(const f32x2* v, void* base, long long off) {
-  uint4* p = reinterpret_cast<uint4*>(static_cast<char*>(base) + off * (F32 ? 4 : 2));
-  if (F32) {
+__device__ __forceinline__ void store16(const f32x2* v, void* base, long long off, bool wide) {
+  Raw16<F32> r;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) {
+    if (F32) {
       const float2 a = unpk(v[2 * i]), b = unpk(v[2 * i + 1]);
-      p[i] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+      r.q[i] = make_uint4(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
+    } else {
+      r.q[i] = make_uint4(pack_bf16(v[4 * i]), pack_bf16(v[4 * i + 1]), pack_bf16(v[4 * i + 2]), pack_bf16(v[4 * i + 3]));
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      p[i] = make_uint4(pack_bf16(v[4 * i]), pack_bf16(v[4 * i + 1]), pack_bf16(v[4 * i + 2]), pack_bf16(v[4 * i + 3]));
   }
+  r.store(base, off, wide);
 }
 
 // max(|a|, |b|, |c|), NaN if one is.
@@ -162,15 +186,17 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float amax16(const f32x2* v) {
+template <int NP>
+__device__ __forceinline__ float amax_pairs(const f32x2* v) {
   float m = 0.f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < NP; ++i) {
     const float2 f = unpk(v[i]);
     m = max3_abs(f.x, f.y, m);
   }
   return m;
 }
+__device__ __forceinline__ float amax16(const f32x2* v) { return amax_pairs<8>(v); }
 
 // The same over a warp's lanes.
 __device__ __forceinline__ float warp_max_abs(float v) {
