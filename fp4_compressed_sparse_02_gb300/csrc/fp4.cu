@@ -147,6 +147,11 @@ __host__ __device__ constexpr uint32_t idesc(int M, int N) {
 constexpr uint32_t kOperandHi = (1024 >> 4) | (1u << 14) | (2u << 29);   // SBO 1024, version, 128-byte swizzle
 constexpr uint32_t kScaleHi = (128 >> 4) | (1u << 14);                   // SBO 128, version, no swizzle
 
+// The tensor map (a kernel parameter) into the cache its copies read it from.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" :: "l"(map) : "memory");
+}
+
 // One lane of the converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -217,8 +222,6 @@ __global__ void __launch_bounds__(lin::THREADS)
     k_fp4_linear(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, lin::Params p) {
   using namespace lin;
   using C = Cfg<BN>;
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * C::STAGE);
@@ -235,6 +238,8 @@ __global__ void __launch_bounds__(lin::THREADS)
   const bool aligned = (smem_u32(smem) & 1023) == 0;
   if (warp == 5) tc::tmem_alloc(tslot, p.tmem_cols);
   if (tid == 0) {
+    prefetch_map(&mw);
+    prefetch_map(&mx);
     for (int s = 0; s < C::STAGES; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -249,6 +254,8 @@ __global__ void __launch_bounds__(lin::THREADS)
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
+  pdl_wait();                                             // all of the above runs beside the previous kernel's end
+  pdl_trigger();
   const uint32_t tb = *tslot;
   int issued = kb0;                                       // loads of [kb0, issued) are on their way
   if (warp == 4) {
@@ -503,8 +510,6 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
                       const __grid_constant__ CUtensorMap msx, const __grid_constant__ CUtensorMap msw,
                       const __grid_constant__ CUtensorMap mo, pairs::Params p) {
   using namespace pairs;
-  pdl_wait();
-  pdl_trigger();
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + BARS);   // the leader's are used
@@ -520,6 +525,10 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
   const bool aligned = (smem_u32(smem) & 1023) == 0;      // the same in every CTA
   if (warp == EPI + 1) tmem_alloc2(tslot, 512);
   if (tid == 0) {
+    lin::prefetch_map(&mw);
+    lin::prefetch_map(&mx);
+    lin::prefetch_map(&msw);
+    lin::prefetch_map(&msx);
     for (int s = 0; s < STAGES; ++s) {
       tc::mbar_init(&full[s], 1);
       tc::mbar_init(&empty[s], 1);
@@ -533,6 +542,8 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
   __syncthreads();
   tc::cluster_sync();                                     // barriers and TMEM of both CTAs are there
   tc::fence_after_sync();
+  pdl_wait();                                             // all of the above runs beside the previous kernel's end
+  pdl_trigger();
   const uint32_t tb = *tslot;
   const int npair = gridDim.x / (2 * S), pr = blockIdx.x / (2 * S);
   const int ntile = p.nft * p.ntt, nkb = (p.nkt + 3) / 4;
