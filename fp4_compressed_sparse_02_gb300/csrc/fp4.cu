@@ -211,10 +211,11 @@ __device__ __forceinline__ void put4(const P& p, long long at, int n, float a, f
 // out^T = w x^T, so that few tokens fill the N side of the product and the weights stream through
 // the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32 partial in shared
 // memory and the CTAs add them in rank order.
-//   Occupancy: at 1 x 5120 -> 32768 (256 tiles) one CTA an SM with nine stages takes 21.0 us, two
-// with four stages 17.2 us (its loads alone: 17.2 us; the floor of 94 MB is 13.9 us): a second
-// CTA's loads run during the first's start and end.
-//   Split, 1 x 32768 -> 5120 (40 tiles), two CTAs an SM: S = 1 51 us, 3 21.1 us, 6 17.8 us, 7 26.3 us
+//   Occupancy: at 1 x 5120 -> 32768 (256 tiles) one CTA an SM with nine stages takes 20.4 us, two
+// with four stages 16.5 us (its loads alone take as long; the floor of 94 MB is 13.9 us): a second
+// CTA's loads run during the first's start and end.  Prefetching further tiles into L2 made it 18 to
+// 20 us.
+//   Split, 1 x 32768 -> 5120 (40 tiles), two CTAs an SM: S = 1 51 us, 3 21 us, 4 17.7 us, 6 16.8 us, 7 26 us
 // (clusters of seven pack badly: some wait for a second round), so S is the largest whose
 // clusters all run at once.
 template <int BN>
@@ -766,13 +767,6 @@ bool groups_of_four(const csa2_fp4_linear_args& a) {
   return a.w.rows % 4 == 0 && ((uintptr_t)a.out & (a.out_dtype == CSA2_F32 ? 15 : 7)) == 0;
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // How many clusters of `cta` CTAs of a kernel the GPU holds at once.
 template <typename K>
 int resident_clusters(K* kernel, int cta, int threads, size_t smem) {
@@ -895,21 +889,21 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64, p.out32 = a.out_dtype == CSA2_F32;
   p.vec4 = groups_of_four(a);
   const int ft = (p.N + lin::BM - 1) / lin::BM, nkb = (p.nkt + 3) / 4;
-  // two CTAs to an SM where both fit, or one with all stages
-  static int two[9] = {0}, one = 0;                       // clusters of s CTAs, and SMs, of the GPU
+  static int one[9] = {0};   // clusters of s CTAs that the GPU holds at once with one CTA an SM, which is what the query counts
   const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
-  if (!one) {
+  if (!one[1]) {
     cudaError_t e = cudaFuncSetAttribute(k_fp4_linear<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess) return e;
-    for (int s = 1; s <= 8; ++s) two[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
-    if (!two[1]) return cudaErrorInvalidConfiguration;
-    one = sm_count();
+    for (int s = 8; s >= 1; --s) one[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
+    if (!one[1]) return cudaErrorInvalidConfiguration;
   }
-  // few tiles: split the sum as far as every cluster still runs at once, two stages a CTA or more
+  // Few tiles (under three quarters of the SMs): split the sum as far as every cluster still runs at
+  // once with two CTAs an SM, two stages a CTA or more.  More tiles than SMs: two CTAs an SM.
   int S = 1;
-  for (int s = 2; s <= 8; ++s)
-    if (ft <= two[s] && 2 * s <= nkb) S = s;
-  p.stages = S == 1 && ft <= one ? C::STAGES : C::STAGES2;
+  if (4 * ft <= 3 * one[1])
+    for (int s = 2; s <= 8; ++s)
+      if (ft <= 2 * one[s] && 2 * s <= nkb) S = s;
+  p.stages = S == 1 && ft <= one[1] ? C::STAGES : C::STAGES2;
   p.tmem_cols = 128;
   while (p.tmem_cols < C::DCOLS + p.stages * C::SFCOLS) p.tmem_cols *= 2;
   cudaLaunchAttribute attr[2];

@@ -483,7 +483,7 @@ cudaError_t launch_rows(K* kernel, int& resident, const NormParams& p, int rows,
     if (e != cudaSuccess) return e;
     resident = sms * (per > 0 ? per : 1);
   }
-  const int blocks = (p.T + rows - 1) / rows;
+  const long long blocks = ((long long)p.T + rows - 1) / rows;
   return launch_k(kernel, (unsigned)(blocks < resident ? blocks : resident) + (tail ? 1u : 0u), threads, 0, st, p);
 }
 

@@ -144,7 +144,7 @@ cudaError_t launch_rope_v(const csa2_rope_args& a, RopeParams p, cudaStream_t st
   const int tx = p.units < kThreads ? p.units : kThreads;
   const int ty = kThreads / tx < a.H ? kThreads / tx : a.H;
   const int per = (a.H + ty - 1) / ty;                    // CTAs that give each thread one head
-  long long gy = (r + a.T - 1) / a.T;                     // fill the GPU, then several heads a thread
+  long long gy = (r + a.T - 1LL) / a.T;                     // fill the GPU, then several heads a thread
   if (gy > per) gy = per;
   const long long gx = a.T < r / gy ? a.T : r / gy;
   const dim3 grid((unsigned)(gx > 0 ? gx : 1), (unsigned)gy), block((unsigned)tx, (unsigned)ty);

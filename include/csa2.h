@@ -448,6 +448,7 @@ typedef struct csa2_fp4_rows {
  *                          divisions), s == 0 -> zero bytes: the rows csa2_swa_quant writes
  *   CSA2_FP4E2M1X2         out4, as csa2_fp4_quant writes y
  * The codes are decided on values that do not depend on how a row is split over threads.
+ * A sum of squares beyond float32's range is taken scaled, so a finite mean stays finite.
  * NaN and infinities follow the formulas; a NaN in a group gives it a NaN scale and zero codes.
  * Strides are in elements between rows (the last dimension is contiguous); any alignment of
  * the element type is accepted, 16-byte aligned rows are faster.  residual_out may be
@@ -529,7 +530,7 @@ csa2_status csa2_rope(const csa2_rope_args* args, void* stream);
  *                     take f_i / factor, a linear ramp over i joins the two ("YaRN", Peng
  *                     et al. 2023, equations 17-23, with the ramp over the channel index)
  * The angle is held as a 64-bit fraction of a turn, so that a far position loses nothing:
- * |error| <= 2^-24 (1 + 1/2) * magnitude.
+ * |error| <= 2.5 * 2^-24 * magnitude.
  * Supported: even d_rope in 2..256, positions <= 2^24, theta > 1, factor >= 1,
  * 0 < beta_slow < beta_fast.  Needs no workspace.
  * -------------------------------------------------------------------------- */
