@@ -45,6 +45,29 @@ def test_fp4_linear(T, N, K, out):
     assert csa2.device_error() == 0
 
 
+@pytest.mark.parametrize("T,N,K", [
+    (130, 77 * 256, 12288),        # 77 tiles of pairs: a last round of one tile, split and launched apart
+    (700, 40 * 256 + 3, 160),      # several rounds, rows that TMA cannot address
+    (520, 19000, 8192)])
+def test_fp4_linear_many_tiles(T, N, K):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(T)
+    r8 = lambda *s: torch.randint(0, 256, s, generator=g, device=DEV, dtype=torch.uint8)
+    sc = lambda R: torch.randint(0x28, 0x48, ((R + 127) // 128, (K + 63) // 64, 512), generator=g, device=DEV,
+                                 dtype=torch.uint8)
+    x, w = csa2.Fp4Rows(r8(T, K // 2), sc(T)), csa2.Fp4Rows(r8(N, K // 2), sc(N))
+    if K % 64:                     # scales past the last column are zero
+        for m in (x, w):
+            m.scales[:, -1].view(-1, 128, 4)[:, :, 2:] = 0
+    y = csa2.fp4_linear(x, w)
+    assert csa2.device_error() == 0
+    assert torch.equal(y, csa2.fp4_linear(x, w))
+    cols = np.unique(np.concatenate([np.arange(40), np.arange(N - 300, N), np.linspace(0, N - 1, 100).astype(int)]))
+    c = lambda t: t.cpu().numpy()
+    at = torch.from_numpy(cols).to(DEV)
+    check(y[:, at], c(x.codes), c(x.row_scales()), c(w.codes[at]), c(w.row_scales()[at]))
+
+
 def test_fp4_linear_exact_sums():
     """Powers of two whose sums are exact in float32: every step of K counts once, in its place."""
     T, N, K = 40, 200, 1120
