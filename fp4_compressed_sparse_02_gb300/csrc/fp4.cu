@@ -207,9 +207,9 @@ __device__ __forceinline__ void put4(const P& p, long long at, int n, float a, f
 
 }  // namespace lin
 
-// Up to 128 tokens: what bounds it is reading the weights once.  Tile = 128 features x BN tokens of
-// out^T = w x^T, so that few tokens fill the N side of the product and the weights stream through
-// the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32 partial in shared
+// Up to 128 tokens (and more where the tiles are few, see launch_fp4_linear): what bounds it is reading
+// the weights once.  Tile = 128 features x BN tokens of out^T = w x^T, so that few tokens fill the N
+// side of the product and the weights stream through the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32 partial in shared
 // memory and the CTAs add them in rank order.
 //   Occupancy: at 1 x 5120 -> 32768 (256 tiles) one CTA an SM with nine stages takes 20.4 us, two
 // with four stages 16.5 us (its loads alone take as long; the floor of 94 MB is 13.9 us): a second
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(lin::THREADS)
   volatile int* failed = reinterpret_cast<volatile int*>(accf + 2);
   const int S = (int)gridDim.x / ((p.N + BM - 1) / BM);   // CTAs of a cluster
   const int rank = blockIdx.x % S;
-  const int f0 = (blockIdx.x / S) * BM;
+  const int f0 = (blockIdx.x / S) * BM, t0 = blockIdx.y * BN, nt = min(BN, p.T - t0);   // more than one token tile: BN = 128
   const int nkb = (p.nkt + 3) / 4;
   const int kb0 = (int)((long long)nkb * rank / S), kb1 = (int)((long long)nkb * (rank + 1) / S);
   // the same in every CTA; the barriers of a cluster are reached either way
@@ -269,13 +269,13 @@ __global__ void __launch_bounds__(lin::THREADS)
           break;
         }
         uint8_t* st = smem + s * C::STAGE;
-        const int nt = min(4, p.nkt - 4 * kb);            // 64-column steps of this stage
-        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(C::A + C::B + nt * 1024));
+        const int steps = min(4, p.nkt - 4 * kb);         // 64-column steps of this stage
+        tc::mbar_arrive_expect_tx(&full[s], (uint32_t)(C::A + C::B + steps * 1024));
         tc::tma_load_2d(st, &mw, kb * BKB, f0, &full[s]);
-        tc::tma_load_2d(st + C::A, &mx, kb * BKB, 0, &full[s]);
+        tc::tma_load_2d(st + C::A, &mx, kb * BKB, t0, &full[s]);
         uint8_t* sf = st + C::A + C::B;
-        tc::bulk_load(sf, p.wt + ((long long)(f0 >> 7) * p.nkt + 4 * kb) * 512, nt * 512, &full[s]);
-        tc::bulk_load(sf + C::SF, p.xt + (long long)4 * kb * 512, nt * 512, &full[s]);
+        tc::bulk_load(sf, p.wt + ((long long)(f0 >> 7) * p.nkt + 4 * kb) * 512, steps * 512, &full[s]);
+        tc::bulk_load(sf + C::SF, p.xt + ((long long)(t0 >> 7) * p.nkt + 4 * kb) * 512, steps * 512, &full[s]);
         issued = kb + 1;
       }
     }
@@ -295,17 +295,17 @@ __global__ void __launch_bounds__(lin::THREADS)
         }
         tc::fence_after_sync();
         const uint32_t a = base + (uint32_t)s * (C::STAGE >> 4), sft = sf0 + (uint32_t)s * C::SFCOLS;
-        const int nt = min(4, p.nkt - 4 * kb);
+        const int steps = min(4, p.nkt - 4 * kb);
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (k < nt) {
+            if (k < steps) {
               sf_copy(sft + 4 * k, a + ((C::A + C::B + 512 * k) >> 4));
               sf_copy(sft + 16 + 4 * k, a + ((C::A + C::B + C::SF + 512 * k) >> 4));
             }
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (k < nt)
+            if (k < steps)
               mma_fp4(tb, a + 2 * k, a + ((C::A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 4 * k, kb > kb0 || k > 0);
           tc::mma_commit(&empty[s]);
         }
@@ -331,47 +331,52 @@ __global__ void __launch_bounds__(lin::THREADS)
       tc::mbar_wait(&full[(kb - kb0) % p.stages], (uint32_t)(((kb - kb0) / p.stages) & 1), MAX_POLL);
   }
   const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
+  // the tile through shared memory, token by token, so that neighbouring lanes store neighbouring features
   if (warp < 4 && !bad) {
     const uint32_t tq = tb + ((uint32_t)(32 * warp) << 16);
-    const int f = 32 * warp + lane;
-    float* part = reinterpret_cast<float*>(smem);
+    float* part = reinterpret_cast<float*>(smem) + 32 * warp + lane;
 #pragma unroll 1
-    for (int c = 0; c < p.T; c += 32) {
+    for (int c = 0; c < nt; c += 32) {
       uint32_t v[32];
       tc::tmem_ld32(tq + (uint32_t)c, v);
       tc::tmem_ld_wait();
-      if (S > 1) {
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < p.T) part[(c + i) * BM + f] = __uint_as_float(v[i]);
-      } else if (f0 + f < p.N) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < p.T) put(p, (long long)(c + i) * p.N + f0 + f, __uint_as_float(v[i]) * alpha);
-      }
+      for (int i = 0; i < 32; ++i)
+        if (c + i < nt) part[(c + i) * BM] = __uint_as_float(v[i]);
     }
   }
   __syncwarp();
-  if (S > 1) {
+  if (S > 1)
     tc::cluster_sync();
-    if (warp < 4 && !bad) {
-      const uint32_t mine = smem_u32(smem);
-      for (int u = rank * 128 + tid; u < p.T * (BM / 4); u += S * 128) {
+  else
+    __syncthreads();
+  if (!bad && f0 + 4 * lane < p.N) {                      // a warp a token: four features a lane
+    const int f = f0 + 4 * lane;
+    constexpr int WARPS = THREADS / 32;
+    if (S == 1) {
+#pragma unroll 4
+      for (int t = warp; t < nt; t += WARPS) {
+        const float4 s = reinterpret_cast<const float4*>(smem)[t * (BM / 4) + lane];
+        put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+      }
+    } else {
+#pragma unroll 2
+      for (int t = rank * WARPS + warp; t < nt; t += S * WARPS) {
+        const uint32_t at = smem_u32(smem) + (t * BM + 4 * lane) * 4;
         float4 v[8];                                      // every peer's piece, on its way at once
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-          if (q < S) v[q] = ld_dsmem_f4(tc::mapa(mine, q) + 16 * u);
+          if (q < S) v[q] = ld_dsmem_f4(tc::mapa(at, q));
         float4 s = v[0];
 #pragma unroll
         for (int q = 1; q < 8; ++q)
           if (q < S) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
-        const int t = u / (BM / 4), f = f0 + 4 * (u % (BM / 4));
-        if (f < p.N) put4(p, (long long)t * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+        put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
       }
     }
-    __syncwarp();
-    tc::cluster_sync();                                   // peers have read this CTA's partial
   }
+  __syncwarp();
+  if (S > 1) tc::cluster_sync();                          // peers have read this CTA's partial
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 5) tc::tmem_dealloc(tb, p.tmem_cols);
@@ -769,6 +774,16 @@ bool groups_of_four(const csa2_fp4_linear_args& a) {
   return a.w.rows % 4 == 0 && ((uintptr_t)a.out & (a.out_dtype == CSA2_F32 ? 15 : 7)) == 0;
 }
 
+int sm_count() {
+  static int sms = 0;
+  if (!sms) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  }
+  return sms;
+}
+
 // How many clusters of `cta` CTAs of a kernel the GPU holds at once.
 template <typename K>
 int resident_clusters(K* kernel, int cta, int threads, size_t smem) {
@@ -906,7 +921,8 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.wt = a.w.scales, p.xt = a.x.scales, p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out;
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64, p.out32 = a.out_dtype == CSA2_F32;
   p.vec4 = groups_of_four(a);
-  const int ft = (p.N + lin::BM - 1) / lin::BM, nkb = (p.nkt + 3) / 4;
+  const int ft = (p.N + lin::BM - 1) / lin::BM, tt = (p.T + BN - 1) / BN, nkb = (p.nkt + 3) / 4;
+  const long long tiles = (long long)ft * tt;
   static int one[9] = {0};   // clusters of s CTAs that the GPU holds at once with one CTA an SM, which is what the query counts
   const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
   if (!one[1]) {
@@ -916,12 +932,14 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
     if (!one[1]) return cudaErrorInvalidConfiguration;
   }
   // Few tiles (under three quarters of the SMs): split the sum as far as every cluster still runs at
-  // once with two CTAs an SM, two stages a CTA or more.  More tiles than SMs: two CTAs an SM.
+  // once with two CTAs an SM, where the stages saved are worth adding the parts (1 x 1024 -> 512, four
+  // stages: 3.2 us whole, 3.4 us split; 128 x 1024 -> 512: 4.1 and 6.7 us; 1 x 2048 -> 512: 3.9 and 3.4 us).
+  // More tiles than SMs: two CTAs an SM.
   int S = 1;
-  if (4 * ft <= 3 * one[1])
+  if (4 * tiles <= 3 * one[1])
     for (int s = 2; s <= 8; ++s)
-      if (ft <= 2 * one[s] && 2 * s <= nkb) S = s;
-  p.stages = S == 1 && ft <= one[1] ? C::STAGES : C::STAGES2;
+      if (tiles <= 2 * one[s] && 2 * s <= nkb && nkb - nkb / s >= 4 + BN / 16) S = s;
+  p.stages = S == 1 && tiles <= one[1] ? C::STAGES : C::STAGES2;
   p.tmem_cols = 128;
   while (p.tmem_cols < C::DCOLS + p.stages * C::SFCOLS) p.tmem_cols *= 2;
   cudaLaunchAttribute attr[2];
@@ -931,7 +949,7 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = (unsigned)(ft * S);
+  cfg.gridDim = dim3((unsigned)(ft * S), (unsigned)tt);
   cfg.blockDim = lin::THREADS;
   cfg.dynamicSmemBytes = (size_t)p.stages * C::STAGE + 256;
   cfg.stream = st;
@@ -948,7 +966,15 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (T <= 16) return launch_linear<16>(a, st);
   if (T <= 32) return launch_linear<32>(a, st);
   if (T <= 64) return launch_linear<64>(a, st);
-  if (T <= 128) return launch_linear<128>(a, st);
+  // Single CTAs while their 128 x 128 tiles run at once, two on an SM, and a CTA's share of the sum is
+  // short: they start and end in 3 us, pairs in 5 to 6 us (and 3 us more where they split the sum), but
+  // a pair does 256 x 256 in little more time than a CTA its 128 x 128.  us, single against pairs:
+  //   384 x 1024 -> 5120 (120 tiles, 4 stages)   4.4  6.5      384 x 8192 -> 5120 (32 stages)  15.3  15.7
+  //   384 x 16384 -> 5120 (64 stages)            27.3 25.6     768 x 4096 -> 5120 (240, 16)    10.6  11.0
+  //   192 x 16384 -> 5120 (80, 64)               17.7 17.7     192 x 32768 -> 5120 (80, 128)   28.3  26.1
+  const long long tiles = (long long)((T + 127) / 128) * ((a.w.rows + 127) / 128);
+  const int sms = sm_count(), nkb = (a.x.cols + 255) / 256;
+  if (T <= 128 || (tiles <= 2 * sms && tiles * nkb <= 32LL * sms)) return launch_linear<128>(a, st);
   const bool tma = ((uintptr_t)a.out & 15) == 0 && (long long)a.w.rows * (a.out_dtype == CSA2_F32 ? 4 : 2) % 16 == 0;
   return tma ? launch_linear_pair<true>(a, st) : launch_linear_pair<false>(a, st);
 }

@@ -45,11 +45,18 @@ def test_fp4_linear(T, N, K, out):
     assert csa2.device_error() == 0
 
 
-@pytest.mark.parametrize("T,N,K", [
-    (130, 77 * 256, 12288),        # 77 tiles of pairs: a last round of one tile, split and launched apart
-    (700, 40 * 256 + 3, 160),      # several rounds, rows that TMA cannot address
-    (520, 19000, 8192)])
-def test_fp4_linear_many_tiles(T, N, K):
+@pytest.mark.parametrize("T,N,K,out", [
+    (130, 77 * 256, 12288, torch.bfloat16),        # 77 tiles of pairs: a last round of one tile, split and launched apart
+    (700, 40 * 256 + 3, 160, torch.bfloat16),      # several rounds, rows that TMA cannot address
+    (700, 40 * 256 + 3, 160, torch.float32),
+    (640, 40 * 256, 288, torch.float32),
+    (520, 19000, 8192, torch.bfloat16),
+    (192, 5120, 20480, torch.bfloat16),            # 20 tiles of pairs, the sum split in a cluster
+    (161, 5119, 20480, torch.float32),
+    (129, 5117, 20512, torch.bfloat16),
+    (500, 1000, 16384, torch.bfloat16),            # 32 tiles of single CTAs, split
+    (1000, 4999, 96, torch.float32)])              # 320 tiles of single CTAs' size
+def test_fp4_linear_many_tiles(T, N, K, out):
     g = torch.Generator(device=DEV)
     g.manual_seed(T)
     r8 = lambda *s: torch.randint(0, 256, s, generator=g, device=DEV, dtype=torch.uint8)
@@ -59,9 +66,9 @@ def test_fp4_linear_many_tiles(T, N, K):
     if K % 64:                     # scales past the last column are zero
         for m in (x, w):
             m.scales[:, -1].view(-1, 128, 4)[:, :, 2:] = 0
-    y = csa2.fp4_linear(x, w)
+    y = csa2.fp4_linear(x, w, out_dtype=out)
     assert csa2.device_error() == 0
-    assert torch.equal(y, csa2.fp4_linear(x, w))
+    assert torch.equal(y, csa2.fp4_linear(x, w, out_dtype=out))
     cols = np.unique(np.concatenate([np.arange(40), np.arange(N - 300, N), np.linspace(0, N - 1, 100).astype(int)]))
     c = lambda t: t.cpu().numpy()
     at = torch.from_numpy(cols).to(DEV)
