@@ -347,43 +347,76 @@ __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
   }
 }
 
-// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row, N channels a thread, neighbouring threads
-// neighbouring channels, read and written one by one; the quantised forms pass the row through
-// shared memory to 16-channel chunks (17 words apart, so that the lanes' banks differ).
-//   4099 x 1001 from float32 to bf16 (24.6 MB, 3.6 us at the copy rate): 8.7 us; with the row in shared memory
-// and one warp adding the threads' sums it took 12.9 us, a thread reading 16 neighbours 28 us.
-template <int OUT, int N>
-__global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
+// Any row: odd widths, unaligned rows, D up to 32768.  A CTA a row, or up to 512 channels a warp a row and
+// kAnyRows rows a CTA (THREADS = 32 * kAnyRows).  N channels a thread: a warp takes 32 N neighbouring
+// channels and reads and writes them 32 at a time, so that every offset is a constant and a row costs few
+// instructions beside its bytes; the quantised forms pass the row through shared memory to 16-channel chunks
+// (17 words apart, so that the lanes' banks differ).
+//   4099 x 1001 from float32 to bf16 (24.6 MB, 3.6 us at the copy rate): 5.2 us with N = 16, 6.4 with 8, 9.7 with 4
+// (every warp adds the whole row's sums); 8.5 us with channels a CTA's width apart, whose addresses are computed
+// one by one; 10.8 us with that form's next row loaded ahead (more registers, fewer rows at a time).
+//   20000 x 333 (40 MB, 5.9 us): 9.7 us, against 20.6 us with a CTA of one warp a row.  Up to 1024 channels a warp (N = 32)
+// gains as little as it loses: 4099 x 1001 5.1 us, with a residual 8.6 against 7.9 us.
+constexpr int kAnyRows = 4;
+
+template <int OUT, int N, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_rms_norm_any(NormParams p) {
   pdl_wait();
   pdl_trigger();
-  extern __shared__ float buf[];
+  extern __shared__ float rows[];
   __shared__ float2 part[32];
   __shared__ float apart[32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nwarp = blockDim.x >> 5, nt = blockDim.x;
-  if (OUT == CSA2_FP4E2M1X2 && blockIdx.x >= p.T) return zero_tail(p);
-  const long long row = blockIdx.x;
-  const auto get = [](const void* base, long long i, bool f32) {
-    return f32 ? static_cast<const float*>(base)[i] : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[i]);
-  };
-  const auto put = [](void* base, long long i, bool f32, float v) {
-    if (f32)
-      static_cast<float*>(base)[i] = v;
+  constexpr bool WARP = THREADS == 32 * kAnyRows;
+  constexpr int ROWS = WARP ? kAnyRows : 1;
+  const int lane = threadIdx.x & 31, warp = WARP ? 0 : threadIdx.x >> 5, tid = 32 * warp + lane;
+  const int nwarp = WARP ? 1 : blockDim.x >> 5, nt = 32 * nwarp;
+  if (OUT == CSA2_FP4E2M1X2 && (long long)blockIdx.x * ROWS >= p.T) return zero_tail(p);
+  const long long row = WARP ? (long long)blockIdx.x * ROWS + threadIdx.x / 32 : blockIdx.x;
+  if (WARP && row >= p.T) return;
+  float* buf = rows + (WARP ? threadIdx.x / 32 * ((p.D + 15) / 16 * 17) : 0);
+  const auto sync = [] {
+    if (WARP)
+      __syncwarp();
     else
-      static_cast<uint16_t*>(base)[i] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+      __syncthreads();
+  };
+  // a warp's 32 N channels are neighbours, so that every offset below is a constant
+  const int first = warp * 32 * N + lane, left = p.D - first;
+  const auto load = [&](float (&v)[N], const void* base, long long at, bool f32) {
+    if (f32) {
+      const float* b = static_cast<const float*>(base) + at + first;
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = 32 * k < left ? b[32 * k] : 0.f;
+    } else {
+      const uint16_t* b = static_cast<const uint16_t*>(base) + at + first;
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] = bf16_bits_to_f32(32 * k < left ? b[32 * k] : (uint16_t)0);
+    }
+  };
+  const auto store = [&](const float (&v)[N], void* base, long long at, bool f32) {
+    if (f32) {
+      float* b = static_cast<float*>(base) + at + first;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (32 * k < left) b[32 * k] = v[k];
+    } else {
+      uint16_t* b = static_cast<uint16_t*>(base) + at + first;
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (32 * k < left) b[32 * k] = __bfloat16_as_ushort(__float2bfloat16_rn(v[k]));
+    }
   };
   float h[N];
-#pragma unroll
-  for (int k = 0; k < N; ++k) h[k] = tid + k * nt < p.D ? get(p.x, row * p.sx + tid + k * nt, p.x32) : 0.f;
+  load(h, p.x, row * p.sx, p.x32);
   if (p.res) {
-    float r[N];
-#pragma unroll
-    for (int k = 0; k < N; ++k) r[k] = tid + k * nt < p.D ? get(p.res, row * p.sr + tid + k * nt, p.r32) : 0.f;
+    float q[N];
+    load(q, p.res, row * p.sr, p.r32);
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      h[k] += r[k];
+      h[k] += q[k];
       if (!p.r32) h[k] = __bfloat162float(__float2bfloat16_rn(h[k]));
-      if (tid + k * nt < p.D) put(p.res_out, row * p.so_res + tid + k * nt, p.r32, h[k]);
     }
+    store(h, p.res_out, row * p.so_res, p.r32);
   }
   float r;
   for (bool scaled = false;; scaled = true) {             // again where squares leave float32's range
@@ -393,31 +426,33 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
     for (int k = 0; k < N / 2; ++k) v[k] = pk(h[2 * k], h[2 * k + 1]);
     squares<N / 2>(v, scaled, hi, lo);
     lanes_sum2(hi, lo, 32);
-    if (scaled) __syncthreads();                          // every warp has read the first sums
-    if (lane == 0) part[warp] = make_float2(hi, lo);
-    __syncthreads();
-    const float2 z = lane < nwarp ? part[lane] : make_float2(0.f, 0.f);
-    hi = z.x, lo = z.y;
-    lanes_sum2(hi, lo, 32);
+    if (!WARP) {
+      if (scaled) __syncthreads();                        // every warp has read the first sums
+      if (lane == 0) part[warp] = make_float2(hi, lo);
+      __syncthreads();
+      const float2 z = lane < nwarp ? part[lane] : make_float2(0.f, 0.f);
+      hi = z.x, lo = z.y;
+      lanes_sum2(hi, lo, 32);
+    }
     r = inverse_rms(hi, lo, p.D, p.eps, scaled);
     if (scaled || isfinite(hi)) break;
   }
   if (OUT == CSA2_FP8E4M3 || (OUT == CSA2_FP4E2M1X2 && !p.gscale)) r = -r;   // as in k_rms_norm
+  float w[N];
+  if (p.w) load(w, p.w, 0, p.w32);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const int i = tid + k * nt;
-    if (i >= p.D) continue;
-    float y = __fmul_rn(h[k], r);
-    if (p.w) y = __fmul_rn(y, get(p.w, i, p.w32));
-    if (OUT == CSA2_BF16 || OUT == CSA2_F32)
-      put(p.out, row * p.so + i, OUT == CSA2_F32, y);
-    else
-      buf[(i >> 4) * 17 + (i & 15)] = y;
+    h[k] = __fmul_rn(h[k], r);
+    if (p.w) h[k] = __fmul_rn(h[k], w[k]);
   }
-  if (OUT == CSA2_BF16 || OUT == CSA2_F32) return;
+  if (OUT == CSA2_BF16 || OUT == CSA2_F32) return store(h, p.out, row * p.so, OUT == CSA2_F32);
+  float* at = buf + (first >> 4) * 17 + (lane & 15);
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if (32 * k < left) at[34 * k] = h[k];
   const int nchunk = (p.D + 15) / 16;
   for (int i = p.D + tid; i < 16 * nchunk; i += nt) buf[(i >> 4) * 17 + (i & 15)] = 0.f;
-  __syncthreads();
+  sync();
   const auto chunk = [&](f32x2* v, int ch) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = ch < nchunk ? pk(buf[ch * 17 + 2 * i], buf[ch * 17 + 2 * i + 1]) : 0;
@@ -431,9 +466,11 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
       rm = max3_abs(rm, amax16(v), 0.f);
     }
     rm = warp_max_abs(rm);
-    if (lane == 0) apart[warp] = rm;
-    __syncthreads();
-    rm = warp_max_abs(lane < nwarp ? apart[lane] : 0.f);
+    if (!WARP) {
+      if (lane == 0) apart[warp] = rm;
+      __syncthreads();
+      rm = warp_max_abs(lane < nwarp ? apart[lane] : 0.f);
+    }
     if (tid == 0) p.out_scale[row] = __fdiv_rn(rm, 448.0f);
   }
   for (int k = 0; k < rounds; ++k) {
@@ -464,7 +501,7 @@ __global__ void __launch_bounds__(1024) k_rms_norm_any(NormParams p) {
     }
   }
   if (OUT == CSA2_FP8E4M3) {
-    __syncthreads();
+    sync();
     for (int i = tid; i < p.D; i += nt)
       static_cast<uint8_t*>(p.out)[row * p.so + i] = (uint8_t)__float_as_uint(buf[(i >> 4) * 17 + (i & 15)]);
   }
@@ -499,20 +536,21 @@ cudaError_t launch_aligned(const NormParams& p, cudaStream_t st) {
   return launch_rows(k_rms_norm<OUT, X32, RES>, resident[threads / 32], p, 1, threads, tail, st);
 }
 
-template <int OUT, int N>
+template <int OUT, int N, int THREADS>
 cudaError_t launch_any(const NormParams& p, cudaStream_t st) {
-  const bool quantised = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2;
-  const int threads = ((p.D + N - 1) / N + 31) & ~31;
-  const size_t smem = quantised ? (size_t)((p.D + 15) / 16) * 17 * 4 : 0;
+  constexpr bool quantised = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2, warp = THREADS == 32 * kAnyRows;
+  const int threads = warp ? THREADS : ((p.D + N - 1) / N + 31) & ~31;
+  const size_t smem = quantised ? (size_t)((p.D + 15) / 16) * 17 * 4 * (warp ? kAnyRows : 1) : 0;
   static bool attr_set = false;
-  if (quantised && !attr_set) {
+  if (quantised && !warp && !attr_set) {
     cudaError_t e =
-        cudaFuncSetAttribute(k_rms_norm_any<OUT, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
+        cudaFuncSetAttribute(k_rms_norm_any<OUT, N, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
     if (e != cudaSuccess) return e;
     attr_set = true;
   }
-  return launch_k(k_rms_norm_any<OUT, N>, (unsigned)p.T + (OUT == CSA2_FP4E2M1X2 && p.T % 128 ? 1u : 0u), threads, smem, st,
-                  p);
+  const unsigned blocks = warp ? (unsigned)(((long long)p.T + kAnyRows - 1) / kAnyRows) : (unsigned)p.T;
+  const bool tail = OUT == CSA2_FP4E2M1X2 && p.T % 128;
+  return launch_k(k_rms_norm_any<OUT, N, THREADS>, blocks + (tail ? 1u : 0u), threads, smem, st, p);
 }
 
 template <int OUT>
@@ -529,7 +567,8 @@ cudaError_t launch_form(const NormParams& p, bool aligned, cudaStream_t st) {
     CSA2_NORM(true, 2);
 #undef CSA2_NORM
   }
-  return p.D <= 8192 ? launch_any<OUT, 8>(p, st) : p.D <= 16384 ? launch_any<OUT, 16>(p, st) : launch_any<OUT, 32>(p, st);
+  if (p.D <= 512) return launch_any<OUT, 16, 32 * kAnyRows>(p, st);
+  return p.D <= 16384 ? launch_any<OUT, 16, 1024>(p, st) : launch_any<OUT, 32, 1024>(p, st);
 }
 
 bool rows_aligned(const void* p, long long stride, int esize, int to = 16) {

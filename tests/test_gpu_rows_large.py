@@ -1,4 +1,5 @@
-"""The row operators where element offsets pass 2^31, and on other streams than the default one."""
+"""The row operators where element offsets pass 2^31, on other streams than the default one, and the norm of rows
+that start off every boundary."""
 import numpy as np
 import pytest
 import torch
@@ -107,3 +108,40 @@ def test_on_another_stream():
     side.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("D", [1, 31, 33, 511, 512, 513, 1023, 16383, 16385])
+@pytest.mark.parametrize("T", [1, 3, 5, 130])
+def test_norm_unaligned(T, D):
+    """Rows that start off every boundary: a warp each up to 512 channels, a CTA each beyond."""
+    r = np.random.default_rng(D + T)
+    x = r.standard_normal((T, D)).astype(np.float32)
+    x[T // 2] = 0
+    x[T - 1] *= 3e18                                 # squares beyond float32, summed again scaled
+    wide = torch.full((T, D + 2), float("nan"), device=DEV)
+    wide[:, 1:-1] = torch.from_numpy(x).to(DEV)
+    w = (1 + 0.1 * r.standard_normal(D)).astype(np.float32)
+    out = torch.full((T, D + 4), 7.0, device=DEV)
+    y, _ = csa2.rms_norm(wide[:, 1:-1], torch.from_numpy(w).to(DEV), out_dtype=torch.float32, out=out[:, 3:3 + D])
+    ref = rows.rms_norm(x, w, 1e-6)
+    assert (np.abs(c(y.double()) - ref) <= np.abs(ref) * 5 * U * 1.001).all()
+    assert (out[:, :3] == 7).all() and (out[:, 3 + D:] == 7).all()      # nothing beside the rows
+    codes, scale, _ = csa2.rms_norm_fp8(wide[:, 1:-1], torch.from_numpy(w).to(DEV))
+    rc, rs = rows.fp8_groups(rows.rms_norm_f32(x, w, 1e-6), 0)
+    assert np.array_equal(c(scale), rs) and np.array_equal(c(codes), rc)
+    if D % 16 == 0:
+        q, _ = csa2.rms_norm_fp4(wide[:, 1:-1])
+        rc, rs = rows.fp4_quantize(rows.rms_norm_f32(x, None, 1e-6))
+        assert np.array_equal(c(q.codes), rc) and np.array_equal(c(q.scales), rows.scale_tiles(rs))
+
+
+@pytest.mark.parametrize("D", [256, 1040])
+def test_norm_unaligned_not_finite(D):
+    x = torch.ones((5, D + 1), device=DEV)
+    x[1, 5], x[3, 9] = float("inf"), float("nan")
+    x[4] = 0
+    y, _ = csa2.rms_norm(x[:, 1:], out_dtype=torch.float32)
+    y = c(y)
+    one = c(csa2.rms_norm(torch.ones((1, D), device=DEV), out_dtype=torch.float32)[0])
+    assert (y[0] == one[0]).all() and (y[2] == one[0]).all() and (y[4] == 0).all()
+    assert np.isnan(y[1, 4]) and (np.delete(y[1], 4) == 0).all() and np.isnan(y[3]).all()
