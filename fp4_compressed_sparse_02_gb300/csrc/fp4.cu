@@ -404,6 +404,16 @@ constexpr int SFCOLS = 16 + 32;            // scale columns of a stage, beside t
                                            // stay until its products are done
 static_assert(STAGE % 1024 == 0 && OUT % 1024 == 0 && BN + STAGES * SFCOLS <= 512, "alignment, TMEM columns");
 
+template <int TOKENS>
+struct Few {                               // k_fp4_linear_few: few tokens on the N side
+  static constexpr int SF = TOKENS > 128 ? SFB : SFA;     // scale tiles of the tokens
+  static constexpr int B = TOKENS / 2 * BKB, STAGE = A + B + SFA + SF;
+  static constexpr int STAGES = (212 * 1024) / STAGE < 8 ? (212 * 1024) / STAGE : 8;
+  static constexpr int SMEM = STAGES * STAGE + 256;
+  static_assert(STAGE % 1024 == 0 && TOKENS + STAGES * SFCOLS <= 512, "alignment, TMEM columns");
+  static_assert(TOKENS % 64 == 0 && STAGES * STAGE >= TOKENS * BM * 4, "a partial result fits where the stages were");
+};
+
 struct Params {
   const float* gx;
   const float* gw;
@@ -768,6 +778,159 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
   if (warp == EPI + 1) tmem_dealloc2(tb, 512);
 }
 
+// Up to BN tokens on CTA pairs: a tile is 256 features x BN tokens of out^T = w x^T, each CTA holds 128
+// features' weights and half of the tokens' rows, so the pair reads the tokens once and its products
+// are no wider than the tokens.  A cluster of S pairs splits the sum over K; the CTAs of a rank add the parts as
+// k_fp4_linear does.
+template <int BN>
+__global__ void __launch_bounds__(pairs::THREADS, 1)
+    k_fp4_linear_few(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                     const __grid_constant__ CUtensorMap msw, const __grid_constant__ CUtensorMap msx, pairs::Params p) {
+  using namespace pairs;
+  using C = Few<BN>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::STAGES * C::STAGE);   // the leader's are used
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* accf = empty + C::STAGES;                     // accumulator complete
+  uint32_t* tslot = reinterpret_cast<uint32_t*>(accf + 1);
+  volatile uint32_t* failed = tslot + 1;
+  const int S = p.split, crank = (int)tc::cluster_ctarank(), part = crank >> 1;
+  const uint32_t rank = crank & 1, leader = crank & ~1;   // rank 0 leads its pair
+  const uint16_t both = (uint16_t)(3u << leader);
+  const bool aligned = (smem_u32(smem) & 1023) == 0;      // the same in every CTA
+  if (warp == EPI + 1) tmem_alloc2(tslot, 512);
+  if (tid == 0) {
+    lin::prefetch_map(&mw);
+    lin::prefetch_map(&mx);
+    lin::prefetch_map(&msw);
+    lin::prefetch_map(&msx);
+    for (int s = 0; s < C::STAGES; ++s) {
+      tc::mbar_init(&full[s], 1);
+      tc::mbar_init(&empty[s], 1);
+    }
+    tc::mbar_init(accf, 1);
+    *failed = 0;
+    if (!aligned) raise_error(&g_err_fp4, CSA2_DEVERR_SMEM_ALIGN);
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();                                     // barriers and TMEM of both CTAs are there
+  tc::fence_after_sync();
+  pdl_wait();                                             // all of the above runs beside the previous kernel's end
+  pdl_trigger();
+  const uint32_t tb = *tslot;
+  const int nkb = (p.nkt + 3) / 4;
+  const int kb0 = (int)((long long)nkb * part / S), kb1 = (int)((long long)nkb * (part + 1) / S);
+  const int f0 = ((int)blockIdx.x / (2 * S) * 2 + (int)rank) * BM;
+  const bool run = aligned && tb == 0;                    // all 512 columns: they start at 0
+  if (warp == EPI) {
+    if (lane == 0 && run) {
+      int s = 0, fill = 0;                                // fill: how often the stages have been filled
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (fill > 0 && !tc::mbar_wait(&empty[s], (uint32_t)((fill - 1) & 1), MAX_POLL)) {
+          raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+          *failed = 1;
+          break;
+        }
+        uint8_t* st = smem + s * C::STAGE;
+        if (rank == 0) tc::mbar_arrive_expect_tx(&full[s], 2u * C::STAGE);
+        const uint32_t mb = tc::mapa(smem_u32(&full[s]), leader);
+        tma_load_pair(st, &mw, kb * BKB, f0, mb);
+        tma_load_pair(st + A, &mx, kb * BKB, (int)rank * (BN / 2), mb);
+        tma_load_pair(st + A + C::B, &msw, kb * 256, f0 >> 7, mb);
+        tma_load_pair(st + A + C::B + SFA, &msx, kb * 256, 0, mb);
+        if (++s == C::STAGES) s = 0, ++fill;
+      }
+    }
+  } else if (warp == EPI + 1) {
+    if (rank == 0 && run) {
+      constexpr uint32_t id = lin::idesc(2 * BM, BN);
+      const uint32_t base = smem_u32(smem) >> 4;
+      int s = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!__all_sync(0xffffffffu, tc::mbar_wait(&full[s], phase, MAX_POLL))) {
+          if (lane == 0) {
+            raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+            *failed = 1;
+          }
+          break;
+        }
+        tc::fence_after_sync();
+        const uint32_t a = base + (uint32_t)s * (C::STAGE >> 4), sft = BN + (uint32_t)s * SFCOLS;
+        const int steps = min(4, p.nkt - 4 * kb);
+        if (lin::elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps) {
+              sf_copy2(sft + 4 * k, a + ((A + C::B + 512 * k) >> 4));
+              sf_copy2(sft + 16 + 8 * k, a + ((A + C::B + SFA + 512 * k) >> 4));
+              if (BN > 128) sf_copy2(sft + 20 + 8 * k, a + ((A + C::B + SFA + 2048 + 512 * k) >> 4));
+            }
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < steps)
+              mma_fp4_pair(0, a + 2 * k, a + ((A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 8 * k, kb > kb0 || k > 0);
+          commit_pair(&empty[s], both);
+        }
+        __syncwarp();
+        if (++s == C::STAGES) s = 0, phase ^= 1;
+      }
+      if (lin::elect_one()) commit_pair(accf, both);
+      __syncwarp();
+    }
+  } else if (run) {
+    if (!tc::mbar_wait_warp(accf, 0, MAX_POLL)) {
+      if (lane == 0) {
+        raise_error(&g_err_fp4, CSA2_DEVERR_TIMEOUT);
+        *failed = 1;
+      }
+    } else {
+      // warp w: features 32 (w % 4) .. of the CTA's 128, half of the tokens; token by token into the stages' place
+      tc::fence_after_sync();
+      const uint32_t tq = (uint32_t)(32 * (warp & 3)) << 16;
+      float* at = reinterpret_cast<float*>(smem) + 32 * (warp & 3) + lane;
+      const int c1 = min(p.T, BN / 2 * (warp / 4 + 1));
+#pragma unroll 1
+      for (int c = BN / 2 * (warp / 4); c < c1; c += 32) {
+        uint32_t v[32];
+        tc::tmem_ld32(tq + (uint32_t)c, v);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) at[(c + i) * BM] = __uint_as_float(v[i]);
+      }
+    }
+  }
+  __syncwarp();
+  tc::cluster_sync();                                     // every part of the sum is there
+  if (warp < EPI && run && f0 + 4 * lane < p.N) {         // a warp a token: four features a lane
+    const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
+    const int f = f0 + 4 * lane;
+#pragma unroll 2
+    for (int t = part * EPI + warp; t < p.T; t += S * EPI) {
+      const uint32_t at = smem_u32(smem) + (t * BM + 4 * lane) * 4;
+      float4 v[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (q < S) v[q] = lin::ld_dsmem_f4(tc::mapa(at, 2 * q + rank));
+      float4 e = v[0];
+#pragma unroll
+      for (int q = 1; q < 4; ++q)
+        if (q < S) e.x += v[q].x, e.y += v[q].y, e.z += v[q].z, e.w += v[q].w;
+      lin::put4(p, (long long)t * p.N + f, p.N - f, e.x * alpha, e.y * alpha, e.z * alpha, e.w * alpha);
+    }
+  }
+  tc::fence_before_sync();
+  __syncwarp();
+  __syncthreads();
+  if (tid == 0 && *failed)                                // given up: the copies in flight land in a few us
+    for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+  __syncwarp();
+  tc::cluster_sync();                                     // the peer's loads, products and reads are done
+  if (warp == EPI + 1) tmem_dealloc2(tb, 512);
+}
+
 namespace {
 
 bool groups_of_four(const csa2_fp4_linear_args& a) {
@@ -911,6 +1074,43 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
 }
 
 template <int BN>
+cudaError_t launch_linear_few(const csa2_fp4_linear_args& a, cudaStream_t st) {
+  using namespace pairs;
+  CUtensorMap mx, mw, msx, msw;
+  if (!codes_map(&mw, a.w.codes, a.w.rows, a.w.cols / 2, BM) || !codes_map(&mx, a.x.codes, a.x.rows, a.x.cols / 2, BN / 2) ||
+      !scales_map(&msw, a.w, 1) || !scales_map(&msx, a.x, BN > 128 ? 2 : 1))
+    return cudaErrorInvalidValue;
+  pairs::Params p{};
+  p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out, p.out32 = a.out_dtype == CSA2_F32, p.vec4 = groups_of_four(a);
+  p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64;
+  const int tiles = (p.N + 2 * BM - 1) / (2 * BM), nkb = (p.nkt + 3) / 4;
+  static int pairs_at[5] = {0};                           // clusters of s pairs the GPU holds at once
+  if (!pairs_at[1]) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_few<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<BN>::SMEM);
+    if (e != cudaSuccess) return e;
+    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_few<BN>, 2 * s, THREADS, Few<BN>::SMEM);
+    if (!pairs_at[1]) return cudaErrorInvalidConfiguration;
+  }
+  p.split = 1;
+  for (int s = 2; s <= 4; ++s)
+    if (tiles <= pairs_at[s] && 2 * s <= nkb) p.split = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2u * (unsigned)p.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)(p.split * tiles));
+  cfg.blockDim = pairs::THREADS;
+  cfg.dynamicSmemBytes = Few<BN>::SMEM;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_fp4_linear_few<BN>, mw, mx, msw, msx, p);
+}
+
+template <int BN>
 cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   using C = lin::Cfg<BN>;
   CUtensorMap mw, mx;
@@ -962,9 +1162,21 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
 
 cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (a.x.rows == 0 || a.w.rows == 0) return cudaSuccess;
-  const int T = a.x.rows;
+  const int T = a.x.rows, sms = sm_count(), nkb = (a.x.cols + 255) / 256, ft = (a.w.rows + 127) / 128;
   if (T <= 16) return launch_linear<16>(a, st);
   if (T <= 32) return launch_linear<32>(a, st);
+  // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs): what a
+  // CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight ways below 16 feature tiles, and start
+  // and end sooner, which decides short sums.  us, single CTAs or wide pairs against pairs on few tokens:
+  //    64 x  4096 -> 2560   6.7   5.4      64 x  8192 -> 5120   7.9  7.8      64 x 32768 -> 5120  19.9 20.3
+  //   128 x  2560 -> 5120   6.3   6.7     128 x  3584 -> 5120   8.9  7.0     128 x 32768 -> 5120  22.7 21.6
+  //   192 x  2048 -> 5120   5.6   7.4     192 x  5120 -> 5120   9.6  8.6     192 x 32768 -> 5120  26.0 23.3
+  //   256 x  4096 -> 5120   8.8   9.4     256 x  8192 -> 5120  11.9 11.3     192 x 32768 -> 512   10.9 15.5
+  if (T <= 256 && ft >= 16 && ft <= sms * 9 / 19 && nkb >= (T <= 128 ? 14 : 18) && (T > 64 || nkb <= 32)) {
+    if (T <= 64) return launch_linear_few<64>(a, st);
+    if (T <= 128) return launch_linear_few<128>(a, st);
+    return T <= 192 ? launch_linear_few<192>(a, st) : launch_linear_few<256>(a, st);
+  }
   if (T <= 64) return launch_linear<64>(a, st);
   // Single CTAs while their 128 x 128 tiles run at once, two on an SM, and a CTA's share of the sum is
   // short: they start and end in 3 us, pairs in 5 to 6 us (and 3 us more where they split the sum), but
@@ -972,8 +1184,7 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   //   384 x 1024 -> 5120 (120 tiles, 4 stages)   4.4  6.5      384 x 8192 -> 5120 (32 stages)  15.3  15.7
   //   384 x 16384 -> 5120 (64 stages)            27.3 25.6     768 x 4096 -> 5120 (240, 16)    10.6  11.0
   //   192 x 16384 -> 5120 (80, 64)               17.7 17.7     192 x 32768 -> 5120 (80, 128)   28.3  26.1
-  const long long tiles = (long long)((T + 127) / 128) * ((a.w.rows + 127) / 128);
-  const int sms = sm_count(), nkb = (a.x.cols + 255) / 256;
+  const long long tiles = (T + 127LL) / 128 * ft;
   if (T <= 128 || (tiles <= 2 * sms && tiles * nkb <= 32LL * sms)) return launch_linear<128>(a, st);
   const bool tma = ((uintptr_t)a.out & 15) == 0 && (long long)a.w.rows * (a.out_dtype == CSA2_F32 ? 4 : 2) % 16 == 0;
   return tma ? launch_linear_pair<true>(a, st) : launch_linear_pair<false>(a, st);
