@@ -1,4 +1,6 @@
 // FP4 rows: the quantiser (csa2_fp4_quant) and the product with FP4 weights (csa2_fp4_linear).
+#include <cfloat>
+
 #include "internal.h"
 #include "rows.cuh"
 #include "tc.cuh"
@@ -207,10 +209,10 @@ __device__ __forceinline__ void put4(const P& p, long long at, int n, float a, f
 
 }  // namespace lin
 
-// Up to 128 tokens (and more where the tiles are few, see launch_fp4_linear): what bounds it is reading
-// the weights once.  Tile = 128 features x BN tokens of out^T = w x^T, so that few tokens fill the N
-// side of the product and the weights stream through the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32 partial in shared
-// memory and the CTAs add them in rank order.
+// Up to 128 tokens, and more where the tiles are few (launch_fp4_linear): what bounds it is reading the weights
+// once.  Tile = 128 features x BN tokens of out^T = w x^T, so that few tokens fill the N side of the product and
+// the weights stream through the M side.  A cluster of S CTAs splits the sum over K; each leaves its float32
+// partial in shared memory and the CTAs add them in rank order.
 //   Occupancy: at 1 x 5120 -> 32768 (256 tiles) one CTA an SM with nine stages takes 20.4 us, two
 // with four stages 16.5 us (its loads alone take as long; the floor of 94 MB is 13.9 us): a second
 // CTA's loads run during the first's start and end.  Prefetching further tiles into L2 made it 18 to
@@ -232,7 +234,7 @@ __global__ void __launch_bounds__(lin::THREADS)
   volatile int* failed = reinterpret_cast<volatile int*>(accf + 2);
   const int S = (int)gridDim.x / ((p.N + BM - 1) / BM);   // CTAs of a cluster
   const int rank = blockIdx.x % S;
-  const int f0 = (blockIdx.x / S) * BM, t0 = blockIdx.y * BN, nt = min(BN, p.T - t0);   // more than one token tile: BN = 128
+  const int f0 = (blockIdx.x / S) * BM, t0 = blockIdx.y * BN, nt = min(BN, p.T - t0);   // several token tiles: BN = 128
   const int nkb = (p.nkt + 3) / 4;
   const int kb0 = (int)((long long)nkb * rank / S), kb1 = (int)((long long)nkb * (rank + 1) / S);
   // the same in every CTA; the barriers of a cluster are reached either way
@@ -519,8 +521,8 @@ __device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) 
 //   Tile: 256 x 192 with two accumulators (results stored while the next tile runs) took 526 us:
 // per product it loads a sixth more.  Reading the accumulator 32 columns at a time between stores
 // took 496 us.  Two thirds of an earlier 1270 us was the issuing thread's own descriptor arithmetic.
-//   Split, 192 x 32768 -> 5120 (20 tiles): 1 46 us, 2 31 us, 3 26 us, 4 40 us (20 clusters of eight
-// do not all run at once); one-CTA tiles of 128 x 192 split in three took 28 us.
+//   Split over K in a cluster (the last round of few tiles), 256 x 32768 -> 5120 (20 tiles): 1 46 us, 2 31 us, 3 26 us,
+// 4 40 us (20 clusters of eight do not all run at once).
 // TMA_OUT: rows of the result that TMA can address; otherwise warps store them 32 columns at a time.
 template <bool TMA_OUT>
 __global__ void __launch_bounds__(pairs::THREADS, 1)
@@ -782,6 +784,10 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
 // features' weights and half of the tokens' rows, so the pair reads the tokens once and its products
 // are no wider than the tokens.  A cluster of S pairs splits the sum over K; the CTAs of a rank add the parts as
 // k_fp4_linear does.
+//   What bounds it, 192 x 32768 -> 5120 (20 tiles split in three, 23.2 us; 14.7 us at the copy rate): 60 of 76 pairs
+// have work, each CTA takes in 34 KB every 0.4 us, which is 45 bytes a cycle; start, end and adding take
+// 6 us.  Pairs of 256 x 256 (the tokens on the M side, a quarter of each product empty) took 26.0 us, CTAs of
+// 128 x 192 28 us.
 template <int BN>
 __global__ void __launch_bounds__(pairs::THREADS, 1)
     k_fp4_linear_few(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
@@ -1123,7 +1129,7 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.vec4 = groups_of_four(a);
   const int ft = (p.N + lin::BM - 1) / lin::BM, tt = (p.T + BN - 1) / BN, nkb = (p.nkt + 3) / 4;
   const long long tiles = (long long)ft * tt;
-  static int one[9] = {0};   // clusters of s CTAs that the GPU holds at once with one CTA an SM, which is what the query counts
+  static int one[9] = {0};                                // clusters of s CTAs that the GPU holds at once, a CTA an SM
   const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
   if (!one[1]) {
     cudaError_t e = cudaFuncSetAttribute(k_fp4_linear<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
@@ -1131,14 +1137,25 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
     for (int s = 8; s >= 1; --s) one[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
     if (!one[1]) return cudaErrorInvalidConfiguration;
   }
-  // Few tiles (under three quarters of the SMs): split the sum as far as every cluster still runs at
-  // once with two CTAs an SM, where the stages saved are worth adding the parts (1 x 1024 -> 512, four
-  // stages: 3.2 us whole, 3.4 us split; 128 x 1024 -> 512: 4.1 and 6.7 us; 1 x 2048 -> 512: 3.9 and 3.4 us).
+  // Few tiles (under three quarters of the SMs): split the sum where the stages saved are worth adding the
+  // parts.  Costs in stages, fitted to 148 sizes: clusters that do not all fit on SMs of their own share some, whose
+  // stages take 1.65 times as long together; adding costs what a tile of 128 tokens writes and reads, less for fewer.
+  //   us by S:  1 x 1024 -> 512    1: 3.2, 4: 3.4       128 x 1024 -> 512    1: 4.1, 2: 6.7
+  //             1 x 4096 -> 5120   3: 4.8, 6: 4.8       777 x 4128 -> 1000   2: 9.7, 5: 10.5
+  //           500 x 8192 -> 1000   4: 8.3, 7: 10.1      384 x 8192 -> 2560   2: 12.3, 4: 10.8
+  //            32 x 8192 -> 2560   5: 5.6, 8: 6.1
   // More tiles than SMs: two CTAs an SM.
   int S = 1;
-  if (4 * tiles <= 3 * one[1])
-    for (int s = 2; s <= 8; ++s)
-      if (tiles <= 2 * one[s] && 2 * s <= nkb && nkb - nkb / s >= 4 + BN / 16) S = s;
+  if (4 * tiles <= 3 * one[1]) {
+    float best = FLT_MAX;
+    for (int s = 1; s <= 8 && (s == 1 || 2 * s <= nkb); ++s) {
+      if (tiles > 2 * one[s]) continue;
+      const bool shared = tiles > one[s];
+      const float stages = (shared ? 1.65f : 1.f) * nkb / s + (shared ? 2.1f * BN / 128 : 0.f);
+      const float cost = stages + (s > 1 ? 3.f + BN / 32.f + s * BN * (0.3f / 128) : 0.f);
+      if (cost < best) best = cost, S = s;
+    }
+  }
   p.stages = S == 1 && tiles <= one[1] ? C::STAGES : C::STAGES2;
   p.tmem_cols = 128;
   while (p.tmem_cols < C::DCOLS + p.stages * C::SFCOLS) p.tmem_cols *= 2;
@@ -1166,8 +1183,9 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (T <= 16) return launch_linear<16>(a, st);
   if (T <= 32) return launch_linear<32>(a, st);
   // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs): what a
-  // CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight ways below 16 feature tiles, and start
-  // and end sooner, which decides short sums.  us, single CTAs or wide pairs against pairs on few tokens:
+  // CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight
+  // ways below 16 feature tiles, and start and end sooner, which decides short sums.  us, single CTAs or
+  // wide pairs against pairs on few tokens:
   //    64 x  4096 -> 2560   6.7   5.4      64 x  8192 -> 5120   7.9  7.8      64 x 32768 -> 5120  19.9 20.3
   //   128 x  2560 -> 5120   6.3   6.7     128 x  3584 -> 5120   8.9  7.0     128 x 32768 -> 5120  22.7 21.6
   //   192 x  2048 -> 5120   5.6   7.4     192 x  5120 -> 5120   9.6  8.6     192 x 32768 -> 5120  26.0 23.3

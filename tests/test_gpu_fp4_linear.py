@@ -140,3 +140,31 @@ def test_quantised_product_end_to_end():
     full = rows.rms_norm(x, None, 1e-6) @ wt.T.astype(np.float64)
     # FP4 keeps about 2.5 bits: the product is near the unquantised one, in norm
     assert np.linalg.norm(c(y) - full) <= 0.25 * np.linalg.norm(full)
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,N,K", [
+    (33, 2045, 4128), (64, 2176, 8192), (50, 9216, 3616),      # pairs on up to 64 tokens
+    (65, 2045, 3616), (128, 5120, 4096), (97, 9100, 16384),    # up to 128
+    (129, 2048, 4640), (192, 3001, 8192), (131, 9216, 4640),   # up to 192
+    (193, 2050, 4640), (256, 5120, 8224),                      # up to 256
+    (300, 4096, 32768), (512, 2044, 32768)])                   # wide pairs, the sum split in a cluster
+def test_fp4_linear_pairs_split(T, N, K, out):
+    test_fp4_linear_many_tiles(T, N, K, out)
+
+
+@pytest.mark.parametrize("T,K,N", [(40, 4096, 2100), (100, 4096, 2100), (150, 5120, 2100), (250, 5120, 2100)])
+def test_fp4_linear_pairs_rows_and_scales(T, K, N):
+    """One nonzero scale a row, and a row and a feature of NaN scales: neither halves nor parts are mixed up."""
+    r = np.random.default_rng(12)
+    wc, ws = r.integers(0, 256, (N, K // 2), dtype=np.uint8), r.integers(0x30, 0x40, (N, K // 16), dtype=np.uint8)
+    xc = r.integers(0, 256, (T, K // 2), dtype=np.uint8)
+    xs = np.zeros((T, K // 16), np.uint8)
+    xs[np.arange(T), (7 * np.arange(T)) % (K // 16)] = 0x38
+    d = lambda c, s: csa2.Fp4Rows(torch.from_numpy(c).to(DEV), torch.from_numpy(rows.scale_tiles(s)).to(DEV))
+    check(csa2.fp4_linear(d(xc, xs), d(wc, ws), out_dtype=torch.float32), xc, xs, wc, ws)
+    xs[T - 3, K // 16 - 1], ws[150, 1], ws[N - 1, K // 32] = 0x7F, 0x7F, 0x7F
+    y = csa2.fp4_linear(d(xc, xs), d(wc, ws), out_dtype=torch.float32).cpu().numpy()
+    nan = np.zeros((T, N), bool)
+    nan[T - 3], nan[:, 150], nan[:, N - 1] = True, True, True
+    assert np.array_equal(np.isnan(y), nan)
