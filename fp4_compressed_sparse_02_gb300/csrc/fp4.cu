@@ -362,18 +362,28 @@ __global__ void __launch_bounds__(lin::THREADS)
         put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
       }
     } else {
-#pragma unroll 2
-      for (int t = rank * WARPS + warp; t < nt; t += S * WARPS) {
-        const uint32_t at = smem_u32(smem) + (t * BM + 4 * lane) * 4;
-        float4 v[8];                                      // every peer's piece, on its way at once
+      // the parts of two tokens on their way at once, of one where there are more parts than four: 777 x 4128 -> 1000
+      // (S = 2) 8.6 us, one by one 9.7; 384 x 4096 -> 1024 (S = 5) 6.3 us, two tokens 6.7
+      const int step = S * WARPS, many = S <= 4 ? 2 : 1;
+      for (int t = rank * WARPS + warp; t < nt; t += many * step) {
+        float4 v[2][8];
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          if (q < S) v[q] = ld_dsmem_f4(tc::mapa(at, q));
-        float4 s = v[0];
+        for (int u = 0; u < 2; ++u) {
+          const uint32_t at = smem_u32(smem) + ((t + u * step) * BM + 4 * lane) * 4;
 #pragma unroll
-        for (int q = 1; q < 8; ++q)
-          if (q < S) s.x += v[q].x, s.y += v[q].y, s.z += v[q].z, s.w += v[q].w;
-        put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+          for (int q = 0; q < 8; ++q)
+            if (q < S && u < many && t + u * step < nt) v[u][q] = ld_dsmem_f4(tc::mapa(at, q));
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int tu = t + u * step;
+          if (u >= many || tu >= nt) continue;
+          float4 s = v[u][0];
+#pragma unroll
+          for (int q = 1; q < 8; ++q)
+            if (q < S) s.x += v[u][q].x, s.y += v[u][q].y, s.z += v[u][q].z, s.w += v[u][q].w;
+          put4(p, (long long)(t0 + tu) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+        }
       }
     }
   }
@@ -783,7 +793,8 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
 // Up to BN tokens on CTA pairs: a tile is 256 features x BN tokens of out^T = w x^T, each CTA holds 128
 // features' weights and half of the tokens' rows, so the pair reads the tokens once and its products
 // are no wider than the tokens.  A cluster of S pairs splits the sum over K; the CTAs of a rank add the parts as
-// k_fp4_linear does.
+// k_fp4_linear does, with loads from the peers' shared memory (bulk copies of each owner's tokens to it took 1.2
+// to 2 us more).
 //   What bounds it, 192 x 32768 -> 5120 (20 tiles split in three, 23.2 us; 14.7 us at the copy rate): 60 of 76 pairs
 // have work, each CTA takes in 34 KB every 0.4 us, which is 45 bytes a cycle; start, end and adding take
 // 6 us.  Pairs of 256 x 256 (the tokens on the M side, a quarter of each product empty) took 26.0 us, CTAs of
@@ -913,18 +924,27 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
   if (warp < EPI && run && f0 + 4 * lane < p.N) {         // a warp a token: four features a lane
     const float alpha = (p.gx ? ld_f32(p.gx) : 1.f) * (p.gw ? ld_f32(p.gw) : 1.f);
     const int f = f0 + 4 * lane;
-#pragma unroll 2
-    for (int t = part * EPI + warp; t < p.T; t += S * EPI) {
-      const uint32_t at = smem_u32(smem) + (t * BM + 4 * lane) * 4;
-      float4 v[4];
+    // two tokens' loads on their way at once: one by one costs 0.75 us more at S = 2, four 0.7 us at S = 3
+    const int step = S * EPI;
+    for (int t = part * EPI + warp; t < p.T; t += 2 * step) {
+      float4 v[2][4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (q < S) v[q] = lin::ld_dsmem_f4(tc::mapa(at, 2 * q + rank));
-      float4 e = v[0];
+      for (int u = 0; u < 2; ++u) {
+        const uint32_t at = smem_u32(smem) + ((t + u * step) * BM + 4 * lane) * 4;
 #pragma unroll
-      for (int q = 1; q < 4; ++q)
-        if (q < S) e.x += v[q].x, e.y += v[q].y, e.z += v[q].z, e.w += v[q].w;
-      lin::put4(p, (long long)t * p.N + f, p.N - f, e.x * alpha, e.y * alpha, e.z * alpha, e.w * alpha);
+        for (int q = 0; q < 4; ++q)
+          if (q < S && t + u * step < p.T) v[u][q] = lin::ld_dsmem_f4(tc::mapa(at, 2 * q + rank));
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int tu = t + u * step;
+        if (tu >= p.T) continue;
+        float4 e = v[u][0];
+#pragma unroll
+        for (int q = 1; q < 4; ++q)
+          if (q < S) e.x += v[u][q].x, e.y += v[u][q].y, e.z += v[u][q].z, e.w += v[u][q].w;
+        lin::put4(p, (long long)tu * p.N + f, p.N - f, e.x * alpha, e.y * alpha, e.z * alpha, e.w * alpha);
+      }
     }
   }
   tc::fence_before_sync();
