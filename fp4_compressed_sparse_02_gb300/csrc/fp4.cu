@@ -527,7 +527,9 @@ __device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) 
 // half of TMEM and the scales part of the rest, so the next tile starts when this one has been
 // read: eight warps take it into registers in one go and release it before anything is stored.
 //   What bounds it, 8192 x 5120 -> 32768: products alone take 316 us, the loads alone 279 us, the
-// scale copies alone 282 us, together without the results 414 us; all of it 445 us, 6.2 PFLOP/s.
+// scale copies alone 282 us; all of it 422 us, 6.5 PFLOP/s (433 us on the slowest of three boards).  Each
+// step's scales are copied right before its product: all of a stage's first, then its products, took 434 us
+// (414 without the results), the next stage's before this one's products a fourth more.
 //   Tile: 256 x 192 with two accumulators (results stored while the next tile runs) took 526 us:
 // per product it loads a sixth more.  Reading the accumulator 32 columns at a time between stores
 // took 496 us.  Two thirds of an earlier 1270 us was the issuing thread's own descriptor arithmetic.
@@ -641,12 +643,9 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
                 sf_copy2(sft + 4 * k, a + ((A + B + 512 * k) >> 4));
                 sf_copy2(sft + 16 + 8 * k, a + ((A + B + SFA + 512 * k) >> 4));
                 sf_copy2(sft + 20 + 8 * k, a + ((A + B + SFA + 2048 + 512 * k) >> 4));
-              }
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (k < nt)
                 mma_fp4_pair(0, a + 2 * k, a + ((A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 8 * k,
                              kb > kb0 || k > 0);
+              }
             commit_pair(&empty[s], both);
           }
           __syncwarp();
@@ -884,11 +883,8 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
               sf_copy2(sft + 4 * k, a + ((A + C::B + 512 * k) >> 4));
               sf_copy2(sft + 16 + 8 * k, a + ((A + C::B + SFA + 512 * k) >> 4));
               if (BN > 128) sf_copy2(sft + 20 + 8 * k, a + ((A + C::B + SFA + 2048 + 512 * k) >> 4));
-            }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (k < steps)
               mma_fp4_pair(0, a + 2 * k, a + ((A + 32 * k) >> 4), id, sft + 4 * k, sft + 16 + 8 * k, kb > kb0 || k > 0);
+            }
           commit_pair(&empty[s], both);
         }
         __syncwarp();
