@@ -68,14 +68,16 @@ __device__ __forceinline__ void load_angles(float* v, const float* p) {
 // and then for the angles.  A token with a bad position is copied as it is.
 //   What bounds it: memory.  8192 tokens x 64 heads x 128 channels in bf16 (273 MB, 40.2 us at the copy
 // rate): 46.0 us; a CTA for each token 52.4 us, two heads' loads at once 51 us (fewer CTAs fit),
-// 256 threads 46.4 us.
+// 256 threads 46.4 us.  The same on rows that start off every boundary (V = 1): 64 us with eight heads' loads at once,
+// 71 with four, 177 with one.
 template <typename T, int V, bool INTERLEAVED>
-__global__ void __launch_bounds__(kThreads, 10) k_rope(RopeParams p) {
+__global__ void __launch_bounds__(kThreads, V > 1 ? 10 : 8) k_rope(RopeParams p) {
   pdl_wait();
   pdl_trigger();
   using Vt = Vec<T, V>;
   constexpr int NP = INTERLEAVED ? (V > 1 ? V / 2 : 1) : V;   // pairs of a unit
   constexpr int PARTS = INTERLEAVED && V > 1 ? 1 : 2;         // vectors of a unit that turns
+  constexpr int HEADS = V > 1 ? 1 : 8;                        // of a thread at once: single channels need more in flight
   const int h0 = blockIdx.y * blockDim.y + threadIdx.y, hs = gridDim.y * blockDim.y;
   const int half = p.d_rope / 2;
   int next = blockIdx.x < p.T ? ld_s32(p.pos + blockIdx.x) : 0;   // a token's position, one token ahead
@@ -100,24 +102,33 @@ __global__ void __launch_bounds__(kThreads, 10) k_rope(RopeParams p) {
         load_angles<NP>(cs, p.cos + (long long)ps * half + u * NP);
         load_angles<NP>(sn, p.sin + (long long)ps * half + u * NP);
       }
-      for (int h = h0; h < p.H; h += hs) {
-        const T* from = x + h * p.xh;
-        T* to = o + h * p.oh;
-        Vt v = *reinterpret_cast<const Vt*>(from + c), w = v;
-        if (PARTS == 2 && turn) w = *reinterpret_cast<const Vt*>(from + c2);
-        if (turns) {
+      for (int h = h0; h < p.H; h += HEADS * hs) {
+        Vt v[HEADS], w[HEADS];
 #pragma unroll
-          for (int i = 0; i < NP; ++i) {
-            T& e0 = PARTS == 1 ? v.e[2 * i] : v.e[i];
-            T& e1 = PARTS == 1 ? v.e[2 * i + (V > 1)] : w.e[i];
-            float a = to_f32(e0), b = to_f32(e1);
-            rope_pair(a, b, cs[i], p.inverse ? -sn[i] : sn[i]);
-            e0 = from_f32<T>(a);
-            e1 = from_f32<T>(b);
-          }
+        for (int j = 0; j < HEADS; ++j) {
+          if (HEADS > 1 && h + j * hs >= p.H) break;
+          const T* from = x + (h + j * hs) * p.xh;
+          v[j] = *reinterpret_cast<const Vt*>(from + c);
+          if (PARTS == 2 && turn) w[j] = *reinterpret_cast<const Vt*>(from + c2);
         }
-        *reinterpret_cast<Vt*>(to + c) = v;
-        if (PARTS == 2 && turn) *reinterpret_cast<Vt*>(to + c2) = w;
+#pragma unroll
+        for (int j = 0; j < HEADS; ++j) {
+          if (HEADS > 1 && h + j * hs >= p.H) break;
+          if (turns) {
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+              T& e0 = PARTS == 1 ? v[j].e[2 * i] : v[j].e[i];
+              T& e1 = PARTS == 1 ? v[j].e[2 * i + (V > 1)] : w[j].e[i];
+              float a = to_f32(e0), b = to_f32(e1);
+              rope_pair(a, b, cs[i], p.inverse ? -sn[i] : sn[i]);
+              e0 = from_f32<T>(a);
+              e1 = from_f32<T>(b);
+            }
+          }
+          T* to = o + (h + j * hs) * p.oh;
+          *reinterpret_cast<Vt*>(to + c) = v[j];
+          if (PARTS == 2 && turn) *reinterpret_cast<Vt*>(to + c2) = w[j];
+        }
       }
     }
   }

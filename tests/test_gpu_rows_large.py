@@ -145,3 +145,31 @@ def test_norm_unaligned_not_finite(D):
     one = c(csa2.rms_norm(torch.ones((1, D), device=DEV), out_dtype=torch.float32)[0])
     assert (y[0] == one[0]).all() and (y[2] == one[0]).all() and (y[4] == 0).all()
     assert np.isnan(y[1, 4]) and (np.delete(y[1], 4) == 0).all() and np.isnan(y[3]).all()
+
+
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("bf16", [True, False])
+@pytest.mark.parametrize("T,H,D,d_rope,first", [(1, 1, 2, 2, 0), (3, 9, 66, 64, 1), (40, 17, 130, 66, 64), (2500, 70, 34, 34, 0)])
+def test_rope_unaligned(T, H, D, d_rope, first, bf16, interleaved):
+    """Heads in eights and the rest of them, on rows that start off every boundary; into new rows and in place."""
+    r = np.random.default_rng(H)
+    x = torch.from_numpy(r.standard_normal((T, H * D + 3)).astype(np.float32)).to(DEV)
+    x = x.bfloat16() if bf16 else x
+    h = x[:, 1:1 + H * D].unflatten(1, (H, D))
+    before, sides = h.clone(), x[:, [0, -2, -1]].clone()
+    cos, sin = synth.rope_tables(500, d_rope)
+    pos = r.integers(0, 500, T).astype(np.int32)
+    t = lambda a: torch.from_numpy(a).to(DEV)
+    y = csa2.rope(h, t(pos), t(cos), t(sin), interleaved=interleaved, first=first)
+    assert torch.equal(h, before)
+    ref = rows.rope(c(before.double()), pos, cos, sin, interleaved, False, first)
+    mag = np.maximum(*(rows.rope(np.abs(c(before.double())), pos, np.abs(cos), s * np.abs(sin), interleaved, False, first)
+                       for s in (-1, 1)))
+    # two products and a sum, then the type; what does not turn is copied
+    tol = mag * 2 * U * 1.001 + np.abs(ref) * (U + (UB if bf16 else 0))
+    assert (np.abs(c(y.double()) - ref) <= tol * (1 + UB)).all()
+    assert torch.equal(y[..., :first], before[..., :first])
+    assert torch.equal(y[..., first + d_rope:], before[..., first + d_rope:])
+    assert csa2.rope(h, t(pos), t(cos), t(sin), interleaved=interleaved, first=first, out=h) is h
+    assert torch.equal(h, y) and torch.equal(x[:, [0, -2, -1]], sides)
+    assert csa2.device_error() == 0
