@@ -352,14 +352,27 @@ __global__ void __launch_bounds__(lin::THREADS)
     tc::cluster_sync();
   else
     __syncthreads();
+  if (!bad && S == 1 && !p.vec4) {                        // a warp a token, neighbouring lanes neighbouring features
+    const int n = p.N - f0 - lane;
+#pragma unroll 4
+    for (int t = warp; t < nt; t += THREADS / 32) {
+      const float* s = reinterpret_cast<const float*>(smem) + t * BM + lane;
+      const long long at = (long long)(t0 + t) * p.N + f0 + lane;
+#pragma unroll
+      for (int i = 0; i < BM; i += 32)
+        if (i < n) put(p, at + i, s[i] * alpha);
+    }
+  }
   if (!bad && f0 + 4 * lane < p.N) {                      // a warp a token: four features a lane
     const int f = f0 + 4 * lane;
     constexpr int WARPS = THREADS / 32;
     if (S == 1) {
+      if (p.vec4) {
 #pragma unroll 4
-      for (int t = warp; t < nt; t += WARPS) {
-        const float4 s = reinterpret_cast<const float4*>(smem)[t * (BM / 4) + lane];
-        put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+        for (int t = warp; t < nt; t += WARPS) {
+          const float4 s = reinterpret_cast<const float4*>(smem)[t * (BM / 4) + lane];
+          put4(p, (long long)(t0 + t) * p.N + f, p.N - f, s.x * alpha, s.y * alpha, s.z * alpha, s.w * alpha);
+        }
       }
     } else {
       // the parts of two tokens on their way at once, of one where there are more parts than four: 777 x 4128 -> 1000
@@ -507,6 +520,37 @@ __device__ __forceinline__ void stage32(const uint32_t (&v)[32], uint32_t at, in
         w[i] = pack_bf16(__uint_as_float(v[8 * j + 2 * i]) * alpha, __uint_as_float(v[8 * j + 2 * i + 1]) * alpha);
       asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(at + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)),
                    "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+}
+
+// stage32's rows out of shared memory to rows that TMA cannot address: a lane a column, `rows` values from `at` on
+// (2048 x 5120 -> 8191: 40 us, against 48 us with the accumulator held until the last store; half a warp a row
+// and two values a store took 47 us).
+template <typename P>
+__device__ __forceinline__ void store_rows(const P& p, uint32_t slice, int lane, long long at, int rows) {
+  constexpr int BATCH = 8;
+  at += lane;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += BATCH) {                // a batch of rows' values, then their stores
+    uint32_t e[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int r = r0 + i;
+      if (p.out32)
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(e[i])
+                     : "r"(slice + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
+      else
+        asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}" : "=r"(e[i])
+                     : "r"(slice + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
+    }
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (r0 + i >= rows) continue;
+      if (p.out32)
+        static_cast<uint32_t*>(p.out)[at + (long long)(r0 + i) * p.N] = e[i];
+      else
+        static_cast<uint16_t*>(p.out)[at + (long long)(r0 + i) * p.N] = (uint16_t)e[i];
     }
   }
 }
@@ -689,17 +733,17 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
         break;                                            // the cluster's only tile
       }
       const int t0 = (2 * tt + (int)rank) * BM + 32 * (warp & 3), f0 = ft * BN + 128 * (warp >> 2);
-      if (TMA_OUT) {
-        uint32_t acc[4][32];                              // all of this warp's part, so that it is free at once
+      uint32_t acc[4][32];                                // all of this warp's part, so that it is free at once
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc::tmem_ld32(tq + 32u * i, acc[i]);
-        tc::tmem_ld_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
+      for (int i = 0; i < 4; ++i) tc::tmem_ld32(tq + 32u * i, acc[i]);
+      tc::tmem_ld_wait();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (t0 >= p.T || f0 + 32 * i >= p.N) continue;
+      for (int i = 0; i < 4; ++i) {
+        if (t0 >= p.T || f0 + 32 * i >= p.N) continue;
+        if (TMA_OUT) {
           // the slice's last store has read it (float32 slices take both halves)
           if (lane == 0) p.out32 ? store_wait_read<0>() : store_wait_read<1>();
           __syncwarp();
@@ -708,46 +752,10 @@ __global__ void __launch_bounds__(pairs::THREADS, 1)
           tc::fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) tma_store(&mo, f0 + 32 * i, t0, at);
-        }
-      } else {
-        const int rows = min(32, p.T - t0);
-#pragma unroll 1
-        for (int c = 0; c < 128; c += 32) {
-          uint32_t v[32];
-          tc::tmem_ld32(tq + (uint32_t)c, v);
-          tc::tmem_ld_wait();
-          if (c == 96) {                                  // this warp has read its part
-            tc::fence_before_sync();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(tc::mapa(smem_u32(acce), leader));
-          }
-          if (rows <= 0 || f0 + c >= p.N) continue;
-          stage32(v, slice, lane, alpha, p.out32);
+        } else {
+          stage32(acc[i], slice, lane, alpha, p.out32);
           __syncwarp();
-          const bool in = f0 + c + lane < p.N;
-          const long long o = (long long)t0 * p.N + f0 + c + lane;
-#pragma unroll
-          for (int r0 = 0; r0 < 32; r0 += 16) {           // sixteen rows' values, then their stores
-            uint32_t e[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int r = r0 + i;
-              if (p.out32)
-                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(e[i])
-                             : "r"(slice + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3)));
-              else
-                asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}" : "=r"(e[i])
-                             : "r"(slice + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + 2 * (lane & 7)));
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (!in || r0 + i >= rows) continue;
-              if (p.out32)
-                static_cast<uint32_t*>(p.out)[o + (long long)(r0 + i) * p.N] = e[i];
-              else
-                static_cast<uint16_t*>(p.out)[o + (long long)(r0 + i) * p.N] = (uint16_t)e[i];
-            }
-          }
+          store_rows(p, slice, lane, (long long)t0 * p.N + f0 + 32 * i, f0 + 32 * i + lane < p.N ? min(32, p.T - t0) : 0);
           __syncwarp();
         }
       }
