@@ -1164,7 +1164,8 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   // Few tiles (under three quarters of the SMs): split the sum where the stages saved are worth adding the
   // parts.  Costs in stages, fitted to 148 sizes: clusters that do not all fit on SMs of their own share some, whose
   // stages take 1.65 times as long together; adding costs what a tile of 128 tokens writes and reads, less for fewer.
-  //   us by S:  1 x 1024 -> 512    1: 3.2, 4: 3.4       128 x 1024 -> 512    1: 4.1, 2: 6.7
+  //   us by S, parts loaded one token at a time:
+  //             1 x 1024 -> 512    1: 3.2, 4: 3.4       128 x 1024 -> 512    1: 4.1, 2: 6.7
   //             1 x 4096 -> 5120   3: 4.8, 6: 4.8       777 x 4128 -> 1000   2: 9.7, 5: 10.5
   //           500 x 8192 -> 1000   4: 8.3, 7: 10.1      384 x 8192 -> 2560   2: 12.3, 4: 10.8
   //            32 x 8192 -> 2560   5: 5.6, 8: 6.1
