@@ -308,24 +308,31 @@ def _float_type(t, name):
     return k
 
 
-def _rows_of(t, name):
-    """(data pointer, row stride) of a CUDA matrix whose rows are contiguous."""
-    if not t.is_cuda:
+def _on_device(t, dev, name):
+    """Refuse a tensor that is not on CUDA device number dev."""
+    at = t.get_device()
+    if at < 0:
         raise ValueError(f"{name}: expected a CUDA tensor")
+    if at != dev:
+        raise ValueError(f"{name}: on cuda:{at}, but the call's tensors are on cuda:{dev}")
+
+
+def _rows_of(t, dev, name):
+    """(data pointer, row stride) of a matrix on CUDA device number dev whose rows are contiguous."""
+    _on_device(t, dev, name)
     rows, last = t.stride()
     if last != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
     return t.data_ptr(), rows
 
 
-def _dense(t, dtype, name):
-    """Data pointer of a contiguous CUDA tensor of one type, 0 of None."""
+def _dense(t, dev, dtype, name):
+    """Data pointer of a contiguous tensor of one type on CUDA device number dev, 0 of None."""
     if t is None:
         return 0
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: expected a CUDA tensor")
+    _on_device(t, dev, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
@@ -340,9 +347,15 @@ _FP4_QUANT = struct.Struct("@NPiq" + _FP4_ROWS + "0P")
 _FP4_LINEAR = struct.Struct("@N" + 2 * _FP4_ROWS + "Pi0P")
 
 
-def _launch(fn, packed, t):
-    """Call fn on the current stream of tensor t's device."""
-    status = getattr(_lib.lib(), fn)(packed, torch._C._cuda_getCurrentRawStream(t.get_device()))
+def _launch(fn, packed, dev):
+    """Call fn on the current stream of CUDA device number dev, with that device current: a launch goes to
+    the current one, whatever device its stream's handle and its pointers belong to."""
+    call = getattr(_lib.lib(), fn)
+    if dev == torch._C._cuda_getDevice():
+        status = call(packed, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            status = call(packed, torch._C._cuda_getCurrentRawStream(dev))
     if status:
         _lib.check(status)
 
@@ -379,28 +392,31 @@ class Fp4Rows:
         return self.scales.view(a, b, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(a * 128, b * 4)[:self.rows,
                                                                                              :self.cols // 16]
 
-    def fields(self):
-        """(codes, scales, gscale, rows, cols) of the C struct, after its checks."""
+    def fields(self, dev=None):
+        """(codes, scales, gscale, rows, cols) of the C struct, after its checks; dev: the CUDA device number
+        that all of them must be on (by default the codes')."""
+        if dev is None:
+            dev = self.codes.get_device()
         rows, half = self.codes.shape
         if self.scales.shape != ((rows + 127) // 128, (half + 31) // 32, 512):
             raise ValueError(f"scales {tuple(self.scales.shape)} do not belong to codes {tuple(self.codes.shape)}")
         g = self.gscale
         if g is not None and g.numel() != 1:
             raise ValueError("gscale must have one element")
-        return (_dense(self.codes, torch.uint8, "codes"), _dense(self.scales, torch.uint8, "scales"),
-                _dense(g, torch.float32, "gscale"), rows, 2 * half)
+        return (_dense(self.codes, dev, torch.uint8, "codes"), _dense(self.scales, dev, torch.uint8, "scales"),
+                _dense(g, dev, torch.float32, "gscale"), rows, 2 * half)
 
 
-def _norm(x, weight, eps, residual, residual_out, out_form, group, out, out_stride, out_scale, out4):
+def _norm(x, dev, weight, eps, residual, residual_out, out_form, group, out, out_stride, out_scale, out4):
     """One csa2_rms_norm call; returns residual_out (allocated here if need be)."""
     T, D = shape = x.shape
-    xp, xs = _rows_of(x, "x")
+    xp, xs = _rows_of(x, dev, "x")
     wp = wt = rp = rs = op = os_ = rt = 0
     if weight is not None:
         if weight.shape != (D,):
             raise ValueError(f"weight must have {D} elements")
         wt = _float_type(weight, "weight")
-        wp = _dense(weight, weight.dtype, "weight")
+        wp = _dense(weight, dev, weight.dtype, "weight")
     if residual is not None:
         if residual_out is None:
             residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
@@ -409,13 +425,13 @@ def _norm(x, weight, eps, residual, residual_out, out_form, group, out, out_stri
         if residual.shape != shape:
             raise ValueError("residual and residual_out must have x's shape and one type")
         rt = _float_type(residual, "residual")
-        rp, rs = _rows_of(residual, "residual")
-        op, os_ = _rows_of(residual_out, "residual_out")
+        rp, rs = _rows_of(residual, dev, "residual")
+        op, os_ = _rows_of(residual_out, dev, "residual_out")
     elif residual_out is not None:
         raise ValueError("residual_out without a residual")
     _launch("csa2_rms_norm", _RMS_NORM.pack(
         _RMS_NORM.size, T, D, xp, _float_type(x, "x"), rt, xs, rp, op, rs, os_, wp, wt, eps, out_form, group, out,
-        out_stride, out_scale, *out4), x)
+        out_stride, out_scale, *out4), dev)
     return residual_out
 
 
@@ -431,8 +447,9 @@ def rms_norm(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, out_
         out = torch.empty(x.shape, dtype=out_dtype, device=x.device)
     elif out.shape != x.shape:
         raise ValueError("out must have x's shape")
-    return out, _norm(x, weight, eps, residual, residual_out, _float_type(out, "out"), 0, *_rows_of(out, "out"), 0,
-                      _NO_FP4)
+    dev = x.get_device()
+    return out, _norm(x, dev, weight, eps, residual, residual_out, _float_type(out, "out"), 0,
+                      *_rows_of(out, dev, "out"), 0, _NO_FP4)
 
 
 def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, group=0, out=None, out_scale=None):
@@ -449,8 +466,9 @@ def rms_norm_fp8(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, 
         out_scale = torch.empty((T, n), dtype=torch.float32, device=x.device)
     elif out_scale.shape != (T, n):
         raise ValueError(f"out_scale must be [{T}, {n}]")
-    residual_out = _norm(x, weight, eps, residual, residual_out, FP8E4M3, group, *_rows_of(out, "out"),
-                         _dense(out_scale, torch.float32, "out_scale"), _NO_FP4)
+    dev = x.get_device()
+    residual_out = _norm(x, dev, weight, eps, residual, residual_out, FP8E4M3, group, *_rows_of(out, dev, "out"),
+                         _dense(out_scale, dev, torch.float32, "out_scale"), _NO_FP4)
     return out, out_scale, residual_out
 
 
@@ -461,7 +479,8 @@ def rms_norm_fp4(x, weight=None, *, eps=1e-6, residual=None, residual_out=None, 
         out = Fp4Rows.allocate(x.shape[0], x.shape[1], x.device, gscale)
     elif gscale is not None:
         raise ValueError("give gscale with out, or out alone")
-    return out, _norm(x, weight, eps, residual, residual_out, FP4E2M1X2, 0, 0, 0, 0, out.fields())
+    dev = x.get_device()
+    return out, _norm(x, dev, weight, eps, residual, residual_out, FP4E2M1X2, 0, 0, 0, 0, out.fields(dev))
 
 
 ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
@@ -481,10 +500,11 @@ def rope_table(positions, d_rope, *, theta=10000.0, scaling="none", factor=1.0, 
                torch.empty(shape, dtype=torch.float32, device=device))
     elif out[0].shape != shape or out[1].shape != shape:
         raise ValueError(f"out tables must be {list(shape)}")
-    cos, sin = (_dense(t, torch.float32, "table") for t in out)
+    dev = out[0].get_device()
+    cos, sin = (_dense(t, dev, torch.float32, "table") for t in out)
     a = _lib.RopeTableArgs(ctypes.sizeof(_lib.RopeTableArgs), positions, d_rope, ROPE_SCALING[scaling],
                            orig_positions, theta, factor, beta_fast, beta_slow, magnitude, cos, sin)
-    _launch("csa2_rope_table", ctypes.byref(a), out[0])
+    _launch("csa2_rope_table", ctypes.byref(a), dev)
     return out
 
 
@@ -502,8 +522,9 @@ def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=N
         out = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
-    if not x.is_cuda or not out.is_cuda:
-        raise ValueError("expected CUDA tensors")
+    dev = x.get_device()
+    _on_device(x, dev, "x")
+    _on_device(out, dev, "out")
     xt, xh, xc = x.stride()
     ot, oh, oc = out.stride()
     if (xc != 1 or oc != 1) and D > 1:
@@ -511,8 +532,8 @@ def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=N
     _launch("csa2_rope", _ROPE.pack(
         _ROPE.size, T, H, D, 2 * half, D - 2 * half if first is None else first, 1 if interleaved else 0,
         1 if inverse else 0, _float_type(x, "x"), x.data_ptr(), out.data_ptr(), xt, xh, ot, oh,
-        _dense(pos, torch.int32, "pos"), _dense(cos, torch.float32, "cos"), _dense(sin, torch.float32, "sin"),
-        positions), x)
+        _dense(pos, dev, torch.int32, "pos"), _dense(cos, dev, torch.float32, "cos"),
+        _dense(sin, dev, torch.float32, "sin"), positions), dev)
     return out
 
 
@@ -526,21 +547,23 @@ def fp4_quant(x, gscale=None, out=None):
         raise ValueError("give gscale with out, or out alone")
     elif out.codes.shape != (T, K // 2):
         raise ValueError("out must have x's shape")
-    xp, xs = _rows_of(x, "x")
-    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, xp, _float_type(x, "x"), xs, *out.fields()), x)
+    dev = x.get_device()
+    xp, xs = _rows_of(x, dev, "x")
+    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, xp, _float_type(x, "x"), xs, *out.fields(dev)), dev)
     return out
 
 
 def fp4_linear(x: Fp4Rows, w: Fp4Rows, *, out_dtype=torch.bfloat16, out=None):
     """The product of FP4 rows x [T, K] with FP4 weights w [N, K] (K % 32 == 0) on the
     block-scaled tensor cores.  Returns out [T, N] bf16 or float32."""
-    fx, fw = x.fields(), w.fields()
+    dev = x.codes.get_device()
+    fx, fw = x.fields(dev), w.fields(dev)
     if out is None:
         out = torch.empty((fx[3], fw[3]), dtype=out_dtype, device=x.codes.device)
     elif out.shape != (fx[3], fw[3]):
         raise ValueError(f"out must be [{fx[3]}, {fw[3]}]")
-    _launch("csa2_fp4_linear", _FP4_LINEAR.pack(_FP4_LINEAR.size, *fx, *fw, _dense(out, out.dtype, "out"),
-                                                _float_type(out, "out")), out)
+    _launch("csa2_fp4_linear", _FP4_LINEAR.pack(_FP4_LINEAR.size, *fx, *fw, _dense(out, dev, out.dtype, "out"),
+                                                _float_type(out, "out")), dev)
     return out
 
 
