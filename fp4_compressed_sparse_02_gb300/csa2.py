@@ -6,6 +6,7 @@ PyTorch provides device memory and the current stream; every computation runs in
 library's kernels.  Outputs are allocated here when the caller passes none (pass them
 in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
 """
+import contextlib
 import ctypes
 import math
 import struct
@@ -20,14 +21,28 @@ PAGE = 64
 BF16, F32, FP8E4M3, FP4E2M1X2 = 0, 1, 2, 3
 
 
-def _ptr(t: Optional[torch.Tensor]):
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError("expected a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+def _on_device(t, dev, name):
+    """Refuse a tensor that is not on CUDA device number dev."""
+    at = t.get_device()
+    if at < 0:
+        raise ValueError(f"{name}: expected a CUDA tensor")
+    if at != dev:
+        raise ValueError(f"{name}: on cuda:{at}, but the call's tensors are on cuda:{dev}")
+
+
+def _pointers(device):
+    """ptr(t): the address of a contiguous tensor on this device, None of None."""
+    dev = device.index
+
+    def ptr(t: Optional[torch.Tensor]):
+        if t is None:
+            return None
+        _on_device(t, dev, "operand")
+        if not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        return ctypes.c_void_p(t.data_ptr())
+
+    return ptr
 
 
 def _expect(t, dtypes, name):
@@ -43,6 +58,14 @@ _F32 = (torch.float32,)
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+_AS_IT_IS = contextlib.nullcontext()
+
+
+def _current(device):
+    """A context in which this CUDA device is the current one (see _launch)."""
+    return _AS_IT_IS if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
 
 @dataclass
@@ -98,16 +121,18 @@ class PagedCache:
             idx_k = torch.zeros((npg, PAGE, d_ik), dtype=torch.bfloat16, device=device)
         return PagedCache(codes, scales, idx_k, page_table, idx_k8, idx_k8_scale)
 
-    def c_struct(self):
+    def c_struct(self, ptr=None):
+        """The C struct; ptr as _pointers gives it (by default: every plane on the codes' device)."""
+        ptr = ptr or _pointers(self.codes.device)
         for t, n in [(self.codes, "codes"), (self.scales, "scales"), (self.idx_k8, "idx_k8")]:
             _expect(t, _U8, n)
         _expect(self.idx_k, _B16, "idx_k")
         _expect(self.idx_k8_scale, _F32, "idx_k8_scale")
         _expect(self.page_table, _I32, "page_table")
         fp8 = self.idx_k8 is not None
-        return _lib.Cache(_ptr(self.codes), _ptr(self.scales), _ptr(self.idx_k), _ptr(self.page_table),
+        return _lib.Cache(ptr(self.codes), ptr(self.scales), ptr(self.idx_k), ptr(self.page_table),
                           self.num_pages, PAGE, self.num_seqs, self.max_pages, self.d, self.d_ik,
-                          FP8E4M3 if fp8 else BF16, _ptr(self.idx_k8), _ptr(self.idx_k8_scale))
+                          FP8E4M3 if fp8 else BF16, ptr(self.idx_k8), ptr(self.idx_k8_scale))
 
 
 class Workspace:
@@ -140,9 +165,11 @@ def _ws(ws, device):
 def _call(fn, args, ws, device):
     L = _lib.lib()
     need = ctypes.c_size_t(0)
-    _lib.check(getattr(L, fn + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
-    buf = _ws(ws, device).get(need.value)
-    _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream()))
+    with _current(device):
+        _lib.check(getattr(L, fn + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+        buf = _ws(ws, device).get(need.value)
+        _on_device(buf, device.index, "ws")
+        _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream()))
 
 
 def compress_quant(cache: PagedCache, seq, entry, *, m=1, C=None, Z=None, H=None, W_kv=None, W_z=None,
@@ -161,16 +188,17 @@ def compress_quant(cache: PagedCache, seq, entry, *, m=1, C=None, Z=None, H=None
     for t, n in [(seq, "seq"), (entry, "entry"), (pos, "pos")]:
         _expect(t, _I32, n)
     d_rope = 0 if rope_cos is None else rope_cos.shape[1] * 2
+    ptr = _pointers(cache.codes.device)
     a = _lib.CompressArgs()
     a.struct_size = ctypes.sizeof(_lib.CompressArgs)
     a.T, a.m, a.d_model, a.h_dtype = T, m, d_model, h_dtype
-    a.H, a.W_kv, a.W_z, a.C, a.Z = _ptr(H), _ptr(W_kv), _ptr(W_z), _ptr(C), _ptr(Z)
+    a.H, a.W_kv, a.W_z, a.C, a.Z = ptr(H), ptr(W_kv), ptr(W_z), ptr(C), ptr(Z)
     a.d_rope = d_rope
     a.rope_max_pos = rope_cos.shape[0] if rope_cos is not None else 0
-    a.rope_cos, a.rope_sin, a.pos = _ptr(rope_cos), _ptr(rope_sin), _ptr(pos)
-    a.seq, a.entry, a.W_ik = _ptr(seq), _ptr(entry), _ptr(W_ik)
-    a.cache = cache.c_struct()
-    a.y_out = _ptr(y_out)
+    a.rope_cos, a.rope_sin, a.pos = ptr(rope_cos), ptr(rope_sin), ptr(pos)
+    a.seq, a.entry, a.W_ik = ptr(seq), ptr(entry), ptr(W_ik)
+    a.cache = cache.c_struct(ptr)
+    a.y_out = ptr(y_out)
     _call("csa2_compress_quant", a, ws, cache.codes.device)
 
 
@@ -185,17 +213,18 @@ def compress_append(cache: PagedCache, H, seq, tok_pos, W_kv, *, m=1, W_z=None, 
     _expect(pend, _F32, "pend")
     for t, n in [(seq, "seq"), (tok_pos, "tok_pos")]:
         _expect(t, _I32, n)
+    ptr = _pointers(cache.codes.device)
     a = _lib.AppendArgs()
     a.struct_size = ctypes.sizeof(_lib.AppendArgs)
     a.B, a.m, a.d_model = B, m, d_model
     a.h_dtype = F32 if H.dtype == torch.float32 else BF16
-    a.H, a.W_kv, a.W_z = _ptr(H), _ptr(W_kv), _ptr(W_z)
+    a.H, a.W_kv, a.W_z = ptr(H), ptr(W_kv), ptr(W_z)
     a.d_rope = 0 if rope_cos is None else rope_cos.shape[1] * 2
     a.rope_max_pos = rope_cos.shape[0] if rope_cos is not None else 0
-    a.rope_cos, a.rope_sin = _ptr(rope_cos), _ptr(rope_sin)
-    a.seq, a.tok_pos, a.pend, a.W_ik = _ptr(seq), _ptr(tok_pos), _ptr(pend), _ptr(W_ik)
-    a.cache = cache.c_struct()
-    a.y_out = _ptr(y_out)
+    a.rope_cos, a.rope_sin = ptr(rope_cos), ptr(rope_sin)
+    a.seq, a.tok_pos, a.pend, a.W_ik = ptr(seq), ptr(tok_pos), ptr(pend), ptr(W_ik)
+    a.cache = cache.c_struct(ptr)
+    a.y_out = ptr(y_out)
     _call("csa2_compress_append", a, ws, cache.codes.device)
 
 
@@ -216,14 +245,15 @@ def index_full(cache: PagedCache, q_idx, w, seq_of, n_vis, max_n, num_blocks=204
     pool, pool_len, topk, topk_len = out
     _expect(q_idx, _B16, "q_idx")
     _expect(w, _F32, "w")
+    ptr = _pointers(dev)
     a = _lib.IndexFullArgs()
     a.struct_size = ctypes.sizeof(_lib.IndexFullArgs)
     a.B, a.H_i = B, H_i
-    a.q_idx, a.w = _ptr(q_idx), _ptr(w)
-    a.cache = cache.c_struct()
-    a.seq_of, a.n_vis, a.max_n = _ptr(seq_of), _ptr(n_vis), int(max_n)
+    a.q_idx, a.w = ptr(q_idx), ptr(w)
+    a.cache = cache.c_struct(ptr)
+    a.seq_of, a.n_vis, a.max_n = ptr(seq_of), ptr(n_vis), int(max_n)
     a.num_blocks, a.per_block, a.k, a.relu = num_blocks, per_block, k, int(bool(relu))
-    a.pool, a.pool_len, a.topk, a.topk_len = _ptr(pool), _ptr(pool_len), _ptr(topk), _ptr(topk_len)
+    a.pool, a.pool_len, a.topk, a.topk_len = ptr(pool), ptr(pool_len), ptr(topk), ptr(topk_len)
     a.group = int(group)
     _call("csa2_index_full", a, ws, dev)
     return out
@@ -236,14 +266,15 @@ def index_reindex(cache: PagedCache, q_idx, w, seq_of, pool, pool_len, k=512, re
     if out is None:
         out = (torch.empty((B, k), dtype=torch.int32, device=dev), torch.empty(B, dtype=torch.int32, device=dev))
     topk, topk_len = out
+    ptr = _pointers(dev)
     a = _lib.IndexReindexArgs()
     a.struct_size = ctypes.sizeof(_lib.IndexReindexArgs)
     a.B, a.H_i = B, H_i
-    a.q_idx, a.w = _ptr(q_idx), _ptr(w)
-    a.cache = cache.c_struct()
-    a.seq_of, a.pool, a.pool_len, a.pool_stride = _ptr(seq_of), _ptr(pool), _ptr(pool_len), pool.shape[1]
+    a.q_idx, a.w = ptr(q_idx), ptr(w)
+    a.cache = cache.c_struct(ptr)
+    a.seq_of, a.pool, a.pool_len, a.pool_stride = ptr(seq_of), ptr(pool), ptr(pool_len), pool.shape[1]
     a.k, a.relu = k, int(bool(relu))
-    a.topk, a.topk_len = _ptr(topk), _ptr(topk_len)
+    a.topk, a.topk_len = ptr(topk), ptr(topk_len)
     _call("csa2_index_reindex", a, ws, dev)
     return out
 
@@ -263,18 +294,19 @@ def sparse_attn(cache: PagedCache, q, seq_of, topk, topk_len, swa, swa_scale, sw
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
     _expect(q, _B16, "q")
+    ptr = _pointers(dev)
     a = _lib.AttnArgs()
     a.struct_size = ctypes.sizeof(_lib.AttnArgs)
-    a.B, a.Hq, a.q = B, Hq, _ptr(q)
-    a.cache = cache.c_struct()
-    a.seq_of, a.topk, a.topk_len, a.k = _ptr(seq_of), _ptr(topk), _ptr(topk_len), topk.shape[1]
-    a.swa, a.swa_scale = _ptr(swa), _ptr(swa_scale)
+    a.B, a.Hq, a.q = B, Hq, ptr(q)
+    a.cache = cache.c_struct(ptr)
+    a.seq_of, a.topk, a.topk_len, a.k = ptr(seq_of), ptr(topk), ptr(topk_len), topk.shape[1]
+    a.swa, a.swa_scale = ptr(swa), ptr(swa_scale)
     a.swa_rows = swa.shape[0] if swa is not None else 0
-    a.swa_start, a.swa_len, a.swa_max = _ptr(swa_start), _ptr(swa_len), int(swa_max)
+    a.swa_start, a.swa_len, a.swa_max = ptr(swa_start), ptr(swa_len), int(swa_max)
     a.softmax_scale = float(softmax_scale)
-    a.out = _ptr(out)
+    a.out = ptr(out)
     a.out_dtype = F32 if out.dtype == torch.float32 else BF16
-    a.lse = _ptr(lse)
+    a.lse = ptr(lse)
     a.inputs_ready = int(bool(inputs_ready))
     _call("csa2_sparse_attn", a, ws, dev)
     return out, lse
@@ -289,13 +321,15 @@ def swa_quant(x, swa, swa_scale, row_idx=None):
     _expect(swa, _U8, "swa")
     _expect(swa_scale, _F32, "swa_scale")
     _expect(row_idx, _I32, "row_idx")
+    ptr = _pointers(x.device)
     a = _lib.SwaQuantArgs()
     a.struct_size = ctypes.sizeof(_lib.SwaQuantArgs)
     a.R, a.d = R, d
     a.x_dtype = F32 if x.dtype == torch.float32 else BF16
-    a.x, a.row_idx, a.swa, a.swa_scale = _ptr(x), _ptr(row_idx), _ptr(swa), _ptr(swa_scale)
+    a.x, a.row_idx, a.swa, a.swa_scale = ptr(x), ptr(row_idx), ptr(swa), ptr(swa_scale)
     a.swa_rows = swa.shape[0]
-    _lib.check(_lib.lib().csa2_swa_quant(ctypes.byref(a), _stream()))
+    with _current(x.device):
+        _lib.check(_lib.lib().csa2_swa_quant(ctypes.byref(a), _stream()))
 
 
 _FLOAT = {torch.bfloat16: BF16, torch.float32: F32}
@@ -306,15 +340,6 @@ def _float_type(t, name):
     if k is None:
         raise TypeError(f"{name}: dtype {t.dtype} is neither bfloat16 nor float32")
     return k
-
-
-def _on_device(t, dev, name):
-    """Refuse a tensor that is not on CUDA device number dev."""
-    at = t.get_device()
-    if at < 0:
-        raise ValueError(f"{name}: expected a CUDA tensor")
-    if at != dev:
-        raise ValueError(f"{name}: on cuda:{at}, but the call's tensors are on cuda:{dev}")
 
 
 def _rows_of(t, dev, name):

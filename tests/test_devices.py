@@ -105,6 +105,42 @@ def run(call, dev, moved=None):
                 lambda name, r, c: fp4(at(name), r, c, at(name + ".gscale") if moved != name else None))
 
 
+def cache(t):
+    return csa2.PagedCache(t("codes", U8, 3, 64, 64), t("scales", U8, 3, 64, 8), t("idx_k", B16, 3, 64, 64),
+                           t("page_table", I32, 2, 2))
+
+
+HOT = {
+    "compress_quant": (lambda t, q: csa2.compress_quant(
+        cache(t), t("seq", I32, 4), t("entry", I32, 4), H=t("H", B16, 4, 256), W_kv=t("W_kv", B16, 256, 128), pos=t("pos", I32, 4),
+        rope_cos=t("rope_cos", F32, 9, 16), rope_sin=t("rope_sin", F32, 9, 16), W_ik=t("W_ik", B16, 128, 64), ws=ws(t)),
+        ["seq", "entry", "H", "W_kv", "pos", "rope_cos", "rope_sin", "W_ik"]),
+    "compress_append": (lambda t, q: csa2.compress_append(
+        cache(t), t("H", B16, 2, 256), t("seq", I32, 2), t("tok_pos", I32, 2), t("W_kv", B16, 256, 128), ws=ws(t)),
+        ["H", "seq", "tok_pos", "W_kv"]),
+    "index_full": (lambda t, q: csa2.index_full(
+        cache(t), t("q_idx", B16, 2, 4, 64), t("w", F32, 2, 4), t("seq_of", I32, 2), t("n_vis", I32, 2), 100, 64, 8, 16,
+        out=(t("pool", I32, 2, 512), t("pool_len", I32, 2), t("topk", I32, 2, 16), t("topk_len", I32, 2)), ws=ws(t)),
+        ["q_idx", "w", "seq_of", "n_vis", "pool", "topk_len"]),
+    "index_reindex": (lambda t, q: csa2.index_reindex(
+        cache(t), t("q_idx", B16, 2, 4, 64), t("w", F32, 2, 4), t("seq_of", I32, 2), t("pool", I32, 2, 512), t("pool_len", I32, 2), 16,
+        out=(t("topk", I32, 2, 16), t("topk_len", I32, 2)), ws=ws(t)), ["q_idx", "pool", "topk"]),
+    "sparse_attn": (lambda t, q: csa2.sparse_attn(
+        cache(t), t("q", B16, 2, 8, 128), t("seq_of", I32, 2), t("topk", I32, 2, 16), t("topk_len", I32, 2), t("swa", U8, 64, 128),
+        t("swa_scale", F32, 64), t("swa_start", I32, 2), t("swa_len", I32, 2), 32, out=t("out", B16, 2, 8, 128),
+        lse=t("lse", F32, 2, 8), ws=ws(t)), ["q", "seq_of", "topk", "swa", "swa_scale", "out", "lse"]),
+    "swa_quant": (lambda t, q: csa2.swa_quant(t("x", B16, 4, 128), t("swa", U8, 64, 128), t("swa_scale", F32, 64), t("row_idx", I32, 4)),
+                  ["x", "swa", "swa_scale", "row_idx"]),
+}
+PLANES = ["codes", "scales", "idx_k", "page_table", "workspace"]
+
+
+def ws(t):
+    w = csa2.Workspace("cpu")
+    w.get = lambda nbytes: t("workspace", U8, 256)
+    return w
+
+
 @pytest.mark.parametrize("dev", [0, 1])
 @pytest.mark.parametrize("name", ROWS)
 def test_row_operators_run_on_their_tensors_device(machine, name, dev):
@@ -117,4 +153,20 @@ def test_row_operators_run_on_their_tensors_device(machine, name, dev):
 def test_row_operators_refuse_operands_of_another_device(machine, name, moved):
     with pytest.raises(ValueError, match="cuda:1"):
         run(ROWS[name], 0, moved)
+    assert machine == []
+
+
+@pytest.mark.parametrize("dev", [0, 1])
+@pytest.mark.parametrize("name", HOT)
+def test_hot_path_runs_on_its_tensors_device(machine, name, dev):
+    run(HOT[name][0], dev)
+    assert [(d, s) for _, d, s in machine] == [(dev, 100 + dev)]
+    assert torch._C._cuda_getDevice() == 0
+
+
+@pytest.mark.parametrize("name,moved", [(n, o) for n, (_, named) in HOT.items()
+                                        for o in named + (PLANES if n != "swa_quant" else [])])
+def test_hot_path_refuses_operands_of_another_device(machine, name, moved):
+    with pytest.raises(ValueError, match="cuda:1"):
+        run(HOT[name][0], 0, moved)
     assert machine == []
