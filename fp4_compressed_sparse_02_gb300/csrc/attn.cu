@@ -1100,12 +1100,9 @@ size_t attn_workspace_bytes(const csa2_attn_args& a) {
 template <int DIM, int MT>
 static cudaError_t run_attn(const csa2_attn_args& a, AttnParams& ap, cudaStream_t st) {
   using C = ACfg<DIM, MT>;
-  static bool attr_set = false;   // per instantiation; harmless to repeat
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_chunk<DIM, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;         // per instantiation
+  const cudaError_t e = limit.raise(k_attn_chunk<DIM, MT>, C::SMEM);
+  if (e != cudaSuccess) return e;
   dim3 grid(ap.nchunk, a.B);
   launch_k(k_attn_chunk<DIM, MT>, grid, ATHREADS, C::SMEM, st, ap);
   launch_k(k_combine<DIM>, dim3(a.B, a.Hq), DIM / 4, 0, st, ap.opart, ap.ml, a.Hq, ap.nchunk, a.out,
@@ -1114,12 +1111,9 @@ static cudaError_t run_attn(const csa2_attn_args& a, AttnParams& ap, cudaStream_
 }
 
 static cudaError_t run_attn_tc(const csa2_attn_args& a, AttnParams& ap, cudaStream_t st) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_attn_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, tca::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(k_attn_tc, tca::SMEM);
+  if (e != cudaSuccess) return e;
   ap.nchunk = tca::NCH;
   CUtensorMap qmap, cmap, smap, wmap;            // q as [B * 64 heads][512] bf16, 64 heads x 64 dims boxes;
                                                 // code / scale rows (one-row boxes, gathered 4 at a time);

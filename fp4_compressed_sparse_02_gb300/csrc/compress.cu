@@ -571,12 +571,9 @@ __global__ void __launch_bounds__(256) k_append_quant_index_k(AppendParams ap, c
 template <int E, int DIK>
 static cudaError_t launch_index_k(const csa2_compress_args& a, int G, cudaStream_t st) {
   const size_t sm = ((size_t)E * a.cache.d + 8 * E * DIK) * sizeof(float);
-  static size_t attr_bytes = 0;                 // opt-in above 48 KB, raised when needed
-  if (sm > attr_bytes) {
-    cudaError_t e = cudaFuncSetAttribute(k_index_k<E, DIK>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
-    if (e != cudaSuccess) return e;
-    attr_bytes = sm;
-  }
+  static SmemLimit limit;                       // opt-in above 48 KB, raised when needed
+  const cudaError_t e = limit.raise(k_index_k<E, DIK>, sm);
+  if (e != cudaSuccess) return e;
   return launch_k(k_index_k<E, DIK>, (G + E - 1) / E, 256, sm, st, a.cache, a.seq, a.entry, G, a.W_ik);
 }
 
@@ -646,7 +643,8 @@ static cudaError_t project_rows(const csa2_compress_args& a, float* out, cudaStr
     s = mma_splits(a.d_model, N);
     const int ks = a.d_model / s;
     const size_t sm = (size_t)64 * (ks * 2 + 16) + (size_t)ks * 144;
-    cudaError_t e = cudaFuncSetAttribute(k_project_mma, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+    static SmemLimit limit;
+    cudaError_t e = limit.raise(k_project_mma, sm);
     if (e != cudaSuccess) return e;
     launch_k(k_project_mma, dim3(N / 64, s), 128, sm, st, static_cast<const uint16_t*>(a.H), a.W_kv, a.W_z, out, a.T,
                                                     a.d_model, d, N, ks);
@@ -656,12 +654,14 @@ static cudaError_t project_rows(const csa2_compress_args& a, float* out, cudaStr
     const size_t sm = (size_t)ks * (128 + 4 * a.T);
     cudaError_t e;
     if (a.h_dtype == CSA2_F32) {
-      e = cudaFuncSetAttribute(k_project_small<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+      static SmemLimit limit;
+      e = limit.raise(k_project_small<float>, sm);
       if (e != cudaSuccess) return e;
       launch_k(k_project_small<float>, dim3(N / 64, s), 256, sm, st, static_cast<const float*>(a.H), a.W_kv, a.W_z,
                                                                out, a.T, a.d_model, d, N, ks);
     } else {
-      e = cudaFuncSetAttribute(k_project_small<uint16_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm);
+      static SmemLimit limit;
+      e = limit.raise(k_project_small<uint16_t>, sm);
       if (e != cudaSuccess) return e;
       launch_k(k_project_small<uint16_t>, dim3(N / 64, s), 256, sm, st, static_cast<const uint16_t*>(a.H), a.W_kv,
                                                                   a.W_z, out, a.T, a.d_model, d, N, ks);

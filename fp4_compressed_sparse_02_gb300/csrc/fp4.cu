@@ -967,15 +967,10 @@ bool groups_of_four(const csa2_fp4_linear_args& a) {
   return a.w.rows % 4 == 0 && ((uintptr_t)a.out & (a.out_dtype == CSA2_F32 ? 15 : 7)) == 0;
 }
 
-int sm_count() {
-  static int sms = 0;
-  if (!sms) {
-    int dev = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  }
-  return sms;
-}
+// How many clusters of s units, s = 1 .. 8 at most, the GPU holds at once.
+struct Clusters {
+  int of[9];
+};
 
 // How many clusters of `cta` CTAs of a kernel the GPU holds at once.
 template <typename K>
@@ -1058,13 +1053,17 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   const long long ntile = (long long)p.nft * p.ntt;
   if (ntile > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   p.vec4 = groups_of_four(a);
-  static int pairs_at[5] = {0};                           // clusters of s pairs the GPU holds at once
-  if (!pairs_at[1]) {
-    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_pair<TMA_OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-    if (e != cudaSuccess) return e;
-    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_pair<TMA_OUT>, 2 * s, THREADS, SMEM);
-    if (!pairs_at[1]) return cudaErrorInvalidConfiguration;
-  }
+  static SmemLimit limit;
+  static PerDevice<Clusters> resident;
+  cudaError_t e = limit.raise(k_fp4_linear_pair<TMA_OUT>, SMEM);
+  if (e != cudaSuccess) return e;
+  const Clusters* clusters_of = nullptr;
+  e = resident.get(&clusters_of, [](Clusters& c) {
+    for (int s = 4; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear_pair<TMA_OUT>, 2 * s, THREADS, SMEM);
+    return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
+  if (e != cudaSuccess) return e;
+  const int* pairs_at = clusters_of->of;                  // clusters of s pairs
   // few tiles: split the sum as far as every cluster still runs at once, two stages a CTA or more
   const int nkb = (p.nkt + 3) / 4;
   const auto split_of = [&](long long tiles) {
@@ -1097,7 +1096,7 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   const long long rest = ntile % pairs_at[1];
   const int split = split_of(rest);
   if (ntile > pairs_at[1] && rest > 0 && split > 1 && nkb - nkb / split >= 32) {
-    const cudaError_t e = launch(0, ntile - rest, 1);
+    e = launch(0, ntile - rest, 1);
     return e != cudaSuccess ? e : launch(ntile - rest, rest, split);
   }
   return launch(0, ntile, split_of(ntile));
@@ -1114,13 +1113,17 @@ cudaError_t launch_linear_few(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out, p.out32 = a.out_dtype == CSA2_F32, p.vec4 = groups_of_four(a);
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64;
   const int tiles = (p.N + 2 * BM - 1) / (2 * BM), nkb = (p.nkt + 3) / 4;
-  static int pairs_at[5] = {0};                           // clusters of s pairs the GPU holds at once
-  if (!pairs_at[1]) {
-    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_few<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<BN>::SMEM);
-    if (e != cudaSuccess) return e;
-    for (int s = 4; s >= 1; --s) pairs_at[s] = resident_clusters(k_fp4_linear_few<BN>, 2 * s, THREADS, Few<BN>::SMEM);
-    if (!pairs_at[1]) return cudaErrorInvalidConfiguration;
-  }
+  static SmemLimit limit;
+  static PerDevice<Clusters> resident;
+  cudaError_t e = limit.raise(k_fp4_linear_few<BN>, Few<BN>::SMEM);
+  if (e != cudaSuccess) return e;
+  const Clusters* clusters_of = nullptr;
+  e = resident.get(&clusters_of, [](Clusters& c) {
+    for (int s = 4; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear_few<BN>, 2 * s, THREADS, Few<BN>::SMEM);
+    return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
+  if (e != cudaSuccess) return e;
+  const int* pairs_at = clusters_of->of;                  // clusters of s pairs
   p.split = 1;
   for (int s = 2; s <= 4; ++s)
     if (tiles <= pairs_at[s] && 2 * s <= nkb) p.split = s;
@@ -1153,14 +1156,18 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.vec4 = groups_of_four(a);
   const int ft = (p.N + lin::BM - 1) / lin::BM, tt = (p.T + BN - 1) / BN, nkb = (p.nkt + 3) / 4;
   const long long tiles = (long long)ft * tt;
-  static int one[9] = {0};                                // clusters of s CTAs that the GPU holds at once, a CTA an SM
-  const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
-  if (!one[1]) {
-    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    if (e != cudaSuccess) return e;
-    for (int s = 8; s >= 1; --s) one[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
-    if (!one[1]) return cudaErrorInvalidConfiguration;
-  }
+  static SmemLimit limit;
+  static PerDevice<Clusters> resident;
+  cudaError_t e = limit.raise(k_fp4_linear<BN>, C::SMEM);
+  if (e != cudaSuccess) return e;
+  const Clusters* clusters_of = nullptr;
+  e = resident.get(&clusters_of, [](Clusters& c) {
+    const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
+    for (int s = 8; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
+    return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
+  });
+  if (e != cudaSuccess) return e;
+  const int* one = clusters_of->of;                       // clusters of s CTAs that the GPU holds at once, a CTA an SM
   // Few tiles (under three quarters of the SMs): split the sum where the stages saved are worth adding the
   // parts.  Costs in stages, fitted to 148 sizes: clusters that do not all fit on SMs of their own share some, whose
   // stages take 1.65 times as long together; adding costs what a tile of 128 tokens writes and reads, less for fewer.
@@ -1204,7 +1211,10 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
 
 cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (a.x.rows == 0 || a.w.rows == 0) return cudaSuccess;
-  const int T = a.x.rows, sms = sm_count(), nkb = (a.x.cols + 255) / 256, ft = (a.w.rows + 127) / 128;
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const int T = a.x.rows, nkb = (a.x.cols + 255) / 256, ft = (a.w.rows + 127) / 128;
   if (T <= 16) return launch_linear<16>(a, st);
   if (T <= 32) return launch_linear<32>(a, st);
   // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs): what a

@@ -1222,12 +1222,9 @@ static cudaError_t launch_scan_short(const ScanParams& sp, cudaStream_t st) {
   constexpr int SEG = 32;
   auto kernel = k_full_scan_short<128, true, SEG>;
   constexpr size_t smem = ss_smem(SEG);
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(kernel, smem);
+  if (e != cudaSuccess) return e;
   int dev = 0, sms = 0, per_sm = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -1361,12 +1358,9 @@ cudaError_t launch_index_full(const csa2_index_full_args& a, void* ws, cudaStrea
   sel.topk = a.topk;
   sel.topk_len = a.topk_len;
   if (a.B >= 256) {                                // many queries: a CTA each, no cluster barriers
-    static bool attr_set = false;
-    if (!attr_set) {
-      cudaError_t e = cudaFuncSetAttribute(k_select_cta, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C1_SMEM);
-      if (e != cudaSuccess) return e;
-      attr_set = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(k_select_cta, C1_SMEM);
+    if (e != cudaSuccess) return e;
     launch_k(k_select_cta, a.B, C1_THREADS, C1_SMEM, st, sel);
   } else {
     PoolScoreParams none{};

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "csa2.h"
+#include "per_device.h"
 
 namespace csa2 {
 

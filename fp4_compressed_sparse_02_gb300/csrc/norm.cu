@@ -509,29 +509,31 @@ __global__ void __launch_bounds__(THREADS) k_rms_norm_any(NormParams p) {
 
 namespace {
 
-// A persistent grid: as many CTAs as the GPU holds at once (looked up once for a kernel and shape).
+// A persistent grid: as many CTAs as the GPU holds at once (looked up once for a kernel, shape and device).
 template <typename K>
-cudaError_t launch_rows(K* kernel, int& resident, const NormParams& p, int rows, int threads, bool tail, cudaStream_t st) {
-  if (!resident) {
-    int dev = 0, sms = 0, per = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
-    if (e != cudaSuccess) return e;
-    resident = sms * (per > 0 ? per : 1);
-  }
+cudaError_t launch_rows(K* kernel, PerDevice<int>& resident, const NormParams& p, int rows, int threads, bool tail,
+                        cudaStream_t st) {
+  const int* most = nullptr;
+  const cudaError_t e = resident.get(&most, [&](int& n) {
+    int sms = 0, per = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, kernel, threads, 0);
+    n = sms * (per > 0 ? per : 1);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
   const long long blocks = ((long long)p.T + rows - 1) / rows;
-  return launch_k(kernel, (unsigned)(blocks < resident ? blocks : resident) + (tail ? 1u : 0u), threads, 0, st, p);
+  return launch_k(kernel, (unsigned)(blocks < *most ? blocks : *most) + (tail ? 1u : 0u), threads, 0, st, p);
 }
 
 template <int OUT, bool X32, int RES>
 cudaError_t launch_aligned(const NormParams& p, cudaStream_t st) {
   const bool tail = OUT == CSA2_FP4E2M1X2 && p.T % 128;
   if (p.D <= 512) {
-    static int resident = 0;
+    static PerDevice<int> resident;
     return launch_rows(k_rms_norm_small<OUT, X32, RES>, resident, p, 256 / p.lanes, 256, tail, st);
   }
-  static int resident[17] = {0};                          // by warps of a CTA
+  static PerDevice<int> resident[17];                     // by warps of a CTA
   const int threads = (p.D / 16 + 31) & ~31;
   return launch_rows(k_rms_norm<OUT, X32, RES>, resident[threads / 32], p, 1, threads, tail, st);
 }
@@ -541,12 +543,10 @@ cudaError_t launch_any(const NormParams& p, cudaStream_t st) {
   constexpr bool quantised = OUT == CSA2_FP8E4M3 || OUT == CSA2_FP4E2M1X2, warp = THREADS == 32 * kAnyRows;
   const int threads = warp ? THREADS : ((p.D + N - 1) / N + 31) & ~31;
   const size_t smem = quantised ? (size_t)((p.D + 15) / 16) * 17 * 4 * (warp ? kAnyRows : 1) : 0;
-  static bool attr_set = false;
-  if (quantised && !warp && !attr_set) {
-    cudaError_t e =
-        cudaFuncSetAttribute(k_rms_norm_any<OUT, N, THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize, 2048 * 17 * 4);
+  if (quantised && !warp) {
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(k_rms_norm_any<OUT, N, THREADS>, 2048 * 17 * 4);
     if (e != cudaSuccess) return e;
-    attr_set = true;
   }
   const unsigned blocks = warp ? (unsigned)(((long long)p.T + kAnyRows - 1) / kAnyRows) : (unsigned)p.T;
   const bool tail = OUT == CSA2_FP4E2M1X2 && p.T % 128;

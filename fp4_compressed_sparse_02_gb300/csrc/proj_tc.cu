@@ -446,12 +446,9 @@ bool index_k_tc_supported(const csa2_compress_args& a, int G) {
 }
 
 cudaError_t launch_index_k_tc(const csa2_compress_args& a, int G, cudaStream_t st) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_index_k_tc, cudaFuncAttributeMaxDynamicSharedMemorySize, iktc::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(k_index_k_tc, iktc::SMEM);
+  if (e != cudaSuccess) return e;
   return launch_k(k_index_k_tc, (G + iktc::M - 1) / iktc::M, iktc::THREADS, iktc::SMEM, st, a.cache, a.seq, a.entry,
                   G, a.W_ik);
 }
@@ -497,21 +494,15 @@ cudaError_t launch_project_tc(const csa2_compress_args& a, float* out, bool fuse
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   const dim3 grid((unsigned)(ntiles < sms ? ntiles : (sms > 0 ? sms : 1)));   // persistent: one CTA per SM
   if (fuse) {
-    static bool attr_set = false;
-    if (!attr_set) {
-      cudaError_t e = cudaFuncSetAttribute(k_proj_tc<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, ptc::SMEM);
-      if (e != cudaSuccess) return e;
-      attr_set = true;
-    }
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(k_proj_tc<true>, ptc::SMEM);
+    if (e != cudaSuccess) return e;
     return launch_k_late(k_proj_tc<true>, grid, ptc::THREADS, ptc::SMEM, st, mh, mkv, mz, out, a.T, a.d_model, d,
                          N, ntn, ntiles, ep);
   }
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_proj_tc<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, ptc::SMEM);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(k_proj_tc<false>, ptc::SMEM);
+  if (e != cudaSuccess) return e;
   // persistent (one CTA per SM): started only once the previous kernel has completed
   return launch_k_late(k_proj_tc<false>, grid, ptc::THREADS, ptc::SMEM, st, mh, mkv, mz, out, a.T, a.d_model, d, N,
                        ntn, ntiles, ep);

@@ -142,16 +142,17 @@ cudaError_t launch_rope_v(const csa2_rope_args& a, RopeParams p, cudaStream_t st
   p.turn_units = a.interleaved ? (V > 1 ? a.d_rope / V : a.d_rope / 2) : a.d_rope / 2 / V;
   p.units = p.turn_units + (in_place ? 0 : (a.D - a.d_rope) / V);
   const auto k = a.interleaved ? k_rope<T, V, true> : k_rope<T, V, false>;
-  static int resident[2] = {0};                           // CTAs the GPU holds at once
-  int& r = resident[a.interleaved != 0];
-  if (!r) {
-    int dev = 0, sms = 0, per = 0;
-    cudaGetDevice(&dev);
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kThreads, 0);
-    if (e != cudaSuccess) return e;
-    r = sms * (per > 0 ? per : 1);
-  }
+  static PerDevice<int> resident[2];                      // CTAs the GPU holds at once
+  const int* most = nullptr;
+  const cudaError_t e = resident[a.interleaved != 0].get(&most, [&](int& n) {
+    int sms = 0, per = 0;
+    cudaError_t e = sm_count(&sms);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per, k, kThreads, 0);
+    n = sms * (per > 0 ? per : 1);
+    return e;
+  });
+  if (e != cudaSuccess) return e;
+  const int r = *most;
   const int tx = p.units < kThreads ? p.units : kThreads;
   const int ty = kThreads / tx < a.H ? kThreads / tx : a.H;
   const int per = (a.H + ty - 1) / ty;                    // CTAs that give each thread one head
@@ -300,9 +301,9 @@ cudaError_t launch_rope_table(const csa2_rope_table_args& a, cudaStream_t st) {
   }
   const bool vec = t.half % 4 == 0 && ((uintptr_t)t.cos & 15) == 0 && ((uintptr_t)t.sin & 15) == 0;
   const int slots = 256 / (vec ? t.half / 4 : t.half);    // half <= 128
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
   const int blocks = (t.positions + slots - 1) / slots, most = 8 * sms;
   return vec ? launch_k(k_rope_table<4>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t)
              : launch_k(k_rope_table<1>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t);

@@ -499,12 +499,9 @@ size_t full_scores_tc_bytes(const csa2_index_full_args& a) {
 template <int HI>
 static cudaError_t launch_score(const CUtensorMap& kmap, const CUtensorMap& qmap, const ScoreParams& p, int smem,
                                 int sms, cudaStream_t st) {
-  static bool attr_set = false;
-  if (!attr_set) {
-    cudaError_t e = cudaFuncSetAttribute(k_score_tc<HI>, cudaFuncAttributeMaxDynamicSharedMemorySize, stc::SMEM_MAX);
-    if (e != cudaSuccess) return e;
-    attr_set = true;
-  }
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(k_score_tc<HI>, stc::SMEM_MAX);
+  if (e != cudaSuccess) return e;
   const int grid = std::max(1, std::min(p.units, sms));
   // persistent (one CTA per SM): started only once the previous kernel has completed
   return launch_k_late(k_score_tc<HI>, grid, stc::THREADS, smem, st, kmap, qmap, p);

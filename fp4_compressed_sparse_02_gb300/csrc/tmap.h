@@ -6,18 +6,21 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 namespace csa2 {
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
-  if (!encode) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> encode{nullptr};   // the same function for every thread and device
+  PFN_cuTensorMapEncodeTiled_v12000 found = encode.load(std::memory_order_relaxed);
+  if (!found) {
     cudaDriverEntryPointQueryResult q;
     void* fn = nullptr;
     if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
         q == cudaDriverEntryPointSuccess)
-      encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+      encode.store(found = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn), std::memory_order_relaxed);
   }
-  return encode;
+  return found;
 }
 
 // bf16 matrix [rows][cols] (row stride `cols` elements), boxes of box_rows x 64 columns,
