@@ -570,7 +570,7 @@ def fp4_quant(x, gscale=None, out=None):
         out = Fp4Rows.allocate(T, K, x.device, gscale)
     elif gscale is not None:
         raise ValueError("give gscale with out, or out alone")
-    elif out.codes.shape != (T, K // 2):
+    elif (out.rows, out.cols) != (T, K):
         raise ValueError("out must have x's shape")
     dev = x.get_device()
     xp, xs = _rows_of(x, dev, "x")
