@@ -204,11 +204,13 @@ csa2_status check_swa_quant(const csa2_swa_quant_args* a) {
 bool is_float(csa2_dtype t) { return t == CSA2_BF16 || t == CSA2_F32; }
 bool on(const void* p, csa2_dtype t) { return ((uintptr_t)p & (t == CSA2_F32 ? 3 : 1)) == 0; }
 
-csa2_status check_fp4_rows(const csa2_fp4_rows& m, const char* name, int multiple) {
+// most: what the kernels' 32-bit offsets reach, with the whole steps they round cols up to, or less
+csa2_status check_fp4_rows(const csa2_fp4_rows& m, const char* name, int multiple, int most) {
   REQUIRE(m.rows >= 0 && m.rows <= (1 << 23), CSA2_ERR_UNSUPPORTED_SHAPE, "%s.rows must be in 0..2^23 (got %d)", name,
           m.rows);
   REQUIRE(m.cols > 0 && m.cols % multiple == 0, CSA2_ERR_UNSUPPORTED_SHAPE,
           "%s.cols must be a positive multiple of %d (got %d)", name, multiple, m.cols);
+  REQUIRE(m.cols <= most, CSA2_ERR_UNSUPPORTED_SHAPE, "%s.cols must be at most %d (got %d)", name, most, m.cols);
   if (m.rows > 0) {
     REQUIRE(m.codes && m.scales, CSA2_ERR_INVALID_ARG, "%s.codes/scales is NULL", name);
     REQUIRE(((uintptr_t)m.codes & 15) == 0 && ((uintptr_t)m.scales & 15) == 0, CSA2_ERR_INVALID_ARG,
@@ -233,7 +235,7 @@ csa2_status check_rms_norm(const csa2_rms_norm_args* a) {
             "scale_group must be 0 or 128 (got %d)", a->scale_group);
   if (a->out_form == CSA2_FP4E2M1X2) {
     REQUIRE(a->out4.rows == a->T && a->out4.cols == a->D, CSA2_ERR_INVALID_ARG, "out4 must be [T][D]");
-    csa2_status s = check_fp4_rows(a->out4, "out4", 16);
+    csa2_status s = check_fp4_rows(a->out4, "out4", 16, 1 << 30);
     if (s != CSA2_OK) return s;
   }
   if (a->T > 0) {
@@ -313,19 +315,21 @@ csa2_status check_fp4_quant(const csa2_fp4_quant_args* a) {
   REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
   REQUIRE(a->struct_size == sizeof(csa2_fp4_quant_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
   REQUIRE(is_float(a->x_dtype), CSA2_ERR_INVALID_ARG, "bad x_dtype");
-  csa2_status s = check_fp4_rows(a->out, "out", 16);
+  csa2_status s = check_fp4_rows(a->out, "out", 16, 1 << 30);
   if (s != CSA2_OK) return s;
   if (a->out.rows > 0)
     REQUIRE(a->x && on(a->x, a->x_dtype), CSA2_ERR_INVALID_ARG, "x is NULL or not aligned to its type");
   return CSA2_OK;
 }
 
+constexpr int kMaxSum = 1 << 26;   // a sum this long ends in a small part of the time that the product's waits allow
+
 csa2_status check_fp4_linear(const csa2_fp4_linear_args* a) {
   REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
   REQUIRE(a->struct_size == sizeof(csa2_fp4_linear_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
-  csa2_status s = check_fp4_rows(a->x, "x", 32);
+  csa2_status s = check_fp4_rows(a->x, "x", 32, kMaxSum);
   if (s != CSA2_OK) return s;
-  s = check_fp4_rows(a->w, "w", 32);
+  s = check_fp4_rows(a->w, "w", 32, kMaxSum);
   if (s != CSA2_OK) return s;
   REQUIRE(a->x.cols == a->w.cols, CSA2_ERR_INVALID_ARG, "x.cols (%d) != w.cols (%d)", a->x.cols, a->w.cols);
   REQUIRE(is_float(a->out_dtype), CSA2_ERR_INVALID_ARG, "bad out_dtype");

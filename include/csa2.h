@@ -422,7 +422,8 @@ csa2_status csa2_swa_quant(const csa2_swa_quant_args* args, void* stream);
  *           order in which the block-scaled tensor-core product reads them.  Scales of
  *           columns past cols must be 0 (csa2_fp4_quant and csa2_rms_norm write 0 there and
  *           for the rows past the last).
- * cols is a multiple of 16 (of 32 for csa2_fp4_linear).  codes and scales 16-byte aligned.
+ * cols is a multiple of 16, at most 2^30 (of 32, at most 2^26, for csa2_fp4_linear); rows at most
+ * 2^23.  codes and scales 16-byte aligned.
  * The cache's planes (csa2_cache) hold the same codes and scales row by row instead: there
  * an entry is read by gathering single rows.
  * -------------------------------------------------------------------------- */
@@ -576,7 +577,7 @@ csa2_status csa2_fp4_quant(const csa2_fp4_quant_args* args, void* stream);
  * Products and block scales are exact; the sum runs in the tensor core's float32 accumulators
  * (and, where the sum is split over CTAs, in a fixed order: results repeat bit for bit);
  * one rounding to out_dtype.  A NaN scale byte (0x7F / 0xFF) makes its row's results NaN.
- * Supported: x.cols == w.cols, a positive multiple of 32.  x.rows and w.rows >= 0.
+ * Supported: x.cols == w.cols, a positive multiple of 32 up to 2^26.  x.rows and w.rows in 0..2^23.
  * Needs no workspace.
  * -------------------------------------------------------------------------- */
 typedef struct csa2_fp4_linear_args {
