@@ -531,7 +531,7 @@ csa2_status csa2_rope(const csa2_rope_args* args, void* stream);
  *                     take f_i / factor, a linear ramp over i joins the two ("YaRN", Peng
  *                     et al. 2023, equations 17-23, with the ramp over the channel index)
  * The angle is held as a 64-bit fraction of a turn, so that a far position loses nothing:
- * |error| <= 2.5 * 2^-24 * magnitude.
+ * |error| <= 2 * 2^-24 * magnitude, most of it the rounding of the result.
  * Supported: even d_rope in 2..256, positions <= 2^24, theta > 1, factor >= 1,
  * 0 < beta_slow < beta_fast.  Needs no workspace.
  * -------------------------------------------------------------------------- */
