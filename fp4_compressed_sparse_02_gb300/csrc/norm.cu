@@ -26,10 +26,11 @@ struct NormParams {
 };
 
 // (hi, lo) += (b, blo) in two float32 words: the rounding error of the sum goes into lo (Knuth's
-// TwoSum).
+// TwoSum).  The low words are added first, so that the sum is the same with its operands exchanged: two lanes that
+// add each other's words get the same pair.
 __device__ __forceinline__ void sum2(float& hi, float& lo, float b, float blo) {
   const float s = __fadd_rn(hi, b), t = __fsub_rn(s, hi);
-  lo += __fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b, t)) + blo;
+  lo = __fadd_rn(__fadd_rn(__fsub_rn(hi, __fsub_rn(s, t)), __fsub_rn(b, t)), __fadd_rn(lo, blo));
   hi = s;
 }
 __device__ __forceinline__ void lanes_sum2(float& hi, float& lo, int lanes) {
@@ -169,9 +170,11 @@ __device__ __forceinline__ void zero_tail(const NormParams& p) {
 
 }  // namespace
 
-// The two kernels below keep the sum of squares in two float32 words.  The mean then differs from the
-// exact one by 2^-46, and the float32 it rounds to, and with it every 4- or 8-bit code, does not
-// depend on the split of the row over threads.
+// The kernels below keep the sum of squares in two float32 words, the same pair in every lane of a row.  The mean
+// differs from the exact one by some 2^-44 of it for rows of like values, 2^-38 where one channel outweighs the others
+// (emulated on a CPU; 2^-33 if every rounding of squares() fell the same way; 2^-149 if that is more).  The float32 it
+// rounds to, and with it every 4- or 8-bit code, is that of the exact mean, and the same for each split of the row over
+// threads, unless the mean lies that near the middle between two float32: one row in 2^19, or 2^13.
 
 // Aligned rows of D = 16 c channels, D <= 512: p.lanes lanes of a warp share a row, each holds one
 // 16-channel chunk from the addition to the last store, and its weights for every row it works on.

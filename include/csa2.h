@@ -440,7 +440,8 @@ typedef struct csa2_fp4_rows {
  * the quantiser of the product that follows.  For each row t:
  *   h   = x + residual (float32), rounded to res_dtype and stored to residual_out;
  *         without a residual h = x
- *   ms  = mean_i h_i^2, summed in two float32 words (error 2^-46) and rounded once
+ *   ms  = mean_i h_i^2, summed in two float32 words and rounded once.  Error before the rounding:
+ *         some 2^-44 of it for rows of like values, below 2^-33 for any (or 2^-149, if that is more)
  *   y_i = (h_i * (1 / sqrt(ms + eps))) * weight_i, each operation rounded to float32
  * and, by out_form:
  *   CSA2_BF16 / CSA2_F32   out[t][i] = y_i, rounded once
@@ -448,7 +449,8 @@ typedef struct csa2_fp4_rows {
  *                          s = amax|y| / 448, byte = E4M3_RNE_satfinite(y / s) (float32
  *                          divisions), s == 0 -> zero bytes: the rows csa2_swa_quant writes
  *   CSA2_FP4E2M1X2         out4, as csa2_fp4_quant writes y
- * The codes are decided on values that do not depend on how a row is split over threads.
+ * One ms serves all channels of a row.  How a row is split over threads changes it, and the codes with it, only where
+ * the mean lies within that error of the middle between two float32.
  * A sum of squares beyond float32's range is taken scaled, so a finite mean stays finite.
  * NaN and infinities follow the formulas; a NaN in a group gives it a NaN scale and zero codes.
  * Strides are in elements between rows (the last dimension is contiguous); any alignment of
