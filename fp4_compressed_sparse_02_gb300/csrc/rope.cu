@@ -1,5 +1,7 @@
 // Rotary positions (csa2_rope) and their tables (csa2_rope_table).
+#include <algorithm>
 #include <cmath>
+#include <cstring>
 
 #include "internal.h"
 #include "rows.cuh"
@@ -190,36 +192,34 @@ struct TableParams {
   float* cos;
   float* sin;
   int positions, half;
-  float magnitude, magnitude_low;  // in two words
+  f32x2 m, minus_m, low;          // the magnitude as a float32, minus it, and what that leaves out, over it: each twice
   unsigned long long turn[128];   // turns per position of channel i, times 2^64
 };
 
-// (m + ml) sin and (m + ml) cos of pi/2 x / 2^32 for a pair of |x| <= 2^31 (an eighth of a turn at most): Taylor's
-// series to the powers 9 and 10, whose next terms are below 2e-9, at the rounded angle a, and the first
-// derivative for what the rounding (of x's last 8 bits, of pi and of the product) left out.  What cosine and
-// sine differ from 1 and a by is small, and takes the magnitude first; 1 and a times it join in the last
-// rounding, whose half step is most of the error (5 to 9 % more of it in root mean square than rounding alone;
-// rounding the functions and then their products made it 28 to 107 % more).
-__device__ __forceinline__ void sincos_pair(int x0, int x1, f32x2 m, f32x2 ml, f32x2& s, f32x2& c) {
+// The magnitude m (1 + low) times sin and cos of pi/2 x / 2^32 for a pair of |x| <= 2^31 (an eighth of a turn at most):
+// Taylor's series to the powers 9 and 10, whose next terms are below 2e-9, at the rounded angle a, and the first
+// derivative for what the rounding (of x's last 8 bits, of pi and of the product) left out.  What cosine and sine
+// differ from 1 and a by, low among it, is small; 1 and a times m join it in the last rounding, whose half step is most of the
+// error: 2 to 7 % more in root mean square than rounding alone (emulated on a CPU), where rounding the functions and
+// then their products made it 28 to 107 % more.
+__device__ __forceinline__ void sincos_pair(int x0, int x1, const TableParams& p, f32x2& s, f32x2& c) {
   const float q = 1.57079632679489662f * 0x1p-32f;
   const float ql = (float)((1.57079632679489662 - (double)1.57079632679489662f) * 0x1p-32);
   const auto k = [](float v) { return pk(v, v); };
   const f32x2 xh = pk((float)(x0 & ~255), (float)(x1 & ~255));
   const f32x2 xl = pk((float)(x0 & 255), (float)(x1 & 255));
-  const f32x2 a = mul2(xh, k(q)), z = mul2(a, a);
-  // minus what a leaves out
-  const f32x2 left = fma2(xh, k(-ql), fma2(xl, k(-q), fma2(xh, k(-q), a)));
+  const f32x2 na = mul2(xh, k(-q)), z = mul2(na, na);     // -a, a^2
+  const f32x2 left = fma2(xh, k(ql), fma2(xl, k(q), fma2(xh, k(q), na)));   // what a leaves out
   f32x2 t = fma2(z, k(-1.0f / 3628800), k(1.0f / 40320));
   t = fma2(z, t, k(-1.0f / 720));
   t = fma2(z, t, k(1.0f / 24));
   t = fma2(z, t, k(-0.5f));
-  const f32x2 dc = fma2(z, t, mul2(left, a));
-  c = add2(m, fma2(dc, m, ml));
+  c = fma2(fma2(z, t, fma2(left, na, p.low)), p.m, p.m);
   t = fma2(z, k(1.0f / 362880), k(-1.0f / 5040));
   t = fma2(z, t, k(1.0f / 120));
   t = fma2(z, t, k(-1.0f / 6));
-  const f32x2 ds = sub2(mul2(mul2(a, z), t), mul2(left, add2(k(1.0f), dc)));
-  s = fma2(a, m, fma2(ds, m, mul2(a, ml)));
+  t = fma2(z, t, p.low);
+  s = fma2(na, p.minus_m, fma2(mul2(na, t), p.minus_m, mul2(left, c)));
 }
 
 }  // namespace
@@ -227,8 +227,9 @@ __device__ __forceinline__ void sincos_pair(int x0, int x1, f32x2 m, f32x2 ml, f
 // The angle p f_i in turns, modulo 1, is a 64-bit product that a thread carries from one of its
 // positions to the next by an addition.  Its nearest multiple of a quarter turn picks which of
 // +-sin, +-cos of the remainder is which.  V channels a thread (4, or 1 where half % 4 != 0).
-//   1,048,576 positions x 32 pairs (268 MB written, 39.5 us at the copy rate): 38.3 us; with the library's
-// sincospif and a 64-bit division for the place it took 271 us.
+//   1,048,576 positions x 32 pairs (268 MB written, 39.5 us at the copy rate): 38.1 us; with the library's
+// sincospif and a 64-bit division for the place it took 271 us, with the magnitude packed in registers instead of the
+// parameters 39.9 us.
 template <int V>
 __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ TableParams t) {
   pdl_wait();
@@ -244,7 +245,6 @@ __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ Tabl
     a[i] = (unsigned long long)p * t.turn[i0 + i];
     d[i] = (unsigned long long)step * t.turn[i0 + i];
   }
-  const f32x2 mag = pk(t.magnitude, t.magnitude), mag_low = pk(t.magnitude_low, t.magnitude_low);
   for (; p < t.positions; p += step) {
     float c[V + V % 2], s[V + V % 2];
 #pragma unroll
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256) k_rope_table(const __grid_constant__ Tabl
       const int x0 = (int)__funnelshift_l((uint32_t)a[i], (uint32_t)(a[i] >> 32), 2);
       const int x1 = (int)__funnelshift_l((uint32_t)a[j], (uint32_t)(a[j] >> 32), 2);
       f32x2 sp, cp;
-      sincos_pair(x0, x1, mag, mag_low, sp, cp);
+      sincos_pair(x0, x1, t, sp, cp);
       const float2 sv = unpk(sp), cv = unpk(cp);
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -283,8 +283,13 @@ cudaError_t launch_rope_table(const csa2_rope_table_args& a, cudaStream_t st) {
   if (a.positions == 0) return cudaSuccess;
   TableParams t{};
   t.cos = a.rope_cos, t.sin = a.rope_sin, t.positions = a.positions, t.half = a.d_rope / 2;
-  t.magnitude = (float)a.magnitude;
-  t.magnitude_low = (float)(a.magnitude - (double)t.magnitude);
+  const auto twice = [](float v) {
+    uint32_t u;
+    memcpy(&u, &v, sizeof(u));
+    return (f32x2)u << 32 | u;
+  };
+  const float m = (float)a.magnitude;
+  t.m = twice(m), t.minus_m = twice(-m), t.low = twice(m > 0.f ? (float)((a.magnitude - m) / m) : 0.f);
   const double two_pi = 6.283185307179586476925;
   double lo = 0, hi = 0;
   if (a.scaling == CSA2_ROPE_YARN) {
@@ -310,9 +315,14 @@ cudaError_t launch_rope_table(const csa2_rope_table_args& a, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const int blocks = (t.positions + slots - 1) / slots, most = 8 * sms;
-  return vec ? launch_k(k_rope_table<4>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t)
-             : launch_k(k_rope_table<1>, (unsigned)(blocks < most ? blocks : most), 256, 0, st, t);
+  // About twelve positions a thread, but from five CTAs an SM (as many as run at once) to 24.  us by CTAs an SM:
+  //     65,536 x 32   5: 4.0,  8: 4.5, 12: 5.4, 24: 5.7      1,048,576 x 32   5: 40.1,  8: 40.3, 12: 38.1, 24: 38.6
+  //     65,536 x 64   5: 6.4,  8: 7.4, 12: 9.0, 24: 14.8     1,048,576 x 64   5: 79.5,  8: 80.8, 12: 77.9, 24: 74.5
+  //    262,144 x 32   5: 11.2, 8: 11.3, 12: 11.5, 24: 12.9    524,288 x 32   5: 20.7,  9: 20.3, 12: 20.4, 24: 21.2
+  // Not whole numbers of them cost more: 524,288 x 32 21.3 us with 6.7.
+  const int all = (t.positions + slots - 1) / slots;
+  const int per_sm = std::min(std::max(all / 12 / sms + 1, 5), 24), blocks = std::min(all, per_sm * sms);
+  return vec ? launch_k(k_rope_table<4>, (unsigned)blocks, 256, 0, st, t) : launch_k(k_rope_table<1>, (unsigned)blocks, 256, 0, st, t);
 }
 
 uint32_t read_clear_error_rope() {

@@ -26,3 +26,9 @@ def test_rope_table_rounds_once(P, d_rope, magnitude):
     # errors a root mean square of 0.15 half steps, beside 0.42 of the rounding itself: 6 % more.  Twice that is allowed
     # for, and a little; rounding twice costs 28 % or more for each of these magnitudes but 1.
     assert np.sqrt(ours) <= 1.15 * np.sqrt(rounding)
+
+
+def test_rope_table_of_a_vanishing_magnitude():
+    """A magnitude below float32's least value gives zeros, not NaN."""
+    for t in csa2.rope_table(300, 64, magnitude=1e-50):
+        assert (t == 0).all()
