@@ -6,7 +6,6 @@ PyTorch provides device memory and the current stream; every computation runs in
 library's kernels.  Outputs are allocated here when the caller passes none (pass them
 in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
 """
-import contextlib
 import ctypes
 import math
 import struct
@@ -37,7 +36,8 @@ def _pointers(device):
     def ptr(t: Optional[torch.Tensor]):
         if t is None:
             return None
-        _on_device(t, dev, "operand")
+        if t.get_device() != dev:
+            _on_device(t, dev, "operand")
         if not t.is_contiguous():
             raise ValueError("expected a contiguous tensor")
         return ctypes.c_void_p(t.data_ptr())
@@ -56,16 +56,21 @@ _U8 = (torch.uint8,)
 _F32 = (torch.float32,)
 
 
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+def _stream(dev):
+    """Handle of CUDA device number dev's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-_AS_IT_IS = contextlib.nullcontext()
+_gpus = 0                                  # how many the process has (asked at the first call)
 
 
-def _current(device):
-    """A context in which this CUDA device is the current one (see _launch)."""
-    return _AS_IT_IS if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+def _is_current(dev):
+    """Whether CUDA device number dev is the current one: a launch goes to that, whatever device its stream's handle and
+    its pointers belong to."""
+    global _gpus
+    if not _gpus:
+        _gpus = torch.cuda.device_count()
+    return _gpus == 1 or dev == torch._C._cuda_getDevice()
 
 
 @dataclass
@@ -163,13 +168,17 @@ def _ws(ws, device):
 
 
 def _call(fn, args, ws, device):
+    """Call fn, which takes a workspace, on the current stream of this device, with the device current."""
+    dev = device.index
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return _call(fn, args, ws, device)
     L = _lib.lib()
     need = ctypes.c_size_t(0)
-    with _current(device):
-        _lib.check(getattr(L, fn + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
-        buf = _ws(ws, device).get(need.value)
-        _on_device(buf, device.index, "ws")
-        _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream()))
+    _lib.check(getattr(L, fn + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
+    buf = _ws(ws, device).get(need.value)
+    _on_device(buf, dev, "ws")
+    _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream(dev)))
 
 
 def compress_quant(cache: PagedCache, seq, entry, *, m=1, C=None, Z=None, H=None, W_kv=None, W_z=None,
@@ -328,8 +337,7 @@ def swa_quant(x, swa, swa_scale, row_idx=None):
     a.x_dtype = F32 if x.dtype == torch.float32 else BF16
     a.x, a.row_idx, a.swa, a.swa_scale = ptr(x), ptr(row_idx), ptr(swa), ptr(swa_scale)
     a.swa_rows = swa.shape[0]
-    with _current(x.device):
-        _lib.check(_lib.lib().csa2_swa_quant(ctypes.byref(a), _stream()))
+    _launch("csa2_swa_quant", ctypes.byref(a), x.get_device())
 
 
 _FLOAT = {torch.bfloat16: BF16, torch.float32: F32}
@@ -344,7 +352,8 @@ def _float_type(t, name):
 
 def _rows_of(t, dev, name):
     """(data pointer, row stride) of a matrix on CUDA device number dev whose rows are contiguous."""
-    _on_device(t, dev, name)
+    if t.get_device() != dev:                           # in line: a call of 5 us asks it five times
+        _on_device(t, dev, name)
     rows, last = t.stride()
     if last != 1 and t.shape[1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
@@ -357,7 +366,8 @@ def _dense(t, dev, dtype, name):
         return 0
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    _on_device(t, dev, name)
+    if t.get_device() != dev:
+        _on_device(t, dev, name)
     if not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous tensor")
     return t.data_ptr()
@@ -373,14 +383,16 @@ _FP4_LINEAR = struct.Struct("@N" + 2 * _FP4_ROWS + "Pi0P")
 
 
 def _launch(fn, packed, dev):
-    """Call fn on the current stream of CUDA device number dev, with that device current: a launch goes to
-    the current one, whatever device its stream's handle and its pointers belong to."""
+    """Call fn on the current stream of CUDA device number dev, with that device current.  dev < 0: the operands,
+    which were compared with it, are not on a GPU."""
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
     call = getattr(_lib.lib(), fn)
-    if dev == torch._C._cuda_getDevice():
-        status = call(packed, torch._C._cuda_getCurrentRawStream(dev))
+    if _is_current(dev):
+        status = call(packed, _stream(dev))
     else:
         with torch.cuda.device(dev):
-            status = call(packed, torch._C._cuda_getCurrentRawStream(dev))
+            status = call(packed, _stream(dev))
     if status:
         _lib.check(status)
 
@@ -548,8 +560,8 @@ def rope(x, pos, cos, sin, *, interleaved=True, inverse=False, first=None, out=N
     elif out.shape != x.shape or out.dtype is not x.dtype:
         raise ValueError("out must have x's shape and type")
     dev = x.get_device()
-    _on_device(x, dev, "x")
-    _on_device(out, dev, "out")
+    if out.get_device() != dev:
+        _on_device(out, dev, "out")
     xt, xh, xc = x.stride()
     ot, oh, oc = out.stride()
     if (xc != 1 or oc != 1) and D > 1:
@@ -570,11 +582,12 @@ def fp4_quant(x, gscale=None, out=None):
         out = Fp4Rows.allocate(T, K, x.device, gscale)
     elif gscale is not None:
         raise ValueError("give gscale with out, or out alone")
-    elif (out.rows, out.cols) != (T, K):
-        raise ValueError("out must have x's shape")
     dev = x.get_device()
     xp, xs = _rows_of(x, dev, "x")
-    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, xp, _float_type(x, "x"), xs, *out.fields(dev)), dev)
+    fields = out.fields(dev)
+    if fields[3] != T or fields[4] != K:
+        raise ValueError("out must have x's shape")
+    _launch("csa2_fp4_quant", _FP4_QUANT.pack(_FP4_QUANT.size, xp, _float_type(x, "x"), xs, *fields), dev)
     return out
 
 
@@ -610,4 +623,4 @@ def selftest_wait_timeout(polls=1000):
     """Run the bounded-wait failure path once (one CTA waits on an mbarrier nothing
     arrives on, gives up after `polls` polls and sets the timeout bit of the device error
     word)."""
-    _lib.check(_lib.lib().csa2_selftest_wait_timeout(int(polls), _stream()))
+    _lib.check(_lib.lib().csa2_selftest_wait_timeout(int(polls), _stream(torch.cuda.current_device())))

@@ -1053,12 +1053,11 @@ cudaError_t launch_linear_pair(const csa2_fp4_linear_args& a, cudaStream_t st) {
   const long long ntile = (long long)p.nft * p.ntt;
   if (ntile > INT32_MAX / 2) return cudaErrorInvalidConfiguration;
   p.vec4 = groups_of_four(a);
-  static SmemLimit limit;
   static PerDevice<Clusters> resident;
-  cudaError_t e = limit.raise(k_fp4_linear_pair<TMA_OUT>, SMEM);
-  if (e != cudaSuccess) return e;
   const Clusters* clusters_of = nullptr;
-  e = resident.get(&clusters_of, [](Clusters& c) {
+  cudaError_t e = resident.get(&clusters_of, [](Clusters& c) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_pair<TMA_OUT>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
     for (int s = 4; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear_pair<TMA_OUT>, 2 * s, THREADS, SMEM);
     return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
@@ -1113,12 +1112,11 @@ cudaError_t launch_linear_few(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.gx = a.x.gscale, p.gw = a.w.gscale, p.out = a.out, p.out32 = a.out_dtype == CSA2_F32, p.vec4 = groups_of_four(a);
   p.T = a.x.rows, p.N = a.w.rows, p.nkt = (a.x.cols + 63) / 64;
   const int tiles = (p.N + 2 * BM - 1) / (2 * BM), nkb = (p.nkt + 3) / 4;
-  static SmemLimit limit;
   static PerDevice<Clusters> resident;
-  cudaError_t e = limit.raise(k_fp4_linear_few<BN>, Few<BN>::SMEM);
-  if (e != cudaSuccess) return e;
   const Clusters* clusters_of = nullptr;
-  e = resident.get(&clusters_of, [](Clusters& c) {
+  cudaError_t e = resident.get(&clusters_of, [](Clusters& c) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear_few<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, Few<BN>::SMEM);
+    if (e != cudaSuccess) return e;
     for (int s = 4; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear_few<BN>, 2 * s, THREADS, Few<BN>::SMEM);
     return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
@@ -1156,12 +1154,11 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   p.vec4 = groups_of_four(a);
   const int ft = (p.N + lin::BM - 1) / lin::BM, tt = (p.T + BN - 1) / BN, nkb = (p.nkt + 3) / 4;
   const long long tiles = (long long)ft * tt;
-  static SmemLimit limit;
   static PerDevice<Clusters> resident;
-  cudaError_t e = limit.raise(k_fp4_linear<BN>, C::SMEM);
-  if (e != cudaSuccess) return e;
   const Clusters* clusters_of = nullptr;
-  e = resident.get(&clusters_of, [](Clusters& c) {
+  cudaError_t e = resident.get(&clusters_of, [](Clusters& c) {
+    cudaError_t e = cudaFuncSetAttribute(k_fp4_linear<BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess) return e;
     const size_t smem2 = (size_t)C::STAGES2 * C::STAGE + 256;
     for (int s = 8; s >= 1; --s) c.of[s] = resident_clusters(k_fp4_linear<BN>, s, lin::THREADS, smem2);
     return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
@@ -1211,12 +1208,12 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
 
 cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   if (a.x.rows == 0 || a.w.rows == 0) return cudaSuccess;
-  int sms = 0;
-  const cudaError_t e = sm_count(&sms);
-  if (e != cudaSuccess) return e;
   const int T = a.x.rows, nkb = (a.x.cols + 255) / 256, ft = (a.w.rows + 127) / 128;
   if (T <= 16) return launch_linear<16>(a, st);
   if (T <= 32) return launch_linear<32>(a, st);
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
   // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs): what a
   // CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight
   // ways below 16 feature tiles, and start and end sooner, which decides short sums.  us, single CTAs or

@@ -65,6 +65,7 @@ def machine(monkeypatch):
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 100 + d, raising=False)
     monkeypatch.setattr(csa2._lib, "lib", lambda: Library())
+    monkeypatch.setattr(csa2, "_gpus", 2)
     return calls
 
 
