@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(256, 5) k_fp4_quant(QuantRowsParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) n[i] = raw.pair(i);
       } else {
-        load16_any(n, p.x, x, X32, 16);
+        load16_any(n, p.x, x, X32);
         if (!over)
 #pragma unroll
           for (int i = 0; i < 8; ++i) n[i] = mul2(n[i], pk(-1.f, -1.f));
@@ -73,7 +73,7 @@ __global__ void __launch_bounds__(256, 5) k_fp4_quant(QuantRowsParams p) {
       } else {
         f32x2 t[8];
         uint32_t b[3];
-        load16_any(t, p.x, x, X32, 16);
+        load16_any(t, p.x, x, X32);
         fp4_encode16_any(t, g, b);
         w[0] = b[0], w[1] = b[1], w[2] = b[2];
       }

@@ -141,28 +141,14 @@ struct Raw16 {
   }
 };
 
-// 16 channels one at a time, for rows that are not aligned; channels from n on are 0.
-__device__ __forceinline__ void load16_any(f32x2* v, const void* base, long long off, bool f32, int n) {
+// 16 channels one at a time, for rows that are not aligned.
+__device__ __forceinline__ void load16_any(f32x2* v, const void* base, long long off, bool f32) {
   float e[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    e[i] = i >= n ? 0.f : f32 ? static_cast<const float*>(base)[off + i]
-                              : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[off + i]);
+    e[i] = f32 ? static_cast<const float*>(base)[off + i] : bf16_bits_to_f32(static_cast<const uint16_t*>(base)[off + i]);
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = pk(e[2 * i], e[2 * i + 1]);
-}
-
-__device__ __forceinline__ void store16_any(const f32x2* v, void* base, long long off, bool f32, int n) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float2 f = unpk(v[i / 2]);
-    const float e = i % 2 ? f.y : f.x;
-    if (i >= n) continue;
-    if (f32)
-      static_cast<float*>(base)[off + i] = e;
-    else
-      static_cast<uint16_t*>(base)[off + i] = __bfloat16_as_ushort(__float2bfloat16_rn(e));
-  }
 }
 
 template <bool F32>
