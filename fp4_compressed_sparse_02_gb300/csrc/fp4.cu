@@ -218,8 +218,7 @@ __device__ __forceinline__ void put4(const P& p, long long at, int n, float a, f
 // CTA's loads run during the first's start and end.  Prefetching further tiles into L2 made it 18 to
 // 20 us.
 //   Split, 1 x 32768 -> 5120 (40 tiles), two CTAs an SM: S = 1 51 us, 3 21 us, 4 17.7 us, 6 16.8 us, 7 26 us
-// (clusters of seven pack badly: some wait for a second round), so S is the largest whose
-// clusters all run at once.
+// (clusters of seven pack badly: some wait for a second round).  launch_linear takes the S of least cost in stages.
 template <int BN>
 __global__ void __launch_bounds__(lin::THREADS)
     k_fp4_linear(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx, lin::Params p) {
@@ -571,7 +570,8 @@ __device__ __forceinline__ void place(const Params& p, int t, int& ft, int& tt) 
 // half of TMEM and the scales part of the rest, so the next tile starts when this one has been
 // read: eight warps take it into registers in one go and release it before anything is stored.
 //   What bounds it, 8192 x 5120 -> 32768: products alone take 316 us, the loads alone 279 us, the
-// scale copies alone 282 us; all of it 422 us, 6.5 PFLOP/s (433 us on the slowest of three boards).  Each
+// scale copies alone 282 us; all of it 422 us, 6.5 PFLOP/s, in bursts of a few ms (433 us on the slowest of three boards);
+// back to back, under the power cap, 465 us, 5.9 PFLOP/s.  Each
 // step's scales are copied right before its product: all of a stage's first, then its products, took 434 us
 // (414 without the results), the next stage's before this one's products a fourth more.
 //   Tile: 256 x 192 with two accumulators (results stored while the next tile runs) took 526 us:
@@ -1164,7 +1164,9 @@ cudaError_t launch_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
     return c.of[1] ? cudaSuccess : cudaErrorInvalidConfiguration;
   });
   if (e != cudaSuccess) return e;
-  const int* one = clusters_of->of;                       // clusters of s CTAs that the GPU holds at once, a CTA an SM
+  // Clusters of s CTAs that the GPU holds at once, a CTA an SM: the occupancy call counts one of these kernels an SM
+  // (152 76 46 36 28 23 15 15 of them on 152 SMs) though two have room and run (see the times by S above).
+  const int* one = clusters_of->of;
   // Few tiles (under three quarters of the SMs): split the sum where the stages saved are worth adding the
   // parts.  Costs in stages, fitted to 148 sizes: clusters that do not all fit on SMs of their own share some, whose
   // stages take 1.65 times as long together; adding costs what a tile of 128 tokens writes and reads, less for fewer.
@@ -1214,8 +1216,8 @@ cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs): what a
-  // CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight
+  // 33 to 256 tokens, sums that split over two pairs or more (36 clusters of four CTAs run at once on 152 SMs, hence nine
+  // nineteenths of the SMs in feature tiles): what a CTA can take in is the bound, and a pair's CTAs take in half of the tokens each.  Single CTAs split eight
   // ways below 16 feature tiles, and start and end sooner, which decides short sums.  us, single CTAs or
   // wide pairs against pairs on few tokens:
   //    64 x  4096 -> 2560   6.7   5.4      64 x  8192 -> 5120   7.9  7.8      64 x 32768 -> 5120  19.9 20.3

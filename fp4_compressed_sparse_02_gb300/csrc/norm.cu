@@ -355,11 +355,14 @@ __global__ void __launch_bounds__(512) k_rms_norm(NormParams p) {
 // channels and reads and writes them 32 at a time, so that every offset is a constant and a row costs few
 // instructions beside its bytes; the quantised forms pass the row through shared memory to 16-channel chunks
 // (17 words apart, so that the lanes' banks differ).
-//   4099 x 1001 from float32 to bf16 (24.6 MB, 3.6 us at the copy rate): 5.2 us with N = 16, 6.4 with 8, 9.7 with 4
-// (every warp adds the whole row's sums); 8.5 us with channels a CTA's width apart, whose addresses are computed
+//   4099 x 1001 from float32 to bf16 (24.6 MB, 3.6 us at the copy rate), float32 weights: 5.2 us with N = 16, 6.3 with 8,
+// 9.7 with 4 (every warp adds the whole row's sums); bf16 weights 5.8 us; 8.5 us with channels a CTA's width apart, whose addresses are computed
 // one by one; 10.8 us with that form's next row loaded ahead (more registers, fewer rows at a time).
 //   20000 x 333 (40 MB, 5.9 us): 9.7 us, against 20.6 us with a CTA of one warp a row.  Up to 1024 channels a warp (N = 32)
 // gains as little as it loses: 4099 x 1001 5.1 us, with a residual 8.6 against 7.9 us.
+//   Aligned rows above 8192 channels come here too, and pay for the narrow accesses: 2048 x 12288 in bf16 with a residual 63 us
+// (201 MB, 29.7 us at the copy rate), 2048 x 16384 77 us (39.5), to FP4 92 us (32.4); 1024 x 32768, two CTAs' registers in
+// one with spills, 87 us (39.5).  k_rms_norm takes 23 us for 2048 x 8192 (19.8).
 constexpr int kAnyRows = 4;
 
 template <int OUT, int N, int THREADS>

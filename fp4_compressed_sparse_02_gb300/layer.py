@@ -8,7 +8,8 @@
     a        = sparse attention(q, cache, top-k, window)       sparse_attn
     out      = FP4 of rope^-1(a) . W_o                         rope (inverse), fp4_quant, fp4_linear
 
-The entry is key and value at once, so what the attention returns still carries the keys'
+The sliding window is the caller's: a step reads the rows it is given and does not write the new token's
+(csa2.swa_quant does).  The entry is key and value at once, so what the attention returns still carries the keys'
 rotation; the query's position turns it back.  Every buffer is allocated once, and a step can be
 captured in a CUDA graph.  ``python -m fp4_compressed_sparse_02_gb300.layer`` runs a Full layer and
 a Reuse layer of a decode batch and prints the time of a step.
