@@ -440,6 +440,8 @@ class Fp4Rows:
         g = self.gscale
         if g is not None and g.numel() != 1:
             raise ValueError("gscale must have one element")
+        if dev < 0:
+            raise ValueError("codes: expected a CUDA tensor")
         return (_dense(self.codes, dev, torch.uint8, "codes"), _dense(self.scales, dev, torch.uint8, "scales"),
                 _dense(g, dev, torch.float32, "gscale"), rows, 2 * half)
 

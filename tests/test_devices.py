@@ -171,3 +171,8 @@ def test_hot_path_refuses_operands_of_another_device(machine, name, moved):
     with pytest.raises(ValueError, match="cuda:1"):
         run(HOT[name][0], 0, moved)
     assert machine == []
+
+
+def test_rows_on_the_cpu_have_no_fields():
+    with pytest.raises(ValueError, match="CUDA"):
+        csa2.Fp4Rows.allocate(4, 64, "cpu").fields()
