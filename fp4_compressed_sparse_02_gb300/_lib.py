@@ -100,6 +100,39 @@ class Fp4LinearArgs(ctypes.Structure):
                 ("out_dtype", c_i32)]
 
 
+class Kv8CacheArg(ctypes.Structure):
+    _fields_ = [("k", c_vp), ("v", c_vp), ("k_scale", c_vp), ("v_scale", c_vp), ("mean", c_vp), ("mean_scale", c_vp),
+                ("page_table", c_vp), ("num_pages", c_i32), ("page_size", c_i32), ("num_seqs", c_i32),
+                ("max_pages", c_i32), ("Hkv", c_i32), ("D", c_i32)]
+
+
+class PagePlanArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("S", c_i32), ("max_pages", c_i32), ("tokens", c_i32),
+                ("num_free", c_i32), ("length", c_vp), ("add", c_vp), ("free_pages", c_vp), ("free_head", c_vp),
+                ("page_table", c_vp), ("start", c_vp), ("seq", c_vp), ("pos", c_vp), ("slot", c_vp),
+                ("new_length", c_vp), ("new_head", c_vp)]
+
+
+class Kv8AppendArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("T", c_i32), ("S", c_i32), ("x_dtype", c_i32), ("k", c_vp),
+                ("v", c_vp), ("k_stride_t", c_i64), ("k_stride_h", c_i64), ("v_stride_t", c_i64),
+                ("v_stride_h", c_i64), ("start", c_vp), ("length", c_vp), ("cache", Kv8CacheArg)]
+
+
+class Kv8SelectArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("T", c_i32), ("S", c_i32), ("Hq", c_i32), ("k", c_i32),
+                ("first", c_i32), ("recent", c_i32), ("max_length", c_i32), ("q", c_vp), ("q_stride_t", c_i64),
+                ("q_stride_h", c_i64), ("start", c_vp), ("length", c_vp), ("cache", Kv8CacheArg), ("pages", c_vp),
+                ("count", c_vp)]
+
+
+class Kv8AttnArgs(ctypes.Structure):
+    _fields_ = [("struct_size", ctypes.c_size_t), ("T", c_i32), ("S", c_i32), ("Hq", c_i32), ("max_new", c_i32),
+                ("window", c_i32), ("softmax_scale", ctypes.c_float), ("q", c_vp), ("q_stride_t", c_i64),
+                ("q_stride_h", c_i64), ("start", c_vp), ("length", c_vp), ("cache", Kv8CacheArg), ("pages", c_vp),
+                ("list_len", c_i32), ("out", c_vp), ("out_dtype", c_i32), ("lse", c_vp)]
+
+
 STATUS = {0: "OK", 1: "ERR_INVALID_ARG", 2: "ERR_UNSUPPORTED_SHAPE", 3: "ERR_WORKSPACE_TOO_SMALL",
           4: "ERR_CUDA", 5: "ERR_DEVICE_CHECK", 6: "ERR_TIMEOUT"}
 
@@ -108,7 +141,9 @@ EXPORTS = ["csa2_compress_quant", "csa2_compress_quant_workspace", "csa2_index_f
            "csa2_sparse_attn", "csa2_sparse_attn_workspace", "csa2_last_error_message",
            "csa2_get_device_error", "csa2_version", "csa2_index_full_noalloc", "csa2_selftest_wait_timeout",
            "csa2_swa_quant", "csa2_compress_append", "csa2_compress_append_workspace",
-           "csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear"]
+           "csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear",
+           "csa2_page_plan", "csa2_kv8_append", "csa2_kv8_select", "csa2_kv8_select_workspace", "csa2_kv8_attn",
+           "csa2_kv8_attn_workspace"]
 
 _lib = None
 
@@ -140,10 +175,18 @@ def lib():
         g.restype = c_i32
     L.csa2_swa_quant.argtypes = [ctypes.POINTER(SwaQuantArgs), c_vp]
     L.csa2_swa_quant.restype = c_i32
-    for name in ["csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear"]:
+    for name in ["csa2_rms_norm", "csa2_rope", "csa2_rope_table", "csa2_fp4_quant", "csa2_fp4_linear",
+                 "csa2_page_plan", "csa2_kv8_append"]:
         f = getattr(L, name)
         f.argtypes = [c_vp, c_vp]          # a struct by reference, or its packed bytes
         f.restype = c_i32
+    for name in ["csa2_kv8_select", "csa2_kv8_attn"]:
+        f = getattr(L, name)
+        f.argtypes = [c_vp, c_vp, ctypes.c_size_t, c_vp]
+        f.restype = c_i32
+        g = getattr(L, name + "_workspace")
+        g.argtypes = [c_vp, ctypes.POINTER(ctypes.c_size_t)]
+        g.restype = c_i32
     L.csa2_index_full_noalloc.argtypes = [ctypes.POINTER(IndexFullArgs), c_vp]
     L.csa2_index_full_noalloc.restype = c_i32
     L.csa2_last_error_message.argtypes = []

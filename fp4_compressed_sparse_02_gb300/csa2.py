@@ -1,7 +1,8 @@
 """Python face of the CSA2 C ABI: torch tensors in, device pointers to libcsa2.so.
 
 Names follow include/csa2.h: compress_quant, index_full, index_reindex, sparse_attn, and the
-operators around them: rms_norm, rope, rope_table, fp4_quant, fp4_linear.
+operators around them: rms_norm, rope, rope_table, fp4_quant, fp4_linear, and, for the model's plain
+attention layers, page_plan, kv8_append, kv8_select, kv8_attn.
 PyTorch provides device memory and the current stream; every computation runs in the
 library's kernels.  Outputs are allocated here when the caller passes none (pass them
 in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
@@ -605,6 +606,215 @@ def fp4_linear(x: Fp4Rows, w: Fp4Rows, *, out_dtype=torch.bfloat16, out=None):
     _launch("csa2_fp4_linear", _FP4_LINEAR.pack(_FP4_LINEAR.size, *fx, *fw, _dense(out, dev, out.dtype, "out"),
                                                 _float_type(out, "out")), dev)
     return out
+
+
+# ---- the paged 8-bit cache --------------------------------------------------------------------
+
+_KV8_CACHE = "PPPPPPPiiiiii"
+_PAGE_PLAN = struct.Struct("@NiiiiPPPPPPPPPPP")
+_KV8_APPEND = struct.Struct("@NiiiPPqqqqPP" + _KV8_CACHE + "0P")
+_KV8_SELECT = struct.Struct("@NiiiiiiiPqqPP" + _KV8_CACHE + "0P" + "PP")
+_KV8_ATTN = struct.Struct("@NiiiiifPqqPP" + _KV8_CACHE + "0P" + "PiPiP")
+
+
+@dataclass
+class Kv8Cache:
+    """Paged keys and values in 8 bits for grouped-query attention layers: k, v uint8 (E4M3 bytes)
+    [pages, Hkv, 64, D], k_scale, v_scale float32 [pages, Hkv], page_table int32 [seqs, max_pages], and, if
+    kv8_select is to choose pages, their summaries mean int8 [pages, Hkv, D] with mean_scale float32
+    [pages, Hkv]."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+    page_table: torch.Tensor
+    mean: Optional[torch.Tensor] = None
+    mean_scale: Optional[torch.Tensor] = None
+
+    @staticmethod
+    def allocate(num_pages, heads, D, page_table, mean=True):
+        """A cache of num_pages pages on the page table's device."""
+        new = lambda dtype, *s: torch.zeros((num_pages, heads) + s, dtype=dtype, device=page_table.device)
+        return Kv8Cache(new(torch.uint8, PAGE, D), new(torch.uint8, PAGE, D), new(torch.float32), new(torch.float32),
+                        page_table, new(torch.int8, D) if mean else None, new(torch.float32) if mean else None)
+
+    def fields(self, dev):
+        """The C struct's values, after its checks; dev: the CUDA device number that all planes must be on."""
+        pages, heads, slots, D = self.k.shape
+        if slots != PAGE or self.v.shape != self.k.shape:
+            raise ValueError(f"k and v must be [pages, heads, {PAGE}, D] alike")
+        if self.k_scale.shape != (pages, heads) or self.v_scale.shape != (pages, heads):
+            raise ValueError(f"k_scale and v_scale must be [{pages}, {heads}]")
+        m, ms = self.mean, self.mean_scale
+        if (m is None) != (ms is None):
+            raise ValueError("mean and mean_scale go together")
+        if m is not None and (m.shape != (pages, heads, D) or ms.shape != (pages, heads)):
+            raise ValueError(f"mean must be [{pages}, {heads}, {D}] and mean_scale [{pages}, {heads}]")
+        seqs, most = self.page_table.shape
+        return (_dense(self.k, dev, torch.uint8, "k plane"), _dense(self.v, dev, torch.uint8, "v plane"),
+                _dense(self.k_scale, dev, torch.float32, "k_scale"), _dense(self.v_scale, dev, torch.float32, "v_scale"),
+                _dense(m, dev, torch.int8, "mean"), _dense(ms, dev, torch.float32, "mean_scale"),
+                _dense(self.page_table, dev, torch.int32, "page_table"), pages, PAGE, seqs, most, heads, D)
+
+
+def _launch_ws(fn, packed, ws, device, dev):
+    """_launch of a call that takes a workspace."""
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    if not _is_current(dev):
+        with torch.cuda.device(dev):
+            return _launch_ws(fn, packed, ws, device, dev)
+    L = _lib.lib()
+    need = ctypes.c_size_t(0)
+    status = getattr(L, fn + "_workspace")(packed, ctypes.byref(need))
+    if status:
+        _lib.check(status)
+    buf = 0
+    if need.value:
+        t = _ws(ws, device).get(need.value)
+        _on_device(t, dev, "ws")
+        buf = t.data_ptr()
+    status = getattr(L, fn)(packed, buf, need.value, _stream(dev))
+    if status:
+        _lib.check(status)
+
+
+def _heads_of(t, dev, name):
+    """(data pointer, token stride, head stride) of a [T, H, D] tensor with contiguous channels."""
+    if t.get_device() != dev:
+        _on_device(t, dev, name)
+    st, sh, sc = t.stride()
+    if sc != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr(), st, sh
+
+
+def _step(cache, start, length, dev):
+    """(sequences, start, length) of a step's rows."""
+    S, = length.shape
+    if start.shape != (S + 1,) or S > cache.page_table.shape[0]:
+        raise ValueError("start must be [S + 1] and length [S], S at most the page table's rows")
+    return S, _dense(start, dev, torch.int32, "start"), _dense(length, dev, torch.int32, "length")
+
+
+@dataclass
+class PagePlan:
+    """The tables of a step (page_plan): start int32 [S+1], seq, pos, slot int32 [tokens], length int32 [S] and
+    head int32 [1] after it."""
+    start: torch.Tensor
+    seq: torch.Tensor
+    pos: torch.Tensor
+    slot: torch.Tensor
+    length: torch.Tensor
+    head: torch.Tensor
+
+    @staticmethod
+    def allocate(seqs, tokens, device):
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
+        return PagePlan(new(seqs + 1), new(tokens), new(tokens), new(tokens), new(seqs), new(1))
+
+
+def page_plan(length, add, page_table, free_pages, free_head, tokens, *, out=None):
+    """The tables of a step in which sequence s, holding length[s] tokens, gets add[s] more (int32 [S]): where its rows
+    stand (start), each row's sequence, position and slot (-1 past the last row, of `tokens`), and page_table
+    int32 [S, max_pages] extended by pages off free_pages int32 [F] from free_head int32 [1] on.
+    out may hold length and free_head themselves, which then advance.  Returns PagePlan."""
+    S, = length.shape
+    if add.shape != (S,) or page_table.shape[0] != S or free_head.numel() != 1:
+        raise ValueError("length and add must be [S], page_table [S, max_pages], free_head [1]")
+    dev = length.get_device()
+    if out is None:
+        out = PagePlan.allocate(S, tokens, length.device)
+    elif (out.start.shape != (S + 1,) or out.length.shape != (S,) or out.head.numel() != 1
+          or any(t.shape != (tokens,) for t in (out.seq, out.pos, out.slot))):
+        raise ValueError("out must be PagePlan.allocate(S, tokens)")
+    i32 = torch.int32
+    _launch("csa2_page_plan", _PAGE_PLAN.pack(
+        _PAGE_PLAN.size, S, page_table.shape[1], tokens, free_pages.shape[0], _dense(length, dev, i32, "length"),
+        _dense(add, dev, i32, "add"), _dense(free_pages, dev, i32, "free_pages"), _dense(free_head, dev, i32, "free_head"),
+        _dense(page_table, dev, i32, "page_table"), _dense(out.start, dev, i32, "start"), _dense(out.seq, dev, i32, "seq"),
+        _dense(out.pos, dev, i32, "pos"), _dense(out.slot, dev, i32, "slot"), _dense(out.length, dev, i32, "out.length"),
+        _dense(out.head, dev, i32, "head")), dev)
+    return out
+
+
+def kv8_append(cache: Kv8Cache, k, v, start, length):
+    """Quantise the new keys and values k, v [T, Hkv, D] (bf16 or float32; tokens and heads may be strided)
+    into the cache: sequence s's are rows start[s] .. start[s+1]-1, and it holds length[s] tokens with them (int32,
+    as page_plan returns them)."""
+    T, H, D = k.shape
+    if v.shape != k.shape or (H, D) != (cache.k.shape[1], cache.k.shape[3]):
+        raise ValueError("k and v must be [T, Hkv, D] of the cache's heads and channels")
+    if v.dtype is not k.dtype:
+        raise TypeError("k and v must have one type")
+    dev = k.get_device()
+    kp, kt, kh = _heads_of(k, dev, "k")
+    vp, vt, vh = _heads_of(v, dev, "v")
+    S, sp, lp = _step(cache, start, length, dev)
+    _launch("csa2_kv8_append", _KV8_APPEND.pack(_KV8_APPEND.size, T, S, _float_type(k, "k"), kp, vp, kt, kh, vt, vh, sp, lp,
+                                                *cache.fields(dev)), dev)
+
+
+def kv8_select(cache: Kv8Cache, q, start, length, k, *, first=1, recent=1, max_length=None, out=None, ws=None):
+    """The pages each new token attends to, by key head: the `first` oldest, the `recent` newest and the best-scoring
+    others, k at most.  q bf16 [T, Hq, D] (tokens and heads may be strided); start, length as in
+    kv8_append; max_length: a bound of length (by default the page table's).  Returns (pages int32 [T, Hkv, k],
+    ascending and padded with -1, count int32 [T, Hkv])."""
+    T, Hq, D = q.shape
+    H = cache.k.shape[1]
+    _expect(q, _B16, "q")
+    if D != cache.k.shape[3]:
+        raise ValueError("q must have the cache's channels")
+    if out is None:
+        out = (torch.empty((T, H, k), dtype=torch.int32, device=q.device),
+               torch.empty((T, H), dtype=torch.int32, device=q.device))
+    elif out[0].shape != (T, H, k) or out[1].shape != (T, H):
+        raise ValueError(f"out must be int32 [{T}, {H}, {k}] and [{T}, {H}]")
+    dev = q.get_device()
+    qp, qt, qh = _heads_of(q, dev, "q")
+    S, sp, lp = _step(cache, start, length, dev)
+    if max_length is None:
+        max_length = min(cache.page_table.shape[1] * PAGE, 1 << 21)
+    _launch_ws("csa2_kv8_select", _KV8_SELECT.pack(
+        _KV8_SELECT.size, T, S, Hq, k, first, recent, max_length, qp, qt, qh, sp, lp, *cache.fields(dev),
+        _dense(out[0], dev, torch.int32, "pages"), _dense(out[1], dev, torch.int32, "count")), ws, q.device, dev)
+    return out
+
+
+def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, window=0, softmax_scale=None,
+             out_dtype=torch.bfloat16, out=None, lse=None, ws=None):
+    """Causal attention of the new tokens q bf16 [T, Hq, D] (tokens and heads may be strided) over the cache, which
+    holds their keys and values already; start, length as in kv8_append.  max_new: about how many new
+    tokens a sequence has at most (picks the kernel; by default T).  pages int32 [T, Hkv, n]: only these pages
+    (kv8_select).  window: only so many newest positions.  Returns (out [T, Hq, D] bf16 or float32, lse
+    float32 [T, Hq])."""
+    T, Hq, D = q.shape
+    H = cache.k.shape[1]
+    _expect(q, _B16, "q")
+    if D != cache.k.shape[3]:
+        raise ValueError("q must have the cache's channels")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+    elif lse.shape != (T, Hq):
+        raise ValueError(f"lse must be [{T}, {Hq}]")
+    n = 0
+    if pages is not None:
+        if pages.shape[:2] != (T, H) or len(pages.shape) != 3:
+            raise ValueError(f"pages must be [{T}, {H}, n]")
+        n = pages.shape[2]
+    dev = q.get_device()
+    qp, qt, qh = _heads_of(q, dev, "q")
+    S, sp, lp = _step(cache, start, length, dev)
+    _launch_ws("csa2_kv8_attn", _KV8_ATTN.pack(
+        _KV8_ATTN.size, T, S, Hq, T if max_new is None else max_new, window,
+        1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, qp, qt, qh, sp, lp, *cache.fields(dev),
+        _dense(pages, dev, torch.int32, "pages"), n, _dense(out, dev, out.dtype, "out"), _float_type(out, "out"),
+        _dense(lse, dev, torch.float32, "lse")), ws, q.device, dev)
+    return out, lse
 
 
 def device_error():

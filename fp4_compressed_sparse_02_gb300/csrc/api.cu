@@ -338,6 +338,128 @@ csa2_status check_fp4_linear(const csa2_fp4_linear_args* a) {
   return CSA2_OK;
 }
 
+csa2_status check_kv8_cache(const csa2_kv8_cache& c, int32_t S, bool rows, bool means) {
+  REQUIRE(c.page_size == CSA2_PAGE_SIZE, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.page_size must be 64 (got %d)", c.page_size);
+  REQUIRE(c.num_pages > 0 && c.num_seqs > 0 && c.max_pages > 0, CSA2_ERR_INVALID_ARG,
+          "cache.num_pages/num_seqs/max_pages must be positive");
+  REQUIRE(c.num_pages <= (1 << 25), CSA2_ERR_UNSUPPORTED_SHAPE, "cache.num_pages must be <= 2^25");
+  REQUIRE(c.max_pages <= (1 << 24), CSA2_ERR_UNSUPPORTED_SHAPE, "cache.max_pages must be <= 2^24");
+  REQUIRE(c.D == 64 || c.D == 128, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.D must be 64 or 128 (got %d)", c.D);
+  REQUIRE(c.Hkv >= 1 && c.Hkv <= 256, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.Hkv must be in 1..256 (got %d)", c.Hkv);
+  REQUIRE(S >= 0 && S <= c.num_seqs, CSA2_ERR_INVALID_ARG, "S must be in 0..cache.num_seqs (got %d)", S);
+  REQUIRE(c.page_table && on(c.page_table, CSA2_F32), CSA2_ERR_INVALID_ARG, "cache.page_table is NULL or not aligned");
+  if (rows) {
+    REQUIRE(c.k && c.v && c.k_scale && c.v_scale, CSA2_ERR_INVALID_ARG, "cache.k/v/k_scale/v_scale is NULL");
+    REQUIRE(((uintptr_t)c.k & 15) == 0 && ((uintptr_t)c.v & 15) == 0, CSA2_ERR_INVALID_ARG,
+            "cache.k/v must be 16-byte aligned");
+    REQUIRE(on(c.k_scale, CSA2_F32) && on(c.v_scale, CSA2_F32), CSA2_ERR_INVALID_ARG, "cache scales are not aligned");
+  }
+  REQUIRE((c.mean == nullptr) == (c.mean_scale == nullptr), CSA2_ERR_INVALID_ARG,
+          "cache.mean and mean_scale go together");
+  REQUIRE(!means || c.mean, CSA2_ERR_INVALID_ARG, "cache.mean is NULL: the cache keeps no summaries");
+  if (c.mean)
+    REQUIRE(((uintptr_t)c.mean & 15) == 0 && on(c.mean_scale, CSA2_F32), CSA2_ERR_INVALID_ARG,
+            "cache.mean must be 16-byte aligned, mean_scale to its type");
+  return CSA2_OK;
+}
+
+// T rows of S sequences
+csa2_status check_kv8_rows(int32_t T, int32_t S, const int32_t* start, const int32_t* length) {
+  REQUIRE(T >= 0 && T <= (1 << 30), CSA2_ERR_INVALID_ARG, "T must be in 0..2^30");
+  if (T > 0 && S > 0)
+    REQUIRE(start && length && on(start, CSA2_F32) && on(length, CSA2_F32), CSA2_ERR_INVALID_ARG,
+            "start/length is NULL or not aligned");
+  return CSA2_OK;
+}
+
+csa2_status check_heads(int32_t Hq, int32_t Hkv) {
+  REQUIRE(Hq >= 1 && Hq % Hkv == 0 && Hq / Hkv <= 128, CSA2_ERR_UNSUPPORTED_SHAPE,
+          "Hq must be 1..128 times Hkv (got %d and %d)", Hq, Hkv);
+  return CSA2_OK;
+}
+
+csa2_status check_page_plan(const csa2_page_plan_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_page_plan_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(a->S >= 0 && a->S <= (1 << 20), CSA2_ERR_UNSUPPORTED_SHAPE, "S must be in 0..2^20 (got %d)", a->S);
+  REQUIRE(a->tokens >= 0 && a->tokens <= (1 << 30), CSA2_ERR_UNSUPPORTED_SHAPE, "tokens must be in 0..2^30 (got %d)",
+          a->tokens);
+  REQUIRE(a->max_pages > 0 && a->max_pages <= (1 << 24), CSA2_ERR_UNSUPPORTED_SHAPE,
+          "max_pages must be in 1..2^24 (got %d)", a->max_pages);
+  REQUIRE(a->num_free >= 0, CSA2_ERR_INVALID_ARG, "num_free < 0");
+  REQUIRE(a->start && a->free_head && a->new_head, CSA2_ERR_INVALID_ARG, "start/free_head/new_head is NULL");
+  if (a->S > 0)
+    REQUIRE(a->length && a->add && a->page_table && a->new_length, CSA2_ERR_INVALID_ARG,
+            "length/add/page_table/new_length is NULL");
+  REQUIRE(a->num_free == 0 || a->free_pages, CSA2_ERR_INVALID_ARG, "free_pages is NULL");
+  if (a->tokens > 0) REQUIRE(a->seq && a->pos && a->slot, CSA2_ERR_INVALID_ARG, "seq/pos/slot is NULL");
+  for (const int32_t* p : {a->length, a->add, a->free_pages, a->free_head, (const int32_t*)a->page_table,
+                           (const int32_t*)a->start, (const int32_t*)a->seq, (const int32_t*)a->pos,
+                           (const int32_t*)a->slot, (const int32_t*)a->new_length, (const int32_t*)a->new_head})
+    REQUIRE(on(p, CSA2_F32), CSA2_ERR_INVALID_ARG, "an array is not aligned to its type");
+  return CSA2_OK;
+}
+
+csa2_status check_kv8_append(const csa2_kv8_append_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_kv8_append_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  REQUIRE(is_float(a->x_dtype), CSA2_ERR_INVALID_ARG, "bad x_dtype");
+  csa2_status s = check_kv8_cache(a->cache, a->S, true, false);
+  if (s != CSA2_OK) return s;
+  s = check_kv8_rows(a->T, a->S, a->start, a->length);
+  if (s != CSA2_OK) return s;
+  if (a->T > 0)
+    REQUIRE(a->k && a->v && on(a->k, a->x_dtype) && on(a->v, a->x_dtype), CSA2_ERR_INVALID_ARG,
+            "k/v is NULL or not aligned to its type");
+  return CSA2_OK;
+}
+
+csa2_status check_kv8_select(const csa2_kv8_select_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_kv8_select_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  csa2_status s = check_kv8_cache(a->cache, a->S, false, true);
+  if (s != CSA2_OK) return s;
+  s = check_kv8_rows(a->T, a->S, a->start, a->length);
+  if (s != CSA2_OK) return s;
+  s = check_heads(a->Hq, a->cache.Hkv);
+  if (s != CSA2_OK) return s;
+  REQUIRE(a->k >= 2 && a->k <= 4096, CSA2_ERR_UNSUPPORTED_SHAPE, "k must be in 2..4096 (got %d)", a->k);
+  REQUIRE(a->first >= 0 && a->recent >= 1 && a->first <= a->k && a->recent <= a->k - a->first, CSA2_ERR_INVALID_ARG,
+          "need first >= 0, recent >= 1, first + recent <= k");
+  REQUIRE(a->max_length >= 0 && a->max_length <= (1 << 21), CSA2_ERR_UNSUPPORTED_SHAPE,
+          "max_length must be in 0..2^21 (got %d)", a->max_length);
+  if (a->T > 0) {
+    REQUIRE(a->q && on(a->q, CSA2_BF16), CSA2_ERR_INVALID_ARG, "q is NULL or not aligned to its type");
+    REQUIRE(a->pages && a->count && on(a->pages, CSA2_F32) && on(a->count, CSA2_F32), CSA2_ERR_INVALID_ARG,
+            "pages/count is NULL or not aligned");
+  }
+  return CSA2_OK;
+}
+
+csa2_status check_kv8_attn(const csa2_kv8_attn_args* a) {
+  REQUIRE(a, CSA2_ERR_INVALID_ARG, "args is NULL");
+  REQUIRE(a->struct_size == sizeof(csa2_kv8_attn_args), CSA2_ERR_INVALID_ARG, "struct_size mismatch");
+  csa2_status s = check_kv8_cache(a->cache, a->S, true, false);
+  if (s != CSA2_OK) return s;
+  s = check_kv8_rows(a->T, a->S, a->start, a->length);
+  if (s != CSA2_OK) return s;
+  s = check_heads(a->Hq, a->cache.Hkv);
+  if (s != CSA2_OK) return s;
+  REQUIRE(a->max_new >= 0, CSA2_ERR_INVALID_ARG, "max_new < 0");
+  REQUIRE(a->window >= 0, CSA2_ERR_INVALID_ARG, "window < 0");
+  REQUIRE(a->softmax_scale > 0.f && a->softmax_scale <= 1e30f, CSA2_ERR_INVALID_ARG, "softmax_scale must be in (0, 1e30]");
+  REQUIRE(is_float(a->out_dtype), CSA2_ERR_INVALID_ARG, "bad out_dtype");
+  if (a->pages)
+    REQUIRE(a->list_len >= 1 && a->list_len <= 4096, CSA2_ERR_UNSUPPORTED_SHAPE, "list_len must be in 1..4096 (got %d)",
+            a->list_len);
+  if (a->T > 0) {
+    REQUIRE(a->q && on(a->q, CSA2_BF16), CSA2_ERR_INVALID_ARG, "q is NULL or not aligned to its type");
+    REQUIRE(a->out && on(a->out, a->out_dtype), CSA2_ERR_INVALID_ARG, "out is NULL or not aligned to its type");
+    REQUIRE(on(a->pages, CSA2_F32) && on(a->lse, CSA2_F32), CSA2_ERR_INVALID_ARG, "pages/lse is not aligned");
+  }
+  return CSA2_OK;
+}
+
 csa2_status check_ws(size_t need, void* ws, size_t have) {
   REQUIRE(have >= need, CSA2_ERR_WORKSPACE_TOO_SMALL, "workspace needs %zu bytes, got %zu", need, have);
   REQUIRE(need == 0 || ws, CSA2_ERR_INVALID_ARG, "workspace is NULL");
@@ -485,6 +607,50 @@ csa2_status csa2_fp4_linear(const csa2_fp4_linear_args* a, void* stream) {
   return cuda_status(csa2::launch_fp4_linear(*a, static_cast<cudaStream_t>(stream)), "csa2_fp4_linear");
 }
 
+csa2_status csa2_page_plan(const csa2_page_plan_args* a, void* stream) {
+  csa2_status s = check_page_plan(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_page_plan(*a, static_cast<cudaStream_t>(stream)), "csa2_page_plan");
+}
+
+csa2_status csa2_kv8_append(const csa2_kv8_append_args* a, void* stream) {
+  csa2_status s = check_kv8_append(a);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_kv8_append(*a, static_cast<cudaStream_t>(stream)), "csa2_kv8_append");
+}
+
+csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* a, size_t* bytes) {
+  csa2_status s = check_kv8_select(a);
+  if (s != CSA2_OK) return s;
+  REQUIRE(bytes, CSA2_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = csa2::kv8_select_workspace_bytes(*a);
+  return ok();
+}
+
+csa2_status csa2_kv8_select(const csa2_kv8_select_args* a, void* ws, size_t ws_bytes, void* stream) {
+  csa2_status s = check_kv8_select(a);
+  if (s != CSA2_OK) return s;
+  s = check_ws(csa2::kv8_select_workspace_bytes(*a), ws, ws_bytes);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_kv8_select(*a, ws, static_cast<cudaStream_t>(stream)), "csa2_kv8_select");
+}
+
+csa2_status csa2_kv8_attn_workspace(const csa2_kv8_attn_args* a, size_t* bytes) {
+  csa2_status s = check_kv8_attn(a);
+  if (s != CSA2_OK) return s;
+  REQUIRE(bytes, CSA2_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = csa2::kv8_attn_workspace_bytes(*a);
+  return ok();
+}
+
+csa2_status csa2_kv8_attn(const csa2_kv8_attn_args* a, void* ws, size_t ws_bytes, void* stream) {
+  csa2_status s = check_kv8_attn(a);
+  if (s != CSA2_OK) return s;
+  s = check_ws(csa2::kv8_attn_workspace_bytes(*a), ws, ws_bytes);
+  if (s != CSA2_OK) return s;
+  return cuda_status(csa2::launch_kv8_attn(*a, ws, static_cast<cudaStream_t>(stream)), "csa2_kv8_attn");
+}
+
 const char* csa2_last_error_message(void) { return g_msg; }
 
 csa2_status csa2_get_device_error(uint32_t* word) {
@@ -493,7 +659,7 @@ csa2_status csa2_get_device_error(uint32_t* word) {
   if (e != cudaSuccess) return cuda_status(e, "csa2_get_device_error");
   *word = csa2::read_clear_error_compress() | csa2::read_clear_error_proj() | csa2::read_clear_error_index() |
           csa2::read_clear_error_score() | csa2::read_clear_error_attn() | csa2::read_clear_error_rope() |
-          csa2::read_clear_error_fp4();
+          csa2::read_clear_error_fp4() | csa2::read_clear_error_paged() | csa2::read_clear_error_kv8();
   csa2_status s = cuda_status(cudaGetLastError(), "csa2_get_device_error");
   if (s != CSA2_OK) return s;
   if (*word & CSA2_DEVERR_TIMEOUT) return fail(CSA2_ERR_TIMEOUT, "a bounded wait gave up (device word 0x%x)", *word);

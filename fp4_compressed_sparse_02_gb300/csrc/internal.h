@@ -65,4 +65,16 @@ cudaError_t launch_fp4_quant(const csa2_fp4_quant_args& a, cudaStream_t st);
 cudaError_t launch_fp4_linear(const csa2_fp4_linear_args& a, cudaStream_t st);
 uint32_t read_clear_error_fp4();
 
+// paged.cu
+cudaError_t launch_page_plan(const csa2_page_plan_args& a, cudaStream_t st);
+cudaError_t launch_kv8_append(const csa2_kv8_append_args& a, cudaStream_t st);
+size_t kv8_select_workspace_bytes(const csa2_kv8_select_args& a);
+cudaError_t launch_kv8_select(const csa2_kv8_select_args& a, void* ws, cudaStream_t st);
+uint32_t read_clear_error_paged();
+
+// kv8_attn.cu
+size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args& a);
+cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t st);
+uint32_t read_clear_error_kv8();
+
 }  // namespace csa2

@@ -69,6 +69,8 @@ typedef enum csa2_dtype { CSA2_BF16 = 0, CSA2_F32 = 1, CSA2_FP8E4M3 = 2, CSA2_FP
 #define CSA2_DEVERR_POS          0x40u /* RoPE position outside [0, rope_max_pos) */
 #define CSA2_DEVERR_TIMEOUT      0x80u /* a bounded wait on tensor-core or TMA completion gave up */
 #define CSA2_DEVERR_SMEM_ALIGN   0x100u /* dynamic shared memory was not 1024-byte aligned */
+#define CSA2_DEVERR_NO_PAGE      0x200u /* csa2_page_plan: the free pages ran out */
+#define CSA2_DEVERR_TOKENS       0x400u /* csa2_page_plan: new tokens beyond `tokens` or the page table */
 
 #define CSA2_PAGE_SIZE 64
 
@@ -591,6 +593,198 @@ typedef struct csa2_fp4_linear_args {
 } csa2_fp4_linear_args;
 
 csa2_status csa2_fp4_linear(const csa2_fp4_linear_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * The paged 8-bit key-value cache, for the layers of a model that are plain grouped-query
+ * attention (whole-context or sliding-window) beside its CSA2 layers.  Pages of 64 tokens and a
+ * page table as in csa2_cache (one table can serve both).  Hkv key heads of D channels; keys and
+ * values are E4M3 bytes with one float32 scale for each page, head and plane, a power of two;
+ * value = byte * scale.  A page that is full also has a summary of its keys for csa2_kv8_select.
+ * Not on the pages: these layers are the rest of the model.
+ * D in {64, 128}; Hkv in 1..256; num_pages <= 2^25, max_pages <= 2^24.
+ *
+ * The new tokens of a step (ragged).  start [S+1] and length [S] describe them to every call
+ * below: sequence s (row s of the page table) has its new tokens in rows start[s] .. start[s+1]-1,
+ * in order, and holds length[s] tokens once they are in, so that row t has position
+ * length[s] - (start[s+1] - t).  start ascends; sequences without new tokens have equal starts.
+ * Rows below start[0] and from start[S] on (padding) are not read, and their outputs are left as
+ * they were.  A row with a position outside [0, max_pages * 64) sets CSA2_DEVERR_PAGE_SLOT and a
+ * page id outside [0, num_pages) CSA2_DEVERR_PAGE_ID; what they would read or write is skipped.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_kv8_cache {
+  uint8_t* k;                  /* [num_pages][Hkv][64][D] E4M3; 16-byte aligned */
+  uint8_t* v;                  /* the same */
+  float* k_scale;              /* [num_pages][Hkv] */
+  float* v_scale;
+  int8_t* mean;                /* [num_pages][Hkv][D] summaries, 16-byte aligned; NULL = none are kept */
+  float* mean_scale;           /* [num_pages][Hkv]; NULL with mean */
+  const int32_t* page_table;   /* [num_seqs][max_pages] */
+  int32_t num_pages;
+  int32_t page_size;           /* must be 64 */
+  int32_t num_seqs;
+  int32_t max_pages;
+  int32_t Hkv;
+  int32_t D;
+} csa2_kv8_cache;
+
+/* ------------------------------------------------------------------------------
+ * csa2_page_plan -- the tables of a step, from what each request holds and gets: row ranges,
+ * sequences, positions and slots of the new tokens, and the page table extended by pages off a
+ * free list.  For sequences s = 0 .. S-1 in order:
+ *   n = add[s], as far as max_pages * 64 - length[s] and the rows left of `tokens` reach;
+ *   start[s+1] = start[s] + n (start[0] = 0), new_length[s] = length[s] + n;
+ *   its pages ceil(length[s] / 64) .. ceil(new_length[s] / 64) - 1 are the next ones of
+ *   free_pages, from free_pages[free_head] on, in order; new_head = free_head + pages taken;
+ *   row t of its tokens: seq[t] = s, pos[t] = length[s] + (t - start[s]),
+ *   slot[t] = 64 * page_table[s][pos / 64] + pos % 64.
+ * Rows from start[S] on get -1 in seq, pos and slot.  seq and pos are csa2_compress_quant's seq
+ * and entry (m = 1), new_length its sequences' n_vis.
+ * A cut add sets CSA2_DEVERR_TOKENS; a negative length or add counts as 0 and sets
+ * CSA2_DEVERR_N_VIS.  When the free pages run out the pages missing become -1 (their tokens'
+ * slots too), new_head = num_free, and CSA2_DEVERR_NO_PAGE is set.  A page id of an older table
+ * entry below 0 gives slot -1.
+ * new_length may be length and new_head free_head (a captured step then advances its own state);
+ * no other overlap.  Supported: S <= 2^20, tokens <= 2^30, max_pages <= 2^24; page ids below 2^25.
+ * Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_page_plan_args {
+  size_t struct_size;
+  int32_t S;
+  int32_t max_pages;
+  int32_t tokens;              /* rows of seq, pos and slot */
+  int32_t num_free;            /* entries of free_pages */
+  const int32_t* length;       /* device [S] tokens held */
+  const int32_t* add;          /* device [S] new tokens */
+  const int32_t* free_pages;   /* device [num_free] */
+  const int32_t* free_head;    /* device [1] entries already taken */
+  int32_t* page_table;         /* device [S][max_pages], extended in place */
+  int32_t* start;              /* device [S+1] */
+  int32_t* seq;                /* device [tokens] */
+  int32_t* pos;                /* device [tokens] */
+  int32_t* slot;               /* device [tokens] */
+  int32_t* new_length;         /* device [S] */
+  int32_t* new_head;           /* device [1] */
+} csa2_page_plan_args;
+
+csa2_status csa2_page_plan(const csa2_page_plan_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_kv8_append -- new keys and values [T][Hkv][D] into the cache.  For each page, head and
+ * plane that new tokens fall into, with `held` tokens of that page in the cache before:
+ *   a     = the largest finite |x| of the new tokens in the page
+ *   need  = the least power of two, 2^-126 at least, with a <= 448 * need
+ *   scale = need if held == 0, else max(need, old scale)
+ *   old bytes, if the scale grew: E4M3_RNE(byte * (old scale / scale))
+ *   new bytes: E4M3_RNE_satfinite(x / scale)  (exact quotients: one rounding)
+ * Infinities saturate and do not take part in a; NaN becomes a NaN byte.
+ * When the page is full afterwards and summaries are kept, for each head:
+ *   m    = the sum of its 64 rows' E4M3 key values (exact in float32; a NaN counts as 0)
+ *   u    = max|m| / 127 (float32 division);  mean = round(m / u), ties to even, 0 if u == 0
+ *   mean_scale = (u / 64) * k_scale  (float32 products)
+ * Bytes past a page's last token are left as they were.  Two sequences of one call must not write
+ * into the same page.
+ * x bf16 or float32; strides in elements, the channels of a head contiguous; any alignment of the
+ * element type, 16-byte aligned rows are faster.  Needs no workspace.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_kv8_append_args {
+  size_t struct_size;
+  int32_t T;                   /* rows of k and v */
+  int32_t S;                   /* sequences: rows of the page table from the first on */
+  csa2_dtype x_dtype;          /* of k and v */
+  const void* k;               /* device, element (t, h, c) at t*k_stride_t + h*k_stride_h + c */
+  const void* v;
+  int64_t k_stride_t;
+  int64_t k_stride_h;
+  int64_t v_stride_t;
+  int64_t v_stride_h;
+  const int32_t* start;        /* device [S+1] */
+  const int32_t* length;       /* device [S] */
+  csa2_kv8_cache cache;
+} csa2_kv8_append_args;
+
+csa2_status csa2_kv8_append(const csa2_kv8_append_args* args, void* stream);
+
+/* ------------------------------------------------------------------------------
+ * csa2_kv8_select -- the pages that each new token attends to, by a score of their summaries.
+ * For row t (position p, so P = p / 64 + 1 pages in sight) and key head h with query heads
+ * h*G .. h*G+G-1, G = Hq / Hkv:
+ *   c     = the sum of the G query heads (in float64, rounded once to float32)
+ *   u     = max|c| / 127 over finite c (float32 division);  r = round(c / u) in -127..127, ties
+ *           to even, 0 if u == 0; a NaN counts as 0, infinities as +-127
+ *   score = float32(r . mean[page][h]) * mean_scale[page][h]   (the product of whole numbers is exact)
+ *   kept  : pages j < first, pages j >= P - recent, and of the others the best scores up to k pages
+ *           in all, equal scores to the lower page; every page if P <= k.
+ * pages[t][h] = kept, ascending, padded with -1; count[t][h] = how many.  A row outside its page
+ * table keeps none.  All steps are exact or rounded once, so the result has no near-ties.
+ * Supported: q bf16, Hq a multiple of Hkv with G <= 128; 2 <= k <= 4096, first >= 0, recent >= 1,
+ * first + recent <= k; max_length <= 2^21 (a host bound of length; longer rows set
+ * CSA2_DEVERR_N_VIS and keep none).
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_kv8_select_args {
+  size_t struct_size;
+  int32_t T;
+  int32_t S;
+  int32_t Hq;
+  int32_t k;
+  int32_t first;
+  int32_t recent;
+  int32_t max_length;          /* host bound: every length[s] <= max_length */
+  const uint16_t* q;           /* device bf16, element (t, h, c) at t*q_stride_t + h*q_stride_h + c */
+  int64_t q_stride_t;
+  int64_t q_stride_h;
+  const int32_t* start;        /* device [S+1] */
+  const int32_t* length;       /* device [S] */
+  csa2_kv8_cache cache;        /* mean, mean_scale, page_table */
+  int32_t* pages;              /* device [T][Hkv][k] */
+  int32_t* count;              /* device [T][Hkv] */
+} csa2_kv8_select_args;
+
+csa2_status csa2_kv8_select(const csa2_kv8_select_args* args, void* workspace, size_t workspace_bytes,
+                            void* stream);
+csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* bytes);
+
+/* ------------------------------------------------------------------------------
+ * csa2_kv8_attn -- causal grouped-query attention of the new tokens over the cache, which holds
+ * their own keys and values already (csa2_kv8_append).  For row t at position p of sequence s and
+ * query head h, with key head h / G:
+ *   seen  = positions max(0, p + 1 - window) .. p  (window 0: from 0), and with `pages` only
+ *           those on the listed pages (csa2_kv8_select)
+ *   x_j   = softmax_scale * q . k_j;  out = sum_j softmax(x)_j v_j;  lse = log sum_j exp(x_j)
+ * An empty `seen` gives out = 0 and lse = -inf.  `pages` entries below 0 are skipped, in any order;
+ * a page listed twice counts twice; one past the page table sets CSA2_DEVERR_PAGE_SLOT.
+ * max_new: about how many new tokens the longest of the call's sequences has.  It only
+ * picks the kernel: results for any value stay within the precision below.
+ * Precision: products on fp16 tensor-core operands with float32 accumulation.  Keys and
+ * values are exact there; each head's q is scaled by a power of two (exact within 2^-28 of its
+ * largest element); probabilities are fp16 (2^-12 relative).  A NaN that a row does not see does
+ * not reach it.
+ * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
+ * window >= 0.
+ * -------------------------------------------------------------------------- */
+typedef struct csa2_kv8_attn_args {
+  size_t struct_size;
+  int32_t T;
+  int32_t S;
+  int32_t Hq;
+  int32_t max_new;
+  int32_t window;
+  float softmax_scale;
+  const uint16_t* q;           /* device bf16, element (t, h, c) at t*q_stride_t + h*q_stride_h + c */
+  int64_t q_stride_t;
+  int64_t q_stride_h;
+  const int32_t* start;        /* device [S+1] */
+  const int32_t* length;       /* device [S] */
+  csa2_kv8_cache cache;
+  const int32_t* pages;        /* device [T][Hkv][list_len], or NULL = all pages */
+  int32_t list_len;
+  void* out;                   /* device [T][Hq][D] */
+  csa2_dtype out_dtype;        /* CSA2_BF16 or CSA2_F32 */
+  float* lse;                  /* device f32 [T][Hq], or NULL */
+} csa2_kv8_attn_args;
+
+csa2_status csa2_kv8_attn(const csa2_kv8_attn_args* args, void* workspace, size_t workspace_bytes,
+                          void* stream);
+csa2_status csa2_kv8_attn_workspace(const csa2_kv8_attn_args* args, size_t* bytes);
 
 /* ------------------------------------------------------------------------------
  * Helpers
