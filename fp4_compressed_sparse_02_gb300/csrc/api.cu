@@ -346,6 +346,7 @@ csa2_status check_kv8_cache(const csa2_kv8_cache& c, int32_t S, bool rows, bool 
   REQUIRE(c.max_pages <= (1 << 24), CSA2_ERR_UNSUPPORTED_SHAPE, "cache.max_pages must be <= 2^24");
   REQUIRE(c.D == 64 || c.D == 128, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.D must be 64 or 128 (got %d)", c.D);
   REQUIRE(c.Hkv >= 1 && c.Hkv <= 256, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.Hkv must be in 1..256 (got %d)", c.Hkv);
+  REQUIRE((int64_t)c.num_pages * c.Hkv <= INT32_MAX, CSA2_ERR_UNSUPPORTED_SHAPE, "cache.num_pages * Hkv must be below 2^31");
   REQUIRE(S >= 0 && S <= c.num_seqs, CSA2_ERR_INVALID_ARG, "S must be in 0..cache.num_seqs (got %d)", S);
   REQUIRE(c.page_table && on(c.page_table, CSA2_F32), CSA2_ERR_INVALID_ARG, "cache.page_table is NULL or not aligned");
   if (rows) {
@@ -445,6 +446,7 @@ csa2_status check_kv8_attn(const csa2_kv8_attn_args* a) {
   if (s != CSA2_OK) return s;
   s = check_heads(a->Hq, a->cache.Hkv);
   if (s != CSA2_OK) return s;
+  REQUIRE(a->S <= (1 << 18), CSA2_ERR_UNSUPPORTED_SHAPE, "S must be at most 2^18 (got %d)", a->S);
   REQUIRE(a->max_new >= 0, CSA2_ERR_INVALID_ARG, "max_new < 0");
   REQUIRE(a->window >= 0, CSA2_ERR_INVALID_ARG, "window < 0");
   REQUIRE(a->softmax_scale > 0.f && a->softmax_scale <= 1e30f, CSA2_ERR_INVALID_ARG, "softmax_scale must be in (0, 1e30]");

@@ -1,6 +1,14 @@
 // Attention over the paged 8-bit cache (csa2_kv8_attn).
+//
+// Rows are (new token, query head of the group) pairs of one sequence and key head; a tile of rows
+// against the tiles of its sequence's pages is one stream.  k_kv8_stream runs streams of at most 16 rows.
+#include <limits.h>
+#include <math.h>
+
 #include "internal.h"
 #include "kv8.cuh"
+#include "tc.cuh"
+#include "tmap.h"
 
 namespace csa2 {
 
@@ -9,109 +17,772 @@ CSA2_DEFINE_ERROR_WORD(g_err_kv8);
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kWaitPolls = 1u << 22;
 
-__device__ __forceinline__ void store_out(const csa2_kv8_attn_args& a, long long i, float v) {
-  if (a.out_dtype == CSA2_F32) reinterpret_cast<float*>(a.out)[i] = v;
-  else reinterpret_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(v);
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
-// A CTA a (row, query head), four warps that take every fourth page: a key a lane for the scores, D / 32 channels a
-// lane for the values.
+__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(map), "r"((uint32_t)__cvta_generic_to_shared(mbar)),
+         "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+// The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and the one that undoes it;
+// 1 for a row of zeros or with an infinity or NaN.
+__device__ __forceinline__ void row_factor(float top, float& f, float& undo) {
+  const int e = (int)(__float_as_uint(top) >> 23);         // biased exponent; 0: zero or below 2^-126
+  f = undo = 1.f;
+  if (top == 0.f || e >= 255) return;
+  const int k = 14 - (e - 127);                            // -113 .. 141
+  const int k1 = k > 127 ? 127 : k;
+  f = __uint_as_float((uint32_t)(k1 + 127) << 23);
+  undo = k1 == 127 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)(127 - k1) << 23);   // 2^-127 is subnormal
+}
+
+// ---- rows of a sequence ----------------------------------------------------------------------
+
+struct Rows {
+  int t0, n;                             // first row of the step, rows x group
+  int end, length;                       // start[s+1], length[s]
+};
+
+__device__ __forceinline__ Rows rows_of(const csa2_kv8_attn_args& a, int s, int G) {
+  Rows r;
+  r.t0 = a.start[s];
+  r.end = a.start[s + 1];
+  r.length = a.length[s];
+  const int e = min(r.end, a.T);
+  r.n = r.t0 >= 0 && e > r.t0 ? (e - r.t0) * G : 0;
+  return r;
+}
+
+// What row t sees: positions [lo, hi).
+__device__ __forceinline__ void seen_by(const csa2_kv8_attn_args& a, const Rows& r, int t, int& lo, int& hi) {
+  const long long p = (long long)r.length - ((long long)r.end - t);
+  if (p < 0 || p >= (long long)a.cache.max_pages * kPage) {
+    raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
+    lo = hi = 0;
+    return;
+  }
+  hi = (int)p + 1;
+  lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
+}
+
+// ---- streams of at most 16 rows --------------------------------------------------------------
+//
+// Every warp is on its own: the half pages (32 tokens) of all streams, one stream after the other,
+// are cut into equal spans, one for each warp, whatever the sequences' lengths are.  A stream cut by
+// the border of a span leaves its parts (running maximum, sum, unnormalised output) in the
+// workspace and k_kv8_join puts them together, in the order of the warps.
+//
+// A warp's half pages come by TMA into its own ring of 8 KB stages (keys, then values), swizzled so that
+// the reads below meet no bank twice.  E4M3 bytes become fp16 pairs in registers (exact), products are
+// mma.sync m16n8k16: rows on M, 8 tokens (scores) or 8 channels (values) on N.  A lane's K fragment is 32
+// consecutive channels of one token (a permutation of the channels that Q's fragments share), its V
+// fragment the bytes of two neighbouring tokens interleaved; the scores' accumulators are the weights' A
+// fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
+// its partial output, in float32.
+constexpr int kWarps = 4, kStreamCtas = 2 * 152, kSpans = kStreamCtas * kWarps, kLeast = 4;
+constexpr int kHalf = kPage / 2;
+
 template <int D>
-__global__ void __launch_bounds__(128) k_kv8_attn(const csa2_kv8_attn_args a) {
-  constexpr int kPer = D / 32;
-  __shared__ float q[D], s_o[4][D], s_m[4], s_l[4];
+struct Ring {
+  static constexpr int kStage = 2 * kHalf * D, kStages = 24576 / kStage;
+  static constexpr int kBytes = kWarps * kStages * kStage;
+};
+
+struct Part {                            // a stream that begins in a span and does not end there
+  int rows, t0, r0, h;                   // rows = 0: none
+};
+
+struct StreamParams {
+  csa2_kv8_attn_args a;
+  int G, aligned;                        // aligned: bit 0 q's rows, bit 1 out's rows on 16 bytes
+  Part* part;                            // [kSpans]
+  int* head;                             // [kSpans] 0: no part of an earlier stream, 1: it goes on, 2: it ends here
+  float2* ml;                            // [kSpans][2][16] maximum, sum; [1]: of the stream that goes on from here
+  float* o;                              // [kSpans][2][16][D]
+};
+
+// One row's channels, held as v[0 .. D/4) by the four lanes of a quad: dims D/4 * c ...
+template <int D>
+__device__ __forceinline__ void store_row(const csa2_kv8_attn_args& a, long long row, int c, const float* v, bool aligned) {
+  const long long at = row * D + c * (D / 4);
+  if (a.out_dtype == CSA2_F32) {
+    float* out = reinterpret_cast<float*>(a.out) + at;
+    if (aligned) {
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < D / 4; ++i) out[i] = v[i];
+    }
+    return;
+  }
+  uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = bf16x2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+    if (aligned) {
+      reinterpret_cast<uint4*>(out)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) out[8 * i + j] = (uint16_t)(w[j / 2] >> 16 * (j & 1));
+    }
+  }
+}
+
+// RT: rows of a tile, 8 or 16.  LIST: streams are (row, head) pairs over their listed pages.
+template <int D, int RT, bool LIST>
+__global__ void __launch_bounds__(32 * kWarps, 2)
+k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const StreamParams p) {
+  constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kNt = D / 8, kR = RT / 8;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ uint64_t bars[kWarps][kSt];
+  __shared__ float2 s_scale[kWarps][kSt];
+  __shared__ int s_token[kWarps][kSt];
+  const csa2_kv8_attn_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  const int G = p.G, Hkv = c.Hkv, span = blockIdx.x * kWarps + warp;
+  uint8_t* ring = smem + warp * kSt * kStage;
+  const uint32_t ring_s = smem_u32(ring);
+  if ((smem_u32(smem) & 1023) != 0) {                      // uniform: the ring's swizzle counts on it
+    if (threadIdx.x == 0) raise_error(&g_err_kv8, CSA2_DEVERR_SMEM_ALIGN);
+    return;
+  }
+  if (lane < kSt) tc::mbar_init(&bars[warp][lane], 1);
+  __syncwarp();
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, hq = blockIdx.y, h = hq / (a.Hq / c.Hkv), lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int s = find_seq(a.start, a.S, t);
-  if (s < 0) return;
-  const int pos = row_pos(c, a.start, a.length, s, t, &g_err_kv8);
-  if (threadIdx.x < D)
-    q[threadIdx.x] = bf16_bits_to_f32(a.q[t * a.q_stride_t + hq * a.q_stride_h + threadIdx.x]) * (a.softmax_scale * kLog2e);
-  __syncthreads();
-  const int from = a.window > 0 && pos + 1 > a.window ? pos + 1 - a.window : 0;
-  const int* list = a.pages ? a.pages + ((long long)t * c.Hkv + h) * a.list_len : nullptr;
-  const int first = list ? 0 : from >> kPageShift;
-  const int last = pos < 0 ? 0 : list ? a.list_len : (pos >> kPageShift) + 1;
-  float m = -INFINITY, l = 0.f, o[kPer] = {};
-  for (int i = first + warp; i < last; i += 4) {
-    const int j = list ? list[i] : i;
-    if (j < 0) continue;
-    if (j >= c.max_pages) {
-      if (lane == 0) raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
-      continue;
+
+  // The work: half pages of sequence s, all its streams together.
+  auto work = [&](int s, int& count, int& first) -> long long {
+    const Rows r = rows_of(a, s, G);
+    const long long limit = (long long)c.max_pages * kPage;
+    const long long len = r.length < 0 ? 0 : r.length < limit ? r.length : limit;
+    long long lo = 0;
+    if (a.window > 0) {
+      lo = (long long)r.length - ((long long)r.end - r.t0) + 1 - a.window;
+      lo = lo < 0 ? 0 : lo < len ? lo : len;
     }
-    if (j > pos >> kPageShift) continue;
-    const int page = page_id(c, s, j, &g_err_kv8);
-    if (page < 0) continue;
-    const long long ph = (long long)page * c.Hkv + h;
-    const float ks = c.k_scale[ph], vs = c.v_scale[ph];
-    for (int b = 0; b < kPage; b += 32) {
-      const int token = j * kPage + b + lane;
-      const bool seen = token <= pos && token >= from;
-      const uint32_t see = __ballot_sync(0xffffffffu, seen);
-      if (!see) continue;
-      float x = -INFINITY;
-      if (seen) {
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(c.k + (ph * kPage + b + lane) * D);
-        float dot = 0.f;
-        for (int e = 0; e < D / 4; ++e) {
-          float f[4];
-          e4m3x4_to_f32(k[e], f);
-          dot += f[0] * q[4 * e] + f[1] * q[4 * e + 1] + f[2] * q[4 * e + 2] + f[3] * q[4 * e + 3];
+    first = (int)(lo / kHalf);
+    count = (int)((len + kHalf - 1) / kHalf) - first;
+    if (count < 1) count = 1;            // rows that see nothing are written all the same
+    return (long long)((r.n + RT - 1) / RT) * Hkv * count;
+  };
+  const int list_tiles = (G + RT - 1) / RT;
+  long long total, base = 0, mine = 0;   // of sequence (LIST: of everything) `s`: its begin and its work
+  int s = 0, count = 0, first = 0;
+  long long pos, stop, per;
+  auto cut = [&] {
+    per = (total + kSpans - 1) / kSpans;
+    if (per < kLeast) per = kLeast;
+    pos = span * per;
+    stop = pos + per < total ? pos + per : total;
+  };
+  if constexpr (LIST) {
+    count = 2 * a.list_len;
+    total = mine = (long long)a.T * list_tiles * Hkv * count;
+    cut();
+  } else {
+    // Sums over 32 sequences at a time, then within the 32 that hold this warp's begin.
+    long long* sums = reinterpret_cast<long long*>(smem + Ring<D>::kBytes);
+    const int chunks = (a.S + 31) / 32;
+    long long before = 0;
+    int chunk = 0;
+    if (chunks > 1) {
+      for (int i = warp; i < chunks; i += kWarps) {
+        int x, y;
+        long long w = i * 32 + lane < a.S ? work(i * 32 + lane, x, y) : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        if (lane == 0) sums[i] = w;
+      }
+      __syncthreads();
+      total = 0;
+      for (int i = 0; i < chunks; i += 32) {
+        long long w = i + lane < chunks ? sums[i + lane] : 0;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+        total += w;
+      }
+      cut();
+      if (pos < stop)
+        while (before + sums[chunk] <= pos) before += sums[chunk++];
+    }
+    long long w = 0;
+    int x = 0, y = 0;
+    if (chunk * 32 + lane < a.S) w = work(chunk * 32 + lane, x, y);
+    long long inc = w;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    if (chunks <= 1) {
+      total = __shfl_sync(0xffffffffu, inc, 31);
+      cut();
+    }
+    if (pos < stop) {
+      const int at = __ffs(__ballot_sync(0xffffffffu, before + inc > pos)) - 1;
+      s = chunk * 32 + at;
+      mine = __shfl_sync(0xffffffffu, w, at);
+      base = before + __shfl_sync(0xffffffffu, inc, at) - mine;
+      count = __shfl_sync(0xffffffffu, x, at);
+      first = __shfl_sync(0xffffffffu, y, at);
+    }
+  }
+
+  Part part = {0, 0, 0, 0};
+  int head = 0;
+  uint32_t phase = 0;                    // of each stage's barrier
+  bool dead = false;
+  while (pos < stop) {
+    if constexpr (!LIST) {
+      while (pos >= base + mine) {
+        base += mine;
+        mine = work(++s, count, first);
+      }
+    }
+    // ---- the stream, and the span's part of it
+    const long long rel = pos - base;
+    const long long u = rel / count;
+    const int x = (int)(rel - u * count), take = (int)(count - x < stop - pos ? count - x : stop - pos);
+    const int h = (int)(u % Hkv);
+    const bool begins = x == 0, ends = x + take == count;
+    int r0;                              // first row of the tile
+    Rows rows;
+    const int* list = nullptr;
+    if constexpr (LIST) {
+      const int tt = (int)(u / Hkv), t = tt / list_tiles;
+      r0 = tt % list_tiles * RT;
+      s = find_seq(a.start, a.S, t);
+      if (s < 0) {                       // padding: nothing to write, not even parts
+        if (!begins) head = ends ? 2 : 1;
+        pos += take;
+        continue;
+      }
+      rows = rows_of(a, s, G);
+      rows.t0 = t;
+      rows.n = G;
+      list = a.pages + ((long long)t * Hkv + h) * a.list_len;
+    } else {
+      r0 = (int)(u / Hkv) * RT;
+      rows = rows_of(a, s, G);
+    }
+    const int nrows = min(RT, rows.n - r0);
+    // ---- this lane's rows g and g + 8: what they see, their query in fragments
+    int lo[kR], hi[kR], lo_min = INT_MAX, lo_max = 0, hi_min = INT_MAX, hi_max = 0;
+    float mul[kR], m[kR], l[kR];
+    uint32_t qa[kKs][2 * kR];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      const int r = g + 8 * i;
+      lo[i] = 0;
+      hi[i] = INT_MAX;
+      mul[i] = 0.f;
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+      float v[D / 4];
+#pragma unroll
+      for (int e = 0; e < D / 4; ++e) v[e] = 0.f;
+      if (r < nrows) {
+        const int t = rows.t0 + (r0 + r) / G;
+        seen_by(a, rows, t, lo[i], hi[i]);
+        lo_min = min(lo_min, lo[i]);
+        lo_max = max(lo_max, lo[i]);
+        hi_min = min(hi_min, hi[i]);
+        hi_max = max(hi_max, hi[i]);
+        const uint16_t* q = a.q + t * a.q_stride_t + (long long)(h * G + (r0 + r) % G) * a.q_stride_h + q4 * (D / 4);
+        if (p.aligned & 1) {
+#pragma unroll
+          for (int e = 0; e < D / 32; ++e) {
+            const uint4 w = reinterpret_cast<const uint4*>(q)[e];
+            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[8 * e + 2 * j] = __uint_as_float(ws[j] << 16);
+              v[8 * e + 2 * j + 1] = __uint_as_float(ws[j] & 0xffff0000u);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) v[e] = bf16_bits_to_f32(q[e]);
         }
-        x = dot * ks;
       }
-      float top = x;
+      float top = 0.f;
 #pragma unroll
-      for (int e = 16; e > 0; e >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-      const float mn = fmaxf(m, top), base = mn == -INFINITY ? 0.f : mn;
-      const float alpha = exp2f(m - base), p = seen ? exp2f(x - base) : 0.f;
-      m = mn;
-      l = l * alpha + p;
+      for (int e = 0; e < D / 4; ++e) top = fabsf(v[e]) >= top ? fabsf(v[e]) : (v[e] != v[e] ? INFINITY : top);
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      float f, undo;
+      row_factor(top, f, undo);
+      mul[i] = undo * (a.softmax_scale * kLog2e);
 #pragma unroll
-      for (int e = 0; e < kPer; ++e) o[e] *= alpha;
-      for (uint32_t left = see; left; left &= left - 1) {
-        const int r = __ffs(left) - 1;
-        const float w = __shfl_sync(0xffffffffu, p, r) * vs;
-        const uint8_t* v = c.v + (ph * kPage + b + r) * D + lane * kPer;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) o[e] += w * e4m3_to_f32(v[e]);
+      for (int j = 0; j < kKs; ++j) {
+        qa[j][i] = f16x2(v[4 * j] * f, v[4 * j + 1] * f);
+        qa[j][kR + i] = f16x2(v[4 * j + 2] * f, v[4 * j + 3] * f);
       }
     }
-  }
 #pragma unroll
-  for (int e = 16; e > 0; e >>= 1) l += __shfl_xor_sync(0xffffffffu, l, e);
+    for (int o = 4; o <= 16; o <<= 1) {
+      lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+      lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+      hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
+      hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
+    }
+    float o[kNt][2 * kR];
+#pragma unroll
+    for (int n = 0; n < kNt; ++n)
+#pragma unroll
+      for (int e = 0; e < 2 * kR; ++e) o[n][e] = 0.f;
+
+    // ---- half pages y0 .. y1 of the stream (LIST: of the list, else from `first` on), those in sight
+    int y0 = x, y1 = x + take;
+    if constexpr (!LIST) {
+      y0 = max(y0, lo_min / kHalf - first);
+      y1 = min(y1, (hi_max + kHalf - 1) / kHalf - first);
+    }
+    int bt = -1;                         // lane i: token, page and scales of half page batch + i; bt < 0: to be skipped
+    int bp = 0;
+    float bk = 0.f, bv = 0.f;
+    auto load_batch = [&](int b) {
+      bt = -1;
+      const int y = b + lane;
+      if (y < y1) {
+        int j, half;
+        if constexpr (LIST) {
+          j = list[y >> 1];
+          half = y & 1;
+          if (j >= c.max_pages) {
+            raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
+            j = -1;
+          }
+        } else {
+          j = (first + y) >> 1;
+          half = (first + y) & 1;
+        }
+        const int token = j * kPage + half * kHalf;
+        if (j >= 0 && token < hi_max && token + kHalf > lo_min) {
+          const int page = page_id(c, s, j, &g_err_kv8);
+          if (page >= 0) {
+            bt = token;
+            bp = page;
+            const long long ph = (long long)page * Hkv + h;
+            bk = c.k_scale[ph];
+            bv = c.v_scale[ph];
+          }
+        }
+      }
+    };
+    int issued = y0;
+    auto issue = [&] {                   // the next half page into its stage
+      const int b = (issued - y0) & 31;
+      if (b == 0) load_batch(issued);
+      const int st = (issued - y0) % kSt;
+      const int token = __shfl_sync(0xffffffffu, bt, b), page = __shfl_sync(0xffffffffu, bp, b);
+      const float ks = __shfl_sync(0xffffffffu, bk, b), vs = __shfl_sync(0xffffffffu, bv, b);
+      if (lane == 0) {
+        s_token[warp][st] = token;
+        if (token >= 0) {
+          s_scale[warp][st] = make_float2(ks, vs);
+          tc::mbar_arrive_expect_tx(&bars[warp][st], kStage);
+          tma_load_3d(ring + st * kStage, &mk, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
+          tma_load_3d(ring + st * kStage + kHalf * D, &mv, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
+        }
+      }
+      ++issued;
+    };
+    for (int i = 0; i < kSt - 1; ++i)
+      if (issued < y1) issue();
+    for (int y = y0; y < y1; ++y) {
+      __syncwarp();                      // every lane has read the stage that is filled next
+      if (issued < y1 && !dead) issue();
+      __syncwarp();
+      const int st = (y - y0) % kSt;
+      if (y >= issued) break;            // after a wait that gave up
+      const int token0 = s_token[warp][st];
+      if (token0 < 0) continue;
+      if (!tc::mbar_wait(&bars[warp][st], phase >> st & 1, kWaitPolls)) {
+        if (!dead) raise_error(&g_err_kv8, CSA2_DEVERR_TIMEOUT);
+        dead = true;
+      }
+      dead = __any_sync(0xffffffffu, dead);
+      phase ^= 1u << st;
+      if (dead) continue;                // the copies in flight are still waited for
+      const float2 sc = s_scale[warp][st];
+      const uint32_t kb = ring_s + st * kStage, vb = kb + kHalf * D;
+      const bool border = token0 < lo_max || token0 + kHalf > hi_min;
+      // scores: four tiles of 8 tokens, this lane's tokens 8 n + 2 q4, + 1 in rows g, g + 8
+      float sx[4][2 * kR];
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const int r = 8 * n + g;
+        uint32_t w[D / 16];
+        if constexpr (D == 128) {
+          const uint4 w0 = lds128(kb + r * 128 + (((2 * q4) ^ (r & 7)) << 4));
+          const uint4 w1 = lds128(kb + r * 128 + (((2 * q4 + 1) ^ (r & 7)) << 4));
+          w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+          w[4] = w1.x; w[5] = w1.y; w[6] = w1.z; w[7] = w1.w;
+        } else {
+          const uint4 w0 = lds128(kb + r * 64 + ((q4 ^ (r >> 1 & 3)) << 4));
+          w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
+        }
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int j = 0; j < kKs; ++j) {
+          const uint32_t b0 = e4m3x2_lo_f16x2(w[j]), b1 = e4m3x2_hi_f16x2(w[j]);
+          if constexpr (kR == 2) mma_f16_16816(d, qa[j][0], qa[j][1], qa[j][2], qa[j][3], b0, b1);
+          else mma_f16_16816(d, qa[j][0], 0u, qa[j][1], 0u, b0, b1);
+        }
+#pragma unroll
+        for (int e = 0; e < 2 * kR; ++e) sx[n][e] = d[e];
+      }
+      float alpha[kR];
+#pragma unroll
+      for (int i = 0; i < kR; ++i) {
+        const float f = mul[i] * sc.x;
+        float top = -INFINITY;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = sx[n][2 * i + e] * f;
+            if (border) {
+              const int token = token0 + 8 * n + 2 * q4 + e;
+              v = token >= lo[i] && token < hi[i] ? v : -INFINITY;
+            }
+            sx[n][2 * i + e] = v;
+            top = fmaxf(top, v);
+          }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const float mn = fmaxf(m[i], top), z = mn == -INFINITY ? 0.f : mn;
+        alpha[i] = ex2(m[i] - z);
+        m[i] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            sx[n][2 * i + e] = ex2(sx[n][2 * i + e] - z);
+            sum += sx[n][2 * i + e];
+          }
+        l[i] = l[i] * alpha[i] + sum;
+      }
+      bool rescale = alpha[0] != 1.f;
+      if constexpr (kR == 2) rescale |= alpha[1] != 1.f;
+      if (__any_sync(0xffffffffu, rescale)) {
+#pragma unroll
+        for (int n = 0; n < kNt; ++n)
+#pragma unroll
+          for (int e = 0; e < 2 * kR; ++e) o[n][e] *= alpha[e / 2];
+      }
+      // values: this lane's rows 16 kt + {2 q4, 2 q4 + 1, 8 + 2 q4, 9 + 2 q4}, channels D/8 * g ...
+      constexpr int kVw = D / 32;        // words of a row a lane
+      uint32_t vw[2][4][kVw];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * kt + 2 * q4 + (e & 1) + 8 * (e >> 1);
+          if constexpr (D == 128) {
+            const uint4 w = lds128(vb + r * 128 + ((g ^ (r & 7)) << 4));
+            vw[kt][e][0] = w.x; vw[kt][e][1] = w.y; vw[kt][e][2] = w.z; vw[kt][e][3] = w.w;
+          } else {
+            const uint2 w = lds64(vb + r * 64 + (((g >> 1) ^ (r >> 1 & 3)) << 4) + (g & 1) * 8);
+            vw[kt][e][0] = w.x; vw[kt][e][1] = w.y;
+          }
+        }
+      uint32_t pa[2][2 * kR];
+#pragma unroll
+      for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+          pa[kt][i] = f16x2(sx[2 * kt][2 * i], sx[2 * kt][2 * i + 1]);
+          pa[kt][kR + i] = f16x2(sx[2 * kt + 1][2 * i], sx[2 * kt + 1][2 * i + 1]);
+        }
+      auto product = [&](const uint32_t (&pw)[2][2 * kR], int w, float (&d)[4][4]) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt) {
+          uint32_t b[2][2];              // [token pair][bytes 0, 1 or 2, 3]: bytes of both tokens side by side
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            b[e][0] = __byte_perm(vw[kt][2 * e][w], vw[kt][2 * e + 1][w], 0x5140);
+            b[e][1] = __byte_perm(vw[kt][2 * e][w], vw[kt][2 * e + 1][w], 0x7362);
+          }
+#pragma unroll
+          for (int n = 0; n < 4; ++n) {
+            const uint32_t b0 = n & 1 ? e4m3x2_hi_f16x2(b[0][n >> 1]) : e4m3x2_lo_f16x2(b[0][n >> 1]);
+            const uint32_t b1 = n & 1 ? e4m3x2_hi_f16x2(b[1][n >> 1]) : e4m3x2_lo_f16x2(b[1][n >> 1]);
+            if constexpr (kR == 2) mma_f16_16816(d[n], pw[kt][0], pw[kt][1], pw[kt][2], pw[kt][3], b0, b1);
+            else mma_f16_16816(d[n], pw[kt][0], 0u, pw[kt][1], 0u, b0, b1);
+          }
+        }
+      };
+      if (border) {
+        // Rows of V that no row of the tile sees may hold anything: they count as zero.  A NaN that only some rows
+        // see is taken out of the product and given to those rows alone.
+        bool nan = false;
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int token = token0 + 16 * kt + 2 * q4 + (e & 1) + 8 * (e >> 1);
+            const bool see = token >= lo_min && token < hi_max;
+#pragma unroll
+            for (int w = 0; w < kVw; ++w) {
+              vw[kt][e][w] = see ? vw[kt][e][w] : 0u;
+              nan |= (((vw[kt][e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+            }
+          }
+        if (__any_sync(0xffffffffu, nan)) {
+          uint32_t keep[2][4][kVw], see[2][2 * kR];
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int w = 0; w < kVw; ++w) {
+                const uint32_t v = vw[kt][e][w], at = (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in each NaN's byte
+                keep[kt][e][w] = v & ~(at * 0xffu);
+                vw[kt][e][w] = at * 0x38u;                   // E4M3 of 1
+              }
+#pragma unroll
+            for (int i = 0; i < kR; ++i)
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int token = token0 + 16 * kt + 8 * half + 2 * q4;
+                see[kt][half * kR + i] = (token >= lo[i] && token < hi[i] ? 0x3c00u : 0u) |
+                                         (token + 1 >= lo[i] && token + 1 < hi[i] ? 0x3c000000u : 0u);
+              }
+          }
+#pragma unroll
+          for (int w = 0; w < kVw; ++w) {
+            float d[4][4];
+            product(see, w, d);
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+              for (int e = 0; e < 2 * kR; ++e)
+                if (d[n][e] != 0.f) o[4 * w + n][e] = NAN;
+          }
+#pragma unroll
+          for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+              for (int w = 0; w < kVw; ++w) vw[kt][e][w] = keep[kt][e][w];
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < kVw; ++w) {
+        float d[4][4];
+        product(pa, w, d);
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int e = 0; e < 2 * kR; ++e) o[4 * w + n][e] += d[n][e] * sc.y;
+      }
+    }
+    __syncwarp();                        // the stages are free for the next stream
+    // ---- its result, or its part
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = g + 8 * i;
+      if (r < nrows) {
+        float v[D / 4];                  // channels D/4 * q4 ...: of columns 2 q4 and 2 q4 + 1 of every tile
+#pragma unroll
+        for (int n = 0; n < kNt; ++n) {
+          v[n] = o[n][2 * i];
+          v[kNt + n] = o[n][2 * i + 1];
+        }
+        if (begins && ends) {
+          const long long row = (long long)(rows.t0 + (r0 + r) / G) * a.Hq + h * G + (r0 + r) % G;
+          const float inv = l[i] == 0.f ? 0.f : __fdiv_rn(1.f, l[i]);
+#pragma unroll
+          for (int e = 0; e < D / 4; ++e) v[e] *= inv;
+          store_row<D>(a, row, q4, v, p.aligned & 2);
+          if (q4 == 0 && a.lse) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+        } else {
+          const long long at = ((long long)span * 2 + (begins ? 1 : 0)) * 16 + r;
+          if (q4 == 0) p.ml[at] = make_float2(m[i], l[i]);
+          float4* dst = reinterpret_cast<float4*>(p.o + at * D + q4 * (D / 4));
+#pragma unroll
+          for (int e = 0; e < D / 16; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+      }
+    }
+    if (!begins) head = ends ? 2 : 1;
+    else if (!ends) part = Part{nrows, rows.t0, r0, h};
+    pos += take;
+  }
   if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+    p.part[span] = part;
+    p.head[span] = head;
   }
+}
+
+// A CTA a span: the stream that begins there and goes on in the next ones, a warp a row, a lane D / 32 channels.
+template <int D>
+__global__ void __launch_bounds__(256) k_kv8_join(const StreamParams p) {
+  constexpr int kPer = D / 32;
+  const csa2_kv8_attn_args& a = p.a;
+  pdl_wait();
+  pdl_trigger();
+  const int w0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Part part = p.part[w0];
+  if (part.rows == 0) return;
+  int last = w0 + 1;                     // the span in which the stream ends
+  while (true) {
+    const int w = last + lane;
+    const uint32_t e = __ballot_sync(0xffffffffu, w >= kSpans || p.head[w] != 1);
+    if (e) {
+      last += __ffs(e) - 1;
+      break;
+    }
+    last += 32;
+  }
+  last = min(last, kSpans - 1);
+  for (int r = warp; r < part.rows; r += 8) {
+    auto at = [&](int w) { return ((long long)w * 2 + (w == w0 ? 1 : 0)) * 16 + r; };
+    float top = -INFINITY;
+    for (int w = w0 + lane; w <= last; w += 32) top = fmaxf(top, p.ml[at(w)].x);
 #pragma unroll
-  for (int e = 0; e < kPer; ++e) s_o[warp][lane * kPer + e] = o[e];
-  __syncthreads();
-  const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3])), base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f, v = 0.f;
-  for (int w = 0; w < 4; ++w) {
-    const float f = exp2f(s_m[w] - base);
-    sum += s_l[w] * f;
-    if (threadIdx.x < D) v += s_o[w][threadIdx.x] * f;
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float z = top == -INFINITY ? 0.f : top;
+    float sum = 0.f, v[kPer] = {};
+    for (int b = w0; b <= last; b += 32) {
+      const int w = b + lane;
+      float f = 0.f;
+      if (w <= last) {
+        const float2 ml = p.ml[at(w)];
+        f = ex2(ml.x - z);
+        sum += ml.y * f;
+      }
+      const int n = min(32, last - b + 1);
+#pragma unroll 8
+      for (int i = 0; i < n; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float* o = p.o + at(b + i) * D + lane * kPer;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) v[e] += o[e] * fi;
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const long long row = (long long)(part.t0 + (part.r0 + r) / p.G) * a.Hq + part.h * p.G + (part.r0 + r) % p.G;
+    const float inv = sum == 0.f ? 0.f : __fdiv_rn(1.f, sum);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      const long long i = row * D + lane * kPer + e;
+      if (a.out_dtype == CSA2_F32) reinterpret_cast<float*>(a.out)[i] = v[e] * inv;
+      else reinterpret_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(v[e] * inv);
+    }
+    if (lane == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
   }
-  const long long row = (long long)t * a.Hq + hq;
-  if (threadIdx.x < D) store_out(a, row * D + threadIdx.x, sum == 0.f ? 0.f : v / sum);
-  if (threadIdx.x == 0 && a.lse) a.lse[row] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// One plane as [num_pages * Hkv][64][D] bytes, boxes of 32 tokens, swizzled over the rows' width.
+bool plane_map(CUtensorMap* map, const void* base, const csa2_kv8_cache& c) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dim[3] = {(cuuint64_t)c.D, kPage, (cuuint64_t)c.num_pages * c.Hkv};
+  const cuuint64_t stride[2] = {(cuuint64_t)c.D, (cuuint64_t)c.D * kPage};
+  const cuuint32_t box[3] = {(cuuint32_t)c.D, kHalf, 1}, one[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dim, stride, box, one,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+struct Layout {
+  size_t part = 0, head, ml, o, bytes;
+  explicit Layout(int D) {
+    head = up256(sizeof(Part) * kSpans);
+    ml = head + up256(sizeof(int) * kSpans);
+    o = ml + up256(sizeof(float2) * kSpans * 32);
+    bytes = o + sizeof(float) * kSpans * 32 * D;
+  }
+};
+
+template <int D, int RT, bool LIST>
+cudaError_t launch_stream(const CUtensorMap& mk, const CUtensorMap& mv, const StreamParams& p, cudaStream_t st) {
+  static SmemLimit limit;
+  const size_t smem = Ring<D>::kBytes + (LIST ? 0 : 8 * (size_t)((p.a.S + 31) / 32));
+  cudaError_t e = limit.raise(k_kv8_stream<D, RT, LIST>, smem);
+  if (e != cudaSuccess) return e;
+  e = launch_k(k_kv8_stream<D, RT, LIST>, dim3(kStreamCtas), dim3(32 * kWarps), smem, st, mk, mv, p);
+  if (e != cudaSuccess) return e;
+  return launch_k(k_kv8_join<D>, dim3(kSpans), dim3(256), 0, st, p);
+}
+
+template <int D>
+cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const StreamParams& p, cudaStream_t st) {
+  if (p.a.pages) return p.G <= 8 ? launch_stream<D, 8, true>(mk, mv, p, st) : launch_stream<D, 16, true>(mk, mv, p, st);
+  return (long long)p.a.max_new * p.G <= 8 ? launch_stream<D, 8, false>(mk, mv, p, st)
+                                           : launch_stream<D, 16, false>(mk, mv, p, st);
 }
 
 }  // namespace
 
-size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args&) { return 0; }
+size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args& a) { return Layout(a.cache.D).bytes; }
 
-cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void*, cudaStream_t st) {
+cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.S == 0) return cudaSuccess;
-  const dim3 grid(a.T, a.Hq);
-  return a.cache.D == 64 ? launch_k(k_kv8_attn<64>, grid, dim3(128), 0, st, a)
-                         : launch_k(k_kv8_attn<128>, grid, dim3(128), 0, st, a);
+  CUtensorMap mk, mv;
+  if (!plane_map(&mk, a.cache.k, a.cache) || !plane_map(&mv, a.cache.v, a.cache)) return cudaErrorInvalidValue;
+  StreamParams p;
+  p.a = a;
+  p.G = a.Hq / a.cache.Hkv;
+  const bool q16 = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride_t) | (uintptr_t)(2 * a.q_stride_h)) & 15) == 0;
+  p.aligned = (q16 ? 1 : 0) | (((uintptr_t)a.out & 15) == 0 ? 2 : 0);
+  const Layout at(a.cache.D);
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  p.part = reinterpret_cast<Part*>(w + at.part);
+  p.head = reinterpret_cast<int*>(w + at.head);
+  p.ml = reinterpret_cast<float2*>(w + at.ml);
+  p.o = reinterpret_cast<float*>(w + at.o);
+  return a.cache.D == 64 ? launch_rows<64>(mk, mv, p, st) : launch_rows<128>(mk, mv, p, st);
 }
 
 uint32_t read_clear_error_kv8() {

@@ -601,7 +601,7 @@ csa2_status csa2_fp4_linear(const csa2_fp4_linear_args* args, void* stream);
  * values are E4M3 bytes with one float32 scale for each page, head and plane, a power of two;
  * value = byte * scale.  A page that is full also has a summary of its keys for csa2_kv8_select.
  * Not on the pages: these layers are the rest of the model.
- * D in {64, 128}; Hkv in 1..256; num_pages <= 2^25, max_pages <= 2^24.
+ * D in {64, 128}; Hkv in 1..256; num_pages <= 2^25, num_pages * Hkv < 2^31, max_pages <= 2^24.
  *
  * The new tokens of a step (ragged).  start [S+1] and length [S] describe them to every call
  * below: sequence s (row s of the page table) has its new tokens in rows start[s] .. start[s+1]-1,
@@ -759,7 +759,7 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * largest element); probabilities are fp16 (2^-12 relative).  A NaN that a row does not see does
  * not reach it.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
- * window >= 0.
+ * window >= 0; S <= 2^18.
  * -------------------------------------------------------------------------- */
 typedef struct csa2_kv8_attn_args {
   size_t struct_size;
