@@ -122,13 +122,13 @@ struct Ring {
 
 struct Part {                            // a stream that begins in a span and does not end there
   int rows, t0, r0, h;                   // rows = 0: none
+  int last;                              // the span in which it ends
 };
 
 struct StreamParams {
   csa2_kv8_attn_args a;
   int G, aligned;                        // aligned: bit 0 q's rows, bit 1 out's rows on 16 bytes
   Part* part;                            // [kSpans]
-  int* head;                             // [kSpans] 0: no part of an earlier stream, 1: it goes on, 2: it ends here
   float2* ml;                            // [kSpans][2][16] maximum, sum; [1]: of the stream that goes on from here
   float* o;                              // [kSpans][2][16][D]
 };
@@ -170,8 +170,6 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
   constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kNt = D / 8, kR = RT / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kSt];
-  __shared__ float2 s_scale[kWarps][kSt];
-  __shared__ int s_token[kWarps][kSt];
   const csa2_kv8_attn_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
@@ -265,8 +263,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
     }
   }
 
-  Part part = {0, 0, 0, 0};
-  int head = 0;
+  Part part = {0, 0, 0, 0, 0};
   uint32_t phase = 0;                    // of each stage's barrier
   bool dead = false;
   while (pos < stop) {
@@ -290,7 +287,6 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       r0 = tt % list_tiles * RT;
       s = find_seq(a.start, a.S, t);
       if (s < 0) {                       // padding: nothing to write, not even parts
-        if (!begins) head = ends ? 2 : 1;
         pos += take;
         continue;
       }
@@ -303,16 +299,90 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       rows = rows_of(a, s, G);
     }
     const int nrows = min(RT, rows.n - r0);
-    // ---- this lane's rows g and g + 8: what they see, their query in fragments
+    // ---- what this lane's rows g and g + 8 see
     int lo[kR], hi[kR], lo_min = INT_MAX, lo_max = 0, hi_min = INT_MAX, hi_max = 0;
+#pragma unroll
+    for (int i = 0; i < kR; ++i) {
+      lo[i] = 0;
+      hi[i] = INT_MAX;
+      if (g + 8 * i < nrows) {
+        seen_by(a, rows, rows.t0 + (r0 + g + 8 * i) / G, lo[i], hi[i]);
+        lo_min = min(lo_min, lo[i]);
+        lo_max = max(lo_max, lo[i]);
+        hi_min = min(hi_min, hi[i]);
+        hi_max = max(hi_max, hi[i]);
+      }
+    }
+#pragma unroll
+    for (int o = 4; o <= 16; o <<= 1) {
+      lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
+      lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+      hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
+      hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
+    }
+    // ---- half pages y0 .. y1 of the stream (LIST: of the list, else from `first` on), those in sight
+    int y0 = x, y1 = x + take;
+    if constexpr (!LIST) {
+      y0 = max(y0, lo_min / kHalf - first);
+      y1 = min(y1, (hi_max + kHalf - 1) / kHalf - first);
+    }
+    // Lane i: first token (-1: to be skipped), page and scales of half page 32 b + i for the batch b that is being
+    // issued, [1], and the one before it, [0], which may still be worked on.
+    int bt[2] = {-1, -1}, bp = 0;
+    float bk[2] = {}, bv[2] = {};
+    auto load_batch = [&](int b) {
+      bt[0] = bt[1];
+      bk[0] = bk[1];
+      bv[0] = bv[1];
+      bt[1] = -1;
+      const int y = b + lane;
+      if (y < y1) {
+        int j, half;
+        if constexpr (LIST) {
+          j = list[y >> 1];
+          half = y & 1;
+          if (j >= c.max_pages) {
+            raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
+            j = -1;
+          }
+        } else {
+          j = (first + y) >> 1;
+          half = (first + y) & 1;
+        }
+        const int token = j * kPage + half * kHalf;
+        if (j >= 0 && token < hi_max && token + kHalf > lo_min) {
+          const int page = page_id(c, s, j, &g_err_kv8);
+          if (page >= 0) {
+            bt[1] = token;
+            bp = page;
+            const long long ph = (long long)page * Hkv + h;
+            bk[1] = c.k_scale[ph];
+            bv[1] = c.v_scale[ph];
+          }
+        }
+      }
+    };
+    int issued = y0;
+    auto issue = [&] {                   // the next half page into its stage
+      const int b = (issued - y0) & 31;
+      if (b == 0) load_batch(issued);
+      const int st = (issued - y0) % kSt;
+      const int token = __shfl_sync(0xffffffffu, bt[1], b), page = __shfl_sync(0xffffffffu, bp, b);
+      if (lane == 0 && token >= 0) {
+        tc::mbar_arrive_expect_tx(&bars[warp][st], kStage);
+        tma_load_3d(ring + st * kStage, &mk, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
+        tma_load_3d(ring + st * kStage + kHalf * D, &mv, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
+      }
+      ++issued;
+    };
+    for (int i = 0; i < kSt - 1; ++i)
+      if (issued < y1) issue();
+    // ---- their query in fragments, while the first copies are under way
     float mul[kR], m[kR], l[kR];
     uint32_t qa[kKs][2 * kR];
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
       const int r = g + 8 * i;
-      lo[i] = 0;
-      hi[i] = INT_MAX;
-      mul[i] = 0.f;
       m[i] = -INFINITY;
       l[i] = 0.f;
       float v[D / 4];
@@ -320,11 +390,6 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       for (int e = 0; e < D / 4; ++e) v[e] = 0.f;
       if (r < nrows) {
         const int t = rows.t0 + (r0 + r) / G;
-        seen_by(a, rows, t, lo[i], hi[i]);
-        lo_min = min(lo_min, lo[i]);
-        lo_max = max(lo_max, lo[i]);
-        hi_min = min(hi_min, hi[i]);
-        hi_max = max(hi_max, hi[i]);
         const uint16_t* q = a.q + t * a.q_stride_t + (long long)(h * G + (r0 + r) % G) * a.q_stride_h + q4 * (D / 4);
         if (p.aligned & 1) {
 #pragma unroll
@@ -356,84 +421,19 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
         qa[j][kR + i] = f16x2(v[4 * j + 2] * f, v[4 * j + 3] * f);
       }
     }
-#pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) {
-      lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
-      lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
-      hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
-      hi_max = max(hi_max, __shfl_xor_sync(0xffffffffu, hi_max, o));
-    }
     float o[kNt][2 * kR];
 #pragma unroll
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
       for (int e = 0; e < 2 * kR; ++e) o[n][e] = 0.f;
 
-    // ---- half pages y0 .. y1 of the stream (LIST: of the list, else from `first` on), those in sight
-    int y0 = x, y1 = x + take;
-    if constexpr (!LIST) {
-      y0 = max(y0, lo_min / kHalf - first);
-      y1 = min(y1, (hi_max + kHalf - 1) / kHalf - first);
-    }
-    int bt = -1;                         // lane i: token, page and scales of half page batch + i; bt < 0: to be skipped
-    int bp = 0;
-    float bk = 0.f, bv = 0.f;
-    auto load_batch = [&](int b) {
-      bt = -1;
-      const int y = b + lane;
-      if (y < y1) {
-        int j, half;
-        if constexpr (LIST) {
-          j = list[y >> 1];
-          half = y & 1;
-          if (j >= c.max_pages) {
-            raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
-            j = -1;
-          }
-        } else {
-          j = (first + y) >> 1;
-          half = (first + y) & 1;
-        }
-        const int token = j * kPage + half * kHalf;
-        if (j >= 0 && token < hi_max && token + kHalf > lo_min) {
-          const int page = page_id(c, s, j, &g_err_kv8);
-          if (page >= 0) {
-            bt = token;
-            bp = page;
-            const long long ph = (long long)page * Hkv + h;
-            bk = c.k_scale[ph];
-            bv = c.v_scale[ph];
-          }
-        }
-      }
-    };
-    int issued = y0;
-    auto issue = [&] {                   // the next half page into its stage
-      const int b = (issued - y0) & 31;
-      if (b == 0) load_batch(issued);
-      const int st = (issued - y0) % kSt;
-      const int token = __shfl_sync(0xffffffffu, bt, b), page = __shfl_sync(0xffffffffu, bp, b);
-      const float ks = __shfl_sync(0xffffffffu, bk, b), vs = __shfl_sync(0xffffffffu, bv, b);
-      if (lane == 0) {
-        s_token[warp][st] = token;
-        if (token >= 0) {
-          s_scale[warp][st] = make_float2(ks, vs);
-          tc::mbar_arrive_expect_tx(&bars[warp][st], kStage);
-          tma_load_3d(ring + st * kStage, &mk, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
-          tma_load_3d(ring + st * kStage + kHalf * D, &mv, 0, token & kHalf, page * Hkv + h, &bars[warp][st]);
-        }
-      }
-      ++issued;
-    };
-    for (int i = 0; i < kSt - 1; ++i)
-      if (issued < y1) issue();
     for (int y = y0; y < y1; ++y) {
       __syncwarp();                      // every lane has read the stage that is filled next
       if (issued < y1 && !dead) issue();
-      __syncwarp();
       const int st = (y - y0) % kSt;
       if (y >= issued) break;            // after a wait that gave up
-      const int token0 = s_token[warp][st];
+      const bool old = (y - y0) >> 5 != (issued - 1 - y0) >> 5;
+      const int token0 = __shfl_sync(0xffffffffu, old ? bt[0] : bt[1], (y - y0) & 31);
       if (token0 < 0) continue;
       if (!tc::mbar_wait(&bars[warp][st], phase >> st & 1, kWaitPolls)) {
         if (!dead) raise_error(&g_err_kv8, CSA2_DEVERR_TIMEOUT);
@@ -442,7 +442,8 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       dead = __any_sync(0xffffffffu, dead);
       phase ^= 1u << st;
       if (dead) continue;                // the copies in flight are still waited for
-      const float2 sc = s_scale[warp][st];
+      const float2 sc = make_float2(__shfl_sync(0xffffffffu, old ? bk[0] : bk[1], (y - y0) & 31),
+                                    __shfl_sync(0xffffffffu, old ? bv[0] : bv[1], (y - y0) & 31));
       const uint32_t kb = ring_s + st * kStage, vb = kb + kHalf * D;
       const bool border = token0 < lo_max || token0 + kHalf > hi_min;
       // scores: four tiles of 8 tokens, this lane's tokens 8 n + 2 q4, + 1 in rows g, g + 8
@@ -651,60 +652,56 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
         }
       }
     }
-    if (!begins) head = ends ? 2 : 1;
-    else if (!ends) part = Part{nrows, rows.t0, r0, h};
+    if (begins && !ends) part = Part{nrows, rows.t0, r0, h, span + (int)((count - take + per - 1) / per)};
     pos += take;
   }
-  if (lane == 0) {
-    p.part[span] = part;
-    p.head[span] = head;
-  }
+  if (lane == 0) p.part[span] = part;
 }
 
 // A CTA a span: the stream that begins there and goes on in the next ones, a warp a row, a lane D / 32 channels.
 template <int D>
 __global__ void __launch_bounds__(256) k_kv8_join(const StreamParams p) {
-  constexpr int kPer = D / 32;
+  constexpr int kPer = D / 32, kAhead = 8;
   const csa2_kv8_attn_args& a = p.a;
   pdl_wait();
   pdl_trigger();
   const int w0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Part part = p.part[w0];
-  if (part.rows == 0) return;
-  int last = w0 + 1;                     // the span in which the stream ends
-  while (true) {
-    const int w = last + lane;
-    const uint32_t e = __ballot_sync(0xffffffffu, w >= kSpans || p.head[w] != 1);
-    if (e) {
-      last += __ffs(e) - 1;
-      break;
-    }
-    last += 32;
-  }
-  last = min(last, kSpans - 1);
+  const int last = min(part.last, kSpans - 1);
   for (int r = warp; r < part.rows; r += 8) {
     auto at = [&](int w) { return ((long long)w * 2 + (w == w0 ? 1 : 0)) * 16 + r; };
-    float top = -INFINITY;
-    for (int w = w0 + lane; w <= last; w += 32) top = fmaxf(top, p.ml[at(w)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float z = top == -INFINITY ? 0.f : top;
-    float sum = 0.f, v[kPer] = {};
+    float top = -INFINITY, sum = 0.f, v[kPer] = {};
     for (int b = w0; b <= last; b += 32) {
-      const int w = b + lane;
-      float f = 0.f;
-      if (w <= last) {
-        const float2 ml = p.ml[at(w)];
-        f = ex2(ml.x - z);
-        sum += ml.y * f;
-      }
-      const int n = min(32, last - b + 1);
-#pragma unroll 8
-      for (int i = 0; i < n; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float* o = p.o + at(b + i) * D + lane * kPer;
+      const int w = b + lane, n = min(32, last - b + 1);
+      const float2 ml = w <= last ? p.ml[at(w)] : make_float2(-INFINITY, 0.f);
+      float mn = fmaxf(top, ml.x);
 #pragma unroll
-        for (int e = 0; e < kPer; ++e) v[e] += o[e] * fi;
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      const float z = mn == -INFINITY ? 0.f : mn, alpha = ex2(top - z), f = ex2(ml.x - z);
+      top = mn;
+      sum = sum * alpha + ml.y * f;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) v[e] *= alpha;
+      for (int i = 0; i < n; i += kAhead) {
+        float o[kAhead][kPer];
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float* src = p.o + at(b + min(i + j, n - 1)) * D + lane * kPer;
+          if constexpr (kPer == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src);
+            o[j][0] = x.x; o[j][1] = x.y; o[j][2] = x.z; o[j][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(src);
+            o[j][0] = x.x; o[j][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) {
+          const float fi = __shfl_sync(0xffffffffu, f, (i + j) & 31);
+          if (i + j < n)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) v[e] += o[j][e] * fi;
+        }
       }
     }
 #pragma unroll
@@ -736,10 +733,9 @@ bool plane_map(CUtensorMap* map, const void* base, const csa2_kv8_cache& c) {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t part = 0, head, ml, o, bytes;
+  size_t part = 0, ml, o, bytes;
   explicit Layout(int D) {
-    head = up256(sizeof(Part) * kSpans);
-    ml = head + up256(sizeof(int) * kSpans);
+    ml = up256(sizeof(Part) * kSpans);
     o = ml + up256(sizeof(float2) * kSpans * 32);
     bytes = o + sizeof(float) * kSpans * 32 * D;
   }
@@ -779,7 +775,6 @@ cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t 
   const Layout at(a.cache.D);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part = reinterpret_cast<Part*>(w + at.part);
-  p.head = reinterpret_cast<int*>(w + at.head);
   p.ml = reinterpret_cast<float2*>(w + at.ml);
   p.o = reinterpret_cast<float*>(w + at.o);
   return a.cache.D == 64 ? launch_rows<64>(mk, mv, p, st) : launch_rows<128>(mk, mv, p, st);
