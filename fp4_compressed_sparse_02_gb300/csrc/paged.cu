@@ -286,23 +286,177 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
 }
 
 // ---- csa2_kv8_select ------------------------------------------------------------------------
+//
+// Scores, then picks.  The scores of up to 8 rows of one sequence and key head are one product of their 8-bit queries
+// with the pages' 8-bit summaries: whole numbers up to 127 are exact in fp16 and their sums of 128 products
+// stay below 2^24, so mma.sync gives the exact dot products whatever its order.
+constexpr int kTile = 8, kScoreThreads = 128, kScorePages = 512;
 
-constexpr int kSelectThreads = 256;
+struct SelectParams {
+  csa2_kv8_select_args a;
+  int G, aligned;                        // aligned: q's rows on 8 bytes
+  int t0, t1;                            // rows of this launch
+  int stride;                            // keys of a (row, head)
+  uint32_t* keys;                        // [t1 - t0][Hkv][stride], by page: larger = better
+};
 
-// A CTA a (row, key head): scores as ordered keys in shared memory, the k-th by four 8-bit digits, the kept pages in
-// ascending order.
+// Four signed bytes as two fp16 pairs: (byte ^ 0x80) under 0x64 is 1024 + 128 + byte.
+__device__ __forceinline__ void s8x4_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t x = w ^ 0x80808080u;
+  const __half2 bias = __half2half2(__ushort_as_half(0x6480));                 // 1152
+  uint32_t a = __byte_perm(x, 0x64646464u, 0x4140), b = __byte_perm(x, 0x64646464u, 0x4342);
+  const __half2 u = __hsub2(*reinterpret_cast<__half2*>(&a), bias), v = __hsub2(*reinterpret_cast<__half2*>(&b), bias);
+  lo = *reinterpret_cast<const uint32_t*>(&u);
+  hi = *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// The 8-bit query of row t and head h, spread over a warp (D / 32 channels a lane), as packed bytes.  The heads' sum is
+// carried with its rounding errors, so that it is rounded once.
 template <int D>
-__global__ void __launch_bounds__(kSelectThreads) k_kv8_select(const csa2_kv8_select_args a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int8_t r8[D];
-  __shared__ float s_top[kSelectThreads / 32];
-  __shared__ uint32_t hist[256];
-  __shared__ long long sums[33];
-  __shared__ uint32_t s_pick[2];
+__device__ __forceinline__ uint32_t query8(const SelectParams& p, int t, int h, int lane) {
+  constexpr int kPer = D / 32;
+  const csa2_kv8_select_args& a = p.a;
+  const uint16_t* q = a.q + t * a.q_stride_t + (long long)h * p.G * a.q_stride_h + lane * kPer;
+  float s[kPer] = {}, err[kPer] = {};
+#pragma unroll 8
+  for (int g = 0; g < p.G; ++g) {
+    const uint16_t* row = q + g * a.q_stride_h;
+    float x[kPer];
+    if (p.aligned) {
+      uint32_t w[kPer / 2];
+      if constexpr (kPer == 4) {
+        const uint2 v = *reinterpret_cast<const uint2*>(row);
+        w[0] = v.x;
+        w[1] = v.y;
+      } else {
+        w[0] = *reinterpret_cast<const uint32_t*>(row);
+      }
+#pragma unroll
+      for (int i = 0; i < kPer / 2; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) x[i] = bf16_bits_to_f32(row[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const float n = __fadd_rn(s[i], x[i]), b = __fsub_rn(n, s[i]);
+      err[i] = __fadd_rn(err[i], __fadd_rn(__fsub_rn(s[i], __fsub_rn(n, b)), __fsub_rn(x[i], b)));
+      s[i] = n;
+    }
+  }
+  float top = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const bool finite = fabsf(s[i]) <= 3.402823466e38f;
+    if (finite) s[i] = __fadd_rn(s[i], err[i]);
+    if (fabsf(s[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(s[i]));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float u = __fdiv_rn(top, 127.f);
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    float r = u > 0.f ? rintf(__fdiv_rn(s[i], u)) : 0.f;
+    r = r != r ? 0.f : fminf(fmaxf(r, -127.f), 127.f);
+    w |= ((uint32_t)(int)r & 0xffu) << 8 * i;
+  }
+  return w;
+}
+
+// A CTA (tile of 8 rows of one sequence, 512 pages, head); a warp 128 pages, 32 at a time.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) k_kv8_score(const SelectParams p) {
+  constexpr int kKs = D / 16, kW = D / 64;                   // products a tile, 16-byte words of a lane's quarter row
+  __shared__ uint32_t r8[kTile][D / 4];
+  const csa2_kv8_select_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x;
+  // Slot floor(start / 8) + s and the ones after it hold the tiles of sequence s (starts within this launch's rows).
+  auto begin = [&](int s) {
+    const int x = a.start[s];
+    return x < p.t0 ? p.t0 : x > p.t1 ? p.t1 : x;
+  };
+  int s = 0, hi = a.S;
+  const int slot = blockIdx.x, h = blockIdx.z, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  while (hi - s > 1) {
+    const int mid = (s + hi) >> 1;
+    if ((begin(mid) - p.t0) / kTile + mid <= slot) s = mid; else hi = mid;
+  }
+  const int b = begin(s), t = b + (slot - (b - p.t0) / kTile - s) * kTile, n = min(kTile, begin(s + 1) - t);
+  if (t < b || n <= 0) return;
+  const long long last = (long long)a.length[s] - ((long long)a.start[s + 1] - (t + n - 1));
+  if (last < 0) return;
+  const long long most = last / kPage + 1;
+  const int P = (int)(most < p.stride ? most : p.stride), end = (P < c.max_pages ? P : c.max_pages) - a.recent;
+  const int first = a.first + blockIdx.y * kScorePages;
+  if (most <= a.k || first >= end) return;
+  for (int i = warp; i < n; i += kScoreThreads / 32) {
+    const uint32_t w = query8<D>(p, t + i, h, lane);
+    if constexpr (D == 128) r8[i][lane] = w;
+    else reinterpret_cast<uint16_t*>(r8[i])[lane] = (uint16_t)w;
+  }
+  __syncthreads();
+  const int g = lane >> 2, q4 = lane & 3;
+  uint32_t qb[kKs][2];
+#pragma unroll
+  for (int j = 0; j < kKs; ++j) s8x4_to_f16(g < n ? r8[g][q4 * kKs + j] : 0u, qb[j][0], qb[j][1]);
+  const int stop = min(end, first + kScorePages);
+  for (int j0 = first + warp * 32; j0 < stop; j0 += kScoreThreads) {
+    const int j = j0 + lane, page = j < stop ? page_id(c, s, j, &g_err_paged) : -1;
+    const float scale = page >= 0 ? c.mean_scale[(long long)page * c.Hkv + h] : 0.f;
+    uint4 w[4][kW];                      // summaries of pages j0 + 8 i + g, channels D/4 * q4 ...
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int id = __shfl_sync(0xffffffffu, page, 8 * i + g);
+      const uint4* m = reinterpret_cast<const uint4*>(c.mean + ((long long)(id < 0 ? 0 : id) * c.Hkv + h) * D + q4 * (D / 4));
+#pragma unroll
+      for (int e = 0; e < kW; ++e) w[i][e] = __ldg(m + e);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float d[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int e = 0; e < kW; ++e) {
+        const uint32_t x[4] = {w[2 * i][e].x, w[2 * i][e].y, w[2 * i][e].z, w[2 * i][e].w};
+        const uint32_t y[4] = {w[2 * i + 1][e].x, w[2 * i + 1][e].y, w[2 * i + 1][e].z, w[2 * i + 1][e].w};
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          uint32_t a0, a1, a2, a3;
+          s8x4_to_f16(x[v], a0, a2);
+          s8x4_to_f16(y[v], a1, a3);
+          mma_f16_16816(d, a0, a1, a2, a3, qb[4 * e + v][0], qb[4 * e + v][1]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int at = 16 * i + 8 * (e >> 1) + g, row = 2 * q4 + (e & 1);
+        const float f = __shfl_sync(0xffffffffu, scale, at);
+        const int id = __shfl_sync(0xffffffffu, page, at);
+        // a page outside the cache comes last
+        if (row < n && j0 + at < stop)
+          p.keys[((long long)(t + row - p.t0) * c.Hkv + h) * p.stride + j0 + at] = id < 0 ? 0u : float_key(__fmul_rn(d[e], f));
+      }
+    }
+  }
+}
+
+// A CTA a (row, head): the k-th best key by digits of 11, 11 and 10 bits, then the kept pages in ascending order.
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) k_kv8_pick(const SelectParams p) {
+  constexpr int kBins = 2048, kPerThread = kBins / THREADS, kPickWarps = THREADS / 32;
+  extern __shared__ uint32_t keys[];
+  __shared__ uint32_t hist[kBins];
+  __shared__ int s_warp[2][kPickWarps + 1], s_pick[2];
+  const csa2_kv8_select_args& a = p.a;
+  const csa2_kv8_cache& c = a.cache;
+  pdl_wait();
+  pdl_trigger();
+  const int t = p.t0 + blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int s = find_seq(a.start, a.S, t);
   if (s < 0) return;
   const long long row = (long long)t * c.Hkv + h;
@@ -314,80 +468,121 @@ __global__ void __launch_bounds__(kSelectThreads) k_kv8_select(const csa2_kv8_se
   }
   const int P = pos < 0 ? 0 : (pos >> kPageShift) + 1;
   if (P <= a.k) {
-    for (int i = tid; i < a.k; i += kSelectThreads) out[i] = i < P ? i : -1;
+    for (int i = tid; i < a.k; i += THREADS) out[i] = i < P ? i : -1;
     if (tid == 0) a.count[row] = P;
     return;
   }
-  const int G = a.Hq / c.Hkv;
-  float q = 0.f;
-  if (tid < D) {
-    double sum = 0.0;
-    for (int g = 0; g < G; ++g)
-      sum += (double)bf16_bits_to_f32(a.q[t * a.q_stride_t + (long long)(h * G + g) * a.q_stride_h + tid]);
-    q = (float)sum;
-  }
-  float top = fabsf(q) <= 3.402823466e38f ? fabsf(q) : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((tid & 31) == 0) s_top[tid >> 5] = top;
-  __syncthreads();
-  if (tid < D) {
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) top = fmaxf(top, s_top[i]);
-    const float u = __fdiv_rn(top, 127.f);
-    float r = u > 0.f ? rintf(__fdiv_rn(q, u)) : 0.f;
-    r = r != r ? 0.f : fminf(fmaxf(r, -127.f), 127.f);
-    r8[tid] = (int8_t)r;
-  }
-  __syncthreads();
-  const int lo = a.first, hi = P - a.recent, want = a.k - a.first - a.recent;
-  for (int j = lo + tid; j < hi; j += kSelectThreads) {
-    const int page = page_id(c, s, j, &g_err_paged);
-    uint32_t key = 0;                                        // a page outside the cache comes last
-    if (page >= 0) {
-      const int* m = reinterpret_cast<const int*>(c.mean + ((long long)page * c.Hkv + h) * D);
-      int dot = 0;
-      for (int i = 0; i < D / 4; ++i) dot = __dp4a(m[i], reinterpret_cast<const int*>(r8)[i], dot);
-      key = float_key(__fmul_rn((float)dot, c.mean_scale[(long long)page * c.Hkv + h]));
-    }
-    keys[j - lo] = key;
-  }
-  const int M = hi - lo;
-  uint32_t prefix = 0;
-  int left = want;                                           // still to take among the keys with this prefix
-  for (int shift = 24; shift >= 0 && left > 0; shift -= 8) {
-    for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-    __syncthreads();
-    const uint32_t mask = shift == 24 ? 0u : ~0u << (shift + 8);
-    for (int i = tid; i < M; i += kSelectThreads)
-      if ((keys[i] & mask) == prefix) atomicAdd(&hist[keys[i] >> shift & 255], 1u);
-    __syncthreads();
-    if (tid == 0) {
-      int n = 0, d = 255;
-      while (d > 0 && n + (int)hist[d] < left) n += hist[d--];
-      s_pick[0] = prefix | (uint32_t)d << shift;
-      s_pick[1] = left - n;
-    }
-    __syncthreads();
-    prefix = s_pick[0];
-    left = s_pick[1];
-  }
-  // above the threshold all, of those equal to it the first `left`
-  for (int i = tid; i < a.first; i += kSelectThreads) out[i] = i;
-  for (int i = tid; i < a.recent; i += kSelectThreads) out[a.k - a.recent + i] = hi + i;
+  const int lo = a.first, hi = P - a.recent, M = hi - lo, want = a.k - a.first - a.recent;
+  for (int i = tid; i < a.first; i += THREADS) out[i] = i;
+  for (int i = tid; i < a.recent; i += THREADS) out[a.k - a.recent + i] = hi + i;
   if (tid == 0) a.count[row] = a.k;
   if (want == 0) return;
-  long long above = 0, equal = 0;
-  for (int i0 = 0; i0 < M; i0 += kSelectThreads) {
-    const int i = i0 + tid;
-    const bool g = i < M && keys[i] > prefix, e = i < M && keys[i] == prefix;
-    long long total;
-    const long long in = block_scan((long long)g << 32 | (long long)e, sums, &total);
-    const long long ga = above + (in >> 32) - g, ea = equal + (in & 0xffffffff) - e;   // before this page
-    if (g || (e && ea < left)) out[a.first + ga + (ea < left ? ea : left)] = lo + i;
-    above += total >> 32;
-    equal += total & 0xffffffff;
+  const uint32_t* src = p.keys + ((long long)(t - p.t0) * c.Hkv + h) * p.stride + lo;
+  for (int i = tid; i < M; i += THREADS) keys[i] = src[i];
+  for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+  __syncthreads();
+  uint32_t prefix = 0, mask = 0;
+  int left = want;                                           // still to take among the keys with this prefix
+#pragma unroll
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t digit = pass == 2 ? 1023u : 2047u;
+    for (int i = tid; i < M; i += THREADS)
+      if ((keys[i] & mask) == prefix) atomicAdd(&hist[keys[i] >> shift & digit], 1u);
+    __syncthreads();
+    // bins from the top: thread i has kPerThread of them, below those of threads before it
+    int own[kPerThread], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPerThread; ++i) {
+      own[i] = (int)hist[kBins - 1 - (tid * kPerThread + i)];
+      sum += own[i];
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) s_warp[0][warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int i = 0; i < warp; ++i) before += s_warp[0][i];
+    if (before < left && before + sum >= left) {
+#pragma unroll
+      for (int i = 0; i < kPerThread; ++i) {
+        if (before < left && before + own[i] >= left) {
+          s_pick[0] = kBins - 1 - (tid * kPerThread + i);
+          s_pick[1] = left - before;
+          break;
+        }
+        before += own[i];
+      }
+    }
+    for (int i = tid; i < kBins; i += THREADS) hist[i] = 0;
+    __syncthreads();
+    prefix |= (uint32_t)s_pick[0] << shift;
+    mask |= digit << shift;
+    left = s_pick[1];
   }
+  // above the threshold all, of those equal to it the first `left`; a warp has a run of the pages
+  const int run = ((M + kPickWarps - 1) / kPickWarps + 31) & ~31, i0 = warp * run, i1 = min(M, i0 + run);
+  int above = 0, equal = 0;
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    above += __popc(__ballot_sync(0xffffffffu, i < i1 && keys[i] > prefix));
+    equal += __popc(__ballot_sync(0xffffffffu, i < i1 && keys[i] == prefix));
+  }
+  if (lane == 0) {
+    s_warp[0][warp] = above;
+    s_warp[1][warp] = equal;
+  }
+  __syncthreads();
+  above = equal = 0;
+  for (int i = 0; i < warp; ++i) {
+    above += s_warp[0][i];
+    equal += s_warp[1][i];
+  }
+  for (int i = i0 + lane; i - lane < i1; i += 32) {
+    const bool g = i < i1 && keys[i] > prefix, e = i < i1 && keys[i] == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e), under = (1u << lane) - 1;
+    const int ga = above + __popc(bg & under), ea = equal + __popc(be & under);
+    if (g || (e && ea < left)) out[a.first + ga + min(ea, left)] = lo + i;
+    above += __popc(bg);
+    equal += __popc(be);
+  }
+}
+
+// Rows of one launch: as many as keep their keys within 256 MB.
+int select_stride(const csa2_kv8_select_args& a) { return (a.max_length + kPage - 1) / kPage; }
+int select_rows(const csa2_kv8_select_args& a) {
+  const long long row = (long long)a.cache.Hkv * (select_stride(a) > 0 ? select_stride(a) : 1);
+  const long long n = (1LL << 26) / row;
+  return (int)(n < 1 ? 1 : n < a.T ? n : a.T);
+}
+
+template <int D>
+cudaError_t launch_select(SelectParams& p, cudaStream_t st) {
+  static SmemLimit limit_many;
+  const csa2_kv8_select_args& a = p.a;
+  const int rows = select_rows(a);
+  for (p.t0 = 0; p.t0 < a.T; p.t0 = p.t1) {
+    p.t1 = a.T - p.t0 < rows ? a.T : p.t0 + rows;
+    cudaError_t e = cudaSuccess;
+    if (p.stride > a.k) {
+      const dim3 grid((p.t1 - p.t0) / kTile + a.S, (p.stride + kScorePages - 1) / kScorePages, a.cache.Hkv);
+      e = launch_k(k_kv8_score<D>, grid, dim3(kScoreThreads), 0, st, p);
+      if (e != cudaSuccess) return e;
+    }
+    const size_t smem = 4 * (size_t)p.stride;
+    const dim3 grid(p.t1 - p.t0, a.cache.Hkv);
+    if (p.stride <= 4096) {
+      e = launch_k(k_kv8_pick<256>, grid, dim3(256), smem, st, p);
+    } else {
+      e = limit_many.raise(k_kv8_pick<1024>, smem);
+      if (e == cudaSuccess) e = launch_k(k_kv8_pick<1024>, grid, dim3(1024), smem, st, p);
+    }
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
@@ -419,19 +614,19 @@ cudaError_t launch_kv8_append(const csa2_kv8_append_args& a, cudaStream_t st) {
   return vec ? go(k_kv8_append<float, 128, true>) : go(k_kv8_append<float, 128, false>);
 }
 
-size_t kv8_select_workspace_bytes(const csa2_kv8_select_args&) { return 0; }
+size_t kv8_select_workspace_bytes(const csa2_kv8_select_args& a) {
+  return 4 * (size_t)select_rows(a) * a.cache.Hkv * select_stride(a);
+}
 
-cudaError_t launch_kv8_select(const csa2_kv8_select_args& a, void*, cudaStream_t st) {
+cudaError_t launch_kv8_select(const csa2_kv8_select_args& a, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.S == 0) return cudaSuccess;
-  const size_t smem = 4 * (size_t)((a.max_length + kPage - 1) / kPage);
-  static SmemLimit limit64, limit128;
-  cudaError_t e;
-  if (a.cache.D == 64) {
-    if ((e = limit64.raise(k_kv8_select<64>, smem)) != cudaSuccess) return e;
-    return launch_k(k_kv8_select<64>, dim3(a.T, a.cache.Hkv), dim3(kSelectThreads), smem, st, a);
-  }
-  if ((e = limit128.raise(k_kv8_select<128>, smem)) != cudaSuccess) return e;
-  return launch_k(k_kv8_select<128>, dim3(a.T, a.cache.Hkv), dim3(kSelectThreads), smem, st, a);
+  SelectParams p;
+  p.a = a;
+  p.G = a.Hq / a.cache.Hkv;
+  p.aligned = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride_t) | (uintptr_t)(2 * a.q_stride_h)) & 7) == 0;
+  p.stride = select_stride(a);
+  p.keys = static_cast<uint32_t*>(ws);
+  return a.cache.D == 64 ? launch_select<64>(p, st) : launch_select<128>(p, st);
 }
 
 uint32_t read_clear_error_paged() {

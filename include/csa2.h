@@ -708,7 +708,8 @@ csa2_status csa2_kv8_append(const csa2_kv8_append_args* args, void* stream);
  * csa2_kv8_select -- the pages that each new token attends to, by a score of their summaries.
  * For row t (position p, so P = p / 64 + 1 pages in sight) and key head h with query heads
  * h*G .. h*G+G-1, G = Hq / Hkv:
- *   c     = the sum of the G query heads (in float64, rounded once to float32)
+ *   c     = the sum of the G query heads, rounded once to float32 (for heads within 2^34 of one
+ *           another and sums in float32's range)
  *   u     = max|c| / 127 over finite c (float32 division);  r = round(c / u) in -127..127, ties
  *           to even, 0 if u == 0; a NaN counts as 0, infinities as +-127
  *   score = float32(r . mean[page][h]) * mean_scale[page][h]   (the product of whole numbers is exact)
@@ -718,7 +719,8 @@ csa2_status csa2_kv8_append(const csa2_kv8_append_args* args, void* stream);
  * table keeps none.  All steps are exact or rounded once, so the result has no near-ties.
  * Supported: q bf16, Hq a multiple of Hkv with G <= 128; 2 <= k <= 4096, first >= 0, recent >= 1,
  * first + recent <= k; max_length <= 2^21 (a host bound of length; longer rows set
- * CSA2_DEVERR_N_VIS and keep none).
+ * CSA2_DEVERR_N_VIS and keep none).  The workspace holds T * Hkv * max_length / 64 scores, 256 MB
+ * at most (or those of one row); longer calls are taken in parts.
  * -------------------------------------------------------------------------- */
 typedef struct csa2_kv8_select_args {
   size_t struct_size;
