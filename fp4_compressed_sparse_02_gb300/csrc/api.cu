@@ -446,6 +446,7 @@ csa2_status check_kv8_attn(const csa2_kv8_attn_args* a) {
   if (s != CSA2_OK) return s;
   s = check_heads(a->Hq, a->cache.Hkv);
   if (s != CSA2_OK) return s;
+  REQUIRE((int64_t)a->T * a->Hq <= INT32_MAX, CSA2_ERR_UNSUPPORTED_SHAPE, "T * Hq must be below 2^31");
   REQUIRE(a->S <= (1 << 18), CSA2_ERR_UNSUPPORTED_SHAPE, "S must be at most 2^18 (got %d)", a->S);
   REQUIRE(a->max_new >= 0, CSA2_ERR_INVALID_ARG, "max_new < 0");
   REQUIRE(a->window >= 0, CSA2_ERR_INVALID_ARG, "window < 0");

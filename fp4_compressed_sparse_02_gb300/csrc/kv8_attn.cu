@@ -2,100 +2,13 @@
 //
 // Rows are (new token, query head of the group) pairs of one sequence and key head; a tile of rows
 // against the tiles of its sequence's pages is one stream.  k_kv8_stream runs streams of at most 16 rows.
-#include <limits.h>
-#include <math.h>
-
-#include "internal.h"
-#include "kv8.cuh"
-#include "tc.cuh"
-#include "tmap.h"
+#include "kv8_attn.cuh"
 
 namespace csa2 {
 
 CSA2_DEFINE_ERROR_WORD(g_err_kv8);
 
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kWaitPolls = 1u << 22;
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t f16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-__device__ __forceinline__ void tma_load_3d(void* dst, const void* map, int x, int y, int z, uint64_t* mbar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
-      :: "r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(map), "r"((uint32_t)__cvta_generic_to_shared(mbar)),
-         "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-// The power of two that brings a row whose largest magnitude is `top` into [2^14, 2^15), and the one that undoes it;
-// 1 for a row of zeros or with an infinity or NaN.
-__device__ __forceinline__ void row_factor(float top, float& f, float& undo) {
-  const int e = (int)(__float_as_uint(top) >> 23);         // biased exponent; 0: zero or below 2^-126
-  f = undo = 1.f;
-  if (top == 0.f || e >= 255) return;
-  const int k = 14 - (e - 127);                            // -113 .. 141
-  const int k1 = k > 127 ? 127 : k;
-  f = __uint_as_float((uint32_t)(k1 + 127) << 23);
-  undo = k1 == 127 ? 5.877471754111438e-39f : __uint_as_float((uint32_t)(127 - k1) << 23);   // 2^-127 is subnormal
-}
-
-// ---- rows of a sequence ----------------------------------------------------------------------
-
-struct Rows {
-  int t0, n;                             // first row of the step, rows x group
-  int end, length;                       // start[s+1], length[s]
-};
-
-__device__ __forceinline__ Rows rows_of(const csa2_kv8_attn_args& a, int s, int G) {
-  Rows r;
-  r.t0 = a.start[s];
-  r.end = a.start[s + 1];
-  r.length = a.length[s];
-  const int e = min(r.end, a.T);
-  r.n = r.t0 >= 0 && e > r.t0 ? (e - r.t0) * G : 0;
-  return r;
-}
-
-// What row t sees: positions [lo, hi).
-__device__ __forceinline__ void seen_by(const csa2_kv8_attn_args& a, const Rows& r, int t, int& lo, int& hi) {
-  const long long p = (long long)r.length - ((long long)r.end - t);
-  if (p < 0 || p >= (long long)a.cache.max_pages * kPage) {
-    raise_error(&g_err_kv8, CSA2_DEVERR_PAGE_SLOT);
-    lo = hi = 0;
-    return;
-  }
-  hi = (int)p + 1;
-  lo = a.window > 0 && hi > a.window ? hi - a.window : 0;
-}
 
 // ---- streams of at most 16 rows --------------------------------------------------------------
 //
@@ -118,19 +31,6 @@ template <int D>
 struct Ring {
   static constexpr int kStage = 2 * kHalf * D, kStages = 24576 / kStage;
   static constexpr int kBytes = kWarps * kStages * kStage;
-};
-
-struct Part {                            // a stream that begins in a span and does not end there
-  int rows, t0, r0, h;                   // rows = 0: none
-  int last;                              // the span in which it ends
-};
-
-struct StreamParams {
-  csa2_kv8_attn_args a;
-  int G, aligned;                        // aligned: bit 0 q's rows, bit 1 out's rows on 16 bytes
-  Part* part;                            // [kSpans]
-  float2* ml;                            // [kSpans][2][16] maximum, sum; [1]: of the stream that goes on from here
-  float* o;                              // [kSpans][2][16][D]
 };
 
 // One row's channels, held as v[0 .. D/4) by the four lanes of a quad: dims D/4 * c ...
@@ -166,7 +66,7 @@ __device__ __forceinline__ void store_row(const csa2_kv8_attn_args& a, long long
 // RT: rows of a tile, 8 or 16.  LIST: streams are (row, head) pairs over their listed pages.
 template <int D, int RT, bool LIST>
 __global__ void __launch_bounds__(32 * kWarps, 2)
-k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const StreamParams p) {
+k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8Params p) {
   constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kNt = D / 8, kR = RT / 8;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kSt];
@@ -306,7 +206,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       lo[i] = 0;
       hi[i] = INT_MAX;
       if (g + 8 * i < nrows) {
-        seen_by(a, rows, rows.t0 + (r0 + g + 8 * i) / G, lo[i], hi[i]);
+        seen_by(a, rows, rows.t0 + (r0 + g + 8 * i) / G, lo[i], hi[i], &g_err_kv8);
         lo_min = min(lo_min, lo[i]);
         lo_max = max(lo_max, lo[i]);
         hi_min = min(hi_min, hi[i]);
@@ -644,7 +544,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
           store_row<D>(a, row, q4, v, p.aligned & 2);
           if (q4 == 0 && a.lse) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
         } else {
-          const long long at = ((long long)span * 2 + (begins ? 1 : 0)) * 16 + r;
+          const long long at = ((long long)span * 2 + (begins ? 1 : 0)) * p.most + r;
           if (q4 == 0) p.ml[at] = make_float2(m[i], l[i]);
           float4* dst = reinterpret_cast<float4*>(p.o + at * D + q4 * (D / 4));
 #pragma unroll
@@ -658,18 +558,19 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
   if (lane == 0) p.part[span] = part;
 }
 
-// A CTA a span: the stream that begins there and goes on in the next ones, a warp a row, a lane D / 32 channels.
+// A CTA (span, rows by the sixteen): the stream that begins there and goes on in the next ones, a warp a row, a lane
+// D / 32 channels.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv8_join(const StreamParams p) {
+__global__ void __launch_bounds__(256) k_kv8_join(const Kv8Params p) {
   constexpr int kPer = D / 32, kAhead = 8;
   const csa2_kv8_attn_args& a = p.a;
   pdl_wait();
   pdl_trigger();
   const int w0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Part part = p.part[w0];
-  const int last = min(part.last, kSpans - 1);
-  for (int r = warp; r < part.rows; r += 8) {
-    auto at = [&](int w) { return ((long long)w * 2 + (w == w0 ? 1 : 0)) * 16 + r; };
+  const int last = min(part.last, p.spans - 1), rows = min(part.rows, (int)blockIdx.y * 16 + 16);
+  for (int r = blockIdx.y * 16 + warp; r < rows; r += 8) {
+    auto at = [&](int w) { return ((long long)w * 2 + (w == w0 ? 1 : 0)) * p.most + r; };
     float top = -INFINITY, sum = 0.f, v[kPer] = {};
     for (int b = w0; b <= last; b += 32) {
       const int w = b + lane, n = min(32, last - b + 1);
@@ -718,73 +619,74 @@ __global__ void __launch_bounds__(256) k_kv8_join(const StreamParams p) {
   }
 }
 
-// One plane as [num_pages * Hkv][64][D] bytes, boxes of 32 tokens, swizzled over the rows' width.
-bool plane_map(CUtensorMap* map, const void* base, const csa2_kv8_cache& c) {
-  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-  if (!enc) return false;
-  const cuuint64_t dim[3] = {(cuuint64_t)c.D, kPage, (cuuint64_t)c.num_pages * c.Hkv};
-  const cuuint64_t stride[2] = {(cuuint64_t)c.D, (cuuint64_t)c.D * kPage};
-  const cuuint32_t box[3] = {(cuuint32_t)c.D, kHalf, 1}, one[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dim, stride, box, one,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, c.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Layout {
   size_t part = 0, ml, o, bytes;
-  explicit Layout(int D) {
-    ml = up256(sizeof(Part) * kSpans);
-    o = ml + up256(sizeof(float2) * kSpans * 32);
-    bytes = o + sizeof(float) * kSpans * 32 * D;
+  Layout(int spans, int rows, int D) {
+    ml = up256(sizeof(Part) * spans);
+    o = ml + up256(sizeof(float2) * spans * 2 * rows);
+    bytes = o + sizeof(float) * spans * 2 * rows * D;
   }
 };
 
 template <int D, int RT, bool LIST>
-cudaError_t launch_stream(const CUtensorMap& mk, const CUtensorMap& mv, const StreamParams& p, cudaStream_t st) {
+cudaError_t launch_stream(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8Params& p, cudaStream_t st) {
   static SmemLimit limit;
   const size_t smem = Ring<D>::kBytes + (LIST ? 0 : 8 * (size_t)((p.a.S + 31) / 32));
   cudaError_t e = limit.raise(k_kv8_stream<D, RT, LIST>, smem);
   if (e != cudaSuccess) return e;
-  e = launch_k(k_kv8_stream<D, RT, LIST>, dim3(kStreamCtas), dim3(32 * kWarps), smem, st, mk, mv, p);
-  if (e != cudaSuccess) return e;
-  return launch_k(k_kv8_join<D>, dim3(kSpans), dim3(256), 0, st, p);
+  return launch_k(k_kv8_stream<D, RT, LIST>, dim3(kStreamCtas), dim3(32 * kWarps), smem, st, mk, mv, p);
 }
 
 template <int D>
-cudaError_t launch_rows(const CUtensorMap& mk, const CUtensorMap& mv, const StreamParams& p, cudaStream_t st) {
+cudaError_t launch_rows(const Kv8Params& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!plane_map(&mk, p.a.cache.k, p.a.cache, kHalf) || !plane_map(&mv, p.a.cache.v, p.a.cache, kHalf))
+    return cudaErrorInvalidValue;
   if (p.a.pages) return p.G <= 8 ? launch_stream<D, 8, true>(mk, mv, p, st) : launch_stream<D, 16, true>(mk, mv, p, st);
   return (long long)p.a.max_new * p.G <= 8 ? launch_stream<D, 8, false>(mk, mv, p, st)
                                            : launch_stream<D, 16, false>(mk, mv, p, st);
 }
 
+// Rows of a sequence and key head from which the tiles of 128 rows take over from the streams of 16.
+bool takes_tiles(const csa2_kv8_attn_args& a) {
+  return !a.pages && (long long)a.max_new * (a.Hq / a.cache.Hkv) > 16;
+}
+
 }  // namespace
 
-size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args& a) { return Layout(a.cache.D).bytes; }
+size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args& a) {
+  return (takes_tiles(a) ? Layout(kTileSpans, kTileRows, a.cache.D) : Layout(kSpans, 16, a.cache.D)).bytes;
+}
 
 cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t st) {
   if (a.T == 0 || a.S == 0) return cudaSuccess;
-  CUtensorMap mk, mv;
-  if (!plane_map(&mk, a.cache.k, a.cache) || !plane_map(&mv, a.cache.v, a.cache)) return cudaErrorInvalidValue;
-  StreamParams p;
+  const bool tiles = takes_tiles(a);
+  Kv8Params p;
   p.a = a;
   p.G = a.Hq / a.cache.Hkv;
   const bool q16 = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride_t) | (uintptr_t)(2 * a.q_stride_h)) & 15) == 0;
   p.aligned = (q16 ? 1 : 0) | (((uintptr_t)a.out & 15) == 0 ? 2 : 0);
-  const Layout at(a.cache.D);
+  p.spans = tiles ? kTileSpans : kSpans;
+  p.most = tiles ? kTileRows : 16;
+  const Layout at(p.spans, p.most, a.cache.D);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part = reinterpret_cast<Part*>(w + at.part);
   p.ml = reinterpret_cast<float2*>(w + at.ml);
   p.o = reinterpret_cast<float*>(w + at.o);
-  return a.cache.D == 64 ? launch_rows<64>(mk, mv, p, st) : launch_rows<128>(mk, mv, p, st);
+  cudaError_t e = tiles ? launch_kv8_tile(p, st) : a.cache.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(p.spans, p.most / 16);
+  return a.cache.D == 64 ? launch_k(k_kv8_join<64>, grid, dim3(256), 0, st, p)
+                         : launch_k(k_kv8_join<128>, grid, dim3(256), 0, st, p);
 }
 
 uint32_t read_clear_error_kv8() {
   uint32_t v = 0, z = 0;
   cudaMemcpyFromSymbol(&v, g_err_kv8, sizeof(v));
   if (v) cudaMemcpyToSymbol(g_err_kv8, &z, sizeof(z));
-  return v;
+  return v | read_clear_error_kv8_tile();
 }
 
 }  // namespace csa2

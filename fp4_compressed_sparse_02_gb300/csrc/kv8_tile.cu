@@ -1,0 +1,795 @@
+// Attention over the paged 8-bit cache for many rows (csa2_kv8_attn): tiles of rows on the tcgen05 tensor cores.
+//
+// S = Q K^T and O += P V with float32 accumulators in TMEM, 128 tokens a step.  The keys' bytes are the operand as
+// they come from memory: Q, scaled by a power of two, is the sum of two E4M3 values, exactly for every bf16 within 2^-9
+// of its row's largest and to 2^-18 of the largest below that.  P is fp16, and the values' bytes become
+// fp16 (exact) once a step, by warps of their own.  Two groups of rows take turns: one's softmax runs
+// under the other's products.
+#include "kv8_attn.cuh"
+
+namespace csa2 {
+
+CSA2_DEFINE_ERROR_WORD(g_err_kv8_tile);
+
+namespace {
+
+// Warps 0-3 and 4-7: the softmax of row tile (or step parity, see SPLIT) 0 and 1, a row a thread; 8-11: values to fp16;
+// 12: TMA; 13: products.  The softmax keeps a row of scores in registers, which the other half gives up.
+constexpr int kStep = 128, kThreads = 512, kConvert = 8, kLoad = 12, kMma = 13;
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each: 65,536, what 512 threads of 128 are launched with
+constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
+constexpr int kRing = 3;                 // steps of bytes under way
+constexpr int kOver = 4;                 // what beginning a stream costs, in steps
+
+template <int D>
+struct Smem {
+  static constexpr int kRaw = kStep * D, kQ = 2 * 128 * D, kF = kStep * D * 2;
+  static constexpr int kK = 2 * kQ, kV = kK + kRing * kRaw, kVf = kV + kRing * kRaw, kBytes = kVf + 2 * kF;
+};
+
+struct Shared {
+  uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], vf_full[2], vf_empty[2];
+  uint64_t s_full[2], p_full[2], o_full[2], q_full, done;
+  float2 ks[kInfo], vs[kInfo];           // scales of a step's two pages; -1: not there
+  float2 ml[128];                        // SPLIT: the second group's maximum and sum
+  float unit[4];                         // of the last segments: the largest value scale
+  int nan[4];                            // a NaN value that only some rows see was taken out
+  float top[4];
+  long long scan[kThreads / 32];
+  long long total, begin;                // of the plan: all streams' cost, that before `slot`
+  int slot, dead;
+  uint32_t tmem;
+};
+
+// Shared-memory descriptor of a K-major operand in 8 bits, rows of D bytes swizzled over their width.
+template <int D>
+__device__ __forceinline__ uint64_t desc8(uint32_t saddr) {
+  uint64_t d = tc::smem_desc_sw128(saddr, 16, 8 * D);
+  if constexpr (D == 64) d += (uint64_t)2 << 61;             // SWIZZLE_64B
+  return d;
+}
+
+// E4M3 operands, float32 accumulators.
+__device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
+      :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+// A bounded wait.  After one has given up, all others of the CTA do at once: every role still goes through its loops, so
+// the kernel ends.
+__device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& m) {
+  bool ok = false, gone = false;
+  for (uint32_t i = 0; i < kWaitPolls && !ok && !gone; i += 64) {
+    ok = tc::mbar_wait(bar, parity, 64);
+    if (!ok) gone = *(volatile int*)&m.dead != 0;
+  }
+  if (!ok && !gone) {
+    *(volatile int*)&m.dead = 1;
+    raise_error(&g_err_kv8_tile, CSA2_DEVERR_TIMEOUT);
+  }
+  __syncwarp();
+  return ok;
+}
+
+// The wait for loads from TMEM, as a step that their values pass through.
+__device__ __forceinline__ void tmem_arrived(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :: "memory");
+}
+
+// ---- the work --------------------------------------------------------------------------------
+
+// A stream of a slot: one tile of rows of a sequence, against the steps [step, step + count).
+struct Slot {
+  Rows rows;
+  int s, r0, n;                          // sequence, first row of the tile, rows; n = 0: an empty slot
+  int lo, hi;                            // what any row sees
+  int lo_max, hi_min;                    // what all rows see
+  int step, count;
+};
+
+// Slot floor(start * G / RT) + s and the ones after it hold the row tiles of sequence s.
+template <int RT>
+__device__ __forceinline__ Slot slot_of(const Kv8Params& p, int slot) {
+  const csa2_kv8_attn_args& a = p.a;
+  auto first = [&](int s) {
+    const int x = a.start[s];
+    return (long long)(x < 0 ? 0 : x > a.T ? a.T : x) * p.G / RT + s;
+  };
+  Slot t = {};
+  int s = 0, end = a.S;
+  while (end - s > 1) {
+    const int mid = (s + end) >> 1;
+    if (first(mid) <= slot) s = mid; else end = mid;
+  }
+  t.s = s;
+  t.rows = rows_of(a, s, p.G);
+  const long long r0 = (slot - first(s)) * RT;
+  if (r0 < 0 || r0 >= t.rows.n) return t;
+  t.r0 = (int)r0;
+  t.n = min(RT, t.rows.n - t.r0);
+  const int limit = a.cache.max_pages * kPage;
+  auto seen = [&](int r) {               // positions up to which row r sees, as if the table had no end
+    return (long long)t.rows.length - ((long long)t.rows.end - (t.rows.t0 + r / p.G)) + 1;
+  };
+  auto clamp = [&](long long x) { return (int)(x < 0 ? 0 : x > limit ? limit : x); };
+  const long long from = seen(t.r0), to = seen(t.r0 + t.n - 1);
+  t.hi_min = clamp(from);
+  t.hi = clamp(to);
+  t.lo = a.window > 0 ? clamp(from - a.window) : 0;
+  t.lo_max = a.window > 0 ? clamp(to - a.window) : 0;
+  if (from < 1 || to > limit) t.hi_min = 0;                // rows outside the table see nothing
+  t.step = t.lo / kStep;
+  t.count = (t.hi + kStep - 1) / kStep - t.step;
+  if (t.count < 1) t.count = 1;          // rows that see nothing are written all the same
+  return t;
+}
+
+// What a slot's stream costs, in steps.
+__device__ __forceinline__ int cost_of(const Slot& t) { return t.count > 0 ? t.count + kOver : 0; }
+
+// A CTA's span of all streams' cost (slot by slot, head by head), walked by every role alike.  A cut within a stream's
+// first kOver units is a cut before its first step.
+template <int RT>
+struct Walk {
+  Slot t;
+  int slot, h, x, take;                  // the segment: steps x .. x + take of the stream
+  int spent;                             // its cost
+  long long left;                        // cost of the span that is still to come, with the segment's
+  int n;                                 // segments before this one
+
+  __device__ __forceinline__ void cut(int at) {              // at: cost of the stream that earlier spans have
+    const int rest = cost_of(t) - at;
+    spent = (int)(rest < left ? rest : left);
+    x = max(0, at - kOver);
+    take = max(0, at + spent - kOver) - x;
+  }
+  __device__ __forceinline__ Walk(const Kv8Params& p, const Shared& m, long long per) {
+    const long long begin = blockIdx.x * per;
+    left = m.total - begin < per ? m.total - begin : per;
+    n = 0;
+    if (left <= 0) return;
+    slot = m.slot;
+    t = slot_of<RT>(p, slot);
+    const long long rel = begin - m.begin;
+    h = (int)(rel / cost_of(t));
+    cut((int)(rel % cost_of(t)));
+    if (take == 0) {
+      n = -1;
+      next(p);
+    }
+  }
+  __device__ __forceinline__ bool on() const { return left > 0; }
+  __device__ __forceinline__ void next(const Kv8Params& p) {
+    ++n;
+    do {
+      left -= spent;
+      if (left <= 0) return;
+      if (++h == p.a.cache.Hkv) {
+        h = 0;
+        do t = slot_of<RT>(p, ++slot); while (t.count == 0);
+      }
+      cut(0);
+    } while (take == 0);
+  }
+  __device__ __forceinline__ bool begins() const { return x == 0; }
+  __device__ __forceinline__ bool ends() const { return x + take == t.count; }
+};
+
+// SPLIT: one tile of 128 rows, whose even and odd steps are two streams of their own that are added up at the end of a
+// segment; else two tiles of 128 rows that share every step.
+template <int D, bool SPLIT>
+__global__ void __launch_bounds__(kThreads, 1)
+k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8Params p) {
+  constexpr int RT = SPLIT ? 128 : 256;
+  using L = Smem<D>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Shared m;
+  const csa2_kv8_attn_args& a = p.a;
+  const csa2_kv8_cache& c = a.cache;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
+  const uint32_t base = smem_u32(smem);
+  if ((base & 1023) != 0) {              // uniform: the swizzles count on it
+    if (tid == 0) raise_error(&g_err_kv8_tile, CSA2_DEVERR_SMEM_ALIGN);
+    return;
+  }
+  if (warp == kMma) tc::tmem_alloc(&m.tmem, 512);
+  if (tid == 0) {
+    for (int i = 0; i < kRing; ++i) {
+      tc::mbar_init(&m.k_full[i], 1);
+      tc::mbar_init(&m.k_empty[i], 1);
+      tc::mbar_init(&m.v_full[i], 1);
+      tc::mbar_init(&m.v_empty[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&m.vf_full[i], 4);
+      tc::mbar_init(&m.vf_empty[i], 1);
+      tc::mbar_init(&m.s_full[i], 1);
+      tc::mbar_init(&m.p_full[i], 4);
+      tc::mbar_init(&m.o_full[i], 1);
+    }
+    tc::mbar_init(&m.q_full, SPLIT ? 4 : 8);
+    tc::mbar_init(&m.done, 1);
+    m.dead = 0;
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- the plan: steps of all slots, and the slot in which this CTA's span begins
+  const int slots = (int)((long long)a.T * G / RT) + a.S;
+  const int chunk = (slots + kThreads - 1) / kThreads;
+  const int c0 = min(slots, tid * chunk), c1 = min(slots, c0 + chunk);
+  long long mine = 0;
+  for (int i = c0; i < c1; ++i) mine += cost_of(slot_of<RT>(p, i));
+  mine *= c.Hkv;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long u = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += u;
+  }
+  if (lane == 31) m.scan[warp] = inc;
+  tc::fence_proxy_async_smem();          // the initialised barriers, for the copies
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  long long total = 0;
+  for (int i = 0; i < kThreads / 32; ++i) {
+    if (i < warp) inc += m.scan[i];
+    total += m.scan[i];
+  }
+  const long long even = (total + kTileSpans - 1) / kTileSpans, per = even > kOver + 2 ? even : kOver + 2;
+  const long long begin = blockIdx.x * per;
+  if (tid == 0) m.total = total;
+  if (begin < total && inc > begin && inc - mine <= begin) {
+    long long at = inc - mine;
+    int i = c0;
+    for (; i < c1 - 1; ++i) {
+      const long long n = (long long)cost_of(slot_of<RT>(p, i)) * c.Hkv;
+      if (at + n > begin) break;
+      at += n;
+    }
+    m.slot = i;
+    m.begin = at;
+  }
+  __syncthreads();
+  const uint32_t tb = m.tmem;
+
+  if (warp >= kConvert) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
+    Walk<RT> w(p, m, per);
+    if (warp == kLoad) {
+      // ---- TMA: the pages of each step, keys and values
+      int step = 0;                      // steps so far
+      for (; w.on(); w.next(p)) {
+        const int pages = (w.t.hi + kPage - 1) / kPage, page0 = 2 * (w.t.step + w.x);
+        int id = -1;                     // lane i: page page0 + 32 b + i
+        float ks = -1.f, vs = -1.f;
+        for (int j = 0; j < w.take; ++j, ++step) {
+          if ((j & 15) == 0) {
+            const int y = page0 + 2 * j + lane;
+            id = y < pages && 2 * j + lane < 2 * w.take ? page_id(c, w.t.s, y, &g_err_kv8_tile) : -1;
+            ks = vs = -1.f;
+            if (id >= 0) {
+              ks = c.k_scale[(long long)id * c.Hkv + w.h];
+              vs = c.v_scale[(long long)id * c.Hkv + w.h];
+            }
+          }
+          const int at = (j & 15) * 2, b = step % kRing;
+          const uint32_t turn = (step / kRing & 1) ^ 1;
+          const int id0 = __shfl_sync(0xffffffffu, id, at), id1 = __shfl_sync(0xffffffffu, id, at + 1);
+          const float k0 = __shfl_sync(0xffffffffu, ks, at), k1 = __shfl_sync(0xffffffffu, ks, at + 1);
+          const float v0 = __shfl_sync(0xffffffffu, vs, at), v1 = __shfl_sync(0xffffffffu, vs, at + 1);
+          const uint32_t bytes = ((id0 >= 0) + (id1 >= 0)) * (L::kRaw / 2);
+          bool ok = await(&m.k_empty[b], turn, m);
+          if (lane == 0 && ok) {
+            m.ks[step % kInfo] = make_float2(k0, k1);
+            m.vs[step % kInfo] = make_float2(v0, v1);
+            uint8_t* dst = smem + L::kK + b * L::kRaw;
+            tc::mbar_arrive_expect_tx(&m.k_full[b], bytes);
+            if (id0 >= 0) tma_load_3d(dst, &mk, 0, 0, id0 * c.Hkv + w.h, &m.k_full[b]);
+            if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mk, 0, 0, id1 * c.Hkv + w.h, &m.k_full[b]);
+          }
+          __syncwarp();
+          ok = await(&m.v_empty[b], turn, m);
+          if (lane == 0 && ok) {
+            uint8_t* dst = smem + L::kV + b * L::kRaw;
+            tc::mbar_arrive_expect_tx(&m.v_full[b], bytes);
+            if (id0 >= 0) tma_load_3d(dst, &mv, 0, 0, id0 * c.Hkv + w.h, &m.v_full[b]);
+            if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mv, 0, 0, id1 * c.Hkv + w.h, &m.v_full[b]);
+          }
+          __syncwarp();
+        }
+      }
+      if (*(volatile int*)&m.dead && lane == 0)              // no copy outlives the CTA
+        for (int i = 0; i < kRing; ++i)
+          for (int back = 1; back <= kRing; ++back) {
+            const int st = step - back;
+            if (st < 0 || st % kRing != i) continue;
+            tc::mbar_wait(&m.k_full[i], st / kRing & 1, kWaitPolls / 64);
+            tc::mbar_wait(&m.v_full[i], st / kRing & 1, kWaitPolls / 64);
+          }
+    } else if (warp == kMma) {
+      // ---- products.  Of each group: S of its next step as soon as its weights have been taken from the last one.
+      constexpr uint32_t id_s = tc::idesc_f16(128, kStep, 0, 0, 0), id_o = tc::idesc_f16(128, D, 0, 0, 1);   // E4M3 is type 0, as fp16
+      int step = 0;                      // steps of earlier segments
+      int ps[2] = {0, 0};                // weights taken from each group so far
+      auto scores = [&](int g, int st) { // group g, step st of the kernel
+        if (lane == 0) {
+          const uint32_t qa = base + (SPLIT ? 0 : g * L::kQ), kb = base + L::kK + st % kRing * L::kRaw;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i)                   // Q's first part, then its second
+            mma_f8_ss(tb + g * 128, desc8<D>(qa + i / (D / 32) * (128 * D) + i % (D / 32) * 32),
+                      desc8<D>(kb + i % (D / 32) * 32), id_s, i > 0);
+          tc::mma_commit(&m.s_full[g]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int g, int st, bool more) {
+        await(&m.p_full[g], ps[g]++ & 1, m);
+        await(&m.vf_full[st & 1], st >> 1 & 1, m);
+        tc::fence_after_sync();
+        if (lane == 0) {
+          const uint32_t vb = base + L::kVf + (st & 1) * L::kF;
+#pragma unroll
+          for (int i = 0; i < kStep / 16; ++i)
+            tc::mma_f16_ts(tb + 256 + g * 128, tb + g * 128 + i * 8, tc::smem_desc_sw128(vb + i * 2048, 16384, 1024), id_o,
+                           more || i > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* bar) {
+        if (lane == 0) tc::mma_commit(bar);
+        __syncwarp();
+      };
+      auto keys = [&](int st) {
+        await(&m.k_full[st % kRing], st / kRing & 1, m);
+        tc::fence_after_sync();
+      };
+      for (; w.on(); w.next(p)) {
+        const int n = w.take;
+        await(&m.q_full, w.n & 1, m);
+        tc::fence_after_sync();
+        if constexpr (SPLIT) {
+          for (int j = 0; j < 2 && j < n; ++j) {
+            keys(step + j);
+            scores(j, step + j);
+            commit(&m.k_empty[(step + j) % kRing]);
+          }
+          for (int j = 0; j < n; ++j) {
+            values(j & 1, step + j, j > 1);
+            commit(&m.vf_empty[(step + j) & 1]);
+            if (j + 2 < n) {
+              keys(step + j + 2);
+              scores(j & 1, step + j + 2);
+              commit(&m.k_empty[(step + j + 2) % kRing]);
+            } else {
+              commit(&m.o_full[j & 1]);
+            }
+          }
+        } else {
+          keys(step);
+          scores(0, step);
+          scores(1, step);
+          commit(&m.k_empty[step % kRing]);
+          for (int j = 0; j < n; ++j) {
+            const int st = step + j;
+            values(0, st, j > 0);
+            if (j + 1 < n) {
+              keys(st + 1);
+              scores(0, st + 1);
+            } else {
+              commit(&m.o_full[0]);
+            }
+            values(1, st, j > 0);
+            commit(&m.vf_empty[st & 1]);
+            if (j + 1 < n) {
+              scores(1, st + 1);
+              commit(&m.k_empty[(st + 1) % kRing]);
+            } else {
+              commit(&m.o_full[1]);
+            }
+          }
+        }
+        step += n;
+      }
+      if (*(volatile int*)&m.dead) {                         // nor a product
+        commit(&m.done);
+        tc::mbar_wait(&m.done, 0, kWaitPolls);
+      }
+    } else if (warp < kLoad) {
+      // ---- values: E4M3 to fp16, a token a thread, into the product's layout (atoms of 64 channels x 128 tokens)
+      const int r = tid - kConvert * 32;
+      int step = 0;
+      for (; w.on(); w.next(p)) {
+        const Slot& t = w.t;
+        // in units of the largest scale of the segment, times 2^-7: exact for scales down to 2^-22 of it
+        float top = 0.f;
+        const int y1 = min((t.hi + kPage - 1) / kPage, 2 * (t.step + w.x + w.take));
+        for (int y = 2 * (t.step + w.x) + r; y < y1; y += 128) {
+          const int id = __ldg(c.page_table + (long long)t.s * c.max_pages + y);
+          if (id >= 0 && id < c.num_pages) top = fmaxf(top, c.v_scale[(long long)id * c.Hkv + w.h]);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) m.top[warp - kConvert] = top;
+        named_sync(2, 128);
+        top = fmaxf(fmaxf(m.top[0], m.top[1]), fmaxf(m.top[2], m.top[3]));
+        if (!(top > 0.f && top < INFINITY)) top = 1.f;
+        if (r == 0) {
+          m.unit[w.n & 3] = top;
+          m.nan[w.n & 3] = 0;
+        }
+        named_sync(2, 128);
+        for (int j = 0; j < w.take; ++j, ++step) {
+          const int token = (t.step + w.x + j) * kStep + r, b = step % kRing;
+          const bool border = token < t.lo_max || token >= t.hi_min;         // not every row sees it
+          const uint32_t raw = base + L::kV + b * L::kRaw + r * D, dst = base + L::kVf + (step & 1) * L::kF + r * 128;
+          await(&m.v_full[b], step / kRing & 1, m);
+          uint4 x[D / 16];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            if constexpr (D == 128) x[i] = lds128(raw + ((i ^ (r & 7)) << 4));
+            else x[i] = lds128(raw + ((i ^ (r >> 1 & 3)) << 4));
+          }
+          const float2 vs = m.vs[step % kInfo];
+          float f = r < kPage ? vs.x : vs.y;
+          const bool there = f != -1.f && token < t.hi && token >= t.lo;
+          f = there ? f * 128.f / top : 0.f;
+          if (!there || border) {
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              uint32_t* v = reinterpret_cast<uint32_t*>(&x[i]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t at = (((v[e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in each NaN's byte
+                v[e] = there ? v[e] & ~(at * 0xffu) : 0u;                     // `border`: rows get their NaNs at the end
+                nan |= there && at != 0;
+              }
+            }
+            if (nan) *(volatile int*)&m.nan[w.n & 3] = 1;
+          }
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&m.v_empty[b]);
+          await(&m.vf_empty[step & 1], (step >> 1 & 1) ^ 1, m);
+          const __half2 f2 = __half2half2(__float2half_rn(f));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t o[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              o[2 * e] = e4m3x2_lo_f16x2(v[e]);
+              o[2 * e + 1] = e4m3x2_hi_f16x2(v[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&o[e]), f2);
+              o[e] = *reinterpret_cast<const uint32_t*>(&y);
+            }
+            const uint32_t atom = dst + (i >> 2) * 16384;
+            sts128(atom + ((((2 * i) & 7) ^ (r & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+            sts128(atom + ((((2 * i + 1) & 7) ^ (r & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+          }
+          tc::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&m.vf_full[step & 1]);
+        }
+      }
+    }
+  } else {
+    // ---- softmax: a row a thread
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
+    Walk<RT> w(p, m, per);
+    const int grp = warp >> 2, r = tid & 127;
+    const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21), s_at = lanes + grp * 128, o_at = lanes + 256 + grp * 128;
+    int step = 0, seen = 0, outs = 0, outs1 = 0;   // steps of earlier segments; scores, outputs waited for
+    Part part = {0, 0, 0, 0, 0};
+    for (; w.on(); w.next(p)) {
+      const Slot& t = w.t;
+      const int row = (SPLIT ? 0 : grp * 128) + r;
+      const bool real = row < t.n;
+      int lo = 0, hi = INT_MAX;
+      const int tok = real ? t.rows.t0 + (t.r0 + row) / G : 0, hq = real ? w.h * G + (t.r0 + row) % G : 0;
+      if (real) seen_by(a, t.rows, tok, lo, hi, &g_err_kv8_tile);
+      // the row of Q: scaled by a power of two to below 2^8, as the sum of two E4M3 rows
+      float mul;
+      {
+        float top = 0.f, f, undo;
+        const uint16_t* q = a.q + tok * a.q_stride_t + (long long)hq * a.q_stride_h;
+        uint32_t v[D / 2];
+        if (!real) {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) v[i] = 0;
+        } else if (p.aligned & 1) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) {
+            const uint4 x = reinterpret_cast<const uint4*>(q)[i];
+            v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) v[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) {
+          const float x0 = fabsf(__uint_as_float(v[i] << 16)), x1 = fabsf(__uint_as_float(v[i] & 0xffff0000u));
+          top = x0 >= top ? x0 : x0 != x0 ? INFINITY : top;
+          top = x1 >= top ? x1 : x1 != x1 ? INFINITY : top;
+        }
+        row_factor(top, f, undo);
+        f *= 0.0078125f;
+        mul = undo * 128.f * (a.softmax_scale * kLog2e);
+        const uint32_t bad = top == INFINITY ? 0x7f7f7f7fu : 0u;               // an infinity makes its row NaN, as a NaN does
+        if (!SPLIT || grp == 0) {
+          const uint32_t dst = base + (SPLIT ? 0 : grp * L::kQ) + r * D;
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            uint32_t hi8[4], lo8[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              hi8[e] = lo8[e] = bad;
+              if (!bad) {
+                hi8[e] = 0;
+                lo8[e] = 0;
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                  const uint32_t u = v[8 * i + 2 * e + d];
+                  const float x0 = __uint_as_float(u << 16) * f, x1 = __uint_as_float(u & 0xffff0000u) * f;
+                  const uint32_t first = cvt_e4m3x2(x0, x1), back = e4m3x2_to_f16x2((uint16_t)first);
+                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&back));
+                  hi8[e] |= first << 16 * d;
+                  lo8[e] |= cvt_e4m3x2(x0 - y.x, x1 - y.y) << 16 * d;
+                }
+              }
+            }
+            const uint32_t at = dst + ((D == 128 ? i ^ (r & 7) : i ^ (r >> 1 & 3)) << 4);
+            sts128(at, make_uint4(hi8[0], hi8[1], hi8[2], hi8[3]));
+            sts128(at + 128 * D, make_uint4(lo8[0], lo8[1], lo8[2], lo8[3]));
+          }
+          tc::fence_proxy_async_smem();
+          tc::fence_before_sync();       // the last segment's TMEM reads
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&m.q_full);
+        }
+      }
+      float top = -INFINITY, l = 0.f;
+      bool any = false;                  // a step of this segment has been added to O
+      for (int j = SPLIT ? grp : 0; j < w.take; j += SPLIT ? 2 : 1) {
+        await(&m.s_full[grp], seen++ & 1, m);
+        tc::fence_after_sync();
+        const float2 ks = m.ks[(step + j) % kInfo];
+        const int token0 = (t.step + w.x + j) * kStep;
+        // positive, so that a masked score's -infinity stays one; a page that is not there is masked as a whole
+        const float f0 = fmaxf(mul * (ks.x == -1.f ? 1.f : ks.x), 1.17549435e-38f);
+        const float f1 = fmaxf(mul * (ks.y == -1.f ? 1.f : ks.y), 1.17549435e-38f);
+        const bool border = __any_sync(0xffffffffu, token0 < lo || token0 + kStep > hi || ks.x == -1.f || ks.y == -1.f);
+        const int from0 = ks.x == -1.f ? INT_MAX : lo - token0, from1 = ks.y == -1.f ? INT_MAX : lo - token0;
+        const int to = hi == INT_MAX ? INT_MAX : hi - token0;
+        float x[kStep];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tc::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x + 32 * i));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_arrived(x + 32 * i);
+        if (border) {
+#pragma unroll
+          for (int e = 0; e < kStep; ++e) {
+            const bool in = e >= (e < kPage ? from0 : from1) && e < to;
+            x[e] = in ? x[e] : -INFINITY;
+          }
+        }
+        float mx[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mx[i] = x[16 * i];
+#pragma unroll
+          for (int e = 1; e < 16; ++e) mx[i] = fmaxf(mx[i], x[16 * i + e]);
+        }
+        const float now = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f0, fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])) * f1);
+        // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
+        // sum are rescaled a few times a row.
+        const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
+        if (__any_sync(0xffffffffu, follow)) {
+          const float alpha = follow ? ex2(top - now) : 1.f;
+          if (follow) top = now;
+          l *= alpha;
+          if (any) {
+#pragma unroll 1
+            for (int i = 0; i < D; i += 32) {
+              float v[32];
+              tc::tmem_ld32(o_at + i, reinterpret_cast<uint32_t*>(v));
+              tmem_arrived(v);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) v[e] *= alpha;
+              tc::tmem_st32(o_at + i, reinterpret_cast<const uint32_t*>(v));
+            }
+          }
+        }
+        any = true;
+        const float z = top == -INFINITY ? 0.f : top;
+        float2 sum[4] = {};
+        const float2 zz = make_float2(-z, -z);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 f = i < 4 ? make_float2(f0, f0) : make_float2(f1, f1);
+          uint32_t w8[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            float2 y = fma2(make_float2(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]), f, zz);
+            y.x = ex2(y.x);
+            y.y = ex2(y.y);
+            w8[e] = f16x2(y.x, y.y);
+            sum[e & 3] = add2(sum[e & 3], y);
+          }
+          tc::tmem_st8(s_at + 8 * i, w8);                    // over the scores
+        }
+        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+        l += sum[0].x + sum[0].y;
+        tc::tmem_st_wait();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&m.p_full[grp]);
+      }
+      // ---- the segment's result, or its part
+      const bool two = SPLIT && w.take > 1;                  // both groups have steps
+      if (SPLIT && grp == 1) m.ml[r] = make_float2(top, l);
+      if (SPLIT) named_sync(1, 256);
+      if (!SPLIT || grp == 0) {
+        await(&m.o_full[grp], outs++ & 1, m);
+        if (two) await(&m.o_full[1], outs1++ & 1, m);
+        tc::fence_after_sync();
+        float a0 = 1.f, a1 = 0.f;
+        if (two) {
+          const float2 o = m.ml[r];
+          const float n = fmaxf(top, o.x), z = n == -INFINITY ? 0.f : n;
+          a0 = ex2(top - z);
+          a1 = ex2(o.x - z);
+          l = l * a0 + o.y * a1;
+          top = n;
+        }
+        const bool whole = w.begins() && w.ends();
+        const float unit = m.unit[w.n & 3] * 0.0078125f;
+        const float inv = whole ? (l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
+        const bool nan = m.nan[w.n & 3] != 0;
+        const long long out_row = (long long)tok * a.Hq + hq;
+        const long long at = ((long long)blockIdx.x * 2 + (w.begins() ? 1 : 0)) * p.most + row;
+#pragma unroll 1
+        for (int i = 0; i < D; i += 32) {
+          float v[32];
+          tc::tmem_ld32(o_at + i, reinterpret_cast<uint32_t*>(v));
+          tmem_arrived(v);
+          if (two) {
+            float u[32];
+            tc::tmem_ld32(o_at + 128 + i, reinterpret_cast<uint32_t*>(u));
+            tmem_arrived(u);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = v[e] * a0 + u[e] * a1;
+          }
+          if (!real) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e) v[e] = v[e] * unit * inv;
+          if (nan) {                     // the NaNs that this row sees, among the tokens that not all rows see
+            const int u0 = (t.step + w.x) * kStep, u1 = u0 + w.take * kStep;
+            uint32_t bits = 0;
+#pragma unroll 1
+            for (int side = 0; side < 2; ++side) {
+              const int b = max(max(u0, lo), side ? max(t.hi_min, t.lo_max) : t.lo), e = min(min(u1, hi), side ? t.hi : t.lo_max);
+#pragma unroll 1
+              for (int y = b; y < e; ++y) {
+                const int id = __ldg(c.page_table + (long long)t.s * c.max_pages + y / kPage);
+                if (id < 0 || id >= c.num_pages) continue;
+                const uint8_t* src = c.v + (((long long)id * c.Hkv + w.h) * kPage + y % kPage) * D + i;
+#pragma unroll 1
+                for (int d = 0; d < 32; ++d) bits |= (uint32_t)((src[d] & 0x7f) == 0x7f) << d;
+              }
+            }
+#pragma unroll
+            for (int d = 0; d < 32; ++d)
+              if (bits >> d & 1) v[d] = NAN;
+          }
+          if (!whole) {
+            float4* dst = reinterpret_cast<float4*>(p.o + at * D + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else if (a.out_dtype == CSA2_F32) {
+            float* dst = reinterpret_cast<float*>(a.out) + out_row * D + i;
+            if (p.aligned & 2) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) reinterpret_cast<float4*>(dst)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) dst[e] = v[e];
+            }
+          } else {
+            uint16_t* dst = reinterpret_cast<uint16_t*>(a.out) + out_row * D + i;
+            uint32_t o[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] = bf16x2(v[2 * e], v[2 * e + 1]);
+            if (p.aligned & 2) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; ++e) dst[e] = (uint16_t)(o[e / 2] >> 16 * (e & 1));
+            }
+          }
+        }
+        if (real) {
+          if (!whole) p.ml[at] = make_float2(top, l);
+          else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
+        }
+      }
+      if (SPLIT) {
+        tc::fence_before_sync();
+        named_sync(1, 256);              // the second group's output and sums have been read
+        tc::fence_after_sync();
+      }
+      if (w.begins() && !w.ends())
+        part = Part{t.n, t.rows.t0, t.r0, w.h, (int)blockIdx.x + (int)((t.count - w.take + per - 1) / per)};
+      step += w.take;
+    }
+    if (tid == 0) p.part[blockIdx.x] = part;
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kMma) tc::tmem_dealloc(tb, 512);
+}
+
+template <int D, bool SPLIT>
+cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8Params& p, cudaStream_t st) {
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(k_kv8_tile<D, SPLIT>, Smem<D>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_k(k_kv8_tile<D, SPLIT>, dim3(kTileSpans), dim3(kThreads), Smem<D>::kBytes, st, mk, mv, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_tile(const Kv8Params& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!plane_map(&mk, p.a.cache.k, p.a.cache, kPage) || !plane_map(&mv, p.a.cache.v, p.a.cache, kPage))
+    return cudaErrorInvalidValue;
+  const bool split = (long long)p.a.max_new * p.G <= 128;
+  if (p.a.cache.D == 64) return split ? launch<64, true>(mk, mv, p, st) : launch<64, false>(mk, mv, p, st);
+  return split ? launch<128, true>(mk, mv, p, st) : launch<128, false>(mk, mv, p, st);
+}
+
+uint32_t read_clear_error_kv8_tile() {
+  uint32_t v = 0, z = 0;
+  cudaMemcpyFromSymbol(&v, g_err_kv8_tile, sizeof(v));
+  if (v) cudaMemcpyToSymbol(g_err_kv8_tile, &z, sizeof(z));
+  return v;
+}
+
+}  // namespace csa2

@@ -761,7 +761,7 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * largest element); probabilities are fp16 (2^-12 relative).  A NaN that a row does not see does
  * not reach it.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
- * window >= 0; S <= 2^18.
+ * window >= 0; S <= 2^18; T * Hq < 2^31.
  * -------------------------------------------------------------------------- */
 typedef struct csa2_kv8_attn_args {
   size_t struct_size;
