@@ -19,6 +19,7 @@ constexpr int kStep = 128, kThreads = 512, kConvert = 8, kLoad = 12, kMma = 13;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each: 65,536, what 512 threads of 128 are launched with
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
+constexpr uint32_t kTilePolls = 1u << 18;
 constexpr int kOver = 4;                 // what beginning a stream costs, in steps
 
 template <int D>
@@ -76,24 +77,43 @@ __device__ __forceinline__ void sts128(uint32_t a, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
+// One thread of a warp whose threads are together.  The compiler knows that it is one, keeps the products' operands in
+// uniform registers and issues a product in a few instructions; behind `lane == 0` it takes several times as many, and
+// the warp, which shares its scheduler with two busy softmax warps, falls behind the tensor core (4096 new tokens at 32K:
+// 6.1 ms).
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
+  return p != 0;
+}
+
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
-// A bounded wait.  After one has given up, all others of the CTA do at once: every role still goes through its loops, so
-// the kernel ends.
+// A bounded wait of one thread (a poll lasts up to some microseconds).  After one has given up, all others of the CTA do
+// at once: every role still goes through its loops, so the kernel ends.
 __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& m) {
-  bool ok = false, gone = false;
-  for (uint32_t i = 0; i < kWaitPolls && !ok && !gone; i += 64) {
-    ok = tc::mbar_wait(bar, parity, 64);
-    if (!ok) gone = *(volatile int*)&m.dead != 0;
+  const uint32_t at = smem_u32(bar);
+  uint32_t done, polls = 0;
+  while (true) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(at), "r"(parity) : "memory");
+    if (done) return true;
+    if (*(volatile int*)&m.dead) return false;
+    if (++polls == kTilePolls) {
+      *(volatile int*)&m.dead = 1;
+      raise_error(&g_err_kv8_tile, CSA2_DEVERR_TIMEOUT);
+      return false;
+    }
   }
-  if (!ok && !gone) {
-    *(volatile int*)&m.dead = 1;
-    raise_error(&g_err_kv8_tile, CSA2_DEVERR_TIMEOUT);
-  }
+}
+
+// The same by every thread of a warp, which are together again after it.
+__device__ __forceinline__ void await_warp(uint64_t* bar, uint32_t parity, Shared& m) {
+  await(bar, parity, m);
   __syncwarp();
-  return ok;
 }
 
 // The wait for loads from TMEM, as a step that their values pass through.
@@ -309,23 +329,22 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           const int id0 = __shfl_sync(0xffffffffu, id, at), id1 = __shfl_sync(0xffffffffu, id, at + 1);
           const float k0 = __shfl_sync(0xffffffffu, ks, at), k1 = __shfl_sync(0xffffffffu, ks, at + 1);
           const float v0 = __shfl_sync(0xffffffffu, vs, at), v1 = __shfl_sync(0xffffffffu, vs, at + 1);
-          const uint32_t bytes = ((id0 >= 0) + (id1 >= 0)) * (L::kRaw / 2);
-          bool ok = await(&m.k_empty[b], turn, m);
-          if (lane == 0 && ok) {
-            m.ks[step % kInfo] = make_float2(k0, k1);
-            m.vs[step % kInfo] = make_float2(v0, v1);
-            uint8_t* dst = smem + L::kK + b * L::kRaw;
-            tc::mbar_arrive_expect_tx(&m.k_full[b], bytes);
-            if (id0 >= 0) tma_load_3d(dst, &mk, 0, 0, id0 * c.Hkv + w.h, &m.k_full[b]);
-            if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mk, 0, 0, id1 * c.Hkv + w.h, &m.k_full[b]);
-          }
-          __syncwarp();
-          ok = await(&m.v_empty[b], turn, m);
-          if (lane == 0 && ok) {
-            uint8_t* dst = smem + L::kV + b * L::kRaw;
-            tc::mbar_arrive_expect_tx(&m.v_full[b], bytes);
-            if (id0 >= 0) tma_load_3d(dst, &mv, 0, 0, id0 * c.Hkv + w.h, &m.v_full[b]);
-            if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mv, 0, 0, id1 * c.Hkv + w.h, &m.v_full[b]);
+          if (lane == 0) {
+            const uint32_t bytes = ((id0 >= 0) + (id1 >= 0)) * (L::kRaw / 2);
+            if (await(&m.k_empty[b], turn, m)) {
+              m.ks[step % kInfo] = make_float2(k0, k1);
+              m.vs[step % kInfo] = make_float2(v0, v1);
+              uint8_t* dst = smem + L::kK + b * L::kRaw;
+              tc::mbar_arrive_expect_tx(&m.k_full[b], bytes);
+              if (id0 >= 0) tma_load_3d(dst, &mk, 0, 0, id0 * c.Hkv + w.h, &m.k_full[b]);
+              if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mk, 0, 0, id1 * c.Hkv + w.h, &m.k_full[b]);
+            }
+            if (await(&m.v_empty[b], turn, m)) {
+              uint8_t* dst = smem + L::kV + b * L::kRaw;
+              tc::mbar_arrive_expect_tx(&m.v_full[b], bytes);
+              if (id0 >= 0) tma_load_3d(dst, &mv, 0, 0, id0 * c.Hkv + w.h, &m.v_full[b]);
+              if (id1 >= 0) tma_load_3d(dst + L::kRaw / 2, &mv, 0, 0, id1 * c.Hkv + w.h, &m.v_full[b]);
+            }
           }
           __syncwarp();
         }
@@ -335,96 +354,84 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           for (int back = 1; back <= kRing; ++back) {
             const int st = step - back;
             if (st < 0 || st % kRing != i) continue;
-            tc::mbar_wait(&m.k_full[i], st / kRing & 1, kWaitPolls / 64);
-            tc::mbar_wait(&m.v_full[i], st / kRing & 1, kWaitPolls / 64);
+            tc::mbar_wait(&m.k_full[i], st / kRing & 1, kTilePolls / 64);
+            tc::mbar_wait(&m.v_full[i], st / kRing & 1, kTilePolls / 64);
           }
     } else if (warp == kMma) {
       // ---- products.  Of each group: S of its next step as soon as its weights have been taken from the last one.
       constexpr uint32_t id_s = tc::idesc_f16(128, kStep, 0, 0, 0), id_o = tc::idesc_f16(128, D, 0, 0, 1);   // E4M3 is type 0, as fp16
-      int step = 0;                      // steps of earlier segments
-      int ps[2] = {0, 0};                // weights taken from each group so far
-      auto scores = [&](int g, int st) { // group g, step st of the kernel
-        if (lane == 0) {
-          const uint32_t qa = base + (SPLIT ? 0 : g * L::kQ), kb = base + L::kK + st % kRing * L::kRaw;
+      const uint64_t q_desc = desc8<D>(base), k_desc = desc8<D>(base + L::kK), v_desc = tc::smem_desc_sw128(base + L::kVf, 16384, 1024);
+      int ring = 0, turn = 0;            // of the next step whose scores are taken
+      int step = 0;                      // of the next step whose values are taken
+      uint32_t ps = 0;                   // parities of the weights
+      auto keys = [&] {
+        await_warp(&m.k_full[ring], turn, m);
+        tc::fence_after_sync();
+      };
+      auto scores = [&](int g, bool last) {                  // last: of the step's
+        if (elect()) {
+          const uint64_t qa = q_desc + (SPLIT ? 0 : g * (L::kQ >> 4)), kb = k_desc + (uint32_t)(ring * (L::kRaw >> 4));
 #pragma unroll
           for (int i = 0; i < D / 16; ++i)                   // Q's first part, then its second
-            mma_f8_ss(tb + g * 128, desc8<D>(qa + i / (D / 32) * (128 * D) + i % (D / 32) * 32),
-                      desc8<D>(kb + i % (D / 32) * 32), id_s, i > 0);
+            mma_f8_ss(tb + g * 128, qa + (i / (D / 32) * (128 * D) + i % (D / 32) * 32) / 16, kb + i % (D / 32) * 2, id_s, i > 0);
           tc::mma_commit(&m.s_full[g]);
+          if (last) tc::mma_commit(&m.k_empty[ring]);
         }
         __syncwarp();
+        if (last && ++ring == kRing) {
+          ring = 0;
+          turn ^= 1;
+        }
       };
-      auto values = [&](int g, int st, bool more) {
-        await(&m.p_full[g], ps[g]++ & 1, m);
-        await(&m.vf_full[st & 1], st >> 1 & 1, m);
+      auto values = [&](int g, bool more, bool last, bool ends) {            // ends: the group's last of the segment
+        await_warp(&m.p_full[g], ps >> g & 1, m);
+        ps ^= 1u << g;
+        if (SPLIT || g == 0) await_warp(&m.vf_full[step & 1], step >> 1 & 1, m);
         tc::fence_after_sync();
-        if (lane == 0) {
-          const uint32_t vb = base + L::kVf + (st & 1) * L::kF;
+        if (elect()) {
+          const uint64_t vb = v_desc + (uint32_t)((step & 1) * (L::kF >> 4));
 #pragma unroll
           for (int i = 0; i < kStep / 16; ++i)
-            tc::mma_f16_ts(tb + 256 + g * 128, tb + g * 128 + i * 8, tc::smem_desc_sw128(vb + i * 2048, 16384, 1024), id_o,
-                           more || i > 0);
+            tc::mma_f16_ts(tb + 256 + g * 128, tb + g * 128 + i * 8, vb + i * (2048 / 16), id_o, more || i > 0);
+          if (last) tc::mma_commit(&m.vf_empty[step & 1]);
+          if (ends) tc::mma_commit(&m.o_full[g]);
         }
         __syncwarp();
-      };
-      auto commit = [&](uint64_t* bar) {
-        if (lane == 0) tc::mma_commit(bar);
-        __syncwarp();
-      };
-      auto keys = [&](int st) {
-        await(&m.k_full[st % kRing], st / kRing & 1, m);
-        tc::fence_after_sync();
       };
       for (; w.on(); w.next(p)) {
         const int n = w.take;
-        await(&m.q_full, w.n & 1, m);
-        tc::fence_after_sync();
+        await_warp(&m.q_full, w.n & 1, m);
         if constexpr (SPLIT) {
           for (int j = 0; j < 2 && j < n; ++j) {
-            keys(step + j);
-            scores(j, step + j);
-            commit(&m.k_empty[(step + j) % kRing]);
+            keys();
+            scores(j, true);
           }
-          for (int j = 0; j < n; ++j) {
-            values(j & 1, step + j, j > 1);
-            commit(&m.vf_empty[(step + j) & 1]);
+          for (int j = 0; j < n; ++j, ++step) {
+            values(j & 1, j > 1, true, j + 2 >= n);
             if (j + 2 < n) {
-              keys(step + j + 2);
-              scores(j & 1, step + j + 2);
-              commit(&m.k_empty[(step + j + 2) % kRing]);
-            } else {
-              commit(&m.o_full[j & 1]);
+              keys();
+              scores(j & 1, true);
             }
           }
         } else {
-          keys(step);
-          scores(0, step);
-          scores(1, step);
-          commit(&m.k_empty[step % kRing]);
-          for (int j = 0; j < n; ++j) {
-            const int st = step + j;
-            values(0, st, j > 0);
-            if (j + 1 < n) {
-              keys(st + 1);
-              scores(0, st + 1);
-            } else {
-              commit(&m.o_full[0]);
+          keys();
+          scores(0, false);
+          scores(1, true);
+          for (int j = 0; j < n; ++j, ++step) {
+            const bool on = j + 1 < n;
+            values(0, j > 0, false, !on);
+            if (on) {
+              keys();
+              scores(0, false);
             }
-            values(1, st, j > 0);
-            commit(&m.vf_empty[st & 1]);
-            if (j + 1 < n) {
-              scores(1, st + 1);
-              commit(&m.k_empty[(st + 1) % kRing]);
-            } else {
-              commit(&m.o_full[1]);
-            }
+            values(1, j > 0, true, !on);
+            if (on) scores(1, true);
           }
         }
-        step += n;
       }
       if (*(volatile int*)&m.dead) {                         // nor a product
-        commit(&m.done);
-        tc::mbar_wait(&m.done, 0, kWaitPolls);
+        if (elect()) tc::mma_commit(&m.done);
+        tc::mbar_wait(&m.done, 0, kTilePolls);
       }
     } else if (warp < kLoad) {
       // ---- values: E4M3 to fp16, a token a thread, into the product's layout (atoms of 64 channels x 128 tokens)
@@ -454,7 +461,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           const int token = (t.step + w.x + j) * kStep + r, b = step % kRing;
           const bool border = token < t.lo_max || token >= t.hi_min;         // not every row sees it
           const uint32_t raw = base + L::kV + b * L::kRaw + r * D, dst = base + L::kVf + (step & 1) * L::kF + r * 128;
-          await(&m.v_full[b], step / kRing & 1, m);
+          await_warp(&m.v_full[b], step / kRing & 1, m);
           uint4 x[D / 16];
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -481,7 +488,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           }
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&m.v_empty[b]);
-          await(&m.vf_empty[step & 1], (step >> 1 & 1) ^ 1, m);
+          await_warp(&m.vf_empty[step & 1], (step >> 1 & 1) ^ 1, m);
           const __half2 f2 = __half2half2(__float2half_rn(f));
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -586,7 +593,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       float top = -INFINITY, l = 0.f;
       bool any = false;                  // a step of this segment has been added to O
       for (int j = SPLIT ? grp : 0; j < w.take; j += SPLIT ? 2 : 1) {
-        await(&m.s_full[grp], seen++ & 1, m);
+        await_warp(&m.s_full[grp], seen++ & 1, m);
         tc::fence_after_sync();
         const float2 ks = m.ks[(step + j) % kInfo];
         const int token0 = (t.step + w.x + j) * kStep;
@@ -665,8 +672,8 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       if (SPLIT && grp == 1) m.ml[r] = make_float2(top, l);
       if (SPLIT) named_sync(1, 256);
       if (!SPLIT || grp == 0) {
-        await(&m.o_full[grp], outs++ & 1, m);
-        if (two) await(&m.o_full[1], outs1++ & 1, m);
+        await_warp(&m.o_full[grp], outs++ & 1, m);
+        if (two) await_warp(&m.o_full[1], outs1++ & 1, m);
         tc::fence_after_sync();
         float a0 = 1.f, a1 = 0.f;
         if (two) {
