@@ -14,7 +14,7 @@ CSA2_DEFINE_ERROR_WORD(g_err_kv8_tile);
 namespace {
 
 // Warps 0-3 and 4-7: the softmax of row tile (or step parity, see SPLIT) 0 and 1, a row a thread; 8-11: values to fp16;
-// 12: TMA; 13: products.  The softmax keeps a row of scores in registers, which the other half gives up.
+// 12: TMA; 13 and 14: the products of group 0 and 1.  The softmax keeps a row of scores in registers, which the other half gives up.
 constexpr int kStep = 128, kThreads = 512, kConvert = 8, kLoad = 12, kMma = 13;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each: 65,536, what 512 threads of 128 are launched with
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
@@ -246,19 +246,19 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   if (tid == 0) {
     for (int i = 0; i < kRing; ++i) {
       tc::mbar_init(&m.k_full[i], 1);
-      tc::mbar_init(&m.k_empty[i], 1);
+      tc::mbar_init(&m.k_empty[i], SPLIT ? 1 : 2);
       tc::mbar_init(&m.v_full[i], 1);
       tc::mbar_init(&m.v_empty[i], 4);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&m.vf_full[i], 4);
-      tc::mbar_init(&m.vf_empty[i], 1);
+      tc::mbar_init(&m.vf_empty[i], SPLIT ? 1 : 2);
       tc::mbar_init(&m.s_full[i], 1);
       tc::mbar_init(&m.p_full[i], 4);
       tc::mbar_init(&m.o_full[i], 1);
     }
     tc::mbar_init(&m.q_full, SPLIT ? 4 : 8);
-    tc::mbar_init(&m.done, 1);
+    tc::mbar_init(&m.done, 2);
     m.dead = 0;
   }
   pdl_wait();
@@ -357,77 +357,56 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             tc::mbar_wait(&m.k_full[i], st / kRing & 1, kTilePolls / 64);
             tc::mbar_wait(&m.v_full[i], st / kRing & 1, kTilePolls / 64);
           }
-    } else if (warp == kMma) {
-      // ---- products.  Of each group: S of its next step as soon as its weights have been taken from the last one.
+    } else if (warp == kMma || warp == kMma + 1) {
+      // ---- products, a warp a group: the weights' product with the values and, right after it, the scores of the group's
+      // next step.  A product's issue lasts about as long as the product, so what a warp waits for is hidden behind
+      // the other's.
       constexpr uint32_t id_s = tc::idesc_f16(128, kStep, 0, 0, 0), id_o = tc::idesc_f16(128, D, 0, 0, 1);   // E4M3 is type 0, as fp16
-      const uint64_t q_desc = desc8<D>(base), k_desc = desc8<D>(base + L::kK), v_desc = tc::smem_desc_sw128(base + L::kVf, 16384, 1024);
-      int ring = 0, turn = 0;            // of the next step whose scores are taken
-      int step = 0;                      // of the next step whose values are taken
-      uint32_t ps = 0;                   // parities of the weights
-      auto keys = [&] {
-        await_warp(&m.k_full[ring], turn, m);
-        tc::fence_after_sync();
-      };
-      auto scores = [&](int g, bool last) {                  // last: of the step's
-        if (elect()) {
-          const uint64_t qa = q_desc + (SPLIT ? 0 : g * (L::kQ >> 4)), kb = k_desc + (uint32_t)(ring * (L::kRaw >> 4));
+      constexpr int kBy = SPLIT ? 2 : 1;
+      const int grp = warp - kMma;
+      const uint64_t q_desc = desc8<D>(base + (SPLIT ? 0 : grp * L::kQ)), k_desc = desc8<D>(base + L::kK);
+      const uint64_t v_desc = tc::smem_desc_sw128(base + L::kVf, 16384, 1024);
+      const uint32_t s_at = tb + grp * 128, o_at = tb + 256 + grp * 128;
+      int step = 0;                      // of the segment's first
+      uint32_t ps = 0;                   // parity of the weights
+      auto keys = [&](int st) { await_warp(&m.k_full[st % kRing], st / kRing & 1, m); };
+      auto scores = [&](int st) {
+        const uint64_t kb = k_desc + (uint32_t)(st % kRing * (L::kRaw >> 4));
 #pragma unroll
-          for (int i = 0; i < D / 16; ++i)                   // Q's first part, then its second
-            mma_f8_ss(tb + g * 128, qa + (i / (D / 32) * (128 * D) + i % (D / 32) * 32) / 16, kb + i % (D / 32) * 2, id_s, i > 0);
-          tc::mma_commit(&m.s_full[g]);
-          if (last) tc::mma_commit(&m.k_empty[ring]);
-        }
-        __syncwarp();
-        if (last && ++ring == kRing) {
-          ring = 0;
-          turn ^= 1;
-        }
-      };
-      auto values = [&](int g, bool more, bool last, bool ends) {            // ends: the group's last of the segment
-        await_warp(&m.p_full[g], ps >> g & 1, m);
-        ps ^= 1u << g;
-        if (SPLIT || g == 0) await_warp(&m.vf_full[step & 1], step >> 1 & 1, m);
-        tc::fence_after_sync();
-        if (elect()) {
-          const uint64_t vb = v_desc + (uint32_t)((step & 1) * (L::kF >> 4));
-#pragma unroll
-          for (int i = 0; i < kStep / 16; ++i)
-            tc::mma_f16_ts(tb + 256 + g * 128, tb + g * 128 + i * 8, vb + i * (2048 / 16), id_o, more || i > 0);
-          if (last) tc::mma_commit(&m.vf_empty[step & 1]);
-          if (ends) tc::mma_commit(&m.o_full[g]);
-        }
-        __syncwarp();
+        for (int i = 0; i < D / 16; ++i)                     // Q's first part, then its second
+          mma_f8_ss(s_at, q_desc + (i / (D / 32) * (128 * D) + i % (D / 32) * 32) / 16, kb + i % (D / 32) * 2, id_s, i > 0);
+        tc::mma_commit(&m.s_full[grp]);
+        tc::mma_commit(&m.k_empty[st % kRing]);
       };
       for (; w.on(); w.next(p)) {
         const int n = w.take;
         await_warp(&m.q_full, w.n & 1, m);
-        if constexpr (SPLIT) {
-          for (int j = 0; j < 2 && j < n; ++j) {
-            keys();
-            scores(j, true);
-          }
-          for (int j = 0; j < n; ++j, ++step) {
-            values(j & 1, j > 1, true, j + 2 >= n);
-            if (j + 2 < n) {
-              keys();
-              scores(j & 1, true);
-            }
-          }
-        } else {
-          keys();
-          scores(0, false);
-          scores(1, true);
-          for (int j = 0; j < n; ++j, ++step) {
-            const bool on = j + 1 < n;
-            values(0, j > 0, false, !on);
-            if (on) {
-              keys();
-              scores(0, false);
-            }
-            values(1, j > 0, true, !on);
-            if (on) scores(1, true);
-          }
+        if (grp < n || !SPLIT) {
+          keys(step + (SPLIT ? grp : 0));
+          tc::fence_after_sync();
+          if (elect()) scores(step + (SPLIT ? grp : 0));
+          __syncwarp();
         }
+        for (int j = SPLIT ? grp : 0; j < n; j += kBy) {
+          const int st = step + j;
+          const bool on = j + kBy < n;
+          if (on) keys(st + kBy);
+          await_warp(&m.vf_full[st & 1], st >> 1 & 1, m);
+          await_warp(&m.p_full[grp], ps, m);
+          ps ^= 1;
+          tc::fence_after_sync();
+          if (elect()) {
+            const uint64_t vb = v_desc + (uint32_t)((st & 1) * (L::kF >> 4));
+#pragma unroll
+            for (int i = 0; i < kStep / 16; ++i)
+              tc::mma_f16_ts(o_at, s_at + i * 8, vb + i * (2048 / 16), id_o, j >= kBy || i > 0);
+            tc::mma_commit(&m.vf_empty[st & 1]);
+            if (on) scores(st + kBy);
+            else tc::mma_commit(&m.o_full[grp]);
+          }
+          __syncwarp();
+        }
+        step += n;
       }
       if (*(volatile int*)&m.dead) {                         // nor a product
         if (elect()) tc::mma_commit(&m.done);
