@@ -13,14 +13,16 @@ CSA2_DEFINE_ERROR_WORD(g_err_kv8_tile);
 
 namespace {
 
-// Warps 0-3 and 4-7: the softmax of row tile (or step parity, see SPLIT) 0 and 1, a row a thread; 8-11: values to fp16;
-// 12: TMA; 13 and 14: the products of group 0 and 1.  The softmax keeps a row of scores in registers, which the other half gives up.
-constexpr int kStep = 128, kThreads = 512, kConvert = 8, kLoad = 12, kMma = 13;
+// Warps 0: TMA; 1 and 2: the products of group 0 and 1; 4-7 and 8-11: the softmax of group 0 and 1 (a row tile, or the
+// even and odd steps, see SPLIT), a row a thread; 12-15: values to fp16.  The warps that must not be late come first: a
+// scheduler prefers its older warps.  The softmax keeps a row of scores in registers, which the others give up.
+constexpr int kStep = 128, kThreads = 512, kLoad = 0, kMma = 1, kSoftmax = 4, kConvert = 12;
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each: 65,536, what 512 threads of 128 are launched with
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
 constexpr uint32_t kTilePolls = 1u << 18;
-constexpr int kOver = 4;                 // what beginning a stream costs, in steps
+constexpr int kOver = 8;                 // what beginning a stream costs, in steps
+constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
 template <int D>
 struct Smem {
@@ -28,9 +30,18 @@ struct Smem {
   static constexpr int kK = 2 * kQ, kV = kK + kRing * kRaw, kVf = kV + kRing * kRaw, kBytes = kVf + 2 * kF;
 };
 
+// A stream of a slot: one tile of rows of a sequence, against the steps [step, step + count).
+struct Slot {
+  Rows rows;
+  int s, r0, n;                          // sequence, first row of the tile, rows; n = 0: an empty slot
+  int lo, hi;                            // what any row sees
+  int lo_max, hi_min;                    // what all rows see
+  int step, count;
+};
+
 struct Shared {
   uint64_t k_full[kRing], k_empty[kRing], v_full[kRing], v_empty[kRing], vf_full[2], vf_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], q_full, done;
+  uint64_t s_full[2], p_full[2], o_full[2], turn[2], q_full, done;
   float2 ks[kInfo], vs[kInfo];           // scales of a step's two pages; -1: not there
   float2 ml[128];                        // SPLIT: the second group's maximum and sum
   float unit[4];                         // of the last segments: the largest value scale
@@ -39,6 +50,7 @@ struct Shared {
   long long scan[kThreads / 32];
   long long total, begin;                // of the plan: all streams' cost, that before `slot`
   int slot, dead;
+  Slot first;                            // slot `slot`
   uint32_t tmem;
 };
 
@@ -56,6 +68,12 @@ __device__ __forceinline__ void mma_f8_ss(uint32_t d_tmem, uint64_t a_desc, uint
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
       :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate) : "memory");
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -85,6 +103,10 @@ __device__ __forceinline__ bool elect() {
   uint32_t p;
   asm volatile("{\n .reg .pred P;\n elect.sync _|P, 0xffffffff;\n selp.u32 %0, 1, 0, P;\n}" : "=r"(p));
   return p != 0;
+}
+
+__device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
+  asm volatile("st.shared.v2.u32 [%0], {%1,%2};" :: "r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -128,32 +150,26 @@ __device__ __forceinline__ void tmem_arrived(float* v) {
 
 // ---- the work --------------------------------------------------------------------------------
 
-// A stream of a slot: one tile of rows of a sequence, against the steps [step, step + count).
-struct Slot {
-  Rows rows;
-  int s, r0, n;                          // sequence, first row of the tile, rows; n = 0: an empty slot
-  int lo, hi;                            // what any row sees
-  int lo_max, hi_min;                    // what all rows see
-  int step, count;
-};
-
 // Slot floor(start * G / RT) + s and the ones after it hold the row tiles of sequence s.
 template <int RT>
-__device__ __forceinline__ Slot slot_of(const Kv8Params& p, int slot) {
+__device__ __forceinline__ long long first_slot(const Kv8Params& p, const int* start, int s) {
+  const int x = start[s];
+  return (long long)(x < 0 ? 0 : x > p.a.T ? p.a.T : x) * p.G / RT + s;
+}
+
+// Slot `slot`, of a sequence from s on; start and length: the step's, or a copy.
+template <int RT>
+__device__ __forceinline__ Slot slot_of(const Kv8Params& p, const int* start, const int* length, int s, int slot) {
   const csa2_kv8_attn_args& a = p.a;
-  auto first = [&](int s) {
-    const int x = a.start[s];
-    return (long long)(x < 0 ? 0 : x > a.T ? a.T : x) * p.G / RT + s;
-  };
   Slot t = {};
-  int s = 0, end = a.S;
-  while (end - s > 1) {
-    const int mid = (s + end) >> 1;
-    if (first(mid) <= slot) s = mid; else end = mid;
-  }
+  while (s + 1 < a.S && first_slot<RT>(p, start, s + 1) <= slot) ++s;
   t.s = s;
-  t.rows = rows_of(a, s, p.G);
-  const long long r0 = (slot - first(s)) * RT;
+  t.rows.t0 = start[s];
+  t.rows.end = start[s + 1];
+  t.rows.length = length[s];
+  const int e = min(t.rows.end, a.T);
+  t.rows.n = t.rows.t0 >= 0 && e > t.rows.t0 ? (e - t.rows.t0) * p.G : 0;
+  const long long r0 = (slot - first_slot<RT>(p, start, s)) * RT;
   if (r0 < 0 || r0 >= t.rows.n) return t;
   t.r0 = (int)r0;
   t.n = min(RT, t.rows.n - t.r0);
@@ -199,7 +215,7 @@ struct Walk {
     n = 0;
     if (left <= 0) return;
     slot = m.slot;
-    t = slot_of<RT>(p, slot);
+    t = m.first;
     const long long rel = begin - m.begin;
     h = (int)(rel / cost_of(t));
     cut((int)(rel % cost_of(t)));
@@ -216,7 +232,7 @@ struct Walk {
       if (left <= 0) return;
       if (++h == p.a.cache.Hkv) {
         h = 0;
-        do t = slot_of<RT>(p, ++slot); while (t.count == 0);
+        do t = slot_of<RT>(p, p.a.start, p.a.length, t.s, ++slot); while (t.count == 0);
       }
       cut(0);
     } while (take == 0);
@@ -256,6 +272,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       tc::mbar_init(&m.s_full[i], 1);
       tc::mbar_init(&m.p_full[i], 4);
       tc::mbar_init(&m.o_full[i], 1);
+      tc::mbar_init(&m.turn[i], 1);
     }
     tc::mbar_init(&m.q_full, SPLIT ? 4 : 8);
     tc::mbar_init(&m.done, 2);
@@ -268,8 +285,28 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   const int slots = (int)((long long)a.T * G / RT) + a.S;
   const int chunk = (slots + kThreads - 1) / kThreads;
   const int c0 = min(slots, tid * chunk), c1 = min(slots, c0 + chunk);
+  const int *start = a.start, *length = a.length;
+  if (a.S <= kCopy) {                    // into the ring, which is empty yet
+    int* copy = reinterpret_cast<int*>(smem + L::kK);
+    for (int i = tid; i <= a.S; i += kThreads) {
+      copy[i] = a.start[i];
+      if (i < a.S) copy[kCopy + 1 + i] = a.length[i];
+    }
+    start = copy;
+    length = copy + kCopy + 1;
+  }
+  __syncthreads();
+  int s0 = 0;                            // the sequence of slot c0
+  for (int end = a.S; end - s0 > 1;) {
+    const int mid = (s0 + end) >> 1;
+    if (first_slot<RT>(p, start, mid) <= c0) s0 = mid; else end = mid;
+  }
   long long mine = 0;
-  for (int i = c0; i < c1; ++i) mine += cost_of(slot_of<RT>(p, i));
+  for (int i = c0, s = s0; i < c1; ++i) {
+    const Slot t = slot_of<RT>(p, start, length, s, i);
+    s = t.s;
+    mine += cost_of(t);
+  }
   mine *= c.Hkv;
   long long inc = mine;
 #pragma unroll
@@ -278,7 +315,6 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     if (lane >= o) inc += u;
   }
   if (lane == 31) m.scan[warp] = inc;
-  tc::fence_proxy_async_smem();          // the initialised barriers, for the copies
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -292,19 +328,21 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   if (tid == 0) m.total = total;
   if (begin < total && inc > begin && inc - mine <= begin) {
     long long at = inc - mine;
+    Slot t = slot_of<RT>(p, start, length, s0, c0);
     int i = c0;
-    for (; i < c1 - 1; ++i) {
-      const long long n = (long long)cost_of(slot_of<RT>(p, i)) * c.Hkv;
-      if (at + n > begin) break;
-      at += n;
+    while (i < c1 - 1 && at + (long long)cost_of(t) * c.Hkv <= begin) {
+      at += (long long)cost_of(t) * c.Hkv;
+      t = slot_of<RT>(p, start, length, t.s, ++i);
     }
     m.slot = i;
     m.begin = at;
+    m.first = t;
   }
+  tc::fence_proxy_async_smem();          // the initialised barriers and the copy's end, for the copies to come
   __syncthreads();
   const uint32_t tb = m.tmem;
 
-  if (warp >= kConvert) {
+  if (warp < kSoftmax || warp >= kConvert) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
     Walk<RT> w(p, m, per);
     if (warp == kLoad) {
@@ -360,7 +398,8 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     } else if (warp == kMma || warp == kMma + 1) {
       // ---- products, a warp a group: the weights' product with the values and, right after it, the scores of the group's
       // next step.  A product's issue lasts about as long as the product, so what a warp waits for is hidden behind
-      // the other's.
+      // the other's.  The groups take turns: left alone they fall into step, both softmaxes and then both products
+      // (4096 new tokens at 32K: 4.5 ms).
       constexpr uint32_t id_s = tc::idesc_f16(128, kStep, 0, 0, 0), id_o = tc::idesc_f16(128, D, 0, 0, 1);   // E4M3 is type 0, as fp16
       constexpr int kBy = SPLIT ? 2 : 1;
       const int grp = warp - kMma;
@@ -368,7 +407,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       const uint64_t v_desc = tc::smem_desc_sw128(base + L::kVf, 16384, 1024);
       const uint32_t s_at = tb + grp * 128, o_at = tb + 256 + grp * 128;
       int step = 0;                      // of the segment's first
-      uint32_t ps = 0;                   // parity of the weights
+      uint32_t ps = 0, turns = 0;        // parity of the weights, turns had
       auto keys = [&](int st) { await_warp(&m.k_full[st % kRing], st / kRing & 1, m); };
       auto scores = [&](int st) {
         const uint64_t kb = k_desc + (uint32_t)(st % kRing * (L::kRaw >> 4));
@@ -392,6 +431,8 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           const bool on = j + kBy < n;
           if (on) keys(st + kBy);
           await_warp(&m.vf_full[st & 1], st >> 1 & 1, m);
+          await_warp(&m.turn[grp], (turns & 1) ^ (grp ? 0 : 1), m);
+          ++turns;
           await_warp(&m.p_full[grp], ps, m);
           ps ^= 1;
           tc::fence_after_sync();
@@ -403,7 +444,13 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             tc::mma_commit(&m.vf_empty[st & 1]);
             if (on) scores(st + kBy);
             else tc::mma_commit(&m.o_full[grp]);
+            tc::mbar_arrive(&m.turn[grp ^ 1]);
           }
+          __syncwarp();
+        }
+        if (SPLIT && grp && (n & 1)) {   // the first group had a step more
+          await_warp(&m.turn[1], turns++ & 1, m);
+          if (elect()) tc::mbar_arrive(&m.turn[0]);
           __syncwarp();
         }
         step += n;
@@ -412,7 +459,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         if (elect()) tc::mma_commit(&m.done);
         tc::mbar_wait(&m.done, 0, kTilePolls);
       }
-    } else if (warp < kLoad) {
+    } else if (warp >= kConvert) {
       // ---- values: E4M3 to fp16, a token a thread, into the product's layout (atoms of 64 channels x 128 tokens)
       const int r = tid - kConvert * 32;
       int step = 0;
@@ -497,7 +544,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
     // ---- softmax: a row a thread
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     Walk<RT> w(p, m, per);
-    const int grp = warp >> 2, r = tid & 127;
+    const int grp = (warp - kSoftmax) >> 2, r = tid & 127;
     const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21), s_at = lanes + grp * 128, o_at = lanes + 256 + grp * 128;
     int step = 0, seen = 0, outs = 0, outs1 = 0;   // steps of earlier segments; scores, outputs waited for
     Part part = {0, 0, 0, 0, 0};
@@ -508,61 +555,70 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       int lo = 0, hi = INT_MAX;
       const int tok = real ? t.rows.t0 + (t.r0 + row) / G : 0, hq = real ? w.h * G + (t.r0 + row) % G : 0;
       if (real) seen_by(a, t.rows, tok, lo, hi, &g_err_kv8_tile);
-      // the row of Q: scaled by a power of two to below 2^8, as the sum of two E4M3 rows
-      float mul;
+      // the warp's rows of Q, two at a time: scaled by a power of two to below 2^8, as the sums of two E4M3 rows
+      float mul = 0.f;
       {
-        float top = 0.f, f, undo;
-        const uint16_t* q = a.q + tok * a.q_stride_t + (long long)hq * a.q_stride_h;
-        uint32_t v[D / 2];
-        if (!real) {
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // lanes a row, rows at a time
+        const int sub = lane % kLanes;
+        const long long mine = real ? tok * a.q_stride_t + (long long)hq * a.q_stride_h : -1;
+        uint4 v[32 / kRows];
 #pragma unroll
-          for (int i = 0; i < D / 2; ++i) v[i] = 0;
-        } else if (p.aligned & 1) {
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 x = reinterpret_cast<const uint4*>(q)[i];
-            v[4 * i] = x.x; v[4 * i + 1] = x.y; v[4 * i + 2] = x.z; v[4 * i + 3] = x.w;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < D / 2; ++i) v[i] = q[2 * i] | (uint32_t)q[2 * i + 1] << 16;
-        }
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) {
-          const float x0 = fabsf(__uint_as_float(v[i] << 16)), x1 = fabsf(__uint_as_float(v[i] & 0xffff0000u));
-          top = x0 >= top ? x0 : x0 != x0 ? INFINITY : top;
-          top = x1 >= top ? x1 : x1 != x1 ? INFINITY : top;
-        }
-        row_factor(top, f, undo);
-        f *= 0.0078125f;
-        mul = undo * 128.f * (a.softmax_scale * kLog2e);
-        const uint32_t bad = top == INFINITY ? 0x7f7f7f7fu : 0u;               // an infinity makes its row NaN, as a NaN does
-        if (!SPLIT || grp == 0) {
-          const uint32_t dst = base + (SPLIT ? 0 : grp * L::kQ) + r * D;
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) {
-            uint32_t hi8[4], lo8[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              hi8[e] = lo8[e] = bad;
-              if (!bad) {
-                hi8[e] = 0;
-                lo8[e] = 0;
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                  const uint32_t u = v[8 * i + 2 * e + d];
-                  const float x0 = __uint_as_float(u << 16) * f, x1 = __uint_as_float(u & 0xffff0000u) * f;
-                  const uint32_t first = cvt_e4m3x2(x0, x1), back = e4m3x2_to_f16x2((uint16_t)first);
-                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                  hi8[e] |= first << 16 * d;
-                  lo8[e] |= cvt_e4m3x2(x0 - y.x, x1 - y.y) << 16 * d;
-                }
-              }
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const long long at = __shfl_sync(0xffffffffu, mine, i * kRows + lane / kLanes);
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (at >= 0) {
+            const uint16_t* q = a.q + at + sub * 8;
+            if (p.aligned & 1) {
+              v[i] = *reinterpret_cast<const uint4*>(q);
+            } else {
+              v[i].x = q[0] | (uint32_t)q[1] << 16;
+              v[i].y = q[2] | (uint32_t)q[3] << 16;
+              v[i].z = q[4] | (uint32_t)q[5] << 16;
+              v[i].w = q[6] | (uint32_t)q[7] << 16;
             }
-            const uint32_t at = dst + ((D == 128 ? i ^ (r & 7) : i ^ (r >> 1 & 3)) << 4);
-            sts128(at, make_uint4(hi8[0], hi8[1], hi8[2], hi8[3]));
-            sts128(at + 128 * D, make_uint4(lo8[0], lo8[1], lo8[2], lo8[3]));
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 32 / kRows; ++i) {
+          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          float x[8], top = 0.f, f, undo;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[2 * e] = __uint_as_float(u[e] << 16);
+            x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+          }
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fabsf(x[e]) >= top ? fabsf(x[e]) : x[e] != x[e] ? INFINITY : top;
+#pragma unroll
+          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          row_factor(top, f, undo);
+          f *= 0.0078125f;
+          const float back = __shfl_sync(0xffffffffu, undo * 128.f * (a.softmax_scale * kLog2e), lane % kRows * kLanes);
+          if (lane / kRows == i) mul = back;
+          if (!SPLIT || grp == 0) {
+            const bool bad = top == INFINITY;                // an infinity makes its row NaN, as a NaN does
+            uint2 hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), lo8 = hi8;
+            if (!bad) {
+              uint32_t h4[4], l4[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float x0 = x[2 * e] * f, x1 = x[2 * e + 1] * f;
+                h4[e] = cvt_e4m3x2(x0, x1);
+                const uint32_t first = e4m3x2_to_f16x2((uint16_t)h4[e]);
+                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&first));
+                l4[e] = cvt_e4m3x2(x0 - y.x, x1 - y.y);
+              }
+              hi8 = make_uint2(h4[0] | h4[1] << 16, h4[2] | h4[3] << 16);
+              lo8 = make_uint2(l4[0] | l4[1] << 16, l4[2] | l4[3] << 16);
+            }
+            const int qr = (warp & 3) * 32 + i * kRows + lane / kLanes, ch = sub >> 1;
+            const uint32_t at = base + (SPLIT ? 0 : grp * L::kQ) + qr * D +
+                                ((D == 128 ? ch ^ (qr & 7) : ch ^ (qr >> 1 & 3)) << 4) + (sub & 1) * 8;
+            sts64(at, hi8);
+            sts64(at + 128 * D, lo8);
+          }
+        }
+        if (!SPLIT || grp == 0) {
           tc::fence_proxy_async_smem();
           tc::fence_before_sync();       // the last segment's TMEM reads
           __syncwarp();
@@ -594,14 +650,14 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             x[e] = in ? x[e] : -INFINITY;
           }
         }
-        float mx[8];
+        float mx[4] = {x[0], x[32], x[64], x[96]};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mx[i] = x[16 * i];
+        for (int i = 0; i < 4; ++i) {
+          mx[i] = fmaxf(mx[i], x[32 * i + 1]);
 #pragma unroll
-          for (int e = 1; e < 16; ++e) mx[i] = fmaxf(mx[i], x[16 * i + e]);
+          for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], x[32 * i + e], x[32 * i + e + 1]);
         }
-        const float now = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * f0, fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7])) * f1);
+        const float now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
         // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
         // sum are rescaled a few times a row.
         const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
@@ -744,7 +800,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         part = Part{t.n, t.rows.t0, t.r0, w.h, (int)blockIdx.x + (int)((t.count - w.take + per - 1) / per)};
       step += w.take;
     }
-    if (tid == 0) p.part[blockIdx.x] = part;
+    if (tid == kSoftmax * 32) p.part[blockIdx.x] = part;
   }
   tc::fence_before_sync();
   __syncthreads();
