@@ -640,43 +640,63 @@ class Kv8Cache:
 
     def fields(self, dev):
         """The C struct's values, after its checks; dev: the CUDA device number that all planes must be on."""
-        pages, heads, slots, D = self.k.shape
-        if slots != PAGE or self.v.shape != self.k.shape:
+        k, v, ks, vs, table, m, ms = self.k, self.v, self.k_scale, self.v_scale, self.page_table, self.mean, self.mean_scale
+        shape = k.shape
+        pages, heads, slots, D = shape
+        per = (pages, heads)
+        if slots != PAGE or v.shape != shape:
             raise ValueError(f"k and v must be [pages, heads, {PAGE}, D] alike")
-        if self.k_scale.shape != (pages, heads) or self.v_scale.shape != (pages, heads):
+        if ks.shape != per or vs.shape != per:
             raise ValueError(f"k_scale and v_scale must be [{pages}, {heads}]")
-        m, ms = self.mean, self.mean_scale
         if (m is None) != (ms is None):
             raise ValueError("mean and mean_scale go together")
-        if m is not None and (m.shape != (pages, heads, D) or ms.shape != (pages, heads)):
+        if m is not None and (m.shape != (pages, heads, D) or ms.shape != per):
             raise ValueError(f"mean must be [{pages}, {heads}, {D}] and mean_scale [{pages}, {heads}]")
-        seqs, most = self.page_table.shape
-        return (_dense(self.k, dev, torch.uint8, "k plane"), _dense(self.v, dev, torch.uint8, "v plane"),
-                _dense(self.k_scale, dev, torch.float32, "k_scale"), _dense(self.v_scale, dev, torch.float32, "v_scale"),
-                _dense(m, dev, torch.int8, "mean"), _dense(ms, dev, torch.float32, "mean_scale"),
-                _dense(self.page_table, dev, torch.int32, "page_table"), pages, PAGE, seqs, most, heads, D)
+        at = []
+        for t, dtype, name in zip((k, v, ks, vs, m, ms, table), _KV8_TYPES, _KV8_NAMES):
+            if t is None:
+                at.append(0)
+                continue
+            if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+                _dense(t, dev, dtype, name)              # says which
+            at.append(t.data_ptr())
+        seqs, most = table.shape
+        return (*at, pages, PAGE, seqs, most, heads, D)
+
+
+_KV8_TYPES = (torch.uint8, torch.uint8, torch.float32, torch.float32, torch.int8, torch.float32, torch.int32)
+_KV8_NAMES = ("k plane", "v plane", "k_scale", "v_scale", "mean", "mean_scale", "page_table")
+_ws_of = {}                                # the default workspaces by device number
 
 
 def _launch_ws(fn, packed, ws, device, dev):
-    """_launch of a call that takes a workspace."""
+    """_launch of a call that takes a workspace.  It is offered the one there is, and asked what it needs only if that is
+    too small."""
     if dev < 0:
         raise ValueError("expected CUDA tensors")
     if not _is_current(dev):
         with torch.cuda.device(dev):
             return _launch_ws(fn, packed, ws, device, dev)
     L = _lib.lib()
-    need = ctypes.c_size_t(0)
-    status = getattr(L, fn + "_workspace")(packed, ctypes.byref(need))
+    if ws is None:
+        ws = _ws_of.get(dev)
+        if ws is None:
+            ws = _ws_of[dev] = _ws(None, device)
+    buf = ws.get(0)
+    if buf.get_device() != dev:
+        _on_device(buf, dev, "ws")
+    call = getattr(L, fn)
+    status = call(packed, buf.data_ptr(), buf.numel(), _stream(dev))
+    if status == _TOO_SMALL:
+        need = ctypes.c_size_t(0)
+        _lib.check(getattr(L, fn + "_workspace")(packed, ctypes.byref(need)))
+        buf = ws.get(need.value)
+        status = call(packed, buf.data_ptr(), need.value, _stream(dev))
     if status:
         _lib.check(status)
-    buf = 0
-    if need.value:
-        t = _ws(ws, device).get(need.value)
-        _on_device(t, dev, "ws")
-        buf = t.data_ptr()
-    status = getattr(L, fn)(packed, buf, need.value, _stream(dev))
-    if status:
-        _lib.check(status)
+
+
+_TOO_SMALL = 3                             # CSA2_ERR_WORKSPACE_TOO_SMALL
 
 
 def _heads_of(t, dev, name):
@@ -710,8 +730,9 @@ class PagePlan:
 
     @staticmethod
     def allocate(seqs, tokens, device):
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=device)
-        return PagePlan(new(seqs + 1), new(tokens), new(tokens), new(tokens), new(seqs), new(1))
+        rows = torch.empty(3 * tokens + 2 * seqs + 2, dtype=torch.int32, device=device)
+        seq, pos, slot, start, length, head = rows.split((tokens, tokens, tokens, seqs + 1, seqs, 1))
+        return PagePlan(start, seq, pos, slot, length, head)
 
 
 def page_plan(length, add, page_table, free_pages, free_head, tokens, *, out=None):

@@ -20,7 +20,7 @@ constexpr int kStep = 128, kThreads = 512, kLoad = 0, kMma = 1, kSoftmax = 4, kC
 constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each: 65,536, what 512 threads of 128 are launched with
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
-constexpr uint32_t kTilePolls = 1u << 18;
+constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a limit wakes late: 5 % at 4096 new tokens)
 constexpr int kOver = 8;                 // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
@@ -113,15 +113,15 @@ __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
-// A bounded wait of one thread (a poll lasts up to some microseconds).  After one has given up, all others of the CTA do
+// A bounded wait of one thread.  After one has given up, all others of the CTA do
 // at once: every role still goes through its loops, so the kernel ends.
 __device__ __forceinline__ bool await(uint64_t* bar, uint32_t parity, Shared& m) {
   const uint32_t at = smem_u32(bar);
   uint32_t done, polls = 0;
   while (true) {
     asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(done) : "r"(at), "r"(parity) : "memory");
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(done) : "r"(at), "r"(parity), "r"(kPollNs) : "memory");
     if (done) return true;
     if (*(volatile int*)&m.dead) return false;
     if (++polls == kTilePolls) {

@@ -42,7 +42,91 @@ __device__ __forceinline__ long long block_scan(long long v, long long* warp_sum
 
 constexpr int kPlanThreads = 1024;
 
-// One CTA: the two prefix sums (rows, pages) over the sequences, 1024 at a time, and the new entries of the page table.
+// What a sequence holds and gets before rows run out: (held, add), with error bits.
+__device__ __forceinline__ void plan_counts(const csa2_page_plan_args& a, int s, long long& held, long long& add, unsigned int& err) {
+  held = a.length[s];
+  add = a.add[s];
+  if (held < 0 || add < 0) err |= CSA2_DEVERR_N_VIS;
+  held = held < 0 ? 0 : held;
+  add = add < 0 ? 0 : add;
+  const long long room = (long long)a.max_pages * kPage - held;
+  if (add > room) {
+    err |= CSA2_DEVERR_TOKENS;
+    add = room < 0 ? 0 : room;
+  }
+}
+
+// Up to 1024 sequences, a thread a sequence: every CTA has both prefix sums (rows, pages) in shared memory and sees to its
+// share of the rows and of the new pages.  CTA 0 writes the sequences' values; where those are the inputs themselves,
+// it is the only one.
+__global__ void __launch_bounds__(kPlanThreads) k_plan(const csa2_page_plan_args a, int rows) {
+  __shared__ long long sums[33];
+  __shared__ int start[kPlanThreads + 1], now[kPlanThreads], old_pages[kPlanThreads], pages_before[kPlanThreads + 1];
+  pdl_wait();
+  pdl_trigger();
+  const int s = threadIdx.x;
+  const int head = a.free_head[0];
+  unsigned int err = 0;
+  long long held = 0, add = 0, total;
+  if (s < a.S) plan_counts(a, s, held, add, err);
+  const long long end = block_scan(add, sums, &total);
+  if (end > a.tokens && add > 0) err |= CSA2_DEVERR_TOKENS;
+  const int e = (int)(end < a.tokens ? end : a.tokens), b = (int)(end - add < a.tokens ? end - add : a.tokens);
+  const long long len = held + (e - b);
+  const int p0 = (int)((held + kPage - 1) / kPage), p1 = (int)((len + kPage - 1) / kPage);
+  const long long pe = block_scan(p1 - p0, sums, &total);
+  start[s + 1] = e;
+  now[s] = (int)len;
+  old_pages[s] = p0;
+  pages_before[s + 1] = (int)pe;
+  if (s == 0) start[0] = pages_before[0] = 0;
+  __syncthreads();                       // and every input of this CTA has been read
+  if (blockIdx.x == 0) {
+    if (s < a.S) {
+      a.start[s + 1] = e;
+      a.new_length[s] = (int)len;
+    }
+    if (s == 0) {
+      const long long h = head + total;
+      a.start[0] = 0;
+      a.new_head[0] = (int)(h < a.num_free ? h : (a.num_free > head ? a.num_free : head));
+    }
+  }
+  auto taken = [&](long long i) {        // the i-th page of this call, -1 if there is none
+    const long long at = head + i;
+    return at >= 0 && at < a.num_free ? a.free_pages[at] : -1;
+  };
+  auto find = [&](const int* before, int x) {                // before[lo] <= x < before[hi]
+    int lo = 0, hi = a.S;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] <= x) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+  for (long long i = (long long)blockIdx.x * kPlanThreads + s; i < total; i += (long long)gridDim.x * kPlanThreads) {
+    const int q = find(pages_before, (int)i), page = taken(i);
+    if (head + i < 0 || head + i >= a.num_free) err |= CSA2_DEVERR_NO_PAGE;
+    a.page_table[(long long)q * a.max_pages + old_pages[q] + (i - pages_before[q])] = page;
+  }
+  const int t0 = blockIdx.x * rows, t1 = min(a.tokens, t0 + rows), last = start[a.S];
+  for (int t = t0 + s; t < t1; t += kPlanThreads) {
+    int q = -1, pos = -1, slot = -1;
+    if (t < last) {
+      q = find(start, t);
+      pos = now[q] - (start[q + 1] - t);
+      const int j = pos / kPage;
+      const int page = j >= old_pages[q] ? taken(pages_before[q] + (j - old_pages[q])) : a.page_table[(long long)q * a.max_pages + j];
+      if (page >= 0) slot = page * kPage + pos % kPage;
+    }
+    a.seq[t] = q;
+    a.pos[t] = pos;
+    a.slot[t] = slot;
+  }
+  if (err) raise_error(&g_err_paged, err);
+}
+
+// More sequences than that.  One CTA: the two prefix sums (rows, pages) over the sequences, 1024 at a time, and the new entries of the page table.
 __global__ void __launch_bounds__(kPlanThreads) k_plan_scan(const csa2_page_plan_args a) {
   __shared__ long long sums[33];
   __shared__ int first_page[kPlanThreads], pages_before[kPlanThreads + 1];
@@ -56,16 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_scan(const csa2_page_plan
     const int s = s0 + threadIdx.x;
     long long held = 0, add = 0;
     if (s < a.S) {
-      held = a.length[s];
-      add = a.add[s];
-      if (held < 0 || add < 0) err |= CSA2_DEVERR_N_VIS;
-      held = held < 0 ? 0 : held;
-      add = add < 0 ? 0 : add;
-      const long long room = (long long)a.max_pages * kPage - held;
-      if (add > room) {
-        err |= CSA2_DEVERR_TOKENS;
-        add = room < 0 ? 0 : room;
-      }
+      plan_counts(a, s, held, add, err);
     }
     long long total;
     const long long end = rows + block_scan(add, sums, &total);
@@ -106,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan_scan(const csa2_page_plan
   if (err) raise_error(&g_err_paged, err);
 }
 
-// A thread a row.
+// The rows after it, a thread a row.
 __global__ void __launch_bounds__(256) k_plan_rows(const csa2_page_plan_args a) {
   pdl_wait();
   pdl_trigger();
@@ -588,6 +663,11 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_page_plan(const csa2_page_plan_args& a, cudaStream_t st) {
+  if (a.S <= kPlanThreads && a.S > 0) {
+    const bool in_place = a.new_length == a.length || a.new_head == a.free_head;
+    const int most = in_place ? 1 : 152, rows = kPlanThreads * (int)(1 + (long long)(a.tokens - 1) / ((long long)most * kPlanThreads));
+    return launch_k(k_plan, dim3(a.tokens > rows ? (a.tokens + rows - 1) / rows : 1), dim3(kPlanThreads), 0, st, a, rows);
+  }
   cudaError_t e = launch_k(k_plan_scan, dim3(1), dim3(kPlanThreads), 0, st, a);
   if (e != cudaSuccess || a.tokens == 0) return e;
   return launch_k(k_plan_rows, dim3((a.tokens + 255) / 256), dim3(256), 0, st, a);
