@@ -731,7 +731,8 @@ class PagePlan:
     @staticmethod
     def allocate(seqs, tokens, device):
         rows = torch.empty(3 * tokens + 2 * seqs + 2, dtype=torch.int32, device=device)
-        seq, pos, slot, start, length, head = rows.split((tokens, tokens, tokens, seqs + 1, seqs, 1))
+        seq, pos, slot, start, length, head = torch.unsafe_split_with_sizes(
+            rows, (tokens, tokens, tokens, seqs + 1, seqs, 1))       # one allocation: six take twice as long
         return PagePlan(start, seq, pos, slot, length, head)
 
 

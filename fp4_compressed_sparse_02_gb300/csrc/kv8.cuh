@@ -6,15 +6,21 @@
 namespace csa2 {
 
 // The sequence of row t: s with start[s] <= t < start[s+1], or -1 for a row of padding.  Whatever
-// start holds, a result >= 0 is below S and satisfies both inequalities.
+// start holds, a result >= 0 is below S and satisfies both inequalities.  By a whole warp, for one t: 32 starts at a
+// time, so that up to 32 sequences take one round of loads and 1024 two.
 __device__ __forceinline__ int find_seq(const int* __restrict__ start, int S, int t) {
-  if (t < start[0] || t >= start[S]) return -1;
-  int lo = 0, hi = S;                    // start[lo] <= t < start[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (start[mid] <= t) lo = mid; else hi = mid;
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = S;                    // start[lo] <= t < start[hi], once both have been looked at
+  const int last = start[S];
+  while (true) {
+    const int step = (hi - lo + 31) >> 5, i = lo + step * lane;
+    const uint32_t in = __ballot_sync(0xffffffffu, i < hi && start[i] <= t);
+    if (lo == 0 && hi == S && ((in & 1) == 0 || t >= last)) return -1;
+    const int at = 31 - __clz(in);
+    lo += step * at;
+    hi = min(hi, lo + step);
+    if (hi - lo <= 1) return lo;
   }
-  return lo;
 }
 
 // Position of row t of sequence s, or -1 (with an error bit) outside its row of the page table.
@@ -54,6 +60,34 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float a, float b) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
   return r;
+}
+
+// Two float32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mov.b64 z, {%6, %7};\n"
+      " fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n add.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n mul.rn.f32x2 w, x, y;\n"
+      " mov.b64 {%0, %1}, w;\n}"
+      : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// The NaNs among four E4M3 bytes: 1 in the byte of each.
+__device__ __forceinline__ uint32_t e4m3x4_nans(uint32_t w) {
+  return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
 }
 
 }  // namespace csa2

@@ -470,7 +470,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
 #pragma unroll
             for (int w = 0; w < kVw; ++w) {
               vw[kt][e][w] = see ? vw[kt][e][w] : 0u;
-              nan |= (((vw[kt][e][w] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+              nan |= e4m3x4_nans(vw[kt][e][w]) != 0;
             }
           }
         if (__any_sync(0xffffffffu, nan)) {
@@ -481,7 +481,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
             for (int e = 0; e < 4; ++e)
 #pragma unroll
               for (int w = 0; w < kVw; ++w) {
-                const uint32_t v = vw[kt][e][w], at = (((v & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;   // 1 in each NaN's byte
+                const uint32_t v = vw[kt][e][w], at = e4m3x4_nans(v);   // 1 in each NaN's byte
                 keep[kt][e][w] = v & ~(at * 0xffu);
                 vw[kt][e][w] = at * 0x38u;                   // E4M3 of 1
               }

@@ -1,6 +1,7 @@
 // The paged 8-bit cache's tables, append and page selection (csa2_page_plan, csa2_kv8_append,
 // csa2_kv8_select).
 #include <limits.h>
+#include <math.h>
 
 #include "internal.h"
 #include "kv8.cuh"
@@ -187,9 +188,13 @@ __global__ void __launch_bounds__(256) k_plan_rows(const csa2_page_plan_args a) 
   pdl_trigger();
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= a.tokens) return;
-  const int s = find_seq(a.start, a.S, t);
-  int pos = -1, slot = -1;
-  if (s >= 0) {
+  int s = -1, pos = -1, slot = -1;
+  if (t < a.start[a.S]) {
+    s = 0;
+    for (int hi = a.S; hi - s > 1;) {
+      const int mid = (s + hi) >> 1;
+      if (a.start[mid] <= t) s = mid; else hi = mid;
+    }
     pos = a.new_length[s] - (a.start[s + 1] - t);
     const int page = a.page_table[(long long)s * a.max_pages + pos / kPage];
     if (page >= 0) slot = page * kPage + pos % kPage;
@@ -216,46 +221,90 @@ struct AppendParams {
   int range;                             // rows whose pages one CTA sees to
 };
 
+// Eight channels of a row as they come.
 template <typename T>
-__device__ __forceinline__ float to_f32(T x) {
-  if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(x);
-  else return x;
-}
+struct Eight {
+  uint4 w[sizeof(T) / 2];
 
-template <typename T, int D, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float* f) {
-  if constexpr (!VEC) {
+  template <bool VEC>
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = to_f32(p[i]);
-  } else if constexpr (sizeof(T) == 2) {
-    const uint4 w = *reinterpret_cast<const uint4*>(p);
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) w[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else if constexpr (sizeof(T) == 2) {
+      uint32_t v[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = __uint_as_float(v[i] << 16);
-      f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | (uint32_t)p[2 * i + 1] << 16;
+      w[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[i] = make_uint4(__float_as_uint(p[4 * i]), __float_as_uint(p[4 * i + 1]), __float_as_uint(p[4 * i + 2]),
+                          __float_as_uint(p[4 * i + 3]));
     }
-  } else {
-    const float4 w = reinterpret_cast<const float4*>(p)[0], z = reinterpret_cast<const float4*>(p)[1];
-    f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
-    f[4] = z.x; f[5] = z.y; f[6] = z.z; f[7] = z.w;
   }
+  // The larger of `top` and the largest magnitude; NaNs count as nothing.  bf16 two at a time.
+  __device__ __forceinline__ float largest(float top) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+      __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[0]));
+#pragma unroll
+      for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v[i])));
+      return fmaxf(top, fmaxf(__bfloat162float(m.x), __bfloat162float(m.y)));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        top = fmaxf(fmaxf(fmaxf(top, fabsf(__uint_as_float(w[i].x))), fabsf(__uint_as_float(w[i].y))),
+                    fmaxf(fabsf(__uint_as_float(w[i].z)), fabsf(__uint_as_float(w[i].w))));
+      return top;
+    }
+  }
+  __device__ __forceinline__ void values(float* f) const {
+    if constexpr (sizeof(T) == 2) {
+      const uint32_t v[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(v[i] << 16);
+        f[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f[4 * i] = __uint_as_float(w[i].x);
+        f[4 * i + 1] = __uint_as_float(w[i].y);
+        f[4 * i + 2] = __uint_as_float(w[i].z);
+        f[4 * i + 3] = __uint_as_float(w[i].w);
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ void add_bytes(float2* m, uint2 w) {            // a NaN counts as 0
+  const uint32_t nx = e4m3x4_nans(w.x), ny = e4m3x4_nans(w.y);
+  if (nx | ny) {
+    w.x &= ~(nx * 0xffu);
+    w.y &= ~(ny * 0xffu);
+  }
+  const uint32_t h[4] = {e4m3x2_lo_f16x2(w.x), e4m3x2_hi_f16x2(w.x), e4m3x2_lo_f16x2(w.y), e4m3x2_hi_f16x2(w.y)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = add2(m[i], __half22float2(*reinterpret_cast<const __half2*>(&h[i])));
 }
 
-// A CTA a (range of rows, head): the pages whose first new token lies in the range, one after the other.
+// A CTA a (range of rows, head): the pages whose first new token lies in the range, one after the other.  A page's new
+// rows are loaded at once and stay in registers from the largest magnitude to the summary.
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParams p) {
-  constexpr int kHalf = kAppendThreads / 2, kPer = D / 8, kRows = kHalf / kPer;   // threads a row, rows a turn
-  __shared__ float s_max[kAppendThreads / 32], s_sum[kHalf / kPer][D], s_top[4];
+  constexpr int kHalf = kAppendThreads / 2, kPer = D / 8, kRows = kHalf / kPer, kTurns = kPage / kRows;   // threads a row, rows a turn
+  __shared__ float s_max[kAppendThreads / 32], s_sum[kRows][D], s_top[4];
   const csa2_kv8_append_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.y, half = threadIdx.x >= kHalf, tid = threadIdx.x - half * kHalf;
+  const int h = blockIdx.x % c.Hkv, half = threadIdx.x >= kHalf, tid = threadIdx.x - half * kHalf;
   const int row0 = tid / kPer, ch = tid % kPer * 8;
   const long long st = half ? a.v_stride_t : a.k_stride_t, sh = half ? a.v_stride_h : a.k_stride_h;
   const T* x = reinterpret_cast<const T*>(half ? a.v : a.k) + h * sh + ch;
-  int t = blockIdx.x * p.range;
+  int t = blockIdx.x / c.Hkv * p.range;
   const int t_end = min(a.T, t + p.range);
   while (t < t_end) {
     const int s = find_seq(a.start, a.S, t);
@@ -275,6 +324,10 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
       t += n;
       continue;
     }
+    Eight<T> rows[kTurns];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i)
+      if (row0 + i * kRows < n) rows[i].template load<VEC>(x + (t + row0 + i * kRows) * st);
     const int page = page_id(c, s, pos >> kPageShift, &g_err_paged);
     if (page < 0) {
       t += n;
@@ -285,14 +338,20 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
     uint8_t* bytes = (half ? c.v : c.k) + ph * (kPage * D);
     const float was = held ? *scale_at : 0.f;
     float top = 0.f;
-    for (int r = row0; r < n; r += kRows) {
-      float f[8];
-      load8<T, D, VEC>(x + (t + r) * st, f);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float m = fabsf(f[i]);
-        if (m <= 3.402823466e38f) top = fmaxf(top, m);
-      }
+    for (int i = 0; i < kTurns; ++i)
+      if (row0 + i * kRows < n) top = rows[i].largest(top);
+    if (top == INFINITY) {               // infinities do not take part
+      top = 0.f;
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i)
+        if (row0 + i * kRows < n) {
+          float f[8];
+          rows[i].values(f);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (fabsf(f[e]) < INFINITY) top = fmaxf(top, fabsf(f[e]));
+        }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -310,37 +369,38 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
         *w = cvt_e4m3x2(f[0] * ratio, f[1] * ratio) | cvt_e4m3x2(f[2] * ratio, f[3] * ratio) << 16;
       }
     }
+    const bool full = c.mean && held + n == kPage;
     const float inv = __fdiv_rn(1.f, scale);                 // a power of two: exact
-    for (int r = row0; r < n; r += kRows) {
-      float f[8];
-      load8<T, D, VEC>(x + (t + r) * st, f);
-      uint2 w;
-      w.x = cvt_e4m3x2(f[0] * inv, f[1] * inv) | cvt_e4m3x2(f[2] * inv, f[3] * inv) << 16;
-      w.y = cvt_e4m3x2(f[4] * inv, f[5] * inv) | cvt_e4m3x2(f[6] * inv, f[7] * inv) << 16;
-      *reinterpret_cast<uint2*>(bytes + (held + r) * D + ch) = w;
-    }
-    __syncthreads();                                         // the page's bytes are written, s_max is read
-    if (tid == 0) *scale_at = scale;
-    if (c.mean && held + n == kPage) {
-      if (!half) {
-        float m[8] = {};
-        for (int r = row0; r < kPage; r += kRows) {
-          const uint2 w = *reinterpret_cast<const uint2*>(bytes + r * D + ch);
-          float f[8];
-          e4m3x4_to_f32(w.x, f);
-          e4m3x4_to_f32(w.y, f + 4);
+    float2 m[4] = {};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) m[i] += f[i] == f[i] ? f[i] : 0.f;
+    for (int i = 0; i < kTurns; ++i)
+      if (row0 + i * kRows < n) {
+        float f[8];
+        rows[i].values(f);
+        uint32_t e[4];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float2 y = mul2(make_float2(f[2 * d], f[2 * d + 1]), make_float2(inv, inv));
+          e[d] = cvt_e4m3x2(y.x, y.y);
         }
+        const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
+        *reinterpret_cast<uint2*>(bytes + (held + row0 + i * kRows) * D + ch) = w;
+        if (full && !half) add_bytes(m, w);
+      }
+    __syncthreads();                                         // old bytes are as they stay, s_max is read
+    if (tid == 0) *scale_at = scale;
+    if (full) {
+      if (!half) {
+        for (int r = row0; r < held; r += kRows) add_bytes(m, *reinterpret_cast<const uint2*>(bytes + r * D + ch));
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s_sum[row0][ch + i] = m[i];
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(&s_sum[row0][ch + 2 * i]) = m[i];
       }
       __syncthreads();
-      float m = 0.f;
+      float sum = 0.f;
       if (threadIdx.x < D) {
 #pragma unroll
-        for (int r = 0; r < kRows; ++r) m += s_sum[r][threadIdx.x];
-        float u = fabsf(m);
+        for (int r = 0; r < kRows; ++r) sum += s_sum[r][threadIdx.x];
+        float u = fabsf(sum);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) u = fmaxf(u, __shfl_xor_sync(0xffffffffu, u, o));
         if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = u;
@@ -351,7 +411,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
 #pragma unroll
         for (int i = 1; i < D / 32; ++i) u = fmaxf(u, s_top[i]);
         u = __fdiv_rn(u, 127.f);
-        c.mean[ph * D + threadIdx.x] = (int8_t)(u > 0.f ? __float2int_rn(__fdiv_rn(m, u)) : 0);
+        c.mean[ph * D + threadIdx.x] = (int8_t)(u > 0.f ? __float2int_rn(__fdiv_rn(sum, u)) : 0);
         if (threadIdx.x == 0) c.mean_scale[ph] = u * 0.015625f * scale;
       }
       __syncthreads();                                       // the sums are read before the next page's
@@ -679,7 +739,9 @@ cudaError_t launch_kv8_append(const csa2_kv8_append_args& a, cudaStream_t st) {
   p.a = a;
   const long long tasks = (long long)a.T * a.cache.Hkv;
   p.range = (int)(tasks / 2432 < 1 ? 1 : tasks / 2432 > 64 ? 64 : tasks / 2432);
-  const dim3 grid((a.T + p.range - 1) / p.range, a.cache.Hkv);
+  const long long ctas = (long long)((a.T + p.range - 1) / p.range) * a.cache.Hkv;   // a token's heads side by side
+  if (ctas > INT_MAX) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)ctas);
   const size_t unit = a.x_dtype == CSA2_BF16 ? 2 : 4;
   auto rows = [&](const void* x, int64_t t, int64_t h) {
     return (((uintptr_t)x | (uintptr_t)(t * unit) | (uintptr_t)(h * unit)) & 15) == 0;
