@@ -214,7 +214,7 @@ __device__ __forceinline__ float scale_for(float a) {
   return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
-constexpr int kAppendThreads = 256;      // half of them for the keys, half for the values
+constexpr int kAppendThreads = 128;
 
 struct AppendParams {
   csa2_kv8_append_args a;
@@ -290,21 +290,21 @@ __device__ __forceinline__ void add_bytes(float2* m, uint2 w) {            // a 
   for (int i = 0; i < 4; ++i) m[i] = add2(m[i], __half22float2(*reinterpret_cast<const __half2*>(&h[i])));
 }
 
-// A CTA a (range of rows, head): the pages whose first new token lies in the range, one after the other.  A page's new
+// A CTA a (range of rows, head, plane): the pages whose first new token lies in the range, one after the other.  A page's new
 // rows are loaded at once and stay in registers from the largest magnitude to the summary.
 template <typename T, int D, bool VEC>
-__global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParams p) {
-  constexpr int kHalf = kAppendThreads / 2, kPer = D / 8, kRows = kHalf / kPer, kTurns = kPage / kRows;   // threads a row, rows a turn
+__global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 8 : 4) k_kv8_append(const AppendParams p) {
+  constexpr int kPer = D / 8, kRows = kAppendThreads / kPer, kTurns = kPage / kRows;   // threads a row, rows a turn
   __shared__ float s_max[kAppendThreads / 32], s_sum[kRows][D], s_top[4];
   const csa2_kv8_append_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
   pdl_wait();
   pdl_trigger();
-  const int h = blockIdx.x % c.Hkv, half = threadIdx.x >= kHalf, tid = threadIdx.x - half * kHalf;
+  const int plane = blockIdx.x & 1, h = blockIdx.x / 2 % c.Hkv, tid = threadIdx.x;   // 0: keys, 1: values
   const int row0 = tid / kPer, ch = tid % kPer * 8;
-  const long long st = half ? a.v_stride_t : a.k_stride_t, sh = half ? a.v_stride_h : a.k_stride_h;
-  const T* x = reinterpret_cast<const T*>(half ? a.v : a.k) + h * sh + ch;
-  int t = blockIdx.x / c.Hkv * p.range;
+  const long long st = plane ? a.v_stride_t : a.k_stride_t, sh = plane ? a.v_stride_h : a.k_stride_h;
+  const T* x = reinterpret_cast<const T*>(plane ? a.v : a.k) + h * sh + ch;
+  int t = blockIdx.x / 2 / c.Hkv * p.range;
   const int t_end = min(a.T, t + p.range);
   while (t < t_end) {
     const int s = find_seq(a.start, a.S, t);
@@ -334,8 +334,8 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
       continue;
     }
     const long long ph = (long long)page * c.Hkv + h;
-    float* scale_at = (half ? c.v_scale : c.k_scale) + ph;
-    uint8_t* bytes = (half ? c.v : c.k) + ph * (kPage * D);
+    float* scale_at = (plane ? c.v_scale : c.k_scale) + ph;
+    uint8_t* bytes = (plane ? c.v : c.k) + ph * (kPage * D);
     const float was = held ? *scale_at : 0.f;
     float top = 0.f;
 #pragma unroll
@@ -355,21 +355,21 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
+    if ((tid & 31) == 0) s_max[tid >> 5] = top;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kHalf / 32; ++i) top = fmaxf(top, s_max[half * (kHalf / 32) + i]);
+    for (int i = 0; i < kAppendThreads / 32; ++i) top = fmaxf(top, s_max[i]);
     const float scale = fmaxf(scale_for(top), was);
     if (held && scale > was) {
       const float ratio = __fdiv_rn(was, scale);
-      for (int i = tid; i < held * D / 4; i += kHalf) {
+      for (int i = tid; i < held * D / 4; i += kAppendThreads) {
         uint32_t* w = reinterpret_cast<uint32_t*>(bytes) + i;
         float f[4];
         e4m3x4_to_f32(*w, f);
         *w = cvt_e4m3x2(f[0] * ratio, f[1] * ratio) | cvt_e4m3x2(f[2] * ratio, f[3] * ratio) << 16;
       }
     }
-    const bool full = c.mean && held + n == kPage;
+    const bool full = c.mean && !plane && held + n == kPage;
     const float inv = __fdiv_rn(1.f, scale);                 // a power of two: exact
     float2 m[4] = {};
 #pragma unroll
@@ -385,16 +385,14 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
         }
         const uint2 w = make_uint2(e[0] | e[1] << 16, e[2] | e[3] << 16);
         *reinterpret_cast<uint2*>(bytes + (held + row0 + i * kRows) * D + ch) = w;
-        if (full && !half) add_bytes(m, w);
+        if (full) add_bytes(m, w);
       }
     __syncthreads();                                         // old bytes are as they stay, s_max is read
     if (tid == 0) *scale_at = scale;
     if (full) {
-      if (!half) {
-        for (int r = row0; r < held; r += kRows) add_bytes(m, *reinterpret_cast<const uint2*>(bytes + r * D + ch));
+      for (int r = row0; r < held; r += kRows) add_bytes(m, *reinterpret_cast<const uint2*>(bytes + r * D + ch));
 #pragma unroll
-        for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(&s_sum[row0][ch + 2 * i]) = m[i];
-      }
+      for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(&s_sum[row0][ch + 2 * i]) = m[i];
       __syncthreads();
       float sum = 0.f;
       if (threadIdx.x < D) {
@@ -739,7 +737,7 @@ cudaError_t launch_kv8_append(const csa2_kv8_append_args& a, cudaStream_t st) {
   p.a = a;
   const long long tasks = (long long)a.T * a.cache.Hkv;
   p.range = (int)(tasks / 2432 < 1 ? 1 : tasks / 2432 > 64 ? 64 : tasks / 2432);
-  const long long ctas = (long long)((a.T + p.range - 1) / p.range) * a.cache.Hkv;   // a token's heads side by side
+  const long long ctas = (long long)((a.T + p.range - 1) / p.range) * a.cache.Hkv * 2;   // a token's heads and planes side by side
   if (ctas > INT_MAX) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)ctas);
   const size_t unit = a.x_dtype == CSA2_BF16 ? 2 : 4;
