@@ -24,8 +24,11 @@ namespace {
 // fragment the bytes of two neighbouring tokens interleaved; the scores' accumulators are the weights' A
 // fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
 // its partial output, in float32.
-constexpr int kWarps = 4, kStreamCtas = 2 * 152, kSpans = kStreamCtas * kWarps, kLeast = 4;
-constexpr int kHalf = kPage / 2;
+constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
+
+// Two CTAs an SM.  Three, at 168 registers a thread and two stages a warp, are slower (64 sequences up to 64K: 726 us
+// against 624; 2048 rows over 32 pages each: 1.40 ms against 1.29).
+constexpr int kStreamCtas = 2 * 152, kSpans = kStreamCtas * kWarps;
 
 template <int D>
 struct Ring {
@@ -636,7 +639,12 @@ cudaError_t launch_stream(const CUtensorMap& mk, const CUtensorMap& mv, const Kv
   const size_t smem = Ring<D>::kBytes + (LIST ? 0 : 8 * (size_t)((p.a.S + 31) / 32));
   cudaError_t e = limit.raise(k_kv8_stream<D, RT, LIST>, smem);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv8_stream<D, RT, LIST>, dim3(kStreamCtas), dim3(32 * kWarps), smem, st, mk, mv, p);
+  return launch_k(k_kv8_stream<D, RT, LIST>, dim3(152 * 2), dim3(32 * kWarps), smem, st, mk, mv, p);
+}
+
+// Whether a sequence's rows of a key head fit a tile of 8.
+bool takes_eight(const csa2_kv8_attn_args& a) {
+  return (a.pages ? 1 : (long long)a.max_new) * (a.Hq / a.cache.Hkv) <= 8;
 }
 
 template <int D>
@@ -644,9 +652,8 @@ cudaError_t launch_rows(const Kv8Params& p, cudaStream_t st) {
   CUtensorMap mk, mv;
   if (!plane_map(&mk, p.a.cache.k, p.a.cache, kHalf) || !plane_map(&mv, p.a.cache.v, p.a.cache, kHalf))
     return cudaErrorInvalidValue;
-  if (p.a.pages) return p.G <= 8 ? launch_stream<D, 8, true>(mk, mv, p, st) : launch_stream<D, 16, true>(mk, mv, p, st);
-  return (long long)p.a.max_new * p.G <= 8 ? launch_stream<D, 8, false>(mk, mv, p, st)
-                                           : launch_stream<D, 16, false>(mk, mv, p, st);
+  if (takes_eight(p.a)) return p.a.pages ? launch_stream<D, 8, true>(mk, mv, p, st) : launch_stream<D, 8, false>(mk, mv, p, st);
+  return p.a.pages ? launch_stream<D, 16, true>(mk, mv, p, st) : launch_stream<D, 16, false>(mk, mv, p, st);
 }
 
 // Rows of a sequence and key head from which the tiles of 128 rows take over from the streams of 16.
@@ -654,10 +661,16 @@ bool takes_tiles(const csa2_kv8_attn_args& a) {
   return !a.pages && (long long)a.max_new * (a.Hq / a.cache.Hkv) > 16;
 }
 
+int spans_of(const csa2_kv8_attn_args& a) {
+  return takes_tiles(a) ? kTileSpans : kSpans;
+}
+int most_of(const csa2_kv8_attn_args& a) { return takes_tiles(a) ? kTileRows : takes_eight(a) ? 8 : 16; }
+Layout layout_of(const csa2_kv8_attn_args& a) { return Layout(spans_of(a), most_of(a), a.cache.D); }
+
 }  // namespace
 
 size_t kv8_attn_workspace_bytes(const csa2_kv8_attn_args& a) {
-  return (takes_tiles(a) ? Layout(kTileSpans, kTileRows, a.cache.D) : Layout(kSpans, 16, a.cache.D)).bytes;
+  return layout_of(a).bytes;
 }
 
 cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t st) {
@@ -668,16 +681,16 @@ cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t 
   p.G = a.Hq / a.cache.Hkv;
   const bool q16 = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride_t) | (uintptr_t)(2 * a.q_stride_h)) & 15) == 0;
   p.aligned = (q16 ? 1 : 0) | (((uintptr_t)a.out & 15) == 0 ? 2 : 0);
-  p.spans = tiles ? kTileSpans : kSpans;
-  p.most = tiles ? kTileRows : 16;
-  const Layout at(p.spans, p.most, a.cache.D);
+  p.spans = spans_of(a);
+  p.most = most_of(a);
+  const Layout at = layout_of(a);
   uint8_t* w = static_cast<uint8_t*>(ws);
   p.part = reinterpret_cast<Part*>(w + at.part);
   p.ml = reinterpret_cast<float2*>(w + at.ml);
   p.o = reinterpret_cast<float*>(w + at.o);
   cudaError_t e = tiles ? launch_kv8_tile(p, st) : a.cache.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.spans, p.most / 16);
+  const dim3 grid(p.spans, (p.most + 15) / 16);
   return a.cache.D == 64 ? launch_k(k_kv8_join<64>, grid, dim3(256), 0, st, p)
                          : launch_k(k_kv8_join<128>, grid, dim3(256), 0, st, p);
 }

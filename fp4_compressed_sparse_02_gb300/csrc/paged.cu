@@ -578,6 +578,69 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(const SelectParams 
   }
 }
 
+// Rows with at most 32 K pages, a warp a (row, head): lane l holds keys l, l + 32, ...; the k-th best bit by bit, by
+// ballots.
+template <int K>
+__global__ void __launch_bounds__(256) k_kv8_pick_warp(const SelectParams p) {
+  const csa2_kv8_select_args& a = p.a;
+  const csa2_kv8_cache& c = a.cache;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, i = blockIdx.x * 8 + (threadIdx.x >> 5), t = p.t0 + i / c.Hkv, h = i % c.Hkv;
+  if (t >= p.t1) return;
+  const int s = find_seq(a.start, a.S, t);
+  if (s < 0) return;
+  const long long row = (long long)t * c.Hkv + h;
+  int* out = a.pages + row * a.k;
+  int pos = row_pos(c, a.start, a.length, s, t, &g_err_paged);
+  if (pos >= a.max_length) {
+    if (lane == 0) raise_error(&g_err_paged, CSA2_DEVERR_N_VIS);
+    pos = -1;
+  }
+  const int P = pos < 0 ? 0 : (pos >> kPageShift) + 1;
+  if (P <= a.k) {
+    for (int j = lane; j < a.k; j += 32) out[j] = j < P ? j : -1;
+    if (lane == 0) a.count[row] = P;
+    return;
+  }
+  const int lo = a.first, hi = P - a.recent, M = hi - lo, want = a.k - a.first - a.recent;
+  for (int j = lane; j < a.first; j += 32) out[j] = j;
+  for (int j = lane; j < a.recent; j += 32) out[a.k - a.recent + j] = hi + j;
+  if (lane == 0) a.count[row] = a.k;
+  if (want == 0) return;
+  const uint32_t* src = p.keys + ((long long)(t - p.t0) * c.Hkv + h) * p.stride + lo;
+  uint32_t key[K];
+#pragma unroll
+  for (int j = 0; j < K; ++j) key[j] = j * 32 + lane < M ? src[j * 32 + lane] : 0u;
+  // the largest threshold that at least `want` keys reach; keys of bad pages are 0, and M > want keys reach that
+  uint32_t least = 0;
+  for (uint32_t bit = 1u << 31; bit; bit >>= 1) {
+    const uint32_t at = least | bit;
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < K; ++j) n += key[j] >= at;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n >= want) least = at;
+    if (n == want) break;                                    // exactly those
+  }
+  int above = 0;
+#pragma unroll
+  for (int j = 0; j < K; ++j) above += key[j] > least;
+  int left = want - __reduce_add_sync(0xffffffffu, above);   // to take of those equal to it, from the first on
+  const uint32_t under = (1u << lane) - 1;
+  int at = a.first;
+#pragma unroll
+  for (int j = 0; j < K; ++j) {
+    const bool in = j * 32 + lane < M;
+    const uint32_t equal = __ballot_sync(0xffffffffu, in && key[j] == least);
+    const bool take = in && (key[j] > least || (key[j] == least && __popc(equal & under) < left));
+    const uint32_t taken = __ballot_sync(0xffffffffu, take);
+    if (take) out[at + __popc(taken & under)] = lo + j * 32 + lane;
+    at += __popc(taken);
+    left = max(0, left - __popc(equal));
+  }
+}
+
 // A CTA a (row, head): the k-th best key by digits of 11, 11 and 10 bits, then the kept pages in ascending order.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_kv8_pick(const SelectParams p) {
@@ -707,7 +770,14 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t st) {
     }
     const size_t smem = 4 * (size_t)p.stride;
     const dim3 grid(p.t1 - p.t0, a.cache.Hkv);
-    if (p.stride <= 4096) {
+    const dim3 warps((unsigned)(((long long)(p.t1 - p.t0) * a.cache.Hkv + 7) / 8));
+    if (p.stride <= 256) {
+      e = launch_k(k_kv8_pick_warp<8>, warps, dim3(256), 0, st, p);
+    } else if (p.stride <= 640) {
+      e = launch_k(k_kv8_pick_warp<20>, warps, dim3(256), 0, st, p);
+    } else if (p.stride <= 1024) {
+      e = launch_k(k_kv8_pick_warp<32>, warps, dim3(256), 0, st, p);
+    } else if (p.stride <= 4096) {
       e = launch_k(k_kv8_pick<256>, grid, dim3(256), smem, st, p);
     } else {
       e = limit_many.raise(k_kv8_pick<1024>, smem);
