@@ -226,12 +226,14 @@ struct Walk {
   __device__ __forceinline__ bool ends() const { return x + take == t.count; }
 };
 
-// SPLIT: one tile of 128 rows, whose even and odd steps are two streams of their own that are added up at the end of a
-// segment; else two tiles of 128 rows that share every step.
-template <int D, bool SPLIT>
+// RT: rows of a stream.  256: the groups are two tiles of 128 rows that share every step.  128 and 64 (SPLIT): the groups
+// have the same rows, one the even steps and one the odd ones, and are added up at the end of a segment.  At 64 rows two
+// threads of a softmax warp share a row (M = 64 puts 16 rows into each quarter of the TMEM lanes), half the columns each.
+template <int D, int RT>
 __global__ void __launch_bounds__(kThreads, 1)
 k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8Params p) {
-  constexpr int RT = SPLIT ? 128 : 256;
+  constexpr bool SPLIT = RT < 256;
+  constexpr int kM = RT == 64 ? 64 : 128, kCols = kStep * kM / 128, kDims = D * kM / 128;   // scores and channels of a thread
   using L = Smem<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Shared m;
@@ -385,7 +387,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       // next step.  A product's issue lasts about as long as the product, so what a warp waits for is hidden behind
       // the other's.  The groups take turns: left alone they fall into step, both softmaxes and then both products
       // (4096 new tokens at 32K: 4.5 ms).
-      constexpr uint32_t id_s = tc::idesc_f16(128, kStep, 0, 0, 0), id_o = tc::idesc_f16(128, D, 0, 0, 1);   // E4M3 is type 0, as fp16
+      constexpr uint32_t id_s = tc::idesc_f16(kM, kStep, 0, 0, 0), id_o = tc::idesc_f16(kM, D, 0, 0, 1);   // E4M3 is type 0, as fp16
       constexpr int kBy = SPLIT ? 2 : 1;
       const int grp = warp - kMma;
       const uint64_t q_desc = desc8<D>(base + (SPLIT ? 0 : grp * L::kQ)), k_desc = desc8<D>(base + L::kK);
@@ -526,11 +528,16 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       }
     }
   } else {
-    // ---- softmax: a row a thread
+    // ---- softmax: a row a thread (kM = 64: two threads)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
     Walk<RT> w(p, m, per);
-    const int grp = (warp - kSoftmax) >> 2, r = tid & 127;
+    const int grp = (warp - kSoftmax) >> 2, half = kM == 64 ? lane >> 4 : 0;
+    const int r = (warp & 3) * (kM / 4) + lane % (kM / 4);
     const uint32_t lanes = tb + ((uint32_t)(warp & 3) << 21), s_at = lanes + grp * 128, o_at = lanes + 256 + grp * 128;
+    auto load_o = [&](uint32_t at, float* v) {               // 32 channels of this thread
+      if constexpr (kM == 64) tc::tmem_ld16x2_32<kDims>(at, reinterpret_cast<uint32_t*>(v));
+      else tc::tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
+    };
     int step = 0, seen = 0, outs = 0, outs1 = 0;   // steps of earlier segments; scores, outputs waited for
     Part part = {0, 0, 0, 0, 0};
     for (; w.on(); w.next(p)) {
@@ -546,9 +553,9 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // lanes a row, rows at a time
         const int sub = lane % kLanes;
         const long long mine = real ? tok * a.q_stride_t + (long long)hq * a.q_stride_h : -1;
-        uint4 v[32 / kRows];
+        uint4 v[kM / 4 / kRows];
 #pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
+        for (int i = 0; i < kM / 4 / kRows; ++i) {
           const long long at = __shfl_sync(0xffffffffu, mine, i * kRows + lane / kLanes);
           v[i] = make_uint4(0, 0, 0, 0);
           if (at >= 0) {
@@ -564,7 +571,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           }
         }
 #pragma unroll
-        for (int i = 0; i < 32 / kRows; ++i) {
+        for (int i = 0; i < kM / 4 / kRows; ++i) {
           const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
           float x[8], top = 0.f, f, undo;
 #pragma unroll
@@ -579,7 +586,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           row_factor(top, f, undo);
           f *= 0.0078125f;
           const float back = __shfl_sync(0xffffffffu, undo * 128.f * (a.softmax_scale * kLog2e), lane % kRows * kLanes);
-          if (lane / kRows == i) mul = back;
+          if (lane % (kM / 4) / kRows == i) mul = back;
           if (!SPLIT || grp == 0) {
             const bool bad = top == INFINITY;                // an infinity makes its row NaN, as a NaN does
             uint2 hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), lo8 = hi8;
@@ -596,7 +603,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
               hi8 = make_uint2(h4[0] | h4[1] << 16, h4[2] | h4[3] << 16);
               lo8 = make_uint2(l4[0] | l4[1] << 16, l4[2] | l4[3] << 16);
             }
-            const int qr = (warp & 3) * 32 + i * kRows + lane / kLanes, ch = sub >> 1;
+            const int qr = (warp & 3) * (kM / 4) + i * kRows + lane / kLanes, ch = sub >> 1;
             const uint32_t at = base + (SPLIT ? 0 : grp * L::kQ) + qr * D +
                                 ((D == 128 ? ch ^ (qr & 7) : ch ^ (qr >> 1 & 3)) << 4) + (sub & 1) * 8;
             sts64(at, hi8);
@@ -623,26 +630,37 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const bool border = __any_sync(0xffffffffu, token0 < lo || token0 + kStep > hi || ks.x == -1.f || ks.y == -1.f);
         const int from0 = ks.x == -1.f ? INT_MAX : lo - token0, from1 = ks.y == -1.f ? INT_MAX : lo - token0;
         const int to = hi == INT_MAX ? INT_MAX : hi - token0;
-        float x[kStep];
+        float x[kCols];                  // of tokens 64 * half + ...
+        if constexpr (kM == 64) {
+          tc::tmem_ld16x2_32<64>(s_at, reinterpret_cast<uint32_t*>(x));
+          tc::tmem_ld16x2_32<64>(s_at + 32, reinterpret_cast<uint32_t*>(x + 32));
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tc::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x + 32 * i));
+          for (int i = 0; i < 4; ++i) tc::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x + 32 * i));
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) tmem_arrived(x + 32 * i);
+        for (int i = 0; i < kCols / 32; ++i) tmem_arrived(x + 32 * i);
         if (border) {
 #pragma unroll
-          for (int e = 0; e < kStep; ++e) {
-            const bool in = e >= (e < kPage ? from0 : from1) && e < to;
-            x[e] = in ? x[e] : -INFINITY;
+          for (int e = 0; e < kCols; ++e) {
+            const int from = kM == 64 ? (half ? from1 : from0) : e < kPage ? from0 : from1, at = kM == 64 ? 64 * half + e : e;
+            x[e] = at >= from && at < to ? x[e] : -INFINITY;
           }
         }
-        float mx[4] = {x[0], x[32], x[64], x[96]};
+        float mx[kCols / 32];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          mx[i] = fmaxf(mx[i], x[32 * i + 1]);
+        for (int i = 0; i < kCols / 32; ++i) {
+          mx[i] = fmaxf(x[32 * i], x[32 * i + 1]);
 #pragma unroll
           for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], x[32 * i + e], x[32 * i + e + 1]);
         }
-        const float now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
+        float now;
+        if constexpr (kM == 64) {
+          now = fmaxf(mx[0], mx[1]) * (half ? f1 : f0);
+          now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+        } else {
+          now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
+        }
         // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
         // sum are rescaled a few times a row.
         const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
@@ -652,13 +670,18 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           l *= alpha;
           if (any) {
 #pragma unroll 1
-            for (int i = 0; i < D; i += 32) {
+            for (int i = 0; i < kDims; i += 32) {
               float v[32];
-              tc::tmem_ld32(o_at + i, reinterpret_cast<uint32_t*>(v));
+              load_o(o_at + i, v);
               tmem_arrived(v);
 #pragma unroll
               for (int e = 0; e < 32; ++e) v[e] *= alpha;
-              tc::tmem_st32(o_at + i, reinterpret_cast<const uint32_t*>(v));
+              if constexpr (kM == 64) {
+                tc::tmem_st16x2_16<kDims>(o_at + i, reinterpret_cast<const uint32_t*>(v));
+                tc::tmem_st16x2_16<kDims>(o_at + i + 16, reinterpret_cast<const uint32_t*>(v + 16));
+              } else {
+                tc::tmem_st32(o_at + i, reinterpret_cast<const uint32_t*>(v));
+              }
             }
           }
         }
@@ -667,18 +690,23 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         float2 sum[4] = {};
         const float2 zz = make_float2(-z, -z);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float2 f = i < 4 ? make_float2(f0, f0) : make_float2(f1, f1);
-          uint32_t w8[8];
+        for (int i = 0; i < kCols / 32; ++i) {
+          const float f = kM == 64 ? (half ? f1 : f0) : i < 2 ? f0 : f1;
+          uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            float2 y = fma2(make_float2(x[16 * i + 2 * e], x[16 * i + 2 * e + 1]), f, zz);
+          for (int e = 0; e < 16; ++e) {
+            float2 y = fma2(make_float2(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), make_float2(f, f), zz);
             y.x = ex2(y.x);
             y.y = ex2(y.y);
-            w8[e] = f16x2(y.x, y.y);
+            w[e] = f16x2(y.x, y.y);
             sum[e & 3] = add2(sum[e & 3], y);
           }
-          tc::tmem_st8(s_at + 8 * i, w8);                    // over the scores
+          if constexpr (kM == 64) {      // over the scores
+            tc::tmem_st16x2_16<32>(s_at + 16 * i, w);
+          } else {
+            tc::tmem_st8(s_at + 16 * i, w);
+            tc::tmem_st8(s_at + 16 * i + 8, w + 8);
+          }
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
@@ -689,7 +717,8 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       }
       // ---- the segment's result, or its part
       const bool two = SPLIT && w.take > 1;                  // both groups have steps
-      if (SPLIT && grp == 1) m.ml[r] = make_float2(top, l);
+      if (kM == 64) l += __shfl_xor_sync(0xffffffffu, l, 16);
+      if (SPLIT && grp == 1 && half == 0) m.ml[r] = make_float2(top, l);
       if (SPLIT) named_sync(1, 256);
       if (!SPLIT || grp == 0) {
         await_warp(&m.o_full[grp], outs++ & 1, m);
@@ -711,13 +740,14 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const long long out_row = (long long)tok * a.Hq + hq;
         const long long at = ((long long)blockIdx.x * 2 + (w.begins() ? 1 : 0)) * p.most + row;
 #pragma unroll 1
-        for (int i = 0; i < D; i += 32) {
+        for (int i0 = 0; i0 < kDims; i0 += 32) {
+          const int i = half * kDims + i0;                   // the channels' first
           float v[32];
-          tc::tmem_ld32(o_at + i, reinterpret_cast<uint32_t*>(v));
+          load_o(o_at + i0, v);
           tmem_arrived(v);
           if (two) {
             float u[32];
-            tc::tmem_ld32(o_at + 128 + i, reinterpret_cast<uint32_t*>(u));
+            load_o(o_at + 128 + i0, u);
             tmem_arrived(u);
 #pragma unroll
             for (int e = 0; e < 32; ++e) v[e] = v[e] * a0 + u[e] * a1;
@@ -771,7 +801,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             }
           }
         }
-        if (real) {
+        if (real && half == 0) {
           if (!whole) p.ml[at] = make_float2(top, l);
           else if (a.lse) a.lse[out_row] = l == 0.f ? -INFINITY : (top + log2f(l)) * kLn2;
         }
@@ -793,23 +823,28 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   if (warp == kMma) tc::tmem_dealloc(tb, 512);
 }
 
-template <int D, bool SPLIT>
+template <int D, int RT>
 cudaError_t launch(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8Params& p, cudaStream_t st) {
   static SmemLimit limit;
-  const cudaError_t e = limit.raise(k_kv8_tile<D, SPLIT>, Smem<D>::kBytes);
+  const cudaError_t e = limit.raise(k_kv8_tile<D, RT>, Smem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv8_tile<D, SPLIT>, dim3(kTileSpans), dim3(kThreads), Smem<D>::kBytes, st, mk, mv, p);
+  return launch_k(k_kv8_tile<D, RT>, dim3(kTileSpans), dim3(kThreads), Smem<D>::kBytes, st, mk, mv, p);
+}
+
+template <int D>
+cudaError_t launch_of(const Kv8Params& p, cudaStream_t st) {
+  CUtensorMap mk, mv;
+  if (!plane_map(&mk, p.a.cache.k, p.a.cache, kPage) || !plane_map(&mv, p.a.cache.v, p.a.cache, kPage))
+    return cudaErrorInvalidValue;
+  const long long rows = (long long)p.a.max_new * p.G;
+  if (rows <= 64) return launch<D, 64>(mk, mv, p, st);
+  return rows <= 128 ? launch<D, 128>(mk, mv, p, st) : launch<D, 256>(mk, mv, p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_tile(const Kv8Params& p, cudaStream_t st) {
-  CUtensorMap mk, mv;
-  if (!plane_map(&mk, p.a.cache.k, p.a.cache, kPage) || !plane_map(&mv, p.a.cache.v, p.a.cache, kPage))
-    return cudaErrorInvalidValue;
-  const bool split = (long long)p.a.max_new * p.G <= 128;
-  if (p.a.cache.D == 64) return split ? launch<64, true>(mk, mv, p, st) : launch<64, false>(mk, mv, p, st);
-  return split ? launch<128, true>(mk, mv, p, st) : launch<128, false>(mk, mv, p, st);
+  return p.a.cache.D == 64 ? launch_of<64>(p, st) : launch_of<128>(p, st);
 }
 
 uint32_t read_clear_error_kv8_tile() {
