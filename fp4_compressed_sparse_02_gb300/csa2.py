@@ -714,7 +714,17 @@ def _step(cache, start, length, dev):
     S, = length.shape
     if start.shape != (S + 1,) or S > cache.page_table.shape[0]:
         raise ValueError("start must be [S + 1] and length [S], S at most the page table's rows")
-    return S, _dense(start, dev, torch.int32, "start"), _dense(length, dev, torch.int32, "length")
+    return S, *_i32_at(dev, (start, length), ("start", "length"))
+
+
+def _i32_at(dev, tensors, names):
+    """Addresses of contiguous int32 tensors on CUDA device number dev."""
+    at = []
+    for t, name in zip(tensors, names):
+        if t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous():
+            _dense(t, dev, torch.int32, name)            # says which
+        at.append(t.data_ptr())
+    return at
 
 
 @dataclass
@@ -745,18 +755,18 @@ def page_plan(length, add, page_table, free_pages, free_head, tokens, *, out=Non
     if add.shape != (S,) or page_table.shape[0] != S or free_head.numel() != 1:
         raise ValueError("length and add must be [S], page_table [S, max_pages], free_head [1]")
     dev = length.get_device()
+    ins = _i32_at(dev, (length, add, free_pages, free_head, page_table), ("length", "add", "free_pages", "free_head", "page_table"))
     if out is None:
         out = PagePlan.allocate(S, tokens, length.device)
-    elif (out.start.shape != (S + 1,) or out.length.shape != (S,) or out.head.numel() != 1
-          or any(t.shape != (tokens,) for t in (out.seq, out.pos, out.slot))):
-        raise ValueError("out must be PagePlan.allocate(S, tokens)")
-    i32 = torch.int32
-    _launch("csa2_page_plan", _PAGE_PLAN.pack(
-        _PAGE_PLAN.size, S, page_table.shape[1], tokens, free_pages.shape[0], _dense(length, dev, i32, "length"),
-        _dense(add, dev, i32, "add"), _dense(free_pages, dev, i32, "free_pages"), _dense(free_head, dev, i32, "free_head"),
-        _dense(page_table, dev, i32, "page_table"), _dense(out.start, dev, i32, "start"), _dense(out.seq, dev, i32, "seq"),
-        _dense(out.pos, dev, i32, "pos"), _dense(out.slot, dev, i32, "slot"), _dense(out.length, dev, i32, "out.length"),
-        _dense(out.head, dev, i32, "head")), dev)
+        at = out.start.data_ptr()                      # one allocation: seq, pos, slot, start, length, head
+        outs = (at, at - 12 * tokens, at - 8 * tokens, at - 4 * tokens, at + 4 * S + 4, at + 8 * S + 4)
+    else:
+        if (out.start.shape != (S + 1,) or out.length.shape != (S,) or out.head.numel() != 1
+                or any(t.shape != (tokens,) for t in (out.seq, out.pos, out.slot))):
+            raise ValueError("out must be PagePlan.allocate(S, tokens)")
+        outs = _i32_at(dev, (out.start, out.seq, out.pos, out.slot, out.length, out.head),
+                       ("start", "seq", "pos", "slot", "out.length", "out.head"))
+    _launch("csa2_page_plan", _PAGE_PLAN.pack(_PAGE_PLAN.size, S, page_table.shape[1], tokens, free_pages.shape[0], *ins, *outs), dev)
     return out
 
 
@@ -815,27 +825,32 @@ def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, win
     _expect(q, _B16, "q")
     if D != cache.k.shape[3]:
         raise ValueError("q must have the cache's channels")
+    dev = q.get_device()
     if out is None:
         out = torch.empty((T, Hq, D), dtype=out_dtype, device=q.device)
+        op = out.data_ptr()
     elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
+    else:
+        op = _dense(out, dev, out.dtype, "out")
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device)
+        lp = lse.data_ptr()
     elif lse.shape != (T, Hq):
         raise ValueError(f"lse must be [{T}, {Hq}]")
+    else:
+        lp = _dense(lse, dev, torch.float32, "lse")
     n = 0
     if pages is not None:
         if pages.shape[:2] != (T, H) or len(pages.shape) != 3:
             raise ValueError(f"pages must be [{T}, {H}, n]")
         n = pages.shape[2]
-    dev = q.get_device()
     qp, qt, qh = _heads_of(q, dev, "q")
-    S, sp, lp = _step(cache, start, length, dev)
+    S, sp, lengths = _step(cache, start, length, dev)
     _launch_ws("csa2_kv8_attn", _KV8_ATTN.pack(
         _KV8_ATTN.size, T, S, Hq, T if max_new is None else max_new, window,
-        1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, qp, qt, qh, sp, lp, *cache.fields(dev),
-        _dense(pages, dev, torch.int32, "pages"), n, _dense(out, dev, out.dtype, "out"), _float_type(out, "out"),
-        _dense(lse, dev, torch.float32, "lse")), ws, q.device, dev)
+        1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, qp, qt, qh, sp, lengths, *cache.fields(dev),
+        _dense(pages, dev, torch.int32, "pages"), n, op, _float_type(out, "out"), lp), ws, q.device, dev)
     return out, lse
 
 

@@ -561,18 +561,18 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
   if (lane == 0) p.part[span] = part;
 }
 
-// A CTA (span, rows by the sixteen): the stream that begins there and goes on in the next ones, a warp a row, a lane
+// A CTA (span, eight rows): the stream that begins there and goes on in the next ones, a warp a row, a lane
 // D / 32 channels.
 template <int D>
-__global__ void __launch_bounds__(256) k_kv8_join(const Kv8Params p) {
-  constexpr int kPer = D / 32, kAhead = 8;
+__global__ void __launch_bounds__(256, 2) k_kv8_join(const Kv8Params p) {
+  constexpr int kPer = D / 32, kAhead = 16;
   const csa2_kv8_attn_args& a = p.a;
   pdl_wait();
   pdl_trigger();
   const int w0 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const Part part = p.part[w0];
-  const int last = min(part.last, p.spans - 1), rows = min(part.rows, (int)blockIdx.y * 16 + 16);
-  for (int r = blockIdx.y * 16 + warp; r < rows; r += 8) {
+  const int last = min(part.last, p.spans - 1), r = blockIdx.y * 8 + warp;
+  if (r < part.rows) {
     auto at = [&](int w) { return ((long long)w * 2 + (w == w0 ? 1 : 0)) * p.most + r; };
     float top = -INFINITY, sum = 0.f, v[kPer] = {};
     for (int b = w0; b <= last; b += 32) {
@@ -602,9 +602,8 @@ __global__ void __launch_bounds__(256) k_kv8_join(const Kv8Params p) {
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
           const float fi = __shfl_sync(0xffffffffu, f, (i + j) & 31);
-          if (i + j < n)
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) v[e] += o[j][e] * fi;
+          for (int e = 0; e < kPer; ++e) v[e] += i + j < n ? o[j][e] * fi : 0.f;
         }
       }
     }
@@ -690,7 +689,7 @@ cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t 
   p.o = reinterpret_cast<float*>(w + at.o);
   cudaError_t e = tiles ? launch_kv8_tile(p, st) : a.cache.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
   if (e != cudaSuccess) return e;
-  const dim3 grid(p.spans, (p.most + 15) / 16);
+  const dim3 grid(p.spans, p.most / 8);
   return a.cache.D == 64 ? launch_k(k_kv8_join<64>, grid, dim3(256), 0, st, p)
                          : launch_k(k_kv8_join<128>, grid, dim3(256), 0, st, p);
 }
