@@ -19,10 +19,11 @@ namespace {
 //
 // A warp's half pages come by TMA into its own ring of 8 KB stages (keys, then values), swizzled so that
 // the reads below meet no bank twice.  E4M3 bytes become fp16 pairs in registers (exact), products are
-// mma.sync m16n8k16: rows on M, 8 tokens (scores) or 8 channels (values) on N.  A lane's K fragment is 32
-// consecutive channels of one token (a permutation of the channels that Q's fragments share), its V
-// fragment the bytes of two neighbouring tokens interleaved; the scores' accumulators are the weights' A
-// fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
+// mma.sync m16n8k16.  Tiles of 16 rows stand on M, with 8 tokens (scores) or 8 channels (values) on N; tiles of 8 rows
+// stand on N, with 16 tokens or channels on M, which halves the products and asks for one 8 x 8 transpose of the weights
+// for 8 tokens.  A lane's K fragment is 32 consecutive channels of one token (a permutation of the channels that Q's
+// fragments share), its V fragment the bytes of two neighbouring tokens interleaved; at 16 rows the scores'
+// accumulators are the weights' A fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
 // its partial output, in float32.
 constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
 
@@ -36,24 +37,23 @@ struct Ring {
   static constexpr int kBytes = kWarps * kStages * kStage;
 };
 
-// One row's channels, held as v[0 .. D/4) by the four lanes of a quad: dims D/4 * c ...
-template <int D>
-__device__ __forceinline__ void store_row(const csa2_kv8_attn_args& a, long long row, int c, const float* v, bool aligned) {
-  const long long at = row * D + c * (D / 4);
+// N channels of the output from element `at` on.
+template <int N>
+__device__ __forceinline__ void store_piece(const csa2_kv8_attn_args& a, long long at, const float* v, bool aligned) {
   if (a.out_dtype == CSA2_F32) {
     float* out = reinterpret_cast<float*>(a.out) + at;
     if (aligned) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+      for (int i = 0; i < N / 4; ++i) reinterpret_cast<float4*>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < D / 4; ++i) out[i] = v[i];
+      for (int i = 0; i < N; ++i) out[i] = v[i];
     }
     return;
   }
   uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + at;
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) {
+  for (int i = 0; i < N / 8; ++i) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[j] = bf16x2(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
@@ -66,16 +66,28 @@ __device__ __forceinline__ void store_row(const csa2_kv8_attn_args& a, long long
   }
 }
 
+// An 8 x 8 matrix of 16-bit values, two of row lane / 4 a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
 // RT: rows of a tile, 8 or 16.  LIST: streams are (row, head) pairs over their listed pages.
 template <int D, int RT, bool LIST>
 __global__ void __launch_bounds__(32 * kWarps, 2)
 k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8Params p) {
-  constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kNt = D / 8, kR = RT / 8;
+  constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kR = RT / 8;
+  constexpr bool kT = RT == 8;           // rows on N
+  constexpr int kNt = kT ? D / 16 : D / 8;                   // accumulators of four
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kSt];
   const csa2_kv8_attn_args& a = p.a;
   const csa2_kv8_cache& c = a.cache;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q4 = lane & 3;
+  // the rows whose sums this lane keeps: g and g + 8, or the two of its accumulators' columns
+  auto own = [&](int i) { return kT ? 2 * q4 + i : g + 8 * i; };
+  constexpr int kLane0 = kT ? 4 : 1, kLane1 = kT ? 32 : 4;   // lanes at these distances hold the same rows
   const int G = p.G, Hkv = c.Hkv, span = blockIdx.x * kWarps + warp;
   uint8_t* ring = smem + warp * kSt * kStage;
   const uint32_t ring_s = smem_u32(ring);
@@ -202,14 +214,14 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       rows = rows_of(a, s, G);
     }
     const int nrows = min(RT, rows.n - r0);
-    // ---- what this lane's rows g and g + 8 see
-    int lo[kR], hi[kR], lo_min = INT_MAX, lo_max = 0, hi_min = INT_MAX, hi_max = 0;
+    // ---- what this lane's rows see
+    int lo[2], hi[2], lo_min = INT_MAX, lo_max = 0, hi_min = INT_MAX, hi_max = 0;
 #pragma unroll
-    for (int i = 0; i < kR; ++i) {
+    for (int i = 0; i < 2; ++i) {
       lo[i] = 0;
       hi[i] = INT_MAX;
-      if (g + 8 * i < nrows) {
-        seen_by(a, rows, rows.t0 + (r0 + g + 8 * i) / G, lo[i], hi[i], &g_err_kv8);
+      if (own(i) < nrows) {
+        seen_by(a, rows, rows.t0 + (r0 + own(i)) / G, lo[i], hi[i], &g_err_kv8);
         lo_min = min(lo_min, lo[i]);
         lo_max = max(lo_max, lo[i]);
         hi_min = min(hi_min, hi[i]);
@@ -217,7 +229,8 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       }
     }
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1) {
+    for (int o = 1; o < 32; o <<= 1) {
+      if (o >= kLane0 && o < kLane1) continue;
       lo_min = min(lo_min, __shfl_xor_sync(0xffffffffu, lo_min, o));
       lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
       hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
@@ -281,13 +294,11 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
     for (int i = 0; i < kSt - 1; ++i)
       if (issued < y1) issue();
     // ---- their query in fragments, while the first copies are under way
-    float mul[kR], m[kR], l[kR];
+    float mul[2], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
     uint32_t qa[kKs][2 * kR];
 #pragma unroll
     for (int i = 0; i < kR; ++i) {
       const int r = g + 8 * i;
-      m[i] = -INFINITY;
-      l[i] = 0.f;
       float v[D / 4];
 #pragma unroll
       for (int e = 0; e < D / 4; ++e) v[e] = 0.f;
@@ -317,18 +328,23 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       float f, undo;
       row_factor(top, f, undo);
-      mul[i] = undo * (a.softmax_scale * kLog2e);
+      if constexpr (kT) {
+        mul[0] = __shfl_sync(0xffffffffu, undo, 8 * q4) * (a.softmax_scale * kLog2e);
+        mul[1] = __shfl_sync(0xffffffffu, undo, 8 * q4 + 4) * (a.softmax_scale * kLog2e);
+      } else {
+        mul[i] = undo * (a.softmax_scale * kLog2e);
+      }
 #pragma unroll
       for (int j = 0; j < kKs; ++j) {
         qa[j][i] = f16x2(v[4 * j] * f, v[4 * j + 1] * f);
         qa[j][kR + i] = f16x2(v[4 * j + 2] * f, v[4 * j + 3] * f);
       }
     }
-    float o[kNt][2 * kR];
+    float o[kNt][4];
 #pragma unroll
     for (int n = 0; n < kNt; ++n)
 #pragma unroll
-      for (int e = 0; e < 2 * kR; ++e) o[n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
 
     for (int y = y0; y < y1; ++y) {
       __syncwarp();                      // every lane has read the stage that is filled next
@@ -349,12 +365,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
                                     __shfl_sync(0xffffffffu, old ? bv[0] : bv[1], (y - y0) & 31));
       const uint32_t kb = ring_s + st * kStage, vb = kb + kHalf * D;
       const bool border = token0 < lo_max || token0 + kHalf > hi_min;
-      // scores: four tiles of 8 tokens, this lane's tokens 8 n + 2 q4, + 1 in rows g, g + 8
-      float sx[4][2 * kR];
-#pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const int r = 8 * n + g;
-        uint32_t w[D / 16];
+      auto key = [&](int r, uint32_t* w) {                   // this lane's quarter of token r's key
         if constexpr (D == 128) {
           const uint4 w0 = lds128(kb + r * 128 + (((2 * q4) ^ (r & 7)) << 4));
           const uint4 w1 = lds128(kb + r * 128 + (((2 * q4 + 1) ^ (r & 7)) << 4));
@@ -364,55 +375,64 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
           const uint4 w0 = lds128(kb + r * 64 + ((q4 ^ (r >> 1 & 3)) << 4));
           w[0] = w0.x; w[1] = w0.y; w[2] = w0.z; w[3] = w0.w;
         }
+      };
+      // scores sx[i][..] of row own(i): tokens at(n)
+      constexpr int kN = kT ? 4 : 8;
+      float sx[2][kN];
+      auto at = [&](int n) { return kT ? 8 * n + g : 8 * (n >> 1) + 2 * q4 + (n & 1); };
+#pragma unroll
+      for (int n = 0; n < (kT ? 2 : 4); ++n) {
+        uint32_t w[D / 16];
         float d[4] = {0.f, 0.f, 0.f, 0.f};
+        if constexpr (kT) {
+          uint32_t w8[D / 16];
+          key(16 * n + g, w);
+          key(16 * n + 8 + g, w8);
 #pragma unroll
-        for (int j = 0; j < kKs; ++j) {
-          const uint32_t b0 = e4m3x2_lo_f16x2(w[j]), b1 = e4m3x2_hi_f16x2(w[j]);
-          if constexpr (kR == 2) mma_f16_16816(d, qa[j][0], qa[j][1], qa[j][2], qa[j][3], b0, b1);
-          else mma_f16_16816(d, qa[j][0], 0u, qa[j][1], 0u, b0, b1);
+          for (int j = 0; j < kKs; ++j)
+            mma_f16_16816(d, e4m3x2_lo_f16x2(w[j]), e4m3x2_lo_f16x2(w8[j]), e4m3x2_hi_f16x2(w[j]), e4m3x2_hi_f16x2(w8[j]),
+                          qa[j][0], qa[j][1]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sx[e & 1][2 * n + (e >> 1)] = d[e];
+        } else {
+          key(8 * n + g, w);
+#pragma unroll
+          for (int j = 0; j < kKs; ++j)
+            mma_f16_16816(d, qa[j][0], qa[j][1], qa[j][2 * kR - 2], qa[j][2 * kR - 1], e4m3x2_lo_f16x2(w[j]), e4m3x2_hi_f16x2(w[j]));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sx[e >> 1][2 * n + (e & 1)] = d[e];
         }
-#pragma unroll
-        for (int e = 0; e < 2 * kR; ++e) sx[n][e] = d[e];
       }
-      float alpha[kR];
+      float alpha[2];
 #pragma unroll
-      for (int i = 0; i < kR; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const float f = mul[i] * sc.x;
         float top = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kN; ++n) {
+          float v = sx[i][n] * f;
+          if (border) v = token0 + at(n) >= lo[i] && token0 + at(n) < hi[i] ? v : -INFINITY;
+          sx[i][n] = v;
+          top = fmaxf(top, v);
+        }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float v = sx[n][2 * i + e] * f;
-            if (border) {
-              const int token = token0 + 8 * n + 2 * q4 + e;
-              v = token >= lo[i] && token < hi[i] ? v : -INFINITY;
-            }
-            sx[n][2 * i + e] = v;
-            top = fmaxf(top, v);
-          }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        for (int e = kLane0; e < kLane1; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
         const float mn = fmaxf(m[i], top), z = mn == -INFINITY ? 0.f : mn;
         alpha[i] = ex2(m[i] - z);
         m[i] = mn;
         float sum = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            sx[n][2 * i + e] = ex2(sx[n][2 * i + e] - z);
-            sum += sx[n][2 * i + e];
-          }
+        for (int n = 0; n < kN; ++n) {
+          sx[i][n] = ex2(sx[i][n] - z);
+          sum += sx[i][n];
+        }
         l[i] = l[i] * alpha[i] + sum;
       }
-      bool rescale = alpha[0] != 1.f;
-      if constexpr (kR == 2) rescale |= alpha[1] != 1.f;
-      if (__any_sync(0xffffffffu, rescale)) {
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
         for (int n = 0; n < kNt; ++n)
 #pragma unroll
-          for (int e = 0; e < 2 * kR; ++e) o[n][e] *= alpha[e / 2];
+          for (int e = 0; e < 4; ++e) o[n][e] *= alpha[kT ? e & 1 : e >> 1];
       }
       // values: this lane's rows 16 kt + {2 q4, 2 q4 + 1, 8 + 2 q4, 9 + 2 q4}, channels D/8 * g ...
       constexpr int kVw = D / 32;        // words of a row a lane
@@ -430,17 +450,23 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
             vw[kt][e][0] = w.x; vw[kt][e][1] = w.y;
           }
         }
-      uint32_t pa[2][2 * kR];
+      // the weights of 16 tokens as a fragment: A of 16 rows, or, transposed, B of 8
+      uint32_t pa[2][kT ? 2 : 4];
 #pragma unroll
       for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-        for (int i = 0; i < kR; ++i) {
-          pa[kt][i] = f16x2(sx[2 * kt][2 * i], sx[2 * kt][2 * i + 1]);
-          pa[kt][kR + i] = f16x2(sx[2 * kt + 1][2 * i], sx[2 * kt + 1][2 * i + 1]);
+        for (int e = 0; e < 2; ++e) {
+          if constexpr (kT) {
+            pa[kt][e] = transpose8(f16x2(sx[0][2 * kt + e], sx[1][2 * kt + e]));
+          } else {
+            pa[kt][e] = f16x2(sx[e][4 * kt], sx[e][4 * kt + 1]);
+            pa[kt][2 + e] = f16x2(sx[e][4 * kt + 2], sx[e][4 * kt + 3]);
+          }
         }
-      auto product = [&](const uint32_t (&pw)[2][2 * kR], int w, float (&d)[4][4]) {
+      constexpr int kDt = kT ? 2 : 4;    // accumulators of a word's four channels
+      auto product = [&](const uint32_t (&pw)[2][kT ? 2 : 4], int w, float (&d)[kDt][4]) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kDt; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) d[n][e] = 0.f;
 #pragma unroll
@@ -451,12 +477,17 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
             b[e][0] = __byte_perm(vw[kt][2 * e][w], vw[kt][2 * e + 1][w], 0x5140);
             b[e][1] = __byte_perm(vw[kt][2 * e][w], vw[kt][2 * e + 1][w], 0x7362);
           }
+          if constexpr (kT) {
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            const uint32_t b0 = n & 1 ? e4m3x2_hi_f16x2(b[0][n >> 1]) : e4m3x2_lo_f16x2(b[0][n >> 1]);
-            const uint32_t b1 = n & 1 ? e4m3x2_hi_f16x2(b[1][n >> 1]) : e4m3x2_lo_f16x2(b[1][n >> 1]);
-            if constexpr (kR == 2) mma_f16_16816(d[n], pw[kt][0], pw[kt][1], pw[kt][2], pw[kt][3], b0, b1);
-            else mma_f16_16816(d[n], pw[kt][0], 0u, pw[kt][1], 0u, b0, b1);
+            for (int n = 0; n < 2; ++n)
+              mma_f16_16816(d[n], e4m3x2_lo_f16x2(b[0][n]), e4m3x2_hi_f16x2(b[0][n]), e4m3x2_lo_f16x2(b[1][n]),
+                            e4m3x2_hi_f16x2(b[1][n]), pw[kt][0], pw[kt][1]);
+          } else {
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+              mma_f16_16816(d[n % kDt], pw[kt][0], pw[kt][1], pw[kt][kT ? 0 : 2], pw[kt][kT ? 0 : 3],
+                            n & 1 ? e4m3x2_hi_f16x2(b[0][n >> 1]) : e4m3x2_lo_f16x2(b[0][n >> 1]),
+                            n & 1 ? e4m3x2_hi_f16x2(b[1][n >> 1]) : e4m3x2_lo_f16x2(b[1][n >> 1]));
           }
         }
       };
@@ -477,7 +508,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
             }
           }
         if (__any_sync(0xffffffffu, nan)) {
-          uint32_t keep[2][4][kVw], see[2][2 * kR];
+          uint32_t keep[2][4][kVw], see[2][kT ? 2 : 4];
 #pragma unroll
           for (int kt = 0; kt < 2; ++kt) {
 #pragma unroll
@@ -488,24 +519,26 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
                 keep[kt][e][w] = v & ~(at * 0xffu);
                 vw[kt][e][w] = at * 0x38u;                   // E4M3 of 1
               }
+            auto one = [&](int i, int n) { return token0 + at(n) >= lo[i] && token0 + at(n) < hi[i] ? 0x3c00u : 0u; };
 #pragma unroll
-            for (int i = 0; i < kR; ++i)
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int token = token0 + 16 * kt + 8 * half + 2 * q4;
-                see[kt][half * kR + i] = (token >= lo[i] && token < hi[i] ? 0x3c00u : 0u) |
-                                         (token + 1 >= lo[i] && token + 1 < hi[i] ? 0x3c000000u : 0u);
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (kT) {
+                see[kt][e] = transpose8(one(0, 2 * kt + e) | one(1, 2 * kt + e) << 16);
+              } else {
+                see[kt][e] = one(e, 4 * kt) | one(e, 4 * kt + 1) << 16;
+                see[kt][2 + e] = one(e, 4 * kt + 2) | one(e, 4 * kt + 3) << 16;
               }
+            }
           }
 #pragma unroll
           for (int w = 0; w < kVw; ++w) {
-            float d[4][4];
+            float d[kDt][4];
             product(see, w, d);
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+            for (int n = 0; n < kDt; ++n)
 #pragma unroll
-              for (int e = 0; e < 2 * kR; ++e)
-                if (d[n][e] != 0.f) o[4 * w + n][e] = NAN;
+              for (int e = 0; e < 4; ++e)
+                if (d[n][e] != 0.f) o[kDt * w + n][e] = NAN;
           }
 #pragma unroll
           for (int kt = 0; kt < 2; ++kt)
@@ -517,41 +550,44 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       }
 #pragma unroll
       for (int w = 0; w < kVw; ++w) {
-        float d[4][4];
+        float d[kDt][4];
         product(pa, w, d);
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < kDt; ++n)
 #pragma unroll
-          for (int e = 0; e < 2 * kR; ++e) o[4 * w + n][e] += d[n][e] * sc.y;
+          for (int e = 0; e < 4; ++e) o[kDt * w + n][e] += d[n][e] * sc.y;
       }
     }
     __syncwarp();                        // the stages are free for the next stream
     // ---- its result, or its part
 #pragma unroll
-    for (int i = 0; i < kR; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int r = g + 8 * i;
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int e = kLane0; e < kLane1; e <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], e);
+      const int r = own(i);
       if (r < nrows) {
-        float v[D / 4];                  // channels D/4 * q4 ...: of columns 2 q4 and 2 q4 + 1 of every tile
+        // a piece of the row's channels: an eighth, of lane g, or a quarter, of columns 2 q4 and 2 q4 + 1 of every tile
+        constexpr int kPiece = kT ? D / 8 : D / 4;
+        const int piece = kT ? g : q4;
+        float v[kPiece];
 #pragma unroll
         for (int n = 0; n < kNt; ++n) {
-          v[n] = o[n][2 * i];
-          v[kNt + n] = o[n][2 * i + 1];
+          v[kT ? 2 * n : n] = o[n][kT ? i : 2 * i];
+          v[kT ? 2 * n + 1 : kNt + n] = o[n][kT ? 2 + i : 2 * i + 1];
         }
         if (begins && ends) {
           const long long row = (long long)(rows.t0 + (r0 + r) / G) * a.Hq + h * G + (r0 + r) % G;
           const float inv = l[i] == 0.f ? 0.f : __fdiv_rn(1.f, l[i]);
 #pragma unroll
-          for (int e = 0; e < D / 4; ++e) v[e] *= inv;
-          store_row<D>(a, row, q4, v, p.aligned & 2);
-          if (q4 == 0 && a.lse) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
+          for (int e = 0; e < kPiece; ++e) v[e] *= inv;
+          store_piece<kPiece>(a, row * D + piece * kPiece, v, p.aligned & 2);
+          if (piece == 0 && a.lse) a.lse[row] = l[i] == 0.f ? -INFINITY : (m[i] + log2f(l[i])) * kLn2;
         } else {
-          const long long at = ((long long)span * 2 + (begins ? 1 : 0)) * p.most + r;
-          if (q4 == 0) p.ml[at] = make_float2(m[i], l[i]);
-          float4* dst = reinterpret_cast<float4*>(p.o + at * D + q4 * (D / 4));
+          const long long to = ((long long)span * 2 + (begins ? 1 : 0)) * p.most + r;
+          if (piece == 0) p.ml[to] = make_float2(m[i], l[i]);
+          float4* dst = reinterpret_cast<float4*>(p.o + to * D + piece * kPiece);
 #pragma unroll
-          for (int e = 0; e < D / 16; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          for (int e = 0; e < kPiece / 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
       }
     }
