@@ -21,7 +21,7 @@ constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
 constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a limit wakes late: 5 % at 4096 new tokens)
-constexpr int kOver = 8;                 // what beginning a stream costs, in steps
+constexpr int kOver = 12;                // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
 template <int D>
