@@ -715,7 +715,7 @@ cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t 
   p.a = a;
   p.G = a.Hq / a.cache.Hkv;
   const bool q16 = (((uintptr_t)a.q | (uintptr_t)(2 * a.q_stride_t) | (uintptr_t)(2 * a.q_stride_h)) & 15) == 0;
-  p.aligned = (q16 ? 1 : 0) | (((uintptr_t)a.out & 15) == 0 ? 2 : 0);
+  p.aligned = (q16 ? 1 : 0) | (((uintptr_t)a.out & 15) == 0 ? 2 : 0) | (((uintptr_t)a.out & 31) == 0 ? 4 : 0);
   p.spans = spans_of(a);
   p.most = most_of(a);
   const Layout at = layout_of(a);

@@ -103,7 +103,7 @@ struct Part {                            // a stream that begins in a span and d
 
 struct Kv8Params {
   csa2_kv8_attn_args a;
-  int G, aligned;                        // aligned: bit 0 q's rows, bit 1 out's rows on 16 bytes
+  int G, aligned;                        // aligned: bit 0 q's rows, bit 1 out's rows on 16 bytes, bit 2 on 32
   int spans, most;                       // most: rows of a part's place
   Part* part;                            // [spans]
   float2* ml;                            // [spans][2][most] maximum, sum; [1]: of the stream that goes on from here

@@ -94,6 +94,12 @@ __device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" :: "r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
+// A whole 32-byte sector of one thread's own row.
+__device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+
 __device__ __forceinline__ void named_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
@@ -547,63 +553,59 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       int lo = 0, hi = INT_MAX;
       const int tok = real ? t.rows.t0 + (t.r0 + row) / G : 0, hq = real ? w.h * G + (t.r0 + row) % G : 0;
       if (real) seen_by(a, t.rows, tok, lo, hi, &g_err_kv8_tile);
-      // the warp's rows of Q, two at a time: scaled by a power of two to below 2^8, as the sums of two E4M3 rows
+      // The warp's rows of Q, kRows at a time: scaled by a power of two to below 2^8, as the sums of two E4M3 rows.
+      // The next head's rows are asked for meanwhile.
       float mul = 0.f;
       {
-        constexpr int kLanes = D / 8, kRows = 32 / kLanes;   // lanes a row, rows at a time
-        const int sub = lane % kLanes;
+        constexpr int kLanes = D / 8, kRows = 32 / kLanes, kAhead = kM / 4 / kRows < 8 ? kM / 4 / kRows : 8;   // lanes a row, rows at a time, loads ahead
+        const int sub = lane % kLanes, ch = sub >> 1;
         const long long mine = real ? tok * a.q_stride_t + (long long)hq * a.q_stride_h : -1;
-        uint4 v[kM / 4 / kRows];
+#pragma unroll 1
+        for (int i0 = 0; i0 < kM / 4 / kRows; i0 += kAhead) {
+          uint4 v[kAhead];
 #pragma unroll
-        for (int i = 0; i < kM / 4 / kRows; ++i) {
-          const long long at = __shfl_sync(0xffffffffu, mine, i * kRows + lane / kLanes);
-          v[i] = make_uint4(0, 0, 0, 0);
-          if (at >= 0) {
-            const uint16_t* q = a.q + at + sub * 8;
-            if (p.aligned & 1) {
-              v[i] = *reinterpret_cast<const uint4*>(q);
-            } else {
-              v[i].x = q[0] | (uint32_t)q[1] << 16;
-              v[i].y = q[2] | (uint32_t)q[3] << 16;
-              v[i].z = q[4] | (uint32_t)q[5] << 16;
-              v[i].w = q[6] | (uint32_t)q[7] << 16;
-            }
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < kM / 4 / kRows; ++i) {
-          const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          float x[8], top = 0.f, f, undo;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[2 * e] = __uint_as_float(u[e] << 16);
-            x[2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-          }
-#pragma unroll
-          for (int e = 0; e < 8; ++e) top = fabsf(x[e]) >= top ? fabsf(x[e]) : x[e] != x[e] ? INFINITY : top;
-#pragma unroll
-          for (int o = 1; o < kLanes; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          row_factor(top, f, undo);
-          f *= 0.0078125f;
-          const float back = __shfl_sync(0xffffffffu, undo * 128.f * (a.softmax_scale * kLog2e), lane % kRows * kLanes);
-          if (lane % (kM / 4) / kRows == i) mul = back;
-          if (!SPLIT || grp == 0) {
-            const bool bad = top == INFINITY;                // an infinity makes its row NaN, as a NaN does
-            uint2 hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu), lo8 = hi8;
-            if (!bad) {
-              uint32_t h4[4], l4[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float x0 = x[2 * e] * f, x1 = x[2 * e + 1] * f;
-                h4[e] = cvt_e4m3x2(x0, x1);
-                const uint32_t first = e4m3x2_to_f16x2((uint16_t)h4[e]);
-                const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&first));
-                l4[e] = cvt_e4m3x2(x0 - y.x, x1 - y.y);
+          for (int i = 0; i < kAhead; ++i) {
+            const long long at = __shfl_sync(0xffffffffu, mine, (i0 + i) * kRows + lane / kLanes);
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (at >= 0) {
+              const uint16_t* q = a.q + at + sub * 8;
+              if (p.aligned & 1) {
+                v[i] = *reinterpret_cast<const uint4*>(q);
+              } else {
+                v[i].x = q[0] | (uint32_t)q[1] << 16;
+                v[i].y = q[2] | (uint32_t)q[3] << 16;
+                v[i].z = q[4] | (uint32_t)q[5] << 16;
+                v[i].w = q[6] | (uint32_t)q[7] << 16;
               }
-              hi8 = make_uint2(h4[0] | h4[1] << 16, h4[2] | h4[3] << 16);
-              lo8 = make_uint2(l4[0] | l4[1] << 16, l4[2] | l4[3] << 16);
             }
-            const int qr = (warp & 3) * (kM / 4) + i * kRows + lane / kLanes, ch = sub >> 1;
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            // the largest magnitude, as bits: infinities and NaNs are above all others
+            uint32_t big = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) big = max(big, max(u[e] << 16 & 0x7fffffffu, u[e] & 0x7fff0000u));
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
+            float f, undo;
+            row_factor(__uint_as_float(big), f, undo);
+            f *= 0.0078125f;
+            const float back = __shfl_sync(0xffffffffu, undo * 128.f * (a.softmax_scale * kLog2e), lane % kRows * kLanes);
+            if (lane % (kM / 4) / kRows == i0 + i) mul = back;
+            if (SPLIT && grp == 1) continue;
+            uint32_t h4[4], l4[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 y = mul2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)), make_float2(f, f));
+              h4[e] = cvt_e4m3x2(y.x, y.y);
+              const uint32_t first = e4m3x2_to_f16x2((uint16_t)h4[e]);
+              const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&first));
+              l4[e] = cvt_e4m3x2(y.x - z.x, y.y - z.y);
+            }
+            uint2 hi8 = make_uint2(h4[0] | h4[1] << 16, h4[2] | h4[3] << 16), lo8 = make_uint2(l4[0] | l4[1] << 16, l4[2] | l4[3] << 16);
+            if (big >= 0x7f800000u) hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // an infinity makes its row NaN, as a NaN does
+            const int qr = (warp & 3) * (kM / 4) + (i0 + i) * kRows + lane / kLanes;
             const uint32_t at = base + (SPLIT ? 0 : grp * L::kQ) + qr * D +
                                 ((D == 128 ? ch ^ (qr & 7) : ch ^ (qr >> 1 & 3)) << 4) + (sub & 1) * 8;
             sts64(at, hi8);
@@ -615,6 +617,11 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           tc::fence_before_sync();       // the last segment's TMEM reads
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&m.q_full);
+        }
+        if (mine >= 0 && w.h + 1 < c.Hkv) {
+          const uint16_t* q = a.q + mine + G * a.q_stride_h;
+#pragma unroll
+          for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + i));
         }
       }
       float top = -INFINITY, l = 0.f;
@@ -775,14 +782,14 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
               if (bits >> d & 1) v[d] = NAN;
           }
           if (!whole) {
-            float4* dst = reinterpret_cast<float4*>(p.o + at * D + i);
+            float* dst = p.o + at * D + i;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 32; e += 8) stg256(dst + e, reinterpret_cast<const uint32_t*>(v + e));
           } else if (a.out_dtype == CSA2_F32) {
             float* dst = reinterpret_cast<float*>(a.out) + out_row * D + i;
-            if (p.aligned & 2) {
+            if (p.aligned & 4) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) reinterpret_cast<float4*>(dst)[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+              for (int e = 0; e < 32; e += 8) stg256(dst + e, reinterpret_cast<const uint32_t*>(v + e));
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) dst[e] = v[e];
@@ -792,9 +799,9 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
             uint32_t o[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) o[e] = bf16x2(v[2 * e], v[2 * e + 1]);
-            if (p.aligned & 2) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) reinterpret_cast<uint4*>(dst)[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            if (p.aligned & 4) {
+              stg256(dst, o);
+              stg256(dst + 16, o + 8);
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) dst[e] = (uint16_t)(o[e / 2] >> 16 * (e & 1));
