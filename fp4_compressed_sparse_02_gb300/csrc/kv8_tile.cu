@@ -579,32 +579,43 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
               }
             }
           }
+          // the largest magnitudes, as bits: infinities and NaNs are above all others; all rows' together, a step at a time
+          uint32_t big[kAhead];
+          float f[kAhead];
 #pragma unroll
           for (int i = 0; i < kAhead; ++i) {
             const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            // the largest magnitude, as bits: infinities and NaNs are above all others
-            uint32_t big = 0;
+            big[i] = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) big = max(big, max(u[e] << 16 & 0x7fffffffu, u[e] & 0x7fff0000u));
+            for (int e = 0; e < 4; ++e) big[i] = max(big[i], max(u[e] << 16 & 0x7fffffffu, u[e] & 0x7fff0000u));
+          }
 #pragma unroll
-            for (int o = 1; o < kLanes; o <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, o));
-            float f, undo;
-            row_factor(__uint_as_float(big), f, undo);
-            f *= 0.0078125f;
+          for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) big[i] = max(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            float undo;
+            row_factor(__uint_as_float(big[i]), f[i], undo);
+            f[i] *= 0.0078125f;
             const float back = __shfl_sync(0xffffffffu, undo * 128.f * (a.softmax_scale * kLog2e), lane % kRows * kLanes);
             if (lane % (kM / 4) / kRows == i0 + i) mul = back;
+          }
+#pragma unroll
+          for (int i = 0; i < kAhead; ++i) {
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
             if (SPLIT && grp == 1) continue;
             uint32_t h4[4], l4[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float2 y = mul2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)), make_float2(f, f));
+              const float2 y = mul2(make_float2(__uint_as_float(u[e] << 16), __uint_as_float(u[e] & 0xffff0000u)), make_float2(f[i], f[i]));
               h4[e] = cvt_e4m3x2(y.x, y.y);
               const uint32_t first = e4m3x2_to_f16x2((uint16_t)h4[e]);
               const float2 z = __half22float2(*reinterpret_cast<const __half2*>(&first));
               l4[e] = cvt_e4m3x2(y.x - z.x, y.y - z.y);
             }
             uint2 hi8 = make_uint2(h4[0] | h4[1] << 16, h4[2] | h4[3] << 16), lo8 = make_uint2(l4[0] | l4[1] << 16, l4[2] | l4[3] << 16);
-            if (big >= 0x7f800000u) hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // an infinity makes its row NaN, as a NaN does
+            if (big[i] >= 0x7f800000u) hi8 = make_uint2(0x7f7f7f7fu, 0x7f7f7f7fu);   // an infinity makes its row NaN, as a NaN does
             const int qr = (warp & 3) * (kM / 4) + (i0 + i) * kRows + lane / kLanes;
             const uint32_t at = base + (SPLIT ? 0 : grp * L::kQ) + qr * D +
                                 ((D == 128 ? ch ^ (qr & 7) : ch ^ (qr >> 1 & 3)) << 4) + (sub & 1) * 8;
