@@ -142,16 +142,20 @@ class PagedCache:
 
 
 class Workspace:
-    """Grow-only device scratch buffer handed to the library calls."""
+    """Grow-only device scratch buffer handed to the library calls.  Calls that may run at the same time (on two
+    streams, or in two graphs that are replayed side by side) need one each."""
 
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
+        self.outgrown = []                 # a captured graph may hold their addresses
 
     def get(self, nbytes):
         if self.buf.numel() < nbytes:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("workspace must be sized before CUDA graph capture")
+            if self.buf.numel():
+                self.outgrown.append(self.buf)
             self.buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -666,32 +670,38 @@ class Kv8Cache:
 
 _KV8_TYPES = (torch.uint8, torch.uint8, torch.float32, torch.float32, torch.int8, torch.float32, torch.int32)
 _KV8_NAMES = ("k plane", "v plane", "k_scale", "v_scale", "mean", "mean_scale", "page_table")
-_ws_of = {}                                # the default workspaces by device number
+_ws_of = {}                                # the default workspaces by device number and stream
 
 
 def _launch_ws(fn, packed, ws, device, dev):
-    """_launch of a call that takes a workspace.  It is offered the one there is, and asked what it needs only if that is
-    too small."""
+    """_launch of a call that takes a workspace (ws None: the stream's own, or, in a capture, the graph's).  It is offered
+    the one there is, and asked what it needs only if that is too small."""
     if dev < 0:
         raise ValueError("expected CUDA tensors")
     if not _is_current(dev):
         with torch.cuda.device(dev):
             return _launch_ws(fn, packed, ws, device, dev)
     L = _lib.lib()
+    stream, call = _stream(dev), getattr(L, fn)
+    need = ctypes.c_size_t(0)
+    if ws is None and torch.cuda.is_current_stream_capturing():
+        # memory of the graph's own: graphs share no workspace, and none with eager calls
+        _lib.check(getattr(L, fn + "_workspace")(packed, ctypes.byref(need)))
+        buf = torch.empty(need.value, dtype=torch.uint8, device=device)
+        _lib.check(call(packed, buf.data_ptr(), need.value, stream))
+        return
     if ws is None:
-        ws = _ws_of.get(dev)
+        ws = _ws_of.get((dev, stream))
         if ws is None:
-            ws = _ws_of[dev] = _ws(None, device)
+            ws = _ws_of[dev, stream] = Workspace(device)
     buf = ws.get(0)
     if buf.get_device() != dev:
         _on_device(buf, dev, "ws")
-    call = getattr(L, fn)
-    status = call(packed, buf.data_ptr(), buf.numel(), _stream(dev))
+    status = call(packed, buf.data_ptr(), buf.numel(), stream)
     if status == _TOO_SMALL:
-        need = ctypes.c_size_t(0)
         _lib.check(getattr(L, fn + "_workspace")(packed, ctypes.byref(need)))
         buf = ws.get(need.value)
-        status = call(packed, buf.data_ptr(), need.value, _stream(dev))
+        status = call(packed, buf.data_ptr(), need.value, stream)
     if status:
         _lib.check(status)
 

@@ -2,7 +2,7 @@
 //
 // S = Q K^T and O += P V with float32 accumulators in TMEM, 128 tokens a step.  The keys' bytes are the operand as
 // they come from memory: Q, scaled by a power of two, is the sum of two E4M3 values, exactly for every bf16 within 2^-9
-// of its row's largest and to 2^-18 of the largest below that.  P is fp16, and the values' bytes become
+// of its row's largest and to 2^-17 of the largest below that.  P is fp16, and the values' bytes become
 // fp16 (exact) once a step, by warps of their own.  Two groups of rows take turns: one's softmax runs
 // under the other's products.
 #include "kv8_attn.cuh"

@@ -755,11 +755,13 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * An empty `seen` gives out = 0 and lse = -inf.  `pages` entries below 0 are skipped, in any order;
  * a page listed twice counts twice; one past the page table sets CSA2_DEVERR_PAGE_SLOT.
  * max_new: about how many new tokens the longest of the call's sequences has.  It only
- * picks the kernel: results for any value stay within the precision below.
- * Precision: products on fp16 tensor-core operands with float32 accumulation.  Keys and
- * values are exact there; each head's q is scaled by a power of two (exact within 2^-28 of its
- * largest element); probabilities are fp16 (2^-12 relative).  A NaN that a row does not see does
- * not reach it.
+ * picks the kernel, by max_new * G rows: results for any value stay within the precision below.
+ * Precision: products on tensor-core operands with float32 accumulation.  Keys and values are
+ * exact there, probabilities fp16 (2^-11 relative, 2^-25 of the largest).  Up to 16 rows each head's q
+ * is fp16 times a power of two, exact within 2^-28 of its largest element.  Above, it is the sum of two
+ * E4M3 numbers times a power of two, exact within 2^-9 of its largest element and to 2^-17 of that
+ * below; and the values of a page whose scale is below 2^-22 of the largest value scale in sight
+ * lose their last bits.  A NaN that a row does not see does not reach it.  Results repeat bit for bit.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
  * window >= 0; S <= 2^18; T * Hq < 2^31.
  * -------------------------------------------------------------------------- */
@@ -784,6 +786,7 @@ typedef struct csa2_kv8_attn_args {
   float* lse;                  /* device f32 [T][Hq], or NULL */
 } csa2_kv8_attn_args;
 
+/* The workspace takes 5 to 40 MB, whatever the sizes.  out and lse must not overlap the inputs. */
 csa2_status csa2_kv8_attn(const csa2_kv8_attn_args* args, void* workspace, size_t workspace_bytes,
                           void* stream);
 csa2_status csa2_kv8_attn_workspace(const csa2_kv8_attn_args* args, size_t* bytes);

@@ -64,10 +64,11 @@ def strided(a, dtype, pad):
     return t[:, pad:pad + H * D].unflatten(1, (H, D))
 
 
-def check_attn(out, lse, c, q, start, length, scale, window=0, pages=None, out_eps=2.0 ** -8):
+def check_attn(out, lse, c, q, start, length, scale, window=0, pages=None, out_eps=2.0 ** -8, q_eps=0.0):
     """Every row of the step against the oracle.  The bound, from the precision that the header states: probabilities
     in fp16 (2^-11, or 2^-25 absolute), logits in float32 sums of D terms (D + 8 roundings, twice: numerator and
-    sum), 2^-14 for the exponential, the sums over up to 2^10 pages and their merging, one rounding of the result."""
+    sum), 2^-14 for the exponential, the sums over up to 2^10 pages and their merging, one rounding of the result.
+    q_eps: how far an element of q may be off, relative to the row's largest."""
     out, lse = out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
     H, D = c["k"].shape[1], c["k"].shape[3]
     Hq = q.shape[1]
@@ -83,6 +84,8 @@ def check_attn(out, lse, c, q, start, length, scale, window=0, pages=None, out_e
                 for g in range(h * G, (h + 1) * G):
                     o, l, (a, sv, x) = kv8.attend(q[t, g].astype(np.float64), k, v, seen, scale)
                     e = (D + 8) * 2.0 ** -24 * x
+                    if q_eps and seen.any():
+                        e += q_eps * np.abs(q[t, g]).max() * np.abs(k[seen]).sum(1).max() * scale
                     if not seen.any():
                         assert (out[t, g] == 0).all() and lse[t, g] == -np.inf, (s, t, g)
                         continue

@@ -267,7 +267,7 @@ def test_select_length_beyond_its_bound_raises():
 
 # ---- kv8_attn -------------------------------------------------------------------------------------
 
-def run_attn(c, g, q, start, length, pad=0, dtype=torch.bfloat16, pages=None, window=0, scale=None, check=True, **kw):
+def run_attn(c, g, q, start, length, pad=0, dtype=torch.bfloat16, pages=None, window=0, scale=None, check=True, q_eps=0.0, **kw):
     T, Hq, D = q.shape
     out = torch.full((T, Hq, D), 777.0, dtype=dtype, device=DEV)
     lse = torch.full((T, Hq), 777.0, device=DEV)
@@ -277,7 +277,7 @@ def run_attn(c, g, q, start, length, pad=0, dtype=torch.bfloat16, pages=None, wi
     rest = [*range(start[0]), *range(start[-1], T)]
     assert (out[rest] == 777).all() and (lse[rest] == 777).all()
     if check:
-        check_attn(out, lse, c, q, start, length, scale or D ** -0.5, window, pages, 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -8)
+        check_attn(out, lse, c, q, start, length, scale or D ** -0.5, window, pages, 2.0 ** -24 if dtype is torch.float32 else 2.0 ** -8, q_eps)
     return out, lse
 
 
@@ -285,7 +285,7 @@ STEPS = {"token": ([1, 63, 64, 65, 700, 129], [1, 1, 1, 1, 1, 1]), "idle": ([300
          "verify": ([6, 70, 200, 128], [6, 3, 1, 5]), "chunk": ([40, 333, 130], [40, 37, 0]), "one": ([1000], [1])}
 
 
-@pytest.mark.parametrize("hint", [1, 8, 100])
+@pytest.mark.parametrize("hint", [1, 8, 20, 100])
 @pytest.mark.parametrize("H,G,D", [(2, 8, 128), (1, 1, 64), (3, 7, 64), (1, 16, 128), (2, 5, 128), (1, 20, 64), (1, 64, 128)])
 @pytest.mark.parametrize("step", STEPS)
 def test_attn(step, H, G, D, hint):
@@ -298,7 +298,7 @@ def test_attn(step, H, G, D, hint):
              max_new=hint)
 
 
-@pytest.mark.parametrize("hint", [1, 8, 100])
+@pytest.mark.parametrize("hint", [1, 8, 20, 100])
 @pytest.mark.parametrize("window", [1, 2, 63, 64, 65, 200, 100000])
 def test_attn_window(window, hint):
     r = np.random.default_rng(window)
@@ -328,7 +328,7 @@ def test_attn_listed_pages(H, G, D, n):
     run_attn(c, to_gpu(c), q, starts(add), length, pages=pages, window=100)
 
 
-@pytest.mark.parametrize("hint", [1, 100])
+@pytest.mark.parametrize("hint", [1, 3, 20, 40, 100])
 def test_attn_nan_in_masked_places(hint):
     """A NaN key or value of the newest token reaches that token's row alone."""
     r = np.random.default_rng(11)
@@ -343,7 +343,7 @@ def test_attn_nan_in_masked_places(hint):
     run_attn(c, to_gpu(c), q, starts(add), length, max_new=hint)
 
 
-@pytest.mark.parametrize("hint", [1, 100])
+@pytest.mark.parametrize("hint", [1, 2, 8, 16, 100])
 def test_attn_scales_far_apart(hint):
     """Pages whose key and value scales differ by 2^12, queries of other magnitudes, equal keys."""
     r = np.random.default_rng(12)
@@ -355,6 +355,171 @@ def test_attn_scales_far_apart(hint):
     q = bf16(r.standard_normal((36, 8, 128)) * np.exp2(r.integers(-20, 4, (36, 8, 1))))
     q[0, 0] = 0
     run_attn(c, to_gpu(c), q, starts(add), length, max_new=hint, dtype=torch.float32)
+
+
+@pytest.mark.parametrize("hint", [1, 2, 8, 16, 100])
+def test_attn_queries_of_wide_range(hint):
+    """Rows whose elements span 2^24, keys alike: every element counts.  Above 16 rows an element is off by at most 2^-17 of
+    its row's largest."""
+    r = np.random.default_rng(15)
+    length, add = [200, 300], [3, 20]
+    c = new_cache(r, 2, 5, 1, 128)
+    fill(r, c, length)
+    q = bf16(r.standard_normal((23, 8, 128)) * np.exp2(r.integers(-24, 1, (23, 8, 128))))
+    q[0, 1] = 0
+    q[1, 2, :100] = 0
+    run_attn(c, to_gpu(c), q, starts(add), length, max_new=hint, dtype=torch.float32, q_eps=2.0 ** -17 if hint * 8 > 16 else 0.0)
+
+
+@pytest.mark.parametrize("hint", [1, 3, 20, 100])
+def test_attn_infinite_queries_reach_their_own_rows_alone(hint):
+    r = np.random.default_rng(16)
+    length, add = [150, 70], [4, 9]
+    c = new_cache(r, 2, 3, 1, 64)
+    fill(r, c, length)
+    q = bf16(r.standard_normal((13, 6, 64)))
+    g = to_gpu(c)
+    want, _ = run_attn(c, g, q, starts(add), length, max_new=hint)
+    q[2, 3, 5], q[7, 0, 1], q[9, 5, 63] = np.inf, np.nan, -np.inf
+    out, lse = run_attn(c, g, q, starts(add), length, max_new=hint, check=False)
+    bad = torch.zeros((13, 6), dtype=torch.bool, device=DEV)
+    bad[2, 3] = bad[7, 0] = bad[9, 5] = True
+    assert (out[~bad] == want[~bad]).all() and out[bad].isnan().all()
+
+
+@pytest.mark.parametrize("hint", [1, 2, 8, 100])
+@pytest.mark.parametrize("S", [33, 70, 2100])
+def test_attn_many_sequences(S, hint):
+    """More sequences than a warp looks at in one go, and more than the plan of the large tiles copies."""
+    r = np.random.default_rng(S)
+    length = r.integers(0, 100, S)
+    add = np.minimum(length, r.integers(0, 3, S))
+    c = new_cache(r, S, 2, 1, 64, spare=1)
+    fill(r, c, length, spread=1)
+    q = bf16(r.standard_normal((int(add.sum()), 4, 64)))
+    run_attn(c, to_gpu(c), q, starts(add), length, max_new=hint)
+
+
+@pytest.mark.parametrize("hint", [1, 100])
+def test_attn_one_long_sequence(hint):
+    """Many spans of one stream, and the same bits on a repeated call, on another stream and with a workspace of its own."""
+    r = np.random.default_rng(17)
+    n = 64 * 150 - 9
+    c = new_cache(r, 1, 150, 1, 128, spare=0)
+    fill(r, c, [n])
+    g = to_gpu(c)
+    q = bf16(r.standard_normal((3, 8, 128)))
+    out, lse = run_attn(c, g, q, starts([3]), [n], max_new=hint)
+    for _ in range(2):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            a, b = run_attn(c, g, q, starts([3]), [n], max_new=hint, ws=csa2.Workspace(DEV), check=False)
+            torch.cuda.current_stream().synchronize()
+        assert (a == out).all() and (b == lse).all()
+
+
+def test_calls_on_two_streams_at_once():
+    """Default workspaces belong to a stream: interleaved calls do not disturb each other."""
+    r = np.random.default_rng(18)
+    sets = []
+    for n in (3000, 5000):
+        c = new_cache(r, 1, 90, 2, 64, spare=0)
+        fill(r, c, [n])
+        q = bf16(r.standard_normal((2, 16, 64)))
+        sets.append((to_gpu(c), gpu(q, torch.bfloat16), gpu(starts([2])), gpu(np.array([n], np.int32)), torch.cuda.Stream()))
+    alone = []
+    for g, q, start, length, _ in sets:
+        pages, _ = csa2.kv8_select(g, q, start, length, 9)
+        alone.append((pages, *csa2.kv8_attn(g, q, start, length, max_new=1), *csa2.kv8_attn(g, q, start, length, pages=pages)))
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, (g, q, start, length, stream) in enumerate(sets):
+            with torch.cuda.stream(stream):
+                pages, _ = csa2.kv8_select(g, q, start, length, 9)
+                got[i].append((pages, *csa2.kv8_attn(g, q, start, length, max_new=1), *csa2.kv8_attn(g, q, start, length, pages=pages)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all((a == b).all() for run in got[i] for a, b in zip(run, alone[i]))
+    graphs, held = [], []
+    for g, q, start, length, _ in sets:                      # and so do graphs that are replayed side by side
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            pages, _ = csa2.kv8_select(g, q, start, length, 9)
+            held.append((pages, *csa2.kv8_attn(g, q, start, length, max_new=1), *csa2.kv8_attn(g, q, start, length, pages=pages)))
+    for _ in range(20):
+        for i in range(2):
+            with torch.cuda.stream(sets[i][4]):
+                graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all((a == b).all() for a, b in zip(held[i], alone[i]))
+
+
+def test_a_graph_outlives_its_workspace_growing():
+    """A workspace grows after a capture that used it: the graph still writes into memory of its own."""
+    r = np.random.default_rng(19)
+    c = new_cache(r, 1, 40, 1, 64, spare=0)
+    fill(r, c, [2500])
+    g = to_gpu(c)
+    q = gpu(bf16(r.standard_normal((1, 8, 64))), torch.bfloat16)
+    args = (g, q, gpu(starts([1])), gpu(np.array([2500], np.int32)))
+    stream, ws = torch.cuda.Stream(), csa2.Workspace(DEV)
+    with torch.cuda.stream(stream):
+        want, _ = csa2.kv8_attn(*args, max_new=1, ws=ws)
+        out = torch.zeros_like(want)
+        stream.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            csa2.kv8_attn(*args, max_new=1, out=out, ws=ws)
+        csa2.kv8_attn(*args, max_new=100, ws=ws)             # needs more
+        other = [torch.full((1 << 20,), 7, dtype=torch.uint8, device=DEV) for _ in range(64)]
+        graph.replay()
+        stream.synchronize()
+    assert (out == want).all() and all((x == 7).all() for x in other)
+
+
+def test_pages_beyond_32_bits():
+    """Planes of 2.6 GB: the last pages, appended to, selected and attended to."""
+    r = np.random.default_rng(20)
+    H, D, P = 2, 128, 160000
+    c = new_cache(r, 1, 12, H, D, spare=0)
+    new = lambda dtype, *s: torch.empty((P, H) + s, dtype=dtype, device=DEV)
+    far = c["table"].max() + 1
+    table = gpu((c["table"] + (P - far)).astype(np.int32))
+    g = csa2.Kv8Cache(new(torch.uint8, 64, D), new(torch.uint8, 64, D), new(torch.float32), new(torch.float32), table,
+                      new(torch.int8, D), new(torch.float32))
+    n = 12 * 64 - 5
+    x = [bf16(r.standard_normal((n, H, D))) for _ in range(2)]
+    kv8.append(c, x[0], x[1], starts([n]), [n])
+    csa2.kv8_append(g, gpu(x[0], torch.bfloat16), gpu(x[1], torch.bfloat16), gpu(starts([n])), gpu(np.array([n], np.int32)))
+    tail = csa2.Kv8Cache(*(getattr(g, f)[P - far:] for f in ("k", "v", "k_scale", "v_scale")), gpu(c["table"]), g.mean[P - far:], g.mean_scale[P - far:])
+    ids = c["table"][0]
+    for f in ("k", "v", "k_scale", "v_scale"):
+        got, want = getattr(tail, f).cpu().numpy()[ids[:-1]], c[f][ids[:-1]]
+        assert (got == want).all(), f
+    q = bf16(r.standard_normal((2, 8, D)))
+    pages = run_select(c, g, q, starts([2]), [n], 5)
+    run_attn(c, g, q, starts([2]), [n], pages=pages.cpu().numpy())
+    for hint in (1, 100):
+        run_attn(c, g, q, starts([2]), [n], max_new=hint)
+
+
+def test_empty_calls():
+    r = np.random.default_rng(22)
+    c = new_cache(r, 2, 2, 1, 64)
+    fill(r, c, [70, 3])
+    g = to_gpu(c)
+    z = lambda *s: torch.empty(s, dtype=torch.bfloat16, device=DEV)
+    start, length = gpu(starts([0, 0])), gpu(np.array([70, 3], np.int32))
+    csa2.kv8_append(g, z(0, 1, 64), z(0, 1, 64), start, length)
+    assert csa2.kv8_select(g, z(0, 2, 64), start, length, 4)[0].shape == (0, 1, 4)
+    assert csa2.kv8_attn(g, z(0, 2, 64), start, length)[0].shape == (0, 2, 64)
+    csa2.kv8_append(g, z(5, 1, 64), z(5, 1, 64), start, length)        # rows of padding alone
+    check_cache(g, c)
+    run_attn(c, g, np.ones((5, 2, 64), np.float32), starts([0, 0]), [70, 3])
+    none = torch.empty(0, dtype=I32, device=DEV)
+    p = csa2.page_plan(none, none, torch.empty((0, 4), dtype=I32, device=DEV), none, gpu(np.zeros(1, np.int32)), 3)
+    assert p.start.tolist() == [0] and p.seq.tolist() == p.slot.tolist() == [-1] * 3 and p.head.tolist() == [0]
 
 
 def test_attn_bad_pages_raises():
@@ -410,7 +575,6 @@ def test_steps_of_a_server():
                        sparse=csa2.kv8_attn(g, x[0], p.start, p.length, pages=pages), pages=pages)
 
         st["add"].zero_()
-        step()                                               # nothing to add: sizes the workspace
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
             step()
