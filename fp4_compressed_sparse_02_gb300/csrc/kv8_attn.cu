@@ -25,6 +25,12 @@ namespace {
 // fragments share), its V fragment the bytes of two neighbouring tokens interleaved; at 16 rows the scores'
 // accumulators are the weights' A fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
 // its partial output, in float32.
+//
+// Bound by memory where a batch has the bytes (64 sequences of up to 64K tokens, 8 x 128 channels: 4.2 GB in 625-645 us,
+// 0.96-0.98 of the copy rate); by a warp's own chain of products and conversions, two warps a scheduler, where pages come
+// from L2 (2048 rows of 32 listed pages each: 1.02 ms for 8.6 GB); by two launches and four dependent loads where
+// there is little (one row over 4097 tokens: 10 + 6 us).  Left out: three CTAs an SM (below); kLeast of 1 to 8 is all
+// the same at one row.
 constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
 
 // Two CTAs an SM.  Three, at 168 registers a thread and two stages a warp, are slower (64 sequences up to 64K: 726 us
@@ -597,11 +603,12 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
   if (lane == 0) p.part[span] = part;
 }
 
+// Rows lie apart in the workspace, so eight loads a lane are under way at once; 6 us at 33 parts of 8 rows.
 // A CTA (span, eight rows): the stream that begins there and goes on in the next ones, a warp a row, a lane
 // D / 32 channels.
 template <int D>
 __global__ void __launch_bounds__(256, 2) k_kv8_join(const Kv8Params p) {
-  constexpr int kPer = D / 32, kAhead = 16;
+  constexpr int kPer = D / 32, kAhead = 8;
   const csa2_kv8_attn_args& a = p.a;
   pdl_wait();
   pdl_trigger();
@@ -691,7 +698,9 @@ cudaError_t launch_rows(const Kv8Params& p, cudaStream_t st) {
   return p.a.pages ? launch_stream<D, 16, true>(mk, mv, p, st) : launch_stream<D, 16, false>(mk, mv, p, st);
 }
 
-// Rows of a sequence and key head from which the tiles of 128 rows take over from the streams of 16.
+// Rows of a sequence and key head from which tiles take over from the streams of 16: those would read the pages once for
+// every 16 rows.  32 sequences of 24K tokens, 8 key heads: 16 rows 269 us as a stream and 332 as tiles of 64, 24 rows 510
+// and 334; 64 rows 998 and 340.
 bool takes_tiles(const csa2_kv8_attn_args& a) {
   return !a.pages && (long long)a.max_new * (a.Hq / a.cache.Hkv) > 16;
 }
@@ -699,7 +708,7 @@ bool takes_tiles(const csa2_kv8_attn_args& a) {
 int spans_of(const csa2_kv8_attn_args& a) {
   return takes_tiles(a) ? kTileSpans : kSpans;
 }
-int most_of(const csa2_kv8_attn_args& a) { return takes_tiles(a) ? kTileRows : takes_eight(a) ? 8 : 16; }
+int most_of(const csa2_kv8_attn_args& a) { return takes_tiles(a) ? tile_rows(a) : takes_eight(a) ? 8 : 16; }
 Layout layout_of(const csa2_kv8_attn_args& a) { return Layout(spans_of(a), most_of(a), a.cache.D); }
 
 }  // namespace

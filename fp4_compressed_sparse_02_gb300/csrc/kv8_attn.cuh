@@ -123,7 +123,12 @@ inline bool plane_map(CUtensorMap* map, const void* base, const csa2_kv8_cache& 
 }
 
 // kv8_tile.cu
-constexpr int kTileSpans = 152, kTileRows = 256;
+constexpr int kTileSpans = 152;
+// Rows of its tiles: a sequence's rows of a key head, if they fit.
+inline int tile_rows(const csa2_kv8_attn_args& a) {
+  const long long rows = (long long)a.max_new * (a.Hq / a.cache.Hkv);
+  return rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+}
 cudaError_t launch_kv8_tile(const Kv8Params& p, cudaStream_t st);
 uint32_t read_clear_error_kv8_tile();
 

@@ -30,6 +30,8 @@ Parity status per function (pins live in tests/test_oracle_*.py):
   compress.*           pinned (closed forms: m=1, constant Z, RoPE identities)
   indexer.*            pinned (counting definition of top-k, pool invariants)
   attention.*          pinned (dense equality, closed forms, permutation)
+  kv8.*                pinned (scale borders, exactness of sums, closed forms; the layers beside
+                       CSA2, which the sources do not describe)
   The scoring formula, RoPE layout and softmax scale are readings; the oracle is
   pinned to those readings, not to any number the pages print (none exists).
 """
