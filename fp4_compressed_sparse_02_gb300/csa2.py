@@ -148,14 +148,18 @@ class Workspace:
     def __init__(self, device="cuda"):
         self.device = device
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
-        self.outgrown = []                 # a captured graph may hold their addresses
+        self.captured = False              # a graph holds its address
+        self.outgrown = []                 # buffers whose addresses graphs hold
 
     def get(self, nbytes):
-        if self.buf.numel() < nbytes:
-            if torch.cuda.is_current_stream_capturing():
+        if torch.cuda.is_current_stream_capturing():
+            if self.buf.numel() < nbytes:
                 raise RuntimeError("workspace must be sized before CUDA graph capture")
-            if self.buf.numel():
+            self.captured = True
+        elif self.buf.numel() < nbytes:
+            if self.captured:
                 self.outgrown.append(self.buf)
+                self.captured = False
             self.buf = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=self.device)
         return self.buf
 
@@ -827,7 +831,7 @@ def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, win
              out_dtype=torch.bfloat16, out=None, lse=None, ws=None):
     """Causal attention of the new tokens q bf16 [T, Hq, D] (tokens and heads may be strided) over the cache, which
     holds their keys and values already; start, length as in kv8_append.  max_new: about how many new
-    tokens a sequence has at most (picks the kernel; by default T).  pages int32 [T, Hkv, n]: only these pages
+    tokens a sequence has at most (picks the kernel; by default T - S + 1, which one has if all have some).  pages int32 [T, Hkv, n]: only these pages
     (kv8_select).  window: only so many newest positions.  Returns (out [T, Hq, D] bf16 or float32, lse
     float32 [T, Hq])."""
     T, Hq, D = q.shape
@@ -858,7 +862,7 @@ def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, win
     qp, qt, qh = _heads_of(q, dev, "q")
     S, sp, lengths = _step(cache, start, length, dev)
     _launch_ws("csa2_kv8_attn", _KV8_ATTN.pack(
-        _KV8_ATTN.size, T, S, Hq, T if max_new is None else max_new, window,
+        _KV8_ATTN.size, T, S, Hq, max(T - S, 0) + 1 if max_new is None else max_new, window,
         1.0 / math.sqrt(D) if softmax_scale is None else softmax_scale, qp, qt, qh, sp, lengths, *cache.fields(dev),
         _dense(pages, dev, torch.int32, "pages"), n, op, _float_type(out, "out"), lp), ws, q.device, dev)
     return out, lse

@@ -565,6 +565,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       }
     }
     __syncwarp();                        // the stages are free for the next stream
+    if (dead) break;
     // ---- its result, or its part
 #pragma unroll
     for (int i = 0; i < 2; ++i) {

@@ -153,6 +153,9 @@ __device__ __forceinline__ long long first_slot(const Kv8Params& p, const int* s
   return (long long)(x < 0 ? 0 : x > p.a.T ? p.a.T : x) * p.G / RT + s;
 }
 
+template <int RT>
+__device__ __forceinline__ int slots_of(const Kv8Params& p) { return (int)((long long)p.a.T * p.G / RT) + p.a.S; }
+
 // Slot `slot`, of a sequence from s on; start and length: the step's, or a copy.
 template <int RT>
 __device__ __forceinline__ Slot slot_of(const Kv8Params& p, const int* start, const int* length, int s, int slot) {
@@ -228,7 +231,13 @@ struct Walk {
       if (left <= 0) return;
       if (++h == p.a.cache.Hkv) {
         h = 0;
-        do t = slot_of<RT>(p, p.a.start, p.a.length, t.s, ++slot); while (t.count == 0);
+        do {
+          if (++slot >= slots_of<RT>(p)) {                   // only if `start` does not ascend
+            left = 0;
+            return;
+          }
+          t = slot_of<RT>(p, p.a.start, p.a.length, t.s, slot);
+        } while (t.count == 0);
       }
       cut(0);
     } while (take == 0);
@@ -280,7 +289,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
   pdl_trigger();
 
   // ---- the plan: steps of all slots, and the slot in which this CTA's span begins
-  const int slots = (int)((long long)a.T * G / RT) + a.S;
+  const int slots = slots_of<RT>(p);
   const int chunk = (slots + kThreads - 1) / kThreads;
   const int c0 = min(slots, tid * chunk), c1 = min(slots, c0 + chunk);
   const int *start = a.start, *length = a.length;
@@ -353,7 +362,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         for (int j = 0; j < w.take; ++j, ++step) {
           if ((j & 15) == 0) {
             const int y = page0 + 2 * j + lane;
-            id = y < pages && 2 * j + lane < 2 * w.take ? page_id(c, w.t.s, y, &g_err_kv8_tile) : -1;
+            id = y >= w.t.lo / kPage && y < pages && 2 * j + lane < 2 * w.take ? page_id(c, w.t.s, y, &g_err_kv8_tile) : -1;
             ks = vs = -1.f;
             if (id >= 0) {
               ks = c.k_scale[(long long)id * c.Hkv + w.h];
@@ -466,7 +475,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         // in units of the largest scale of the segment, times 2^-7: exact for scales down to 2^-22 of it
         float top = 0.f;
         const int y1 = min((t.hi + kPage - 1) / kPage, 2 * (t.step + w.x + w.take));
-        for (int y = 2 * (t.step + w.x) + r; y < y1; y += 128) {
+        for (int y = max(t.lo / kPage, 2 * (t.step + w.x)) + r; y < y1; y += 128) {
           const int id = __ldg(c.page_table + (long long)t.s * c.max_pages + y);
           if (id >= 0 && id < c.num_pages) top = fmaxf(top, c.v_scale[(long long)id * c.Hkv + w.h]);
         }

@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kPlanThreads) k_plan(const csa2_page_plan_args
   if (err) raise_error(&g_err_paged, err);
 }
 
-// More sequences than that.  One CTA: the two prefix sums (rows, pages) over the sequences, 1024 at a time, and the new entries of the page table.
+// More sequences than that, or many rows in place.  One CTA: the two prefix sums (rows, pages) over the sequences, 1024 at a time, and the new entries of the page table.
 __global__ void __launch_bounds__(kPlanThreads) k_plan_scan(const csa2_page_plan_args a) {
   __shared__ long long sums[33];
   __shared__ int first_page[kPlanThreads], pages_before[kPlanThreads + 1];
@@ -798,8 +798,9 @@ cudaError_t launch_select(SelectParams& p, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_page_plan(const csa2_page_plan_args& a, cudaStream_t st) {
-  if (a.S <= kPlanThreads && a.S > 0) {
-    const bool in_place = a.new_length == a.length || a.new_head == a.free_head;
+  // In place one CTA writes all rows: 7 us for 8192, 149 us for 262,144 of 16 sequences.
+  const bool in_place = a.new_length == a.length || a.new_head == a.free_head;
+  if (a.S <= kPlanThreads && a.S > 0 && (!in_place || a.tokens <= 4096)) {
     const int most = in_place ? 1 : 152, rows = kPlanThreads * (int)(1 + (long long)(a.tokens - 1) / ((long long)most * kPlanThreads));
     return launch_k(k_plan, dim3(a.tokens > rows ? (a.tokens + rows - 1) / rows : 1), dim3(kPlanThreads), 0, st, a, rows);
   }

@@ -752,6 +752,7 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  *   seen  = positions max(0, p + 1 - window) .. p  (window 0: from 0), and with `pages` only
  *           those on the listed pages (csa2_kv8_select)
  *   x_j   = softmax_scale * q . k_j;  out = sum_j softmax(x)_j v_j;  lse = log sum_j exp(x_j)
+ * Pages that no row sees are not looked up: behind a window their table entries may hold anything.
  * An empty `seen` gives out = 0 and lse = -inf.  `pages` entries below 0 are skipped, in any order;
  * a page listed twice counts twice; one past the page table sets CSA2_DEVERR_PAGE_SLOT.
  * max_new: about how many new tokens the longest of the call's sequences has.  It only

@@ -84,11 +84,12 @@ def test_plan_negative_counts_raises():
     run_plan([-5, 10], [3, -2], 4, np.arange(9), 0, 8, np.zeros((2, 4), np.int32), err=0x4)
 
 
-def test_plan_advances_its_own_state_in_a_graph():
+@pytest.mark.parametrize("tokens,new", [(60, 3), (4096, 30), (4097, 30)])
+def test_plan_advances_its_own_state_in_a_graph(tokens, new):
     """Captured once, replayed: lengths, table and free list advance as step by step."""
     r = np.random.default_rng(3)
-    S, most, tokens = 37, 6, 60
-    length, add = r.integers(0, 130, S), r.integers(0, 3, S)
+    S, most = 37, 6
+    length, add = r.integers(0, 130, S), r.integers(0, new, S)
     table, free = held_table(r, length, most, S * most)
     g = dict(length=gpu(length.astype(np.int32)), add=gpu(add.astype(np.int32)), table=gpu(table), free=gpu(free), head=gpu(np.zeros(1, np.int32)))
     out = csa2.PagePlan.allocate(S, tokens, DEV)
@@ -307,6 +308,32 @@ def test_attn_window(window, hint):
     fill(r, c, length)
     q = bf16(r.standard_normal((sum(add), 6, 128)))
     run_attn(c, to_gpu(c), q, starts(add), length, window=window, max_new=hint)
+
+
+@pytest.mark.parametrize("hint", [1, 8, 20, 100])
+@pytest.mark.parametrize("window", [1, 65, 200])
+def test_attn_window_with_its_old_pages_given_back(window, hint):
+    """Table entries of pages behind the window are not looked at."""
+    r = np.random.default_rng(window)
+    length, add = [64, 130, 705, 321], [1, 7, 21, 1]
+    c = new_cache(r, 4, 12, 2, 128)
+    fill(r, c, length)
+    for s in range(4):
+        c["table"][s, :max(0, length[s] - add[s] + 1 - window) // 64] = -1
+    q = bf16(r.standard_normal((sum(add), 6, 128)))
+    run_attn(c, to_gpu(c), q, starts(add), length, window=window, max_new=hint)
+
+
+def test_attn_without_a_hint():
+    """The default takes the kernel that the step's rows allow for: the same bits as with the hint."""
+    r = np.random.default_rng(5)
+    c = new_cache(r, 3, 12, 2, 128)
+    fill(r, c, [200, 64, 700])
+    g, q = to_gpu(c), bf16(r.standard_normal((9, 16, 128)))
+    for add in ([1, 1, 1], [3, 5, 1]):
+        args = (c, g, q[:sum(add)], starts(add), [200, 64, 700])
+        got, want = run_attn(*args), run_attn(*args, max_new=sum(add) - 2, check=False)
+        assert all((a == b).all() for a, b in zip(got, want))
 
 
 @pytest.mark.parametrize("H,G,D,n", [(2, 8, 128, 1), (1, 1, 64, 5), (3, 7, 64, 9), (1, 16, 128, 4), (1, 40, 128, 7), (2, 4, 128, 70)])

@@ -265,3 +265,20 @@ def test_select_keeps_the_best_middle_pages():
     assert kv8.select(c, q, 0, 9 * 64, 3, 1, 1) == [[0, 5, 8]]          # equal scores: the older page
     assert kv8.select(c, -q, 0, 8 * 64 + 1, 4, 1, 1) == [[0, 1, 2, 8]]
     assert kv8.select(c, q, 0, 3 * 64, 4, 1, 1) == [[0, 1, 2]]
+
+
+def test_workspace_keeps_what_graphs_hold(monkeypatch):
+    capturing = [False]
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing[0])
+    w = csa2.Workspace("cpu")
+    a = w.get(10)
+    b = w.get(20)
+    assert w.outgrown == [] and b.numel() == 20 and a is not b
+    capturing[0] = True
+    assert w.get(15) is b
+    with pytest.raises(RuntimeError, match="sized before"):
+        w.get(21)
+    capturing[0] = False
+    w.get(30)
+    w.get(40)
+    assert [x.numel() for x in w.outgrown] == [20]
