@@ -27,19 +27,20 @@ namespace {
 // its partial output, in float32.
 //
 // Bound by memory where a batch has the bytes (64 sequences of up to 64K tokens, 8 x 128 channels: 4.2 GB in 625-645 us,
-// 0.96-0.98 of the copy rate); by a warp's own chain of products and conversions, two warps a scheduler, where pages come
-// from L2 (2048 rows of 32 listed pages each: 1.02 ms for 8.6 GB); by two launches and four dependent loads where
-// there is little (one row over 4097 tokens: 10 + 6 us).  Left out: three CTAs an SM (below); kLeast of 1 to 8 is all
-// the same at one row.
+// 0.96-0.98 of the copy rate); by a warp's own chain of products and conversions, three warps a scheduler, where pages come
+// from L2 (2048 rows of 32 listed pages each: 0.87 ms for 8.6 GB, which the copies alone take 0.43 ms for); by two launches
+// and four dependent loads where there is little (one row over 4097 tokens: 10 + 6 us).  Left out: E4M3 products by
+// mma.sync (100 instructions more a half page than fp16 ones with their conversions: 1.17 ms); kLeast of 1 to 8 is all the
+// same at one row.
 constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
 
-// Two CTAs an SM.  Three, at 168 registers a thread and two stages a warp, are slower (64 sequences up to 64K: 726 us
-// against 624; 2048 rows over 32 pages each: 1.40 ms against 1.29).
-constexpr int kStreamCtas = 2 * 152, kSpans = kStreamCtas * kWarps;
-
-template <int D>
-struct Ring {
-  static constexpr int kStage = 2 * kHalf * D, kStages = 24576 / kStage;
+// CTAs an SM.  Three, at 168 registers a thread and two stages a warp, where 8 rows have lists and pages come from L2
+// (2048 rows over 32 pages each: 0.95 ms against 1.10); two, with three stages, where the bytes come from memory (64 sequences
+// up to 64K: 649 us against 654) and at 16 rows, whose accumulators do not fit 168 registers.
+template <int D, int RT, bool LIST>
+struct Shape {
+  static constexpr int kCtas = RT == 8 && LIST ? 3 : 2, kSpans = kCtas * 152 * kWarps;
+  static constexpr int kStage = 2 * kHalf * D, kStages = (kCtas == 3 ? 16384 : 24576) / kStage;
   static constexpr int kBytes = kWarps * kStages * kStage;
 };
 
@@ -81,9 +82,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
 
 // RT: rows of a tile, 8 or 16.  LIST: streams are (row, head) pairs over their listed pages.
 template <int D, int RT, bool LIST>
-__global__ void __launch_bounds__(32 * kWarps, 2)
+__global__ void __launch_bounds__(32 * kWarps, (Shape<D, RT, LIST>::kCtas))
 k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8Params p) {
-  constexpr int kSt = Ring<D>::kStages, kStage = Ring<D>::kStage, kKs = D / 16, kR = RT / 8;
+  using L = Shape<D, RT, LIST>;
+  constexpr int kSt = L::kStages, kStage = L::kStage, kKs = D / 16, kR = RT / 8, kSpans = L::kSpans;
   constexpr bool kT = RT == 8;           // rows on N
   constexpr int kNt = kT ? D / 16 : D / 8;                   // accumulators of four
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -137,7 +139,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
     cut();
   } else {
     // Sums over 32 sequences at a time, then within the 32 that hold this warp's begin.
-    long long* sums = reinterpret_cast<long long*>(smem + Ring<D>::kBytes);
+    long long* sums = reinterpret_cast<long long*>(smem + L::kBytes);
     const int chunks = (a.S + 31) / 32;
     long long before = 0;
     int chunk = 0;
@@ -679,10 +681,10 @@ struct Layout {
 template <int D, int RT, bool LIST>
 cudaError_t launch_stream(const CUtensorMap& mk, const CUtensorMap& mv, const Kv8Params& p, cudaStream_t st) {
   static SmemLimit limit;
-  const size_t smem = Ring<D>::kBytes + (LIST ? 0 : 8 * (size_t)((p.a.S + 31) / 32));
+  const size_t smem = Shape<D, RT, LIST>::kBytes + (LIST ? 0 : 8 * (size_t)((p.a.S + 31) / 32));
   cudaError_t e = limit.raise(k_kv8_stream<D, RT, LIST>, smem);
   if (e != cudaSuccess) return e;
-  return launch_k(k_kv8_stream<D, RT, LIST>, dim3(152 * 2), dim3(32 * kWarps), smem, st, mk, mv, p);
+  return launch_k(k_kv8_stream<D, RT, LIST>, dim3(152 * Shape<D, RT, LIST>::kCtas), dim3(32 * kWarps), smem, st, mk, mv, p);
 }
 
 // Whether a sequence's rows of a key head fit a tile of 8.
@@ -707,7 +709,7 @@ bool takes_tiles(const csa2_kv8_attn_args& a) {
 }
 
 int spans_of(const csa2_kv8_attn_args& a) {
-  return takes_tiles(a) ? kTileSpans : kSpans;
+  return takes_tiles(a) ? kTileSpans : a.pages && takes_eight(a) ? Shape<64, 8, true>::kSpans : Shape<64, 8, false>::kSpans;
 }
 int most_of(const csa2_kv8_attn_args& a) { return takes_tiles(a) ? tile_rows(a) : takes_eight(a) ? 8 : 16; }
 Layout layout_of(const csa2_kv8_attn_args& a) { return Layout(spans_of(a), most_of(a), a.cache.D); }
