@@ -11,6 +11,7 @@
 // tokens at 32K and a fresh prompt, 64 heads of 128: 3.2 ms, 1.31 PFLOP/s, 0.67 of the measured peak; 32 x 6 tokens at
 // 8K to 32K, 48 rows: 280 us, 0.71 of the copy rate.
 #include "kv8_attn.cuh"
+#include "kv8_order.h"
 
 namespace csa2 {
 
@@ -415,7 +416,6 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       const uint32_t s_at = tb + grp * 128, o_at = tb + 256 + grp * 128;
       int step = 0;                      // of the segment's first
       uint32_t ps = 0, turns = 0;        // parity of the weights, turns had
-      auto keys = [&](int st) { await_warp(&m.k_full[st % kRing], st / kRing & 1, m); };
       auto scores = [&](int st) {
         const uint64_t kb = k_desc + (uint32_t)(st % kRing * (L::kRaw >> 4));
 #pragma unroll
@@ -425,42 +425,39 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         tc::mma_commit(&m.k_empty[st % kRing]);
       };
       for (; w.on(); w.next(p)) {
-        const int n = w.take;
-        await_warp(&m.q_full, w.n & 1, m);
-        if (grp < n || !SPLIT) {
-          keys(step + (SPLIT ? grp : 0));
-          tc::fence_after_sync();
-          if (elect()) scores(step + (SPLIT ? grp : 0));
-          __syncwarp();
-        }
-        for (int j = SPLIT ? grp : 0; j < n; j += kBy) {
-          const int st = step + j;
-          const bool on = j + kBy < n;
-          if (on) keys(st + kBy);
-          await_warp(&m.vf_full[st & 1], st >> 1 & 1, m);
-          await_warp(&m.turn[grp], (turns & 1) ^ (grp ? 0 : 1), m);
-          ++turns;
-          await_warp(&m.p_full[grp], ps, m);
-          ps ^= 1;
-          tc::fence_after_sync();
-          if (elect()) {
-            const uint64_t vb = v_desc + (uint32_t)((st & 1) * (L::kF >> 4));
+        product_order<kBy>(
+            grp, step, w.take, [&] { await_warp(&m.q_full, w.n & 1, m); },
+            [&](int st) { await_warp(&m.k_full[st % kRing], st / kRing & 1, m); },
+            [&](int st) {
+              tc::fence_after_sync();
+              if (elect()) scores(st);
+              __syncwarp();
+            },
+            [&](int st) { await_warp(&m.vf_full[st & 1], st >> 1 & 1, m); },
+            [&] { await_warp(&m.turn[grp], (turns++ & 1) ^ (grp ? 0 : 1), m); },
+            [&] {
+              await_warp(&m.p_full[grp], ps, m);
+              ps ^= 1;
+            },
+            [&](int st, bool add, bool on) {
+              tc::fence_after_sync();
+              if (elect()) {
+                const uint64_t vb = v_desc + (uint32_t)((st & 1) * (L::kF >> 4));
 #pragma unroll
-            for (int i = 0; i < kStep / 16; ++i)
-              tc::mma_f16_ts(o_at, s_at + i * 8, vb + i * (2048 / 16), id_o, j >= kBy || i > 0);
-            tc::mma_commit(&m.vf_empty[st & 1]);
-            if (on) scores(st + kBy);
-            else tc::mma_commit(&m.o_full[grp]);
-            tc::mbar_arrive(&m.turn[grp ^ 1]);
-          }
-          __syncwarp();
-        }
-        if (SPLIT && grp && (n & 1)) {   // the first group had a step more
-          await_warp(&m.turn[1], turns++ & 1, m);
-          if (elect()) tc::mbar_arrive(&m.turn[0]);
-          __syncwarp();
-        }
-        step += n;
+                for (int i = 0; i < kStep / 16; ++i)
+                  tc::mma_f16_ts(o_at, s_at + i * 8, vb + i * (2048 / 16), id_o, add || i > 0);
+                tc::mma_commit(&m.vf_empty[st & 1]);
+                if (on) scores(st + kBy);
+                else tc::mma_commit(&m.o_full[grp]);
+                tc::mbar_arrive(&m.turn[grp ^ 1]);
+              }
+              __syncwarp();
+            },
+            [&] {
+              if (elect()) tc::mbar_arrive(&m.turn[grp ^ 1]);
+              __syncwarp();
+            });
+        step += w.take;
       }
       if (*(volatile int*)&m.dead) {                         // nor a product
         if (elect()) tc::mma_commit(&m.done);
