@@ -20,15 +20,17 @@ namespace csa2 {
 //   products(st, add, on)   issue the product of the weights with the values (add: to what is there), then, if `on`, the
 //                           scores of step st + BY; pass
 //
-// A wait by parity tells a phase from the one before it, not from the one two before: it may stand only where the phase
-// before the awaited one is known to be over.  The keys of step st and of st - 3 come through one barrier, and with BY = 2
-// the two steps belong to different groups.
+// A wait by parity tells a phase from the one before it, not from the one two before or two after: it may stand only where
+// the phase before the awaited one is known to be over, and the one after it to be still to come.  The keys of step st and
+// of st - 3 come through one barrier, and with BY = 2 the two steps belong to different groups.  In a segment of one step
+// the second group has none, and the next segment's Q does not wait for it: it only takes its turn, which is behind
+// the first group's wait for Q.
 template <int BY, class Query, class Keys, class Scores, class Values, class Turn, class Weights, class Products, class Pass>
 CSA2_ORDER void product_order(int grp, int step, int n, Query query, Keys keys, Scores scores, Values values, Turn turn,
                               Weights weights, Products products, Pass pass) {
-  query();
   const int first = BY == 2 ? grp : 0;
   if (first < n) {
+    query();
     keys(step + first);
     scores(step + first);
   }

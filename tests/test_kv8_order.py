@@ -183,7 +183,8 @@ def explore(order, by, segments):
 
 
 @pytest.mark.parametrize("by,segments", [(2, [1]), (2, [2]), (2, [3]), (2, [4]), (2, [5]), (2, [6]), (2, [7]), (2, [3, 4]), (2, [4, 3]),
-                                         (2, [5, 3]), (2, [2, 2, 4]), (1, [1]), (1, [4]), (1, [5]), (1, [2, 3])])
+                                         (2, [5, 3]), (2, [2, 2, 4]), (2, [1, 5]), (2, [1, 1, 2, 4]), (2, [2, 1, 4]), (2, [1, 1, 1, 3]),
+                                         (1, [1]), (1, [4]), (1, [5]), (1, [2, 3])])
 def test_no_product_reads_what_is_not_there(order, by, segments):
     explore(order, by, segments)
 
