@@ -27,6 +27,7 @@ constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
 constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a limit wakes late: 5 % at 4096 new tokens)
+constexpr int kRun = 128;                // steps of a group whose sums are taken by themselves
 constexpr int kOver = 12;                // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
@@ -646,7 +647,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + i));
         }
       }
-      float top = -INFINITY, l = 0.f;
+      float top = -INFINITY, l = 0.f, held = 0.f;            // held: the sum of earlier runs
       bool any = false;                  // a step of this segment has been added to O
       for (int j = SPLIT ? grp : 0; j < w.take; j += SPLIT ? 2 : 1) {
         await_warp(&m.s_full[grp], seen++ & 1, m);
@@ -697,6 +698,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           const float alpha = follow ? ex2(top - now) : 1.f;
           if (follow) top = now;
           l *= alpha;
+          held *= alpha;
           if (any) {
 #pragma unroll 1
             for (int i = 0; i < kDims; i += 32) {
@@ -739,6 +741,10 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         }
         sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
         l += sum[0].x + sum[0].y;
+        if ((j / (SPLIT ? 2 : 1)) % kRun == kRun - 1) {      // small weights of a long stream count beside a sum near 1
+          held += l;
+          l = 0.f;
+        }
         tc::tmem_st_wait();
         tc::fence_before_sync();
         __syncwarp();
@@ -746,6 +752,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       }
       // ---- the segment's result, or its part
       const bool two = SPLIT && w.take > 1;                  // both groups have steps
+      l += held;
       if (kM == 64) l += __shfl_xor_sync(0xffffffffu, l, 16);
       if (SPLIT && grp == 1 && half == 0) m.ml[r] = make_float2(top, l);
       if (SPLIT) named_sync(1, 256);
