@@ -682,11 +682,13 @@ __global__ void __launch_bounds__(256, 2) k_kv8_join(const Kv8Params p) {
 size_t up256(size_t n) { return (n + 255) & ~(size_t)255; }
 
 struct Layout {
-  size_t part = 0, ml, o, bytes;
-  Layout(int spans, int rows, int D) {
+  size_t part = 0, ml, o, second_ml, second, bytes;
+  Layout(int spans, int rows, int D, bool split) {
     ml = up256(sizeof(Part) * spans);
     o = ml + up256(sizeof(float2) * spans * 2 * rows);
-    bytes = o + sizeof(float) * spans * 2 * rows * D;
+    second_ml = o + up256(sizeof(float) * spans * 2 * rows * D);
+    second = second_ml + (split ? up256(sizeof(float2) * spans * rows) : 0);
+    bytes = second + (split ? sizeof(float) * spans * rows * D : 0);
   }
 };
 
@@ -724,7 +726,9 @@ int spans_of(const csa2_kv8_attn_args& a) {
   return takes_tiles(a) ? kTileSpans : a.pages && takes_eight(a) ? Shape<64, 8, true>::kSpans : Shape<64, 8, false>::kSpans;
 }
 int most_of(const csa2_kv8_attn_args& a) { return takes_tiles(a) ? tile_rows(a) : takes_eight(a) ? 8 : 16; }
-Layout layout_of(const csa2_kv8_attn_args& a) { return Layout(spans_of(a), most_of(a), a.cache.D); }
+Layout layout_of(const csa2_kv8_attn_args& a) {
+  return Layout(spans_of(a), most_of(a), a.cache.D, takes_tiles(a) && tile_rows(a) < 256);
+}
 
 }  // namespace
 
@@ -747,6 +751,8 @@ cudaError_t launch_kv8_attn(const csa2_kv8_attn_args& a, void* ws, cudaStream_t 
   p.part = reinterpret_cast<Part*>(w + at.part);
   p.ml = reinterpret_cast<float2*>(w + at.ml);
   p.o = reinterpret_cast<float*>(w + at.o);
+  p.second_ml = reinterpret_cast<float2*>(w + at.second_ml);
+  p.second = reinterpret_cast<float*>(w + at.second);
   cudaError_t e = tiles ? launch_kv8_tile(p, st) : a.cache.D == 64 ? launch_rows<64>(p, st) : launch_rows<128>(p, st);
   if (e != cudaSuccess) return e;
   const dim3 grid(p.spans, p.most / 8);

@@ -108,6 +108,8 @@ struct Kv8Params {
   Part* part;                            // [spans]
   float2* ml;                            // [spans][2][most] maximum, sum; [1]: of the stream that goes on from here
   float* o;                              // [spans][2][most][D] sums of weighted values
+  float2* second_ml;                     // tiles of up to 128 rows: [spans][most] maximum, sum, and
+  float* second;                         // [spans][most][D] sums of weighted values, of the second group's earlier runs
 };
 
 // One plane as [num_pages * Hkv][64][D] bytes, boxes of `tokens` tokens, swizzled over the rows' width.

@@ -17,15 +17,17 @@ namespace csa2 {
 //   scores(st)              issue the product of Q with the step's keys
 //   turn(), pass()          wait for this group's turn; give it to the other group
 //   weights()               wait for the weights of the group's next step
-//   products(st, add, on)   issue the product of the weights with the values (add: to what is there), then, if `on`, the
-//                           scores of step st + BY; pass
+//   products(st, add, out, on)
+//                           issue the product of the weights with the values (add: to what is there; out: the sum is read
+//                           after it), then, if `on`, the scores of step st + BY; pass
+// A sum has up to RUN steps of the group.  Who makes the weights reads it before it hands out the next step's.
 //
 // A wait by parity tells a phase from the one before it, not from the one two before or two after: it may stand only where
 // the phase before the awaited one is known to be over, and the one after it to be still to come.  The keys of step st and
 // of st - 3 come through one barrier, and with BY = 2 the two steps belong to different groups.  In a segment of one step
 // the second group has none, and the next segment's Q does not wait for it: it only takes its turn, which is behind
 // the first group's wait for Q.
-template <int BY, class Query, class Keys, class Scores, class Values, class Turn, class Weights, class Products, class Pass>
+template <int BY, int RUN, class Query, class Keys, class Scores, class Values, class Turn, class Weights, class Products, class Pass>
 CSA2_ORDER void product_order(int grp, int step, int n, Query query, Keys keys, Scores scores, Values values, Turn turn,
                               Weights weights, Products products, Pass pass) {
   const int first = BY == 2 ? grp : 0;
@@ -42,7 +44,8 @@ CSA2_ORDER void product_order(int grp, int step, int n, Query query, Keys keys, 
     turn();                              // the other group's products of step st - 1 are issued, so its keys have been there
     if (BY == 2 && on) keys(st + 2);
     weights();
-    products(st, j >= BY, on);
+    const int i = j / BY % RUN;
+    products(st, i > 0, i == RUN - 1 || !on, on);
   }
   if (BY == 2 && grp == 1 && (n & 1)) {  // the first group had a step more
     turn();

@@ -27,7 +27,11 @@ constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;           // 256 threads each
 constexpr int kInfo = 8;                 // steps whose scales are kept: more than can be under way
 constexpr int kRing = 3;                 // steps of bytes under way
 constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a limit wakes late: 5 % at 4096 new tokens)
-constexpr int kRun = 128;                // steps of a group whose sums are taken by themselves
+// Steps of a group whose sums are taken by themselves.  The tensor core drops what lies below the last bit of a sum, so that O
+// would be too small by 1e-7 for each of a step's eight products (by 0.7 % after a million tokens), and a sum of weights
+// near 1 leaves no room for small ones.  A run's O is off by 2^-12 at most.  4096 new tokens at 32K: 3.35 ms, as without
+// runs; 3.43 with runs of 128 steps, 3.69 of 64 (before both ends of a run shared their code).
+constexpr int kRun = 256;
 constexpr int kOver = 12;                // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
@@ -101,10 +105,15 @@ __device__ __forceinline__ void sts64(uint32_t a, uint2 v) {
   asm volatile("st.shared.v2.u32 [%0], {%1,%2};" :: "r"(a), "r"(v.x), "r"(v.y) : "memory");
 }
 
-// A whole 32-byte sector of one thread's own row.
+// A whole 32-byte sector of one thread's own row, and back.
 __device__ __forceinline__ void stg256(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
                :: "l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]) : "memory");
+}
+
+__device__ __forceinline__ void ldg256(const void* p, float* v) {
+  asm volatile("ld.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p) : "memory");
 }
 
 __device__ __forceinline__ void named_sync(int id, int threads) {
@@ -426,7 +435,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         tc::mma_commit(&m.k_empty[st % kRing]);
       };
       for (; w.on(); w.next(p)) {
-        product_order<kBy>(
+        product_order<kBy, kRun>(
             grp, step, w.take, [&] { await_warp(&m.q_full, w.n & 1, m); },
             [&](int st) { await_warp(&m.k_full[st % kRing], st / kRing & 1, m); },
             [&](int st) {
@@ -440,7 +449,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
               await_warp(&m.p_full[grp], ps, m);
               ps ^= 1;
             },
-            [&](int st, bool add, bool on) {
+            [&](int st, bool add, bool out, bool on) {
               tc::fence_after_sync();
               if (elect()) {
                 const uint64_t vb = v_desc + (uint32_t)((st & 1) * (L::kF >> 4));
@@ -448,8 +457,8 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
                 for (int i = 0; i < kStep / 16; ++i)
                   tc::mma_f16_ts(o_at, s_at + i * 8, vb + i * (2048 / 16), id_o, add || i > 0);
                 tc::mma_commit(&m.vf_empty[st & 1]);
+                if (out) tc::mma_commit(&m.o_full[grp]);
                 if (on) scores(st + kBy);
-                else tc::mma_commit(&m.o_full[grp]);
                 tc::mbar_arrive(&m.turn[grp ^ 1]);
               }
               __syncwarp();
@@ -556,8 +565,19 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       if constexpr (kM == 64) tc::tmem_ld16x2_32<kDims>(at, reinterpret_cast<uint32_t*>(v));
       else tc::tmem_ld32(at, reinterpret_cast<uint32_t*>(v));
     };
-    int step = 0, seen = 0, outs = 0, outs1 = 0;   // steps of earlier segments; scores, outputs waited for
+    auto store_o = [&](uint32_t at, const float* v) {
+      if constexpr (kM == 64) {
+        tc::tmem_st16x2_16<kDims>(at, reinterpret_cast<const uint32_t*>(v));
+        tc::tmem_st16x2_16<kDims>(at + 16, reinterpret_cast<const uint32_t*>(v + 16));
+      } else {
+        tc::tmem_st32(at, reinterpret_cast<const uint32_t*>(v));
+      }
+    };
+    constexpr int kBy = SPLIT ? 2 : 1;
+    int step = 0, seen = 0, outs = 0;   // steps of earlier segments; scores, sums waited for
     Part part = {0, 0, 0, 0, 0};
+    // Earlier runs' maximum, sum and O of a row: in its part's place, the second group's of a SPLIT in their own
+    const bool aside = SPLIT && grp == 1;
     for (; w.on(); w.next(p)) {
       const Slot& t = w.t;
       const int row = (SPLIT ? 0 : grp * 128) + r;
@@ -647,119 +667,157 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(q + i));
         }
       }
-      float top = -INFINITY, l = 0.f, held = 0.f;            // held: the sum of earlier runs
-      bool any = false;                  // a step of this segment has been added to O
-      for (int j = SPLIT ? grp : 0; j < w.take; j += SPLIT ? 2 : 1) {
-        await_warp(&m.s_full[grp], seen++ & 1, m);
-        tc::fence_after_sync();
-        const float2 ks = m.ks[(step + j) % kInfo];
-        const int token0 = (t.step + w.x + j) * kStep;
-        // positive, so that a masked score's -infinity stays one; a page that is not there is masked as a whole
-        const float f0 = fmaxf(mul * (ks.x == -1.f ? 1.f : ks.x), 1.17549435e-38f);
-        const float f1 = fmaxf(mul * (ks.y == -1.f ? 1.f : ks.y), 1.17549435e-38f);
-        const bool border = __any_sync(0xffffffffu, token0 < lo || token0 + kStep > hi || ks.x == -1.f || ks.y == -1.f);
-        const int from0 = ks.x == -1.f ? INT_MAX : lo - token0, from1 = ks.y == -1.f ? INT_MAX : lo - token0;
-        const int to = hi == INT_MAX ? INT_MAX : hi - token0;
-        float x[kCols];                  // of tokens 64 * half + ...
-        if constexpr (kM == 64) {
-          tc::tmem_ld16x2_32<64>(s_at, reinterpret_cast<uint32_t*>(x));
-          tc::tmem_ld16x2_32<64>(s_at + 32, reinterpret_cast<uint32_t*>(x + 32));
-        } else {
+      float top = -INFINITY, l = 0.f;
+      bool any = false;                  // a step of this run has been added to O
+      const int grp0 = SPLIT ? grp : 0;
+      for (int j = grp0; j < w.take;) {
+        const int end = min(w.take, j + kRun * kBy);
+        for (; j < end; j += kBy) {
+          await_warp(&m.s_full[grp], seen++ & 1, m);
+          tc::fence_after_sync();
+          const float2 ks = m.ks[(step + j) % kInfo];
+          const int token0 = (t.step + w.x + j) * kStep;
+          // positive, so that a masked score's -infinity stays one; a page that is not there is masked as a whole
+          const float f0 = fmaxf(mul * (ks.x == -1.f ? 1.f : ks.x), 1.17549435e-38f);
+          const float f1 = fmaxf(mul * (ks.y == -1.f ? 1.f : ks.y), 1.17549435e-38f);
+          const bool border = __any_sync(0xffffffffu, token0 < lo || token0 + kStep > hi || ks.x == -1.f || ks.y == -1.f);
+          const int from0 = ks.x == -1.f ? INT_MAX : lo - token0, from1 = ks.y == -1.f ? INT_MAX : lo - token0;
+          const int to = hi == INT_MAX ? INT_MAX : hi - token0;
+          float x[kCols];                  // of tokens 64 * half + ...
+          if constexpr (kM == 64) {
+            tc::tmem_ld16x2_32<64>(s_at, reinterpret_cast<uint32_t*>(x));
+            tc::tmem_ld16x2_32<64>(s_at + 32, reinterpret_cast<uint32_t*>(x + 32));
+          } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tc::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x + 32 * i));
-        }
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) tmem_arrived(x + 32 * i);
-        if (border) {
-#pragma unroll
-          for (int e = 0; e < kCols; ++e) {
-            const int from = kM == 64 ? (half ? from1 : from0) : e < kPage ? from0 : from1, at = kM == 64 ? 64 * half + e : e;
-            x[e] = at >= from && at < to ? x[e] : -INFINITY;
+            for (int i = 0; i < 4; ++i) tc::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x + 32 * i));
           }
-        }
-        float mx[kCols / 32];
 #pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) {
-          mx[i] = fmaxf(x[32 * i], x[32 * i + 1]);
+          for (int i = 0; i < kCols / 32; ++i) tmem_arrived(x + 32 * i);
+          if (border) {
 #pragma unroll
-          for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], x[32 * i + e], x[32 * i + e + 1]);
-        }
-        float now;
-        if constexpr (kM == 64) {
-          now = fmaxf(mx[0], mx[1]) * (half ? f1 : f0);
-          now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
-        } else {
-          now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
-        }
-        // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
-        // sum are rescaled a few times a row.
-        const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
-        if (__any_sync(0xffffffffu, follow)) {
-          const float alpha = follow ? ex2(top - now) : 1.f;
-          if (follow) top = now;
-          l *= alpha;
-          held *= alpha;
-          if (any) {
+            for (int e = 0; e < kCols; ++e) {
+              const int from = kM == 64 ? (half ? from1 : from0) : e < kPage ? from0 : from1, at = kM == 64 ? 64 * half + e : e;
+              x[e] = at >= from && at < to ? x[e] : -INFINITY;
+            }
+          }
+          float mx[kCols / 32];
+#pragma unroll
+          for (int i = 0; i < kCols / 32; ++i) {
+            mx[i] = fmaxf(x[32 * i], x[32 * i + 1]);
+#pragma unroll
+            for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], x[32 * i + e], x[32 * i + e + 1]);
+          }
+          float now;
+          if constexpr (kM == 64) {
+            now = fmaxf(mx[0], mx[1]) * (half ? f1 : f0);
+            now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, 16));
+          } else {
+            now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
+          }
+          // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
+          // sum are rescaled a few times a row.
+          const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
+          if (__any_sync(0xffffffffu, follow)) {
+            const float alpha = follow ? ex2(top - now) : 1.f;
+            if (follow) top = now;
+            l *= alpha;
+            if (any) {
 #pragma unroll 1
-            for (int i = 0; i < kDims; i += 32) {
-              float v[32];
-              load_o(o_at + i, v);
-              tmem_arrived(v);
+              for (int i = 0; i < kDims; i += 32) {
+                float v[32];
+                load_o(o_at + i, v);
+                tmem_arrived(v);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) v[e] *= alpha;
-              if constexpr (kM == 64) {
-                tc::tmem_st16x2_16<kDims>(o_at + i, reinterpret_cast<const uint32_t*>(v));
-                tc::tmem_st16x2_16<kDims>(o_at + i + 16, reinterpret_cast<const uint32_t*>(v + 16));
-              } else {
-                tc::tmem_st32(o_at + i, reinterpret_cast<const uint32_t*>(v));
+                for (int e = 0; e < 32; ++e) v[e] *= alpha;
+                store_o(o_at + i, v);
               }
             }
           }
-        }
-        any = true;
-        const float z = top == -INFINITY ? 0.f : top;
-        float2 sum[4] = {};
-        const float2 zz = make_float2(-z, -z);
+          any = true;
+          const float z = top == -INFINITY ? 0.f : top;
+          float2 sum[4] = {};
+          const float2 zz = make_float2(-z, -z);
 #pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) {
-          const float f = kM == 64 ? (half ? f1 : f0) : i < 2 ? f0 : f1;
-          uint32_t w[16];
+          for (int i = 0; i < kCols / 32; ++i) {
+            const float f = kM == 64 ? (half ? f1 : f0) : i < 2 ? f0 : f1;
+            uint32_t w[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            float2 y = fma2(make_float2(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), make_float2(f, f), zz);
-            y.x = ex2(y.x);
-            y.y = ex2(y.y);
-            w[e] = f16x2(y.x, y.y);
-            sum[e & 3] = add2(sum[e & 3], y);
+            for (int e = 0; e < 16; ++e) {
+              float2 y = fma2(make_float2(x[32 * i + 2 * e], x[32 * i + 2 * e + 1]), make_float2(f, f), zz);
+              y.x = ex2(y.x);
+              y.y = ex2(y.y);
+              w[e] = f16x2(y.x, y.y);
+              sum[e & 3] = add2(sum[e & 3], y);
+            }
+            if constexpr (kM == 64) {      // over the scores
+              tc::tmem_st16x2_16<32>(s_at + 16 * i, w);
+            } else {
+              tc::tmem_st8(s_at + 16 * i, w);
+              tc::tmem_st8(s_at + 16 * i + 8, w + 8);
+            }
           }
-          if constexpr (kM == 64) {      // over the scores
-            tc::tmem_st16x2_16<32>(s_at + 16 * i, w);
+          sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+          l += sum[0].x + sum[0].y;
+          tc::tmem_st_wait();
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&m.p_full[grp]);
+        }
+        if (kM == 64) l += __shfl_xor_sync(0xffffffffu, l, 16);
+        await_warp(&m.o_full[grp], outs++ & 1, m);
+        tc::fence_after_sync();
+        if ((w.take - grp0 + kBy - 1) / kBy > kRun) {
+          // ---- a run's sums: with those of earlier ones, to the workspace or, at last, back into TMEM
+          const bool more = j / kBy > kRun, last = j >= w.take;
+          const long long at = ((long long)blockIdx.x * (aside ? 1 : 2) + (!aside && w.begins() ? 1 : 0)) * p.most + row;
+          float2* ml = (aside ? p.second_ml : p.ml) + at;
+          float* run = (aside ? p.second : p.o) + at * D + half * kDims;
+          float2 old = make_float2(-INFINITY, 0.f);
+          if (real && more) old = *ml;
+          const float back = old.x == top ? 1.f : ex2(old.x - top);
+          l += old.y * back;
+          __syncwarp();
+          if (real && half == 0) *ml = make_float2(top, l);
+#pragma unroll 1
+          for (int i = 0; i < kDims; i += 32) {
+            float v[32];
+            load_o(o_at + i, v);
+            tmem_arrived(v);
+            if (real && more) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                float u[8];
+                ldg256(run + i + e, u);
+#pragma unroll
+                for (int d = 0; d < 8; ++d) v[e + d] += u[d] * back;
+              }
+            }
+            __syncwarp();
+            if (last) {
+              store_o(o_at + i, v);
+            } else if (real) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) stg256(run + i + e, reinterpret_cast<const uint32_t*>(v + e));
+            }
+          }
+          if (last) {
+            tc::tmem_st_wait();
           } else {
-            tc::tmem_st8(s_at + 16 * i, w);
-            tc::tmem_st8(s_at + 16 * i + 8, w + 8);
+            l = 0.f;
+            any = false;
           }
         }
-        sum[0] = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-        l += sum[0].x + sum[0].y;
-        if ((j / (SPLIT ? 2 : 1)) % kRun == kRun - 1) {      // small weights of a long stream count beside a sum near 1
-          held += l;
-          l = 0.f;
-        }
-        tc::tmem_st_wait();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&m.p_full[grp]);
       }
       // ---- the segment's result, or its part
       const bool two = SPLIT && w.take > 1;                  // both groups have steps
-      l += held;
-      if (kM == 64) l += __shfl_xor_sync(0xffffffffu, l, 16);
       if (SPLIT && grp == 1 && half == 0) m.ml[r] = make_float2(top, l);
-      if (SPLIT) named_sync(1, 256);
-      if (!SPLIT || grp == 0) {
-        await_warp(&m.o_full[grp], outs++ & 1, m);
-        if (two) await_warp(&m.o_full[1], outs1++ & 1, m);
+      if (SPLIT) {
+        tc::fence_before_sync();
+        named_sync(1, 256);
         tc::fence_after_sync();
+      }
+      if (!SPLIT || grp == 0) {
+        const long long at = ((long long)blockIdx.x * 2 + (w.begins() ? 1 : 0)) * p.most + row;
         float a0 = 1.f, a1 = 0.f;
         if (two) {
           const float2 o = m.ml[r];
@@ -774,7 +832,6 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         const float inv = whole ? (l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
         const bool nan = m.nan[w.n & 3] != 0;
         const long long out_row = (long long)tok * a.Hq + hq;
-        const long long at = ((long long)blockIdx.x * 2 + (w.begins() ? 1 : 0)) * p.most + row;
 #pragma unroll 1
         for (int i0 = 0; i0 < kDims; i0 += 32) {
           const int i = half * kDims + i0;                   // the channels' first

@@ -61,3 +61,14 @@ def test_sum_of_small_weights_beside_a_large_one(form, lead):
     the result's own size."""
     for _, err, e in step(form, (1 << 20) - 5, lead, 0.0):
         assert float(err.abs().max()) <= e + 2 * 2.0 ** -14 + 2.0 ** -16 + 2.0 ** -21 * (lead + 2), float(err.abs().max())
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n", [(1 << 14) - 3, 1 << 15, (1 << 15) + 130, 1 << 16, (1 << 16) + 1, (1 << 17) + 300, (1 << 20) - 5])
+def test_sums_of_many_values_of_one_sign(form, n):
+    """The output where nothing cancels: weights in fp16 (2^-11), 2^-14 for the exponentials, the logits twice, the sum as
+    above.  Tiles: the tensor core cuts sums off rather than rounding them, at most a unit of 2^-23 for each of eight products a step,
+    of 256 steps: 2^-12.  Streams: up to 2^15 additions, each half a step off either way: six standard deviations of
+    their sum, 6 x 2^7.5 x 2^-24 / sqrt(3) < 2^-14."""
+    for err, _, e in step(form, n, 2, 1.0):
+        assert float(err.abs().max()) <= 2.0 ** -11 + 2.0 ** -14 + 2 * e + 2 * 2.0 ** -14 + 2.0 ** -12, (float(err.mean()), float(err.abs().max()))

@@ -20,8 +20,8 @@ def order(tmp_path_factory):
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
 
-    def ops(by, grp, segments):
-        out = subprocess.run([exe, str(by), str(grp), *map(str, segments)], capture_output=True, text=True, check=True).stdout
+    def ops(by, grp, segments, run=128):
+        out = subprocess.run([exe, str(by), str(run), str(grp), *map(str, segments)], capture_output=True, text=True, check=True).stdout
         return [tuple(int(w) if w.isdigit() else w for w in line.split()) for line in out.splitlines()]
     return ops
 
@@ -31,34 +31,35 @@ def passes(done, use):
     return (done & 1) != (use & 1)
 
 
-def explore(order, by, segments):
+def explore(order, by, segments, run):
     """Every reachable state; raises AssertionError at the first wrong read or at a state in which nothing can go on.
 
     A state: the program counters of the loader, the converter, the two product warps and the two softmaxes; the copies
     under way; the products issued by each group that have not ended; the phases of each barrier that are over."""
     total = sum(segments)
     begin = [sum(segments[:i]) for i in range(len(segments) + 1)]
-    prod = [order(by, g, segments) for g in (0, 1)]
+    prod = [order(by, g, segments, run) for g in (0, 1)]
     own = [[st for i, n in enumerate(segments) for st in range(begin[i], begin[i] + n) if by == 1 or (st - begin[i]) % 2 == g] for g in (0, 1)]
     # the loader: wait for the stage, copy (keys, then values); the converter: wait, free, wait, done
     load = [x for st in range(total) for x in (("k", st), ("v", st))]
     conv = [x for st in range(total) for x in (("take", st), ("give", st))]
-    # a softmax: at a segment's begin it hands out Q (the first group's alone with by = 2), then a step's weights, and at
-    # the end waits for the outputs (the first group also for the second's)
+    # a softmax: at a segment's begin it hands out Q (the first group's alone with by = 2), then a step's weights, after a run
+    # waits for its sums and reads them, and at the end the two meet
     soft = [[], []]
     for g in (0, 1):
         for i, n in enumerate(segments):
             mine = [st for st in own[g] if begin[i] <= st < begin[i + 1]]
             if by == 1 or g == 0:
                 soft[g].append(("query", i))
-            soft[g] += [("weigh", st) for st in mine]
-            if by == 2:
-                soft[g].append(("meet", i))
-            if by == 1 or g == 0:
-                soft[g].append(("out", i))
-            if by == 2:
-                soft[g].append(("meet again", i))
+            for k, st in enumerate(mine):
+                soft[g].append(("weigh", st))
+                if k % run == run - 1 or k + 1 == len(mine):
+                    soft[g].append(("run", (i, k // run)))
+            if by == 2:                                      # before and after the first reads the second's sums
+                soft[g] += [("meet", i), ("meet again", i)]
     count = lambda g, st: own[g].index(st)           # the how-manieth step of its group
+    # sums that group g gives out before a segment
+    before = lambda g, i: sum(-(-sum(begin[k] <= st < begin[k + 1] for st in own[g]) // run) for k in range(i))
     empties = {1: 2, 2: 1}[by]                       # arrivals that free a stage of keys (and of fp16 values)
     # state: (load pc, conv pc, prod pcs, soft pcs, copies, queues, bars); bars: phases over, and arrivals of the open phase
     names = ([("k_full", b) for b in range(RING)] + [("k_empty", b) for b in range(RING)] + [("v_full", b) for b in range(RING)]
@@ -129,20 +130,24 @@ def explore(order, by, segments):
                     assert done(bars, ("vf_full", st & 1)) == (st >> 1) + 1, f"fp16 values of step {st} are not there"
                     assert done(bars, ("p_full", g)) == count(g, st) + 1, f"weights of step {st} are not there"
                     q = queues[:g] + (queues[g] + (op,),) + queues[g + 1:]
+                    k = next(k for k, x in enumerate(soft[g]) if x == ("weigh", st))
+                    if not op[2] and k and soft[g][k - 1][0] == "run":
+                        assert sp[g] >= k, f"step {st} overwrites sums that are not read"
+                elif name == "out":
+                    q = queues[:g] + (queues[g] + (op,),) + queues[g + 1:]
                 elif name == "pass":
                     after = arrive(bars, ("turn", 1 - g))
                 if go:
                     yield (lp, cp, tuple(x + (i == g) for i, x in enumerate(pp)), sp, copies, q, after)
             if queues[g]:                                    # a group's products end in their order
-                name, st = queues[g][0]
+                name, st = (*queues[g][0], None)[:2]
                 q = queues[:g] + (queues[g][1:],) + queues[g + 1:]
                 if name == "scores":
                     after = arrive(arrive(bars, ("s_full", g)), ("k_empty", st % RING))
+                elif name == "out":
+                    after = arrive(bars, ("o_full", g))
                 else:
                     after = arrive(bars, ("vf_empty", st & 1))
-                    i = next(i for i in range(len(segments)) if begin[i] <= st < begin[i + 1])
-                    if st + by >= begin[i + 1]:
-                        after = arrive(after, ("o_full", g))
                 yield (lp, cp, pp, sp, copies, q, after)
             if sp[g] < len(soft[g]):
                 kind, x = soft[g][sp[g]]
@@ -156,13 +161,9 @@ def explore(order, by, segments):
                         after = arrive(bars, ("p_full", g))
                 elif kind in ("meet", "meet again"):
                     go = sp[1 - g] < len(soft[1 - g]) and soft[1 - g].index((kind, x)) <= sp[1 - g] or sp[1 - g] == len(soft[1 - g])
-                elif by == 1:
-                    go = passes(done(bars, ("o_full", g)), x)
                 else:
-                    go = passes(done(bars, ("o_full", 0)), x)
-                    if segments[x] > 1:
-                        two = sum(n > 1 for n in segments[:x])
-                        go = go and passes(done(bars, ("o_full", 1)), two)
+                    go = passes(done(bars, ("o_full", g)), before(g, x[0]) + x[1])
+                    assert not go or done(bars, ("o_full", g)) == before(g, x[0]) + x[1] + 1, "a run's sums are not there"
                 if go:
                     yield (lp, cp, pp, tuple(x + (i == g) for i, x in enumerate(sp)), copies, queues, after)
 
@@ -186,7 +187,17 @@ def explore(order, by, segments):
                                          (2, [5, 3]), (2, [2, 2, 4]), (2, [1, 5]), (2, [1, 1, 2, 4]), (2, [2, 1, 4]), (2, [1, 1, 1, 3]),
                                          (1, [1]), (1, [4]), (1, [5]), (1, [2, 3])])
 def test_no_product_reads_what_is_not_there(order, by, segments):
-    explore(order, by, segments)
+    explore(order, by, segments, 128)
+
+
+@pytest.mark.parametrize("by,segments", [(2, [4]), (2, [5]), (2, [6]), (2, [7]), (2, [5, 4]), (2, [1, 5]), (2, [6, 2]), (1, [2]), (1, [3]), (1, [5]), (1, [3, 2])])
+def test_sums_of_runs_are_read_before_the_next(order, by, segments):
+    """The same with runs of two steps of a group: each run's sums are whole when they are read and stay until then."""
+    explore(order, by, segments, 2)
+    for g in (0, 1):
+        adds = [o[2] for o in order(by, g, segments, 2) if o[0] == "products"]
+        mine = [len(range(g if by == 2 else 0, n, by)) for n in segments]
+        assert adds == [k % 2 for n in mine for k in range(n)]
 
 
 @pytest.mark.parametrize("by,segments", [(1, [3, 2]), (2, [3, 1, 4])])
