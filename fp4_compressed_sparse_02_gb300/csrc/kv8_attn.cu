@@ -33,6 +33,10 @@ namespace {
 // mma.sync (100 instructions more a half page than fp16 ones with their conversions: 1.17 ms); kLeast of 1 to 8 is all the
 // same at one row.
 constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
+// Weights are 2^15 times exp2(logit - maximum), so that fp16 reaches down to 2^-40 of the largest: a million tokens that are
+// smaller than that count for nothing.  Without the factor it reaches 2^-25, and behind a token that leads by 17 nats all
+// others were lost.
+constexpr float kWeight = 15.f, kWeightUndo = 1.f / 32768.f;
 
 // CTAs an SM.  Three, at 168 registers a thread and two stages a warp, where 8 rows have lists and pages come from L2
 // (2048 rows over 32 pages each: 0.95 ms against 1.10); two, with three stages, where the bytes come from memory (64 sequences
@@ -281,7 +285,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
             bp = page;
             const long long ph = (long long)page * Hkv + h;
             bk[1] = c.k_scale[ph];
-            bv[1] = c.v_scale[ph];
+            bv[1] = c.v_scale[ph] * kWeightUndo;
           }
         }
       }
@@ -425,8 +429,8 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
         }
 #pragma unroll
         for (int e = kLane0; e < kLane1; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-        const float mn = fmaxf(m[i], top), z = mn == -INFINITY ? 0.f : mn;
-        alpha[i] = ex2(m[i] - z);
+        const float mn = fmaxf(m[i], top), z0 = mn == -INFINITY ? 0.f : mn, z = z0 - kWeight;
+        alpha[i] = ex2(m[i] - z0);
         m[i] = mn;
         float sum = 0.f;
 #pragma unroll
@@ -585,6 +589,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
       l[i] += held[i];
 #pragma unroll
       for (int e = kLane0; e < kLane1; e <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], e);
+      l[i] *= kWeightUndo;
       const int r = own(i);
       if (r < nrows) {
         // a piece of the row's channels: an eighth, of lane g, or a quarter, of columns 2 q4 and 2 q4 + 1 of every tile

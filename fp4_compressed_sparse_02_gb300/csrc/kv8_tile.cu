@@ -32,6 +32,9 @@ constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a
 // near 1 leaves no room for small ones.  A run's O is off by 2^-12 at most.  4096 new tokens at 32K: 3.35 ms, as without
 // runs; 3.43 with runs of 128 steps, 3.69 of 64 (before both ends of a run shared their code).
 constexpr int kRun = 256;
+// Weights are 2^kWeight times exp2(logit - top), and the maximum is up to 2^kFollow above top: together within fp16, which
+// reaches down to 2^-36 of a weight at top.
+constexpr float kWeight = 11.f, kFollow = 4.f, kWeightUndo = 1.f / 2048.f;
 constexpr int kOver = 12;                // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
@@ -714,9 +717,9 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           } else {
             now = fmaxf(fmaxf(mx[0], mx[1]) * f0, fmaxf(mx[2], mx[3]) * f1);
           }
-          // The maximum follows only when it grows by 2^8 or more: weights up to 2^8 are as exact in fp16, and O and the
-          // sum are rescaled a few times a row.
-          const bool follow = now > top + 8.f || (top == -INFINITY && now > top);
+          // The maximum follows only when it grows by more than 2^kFollow (a published method of attention kernels): weights
+          // above it are as exact in fp16, and O and the sum are rescaled a few times a row.
+          const bool follow = now > top + kFollow || (top == -INFINITY && now > top);
           if (__any_sync(0xffffffffu, follow)) {
             const float alpha = follow ? ex2(top - now) : 1.f;
             if (follow) top = now;
@@ -736,7 +739,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           any = true;
           const float z = top == -INFINITY ? 0.f : top;
           float2 sum[4] = {};
-          const float2 zz = make_float2(-z, -z);
+          const float2 zz = make_float2(kWeight - z, kWeight - z);
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
             const float f = kM == 64 ? (half ? f1 : f0) : i < 2 ? f0 : f1;
@@ -810,6 +813,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       }
       // ---- the segment's result, or its part
       const bool two = SPLIT && w.take > 1;                  // both groups have steps
+      l *= kWeightUndo;
       if (SPLIT && grp == 1 && half == 0) m.ml[r] = make_float2(top, l);
       if (SPLIT) {
         tc::fence_before_sync();
@@ -828,7 +832,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           top = n;
         }
         const bool whole = w.begins() && w.ends();
-        const float unit = m.unit[w.n & 3] * 0.0078125f;
+        const float unit = m.unit[w.n & 3] * (0.0078125f * kWeightUndo);
         const float inv = whole ? (l == 0.f ? 0.f : __fdiv_rn(1.f, l)) : 1.f;
         const bool nan = m.nan[w.n & 3] != 0;
         const long long out_row = (long long)tok * a.Hq + hq;

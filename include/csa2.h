@@ -758,12 +758,13 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * max_new: about how many new tokens the longest of the call's sequences has.  It only
  * picks the kernel, by max_new * G rows: results for any value stay within the precision below.
  * Precision: products on tensor-core operands with float32 accumulation.  Keys and values are
- * exact there, probabilities fp16 (2^-11 relative, 2^-25 of the largest).  Up to 16 rows each head's q
- * is fp16 times a power of two, exact within 2^-28 of its largest element.  Above, it is the sum of two
- * E4M3 numbers times a power of two, exact within 2^-9 of its largest element and to 2^-17 of that
- * below; and the values of a page whose scale is below 2^-22 of the largest value scale in sight
- * lose their last bits; and sums, which the tensor cores cut off rather than round, are off by up to 2^-12 of their
- * terms' magnitudes.  A NaN that a row does not see does not reach it.  Results repeat bit for bit.
+ * exact there, probabilities fp16: 2^-11 relative, and down to 2^-40 of the largest up to 16 rows, 2^-36
+ * above.  Up to 16 rows each head's q is fp16 times a power of two, exact within 2^-28 of its largest
+ * element.  Above, it is the sum of two E4M3 numbers times a power of two, exact within 2^-9 of its
+ * largest element and to 2^-17 of that below; the values of a page whose scale is below 2^-22 of the
+ * largest value scale in sight lose their last bits; and sums, which the tensor cores cut off rather
+ * than round, are off by up to 2^-12 of their terms' magnitudes.  A NaN that a row does not see does not
+ * reach it.  Results repeat bit for bit.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
  * window >= 0; S <= 2^18; T * Hq < 2^31.
  * -------------------------------------------------------------------------- */

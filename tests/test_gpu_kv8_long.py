@@ -17,8 +17,8 @@ FORMS = {"8 rows": (64, 1, 1, 1), "16 rows": (64, 12, 1, 1), "64 rows": (8, 8, 3
 
 def step(form, n, lead, sink_value, seed=0):
     """19 sequences of n tokens whose first token leads the others by about `lead` nats and has values `sink_value`; the
-    others' values lie in 0.5 .. 5.  Yields (error of out / |out|, error of lse, the logits' error bound), for every row of
-    the first and the last sequence."""
+    others' values lie in 0.5 .. 5.  Yields (error of out / |out|, error of lse, the logits' error bound, sum of values /
+    (sum of weights x |out|), the largest weight being 1), for every row of the first and the last sequence."""
     H, G, new, hint = FORMS[form]
     S = 19
     r = np.random.default_rng(seed)
@@ -50,7 +50,8 @@ def step(form, n, lead, sink_value, seed=0):
         got = out[t].reshape(H, G, D).double()
         # D + 8 roundings of a logit's sum
         e = (D + 8) * 2.0 ** -24 * float((gpu(np.abs(q[t]).reshape(H, G, D).astype(np.float64)).sum(-1).amax() * 8) * D ** -0.5)
-        yield (got - want) / want, lse[t].reshape(H, G).double() - (top[..., 0, 0] + z.log()), e
+        values = torch.einsum("pt,phtd->hd", times, vd)[:, None] / (z[..., None] * want)
+        yield (got - want) / want, lse[t].reshape(H, G).double() - (top[..., 0, 0] + z.log()), e, values
 
 
 @pytest.mark.parametrize("form", FORMS)
@@ -59,7 +60,7 @@ def test_sum_of_small_weights_beside_a_large_one(form, lead):
     """The logarithm of the sum.  A sum of sums: at most 2^10 terms one after the other at either level, each half a step of
     float32 (2^-24) off, relative to the whole; 2^-16 for the exponentials, the logarithm and the merging, 2^-21 for
     the result's own size."""
-    for _, err, e in step(form, (1 << 20) - 5, lead, 0.0):
+    for _, err, e, _ in step(form, (1 << 20) - 5, lead, 0.0):
         assert float(err.abs().max()) <= e + 2 * 2.0 ** -14 + 2.0 ** -16 + 2.0 ** -21 * (lead + 2), float(err.abs().max())
 
 
@@ -70,5 +71,17 @@ def test_sums_of_many_values_of_one_sign(form, n):
     above.  Tiles: the tensor core cuts sums off rather than rounding them, at most a unit of 2^-23 for each of eight products a step,
     of 256 steps: 2^-12.  Streams: up to 2^15 additions, each half a step off either way: six standard deviations of
     their sum, 6 x 2^7.5 x 2^-24 / sqrt(3) < 2^-14."""
-    for err, _, e in step(form, n, 2, 1.0):
+    for err, _, e, _ in step(form, n, 2, 1.0):
         assert float(err.abs().max()) <= 2.0 ** -11 + 2.0 ** -14 + 2 * e + 2 * 2.0 ** -14 + 2.0 ** -12, (float(err.mean()), float(err.abs().max()))
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("n", [1 << 12, (1 << 20) - 5])
+@pytest.mark.parametrize("lead", [12, 15, 17, 18, 20, 22])
+def test_values_of_small_weights_beside_a_large_one(form, n, lead):
+    """The first token has the largest weight by far and values of zero: the output is the others' alone.  The bound is that of
+    the sums above, and 2^-40 (tiles 2^-36) of the largest weight for each other one, where fp16 ends."""
+    least = 2.0 ** -40 if form in ("8 rows", "16 rows") else 2.0 ** -36
+    for err, _, e, values in step(form, n, lead, 0.0):
+        bound = 2.0 ** -11 + 2.0 ** -14 + 2 * e + 2 * 2.0 ** -14 + 2.0 ** -12 + least * values
+        assert bool((err.abs() <= bound).all()), (float(err.abs().max()), float((err.abs() / bound).max()))
