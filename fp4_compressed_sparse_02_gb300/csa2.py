@@ -10,6 +10,7 @@ in, together with a pre-sized Workspace, to capture calls in a CUDA graph).
 import ctypes
 import math
 import struct
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -143,10 +144,12 @@ class PagedCache:
 
 class Workspace:
     """Grow-only device scratch buffer handed to the library calls.  Calls that may run at the same time (on two
-    streams, or in two graphs that are replayed side by side) need one each."""
+    streams, or in two graphs that are replayed side by side) need one each.  Threads may share one on one stream: a call
+    holds its lock until all of its kernels are launched."""
 
     def __init__(self, device="cuda"):
         self.device = device
+        self.lock = threading.RLock()
         self.buf = torch.empty(0, dtype=torch.uint8, device=device)
         self.captured = False              # a graph holds its address
         self.outgrown = []                 # buffers whose addresses graphs hold
@@ -171,9 +174,7 @@ def _ws(ws, device):
     if ws is not None:
         return ws
     key = str(device)
-    if key not in _default_ws:
-        _default_ws[key] = Workspace(device)
-    return _default_ws[key]
+    return _default_ws.get(key) or _default_ws.setdefault(key, Workspace(device))
 
 
 def _call(fn, args, ws, device):
@@ -185,9 +186,11 @@ def _call(fn, args, ws, device):
     L = _lib.lib()
     need = ctypes.c_size_t(0)
     _lib.check(getattr(L, fn + "_workspace")(ctypes.byref(args), ctypes.byref(need)))
-    buf = _ws(ws, device).get(need.value)
-    _on_device(buf, dev, "ws")
-    _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream(dev)))
+    ws = _ws(ws, device)
+    with ws.lock:
+        buf = ws.get(need.value)
+        _on_device(buf, dev, "ws")
+        _lib.check(getattr(L, fn)(ctypes.byref(args), ctypes.c_void_p(buf.data_ptr()), need.value, _stream(dev)))
 
 
 def compress_quant(cache: PagedCache, seq, entry, *, m=1, C=None, Z=None, H=None, W_kv=None, W_z=None,
@@ -677,6 +680,10 @@ _KV8_NAMES = ("k plane", "v plane", "k_scale", "v_scale", "mean", "mean_scale", 
 _ws_of = {}                                # the default workspaces by device number and stream
 
 
+def _stream_ws(dev, stream, device):
+    return _ws_of.get((dev, stream)) or _ws_of.setdefault((dev, stream), Workspace(device))
+
+
 def _launch_ws(fn, packed, ws, device, dev):
     """_launch of a call that takes a workspace (ws None: the stream's own, or, in a capture, the graph's).  It is offered
     the one there is, and asked what it needs only if that is too small."""
@@ -695,19 +702,18 @@ def _launch_ws(fn, packed, ws, device, dev):
         _lib.check(call(packed, buf.data_ptr(), need.value, stream))
         return
     if ws is None:
-        ws = _ws_of.get((dev, stream))
-        if ws is None:
-            ws = _ws_of[dev, stream] = Workspace(device)
-    buf = ws.get(0)
-    if buf.get_device() != dev:
-        _on_device(buf, dev, "ws")
-    status = call(packed, buf.data_ptr(), buf.numel(), stream)
-    if status == _TOO_SMALL:
-        _lib.check(getattr(L, fn + "_workspace")(packed, ctypes.byref(need)))
-        buf = ws.get(need.value)
-        status = call(packed, buf.data_ptr(), need.value, stream)
-    if status:
-        _lib.check(status)
+        ws = _stream_ws(dev, stream, device)
+    with ws.lock:                              # one call's kernels behind another's, not in between
+        buf = ws.get(0)
+        if buf.get_device() != dev:
+            _on_device(buf, dev, "ws")
+        status = call(packed, buf.data_ptr(), buf.numel(), stream)
+        if status == _TOO_SMALL:
+            _lib.check(getattr(L, fn + "_workspace")(packed, ctypes.byref(need)))
+            buf = ws.get(need.value)
+            status = call(packed, buf.data_ptr(), need.value, stream)
+        if status:
+            _lib.check(status)
 
 
 _TOO_SMALL = 3                             # CSA2_ERR_WORKSPACE_TOO_SMALL
