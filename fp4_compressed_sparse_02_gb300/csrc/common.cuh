@@ -61,6 +61,14 @@ inline cudaError_t launch_k_late(void (*kernel)(KArgs...), dim3 grid, dim3 block
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// A load that stays behind pdl_wait(), which ld.global.nc and __ldg do not promise: the previous kernel on the stream may
+// be the one that writes the table.
+__device__ __forceinline__ int ld_s32(const int* p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ void raise_error(unsigned int* word, unsigned int bit) {
   atomicOr(word, bit);
 }

@@ -5,10 +5,14 @@
 
 namespace csa2 {
 
+// Every load of tables, rows, scales and bytes is an ordinary one behind pdl_wait(): the kernel before on the stream may be the
+// one that writes them, and it still runs when this one's CTAs start.  (Page ids by ld_s32: where the compiler may move
+// them, the tiles' conversion of the values comes out slower, 342 us against 274 for 32 x 6 tokens.)
+
 // The sequence of row t: s with start[s] <= t < start[s+1], or -1 for a row of padding.  Whatever
 // start holds, a result >= 0 is below S and satisfies both inequalities.  By a whole warp, for one t: 32 starts at a
 // time, so that up to 32 sequences take one round of loads and 1024 two.
-__device__ __forceinline__ int find_seq(const int* __restrict__ start, int S, int t) {
+__device__ __forceinline__ int find_seq(const int* start, int S, int t) {
   const int lane = threadIdx.x & 31;
   int lo = 0, hi = S;                    // start[lo] <= t < start[hi], once both have been looked at
   const int last = start[S];
@@ -36,7 +40,7 @@ __device__ __forceinline__ int row_pos(const csa2_kv8_cache& c, const int* start
 
 // Page id of page j (< max_pages) of sequence s, or -1 (with an error bit).
 __device__ __forceinline__ int page_id(const csa2_kv8_cache& c, int s, int j, unsigned int* err) {
-  const int page = __ldg(c.page_table + (long long)s * c.max_pages + j);
+  const int page = ld_s32(c.page_table + (long long)s * c.max_pages + j);
   if (page < 0 || page >= c.num_pages) {
     raise_error(err, CSA2_DEVERR_PAGE_ID);
     return -1;

@@ -486,7 +486,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
         float top = 0.f;
         const int y1 = min((t.hi + kPage - 1) / kPage, 2 * (t.step + w.x + w.take));
         for (int y = max(t.lo / kPage, 2 * (t.step + w.x)) + r; y < y1; y += 128) {
-          const int id = __ldg(c.page_table + (long long)t.s * c.max_pages + y);
+          const int id = ld_s32(c.page_table + (long long)t.s * c.max_pages + y);
           if (id >= 0 && id < c.num_pages) top = fmaxf(top, c.v_scale[(long long)id * c.Hkv + w.h]);
         }
 #pragma unroll
@@ -860,7 +860,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
               const int b = max(max(u0, lo), side ? max(t.hi_min, t.lo_max) : t.lo), e = min(min(u1, hi), side ? t.hi : t.lo_max);
 #pragma unroll 1
               for (int y = b; y < e; ++y) {
-                const int id = __ldg(c.page_table + (long long)t.s * c.max_pages + y / kPage);
+                const int id = ld_s32(c.page_table + (long long)t.s * c.max_pages + y / kPage);
                 if (id < 0 || id >= c.num_pages) continue;
                 const uint8_t* src = c.v + (((long long)id * c.Hkv + w.h) * kPage + y % kPage) * D + i;
 #pragma unroll 1

@@ -553,7 +553,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(const SelectParams 
       const int id = __shfl_sync(0xffffffffu, page, 8 * i + g);
       const uint4* m = reinterpret_cast<const uint4*>(c.mean + ((long long)(id < 0 ? 0 : id) * c.Hkv + h) * D + q4 * (D / 4));
 #pragma unroll
-      for (int e = 0; e < kW; ++e) w[i][e] = __ldg(m + e);
+      for (int e = 0; e < kW; ++e) w[i][e] = m[e];
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
