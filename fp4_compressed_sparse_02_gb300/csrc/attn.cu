@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(ATHREADS, 1) k_attn_chunk(AttnParams p) {
       if (j < tl) {
         int e = __ldg(p.topk + (long long)b * p.k + j);
         if (e >= 0) {
-          row = entry_row(p.cache, __ldg(p.seq_of + b), e, &g_err_attn);
+          row = entry_row(p.cache, ld_s32(p.seq_of + b), e, &g_err_attn);
           kind = row >= 0 ? 1 : 0;
           sc = kind ? 1.f : 0.f;
         }
@@ -593,7 +593,7 @@ __global__ void __cluster_dims__(tca::NCH, 1, 1) __launch_bounds__(tca::THREADS,
     const int j = chunk * KT + fkey, w = chunk * KW + (tid >> 3);
     const int tl = p.topk_len ? __ldg(p.topk_len + b) : p.k;
     const int e = (j < p.k) ? __ldg(p.topk + (long long)b * p.k + j) : -1;
-    const int sq = __ldg(p.seq_of + b);
+    const int sq = ld_s32(p.seq_of + b);
     const int wl = p.swa_max > 0 ? __ldg(p.swa_len + b) : 0;
     const long long r0 = p.swa_max > 0 ? (long long)__ldg(p.swa_start + b) + chunk * KW : 0;
     int page = -1;

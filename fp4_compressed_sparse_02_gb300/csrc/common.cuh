@@ -80,7 +80,7 @@ __device__ __forceinline__ long long entry_row(const csa2_cache& c, int s, long 
   long long p = e >> kPageShift;
   if (s < 0 || s >= c.num_seqs) { raise_error(err, CSA2_DEVERR_SEQ); return -1; }
   if (e < 0 || p >= c.max_pages) { raise_error(err, CSA2_DEVERR_PAGE_SLOT); return -1; }
-  int page = __ldg(c.page_table + (long long)s * c.max_pages + p);
+  int page = ld_s32(c.page_table + (long long)s * c.max_pages + p);
   if (page < 0 || page >= c.num_pages) { raise_error(err, CSA2_DEVERR_PAGE_ID); return -1; }
   return ((long long)page << kPageShift) | (e & (kPage - 1));
 }
@@ -95,7 +95,7 @@ __device__ __forceinline__ int entry_page_load(const csa2_cache& c, int s, long 
   if (s < 0 || s >= c.num_seqs) { raise_error(err, CSA2_DEVERR_SEQ); return -1; }
   if (e < 0 || p >= c.max_pages) { raise_error(err, CSA2_DEVERR_PAGE_SLOT); return -1; }
   slot_ok = true;
-  return __ldg(c.page_table + (long long)s * c.max_pages + p);
+  return ld_s32(c.page_table + (long long)s * c.max_pages + p);
 }
 __device__ __forceinline__ long long entry_row_of_page(const csa2_cache& c, int page, long long e, unsigned int* err) {
   if (page < 0 || page >= c.num_pages) { raise_error(err, CSA2_DEVERR_PAGE_ID); return -1; }

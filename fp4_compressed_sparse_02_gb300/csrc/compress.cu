@@ -348,8 +348,8 @@ __device__ __forceinline__ void quant_group_at(const QuantParams& p, long long g
 }
 
 __device__ __forceinline__ void quant_group(const QuantParams& p, long long g, int q, float* deq) {
-  const int ps = (p.d_rope > 0 && q * 16 >= p.d - p.d_rope) ? __ldg(p.pos + g) : 0;
-  quant_group_at(p, g, q, deq, ps, __ldg(p.seq + g), __ldg(p.entry + g));
+  const int ps = (p.d_rope > 0 && q * 16 >= p.d - p.d_rope) ? ld_s32(p.pos + g) : 0;
+  quant_group_at(p, g, q, deq, ps, ld_s32(p.seq + g), ld_s32(p.entry + g));
 }
 
 __global__ void __launch_bounds__(256) k_quant(QuantParams p) {
@@ -374,8 +374,8 @@ __device__ __forceinline__ void index_k_product(const csa2_cache& cache, const l
                                                 float* part, const uint16_t* __restrict__ Wik);
 
 template <int E, int DIK>
-__global__ void __launch_bounds__(256) k_index_k(csa2_cache cache, const int* __restrict__ seq,
-                                                 const int* __restrict__ entry, int G,
+__global__ void __launch_bounds__(256) k_index_k(csa2_cache cache, const int* seq,
+                                                 const int* entry, int G,
                                                  const uint16_t* __restrict__ Wik) {
   pdl_wait();
   pdl_trigger();
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(256) k_index_k(csa2_cache cache, const int* __
   const int g0 = blockIdx.x * E;
   if (tid < E) {
     const int g = g0 + tid;
-    rows[tid] = (g < G) ? entry_row(cache, __ldg(seq + g), __ldg(entry + g), &g_err_compress) : -1;
+    rows[tid] = (g < G) ? entry_row(cache, ld_s32(seq + g), ld_s32(entry + g), &g_err_compress) : -1;
   }
   __syncthreads();
   for (int i = tid; i < E * d / 2; i += 256) {
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(256) k_quant_index_k(QuantParams p, const uint
   __shared__ long long rows[1];
   const long long g = blockIdx.x;
   if (threadIdx.x < p.d / 16) quant_group(p, g, threadIdx.x, deq);
-  if (threadIdx.x == 0) rows[0] = entry_row(p.cache, __ldg(p.seq + g), __ldg(p.entry + g), &g_err_compress);
+  if (threadIdx.x == 0) rows[0] = entry_row(p.cache, ld_s32(p.seq + g), ld_s32(p.entry + g), &g_err_compress);
   __syncthreads();
   index_k_product<1, DIK>(p.cache, rows, deq, part, Wik);
 }
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(256) k_append_quant_index_k(AppendParams ap, c
   float* part = qk_sm + ap.q.d;                  // [8][DIK]
   __shared__ long long rows[1];
   const int b = blockIdx.x, tid = threadIdx.x, d = ap.q.d, m = ap.q.m;
-  const int s = __ldg(ap.q.seq + b), t = __ldg(ap.tok_pos + b);
+  const int s = ld_s32(ap.q.seq + b), t = ld_s32(ap.tok_pos + b);
   if (s < 0 || s >= ap.q.cache.num_seqs || t < 0) {           // the same for the whole CTA
     if (tid == 0) raise_error(&g_err_compress, t < 0 ? CSA2_DEVERR_POS : CSA2_DEVERR_SEQ);
     return;

@@ -295,12 +295,12 @@ __global__ void __launch_bounds__(256, 2) k_full_scan(ScanParams p) {
   for (long long u = (long long)blockIdx.x * 8 + warp; u < total; u += (long long)gridDim.x * 8) {
   const int b = (int)(u / p.NB);
   const int j = (int)(u % p.NB);
-  int n = __ldg(p.n_vis + b);
+  int n = ld_s32(p.n_vis + b);
   if (n < 0 || n > p.max_n) {
     if (lane == 0 && j == 0) raise_error(&g_err_index, CSA2_DEVERR_N_VIS);
     n = max(0, min(n, p.max_n));
   }
-  const int s = __ldg(p.seq_of + b);
+  const int s = ld_s32(p.seq_of + b);
   const long long lo = ((long long)j * n) / p.NB;
   const long long hi = ((long long)(j + 1) * n) / p.NB;
   const int P = p.P;
@@ -433,12 +433,12 @@ __global__ void __launch_bounds__(256, 2) k_full_scan_short(ScanParams p) {
   // persistent: warp w of CTA x takes units u = 8 x + w, + 8 gridDim.x, ... (u = b segs + seg)
   for (long long u = (long long)blockIdx.x * 8 + warp; u < total; u += (long long)gridDim.x * 8) {
     const int b = (int)(u / segs), j0 = (int)(u % segs) * SEG;
-    int n = __ldg(p.n_vis + b);
+    int n = ld_s32(p.n_vis + b);
     if (n < 0 || n > p.max_n) {
       if (lane == 0 && j0 == 0) raise_error(&g_err_index, CSA2_DEVERR_N_VIS);
       n = max(0, min(n, p.max_n));
     }
-    const int s = __ldg(p.seq_of + b);
+    const int s = ld_s32(p.seq_of + b);
     if (b != fb) {
       const uint8_t* qb = reinterpret_cast<const uint8_t*>(F8 ? (const void*)p.q8 : (const void*)p.q) +
                           (long long)b * p.H_i * DK * QB;
@@ -553,17 +553,17 @@ __global__ void __launch_bounds__(256, 2) k_full_scan_g(ScanParams p) {
   for (long long u = (long long)blockIdx.x * 8 + warp; u < total; u += (long long)gridDim.x * 8) {
     const int grp = (int)(u / p.NB), j = (int)(u % p.NB);
     const int b0 = grp * G;
-    const int s = __ldg(p.seq_of + b0);
+    const int s = ld_s32(p.seq_of + b0);
     int n[G], lo[G], hi[G];
     int rlo = 0x7fffffff, rhi = 0;
 #pragma unroll
     for (int q = 0; q < G; ++q) {
-      int nq = __ldg(p.n_vis + b0 + q);
+      int nq = ld_s32(p.n_vis + b0 + q);
       if (nq < 0 || nq > p.max_n) {
         if (lane == 0 && j == 0) raise_error(&g_err_index, CSA2_DEVERR_N_VIS);
         nq = max(0, min(nq, p.max_n));
       }
-      if (q > 0 && __ldg(p.seq_of + b0 + q) != s && lane == 0 && j == 0) raise_error(&g_err_index, CSA2_DEVERR_SEQ);
+      if (q > 0 && ld_s32(p.seq_of + b0 + q) != s && lane == 0 && j == 0) raise_error(&g_err_index, CSA2_DEVERR_SEQ);
       n[q] = nq;
       lo[q] = (int)(((long long)j * nq) / p.NB);
       hi[q] = (int)(((long long)(j + 1) * nq) / p.NB);
@@ -861,7 +861,7 @@ __global__ void __cluster_dims__(NCL, 1, 1) __launch_bounds__(CT, 512 / CT) k_se
   const int rank = (int)tc::cluster_ctarank();
   int P;
   if (p.n_vis) {
-    int n = __ldg(p.n_vis + b);
+    int n = ld_s32(p.n_vis + b);
     n = max(0, min(n, p.max_n));
     P = min(n, p.stride);
   } else {
@@ -898,7 +898,7 @@ __global__ void __cluster_dims__(NCL, 1, 1) __launch_bounds__(CT, 512 / CT) k_se
     constexpr int U = 4 * TPI;                     // rows per lane per iteration
     constexpr int NT = CL_SLICE / (32 * TPI) / (CL_THREADS / 32);   // iterations per warp: 8 (bf16), 4 (FP8)
     const int g = lane >> 2, c = lane & 3;
-    const int sq = __ldg(sp.seq_of + b);
+    const int sq = ld_s32(sp.seq_of + b);
     // as in the Full scan: more than two head groups stream their Q fragments from L1
     constexpr bool STREAM_Q = NHG > 2;
     constexpr int NHG_REG = STREAM_Q ? 1 : NHG;
@@ -1077,7 +1077,7 @@ __global__ void __launch_bounds__(C1_THREADS, 3) k_select_cta(SelectParams p) {
   const int tid = threadIdx.x;
   const int b = blockIdx.x;
   for (int i = tid; i < 4 * 256; i += C1_THREADS) (&hist[0][0])[i] = 0;
-  const int n = max(0, min(__ldg(p.n_vis + b), p.max_n));
+  const int n = max(0, min(ld_s32(p.n_vis + b), p.max_n));
   const int P = min(n, p.stride);
   const long long rowb = (long long)b * p.stride;
   const int k = p.k;

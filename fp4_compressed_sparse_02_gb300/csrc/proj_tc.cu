@@ -186,9 +186,9 @@ __global__ void __launch_bounds__(ptc::THREADS, 1)
         long long erow = -1;
         int ps = -1;
         if (writer && g < ep.G) {
-          erow = entry_row(ep.cache, __ldg(ep.seq + g), __ldg(ep.entry + g), &g_err_proj);
+          erow = entry_row(ep.cache, ld_s32(ep.seq + g), ld_s32(ep.entry + g), &g_err_proj);
           if (ep.d_rope > 0 && cbase + CW > d - ep.d_rope) {
-            ps = __ldg(ep.pos + g);
+            ps = ld_s32(ep.pos + g);
             if (ps < 0 || ps >= ep.rope_max_pos) {
               raise_error(&g_err_proj, CSA2_DEVERR_POS);
               ps = -1;
@@ -281,7 +281,7 @@ constexpr uint32_t MAX_POLL = 1u << 24;
 }  // namespace iktc
 
 __global__ void __launch_bounds__(iktc::THREADS, 1)
-    k_index_k_tc(csa2_cache cache, const int* __restrict__ seq, const int* __restrict__ entry, int G,
+    k_index_k_tc(csa2_cache cache, const int* seq, const int* entry, int G,
                  const uint16_t* __restrict__ Wik) {
   using namespace iktc;
   pdl_wait();
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(iktc::THREADS, 1)
   }
   if (tid < M) {
     const int g = blockIdx.x * M + tid;
-    rows[tid] = (g < G) ? entry_row(cache, __ldg(seq + g), __ldg(entry + g), &g_err_proj) : -1;
+    rows[tid] = (g < G) ? entry_row(cache, ld_s32(seq + g), ld_s32(entry + g), &g_err_proj) : -1;
   }
   tc::fence_before_sync();
   __syncthreads();

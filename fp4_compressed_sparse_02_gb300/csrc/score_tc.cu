@@ -61,9 +61,9 @@ __device__ __forceinline__ void unit_span(const ScoreParams& p, int u, int& qt, 
   qt = u / p.nchunks;
   const int ch = u % p.nchunks;
   const int b = qt * p.QT + lane;
-  const int n = lane < p.QT ? max(0, min(__ldg(p.n_vis + b), p.max_n)) : 0;
+  const int n = lane < p.QT ? max(0, min(ld_s32(p.n_vis + b), p.max_n)) : 0;
   const int nmax = __reduce_max_sync(0xffffffffu, n);
-  seq = __ldg(p.seq_of + qt * p.QT);
+  seq = ld_s32(p.seq_of + qt * p.QT);
   t0 = ch * p.chunk;
   t1 = min(t0 + p.chunk, (nmax + stc::BM - 1) / stc::BM);
 }
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(stc::THREADS, 1)
       unit_span(p, u, qt, t0, t1, seq);
       if (t1 <= t0) continue;
       // the queries of a tile share one sequence (a group of the call)
-      if (__any_sync(0xffffffffu, lane < p.QT && __ldg(p.seq_of + qt * p.QT + lane) != seq) && lane == 0)
+      if (__any_sync(0xffffffffu, lane < p.QT && ld_s32(p.seq_of + qt * p.QT + lane) != seq) && lane == 0)
         raise_error(&g_err_score, CSA2_DEVERR_SEQ);
       if (lane == 0) {
         if (ul > 0 && !tc::mbar_wait(bempty, (uint32_t)((ul - 1) & 1), MAX_POLL)) {
@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(stc::THREADS, 1)
         const int slot = 2 * t0 + 32 * h + lane;
         int v = 0;
         if (seq_ok && slot < 2 * t1 && slot < p.max_pages) {
-          v = __ldg(p.page_table + (long long)seq * p.max_pages + slot);
+          v = ld_s32(p.page_table + (long long)seq * p.max_pages + slot);
           if (v < 0 || v >= p.num_pages) {
             raise_error(&g_err_score, CSA2_DEVERR_PAGE_ID);
             v = 0;
@@ -295,7 +295,7 @@ __device__ __forceinline__ int bt_pad(int i) { return i + (i >> 5); }
 __host__ __device__ constexpr int bt_warp_floats(int per_blk) { return 32 * per_blk + per_blk + 1; }
 template <int P>
 __global__ void __launch_bounds__(BT_WARPS * 32) k_block_topp(const float* __restrict__ S, int ldS,
-                                                              const int* __restrict__ n_vis, int max_n, int B, int NB,
+                                                              const int* n_vis, int max_n, int B, int NB,
                                                               int wfloats, int* __restrict__ pool,
                                                               float* __restrict__ pool_score) {
   pdl_wait();
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(BT_WARPS * 32) k_block_topp(const float* __res
   const long long gw = (long long)blockIdx.x * BT_WARPS + warp;
   if (gw >= (long long)B * segs) return;
   const int b = (int)(gw / segs), j0 = (int)(gw % segs) * 32;
-  const int n = max(0, min(__ldg(n_vis + b), max_n));
+  const int n = max(0, min(ld_s32(n_vis + b), max_n));
   // block bounds floor(j n / NB): in 32 bits when j n fits (the usual case), one per lane,
   // the next lane's lower bound being this lane's upper one
   const bool narrow = (unsigned long long)n * (unsigned)NB <= 0xFFFFFFFFull;
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(BT_WARPS * 32) k_block_topp(const float* __res
 constexpr int BTW_WARPS = 8;
 template <int P>
 __global__ void __launch_bounds__(BTW_WARPS * 32) k_block_topp_w(const float* __restrict__ S, int ldS,
-                                                                const int* __restrict__ n_vis, int max_n, int B,
+                                                                const int* n_vis, int max_n, int B,
                                                                 int NB, int* __restrict__ pool,
                                                                 float* __restrict__ pool_score) {
   pdl_wait();
@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(BTW_WARPS * 32) k_block_topp_w(const float* __
   const long long gw = (long long)blockIdx.x * BTW_WARPS + (threadIdx.x >> 5);
   if (gw >= (long long)B * NB) return;
   const int b = (int)(gw / NB), j = (int)(gw % NB);
-  const int n = max(0, min(__ldg(n_vis + b), max_n));
+  const int n = max(0, min(ld_s32(n_vis + b), max_n));
   const int lo = (int)(((long long)j * n) / NB), hi = (int)(((long long)(j + 1) * n) / NB);
   const int cnt = hi - lo;
   if (cnt <= 0) return;

@@ -22,3 +22,11 @@ def test_the_paged_8_bit_cache_is_read_coherently(name):
     """A step's plan, append, selection and attention follow one another: each reads the tables, summaries, scales and bytes
     that the ones before it write."""
     assert [(n, t.strip()) for n, t in lines(name) if NC.search(t)] == []
+
+
+@pytest.mark.parametrize("name", ["common.cuh", "compress.cu", "proj_tc.cu", "index.cu", "score_tc.cu", "attn.cu"])
+def test_what_a_plan_writes_is_read_coherently(name):
+    """csa2_page_plan's table, sequences, positions and lengths go into the compressor, the indexer and the attention."""
+    table = r"(?:\w+\.)*(?:page_table|seq|entry|pos|tok_pos|seq_of|n_vis)\b"
+    bad = re.compile(rf"__ldg\(\s*{table}|const (?:int|int32_t)\*\s*__restrict__\s*(?:page_table|seq|entry|pos|tok_pos|seq_of|n_vis)\b")
+    assert [(n, t.strip()) for n, t in lines(name) if bad.search(t)] == []
