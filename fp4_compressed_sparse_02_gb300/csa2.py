@@ -865,6 +865,8 @@ def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, win
         if pages.shape[:2] != (T, H) or len(pages.shape) != 3:
             raise ValueError(f"pages must be [{T}, {H}, n]")
         n = pages.shape[2]
+        if n == 0:                             # (its address is 0, which would mean all pages)
+            raise ValueError("pages must have room for at least one page; -1 for none")
     qp, qt, qh = _heads_of(q, dev, "q")
     S, sp, lengths = _step(cache, start, length, dev)
     _launch_ws("csa2_kv8_attn", _KV8_ATTN.pack(
