@@ -810,8 +810,9 @@ def kv8_append(cache: Kv8Cache, k, v, start, length):
 def kv8_select(cache: Kv8Cache, q, start, length, k, *, first=1, recent=1, max_length=None, out=None, ws=None):
     """The pages each new token attends to, by key head: the `first` oldest, the `recent` newest and the best-scoring
     others, k at most.  q bf16 [T, Hq, D] (tokens and heads may be strided); start, length as in
-    kv8_append; max_length: a bound of length (by default the page table's).  Returns (pages int32 [T, Hkv, k],
-    ascending and padded with -1, count int32 [T, Hkv])."""
+    kv8_append; max_length: a bound of length.  It sizes the workspace and picks the kernel; by default it is the page table's
+    width, which costs where that is much wider than the contexts (2048 rows at 32K: 77 us with the bound, 480 under a table
+    for a million tokens).  Returns (pages int32 [T, Hkv, k], ascending and padded with -1, count int32 [T, Hkv])."""
     T, Hq, D = q.shape
     H = cache.k.shape[1]
     _expect(q, _B16, "q")
@@ -836,10 +837,12 @@ def kv8_select(cache: Kv8Cache, q, start, length, k, *, first=1, recent=1, max_l
 def kv8_attn(cache: Kv8Cache, q, start, length, *, max_new=None, pages=None, window=0, softmax_scale=None,
              out_dtype=torch.bfloat16, out=None, lse=None, ws=None):
     """Causal attention of the new tokens q bf16 [T, Hq, D] (tokens and heads may be strided) over the cache, which
-    holds their keys and values already; start, length as in kv8_append.  max_new: about how many new
-    tokens a sequence has at most (picks the kernel; by default T - S + 1, which one has if all have some).  pages int32 [T, Hkv, n]: only these pages
-    (kv8_select).  window: only so many newest positions.  Returns (out [T, Hq, D] bf16 or float32, lse
-    float32 [T, Hq])."""
+    holds their keys and values already; start, length as in kv8_append.  max_new: about how many new tokens a sequence
+    has at most.  It picks one kernel for all sequences of the call; by default it is T - S + 1, which one has if all have
+    some, and which rows of padding raise: give it for a padded step.  Single rows beside a long chunk are faster in a call
+    of their own, over their range of the page table's rows, of start and of length.  pages int32 [T, Hkv, n]: only these
+    pages (kv8_select).  window: only so many newest positions.  Returns (out [T, Hq, D] bf16 or float32, lse float32
+    [T, Hq])."""
     T, Hq, D = q.shape
     H = cache.k.shape[1]
     _expect(q, _B16, "q")

@@ -26,8 +26,8 @@ namespace {
 // accumulators are the weights' A fragments.  The scales stay out of fp16: a page's key scale multiplies its logits, its value scale
 // its partial output, in float32.
 //
-// Bound by memory where a batch has the bytes (64 sequences of up to 64K tokens, 8 x 128 channels: 4.2 GB in 625-645 us,
-// 0.96-0.98 of the copy rate); by a warp's own chain of products and conversions, three warps a scheduler, where pages come
+// Bound by memory where a batch has the bytes (64 sequences of up to 64K tokens, 8 x 128 channels: 4.2 GB in 625-650 us,
+// 0.95-0.98 of the copy rate); by a warp's own chain of products and conversions, three warps a scheduler, where pages come
 // from L2 (2048 rows of 32 listed pages each: 0.87 ms for 8.6 GB, which the copies alone take 0.43 ms for); by two launches
 // and four dependent loads where there is little (one row over 4097 tokens: 10 + 6 us).  Left out: E4M3 products by
 // mma.sync (100 instructions more a half page than fp16 ones with their conversions: 1.17 ms); kLeast of 1 to 8 is all the
@@ -623,9 +623,8 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
   if (lane == 0) p.part[span] = part;
 }
 
-// Rows lie apart in the workspace, so eight loads a lane are under way at once; 6 us at 33 parts of 8 rows.
 // A CTA (span, eight rows): the stream that begins there and goes on in the next ones, a warp a row, a lane
-// D / 32 channels.
+// D / 32 channels.  Rows lie apart in the workspace, so eight loads a lane are under way at once; 6 us at 33 parts of 8 rows.
 template <int D>
 __global__ void __launch_bounds__(256, 2) k_kv8_join(const Kv8Params p) {
   constexpr int kPer = D / 32, kAhead = 8;

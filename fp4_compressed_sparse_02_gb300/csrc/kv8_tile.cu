@@ -8,8 +8,8 @@
 //
 // 256 rows and 128 tokens are 67 MFLOP, 2080 cycles of the tensor core; a step takes some 3300: a group's chain of scores
 // (products, wake-up, TMEM loads, maximum, exponentials, weights) lasts longer than the other group's products.  4096 new
-// tokens at 32K and a fresh prompt, 64 heads of 128: 3.2 ms, 1.31 PFLOP/s, 0.67 of the measured peak; 32 x 6 tokens at
-// 8K to 32K, 48 rows: 280 us, 0.71 of the copy rate.
+// tokens at 32K and a fresh prompt, 64 heads of 128: 3.2 to 3.4 ms (the longer one after the other, into the power cap), 1.27 to
+// 1.33 PFLOP/s, 0.65 to 0.68 of the measured peak; 32 x 6 tokens at 8K to 32K, 48 rows: 274 us, 0.73 of the copy rate.
 #include "kv8_attn.cuh"
 #include "kv8_order.h"
 

@@ -57,11 +57,10 @@ __device__ __forceinline__ void plan_counts(const csa2_page_plan_args& a, int s,
   }
 }
 
-// Bound by the launch and by two rounds of dependent loads: 4.1 us for 64 rows, 8.5 us for 262,144 (3.1 MB).  As two kernels,
-// one CTA's sums and then the rows, those took 8 and 14 us of a graph.
 // Up to 1024 sequences, a thread a sequence: every CTA has both prefix sums (rows, pages) in shared memory and sees to its
 // share of the rows and of the new pages.  CTA 0 writes the sequences' values; where those are the inputs themselves,
-// it is the only one.
+// it is the only one.  Bound by the launch and by two rounds of dependent loads: 4.1 us for 64 rows, 8.5 us for 262,144
+// (3.1 MB).  As two kernels, one CTA's sums and then the rows, those took 8 and 14 us of a graph.
 __global__ void __launch_bounds__(kPlanThreads) k_plan(const csa2_page_plan_args a, int rows) {
   __shared__ long long sums[33];
   __shared__ int start[kPlanThreads + 1], now[kPlanThreads], old_pages[kPlanThreads], pages_before[kPlanThreads + 1];
@@ -295,7 +294,8 @@ __device__ __forceinline__ void add_bytes(float2* m, uint2 w) {            // a 
 // A CTA a (range of rows, head, plane): the pages whose first new token lies in the range, one after the other.  A page's new
 // rows are loaded at once and stay in registers from the largest magnitude to the summary.  38K rows of 8 x 128 in bf16
 // (234 MB): 46 us, 0.75 of the copy rate, of which loading alone fills a part: a CTA's barriers stand between its
-// loads and its stores, and eight CTAs an SM overlap them.  Keys and values in one CTA of 256 threads: 56 us.
+// loads and its stores, and eight CTAs an SM overlap them.  Keys and values in one CTA of 256 threads: 56 us.  The same
+// rows in float32 (390 MB), four CTAs an SM: 75 us from a cold L2, 0.77, where bf16 takes 52.
 template <typename T, int D, bool VEC>
 __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 8 : 4) k_kv8_append(const AppendParams p) {
   constexpr int kPer = D / 8, kRows = kAppendThreads / kPer, kTurns = kPage / kRows;   // threads a row, rows a turn
@@ -426,8 +426,8 @@ __global__ void __launch_bounds__(kAppendThreads, sizeof(T) == 2 ? 8 : 4) k_kv8_
 //
 // Scores, then picks.  The scores of up to 8 rows of one sequence and key head are one product of their 8-bit queries
 // with the pages' 8-bit summaries: whole numbers up to 127 are exact in fp16 and their sums of 128 products
-// stay below 2^24, so mma.sync gives the exact dot products whatever its order.  Bound by memory latency: 1,024 summaries a
-// CTA and four rounds (32 rows at up to 128K: 16 us for 45 MB); eight rows share what they read (2048 rows: 38 us).
+// stay below 2^24, so mma.sync gives the exact dot products whatever its order.  Bound by memory latency: 512 summaries a
+// CTA, 128 a warp in four rounds (32 rows at up to 128K: 16 us for 45 MB); eight rows share what they read (2048 rows: 38 us).
 constexpr int kTile = 8, kScoreThreads = 128, kScorePages = 512;
 
 struct SelectParams {
@@ -583,9 +583,8 @@ __global__ void __launch_bounds__(kScoreThreads) k_kv8_score(const SelectParams 
   }
 }
 
-// 16,384 pairs of 512 pages: 33 us, where a CTA a pair took 113; 66 keys a lane, for 2048 pages, 17 us against 10.
 // Rows with at most 32 K pages, a warp a (row, head): lane l holds keys l, l + 32, ...; the k-th best bit by bit, by
-// ballots.
+// ballots.  16,384 pairs of 512 pages: 33 us, where a CTA a pair took 113; 66 keys a lane, for 2048 pages, 17 us against 10.
 template <int K>
 __global__ void __launch_bounds__(256) k_kv8_pick_warp(const SelectParams p) {
   const csa2_kv8_select_args& a = p.a;
@@ -647,8 +646,8 @@ __global__ void __launch_bounds__(256) k_kv8_pick_warp(const SelectParams p) {
   }
 }
 
-// 10 us for 256 (row, head) pairs of up to 2048 pages, 13 for 8 of 16,384.
-// A CTA a (row, head): the k-th best key by digits of 11, 11 and 10 bits, then the kept pages in ascending order.
+// A CTA a (row, head): the k-th best key by digits of 11, 11 and 10 bits, then the kept pages in ascending order.  10 us for 256
+// pairs of up to 2048 pages, 13 for 8 of 16,384.
 template <int THREADS>
 __global__ void __launch_bounds__(THREADS) k_kv8_pick(const SelectParams p) {
   constexpr int kBins = 2048, kPerThread = kBins / THREADS, kPickWarps = THREADS / 32;
