@@ -28,7 +28,7 @@ namespace {
 //
 // Bound by memory where a batch has the bytes (64 sequences of up to 64K tokens, 8 x 128 channels: 4.2 GB in 625-650 us,
 // 0.95-0.98 of the copy rate); by a warp's own chain of products and conversions, three warps a scheduler, where pages come
-// from L2 (2048 rows of 32 listed pages each: 0.87 ms for 8.6 GB, which the copies alone take 0.43 ms for); by two launches
+// from L2 (2048 rows of 32 listed pages each: 0.88 ms for 8.6 GB, which the copies alone take 0.43 ms for); by two launches
 // and four dependent loads where there is little (one row over 4097 tokens: 10 + 6 us).  Left out: E4M3 products by
 // mma.sync (100 instructions more a half page than fp16 ones with their conversions: 1.17 ms); kLeast of 1 to 8 is all the
 // same at one row.
@@ -39,7 +39,7 @@ constexpr int kWarps = 4, kLeast = 4, kHalf = kPage / 2;
 constexpr float kWeight = 15.f, kWeightUndo = 1.f / 32768.f;
 
 // CTAs an SM.  Three, at 168 registers a thread and two stages a warp, where 8 rows have lists and pages come from L2
-// (2048 rows over 32 pages each: 0.95 ms against 1.10); two, with three stages, where the bytes come from memory (64 sequences
+// (2048 rows over 32 pages each, with their selection: 0.97 ms, 1.10 at two); two, with three stages, where the bytes come from memory (64 sequences
 // up to 64K: 649 us against 654) and at 16 rows, whose accumulators do not fit 168 registers.
 template <int D, int RT, bool LIST>
 struct Shape {

@@ -638,7 +638,8 @@ typedef struct csa2_kv8_cache {
  *   row t of its tokens: seq[t] = s, pos[t] = length[s] + (t - start[s]),
  *   slot[t] = 64 * page_table[s][pos / 64] + pos % 64.
  * Rows from start[S] on get -1 in seq, pos and slot.  seq and pos are csa2_compress_quant's seq
- * and entry (m = 1), new_length its sequences' n_vis.
+ * and entry (m = 1; it skips the rows of -1 and reports them as CSA2_DEVERR_SEQ), new_length its
+ * sequences' n_vis.
  * A cut add sets CSA2_DEVERR_TOKENS; a negative length or add counts as 0 and sets
  * CSA2_DEVERR_N_VIS.  When the free pages run out the pages missing become -1 (their tokens'
  * slots too), new_head = num_free, and CSA2_DEVERR_NO_PAGE is set.  A page id of an older table
@@ -763,7 +764,8 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * element.  Above, it is the sum of two E4M3 numbers times a power of two, exact within 2^-9 of its
  * largest element and to 2^-17 of that below; the values of a page whose scale is below 2^-22 of the
  * largest value scale in sight lose their last bits; and sums, which the tensor cores cut off rather
- * than round, are off by up to 2^-12 of their terms' magnitudes.  A NaN that a row does not see does not
+ * than round, are off by up to 2^-12 of their terms' magnitudes.  The sum of the values that a row sees,
+ * each times its weight over the largest, must stay in float32's range.  A NaN that a row does not see does not
  * reach it.  Results repeat bit for bit.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
  * window >= 0; S <= 2^18; T * Hq < 2^31.
