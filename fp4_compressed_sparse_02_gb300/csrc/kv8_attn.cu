@@ -429,7 +429,7 @@ k_kv8_stream(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUt
         }
 #pragma unroll
         for (int e = kLane0; e < kLane1; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
-        const float mn = fmaxf(m[i], top), z0 = mn == -INFINITY ? 0.f : mn, z = z0 - kWeight;
+        const float mn = fmaxf(m[i], top), z0 = mn == -INFINITY ? 0.f : mn, z = __fsub_ru(z0, kWeight);   // (a weight above 2^15 would leave fp16)
         alpha[i] = ex2(m[i] - z0);
         m[i] = mn;
         float sum = 0.f;

@@ -33,8 +33,10 @@ constexpr uint32_t kPollNs = 200, kTilePolls = 1u << 20;    // (a poll without a
 // runs; 3.43 with runs of 128 steps, 3.69 of 64 (before both ends of a run shared their code).
 constexpr int kRun = 256;
 // Weights are 2^kWeight times exp2(logit - top), and the maximum is up to 2^kFollow above top: together within fp16, which
-// reaches down to 2^-36 of a weight at top.
-constexpr float kWeight = 11.f, kFollow = 4.f, kWeightUndo = 1.f / 2048.f;
+// reaches down to 2^-36 of a weight at top.  top is rounded, the product in x f - top is not: for logits below 2^28 (base 2),
+// whose units are 16 at most, the sums below are rounded so that a weight stays within 2^15.5 and the largest above
+// 2^-8.  Beyond, a row is NaN; rounding the products first cost 3 to 10 % of 4096 new tokens at 32K.
+constexpr float kWeight = 11.f, kFollow = 4.f, kWeightUndo = 1.f / 2048.f, kMostLogit = 268435456.f;
 constexpr int kOver = 12;                // what beginning a stream costs, in steps
 constexpr int kCopy = 2047;              // sequences whose starts and lengths the plan copies
 
@@ -719,7 +721,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           }
           // The maximum follows only when it grows by more than 2^kFollow (a published method of attention kernels): weights
           // above it are as exact in fp16, and O and the sum are rescaled a few times a row.
-          const bool follow = now > top + kFollow || (top == -INFINITY && now > top);
+          const bool follow = now > __fadd_rd(top, kFollow) || (top == -INFINITY && now > top);
           if (__any_sync(0xffffffffu, follow)) {
             const float alpha = follow ? ex2(top - now) : 1.f;
             if (follow) top = now;
@@ -739,7 +741,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
           any = true;
           const float z = top == -INFINITY ? 0.f : top;
           float2 sum[4] = {};
-          const float2 zz = make_float2(kWeight - z, kWeight - z);
+          const float2 zz = make_float2(__fadd_rd(kWeight, -z), __fadd_rd(kWeight, -z));
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
             const float f = kM == 64 ? (half ? f1 : f0) : i < 2 ? f0 : f1;
@@ -814,6 +816,7 @@ k_kv8_tile(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUten
       // ---- the segment's result, or its part
       const bool two = SPLIT && w.take > 1;                  // both groups have steps
       l *= kWeightUndo;
+      if (fabsf(top) >= kMostLogit && top != -INFINITY) l = NAN;
       if (SPLIT && grp == 1 && half == 0) m.ml[r] = make_float2(top, l);
       if (SPLIT) {
         tc::fence_before_sync();
