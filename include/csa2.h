@@ -763,11 +763,11 @@ csa2_status csa2_kv8_select_workspace(const csa2_kv8_select_args* args, size_t* 
  * above.  Up to 16 rows each head's q is fp16 times a power of two, exact within 2^-28 of its largest
  * element.  Above, it is the sum of two E4M3 numbers times a power of two, exact within 2^-9 of its
  * largest element and to 2^-17 of that below; the values of a page whose scale is below 2^-22 of the
- * largest value scale in sight lose their last bits; and sums, which the tensor cores cut off rather
- * than round, are off by up to 2^-12 of their terms' magnitudes.  The sum of the values that a row sees,
- * each times its weight over the largest, must stay in float32's range; and above 16 rows a row whose
- * largest logit, over log 2, reaches 2^28 in magnitude gives NaN (one that sees other such logits may).  A NaN that a row does not see does not
- * reach it.  Results repeat bit for bit.
+ * largest value scale in sight lose their last bits; sums, which the tensor cores cut off rather than
+ * round, are off by up to 2^-12 of their terms' magnitudes; and a row whose largest logit, over log 2,
+ * reaches 2^28 in magnitude gives NaN (one that sees other such logits may).  The sum of the values that
+ * a row sees, each times its weight over the largest, must stay in float32's range.  A NaN that a row
+ * does not see does not reach it.  Results repeat bit for bit.
  * Supported: q bf16; Hq a multiple of Hkv with G <= 128; 1 <= list_len <= 4096 with pages;
  * window >= 0; S <= 2^18; T * Hq < 2^31.
  * -------------------------------------------------------------------------- */
